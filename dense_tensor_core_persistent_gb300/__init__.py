@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libdtcp_gemm.so")
@@ -43,6 +44,7 @@ EXPORTS = (
     "gemm_nvfp4_blocked_scale_bytes", "gemm_nvfp4_pack_scales", "gemm_nvfp4_blocked", "gemm_nvfp4_blocked_ex",
     "gemm_nvfp4_noalloc", "gemm_measure_mma_rate", "gemm_bf16_fused", "gemm_nvfp4_fused", "gemm_nvfp4_blocked_fused",
     "gemm_bf16_plan", "gemm_clc_rule", "gemm_nvfp4_plan", "gemm_bf16_wide_rule",
+    "gemm_rms_norm", "gemm_rms_norm_backward",
 )
 
 # gemm_activation_t
@@ -121,6 +123,21 @@ def epilogue(alpha=1.0, beta=0.0, bias=None, activation=GEMM_ACT_NONE) -> gemm_e
     return gemm_epilogue_t(alpha, beta, None if bias is None else _ptr(bias), activation, 0)
 
 
+GEMM_NORM_BF16 = 0
+GEMM_NORM_E4M3 = 1
+GEMM_NORM_NVFP4 = 2
+
+
+class gemm_norm_strides_t(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_longlong), ("residual", ctypes.c_longlong), ("sum", ctypes.c_longlong),
+                ("y", ctypes.c_longlong)]
+
+
+class gemm_norm_backward_strides_t(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_longlong), ("sum", ctypes.c_longlong), ("dsum", ctypes.c_longlong),
+                ("dx", ctypes.c_longlong)]
+
+
 _lib = None
 
 
@@ -179,6 +196,11 @@ def lib() -> ctypes.CDLL:
         l.gemm_bf16_wide_rule.argtypes = [I, I, I, I]
         l.gemm_bf16_wide_rule.restype = I
         l.gemm_measure_mma_rate.restype = I
+        F = ctypes.c_float
+        l.gemm_rms_norm.argtypes = [P, P, P, P, P, P, P, I, I, F, I, P, ctypes.POINTER(gemm_norm_strides_t)]
+        l.gemm_rms_norm.restype = I
+        l.gemm_rms_norm_backward.argtypes = [P, P, P, P, P, P, P, I, I, P, ctypes.POINTER(gemm_norm_backward_strides_t)]
+        l.gemm_rms_norm_backward.restype = I
         _lib = l
     return _lib
 
@@ -369,6 +391,20 @@ def measure_mma_rate(kind: int) -> float:
     return out.value
 
 
+def gemm_rms_norm(X, R, W, S, Y, scales, rstd, rows: int, cols: int, eps: float, fmt: int = GEMM_NORM_BF16,
+                  stream=None, strides: gemm_norm_strides_t | None = None) -> None:
+    """s = bf16(X + R), Y = s / sqrt(mean(s^2) + eps) * W in one of three formats; see include/gemm.h."""
+    _check(lib().gemm_rms_norm(_ptr(X), _ptr(R), _ptr(W), _ptr(S), _ptr(Y), _ptr(scales), _ptr(rstd), rows, cols, eps,
+                               fmt, _stream(stream), _byref_or_null(strides)), "gemm_rms_norm")
+
+
+def gemm_rms_norm_backward(dY, S, W, rstd, dS, dX, dW, rows: int, cols: int, stream=None,
+                           strides: gemm_norm_backward_strides_t | None = None) -> None:
+    """Gradient of gemm_rms_norm's BF16 form; see include/gemm.h."""
+    _check(lib().gemm_rms_norm_backward(_ptr(dY), _ptr(S), _ptr(W), _ptr(rstd), _ptr(dS), _ptr(dX), _ptr(dW), rows,
+                                        cols, _stream(stream), _byref_or_null(strides)), "gemm_rms_norm_backward")
+
+
 # ---------------------------------------------------------------- torch-tensor conveniences
 
 def matmul_bf16(A, B, out=None, stream=None, opts=None):
@@ -414,3 +450,91 @@ def matmul_nvfp4(A, SFA, B, SFB, out=None, stream=None, opts=None):
         out = torch.empty(M, N, dtype=torch.bfloat16, device=A.device)
     gemm_nvfp4(A, SFA, B, SFB, out, M, N, K, stream, opts)
     return out
+
+
+def _matrix(t, what, dtype, shape=None):
+    """A CUDA matrix of `dtype` whose rows are contiguous -> its row stride (0: rows follow one another)."""
+    if t.dim() != 2 or t.dtype != dtype or not t.is_cuda or (shape is not None and tuple(t.shape) != tuple(shape)):
+        want = "" if shape is None else f" of shape {tuple(shape)}"
+        raise ValueError(f"{what}: a CUDA {dtype} matrix{want} is needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous (strides {t.stride()})")
+    if rows <= 1 or cols == 0 or t.stride(0) == cols:
+        return 0
+    if t.stride(0) < cols:
+        raise ValueError(f"{what}: rows must not overlap (strides {t.stride()})")
+    return t.stride(0)
+
+
+def _vector(t, what, dtype, n):
+    if t.dim() != 1 or t.dtype != dtype or not t.is_cuda or t.numel() != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what}: a contiguous CUDA {dtype} vector of {n} is needed, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+class NormOutput(NamedTuple):
+    """y: BF16, float8_e4m3fn, or packed E2M1 bytes; scales: None, FP32 a row, or E4M3 bytes per 16;
+    sum: the residual stream after the addition; rstd: FP32 a row, or None."""
+    y: object
+    scales: object
+    sum: object
+    rstd: object
+
+
+_NORM_FORMATS = {"bf16": GEMM_NORM_BF16, "e4m3": GEMM_NORM_E4M3, "nvfp4": GEMM_NORM_NVFP4}
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-5, out: str = "bf16", save: bool = False,
+             inplace: bool = False, stream=None) -> NormOutput:
+    """RMS norm of the rows of x + residual (rows x cols BF16). `out`: "bf16", "e4m3" (scales: FP32 a row)
+    or "nvfp4" (y and scales are A and SFA of matmul_nvfp4). `save`: keep rstd for rms_norm_backward.
+    `inplace`: the sum overwrites `residual`."""
+    import torch
+    if out not in _NORM_FORMATS:
+        raise ValueError(f"out: one of {sorted(_NORM_FORMATS)} is needed, got {out!r}")
+    bf16 = torch.bfloat16
+    ldx, ldr, lds = _matrix(x, "x", bf16), 0, 0
+    rows, cols = x.shape
+    total = x
+    if residual is not None:
+        ldr = _matrix(residual, "residual", bf16, x.shape)
+        total = residual if inplace else torch.empty((rows, cols), dtype=bf16, device=x.device)
+        lds = ldr if inplace else 0
+    elif inplace:
+        raise ValueError("inplace: there is no residual to overwrite")
+    if weight is not None:
+        _vector(weight, "weight", bf16, cols)
+    fmt, scales = _NORM_FORMATS[out], None
+    if fmt == GEMM_NORM_BF16:
+        y = torch.empty((rows, cols), dtype=bf16, device=x.device)
+    elif fmt == GEMM_NORM_E4M3:
+        y = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
+        scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+    else:
+        y = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=x.device)
+    rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if save else None
+    strides = gemm_norm_strides_t(ldx, ldr, lds, 0) if ldx or ldr or lds else None
+    gemm_rms_norm(x, residual, weight, total if residual is not None else None, y, scales, rstd, rows, cols, eps, fmt,
+                  stream, strides)
+    return NormOutput(y, scales, total, rstd)
+
+
+def rms_norm_backward(dy, total, weight, rstd, dsum=None, weight_grad: bool = True, stream=None):
+    """(dx, dweight) of rms_norm with BF16 output: `total` and `rstd` are NormOutput.sum and .rstd, `dsum` the
+    gradient that reaches the sum past the norm. dx is the gradient of x and of the residual; dweight is FP32."""
+    import torch
+    bf16 = torch.bfloat16
+    lds = _matrix(total, "total", bf16)
+    rows, cols = total.shape
+    lddy = _matrix(dy, "dy", bf16, total.shape)
+    ldds = _matrix(dsum, "dsum", bf16, total.shape) if dsum is not None else 0
+    _vector(rstd, "rstd", torch.float32, rows)
+    if weight is not None:
+        _vector(weight, "weight", bf16, cols)
+    dx = torch.empty((rows, cols), dtype=bf16, device=dy.device)
+    dw = torch.empty(cols, dtype=torch.float32, device=dy.device) if weight_grad else None
+    strides = gemm_norm_backward_strides_t(lddy, lds, ldds, 0) if lddy or lds or ldds else None
+    gemm_rms_norm_backward(dy, total, weight, rstd, dsum, dx, dw, rows, cols, stream, strides)
+    return dx, dw

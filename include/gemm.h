@@ -429,6 +429,61 @@ enum {
 };
 int gemm_measure_mma_rate(int kind, double* flop_per_clock_per_sm);
 
+/* ---------------------------------------------------------------- operators around the products */
+
+/* Output formats of gemm_rms_norm. */
+enum {
+  GEMM_NORM_BF16 = 0,  /* Y: rows x cols BF16 */
+  GEMM_NORM_E4M3 = 1,  /* Y: rows x cols E4M3 codes; scales: one FP32 per row; y ~ code * scale */
+  GEMM_NORM_NVFP4 = 2  /* Y: rows x cols/2 bytes of E2M1 codes; scales: rows x cols/16 E4M3 bytes: A and SFA of gemm_nvfp4 */
+};
+
+/* Row strides in elements (E4M3: of Y in bytes); 0 = cols. A stride is at least cols. */
+typedef struct {
+  long long x, residual, sum, y;
+} gemm_norm_strides_t;
+
+typedef struct {
+  long long dy, sum, dsum, dx;
+} gemm_norm_backward_strides_t;
+
+/*
+ * gemm_rms_norm -- root-mean-square norm of each row of a residual stream:
+ *   s = bf16_rne(X + R),  rstd = 1 / sqrt(mean(s^2) + eps),  y = s * rstd * W,
+ * in FP32 from the rounded s, y rounded once to the output format.
+ *   X, R: rows x cols BF16; R may be NULL (s = X).   W: cols BF16, or NULL (all ones).
+ *   S: rows x cols BF16, receives s; required with R, else may be NULL. S may be X or R itself.
+ *   Y, scales: see the formats above. E4M3: scale = max|y| / 448 of the row, code = e4m3_rne(y / scale)
+ *   (a row of zeros: scale 0, codes 0). NVFP4: scale = e4m3_rne(min(max|y| / 6, 448)) of the 16
+ *   columns, code = e2m1_rne(y / scale), at most 6 in magnitude (scale 0: codes 0). A tensor-wide
+ *   factor, where one is wanted, goes into W and its inverse into gemm_epilogue_t.alpha.
+ *   rstd: rows FP32 for the backward pass, or NULL.
+ * An infinity or NaN in a row makes rstd 0 or NaN and shows in the row's outputs as the formula
+ * gives it (NaN scales for E4M3 and NVFP4); other rows are not touched by it.
+ * Constraints: rows, cols >= 0 (0: nothing to do); cols <= 32760; eps >= 0; pointers aligned to
+ * their element; NVFP4: cols % 16 == 0, Y and scales without strides, X, R, W, S 16-byte aligned with
+ * strides that are multiples of 8. Any other cols, stride or alignment is taken; rows that start
+ * on 16-byte boundaries are fastest, then rows whose tensors share their misalignment.
+ * One kernel launch, asynchronous on `stream`; no workspace.
+ */
+int gemm_rms_norm(const void* X, const void* R, const void* W, void* S, void* Y, void* scales, float* rstd, int rows,
+                  int cols, float eps, int format, void* stream, const gemm_norm_strides_t* strides);
+
+/*
+ * gemm_rms_norm_backward -- gradient of gemm_rms_norm with BF16 output:
+ *   xh = S * rstd,  c = mean(dY * W * xh),  dX = bf16_rne(rstd * (dY * W - xh * c) + dS),
+ *   dW = sum over rows of dY * xh   (FP32).
+ *   S, rstd: what the forward call wrote (S = X where it had no R).
+ *   dS: rows x cols BF16, the gradient that reaches s past the norm (the residual path), or NULL.
+ *   dX: rows x cols BF16, the gradient of s and so of both X and R; it may be dY, dS or S itself.
+ *   dW: cols FP32, or NULL (not computed). rows == 0 sets it to zero.
+ * The same inputs give the same bits (dW: one partial sum a CTA, added in a fixed order).
+ * Constraints as above. One kernel launch, and with dW and more than one row a second one and a
+ * workspace of at most 8 * 152 * cols floats from the library's stream-ordered pool.
+ */
+int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const float* rstd, const void* dS, void* dX,
+                           float* dW, int rows, int cols, void* stream, const gemm_norm_backward_strides_t* strides);
+
 #ifdef __cplusplus
 }
 #endif
