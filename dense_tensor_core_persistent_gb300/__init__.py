@@ -44,7 +44,7 @@ EXPORTS = (
     "gemm_nvfp4_blocked_scale_bytes", "gemm_nvfp4_pack_scales", "gemm_nvfp4_blocked", "gemm_nvfp4_blocked_ex",
     "gemm_nvfp4_noalloc", "gemm_measure_mma_rate", "gemm_bf16_fused", "gemm_nvfp4_fused", "gemm_nvfp4_blocked_fused",
     "gemm_bf16_plan", "gemm_clc_rule", "gemm_nvfp4_plan", "gemm_bf16_wide_rule",
-    "gemm_rms_norm", "gemm_rms_norm_backward",
+    "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_token_logprobs", "gemm_token_logprobs_backward",
 )
 
 # gemm_activation_t
@@ -128,6 +128,10 @@ GEMM_NORM_E4M3 = 1
 GEMM_NORM_NVFP4 = 2
 
 
+GEMM_LOGITS_BF16 = 0
+GEMM_LOGITS_F32 = 1
+
+
 class gemm_norm_strides_t(ctypes.Structure):
     _fields_ = [("x", ctypes.c_longlong), ("residual", ctypes.c_longlong), ("sum", ctypes.c_longlong),
                 ("y", ctypes.c_longlong)]
@@ -201,6 +205,11 @@ def lib() -> ctypes.CDLL:
         l.gemm_rms_norm.restype = I
         l.gemm_rms_norm_backward.argtypes = [P, P, P, P, P, P, P, I, I, P, ctypes.POINTER(gemm_norm_backward_strides_t)]
         l.gemm_rms_norm_backward.restype = I
+        LL = ctypes.c_longlong
+        l.gemm_token_logprobs.argtypes = [P, I, P, P, P, P, I, P, P, I, I, LL, F, P]
+        l.gemm_token_logprobs.restype = I
+        l.gemm_token_logprobs_backward.argtypes = [P, I, P, P, P, P, P, P, I, I, LL, LL, F, P]
+        l.gemm_token_logprobs_backward.restype = I
         _lib = l
     return _lib
 
@@ -405,6 +414,22 @@ def gemm_rms_norm_backward(dY, S, W, rstd, dS, dX, dW, rows: int, cols: int, str
                                         cols, _stream(stream), _byref_or_null(strides)), "gemm_rms_norm_backward")
 
 
+def gemm_token_logprobs(logits, kind: int, tokens, logprob, entropy, lse, top: int, top_logprobs, top_ids, rows: int,
+                        vocab: int, ld: int = 0, scale: float = 1.0, stream=None) -> None:
+    """Log probabilities of given tokens, entropy and the `top` alternatives of each row; see include/gemm.h."""
+    _check(lib().gemm_token_logprobs(_ptr(logits), kind, _ptr(tokens), _ptr(logprob), _ptr(entropy), _ptr(lse), top,
+                                     _ptr(top_logprobs), _ptr(top_ids), rows, vocab, ld, scale, _stream(stream)),
+           "gemm_token_logprobs")
+
+
+def gemm_token_logprobs_backward(logits, kind: int, tokens, lse, entropy, dlogprob, dentropy, dlogits, rows: int,
+                                 vocab: int, ld: int = 0, ldd: int = 0, scale: float = 1.0, stream=None) -> None:
+    """Gradient of logprob and entropy with respect to the logits; see include/gemm.h."""
+    _check(lib().gemm_token_logprobs_backward(_ptr(logits), kind, _ptr(tokens), _ptr(lse), _ptr(entropy),
+                                              _ptr(dlogprob), _ptr(dentropy), _ptr(dlogits), rows, vocab, ld, ldd,
+                                              scale, _stream(stream)), "gemm_token_logprobs_backward")
+
+
 # ---------------------------------------------------------------- torch-tensor conveniences
 
 def matmul_bf16(A, B, out=None, stream=None, opts=None):
@@ -538,3 +563,60 @@ def rms_norm_backward(dy, total, weight, rstd, dsum=None, weight_grad: bool = Tr
     strides = gemm_norm_backward_strides_t(lddy, lds, ldds, 0) if lddy or lds or ldds else None
     gemm_rms_norm_backward(dy, total, weight, rstd, dsum, dx, dw, rows, cols, stream, strides)
     return dx, dw
+
+
+class TokenLogprobs(NamedTuple):
+    """FP32 per row: logprob (None without tokens), entropy, lse; rows x top: top_logprobs (FP32), top_ids (int32)."""
+    logprob: object
+    entropy: object
+    lse: object
+    top_logprobs: object
+    top_ids: object
+
+
+def _logits_kind(logits):
+    import torch
+    if logits.dtype == torch.bfloat16:
+        return GEMM_LOGITS_BF16
+    if logits.dtype == torch.float32:
+        return GEMM_LOGITS_F32
+    raise ValueError(f"logits: BF16 or FP32 is needed, got {logits.dtype}")
+
+
+def token_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, stream=None) -> TokenLogprobs:
+    """Log probabilities of `tokens` (rows int64; negative: none) under softmax(scale * logits) of each row, the
+    entropy, and the `top` most likely alternatives (equal logits: the lower index first)."""
+    import torch
+    kind = _logits_kind(logits)
+    ld = _matrix(logits, "logits", logits.dtype)
+    rows, vocab = logits.shape
+    if tokens is not None:
+        _vector(tokens, "tokens", torch.int64, rows)
+    out = torch.empty((3, rows), dtype=torch.float32, device=logits.device)
+    logprob, entropy, lse = out.unbind(0)
+    top_logprobs = top_ids = None
+    if top > 0:
+        top_logprobs = torch.empty((rows, top), dtype=torch.float32, device=logits.device)
+        top_ids = torch.empty((rows, top), dtype=torch.int32, device=logits.device)
+    gemm_token_logprobs(logits, kind, tokens, logprob if tokens is not None else None, entropy, lse, top, top_logprobs,
+                        top_ids, rows, vocab, ld, scale, stream)
+    return TokenLogprobs(logprob if tokens is not None else None, entropy, lse, top_logprobs, top_ids)
+
+
+def token_logprobs_backward(logits, tokens, lse, entropy, dlogprob, dentropy=None, scale: float = 1.0,
+                            inplace: bool = False, stream=None):
+    """dlogits of token_logprobs, in the type of the logits; `inplace` overwrites them. tokens and dlogprob may
+    both be None, and dentropy."""
+    import torch
+    kind = _logits_kind(logits)
+    ld = _matrix(logits, "logits", logits.dtype)
+    rows, vocab = logits.shape
+    for t, what, dtype in ((tokens, "tokens", torch.int64), (lse, "lse", torch.float32),
+                           (entropy, "entropy", torch.float32), (dlogprob, "dlogprob", torch.float32),
+                           (dentropy, "dentropy", torch.float32)):
+        if t is not None:
+            _vector(t, what, dtype, rows)
+    dlogits = logits if inplace else torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    gemm_token_logprobs_backward(logits, kind, tokens, lse, entropy, dlogprob, dentropy, dlogits, rows, vocab, ld,
+                                 ld if inplace else 0, scale, stream)
+    return dlogits

@@ -484,6 +484,47 @@ int gemm_rms_norm(const void* X, const void* R, const void* W, void* S, void* Y,
 int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const float* rstd, const void* dS, void* dX,
                            float* dW, int rows, int cols, void* stream, const gemm_norm_backward_strides_t* strides);
 
+/* Types of the logits of gemm_token_logprobs. */
+enum { GEMM_LOGITS_BF16 = 0, GEMM_LOGITS_F32 = 1 };
+
+/*
+ * gemm_token_logprobs -- log probabilities under the softmax of each row of logits:
+ *   z = scale * logits,  lse = log sum_j exp(z_j),  p_j = exp(z_j - lse),
+ *   logprob = z_token - lse,  entropy = -sum_j p_j log p_j (nats),
+ *   and the `top` largest log probabilities with their indices, in order.
+ *   logits: rows x vocab, BF16 or FP32, row stride ld elements (0 = vocab), element-aligned.
+ *   tokens: rows int64. A negative token is a place without one: its logprob is 0. A token >= vocab
+ *   gives NaN. tokens and logprob may both be NULL.
+ *   logprob, entropy, lse: rows FP32.
+ *   top: 0..32 and at most vocab; top_logprobs: rows x top FP32, top_ids: rows x top int32. The order is
+ *   that of the logits; equal logits (-0 and 0 among them) go by the lower index; NaN comes first.
+ *   scale: an inverse temperature, finite and > 0.
+ * Sums are FP32 with a running maximum. Logits of minus infinity (or of the type's lowest value next to
+ * ordinary ones) have probability 0 and take no part in the entropy. A row of nothing but minus infinity has
+ * lse and log probabilities of minus infinity (0 for a place without a token) and entropy 0. A NaN or plus
+ * infinity in a row makes its outputs NaN.
+ * rows == 0: nothing to do. vocab == 0 with rows: GEMM_ERR_INVALID_ARG. One kernel launch, asynchronous on
+ * `stream`, no workspace; the same inputs give the same bits.
+ */
+int gemm_token_logprobs(const void* logits, int type, const long long* tokens, float* logprob, float* entropy, float* lse,
+                        int top, float* top_logprobs, int* top_ids, int rows, int vocab, long long ld, float scale,
+                        void* stream);
+
+/*
+ * gemm_token_logprobs_backward -- gradient of logprob and entropy with respect to the logits:
+ *   dlogits_j = scale * (dlogprob * (1[j = token] - p_j) - dentropy * p_j * (log p_j + entropy)),
+ * rounded once to the type of the logits.
+ *   lse, entropy: what gemm_token_logprobs wrote. dlogprob, dentropy: rows FP32; dlogprob and tokens may both be
+ *   NULL, and dentropy (then entropy is not read). A negative token takes no part (its dlogprob is not read into
+ *   the row); a token >= vocab makes the row NaN.
+ *   dlogits: rows x vocab of the type of the logits, row stride ldd (0 = vocab); it may be the logits themselves
+ *   (with ldd = ld). A row of nothing but minus infinity gets zeros; logits of minus infinity get 0.
+ * One kernel launch, asynchronous on `stream`, no workspace.
+ */
+int gemm_token_logprobs_backward(const void* logits, int type, const long long* tokens, const float* lse,
+                                 const float* entropy, const float* dlogprob, const float* dentropy, void* dlogits,
+                                 int rows, int vocab, long long ld, long long ldd, float scale, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -63,3 +63,37 @@ def test_no_device_is_reported():
         pytest.skip("a GPU is present")
     assert norm() == g.GEMM_ERR_NO_DEVICE
     assert norm_backward() == g.GEMM_ERR_NO_DEVICE
+
+
+def logprobs(l=16, kind=0, tokens=16, lp=16, ent=16, lse=16, top=0, tl=16, ti=16, rows=2, vocab=32, ld=0, scale=1.0):
+    return g.lib().gemm_token_logprobs(l, kind, tokens, lp, ent, lse, top, tl, ti, rows, vocab, ld, scale, 0)
+
+
+def logprobs_backward(l=16, kind=0, tokens=16, lse=16, ent=16, dlp=16, dh=16, dl=16, rows=2, vocab=32, ld=0, ldd=0,
+                      scale=1.0):
+    return g.lib().gemm_token_logprobs_backward(l, kind, tokens, lse, ent, dlp, dh, dl, rows, vocab, ld, ldd, scale, 0)
+
+
+def test_token_logprobs_refusals():
+    assert logprobs(rows=0, l=0) == g.GEMM_OK
+    assert logprobs(rows=-1) == BAD and logprobs(vocab=-1) == BAD and logprobs(vocab=0) == BAD
+    assert logprobs(kind=2) == BAD and logprobs(top=-1) == BAD and logprobs(top=33) == SHAPE
+    assert logprobs(top=8, vocab=7) == BAD
+    assert logprobs(top=3, tl=0) == BAD and logprobs(top=3, ti=0) == BAD
+    assert logprobs(l=0) == BAD and logprobs(ent=0) == BAD and logprobs(lse=0) == BAD and logprobs(tokens=0) == BAD
+    assert logprobs(ld=31) == BAD and logprobs(ld=-1) == BAD
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert logprobs(scale=scale) == BAD
+    assert logprobs(l=17) == ALIGN and logprobs(kind=1, l=18) == ALIGN and logprobs(tokens=20) == ALIGN
+    assert logprobs(lse=18) == ALIGN
+    assert logprobs(vocab=(1 << 30) + 1) == SHAPE
+
+
+def test_token_logprobs_backward_refusals():
+    assert logprobs_backward(rows=0, l=0) == g.GEMM_OK
+    assert logprobs_backward(rows=-1) == BAD and logprobs_backward(vocab=0) == BAD and logprobs_backward(kind=-1) == BAD
+    assert logprobs_backward(dlp=0) == BAD and logprobs_backward(tokens=0) == BAD  # one without the other
+    assert logprobs_backward(ent=0) == BAD and logprobs_backward(lse=0) == BAD and logprobs_backward(dl=0) == BAD
+    assert logprobs_backward(ld=8) == BAD and logprobs_backward(ldd=8) == BAD
+    assert logprobs_backward(scale=0.0) == BAD
+    assert logprobs_backward(dl=17) == ALIGN and logprobs_backward(dlp=18) == ALIGN
