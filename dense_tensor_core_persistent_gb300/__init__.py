@@ -45,6 +45,7 @@ EXPORTS = (
     "gemm_nvfp4_noalloc", "gemm_measure_mma_rate", "gemm_bf16_fused", "gemm_nvfp4_fused", "gemm_nvfp4_blocked_fused",
     "gemm_bf16_plan", "gemm_clc_rule", "gemm_nvfp4_plan", "gemm_bf16_wide_rule",
     "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_token_logprobs", "gemm_token_logprobs_backward",
+    "gemm_glu_bf16", "gemm_glu_e4m3", "gemm_glu_bf16_backward",
 )
 
 # gemm_activation_t
@@ -132,6 +133,16 @@ GEMM_LOGITS_BF16 = 0
 GEMM_LOGITS_F32 = 1
 
 
+GEMM_GLU_SILU = 0
+GEMM_GLU_GELU_TANH = 1
+GEMM_GLU_RELU = 2
+
+
+class gemm_glu_strides_t(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_longlong), ("h", ctypes.c_longlong), ("dh", ctypes.c_longlong),
+                ("dx", ctypes.c_longlong)]
+
+
 class gemm_norm_strides_t(ctypes.Structure):
     _fields_ = [("x", ctypes.c_longlong), ("residual", ctypes.c_longlong), ("sum", ctypes.c_longlong),
                 ("y", ctypes.c_longlong)]
@@ -210,6 +221,13 @@ def lib() -> ctypes.CDLL:
         l.gemm_token_logprobs.restype = I
         l.gemm_token_logprobs_backward.argtypes = [P, I, P, P, P, P, P, P, I, I, LL, LL, F, P]
         l.gemm_token_logprobs_backward.restype = I
+        GS = ctypes.POINTER(gemm_glu_strides_t)
+        l.gemm_glu_bf16.argtypes = [P, P, P, P, P, I, I, I, I, P, GS]
+        l.gemm_glu_bf16.restype = I
+        l.gemm_glu_e4m3.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P, GS]
+        l.gemm_glu_e4m3.restype = I
+        l.gemm_glu_bf16_backward.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, P, GS]
+        l.gemm_glu_bf16_backward.restype = I
         _lib = l
     return _lib
 
@@ -430,6 +448,28 @@ def gemm_token_logprobs_backward(logits, kind: int, tokens, lse, entropy, dlogpr
                                               scale, _stream(stream)), "gemm_token_logprobs_backward")
 
 
+def gemm_glu_bf16(X, Wg, Wu, H, preact, M: int, N: int, K: int, act: int = GEMM_GLU_SILU, stream=None,
+                  strides: gemm_glu_strides_t | None = None) -> None:
+    """H = act(X Wg^T) * (X Wu^T) in BF16, keeping [g | u] in preact if given; see include/gemm.h."""
+    _check(lib().gemm_glu_bf16(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(H), _ptr(preact), M, N, K, act, _stream(stream),
+                               _byref_or_null(strides)), "gemm_glu_bf16")
+
+
+def gemm_glu_e4m3(X, x_scale, Wg, wg_scale, Wu, wu_scale, H, M: int, N: int, K: int, act: int = GEMM_GLU_SILU,
+                  stream=None, strides: gemm_glu_strides_t | None = None) -> None:
+    """gemm_glu_bf16 from E4M3 operands with a scale per row; see include/gemm.h."""
+    _check(lib().gemm_glu_e4m3(_ptr(X), _ptr(x_scale), _ptr(Wg), _ptr(wg_scale), _ptr(Wu), _ptr(wu_scale), _ptr(H), M,
+                               N, K, act, _stream(stream), _byref_or_null(strides)), "gemm_glu_e4m3")
+
+
+def gemm_glu_bf16_backward(dH, X, Wg, Wu, preact, dX, dWg, dWu, M: int, N: int, K: int, act: int = GEMM_GLU_SILU,
+                           stream=None, strides: gemm_glu_strides_t | None = None) -> None:
+    """Gradient of gemm_glu_bf16; see include/gemm.h."""
+    _check(lib().gemm_glu_bf16_backward(_ptr(dH), _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(preact), _ptr(dX), _ptr(dWg),
+                                        _ptr(dWu), M, N, K, act, _stream(stream), _byref_or_null(strides)),
+           "gemm_glu_bf16_backward")
+
+
 # ---------------------------------------------------------------- torch-tensor conveniences
 
 def matmul_bf16(A, B, out=None, stream=None, opts=None):
@@ -620,3 +660,71 @@ def token_logprobs_backward(logits, tokens, lse, entropy, dlogprob, dentropy=Non
     gemm_token_logprobs_backward(logits, kind, tokens, lse, entropy, dlogprob, dentropy, dlogits, rows, vocab, ld,
                                  ld if inplace else 0, scale, stream)
     return dlogits
+
+
+_GLU_ACTS = {"silu": GEMM_GLU_SILU, "gelu_tanh": GEMM_GLU_GELU_TANH, "relu": GEMM_GLU_RELU}
+
+
+def _glu_act(act):
+    if act not in _GLU_ACTS:
+        raise ValueError(f"act: one of {sorted(_GLU_ACTS)} is needed, got {act!r}")
+    return _GLU_ACTS[act]
+
+
+def _contiguous(t, what, dtype, shape):
+    if _matrix(t, what, dtype, shape):
+        raise ValueError(f"{what}: rows must follow one another (strides {t.stride()})")
+    return t
+
+
+def glu_bf16(x, wg, wu, act: str = "silu", save: bool = False, stream=None):
+    """act(x wg^T) * (x wu^T) for BF16 x (M x K), wg and wu (N x K) -> M x N BF16. `save`: also what
+    glu_bf16_backward needs, as (h, saved)."""
+    import torch
+    kind, bf16 = _glu_act(act), torch.bfloat16
+    ldx = _matrix(x, "x", bf16)
+    M, K = x.shape
+    N = wg.shape[0]
+    _contiguous(wg, "wg", bf16, (N, K))
+    _contiguous(wu, "wu", bf16, (N, K))
+    h = torch.empty((M, N), dtype=bf16, device=x.device)
+    saved = torch.empty((M, 2 * N), dtype=torch.float32, device=x.device) if save else None
+    gemm_glu_bf16(x, wg, wu, h, saved, M, N, K, kind, stream, gemm_glu_strides_t(ldx, 0, 0, 0) if ldx else None)
+    return (h, saved) if save else h
+
+
+def glu_e4m3(x, x_scale, wg, wg_scale, wu, wu_scale, act: str = "silu", stream=None):
+    """glu_bf16 from float8_e4m3fn operands with an FP32 scale per row (x: rms_norm(..., out="e4m3"))."""
+    import torch
+    kind, e4m3 = _glu_act(act), torch.float8_e4m3fn
+    ldx = _matrix(x, "x", e4m3)
+    M, K = x.shape
+    N = wg.shape[0]
+    _contiguous(wg, "wg", e4m3, (N, K))
+    _contiguous(wu, "wu", e4m3, (N, K))
+    for t, what, n in ((x_scale, "x_scale", M), (wg_scale, "wg_scale", N), (wu_scale, "wu_scale", N)):
+        _vector(t, what, torch.float32, n)
+    h = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    gemm_glu_e4m3(x, x_scale, wg, wg_scale, wu, wu_scale, h, M, N, K, kind, stream,
+                  gemm_glu_strides_t(ldx, 0, 0, 0) if ldx else None)
+    return h
+
+
+def glu_bf16_backward(dh, x, wg, wu, saved, act: str = "silu", input_grad: bool = True, weight_grads: bool = True,
+                      stream=None):
+    """(dx, dwg, dwu) of glu_bf16(..., save=True); None in the place of a gradient that is not asked for."""
+    import torch
+    kind, bf16 = _glu_act(act), torch.bfloat16
+    ldx = _matrix(x, "x", bf16)
+    M, K = x.shape
+    N = wg.shape[0]
+    lddh = _matrix(dh, "dh", bf16, (M, N))
+    _contiguous(wg, "wg", bf16, (N, K))
+    _contiguous(wu, "wu", bf16, (N, K))
+    _contiguous(saved, "saved", torch.float32, (M, 2 * N))
+    dx = torch.empty((M, K), dtype=bf16, device=x.device) if input_grad else None
+    dwg = torch.empty((N, K), dtype=bf16, device=x.device) if weight_grads else None
+    dwu = torch.empty((N, K), dtype=bf16, device=x.device) if weight_grads else None
+    gemm_glu_bf16_backward(dh, x, wg, wu, saved, dx, dwg, dwu, M, N, K, kind, stream,
+                           gemm_glu_strides_t(ldx, 0, lddh, 0) if ldx or lddh else None)
+    return dx, dwg, dwu

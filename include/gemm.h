@@ -525,6 +525,53 @@ int gemm_token_logprobs_backward(const void* logits, int type, const long long* 
                                  const float* entropy, const float* dlogprob, const float* dentropy, void* dlogits,
                                  int rows, int vocab, long long ld, long long ldd, float scale, void* stream);
 
+/* Activations of the gated feed-forward block. */
+enum {
+  GEMM_GLU_SILU = 0,      /* g / (1 + exp(-g)) */
+  GEMM_GLU_GELU_TANH = 1, /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+  GEMM_GLU_RELU = 2       /* max(g, 0) */
+};
+
+/* Row strides in elements, 0 = contiguous; each is at least its row and a multiple of 16 bytes. */
+typedef struct {
+  long long x, h, dh, dx;
+} gemm_glu_strides_t;
+
+/*
+ * gemm_glu_bf16 -- the gated feed-forward block's two projections, its activation and the product, in one kernel:
+ *   g = X Wg^T,  u = X Wu^T,  H = bf16_rne(act(g) * u),  FP32 accumulation and activation.
+ *   X: M x K BF16; Wg, Wu: N x K BF16 (row-major, K contiguous); H: M x N BF16.
+ *   preact: M x 2N FP32, receives [g | u] for the backward pass, or NULL.
+ *   act: GEMM_GLU_*. strides: of X and H (and, backward, dH and dX), or NULL.
+ * Constraints: M, N, K >= 0; K % 8 == 0 and N % 8 == 0; pointers 16-byte aligned. M == 0 or N == 0: nothing to do.
+ * K == 0: H (and preact) are set to zero. The block's second product is gemm_bf16 (gemm_bf16_fused with beta = 1
+ * adds the residual). Asynchronous on `stream`; no workspace.
+ */
+int gemm_glu_bf16(const void* X, const void* Wg, const void* Wu, void* H, float* preact, int M, int N, int K, int act,
+                  void* stream, const gemm_glu_strides_t* strides);
+
+/*
+ * gemm_glu_e4m3 -- the same from E4M3 operands with one FP32 scale per row (those of gemm_rms_norm's E4M3 output):
+ *   g[m][n] = x_scale[m] * wg_scale[n] * sum_k X[m][k] Wg[n][k], u alike; H as above.
+ * Constraints: K % 16 == 0, N % 8 == 0, stride of X in bytes a multiple of 16; otherwise as gemm_glu_bf16.
+ */
+int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const float* wg_scale, const void* Wu,
+                  const float* wu_scale, void* H, int M, int N, int K, int act, void* stream,
+                  const gemm_glu_strides_t* strides);
+
+/*
+ * gemm_glu_bf16_backward -- gradient of gemm_glu_bf16 from what it kept in preact = [g | u]:
+ *   dg = bf16_rne(dH * u * act'(g)),  du = bf16_rne(dH * act(g)),
+ *   dX = bf16_rne(dg Wg + du Wu),  dWg = bf16_rne(dg^T X),  dWu = bf16_rne(du^T X),  FP32 accumulation.
+ *   dH: M x N, dX: M x K, dWg, dWu: N x K, all BF16. dX may be NULL (not computed), dWg and dWu may both be.
+ *   act'(0) of ReLU is 0.
+ * Constraints as gemm_glu_bf16. Sums over nothing (M == 0 for dWg and dWu, N == 0 for dX) are set to zero.
+ * Up to three kernel launches; [dg | du] lives in a workspace of 4 M N bytes from the library's stream-ordered pool.
+ */
+int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const void* Wu, const float* preact, void* dX,
+                           void* dWg, void* dWu, int M, int N, int K, int act, void* stream,
+                           const gemm_glu_strides_t* strides);
+
 #ifdef __cplusplus
 }
 #endif

@@ -97,3 +97,45 @@ def test_token_logprobs_backward_refusals():
     assert logprobs_backward(ld=8) == BAD and logprobs_backward(ldd=8) == BAD
     assert logprobs_backward(scale=0.0) == BAD
     assert logprobs_backward(dl=17) == ALIGN and logprobs_backward(dlp=18) == ALIGN
+
+
+def glu(x=16, wg=16, wu=16, h=16, pre=0, M=2, N=8, K=8, act=0, strides=None):
+    return g.lib().gemm_glu_bf16(x, wg, wu, h, pre, M, N, K, act, 0, strides)
+
+
+def glu8(x=16, xs=16, wg=16, gs=16, wu=16, us=16, h=16, M=2, N=8, K=16, act=0, strides=None):
+    return g.lib().gemm_glu_e4m3(x, xs, wg, gs, wu, us, h, M, N, K, act, 0, strides)
+
+
+def glu_backward(dh=16, x=16, wg=16, wu=16, pre=16, dx=16, dwg=16, dwu=16, M=2, N=8, K=8, act=0, strides=None):
+    return g.lib().gemm_glu_bf16_backward(dh, x, wg, wu, pre, dx, dwg, dwu, M, N, K, act, 0, strides)
+
+
+def test_glu_refusals():
+    assert glu(M=0, x=0, h=0) == g.GEMM_OK and glu(N=0, h=0) == g.GEMM_OK
+    assert glu(M=-1) == BAD and glu(N=-8) == BAD and glu(K=-8) == BAD and glu(act=3) == BAD and glu(act=-1) == BAD
+    assert glu(x=0) == BAD and glu(wg=0) == BAD and glu(wu=0) == BAD and glu(h=0) == BAD
+    assert glu(K=12) == SHAPE and glu(N=12) == SHAPE
+    assert glu(x=24) == ALIGN and glu(h=8) == ALIGN and glu(pre=8) == ALIGN
+    assert glu(strides=g.gemm_glu_strides_t(4, 0, 0, 0)) == BAD
+    assert glu(strides=g.gemm_glu_strides_t(12, 0, 0, 0)) == SHAPE
+    assert glu(strides=g.gemm_glu_strides_t(0, 12, 0, 0)) == SHAPE
+
+
+def test_glu_e4m3_refusals():
+    assert glu8(M=0, x=0, h=0) == g.GEMM_OK
+    assert glu8(M=-1) == BAD and glu8(act=9) == BAD and glu8(xs=0) == BAD and glu8(gs=0) == BAD and glu8(us=0) == BAD
+    assert glu8(K=24) == SHAPE and glu8(N=4) == SHAPE and glu8(strides=g.gemm_glu_strides_t(24, 0, 0, 0)) == SHAPE
+    assert glu8(x=24) == ALIGN and glu8(xs=18) == ALIGN and glu8(us=17) == ALIGN
+
+
+def test_glu_backward_refusals():
+    assert glu_backward(dx=0, dwg=0, dwu=0) == g.GEMM_OK  # nothing asked for
+    assert glu_backward(M=0, dwg=0, dwu=0) == g.GEMM_OK
+    assert glu_backward(dwg=0) == BAD and glu_backward(dwu=0) == BAD  # one without the other
+    assert glu_backward(dh=0) == BAD and glu_backward(pre=0) == BAD and glu_backward(wg=0) == BAD and glu_backward(x=0) == BAD
+    assert glu_backward(M=-1) == BAD and glu_backward(act=7) == BAD
+    assert glu_backward(K=4) == SHAPE and glu_backward(N=20) == SHAPE
+    assert glu_backward(strides=g.gemm_glu_strides_t(0, 0, 12, 0)) == SHAPE
+    assert glu_backward(strides=g.gemm_glu_strides_t(0, 0, 0, 4)) == BAD
+    assert glu_backward(dwg=8) == ALIGN and glu_backward(pre=8) == ALIGN
