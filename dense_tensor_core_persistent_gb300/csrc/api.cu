@@ -186,6 +186,26 @@ int encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
 
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
+int resident_ctas(const void* kernel, int threads) {
+  struct Entry {
+    const void* kernel;
+    int threads, ctas;
+  };
+  static std::mutex mu;
+  static Entry entries[128];
+  static int count = 0;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < count; ++i)
+    if (entries[i].kernel == kernel && entries[i].threads == threads) return entries[i].ctas;
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 1;
+  }
+  if (count < 128) entries[count++] = Entry{kernel, threads, n};
+  return n;
+}
+
 // ---------------------------------------------------------------- tile order
 
 int choose_group_m(int M, int N, int K, int tile_m, int tile_n, double bytes_per_row_elem,

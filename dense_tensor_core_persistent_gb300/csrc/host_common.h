@@ -36,6 +36,9 @@ unsigned* device_status_word(int device);
 
 void count_launch();
 
+// CTAs of `threads` threads (no dynamic shared memory) that an SM holds together; asked once per kernel and size.
+int resident_ctas(const void* kernel, int threads);
+
 // Resolved per-call options.
 // Fused epilogue of the *_fused calls: C = act(alpha * acc + beta * C_old + bias[col]).
 struct EpilogueOptions {

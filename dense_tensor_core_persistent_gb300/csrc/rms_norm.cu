@@ -11,7 +11,7 @@
 //
 // Both directions are bound by the bytes they move (forward at most 8 per element, backward 8),
 // so a row is read once: a CTA keeps the whole row in registers between its reduction and its
-// output (groups of 8 columns per thread, up to 4 groups x 1024 threads = 32768 columns).
+// output (groups of 8 columns per thread, up to 8 groups x 512 threads = 32768 columns).
 // CTAs are persistent and step over rows by the grid size, so a thread always owns the same
 // columns: the weight is read once per CTA and the weight's gradient is summed in registers,
 // one partial row per CTA, which a second kernel adds in a fixed order (no atomics).
@@ -31,7 +31,7 @@
 
 namespace dtcp {
 
-constexpr int kNormMaxCols = 32768 - 8;  // 4 groups of 8 columns x 1024 threads, less one group for the boundary
+constexpr int kNormMaxCols = 32768 - 8;  // 8 groups of 8 columns x 512 threads, less one group for the boundary
 
 struct NormParams {
   const uint16_t* x;
@@ -77,27 +77,102 @@ __device__ __forceinline__ uint4 pack8(const F8& f) {
   return make_uint4(pack2(f.v[0], f.v[1]), pack2(f.v[2], f.v[3]), pack2(f.v[4], f.v[5]), pack2(f.v[6], f.v[7]));
 }
 
-// Columns c .. c+7 of a row as BF16, zero outside [0, cols). ALIGNED: c and cols are multiples
-// of 8 and the row starts on a 16-byte boundary.
-template <bool ALIGNED>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int cols) {
-  if (ALIGNED) return c < cols ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
-  if (c >= 0 && c + 8 <= cols && (reinterpret_cast<uintptr_t>(row + c) & 15u) == 0)
-    return *reinterpret_cast<const uint4*>(row + c);
+// How the rows of a call's tensors lie against the groups of 8 columns.
+enum NormAccess {
+  kAligned = 0,  // every row starts on a 16-byte boundary, cols a multiple of 8
+  kShared = 1,   // all tensors share their misalignment: whole vectors but in a row's first and last group
+  kElements = 2  // anything else: element by element
+};
+
+__device__ __forceinline__ bool whole(int c, int cols) { return c >= 0 && c + 8 <= cols; }
+__device__ __forceinline__ bool edge(int c, int cols) { return !whole(c, cols) && c + 8 > 0 && c < cols; }
+
+__device__ __forceinline__ uint4 load_elements(const uint16_t* row, int c, int cols) {
   uint32_t e[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) e[j] = (c + j >= 0 && c + j < cols) ? row[c + j] : 0u;
   return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
 
-template <bool ALIGNED>
-__device__ __forceinline__ void store8(uint16_t* row, int c, int cols, uint4 v) {
-  if (ALIGNED) {
-    if (c < cols) *reinterpret_cast<uint4*>(row + c) = v;
+// The groups of NT rows (a null row is not read) as BF16, zero outside [0, cols). Whole vectors are
+// read at a row's ends too, and what is not the row's is masked off (no branch: everything is in
+// flight together). `inner`: the vectors at the ends lie between the tensor's first and last
+// element; in its first and last row they are read element by element.
+template <int NT, int VPT, int ACCESS>
+__device__ __forceinline__ void load_rows(uint4 (&v)[NT][VPT], const uint16_t* const (&row)[NT], const int (&col)[VPT],
+                                          int cols, bool inner) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) v[t][k] = make_uint4(0u, 0u, 0u, 0u);
+  if (ACCESS == kElements || (ACCESS == kShared && !inner)) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+        if (row[t] != nullptr) v[t][k] = load_elements(row[t], col[k], cols);
     return;
   }
-  if (c >= 0 && c + 8 <= cols && (reinterpret_cast<uintptr_t>(row + c) & 15u) == 0) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+      if (row[t] != nullptr && col[k] < cols) v[t][k] = *reinterpret_cast<const uint4*>(row[t] + col[k]);
+  if (ACCESS == kShared) {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int n = cols - col[k];  // elements up to the row's end
+      uint32_t m[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        m[j] = n >= 2 * j + 2 ? 0xFFFFFFFFu : n == 2 * j + 1 ? 0x0000FFFFu : 0u;
+        if (k == 0) {  // only a thread's first group can begin before the row
+          const int c = col[0] + 2 * j;
+          m[j] &= c >= 0 ? 0xFFFFFFFFu : c == -1 ? 0xFFFF0000u : 0u;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        v[t][k].x &= m[0];
+        v[t][k].y &= m[1];
+        v[t][k].z &= m[2];
+        v[t][k].w &= m[3];
+      }
+    }
+  }
+}
+
+// The part of a vector of eight 2-byte elements that lies in the row, in at most three naturally aligned pieces a
+// side (the vector's own place is 16-byte aligned): elements a .. b-1.
+__device__ __forceinline__ void store_part(uint16_t* at, uint4 v, int a, int b) {
+  if (a <= 0 && b >= 8) return;
+  auto half = [&](int j) { const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w; return static_cast<uint16_t>(j & 1 ? w >> 16 : w); };
+  if (a > 0 && b >= 8) {  // a row's first group: the elements from a on
+    if (a & 1) at[a] = half(a);
+    const int c = (a + 1) & ~1;
+    if (c & 2) *reinterpret_cast<uint32_t*>(at + c) = c == 2 ? v.y : v.w;
+    if (c <= 4) *reinterpret_cast<uint2*>(at + 4) = make_uint2(v.z, v.w);
+    return;
+  }
+  if (a <= 0) {  // its last group: the elements before b
+    if (b & 4) *reinterpret_cast<uint2*>(at) = make_uint2(v.x, v.y);
+    const int c = b & 4;
+    if (b & 2) *reinterpret_cast<uint32_t*>(at + c) = c ? v.z : v.x;
+    if (b & 1) at[b - 1] = half(b - 1);
+    return;
+  }
+  for (int j = a; j < b; ++j) at[j] = half(j);  // a row inside one group
+}
+
+template <int ACCESS>
+__device__ __forceinline__ void store8(uint16_t* row, int c, int cols, uint4 v) {
+  if (ACCESS != kElements && (ACCESS == kAligned ? c < cols : whole(c, cols))) {
     *reinterpret_cast<uint4*>(row + c) = v;
+    return;
+  }
+  if (ACCESS == kAligned) return;
+  if (ACCESS == kShared) {
+    if (edge(c, cols)) store_part(row + c, v, -c, cols - c);
     return;
   }
   const uint32_t e[4] = {v.x, v.y, v.z, v.w};
@@ -106,17 +181,32 @@ __device__ __forceinline__ void store8(uint16_t* row, int c, int cols, uint4 v) 
     if (c + j >= 0 && c + j < cols) row[c + j] = static_cast<uint16_t>(e[j / 2] >> (16 * (j & 1)));
 }
 
-template <bool ALIGNED>
+template <int ACCESS>
 __device__ __forceinline__ void store8_bytes(uint8_t* row, int c, int cols, uint2 v) {
-  if (c >= 0 && c + 8 <= cols && (ALIGNED || (reinterpret_cast<uintptr_t>(row + c) & 7u) == 0)) {
+  if (ACCESS != kElements && (ACCESS == kAligned ? c < cols : whole(c, cols))) {
     *reinterpret_cast<uint2*>(row + c) = v;
     return;
   }
-  if (ALIGNED) return;
+  if (ACCESS == kAligned || (ACCESS == kShared && !edge(c, cols))) return;
   const uint32_t e[2] = {v.x, v.y};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     if (c + j >= 0 && c + j < cols) row[c + j] = static_cast<uint8_t>(e[j / 4] >> (8 * (j & 3)));
+}
+
+// The weight of a thread's groups: once per CTA, so element by element unless rows are aligned.
+template <int VPT, int ACCESS>
+__device__ __forceinline__ void load_weight(uint4 (&w)[VPT], const uint16_t* weight, const int (&col)[VPT], int cols) {
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    constexpr uint32_t kOnes = 0x3F803F80u;
+    w[k] = make_uint4(kOnes, kOnes, kOnes, kOnes);
+    if (weight == nullptr) continue;
+    if (ACCESS == kAligned)
+      w[k] = col[k] < cols ? *reinterpret_cast<const uint4*>(weight + col[k]) : make_uint4(0u, 0u, 0u, 0u);
+    else
+      w[k] = load_elements(weight, col[k], cols);
+  }
 }
 
 // Four FP32 values -> E4M3 codes (to nearest, ties to even; beyond 448 -> 448; NaN -> NaN), first in the low byte.
@@ -176,6 +266,12 @@ __device__ __forceinline__ uint32_t block_max_bits(uint32_t v, uint32_t* slots, 
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// Whether the 16-byte vectors at the ends of a row lie between the first element of the first row and the last
+// element of the last one (strides are at least cols).
+__device__ __forceinline__ bool row_inner(long long row, int rows, int cols) {
+  return row * cols >= 7 && (rows - 1 - row) * cols >= 7;
+}
+
 // The columns by which a row starts past a 16-byte boundary.
 __device__ __forceinline__ int row_phase(const uint16_t* row) {
   return static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 7u);
@@ -183,35 +279,36 @@ __device__ __forceinline__ int row_phase(const uint16_t* row) {
 
 // ---------------------------------------------------------------- forward
 
-template <int VPT, int FORMAT, bool ALIGNED>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
+// Registers per thread by groups per thread: 1024 threads with one group, 512 with more, and with two or
+// four as few as hold a row without spills, so that several CTAs fit on an SM.
+template <int VPT>
+constexpr int norm_regs(int two, int four) { return VPT == 1 ? 64 : VPT == 2 ? two : VPT == 4 ? four : 128; }
+
+template <int VPT, int FORMAT, int ACCESS>
+__global__ void __maxnreg__(norm_regs<VPT>(64, 80)) rms_norm_kernel(const NormParams p) {
   __shared__ float slots[2][32];
   __shared__ uint32_t slots_max[2][32];
   const int warps = blockDim.x >> 5;
   pdl_launch_dependents();
   pdl_wait();
-  const int phase = ALIGNED ? 0 : row_phase(p.x + blockIdx.x * p.ldx);
+  const int phase = ACCESS == kAligned ? 0 : row_phase(p.x + blockIdx.x * p.ldx);
   int col[VPT];
-  uint4 w[VPT];
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
+  for (int k = 0; k < VPT; ++k)
     col[k] = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x)) - phase;
-    constexpr uint32_t kOnes = 0x3F803F80u;
-    w[k] = p.w != nullptr ? load8<ALIGNED>(p.w, col[k], p.cols) : make_uint4(kOnes, kOnes, kOnes, kOnes);
-  }
+  uint4 w[VPT];
+  load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
   int parity = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
-    uint4 s[VPT];
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) s[k] = load8<ALIGNED>(p.x + row * p.ldx, col[k], p.cols);
+    uint4 in[2][VPT];
+    const uint16_t* const rows[2] = {p.x + row * p.ldx, p.r != nullptr ? p.r + row * p.ldr : nullptr};
+    load_rows<2, VPT, ACCESS>(in, rows, col, p.cols, row_inner(row, p.rows, p.cols));
+    uint4(&s)[VPT] = in[0];
     if (p.r != nullptr) {
-      uint4 r[VPT];
-#pragma unroll
-      for (int k = 0; k < VPT; ++k) r[k] = load8<ALIGNED>(p.r + row * p.ldr, col[k], p.cols);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         F8 a = unpack8(s[k]);
-        const F8 b = unpack8(r[k]);
+        const F8 b = unpack8(in[1][k]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a.v[j] += b.v[j];
         s[k] = pack8(a);
@@ -220,7 +317,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (p.s != nullptr) store8<ALIGNED>(p.s + row * p.lds, col[k], p.cols, s[k]);
+      if (p.s != nullptr) store8<ACCESS>(p.s + row * p.lds, col[k], p.cols, s[k]);
       const F8 a = unpack8(s[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = fmaf(a.v[j], a.v[j], sum);
@@ -235,7 +332,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
         const F8 g = unpack8(w[k]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a.v[j] = a.v[j] * rstd * g.v[j];
-        store8<ALIGNED>(static_cast<uint16_t*>(p.y) + row * p.ldy, col[k], p.cols, pack8(a));
+        store8<ACCESS>(static_cast<uint16_t*>(p.y) + row * p.ldy, col[k], p.cols, pack8(a));
       }
     } else if constexpr (FORMAT == GEMM_NORM_E4M3) {
       uint32_t top = 0;
@@ -244,7 +341,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
         const F8 a = unpack8(s[k]), g = unpack8(w[k]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (ALIGNED || (col[k] + j >= 0 && col[k] + j < p.cols)) top = max(top, abs_bits(a.v[j] * rstd * g.v[j]));
+          top = max(top, abs_bits(a.v[j] * rstd * g.v[j]));
       }
       top = block_max_bits(top, slots_max[parity], warps);
       const float scale = __uint_as_float(top) / 448.0f;
@@ -258,7 +355,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
         const F8 g = unpack8(w[k]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a.v[j] = a.v[j] * rstd * g.v[j] * inverse;
-        store8_bytes<ALIGNED>(static_cast<uint8_t*>(p.y) + row * p.ldy, col[k], p.cols,
+        store8_bytes<ACCESS>(static_cast<uint8_t*>(p.y) + row * p.ldy, col[k], p.cols,
                               make_uint2(e4m3x4(a.v[0], a.v[1], a.v[2], a.v[3]), e4m3x4(a.v[4], a.v[5], a.v[6], a.v[7])));
       }
     } else {
@@ -289,32 +386,31 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
 
 // ---------------------------------------------------------------- backward
 
-template <int VPT, bool ALIGNED>
-__global__ void __launch_bounds__(1024) rms_norm_backward_kernel(const NormBackwardParams p) {
+template <int VPT, int ACCESS>
+__global__ void __maxnreg__(norm_regs<VPT>(80, 128)) rms_norm_backward_kernel(const NormBackwardParams p) {
   __shared__ float slots[2][32];
   const int warps = blockDim.x >> 5;
   pdl_launch_dependents();
   pdl_wait();
-  const int phase = ALIGNED ? 0 : row_phase(p.s + blockIdx.x * p.lds);
+  const int phase = ACCESS == kAligned ? 0 : row_phase(p.s + blockIdx.x * p.lds);
   int col[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k)
+    col[k] = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x)) - phase;
   uint4 w[VPT];
   F8 dw[VPT];
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    col[k] = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x)) - phase;
-    constexpr uint32_t kOnes = 0x3F803F80u;
-    w[k] = p.w != nullptr ? load8<ALIGNED>(p.w, col[k], p.cols) : make_uint4(kOnes, kOnes, kOnes, kOnes);
+  for (int k = 0; k < VPT; ++k)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[k].v[j] = 0.0f;
-  }
+  load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
   int parity = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
-    uint4 s[VPT], dy[VPT];
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      s[k] = load8<ALIGNED>(p.s + row * p.lds, col[k], p.cols);
-      dy[k] = load8<ALIGNED>(p.dy + row * p.lddy, col[k], p.cols);
-    }
+    uint4 in[3][VPT];
+    const uint16_t* const rows[3] = {p.s + row * p.lds, p.dy + row * p.lddy,
+                                     p.ds != nullptr ? p.ds + row * p.ldds : nullptr};
+    load_rows<3, VPT, ACCESS>(in, rows, col, p.cols, row_inner(row, p.rows, p.cols));
+    const uint4(&s)[VPT] = in[0], (&dy)[VPT] = in[1], (&ds)[VPT] = in[2];
     const float rstd = p.rstd[row];
     float sum = 0.0f;
 #pragma unroll
@@ -335,11 +431,11 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_kernel(const NormBackw
 #pragma unroll
       for (int j = 0; j < 8; ++j) o.v[j] = rstd * (d.v[j] * g.v[j] - a.v[j] * rstd * c);
       if (p.ds != nullptr) {
-        const F8 e = unpack8(load8<ALIGNED>(p.ds + row * p.ldds, col[k], p.cols));
+        const F8 e = unpack8(ds[k]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) o.v[j] += e.v[j];
       }
-      store8<ALIGNED>(p.dx + row * p.lddx, col[k], p.cols, pack8(o));
+      store8<ACCESS>(p.dx + row * p.lddx, col[k], p.cols, pack8(o));
     }
   }
   if (p.partial != nullptr) {
@@ -352,46 +448,58 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_kernel(const NormBackw
   }
 }
 
-// dw[c] = sum of the partial rows in order: 8 warps take every eighth row of 32 columns, then add up.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, int rows, int cols, float* dw) {
-  __shared__ float part[8][33];
+// dw[c] = sum of the partial rows in a fixed order: 32 warps take every 32nd row of 32 columns, then add up.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const float* partial, int rows, int cols, float* dw) {
+  __shared__ float part[kSumWarps][33];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.0f;
   if (c < cols)
-    for (int r = warp; r < rows; r += 8) v += partial[static_cast<long long>(r) * cols + c];
+    for (int r = warp; r < rows; r += kSumWarps) v += partial[static_cast<long long>(r) * cols + c];
   part[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && c < cols) {
     v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v += part[k][lane];
+    for (int k = 0; k < kSumWarps; ++k) v += part[k][lane];
     dw[c] = v;
   }
 }
 
 // ---------------------------------------------------------------- host side
 
+// Groups of 8 columns per thread for many rows.
+constexpr int kForwardGroups = 4, kBackwardGroups = 2;
+
 struct NormShape {
-  int threads, vpt, grid;
+  int threads, vpt;
 };
 
-// Threads and groups per thread that hold a row, and persistent CTAs to fill the SMs' threads.
-NormShape norm_shape(int rows, int cols, int num_sms, bool aligned) {
+// Threads and groups per thread that hold a row.
+//   Few rows (no more than SMs): one group per thread, the shortest time from load to output.
+//   Many rows: `many` groups per thread, so that an SM holds several CTAs whose reductions overlap
+//   the others' loads.
+NormShape norm_shape(int rows, int cols, int num_sms, bool aligned, int many) {
   const int groups = ceil_div(cols, 8) + (aligned ? 0 : 1);
   NormShape s;
-  s.vpt = groups <= 1024 ? 1 : groups <= 2048 ? 2 : 4;
-  s.threads = std::max(32, ceil_div(ceil_div(groups, s.vpt), 32) * 32);
-  const int per_sm = std::max(1, 2048 / s.threads);
-  const int most = std::max(8, num_sms * std::min(per_sm, 8) / 8 * 8);
-  s.grid = std::min(rows, most);
-  return s;
+  s.vpt = rows <= num_sms ? 1 : many;
+  if (s.vpt > 1 && s.vpt < 4 && ceil_div(groups, s.vpt) > 288) s.vpt *= 2;
+  for (;; s.vpt *= 2) {
+    const int most = s.vpt == 1 ? 1024 : 512;
+    s.threads = std::max(32, ceil_div(ceil_div(groups, s.vpt), 32) * 32);
+    if (s.threads <= most) return s;
+  }
 }
 
-template <typename P, typename K>
-int launch(K kernel, int grid, int threads, cudaStream_t stream, const P& p) {
+// CTAs of a persistent launch: as many as fit on the SMs together, a multiple of 8, or one per row.
+int norm_grid(const void* kernel, int rows, int threads, int num_sms) {
+  return std::min(rows, std::max(8, num_sms * resident_ctas(kernel, threads) / 8 * 8));
+}
+
+int norm_launch(const void* kernel, int grid, int threads, cudaStream_t stream, void** args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -401,7 +509,7 @@ int launch(K kernel, int grid, int threads, cudaStream_t stream, const P& p) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
+  if (cudaLaunchKernelExC(&cfg, kernel, args) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
   }
@@ -409,25 +517,37 @@ int launch(K kernel, int grid, int threads, cudaStream_t stream, const P& p) {
   return GEMM_OK;
 }
 
+template <int FORMAT, int ACCESS>
+const void* forward_kernel(int vpt) {
+  return vpt == 1   ? reinterpret_cast<const void*>(rms_norm_kernel<1, FORMAT, ACCESS>)
+         : vpt == 2 ? reinterpret_cast<const void*>(rms_norm_kernel<2, FORMAT, ACCESS>)
+         : vpt == 4 ? reinterpret_cast<const void*>(rms_norm_kernel<4, FORMAT, ACCESS>)
+                    : reinterpret_cast<const void*>(rms_norm_kernel<8, FORMAT, ACCESS>);
+}
 template <int FORMAT>
-int launch_forward(const NormShape& s, bool aligned, cudaStream_t stream, const NormParams& p) {
-  if (aligned) {
-    if (s.vpt == 1) return launch(rms_norm_kernel<1, FORMAT, true>, s.grid, s.threads, stream, p);
-    if (s.vpt == 2) return launch(rms_norm_kernel<2, FORMAT, true>, s.grid, s.threads, stream, p);
-    return launch(rms_norm_kernel<4, FORMAT, true>, s.grid, s.threads, stream, p);
-  }
-  if constexpr (FORMAT != GEMM_NORM_NVFP4) {
-    if (s.vpt == 1) return launch(rms_norm_kernel<1, FORMAT, false>, s.grid, s.threads, stream, p);
-    if (s.vpt == 2) return launch(rms_norm_kernel<2, FORMAT, false>, s.grid, s.threads, stream, p);
-    return launch(rms_norm_kernel<4, FORMAT, false>, s.grid, s.threads, stream, p);
-  }
-  return GEMM_ERR_MISALIGNED;
+const void* forward_kernel(int vpt, bool aligned, bool shared) {
+  return aligned  ? forward_kernel<FORMAT, kAligned>(vpt)
+         : shared ? forward_kernel<FORMAT, kShared>(vpt)
+                  : forward_kernel<FORMAT, kElements>(vpt);
 }
 
-// Whether every row of a tensor of 2-byte elements starts on a 16-byte boundary.
-bool rows_aligned(const void* p, long long ld, int bytes = 16) {
-  return (reinterpret_cast<uintptr_t>(p) % bytes) == 0 && ld % 8 == 0;
+template <int ACCESS>
+const void* backward_kernel(int vpt) {
+  return vpt == 1   ? reinterpret_cast<const void*>(rms_norm_backward_kernel<1, ACCESS>)
+         : vpt == 2 ? reinterpret_cast<const void*>(rms_norm_backward_kernel<2, ACCESS>)
+         : vpt == 4 ? reinterpret_cast<const void*>(rms_norm_backward_kernel<4, ACCESS>)
+                    : reinterpret_cast<const void*>(rms_norm_backward_kernel<8, ACCESS>);
 }
+
+// A tensor's rows against 16-byte boundaries: the elements of the first row and of the stride past one.
+struct RowPlace {
+  unsigned first, stride;
+  RowPlace(const void* p, long long ld, int bytes)
+      : first(static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) / bytes % 8)), stride(static_cast<unsigned>(ld % 8)) {}
+  bool operator==(const RowPlace& o) const { return first == o.first && stride == o.stride; }
+  bool aligned() const { return first == 0 && stride == 0; }
+};
+
 bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 }  // namespace
@@ -469,18 +589,22 @@ int gemm_rms_norm(const void* X, const void* R, const void* W, void* S, void* Y,
   p.rows = rows;
   p.cols = cols;
   p.eps = eps;
-  const bool aligned = cols % 8 == 0 && rows_aligned(X, p.ldx) && (R == nullptr || rows_aligned(R, p.ldr)) &&
-                       rows_aligned(W, 0) && (S == nullptr || rows_aligned(S, p.lds)) &&
-                       (format == GEMM_NORM_NVFP4 || rows_aligned(Y, p.ldy, format == GEMM_NORM_BF16 ? 16 : 8));
+  const RowPlace place(X, p.ldx, 2);
+  bool shared = (R == nullptr || RowPlace(R, p.ldr, 2) == place) && (S == nullptr || RowPlace(S, p.lds, 2) == place);
+  if (format == GEMM_NORM_BF16) shared = shared && RowPlace(Y, p.ldy, 2) == place;
+  if (format == GEMM_NORM_E4M3) shared = shared && RowPlace(Y, p.ldy, 1) == place;  // (8-byte vectors of codes)
+  const bool aligned = shared && place.aligned() && cols % 8 == 0 && !misaligned(W, 16);
   if (format == GEMM_NORM_NVFP4 && !aligned) return GEMM_ERR_MISALIGNED;
   int device = 0, err = 0;
   const DeviceInfo* info = current_device_info(&device, &err);
   if (info == nullptr) return err;
-  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (format == GEMM_NORM_BF16) return launch_forward<GEMM_NORM_BF16>(shape, aligned, s, p);
-  if (format == GEMM_NORM_E4M3) return launch_forward<GEMM_NORM_E4M3>(shape, aligned, s, p);
-  return launch_forward<GEMM_NORM_NVFP4>(shape, aligned, s, p);
+  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned, kForwardGroups);
+  const void* kernel = format == GEMM_NORM_NVFP4  ? forward_kernel<GEMM_NORM_NVFP4, kAligned>(shape.vpt)
+                       : format == GEMM_NORM_E4M3 ? forward_kernel<GEMM_NORM_E4M3>(shape.vpt, aligned, shared)
+                                                  : forward_kernel<GEMM_NORM_BF16>(shape.vpt, aligned, shared);
+  void* args[] = {&p};
+  return norm_launch(kernel, norm_grid(kernel, rows, shape.threads, info->num_sms), shape.threads,
+                     static_cast<cudaStream_t>(stream), args);
 }
 
 int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const float* rstd, const void* dS, void* dX,
@@ -522,14 +646,20 @@ int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const f
   p.partial = nullptr;
   p.rows = rows;
   p.cols = cols;
-  const bool aligned = cols % 8 == 0 && rows_aligned(dY, p.lddy) && rows_aligned(S, p.lds) && rows_aligned(W, 0) &&
-                       (dS == nullptr || rows_aligned(dS, p.ldds)) && rows_aligned(dX, p.lddx);
-  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned);
+  const RowPlace place(S, p.lds, 2);
+  const bool shared = RowPlace(dY, p.lddy, 2) == place && (dS == nullptr || RowPlace(dS, p.ldds, 2) == place) &&
+                      RowPlace(dX, p.lddx, 2) == place;
+  const bool aligned = shared && place.aligned() && cols % 8 == 0 && !misaligned(W, 16);
+  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned, kBackwardGroups);
+  const void* kernel = aligned  ? backward_kernel<kAligned>(shape.vpt)
+                       : shared ? backward_kernel<kShared>(shape.vpt)
+                                : backward_kernel<kElements>(shape.vpt);
+  const int grid = norm_grid(kernel, rows, shape.threads, info->num_sms);
   void* ws = nullptr;
-  if (dW != nullptr && shape.grid > 1) {
+  if (dW != nullptr && grid > 1) {
     cudaMemPool_t pool = workspace_pool(device);
     if (pool == nullptr ||
-        cudaMallocFromPoolAsync(&ws, static_cast<size_t>(shape.grid) * cols * 4, pool, st) != cudaSuccess) {
+        cudaMallocFromPoolAsync(&ws, static_cast<size_t>(grid) * cols * 4, pool, st) != cudaSuccess) {
       cudaGetLastError();
       return GEMM_ERR_OUT_OF_MEMORY;
     }
@@ -537,33 +667,14 @@ int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const f
   } else if (dW != nullptr) {
     p.partial = dW;  // one CTA: its partial row is the sum
   }
-  int rc;
-  if (aligned)
-    rc = shape.vpt == 1   ? launch(rms_norm_backward_kernel<1, true>, shape.grid, shape.threads, st, p)
-         : shape.vpt == 2 ? launch(rms_norm_backward_kernel<2, true>, shape.grid, shape.threads, st, p)
-                          : launch(rms_norm_backward_kernel<4, true>, shape.grid, shape.threads, st, p);
-  else
-    rc = shape.vpt == 1   ? launch(rms_norm_backward_kernel<1, false>, shape.grid, shape.threads, st, p)
-         : shape.vpt == 2 ? launch(rms_norm_backward_kernel<2, false>, shape.grid, shape.threads, st, p)
-                          : launch(rms_norm_backward_kernel<4, false>, shape.grid, shape.threads, st, p);
+  void* args[] = {&p};
+  int rc = norm_launch(kernel, grid, shape.threads, st, args);
   if (ws != nullptr) {
     if (rc == GEMM_OK) {
-      cudaLaunchConfig_t cfg = {};
-      cudaLaunchAttribute attr[1];
-      cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(cols, 32)), 1, 1);
-      cfg.blockDim = dim3(256, 1, 1);
-      cfg.stream = st;
-      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[0].val.programmaticStreamSerializationAllowed = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaLaunchKernelEx(&cfg, column_sum_kernel, static_cast<const float*>(p.partial), shape.grid, cols, dW) !=
-          cudaSuccess) {
-        cudaGetLastError();
-        rc = GEMM_ERR_LAUNCH;
-      } else {
-        count_launch();
-      }
+      const float* partial = p.partial;
+      int partial_rows = grid;
+      void* sum_args[] = {&partial, &partial_rows, &cols, &dW};
+      rc = norm_launch(reinterpret_cast<const void*>(column_sum_kernel), ceil_div(cols, 32), 32 * kSumWarps, st, sum_args);
     }
     if (cudaFreeAsync(ws, st) != cudaSuccess && rc == GEMM_OK) rc = GEMM_ERR_LAUNCH;
   }
