@@ -16,6 +16,7 @@
 // columns). The MMA takes them as they lie in memory: TMA boxes of 64 columns x 128 rows put the
 // non-summed dimension innermost and the descriptors say so ("MN-major"), so nothing is transposed.
 //
+// A last wave of tiles at most half full runs as halves of its tiles (N = 128 MMAs).
 // A stage holds 128 (BF16) or 256 (E4M3) of the summed dimension, 8 MMAs per barrier wait, 3 stages.
 // Warp roles: 0 loads A, 2 loads B, 1 allocates TMEM and issues the MMAs (leader CTA), 4..7 epilogue,
 // one TMEM lane quadrant each; stores go through swizzled staging tiles and TMA.
@@ -31,6 +32,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "glu_act.cuh"
 #include "host_common.h"
 
 namespace dtcp {
@@ -40,6 +42,7 @@ enum GluMode { kGluForward = 0, kGluForwardE4m3 = 1, kGluDx = 2, kGluDw = 3 };
 struct GluParams {
   int rows, cols;        // of one output (dW: of dWg)
   int num_m_blocks, num_n_blocks, num_tiles, k_iters;
+  int split_tiles, num_items;  // trailing tiles cut into halves of their columns; work items = tiles + split_tiles
   int depth;             // the summed dimension (dX: of one half)
   int half_blocks;       // dW: M-blocks of dWg; the ones after them are dWu's
   int half_iters;        // dX: stages of the first half
@@ -109,42 +112,6 @@ __device__ __forceinline__ uint64_t umma_desc_mn(uint32_t smem_addr) {
          (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
 
-__device__ __forceinline__ float nan_max0(float v) {  // max(v, 0), NaN for NaN
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(0.0f));
-  return r;
-}
-
-// act(g). SiLU: g / (1 + exp(-g)); GELU, tanh form, as g / (1 + exp(-2 v)), v = sqrt(2/pi) (g + 0.044715 g^3).
-// An exponential that overflows gives 1 / inf = 0.
-__device__ __forceinline__ float glu_act(float g, int act) {
-  if (act == GEMM_GLU_SILU) return g * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * g));
-  if (act == GEMM_GLU_GELU_TANH) {
-    const float t = fmaf(0.044715f * g, g * g, g);
-    return g * rcp_approx(1.0f + ex2_approx(-2.302208198144325f * t));
-  }
-  return nan_max0(g);
-}
-
-// act(g) and act'(g).
-__device__ __forceinline__ void glu_act_grad(float g, int act, float& a, float& da) {
-  if (act == GEMM_GLU_SILU) {
-    const float s = rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * g));
-    a = g * s;
-    da = s * fmaf(g, 1.0f - s, 1.0f);
-  } else if (act == GEMM_GLU_GELU_TANH) {
-    const float t = fmaf(0.044715f * g, g * g, g);
-    const float s = rcp_approx(1.0f + ex2_approx(-2.302208198144325f * t));
-    a = g * s;
-    const float slope = s * (1.0f - s);  // 0 once s is 0 or 1, whatever the polynomial's size
-    const float dv = 1.5957691216057308f * fmaf(0.134145f * g, g, 1.0f);
-    da = slope == 0.0f ? s : fmaf(g * slope, dv, s);
-  } else {
-    a = nan_max0(g);
-    da = g > 0.0f ? 1.0f : (g != g ? g : 0.0f);
-  }
-}
-
 // ---------------------------------------------------------------- producers (warps 0, 2)
 
 template <int MODE>
@@ -159,8 +126,12 @@ __device__ __forceinline__ void glu_producer(const GluParams& p, const CUtensorM
   uint32_t stage = 0, phase = 0;
   bool ok = true;
   int it = 0;
-  for (int i = cluster_idx; i < p.num_tiles && ok; i += num_clusters, ++it) {
-    const TileCoord tc = tile_coord(i, p.num_m_blocks, p.num_n_blocks, p.group_m);
+  for (int i = cluster_idx; i < p.num_items && ok; i += num_clusters, ++it) {
+    const WorkItem w = work_item(i, p.num_tiles, p.split_tiles);
+    const TileCoord tc = tile_coord(w.tile, p.num_m_blocks, p.num_n_blocks, p.group_m);
+    const int half = w.half > 0 ? 1 : 0;
+    const int b_boxes = w.half >= 0 ? 1 : 2;  // of 64 rows (K-major: per atom) or 64 columns (MN-major)
+    const uint32_t stage_bytes = L::OPERAND_BYTES + L::OPERAND_BYTES / 2 * b_boxes;
     const bool down = (it & 1) != 0;  // start on the blocks the last wave of tiles read last
     const CUtensorMap* map = m0;
     int first;  // the operand's first row (K-major) or column (MN-major)
@@ -173,9 +144,9 @@ __device__ __forceinline__ void glu_producer(const GluParams& p, const CUtensorM
       first = mb * L::TILE_M + static_cast<int>(rank) * L::CTA_M;
     } else if (MODE == kGluForward || MODE == kGluForwardE4m3) {
       if (rank == 1) map = m1;
-      first = tc.n_blk * L::FEATURES;
+      first = tc.n_blk * L::FEATURES + half * (L::FEATURES / 2);
     } else {
-      first = tc.n_blk * L::BLOCK_N + static_cast<int>(rank) * L::B_ROWS;
+      first = tc.n_blk * L::BLOCK_N + half * (L::BLOCK_N / 2) + static_cast<int>(rank) * 64 * b_boxes;
     }
     for (int kb = 0; kb < p.k_iters; ++kb) {
       if (!wait_phase_inline(bar_empty + 8 * stage, phase ^ 1u, wctx, status_code(kRoleProducer, stage))) {
@@ -188,15 +159,24 @@ __device__ __forceinline__ void glu_producer(const GluParams& p, const CUtensorM
         if (k >= p.half_iters) k -= p.half_iters;
       }
       const uint32_t full = bar_full + 8 * stage;
-      if (load_a && rank == 0) mbar_arrive_expect_tx(full, 2u * L::STAGE_BYTES);
+      if (load_a && rank == 0) mbar_arrive_expect_tx(full, 2u * stage_bytes);
       const uint32_t bar = mapa_shared(full, 0);
       const uint32_t dst = dst0 + stage * L::OPERAND_BYTES;
+      if (load_a ? A_MN : B_MN) {
+        const int boxes = load_a ? 2 : b_boxes;
+        for (int c = 0; c < boxes; ++c)
+          tma_load_2d_pair(dst + c * L::ATOM_BYTES, map, first + c * 64, k * STAGE_K, bar);
+      } else {
 #pragma unroll
-      for (int a = 0; a < L::ATOMS; ++a) {
-        if (load_a ? A_MN : B_MN)
-          tma_load_2d_pair(dst + a * L::ATOM_BYTES, map, first + a * 64, k * STAGE_K, bar);
-        else
-          tma_load_2d_pair(dst + a * L::ATOM_BYTES, map, k * STAGE_K + a * (STAGE_K / L::ATOMS), first, bar);
+        for (int a = 0; a < L::ATOMS; ++a) {
+          const int x = k * STAGE_K + a * (STAGE_K / L::ATOMS);
+          if (load_a) {
+            tma_load_2d_pair(dst + a * L::ATOM_BYTES, map, x, first, bar);
+          } else {
+            for (int c = 0; c < b_boxes; ++c)
+              tma_load_2d_pair(dst + a * L::ATOM_BYTES + c * (L::ATOM_BYTES / 2), map, x, first + c * 64, bar);
+          }
+        }
       }
       stage = stage + 1 == L::STAGES ? 0u : stage + 1;
       phase = stage == 0 ? phase ^ 1u : phase;
@@ -213,7 +193,8 @@ __device__ __forceinline__ void glu_mma(const GluParams& p, uint32_t base, uint3
   using L = GluLayout;
   constexpr bool A_MN = MODE == kGluDw, B_MN = MODE == kGluDx || MODE == kGluDw, E4M3 = MODE == kGluForwardE4m3;
   constexpr int STAGE_K = E4M3 ? 256 : 128, MMA_K = E4M3 ? 32 : 16;
-  constexpr uint32_t IDESC = E4M3 ? idesc_e4m3(256, L::BLOCK_N) : idesc_glu(256, L::BLOCK_N, A_MN, B_MN);
+  constexpr uint32_t IDESC_FULL = E4M3 ? idesc_e4m3(256, L::BLOCK_N) : idesc_glu(256, L::BLOCK_N, A_MN, B_MN);
+  constexpr uint32_t IDESC_HALF = E4M3 ? idesc_e4m3(256, L::BLOCK_N / 2) : idesc_glu(256, L::BLOCK_N / 2, A_MN, B_MN);
   const uint32_t bar_full = base + L::OFF_BAR, bar_empty = bar_full + 8 * L::STAGES;
   const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
   const uint64_t a0 = A_MN ? umma_desc_mn(base + L::OFF_A) : umma_desc_sw128(base + L::OFF_A);
@@ -226,7 +207,8 @@ __device__ __forceinline__ void glu_mma(const GluParams& p, uint32_t base, uint3
   uint32_t stage = 0, phase = 0;
   bool ok = true;
   int it = 0;
-  for (int i = cluster_idx; i < p.num_tiles && ok; i += num_clusters, ++it) {
+  for (int i = cluster_idx; i < p.num_items && ok; i += num_clusters, ++it) {
+    const uint32_t idesc = work_item(i, p.num_tiles, p.split_tiles).half >= 0 ? IDESC_HALF : IDESC_FULL;
     const bool down = (it & 1) != 0;
     const uint32_t slot = static_cast<uint32_t>(it) & 1u;
     if (!wait_phase_inline(bar_tempty + 8 * slot, ((static_cast<uint32_t>(it) >> 1) & 1u) ^ 1u, wctx,
@@ -249,8 +231,8 @@ __device__ __forceinline__ void glu_mma(const GluParams& p, uint32_t base, uint3
       const int steps = left >= STAGE_K ? L::KSTEPS : (left + MMA_K - 1) / MMA_K;
       auto one = [&](int kk) {
         const uint64_t ad = umma_desc_advance(a, step(A_MN, kk)), bd = umma_desc_advance(b, step(B_MN, kk));
-        if constexpr (E4M3) mma_e4m3_pair(d, ad, bd, IDESC, (kb | kk) != 0 ? 1u : 0u);
-        else mma_f16<2>(d, ad, bd, IDESC, (kb | kk) != 0 ? 1u : 0u);
+        if constexpr (E4M3) mma_e4m3_pair(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+        else mma_f16<2>(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
       };
       if (steps == L::KSTEPS) {
 #pragma unroll
@@ -335,9 +317,24 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const CUtensorM
   const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
   GluStaging st{base + L::OFF_EPI + q * L::EPI_BUFS * L::EPI_BUF_BYTES, 0u};
   int it = 0;
-  for (int i = cluster_idx; i < p.num_tiles; i += num_clusters, ++it) {
-    const TileCoord tc = tile_coord(i, p.num_m_blocks, p.num_n_blocks, p.group_m);
+  for (int i = cluster_idx; i < p.num_items; i += num_clusters, ++it) {
+    const WorkItem w = work_item(i, p.num_tiles, p.split_tiles);
+    const TileCoord tc = tile_coord(w.tile, p.num_m_blocks, p.num_n_blocks, p.group_m);
+    const int columns = w.half >= 0 ? L::BLOCK_N / 2 : L::BLOCK_N;  // of the item's accumulator
+    const int col0 = tc.n_blk * (FORWARD ? L::FEATURES : L::BLOCK_N) + (w.half > 0 ? columns / (FORWARD ? 2 : 1) : 0);
     const uint32_t slot = static_cast<uint32_t>(it) & 1u;
+    // E4M3: this lane's row scale and its features' scales, while the MMAs run
+    float x_scale = 1.0f, w_scale[2][L::FEATURES / 32];
+    if constexpr (MODE == kGluForwardE4m3) {
+      const int row = tc.m_blk * L::TILE_M + static_cast<int>(rank) * L::CTA_M + static_cast<int>(q * 32 + lane);
+      if (row < p.rows) x_scale = p.x_scale[row];
+#pragma unroll
+      for (int c = 0; c < L::FEATURES / 32; ++c) {
+        const int f = col0 + c * 32 + static_cast<int>(lane);
+        w_scale[0][c] = f < p.cols ? p.g_scale[f] : 0.0f;
+        w_scale[1][c] = f < p.cols ? p.u_scale[f] : 0.0f;
+      }
+    }
     if (!wait_phase_warp(bar_tfull + 8 * slot, (static_cast<uint32_t>(it) >> 1) & 1u, wctx,
                          status_code(kRoleEpilogue, slot)))
       break;
@@ -352,25 +349,27 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const CUtensorM
     const uint32_t taddr = tmem_base + ((q * 32u) << 16) + slot * L::ACC_COLS;
     if (row0 < p.rows) {
       if constexpr (FORWARD) {
-        float xs = 1.0f;
-        if (MODE == kGluForwardE4m3 && row0 + static_cast<int>(lane) < p.rows) xs = p.x_scale[row0 + lane];
-#pragma unroll 1
+        const float xs = x_scale;
+#pragma unroll MODE == kGluForwardE4m3 ? 4 : 1
         for (int c = 0; c < L::FEATURES; c += 32) {
-          const int col = tc.n_blk * L::FEATURES + c;
-          if (col >= p.cols) break;
+          const int col = col0 + c;
+          if (c >= columns / 2 || col >= p.cols) break;
+          float gs = 0.0f, us = 0.0f;  // E4M3: the scales of feature col + lane
+          if constexpr (MODE == kGluForwardE4m3) {
+            gs = w_scale[0][c / 32];
+            us = w_scale[1][c / 32];
+          }
           uint32_t g[32], u[32];
           tmem_ld_32x32b_x32(taddr + c, g);
-          tmem_ld_32x32b_x32(taddr + L::FEATURES + c, u);
+          tmem_ld_32x32b_x32(taddr + columns / 2 + c, u);
           tmem_ld_wait();
           float h[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             float gv = __uint_as_float(g[j]), uv = __uint_as_float(u[j]);
             if constexpr (MODE == kGluForwardE4m3) {
-              if (col + j < p.cols) {
-                gv *= xs * __ldg(p.g_scale + col + j);
-                uv *= xs * __ldg(p.u_scale + col + j);
-              }
+              gv *= xs * __shfl_sync(0xffffffffu, gs, j);
+              uv *= xs * __shfl_sync(0xffffffffu, us, j);
             }
             h[j] = glu_act(gv, p.act) * uv;
           }
@@ -382,8 +381,8 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const CUtensorM
         }
       } else {
 #pragma unroll 1
-        for (int c = 0; c < L::BLOCK_N; c += 32) {
-          const int col = tc.n_blk * L::BLOCK_N + c;
+        for (int c = 0; c < columns; c += 32) {
+          const int col = col0 + c;
           if (col >= p.cols) break;
           uint32_t v[32];
           tmem_ld_32x32b_x32(taddr + c, v);
@@ -540,6 +539,11 @@ int glu_max_clusters(int device) {
   return n;
 }
 
+// B's boxes are half its rows, so that a half tile's load is one box.
+int map_kb(CUtensorMap* m, const void* p, int depth, int rows) {
+  return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, depth, rows, uint64_t(depth) * 2, 64, 64,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+}
 // A BF16 operand with the summed dimension along its rows (K-major) or along its columns (MN-major).
 int map_k(CUtensorMap* m, const void* p, int depth, int rows, long long ld) {
   return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, depth, rows, uint64_t(ld) * 2, 64, 128,
@@ -567,7 +571,9 @@ int glu_launch(GluMaps& m, GluParams& p, int virtual_rows, int virtual_cols, int
   if (p.status == nullptr) return GEMM_ERR_NO_DEVICE;
   const int max_clusters = glu_max_clusters(device);
   if (max_clusters <= 0) return GEMM_ERR_LAUNCH;
-  const int clusters = std::min(p.num_tiles, max_clusters);
+  p.split_tiles = tail_split_tiles(p.num_tiles, max_clusters);
+  p.num_items = p.num_tiles + p.split_tiles;
+  const int clusters = std::min(p.num_items, max_clusters);
   p.group_m = choose_group_m(virtual_rows, virtual_cols, virtual_depth, L::TILE_M, L::BLOCK_N, bytes, 0.0, clusters,
                              info->l2_bytes);
   cudaLaunchConfig_t cfg = {};
@@ -646,11 +652,15 @@ int gemm_glu_bf16(const void* X, const void* Wg, const void* Wu, void* H, float*
     if (st == GEMM_OK && preact != nullptr) st = zero_rows(preact, size_t(N) * 8, (long long)N * 8, M, s);
     return st;
   }
+  if (M <= kGluFewRows) {
+    GluFewParams f = {X, Wg, Wu, static_cast<uint16_t*>(H), preact, nullptr, nullptr, nullptr, ld.x, ld.h, M, N, K, act};
+    return run_glu_few(f, false, s);
+  }
   GluMaps m;
   GluParams p = {};
   int st = map_k(&m.a0, X, K, M, ld.x);
-  if (st == GEMM_OK) st = map_k(&m.b0, Wg, K, N, K);
-  if (st == GEMM_OK) st = map_k(&m.b1, Wu, K, N, K);
+  if (st == GEMM_OK) st = map_kb(&m.b0, Wg, K, N);
+  if (st == GEMM_OK) st = map_kb(&m.b1, Wu, K, N);
   if (st == GEMM_OK) st = map_out(&m.c0, H, N, M, ld.h);
   if (st != GEMM_OK) return st;
   m.a1 = m.a0;
@@ -696,14 +706,18 @@ int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const flo
   if (info == nullptr) return err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (K == 0) return zero_rows(H, size_t(N) * 2, ld.h * 2, M, s);
+  if (M <= kGluFewRowsE4m3) {
+    GluFewParams f = {X, Wg, Wu, static_cast<uint16_t*>(H), nullptr, x_scale, wg_scale, wu_scale, ld.x, ld.h, M, N, K, act};
+    return run_glu_few(f, true, s);
+  }
   GluMaps m;
   GluParams p = {};
-  auto map8 = [&](CUtensorMap* t, const void* q, int rows, long long stride) {
-    return encode_tmap_2d(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, rows, stride, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  auto map8 = [&](CUtensorMap* t, const void* q, int rows, long long stride, int box_rows) {
+    return encode_tmap_2d(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, rows, stride, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  int st = map8(&m.a0, X, M, ld.x);
-  if (st == GEMM_OK) st = map8(&m.b0, Wg, N, K);
-  if (st == GEMM_OK) st = map8(&m.b1, Wu, N, K);
+  int st = map8(&m.a0, X, M, ld.x, 128);
+  if (st == GEMM_OK) st = map8(&m.b0, Wg, N, K, 64);
+  if (st == GEMM_OK) st = map8(&m.b1, Wu, N, K, 64);
   if (st == GEMM_OK) st = map_out(&m.c0, H, N, M, ld.h);
   if (st != GEMM_OK) return st;
   m.a1 = m.a0;
