@@ -186,23 +186,23 @@ int encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
 
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
-int resident_ctas(const void* kernel, int threads) {
+int resident_ctas(const void* kernel, int threads, int smem) {
   struct Entry {
     const void* kernel;
-    int threads, ctas;
+    int threads, smem, ctas;
   };
   static std::mutex mu;
   static Entry entries[128];
   static int count = 0;
   std::lock_guard<std::mutex> lock(mu);
   for (int i = 0; i < count; ++i)
-    if (entries[i].kernel == kernel && entries[i].threads == threads) return entries[i].ctas;
+    if (entries[i].kernel == kernel && entries[i].threads == threads && entries[i].smem == smem) return entries[i].ctas;
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) {
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) {
     cudaGetLastError();
     return 1;
   }
-  if (count < 128) entries[count++] = Entry{kernel, threads, n};
+  if (count < 128) entries[count++] = Entry{kernel, threads, smem, n};
   return n;
 }
 

@@ -36,8 +36,9 @@ unsigned* device_status_word(int device);
 
 void count_launch();
 
-// CTAs of `threads` threads (no dynamic shared memory) that an SM holds together; asked once per kernel and size.
-int resident_ctas(const void* kernel, int threads);
+// CTAs of `threads` threads and `smem` bytes of dynamic shared memory that an SM holds together; asked once per kernel
+// and size.
+int resident_ctas(const void* kernel, int threads, int smem);
 
 // Resolved per-call options.
 // Fused epilogue of the *_fused calls: C = act(alpha * acc + beta * C_old + bias[col]).

@@ -95,12 +95,12 @@ __device__ __forceinline__ uint4 load_elements(const uint16_t* row, int c, int c
 }
 
 // The groups of NT rows (a null row is not read) as BF16, zero outside [0, cols). Whole vectors are
-// read at a row's ends too, and what is not the row's is masked off (no branch: everything is in
-// flight together). `inner`: the vectors at the ends lie between the tensor's first and last
-// element; in its first and last row they are read element by element.
+// read at a row's ends too, and what is not the row's is masked off (after everything is in flight;
+// `ends`: bit k if group k of any lane of the warp is at an end). `inner`: the vectors at the ends lie
+// between the tensor's first and last element; in its first and last row they are read element by element.
 template <int NT, int VPT, int ACCESS>
 __device__ __forceinline__ void load_rows(uint4 (&v)[NT][VPT], const uint16_t* const (&row)[NT], const int (&col)[VPT],
-                                          int cols, bool inner) {
+                                          int cols, bool inner, uint32_t ends) {
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -121,6 +121,7 @@ __device__ __forceinline__ void load_rows(uint4 (&v)[NT][VPT], const uint16_t* c
   if (ACCESS == kShared) {
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
+      if (((ends >> k) & 1u) == 0) continue;
       const int n = cols - col[k];  // elements up to the row's end
       uint32_t m[4];
 #pragma unroll
@@ -146,7 +147,10 @@ __device__ __forceinline__ void load_rows(uint4 (&v)[NT][VPT], const uint16_t* c
 // side (the vector's own place is 16-byte aligned): elements a .. b-1.
 __device__ __forceinline__ void store_part(uint16_t* at, uint4 v, int a, int b) {
   if (a <= 0 && b >= 8) return;
-  auto half = [&](int j) { const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w; return static_cast<uint16_t>(j & 1 ? w >> 16 : w); };
+  auto half = [&](int j) {
+    const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
+    return static_cast<uint16_t>(j & 1 ? w >> 16 : w);
+  };
   if (a > 0 && b >= 8) {  // a row's first group: the elements from a on
     if (a & 1) at[a] = half(a);
     const int c = (a + 1) & ~1;
@@ -162,6 +166,15 @@ __device__ __forceinline__ void store_part(uint16_t* at, uint4 v, int a, int b) 
     return;
   }
   for (int j = a; j < b; ++j) at[j] = half(j);  // a row inside one group
+}
+
+// Bit k if group k of any lane of the warp is neither whole nor empty.
+template <int VPT>
+__device__ __forceinline__ uint32_t row_ends(const int (&col)[VPT], int cols) {
+  uint32_t ends = 0;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) ends |= __any_sync(0xffffffffu, edge(col[k], cols)) ? 1u << k : 0u;
+  return ends;
 }
 
 template <int ACCESS>
@@ -298,11 +311,12 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 80)) rms_norm_kernel(const NormPa
     col[k] = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x)) - phase;
   uint4 w[VPT];
   load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
+  const uint32_t ends = ACCESS == kShared ? row_ends(col, p.cols) : 0u;
   int parity = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
     uint4 in[2][VPT];
     const uint16_t* const rows[2] = {p.x + row * p.ldx, p.r != nullptr ? p.r + row * p.ldr : nullptr};
-    load_rows<2, VPT, ACCESS>(in, rows, col, p.cols, row_inner(row, p.rows, p.cols));
+    load_rows<2, VPT, ACCESS>(in, rows, col, p.cols, row_inner(row, p.rows, p.cols), ends);
     uint4(&s)[VPT] = in[0];
     if (p.r != nullptr) {
 #pragma unroll
@@ -356,7 +370,8 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 80)) rms_norm_kernel(const NormPa
 #pragma unroll
         for (int j = 0; j < 8; ++j) a.v[j] = a.v[j] * rstd * g.v[j] * inverse;
         store8_bytes<ACCESS>(static_cast<uint8_t*>(p.y) + row * p.ldy, col[k], p.cols,
-                              make_uint2(e4m3x4(a.v[0], a.v[1], a.v[2], a.v[3]), e4m3x4(a.v[4], a.v[5], a.v[6], a.v[7])));
+                              make_uint2(e4m3x4(a.v[0], a.v[1], a.v[2], a.v[3]),
+                                         e4m3x4(a.v[4], a.v[5], a.v[6], a.v[7])));
       }
     } else {
 #pragma unroll
@@ -372,8 +387,9 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 80)) rms_norm_kernel(const NormPa
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));  // the other 8 of the block's 16 columns
         const uint32_t code = e4m3_code(__uint_as_float(top) / 6.0f);
         const float sf = e4m3_value(code);
+        const float inverse = sf > 0.0f ? 1.0f / sf : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a.v[j] = sf > 0.0f ? a.v[j] / sf : 0.0f;
+        for (int j = 0; j < 8; ++j) a.v[j] *= inverse;
         if (col[k] < p.cols) {
           static_cast<uint32_t*>(p.y)[(row * p.cols + col[k]) / 8] = e2m1x8(a.v);
           if ((threadIdx.x & 1) == 0)
@@ -404,12 +420,13 @@ __global__ void __maxnreg__(norm_regs<VPT>(80, 128)) rms_norm_backward_kernel(co
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[k].v[j] = 0.0f;
   load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
+  const uint32_t ends = ACCESS == kShared ? row_ends(col, p.cols) : 0u;
   int parity = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
     uint4 in[3][VPT];
     const uint16_t* const rows[3] = {p.s + row * p.lds, p.dy + row * p.lddy,
                                      p.ds != nullptr ? p.ds + row * p.ldds : nullptr};
-    load_rows<3, VPT, ACCESS>(in, rows, col, p.cols, row_inner(row, p.rows, p.cols));
+    load_rows<3, VPT, ACCESS>(in, rows, col, p.cols, row_inner(row, p.rows, p.cols), ends);
     const uint4(&s)[VPT] = in[0], (&dy)[VPT] = in[1], (&ds)[VPT] = in[2];
     const float rstd = p.rstd[row];
     float sum = 0.0f;
@@ -458,6 +475,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const float*
   const int c = blockIdx.x * 32 + lane;
   float v = 0.0f;
   if (c < cols)
+#pragma unroll 8
     for (int r = warp; r < rows; r += kSumWarps) v += partial[static_cast<long long>(r) * cols + c];
   part[warp][lane] = v;
   __syncthreads();
@@ -471,8 +489,9 @@ __global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const float*
 
 // ---------------------------------------------------------------- host side
 
-// Groups of 8 columns per thread for many rows.
-constexpr int kForwardGroups = 4, kBackwardGroups = 2;
+// Groups of 8 columns per thread for many rows; measured on GB300: forward 4000 x 4096 20.6 us with 4 and 21.3 with 2,
+// off the 16-byte boundary 4001 x 4099 28.4 and 26.5; backward 33.1 us with 2 and 39.4 with 4.
+constexpr int kForwardGroups = 4, kForwardGroupsOff = 2, kBackwardGroups = 2;
 
 struct NormShape {
   int threads, vpt;
@@ -496,7 +515,7 @@ NormShape norm_shape(int rows, int cols, int num_sms, bool aligned, int many) {
 
 // CTAs of a persistent launch: as many as fit on the SMs together, a multiple of 8, or one per row.
 int norm_grid(const void* kernel, int rows, int threads, int num_sms) {
-  return std::min(rows, std::max(8, num_sms * resident_ctas(kernel, threads) / 8 * 8));
+  return std::min(rows, std::max(8, num_sms * resident_ctas(kernel, threads, 0) / 8 * 8));
 }
 
 int norm_launch(const void* kernel, int grid, int threads, cudaStream_t stream, void** args) {
@@ -598,7 +617,7 @@ int gemm_rms_norm(const void* X, const void* R, const void* W, void* S, void* Y,
   int device = 0, err = 0;
   const DeviceInfo* info = current_device_info(&device, &err);
   if (info == nullptr) return err;
-  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned, kForwardGroups);
+  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned, aligned ? kForwardGroups : kForwardGroupsOff);
   const void* kernel = format == GEMM_NORM_NVFP4  ? forward_kernel<GEMM_NORM_NVFP4, kAligned>(shape.vpt)
                        : format == GEMM_NORM_E4M3 ? forward_kernel<GEMM_NORM_E4M3>(shape.vpt, aligned, shared)
                                                   : forward_kernel<GEMM_NORM_BF16>(shape.vpt, aligned, shared);

@@ -4,20 +4,27 @@
 //   z = a l,  lse = log sum_j exp(z_j),  logprob = z_t - lse,  H = lse - sum_j p_j z_j,  p_j = exp(z_j - lse)
 //   dl_j = a (dlp (1[j = t] - p_j) - dH p_j (log p_j + H))
 //
-// One pass: a thread keeps the running maximum m of its logits, s = sum exp(a (l - m)) and
-// q = sum exp(a (l - m)) (l - m), all FP32; a larger maximum m' scales s by f = exp(a (m - m')) and
-// makes q (q + s (m - m')) f. Partial triples join by the same rule, so threads, warps and the CTAs of
-// a cluster that share a row combine in any fixed order: lse = a m + log s, H = log s - a q / s.
+// One pass in powers of two: with c = a log2(e), a thread keeps the maximum m of its logits, a reference logit r with
+// m - 16 / c <= r <= m, s = sum 2^t and q = sum t 2^t over t = c (l - r), all FP32. The scale of s and q costs FP32 no
+// precision, so r follows m only when m has run 16 / c ahead: s f and (q + s d) f with d = c (r - r'), f = 2^d; a
+// warp's lanes hardly ever do that after their first logits, where following every new maximum would cost a warp a
+// rescaling in almost every step. Partial results join by the same rule, so threads, warps and the CTAs of a cluster
+// that share a row combine in a fixed order: lse = a r + ln s, H = ln s - ln 2 q / s. Where c r is beyond 2^60, logits
+// that differ at all have no mass next to m: s counts the logits equal to m.
 //
-// Alternatives: logits are ordered by 64-bit keys (value, then the lower index), all different. The k-th
-// largest of the threads' maxima is no larger than the row part's k-th largest logit, so only the k
-// threads at or above it hold candidates, and only their logits are read again (from L2).
+// Alternatives: a value that k threads' maxima reach is no larger than the k-th largest logit. At a row's end the CTA
+// takes such a bound, and the threads whose maxima reach it have the logits read again (from L2) that may: each thread
+// remembers its two largest chunk maxima and the chunk of the first, so that is one chunk's part of 8 vectors for most
+// of them. The few logits that reach the bound are put in order by 64-bit keys (value, then the lower index), all
+// different. Logits of minus infinity take no part: where there are fewer others than are wanted, the lowest indices
+// follow.
 //
 // Bound by the bytes of the logits. A row is split over a cluster of 1 to 8 CTAs that join through
 // shared memory, so few rows still use many SMs and no workspace or second launch is needed.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "common.cuh"
@@ -25,10 +32,17 @@
 
 namespace dtcp {
 
-constexpr int kLogprobThreads = 512;
+constexpr int kLogprobThreads = 256;
 constexpr int kLogprobWarps = kLogprobThreads / 32;
 constexpr int kLogprobMaxTop = 32;
-constexpr float kLog2e = 1.4426950408889634f;
+// The row parts stream through a ring of chunks in shared memory: bulk copies keep chunks in flight without
+// holding registers, also through the reductions at a row's end, when they are the next row's.
+constexpr int kLogprobBatch = 8;  // vectors per thread and chunk
+constexpr int kLogprobChunk = kLogprobBatch * kLogprobThreads;  // vectors
+constexpr int kLogprobStages = 2;
+constexpr int kLogprobCtas = 3;  // per SM
+constexpr int kLogprobRingBytes = kLogprobStages * kLogprobChunk * 16;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct LogprobParams {
   const void* logits;
@@ -41,6 +55,8 @@ struct LogprobParams {
   long long ld;
   int rows, vocab, top, cluster;
   float scale;
+  unsigned* status;
+  unsigned long long wait_limit_ns;
 };
 
 struct LogprobBackwardParams {
@@ -73,7 +89,26 @@ template <>
 struct Vec<uint16_t> {  // BF16
   static constexpr int N = 8;
   static __device__ __forceinline__ float value(uint16_t e) { return __uint_as_float(static_cast<uint32_t>(e) << 16); }
-  static __device__ __forceinline__ uint16_t minus_inf() { return 0xFF80u; }
+  static constexpr uint32_t kMinusInfWord = 0xFF80FF80u;
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  // Largest element (NaN if one is) of `n` vectors, and pair j of the elements in packed FP32.
+  template <int M>
+  static __device__ __forceinline__ float largest(const uint4 (&p)[M]) {
+    uint32_t a[M];
+#pragma unroll
+    for (int u = 0; u < M; ++u) a[u] = max2(max2(p[u].x, p[u].y), max2(p[u].z, p[u].w));
+#pragma unroll
+    for (int u = 1; u < M; ++u) a[0] = max2(a[0], a[u]);
+    return max_nan(__uint_as_float(a[0] << 16), __uint_as_float(a[0] & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint64_t pair(uint4 p, int j) {
+    const uint32_t w = j == 0 ? p.x : j == 1 ? p.y : j == 2 ? p.z : p.w;
+    return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
   static __device__ __forceinline__ void unpack(uint4 p, float (&v)[8]) {
     const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
@@ -96,7 +131,22 @@ template <>
 struct Vec<float> {
   static constexpr int N = 4;
   static __device__ __forceinline__ float value(float e) { return e; }
-  static __device__ __forceinline__ float minus_inf() { return kMinusInf; }
+  static constexpr uint32_t kMinusInfWord = 0xFF800000u;
+  template <int M>
+  static __device__ __forceinline__ float largest(const uint4 (&p)[M]) {
+    float a[M];
+#pragma unroll
+    for (int u = 0; u < M; ++u)
+      a[u] = max_nan(max_nan(__uint_as_float(p[u].x), __uint_as_float(p[u].y)),
+                     max_nan(__uint_as_float(p[u].z), __uint_as_float(p[u].w)));
+#pragma unroll
+    for (int u = 1; u < M; ++u) a[0] = max_nan(a[0], a[u]);
+    return a[0];
+  }
+  static __device__ __forceinline__ uint64_t pair(uint4 p, int j) {
+    return j == 0 ? f2_pack(__uint_as_float(p.x), __uint_as_float(p.y))
+                  : f2_pack(__uint_as_float(p.z), __uint_as_float(p.w));
+  }
   static __device__ __forceinline__ void unpack(uint4 p, float (&v)[4]) {
     v[0] = __uint_as_float(p.x);
     v[1] = __uint_as_float(p.y);
@@ -119,8 +169,13 @@ struct Row {
     phase = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
     vectors = static_cast<int>((static_cast<long long>(n) + phase + Vec<T>::N - 1) / Vec<T>::N);
   }
+  // First vector of part `k` of `parts`.
+  __device__ __forceinline__ int begin(int k, int parts) const {
+    return static_cast<int>(static_cast<long long>(vectors) * k / parts);
+  }
   __device__ __forceinline__ int first(int v) const { return v * Vec<T>::N - phase; }
   __device__ __forceinline__ bool whole(int v) const { return first(v) >= 0 && first(v) <= vocab - Vec<T>::N; }
+  __device__ __forceinline__ uint4 raw(int v) const { return *reinterpret_cast<const uint4*>(base + first(v)); }
   // Minus infinity outside the row.
   __device__ __forceinline__ void load(int v, float (&x)[Vec<T>::N]) const {
     const int c = first(v);
@@ -130,6 +185,63 @@ struct Row {
     }
 #pragma unroll
     for (int j = 0; j < Vec<T>::N; ++j) x[j] = (c + j >= 0 && c + j < vocab) ? Vec<T>::value(base[c + j]) : kMinusInf;
+  }
+};
+
+// Part `k` of `parts` of a row: vectors [v0, v1), of which [n0, n1) are whole. Thread (v - n0) mod 512 owns vector v.
+template <typename T>
+struct Part {
+  int v0, v1, n0, n1;
+  __device__ __forceinline__ Part(const Row<T>& row, int k, int parts) {
+    v0 = row.begin(k, parts);
+    v1 = row.begin(k + 1, parts);
+    n0 = v0;
+    n1 = v1;
+    if (v0 == v1) return;
+    if (v0 == 0 && !row.whole(0)) n0 = 1;
+    if (n1 == row.vectors && n1 > n0 && !row.whole(n1 - 1)) --n1;
+  }
+  __device__ __forceinline__ int owner(int v) const { return (v - n0) & (kLogprobThreads - 1); }
+};
+
+// Copies `bytes` (a multiple of 16) from global to this CTA's shared memory, both at 16-byte boundaries; completion is
+// counted on the mbarrier `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// The chunks of this CTA's row parts in order, one row after another (one thread's state).
+template <typename T>
+struct Feed {
+  const T* logits;
+  long long ld, row, step;
+  int rows, vocab, rank, cluster;
+  int at, end;  // next vector and end of the current row part
+  const T* base;
+  int phase;
+
+  __device__ __forceinline__ void start(long long r) {
+    for (row = r; row < rows; row += step) {
+      const Row<T> x(logits + row * ld, vocab);
+      const Part<T> part(x, rank, cluster);
+      if (part.n0 < part.n1) {
+        base = x.base;
+        phase = x.phase;
+        at = part.n0;
+        end = part.n1;
+        return;
+      }
+    }
+  }
+  __device__ __forceinline__ void issue(uint32_t dst, uint32_t bar) {
+    if (row >= rows) return;
+    const int n = min(end - at, kLogprobChunk);
+    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n) * 16u);
+    bulk_load(dst, base + (static_cast<long long>(at) * Vec<T>::N - phase), static_cast<uint32_t>(n) * 16u, bar);
+    at += n;
+    if (at == end) start(row + step);
   }
 };
 
@@ -155,45 +267,43 @@ __device__ __forceinline__ unsigned long long warp_max_key(unsigned long long ke
   return static_cast<unsigned long long>(hi) << 32 | lo;
 }
 
-// Descending order over the lanes of a warp (bitonic).
-__device__ __forceinline__ unsigned long long warp_sort(unsigned long long key) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
-    for (int stride = size / 2; stride > 0; stride >>= 1) {
-      const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, stride);
-      const bool keep_max = ((lane & stride) == 0) == ((lane & size) == 0);
-      key = keep_max ? (key > other ? key : other) : (key < other ? key : other);
-    }
-  }
-  return key;
-}
+constexpr float kAhead = 16.0f;                        // (m - r) c at most
+constexpr float kOrdinary = 1.152921504606847e18f;     // |r c| below 2^60
 
-struct Triple {
-  float m, s, q;
+// Sums of a part of a row, relative to its reference (see above); m minus infinity: no mass.
+struct Sums {
+  float m, ref, s, q;
 };
 
-__device__ __forceinline__ float clamp_low(float d) { return max_nan(d, -1.0e30f); }
+// c (from - to), with no mass (and no NaN) left where that has no finite value.
+__device__ __forceinline__ float shift(float from, float to, float c) { return fmaxf((from - to) * c, -1.0e30f); }
 
-// Joins two parts of a row; c = a log2(e). A part whose maximum is minus infinity holds no mass.
-__device__ __forceinline__ Triple join(const Triple& a, const Triple& b, float c) {
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c) {
   if (a.m == kMinusInf) return b;
   if (b.m == kMinusInf) return a;
-  Triple r;
+  Sums r;
   r.m = max_nan(a.m, b.m);
-  const float da = clamp_low(a.m - r.m), db = clamp_low(b.m - r.m);
-  const float fa = ex2_approx(da * c), fb = ex2_approx(db * c);
-  r.s = a.s * fa + b.s * fb;
-  r.q = (a.q + a.s * da) * fa + (b.q + b.s * db) * fb;
+  if (a.ref == b.ref) {
+    r.ref = a.ref;
+    r.s = a.s + b.s;
+    r.q = a.q + b.q;
+    return r;
+  }
+  const bool a_low = a.m < b.m;  // (a NaN has made s one, whichever way this goes)
+  const Sums lo = a_low ? a : b, hi = a_low ? b : a;
+  const float d = shift(lo.ref, hi.ref, c), f = ex2_approx(d);
+  r.ref = hi.ref;
+  r.s = fmaf(lo.s, f, hi.s);
+  r.q = fmaf(fmaf(lo.s, d, lo.q), f, hi.q);
   return r;
 }
 
-__device__ __forceinline__ Triple warp_join(Triple t, float c) {
+__device__ __forceinline__ Sums warp_join(Sums t, float c) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    Triple u;
+    Sums u;
     u.m = __shfl_xor_sync(0xffffffffu, t.m, o);
+    u.ref = __shfl_xor_sync(0xffffffffu, t.ref, o);
     u.s = __shfl_xor_sync(0xffffffffu, t.s, o);
     u.q = __shfl_xor_sync(0xffffffffu, t.q, o);
     t = join(t, u, c);
@@ -212,208 +322,451 @@ __device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
   return v;
 }
 
+constexpr int kLogprobList = 768;  // candidates of a row part
+constexpr int kLogprobDeep = 6;    // largest values of each warp that a bound is taken from
+
 struct LogprobShared {
-  Triple parts[kLogprobWarps];
-  Triple total;
-  unsigned long long lists[kLogprobWarps][32];  // each warp's thread maxima in order; then candidates
-  unsigned long long winners[kLogprobMaxTop];   // the CTA's k largest thread maxima
-  unsigned long long top[kLogprobMaxTop];       // the CTA's k largest logits
+  Sums parts[kLogprobWarps];
+  Sums total;
+  uint32_t highest[2][kLogprobDeep][kLogprobWarps];  // each warp's largest values in order, for the two bounds of a row
+  unsigned long long cand[kLogprobList];
+  unsigned long long survivors[kLogprobThreads];
+  unsigned long long top[kLogprobMaxTop];  // the CTA's k largest logits
   unsigned long long best[kLogprobWarps];
-  unsigned long long joined[8 * kLogprobMaxTop];
-  int candidates;
+  unsigned long long full[kLogprobStages], empty[kLogprobStages];  // mbarriers of the ring
+  uint32_t winner[kLogprobThreads];  // threads whose logits are read again, with the chunk
+  int candidates, left, winners, scanners;
+  uint32_t abort;
 };
 
-// The `top` largest logits of this CTA's vectors [v0, v1) into sh.top, in order (0 where there are fewer).
-template <typename T>
-__device__ void select_top(LogprobShared& sh, const Row<T>& row, int v0, int v1, int thread_vector, int top) {
-  constexpr int N = Vec<T>::N;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // this thread's largest logit, the lowest index first
-  unsigned long long mine = 0;
-  if (thread_vector < v1) {
-    float x[N];
-    row.load(thread_vector, x);
-    const int c = row.first(thread_vector);
+// The order of logits as unsigned numbers: 0 for minus infinity (and for none).
+__device__ __forceinline__ uint32_t order_of(float l) {
+  return l == kMinusInf ? 0u : static_cast<uint32_t>(key_of(l, 0) >> 32);
+}
+__device__ __forceinline__ float order_value(uint32_t o) {
+  return o == 0 ? kMinusInf : key_value(static_cast<unsigned long long>(o) << 32);
+}
+
+// An order that at least `top` of the threads' orders reach, or 0: if j of them in each of r warps reach one and
+// j r >= top, top do; the largest such one over j is the r-th largest of the warps' j-th largest. One barrier.
+__device__ __forceinline__ uint32_t cta_bound(uint32_t (&highest)[kLogprobDeep][kLogprobWarps], uint32_t mine,
+                                              int top) {
+  static_assert(kLogprobWarps == 8, "groups of 8 lanes take one value of each warp");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (c + j >= 0 && c + j < row.vocab) {
-        const unsigned long long key = key_of(x[j], c + j);
-        mine = key > mine ? key : mine;
-      }
-  }
-  sh.lists[warp][lane] = warp_sort(mine);
-  if (tid < kLogprobMaxTop) sh.top[tid] = 0;
-  if (tid == 0) sh.candidates = 0;
-  __syncthreads();
-  if (warp == 0) {
-    int at = 0;
-    unsigned long long head = lane < kLogprobWarps ? sh.lists[lane][0] : 0ull;
-    for (int j = 0; j < top; ++j) {
-      const unsigned long long best = warp_max_key(head);
-      if (lane == 0) sh.winners[j] = best;
-      if (head == best && best != 0) {
-        ++at;
-        head = at < 32 ? sh.lists[lane][at] : 0ull;
-      }
+  for (int j = 0; j < kLogprobDeep; ++j) {
+    const uint32_t most = __reduce_max_sync(0xffffffffu, mine);
+    if (lane == __ffs(static_cast<int>(__ballot_sync(0xffffffffu, mine == most))) - 1) {
+      highest[j][warp] = most;
+      mine = 0u;
     }
   }
   __syncthreads();
-  const unsigned long long threshold = sh.winners[top - 1];  // 0: fewer threads hold logits than are wanted
-  unsigned long long* cand = &sh.lists[0][0];
-  for (int j = warp; j < top; j += kLogprobWarps) {
-    const unsigned long long key = sh.winners[j];
-    if (key == 0) break;
-    const int owner = ((key_index(key) + row.phase) / N - v0) % kLogprobThreads;
-    for (int v = v0 + owner + lane * kLogprobThreads; v < v1; v += 32 * kLogprobThreads) {
-      float x[N];
-      row.load(v, x);
-      const int c = row.first(v);
+  uint32_t bound = 0u;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (c + i >= 0 && c + i < row.vocab) {
-          const unsigned long long k = key_of(x[i], c + i);
-          if (k >= threshold) {
-            const int n = atomicAdd(&sh.candidates, 1);
-            if (n < kLogprobThreads) cand[n] = k;
-          }
-        }
+  for (int j0 = 0; j0 < kLogprobDeep; j0 += 4) {
+    const int j = j0 + (lane >> 3), i = lane & 7;
+    const uint32_t v = j < kLogprobDeep ? highest[j][i] : 0u;
+    int larger = 0;
+#pragma unroll
+    for (int x = 1; x < 8; ++x) {
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, v, x);
+      larger += other > v || (other == v && (i ^ x) < i) ? 1 : 0;
     }
+    if (larger == (top + j) / (j + 1) - 1) bound = v > bound ? v : bound;
   }
-  __syncthreads();
-  const int n = sh.candidates;
-  if (n <= kLogprobThreads) {
-    // the order by counting: keys are all different, so the places do not depend on the order of arrival
-    if (tid < n) {
-      const unsigned long long key = cand[tid];
-      int rank = 0;
-      for (int i = 0; i < n; ++i) rank += cand[i] > key ? 1 : 0;
-      if (rank < top) sh.top[rank] = key;
-    }
-    __syncthreads();
-    return;
+  return __reduce_max_sync(0xffffffffu, bound);
+}
+
+__device__ __forceinline__ void list_candidate(LogprobShared& sh, unsigned long long key) {
+  const int n = atomicAdd(&sh.candidates, 1);
+  if (n < kLogprobList) sh.cand[n] = key;
+}
+
+// The largest logit of a thread's part of each chunk: the largest of them, its chunk, and the second largest (NaN:
+// there may be any number of large ones).
+struct Peaks {
+  float first, second;
+  int chunk;
+  __device__ __forceinline__ void see(float most, int at) {
+    const bool more = most > first || (most != most && first == first);
+    float low;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(low) : "f"(most), "f"(first));
+    second = max_nan(second, low);
+    first = max_nan(first, most);
+    chunk = more ? at : chunk;
   }
-  // more candidates than places for them (long runs of large logits in few threads): the largest one below the last, `top` times
+};
+
+// The `top` largest keys into sh.top by taking the largest one below the last, `top` times. below(last): the
+// thread's largest key below `last`.
+template <typename F>
+__device__ __forceinline__ void extract_top(LogprobShared& sh, int top, F below) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long last = ~0ull;
   for (int j = 0; j < top; ++j) {
-    unsigned long long best = 0;
-    for (int w = warp; w < top; w += kLogprobWarps) {
-      const unsigned long long key = sh.winners[w];
-      if (key == 0) break;
-      const int owner = ((key_index(key) + row.phase) / N - v0) % kLogprobThreads;
-      for (int v = v0 + owner + lane * kLogprobThreads; v < v1; v += 32 * kLogprobThreads) {
+    const unsigned long long best = warp_max_key(below(last));
+    if (lane == 0) sh.best[warp] = best;
+    __syncthreads();
+    last = warp_max_key(lane < kLogprobWarps ? sh.best[lane] : 0ull);
+    if (threadIdx.x == 0) sh.top[j] = last;
+    __syncthreads();
+  }
+}
+
+// The `top` largest logits of this CTA's part of a row into sh.top, in order (0 where there are fewer). The logits of
+// vectors that are not whole have been listed (before a barrier).
+template <typename T>
+__device__ void select_top(LogprobShared& sh, const Row<T>& row, const Part<T>& part, const Peaks& peaks, int top) {
+  constexpr int N = Vec<T>::N;
+  const int tid = threadIdx.x;
+  const float bound = order_value(cta_bound(sh.highest[0], order_of(peaks.first), top));
+  auto reaches = [&](float l) { return !(l < bound) && l != kMinusInf; };  // (a NaN does)
+  // the threads whose logits are read again: one chunk of them, or all
+  if (reaches(peaks.first)) {
+    if (reaches(peaks.second)) sh.winner[kLogprobThreads - 1 - atomicAdd(&sh.scanners, 1)] = static_cast<uint32_t>(tid);
+    else sh.winner[atomicAdd(&sh.winners, 1)] = static_cast<uint32_t>(tid) | static_cast<uint32_t>(peaks.chunk) << 8;
+  }
+  __syncthreads();
+  auto list = [&](int v) {
+    if (v >= part.n1) return;
+    const uint4 w[1] = {row.raw(v)};
+    if (!reaches(Vec<T>::largest(w))) return;
+    float x[N];
+    Vec<T>::unpack(w[0], x);
+    const int c = row.first(v);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (reaches(x[j])) list_candidate(sh, key_of(x[j], c + j));
+  };
+  for (int i = tid; i < sh.winners * kLogprobBatch; i += kLogprobThreads) {
+    const uint32_t w = sh.winner[i / kLogprobBatch];
+    list(part.n0 + static_cast<int>(w >> 8) * kLogprobChunk + (i % kLogprobBatch) * kLogprobThreads +
+         static_cast<int>(w & 0xFFu));
+  }
+  const int steps = (part.n1 - part.n0 + kLogprobThreads - 1) / kLogprobThreads;
+  for (int k = 0; k < sh.scanners; ++k)
+    for (int i = tid; i < steps; i += kLogprobThreads)
+      list(part.n0 + static_cast<int>(sh.winner[kLogprobThreads - 1 - k]) + i * kLogprobThreads);
+  __syncthreads();
+  const int n = sh.candidates;
+  if (n > kLogprobList) {
+    // more candidates than the list holds (very many equal ones): from the row itself
+    extract_top(sh, top, [&](unsigned long long last) {
+      unsigned long long best = 0;
+      for (int v = part.v0 + tid; v < part.v1; v += kLogprobThreads) {
         float x[N];
         row.load(v, x);
         const int c = row.first(v);
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (c + i >= 0 && c + i < row.vocab) {
+          if (x[i] != kMinusInf && c + i >= 0 && c + i < row.vocab) {
             const unsigned long long k = key_of(x[i], c + i);
             if (k < last && k > best) best = k;
           }
       }
-    }
-    best = warp_max_key(best);
-    if (lane == 0) sh.best[warp] = best;
-    __syncthreads();
-    last = warp_max_key(lane < kLogprobWarps ? sh.best[lane] : 0ull);
-    if (tid == 0) sh.top[j] = last;
-    __syncthreads();
+      return best;
+    });
+    return;
   }
+  const unsigned long long* keys = sh.cand;
+  int left = n;
+  if (n > kLogprobThreads) {
+    // cut the list by a bound of its own
+    uint32_t mine = 0;
+    for (int i = tid; i < n; i += kLogprobThreads) mine = max(mine, static_cast<uint32_t>(sh.cand[i] >> 32));
+    const uint32_t cut = cta_bound(sh.highest[1], mine, top);
+    for (int i = tid; i < n; i += kLogprobThreads)
+      if (static_cast<uint32_t>(sh.cand[i] >> 32) >= cut) {
+        const int k = atomicAdd(&sh.left, 1);
+        if (k < kLogprobThreads) sh.survivors[k] = sh.cand[i];
+      }
+    __syncthreads();
+    keys = sh.survivors;
+    left = sh.left;
+  }
+  if (left <= kLogprobThreads) {
+    // the order by counting: keys are all different, so the places do not depend on the order of arrival
+    if (tid < left) {
+      const unsigned long long key = keys[tid];
+      int place = 0;
+#pragma unroll 8
+      for (int i = 0; i < left; ++i) place += keys[i] > key ? 1 : 0;
+      if (place < top) sh.top[place] = key;
+    }
+    __syncthreads();
+    return;
+  }
+  extract_top(sh, top, [&](unsigned long long last) {
+    unsigned long long best = 0;
+    for (int i = tid; i < n; i += kLogprobThreads)
+      if (sh.cand[i] < last && sh.cand[i] > best) best = sh.cand[i];
+    return best;
+  });
 }
 
+// What a thread has seen of its row: its sums in two lanes of packed FP32.
+struct Running {
+  float m, ref;
+  uint64_t s, q;
+
+  // (not NaN, not infinite)
+  __device__ __forceinline__ bool ordinary(float c) const { return fabsf(ref * c) < kOrdinary; }
+  // Logits follow of which `top` is the largest.
+  __device__ __forceinline__ void see(float top, float c) {
+    const bool none = m == kMinusInf;
+    m = max_nan(m, top);
+    if (none ? m != kMinusInf : !((m - ref) * c <= kAhead)) {
+      if (!none) {
+        const float d = shift(ref, m, c), f = ex2_approx(d);
+        const uint64_t f2 = f2_pack(f, f);
+        q = f2_mul(f2_fma(s, f2_pack(d, d), q), f2);
+        s = f2_mul(s, f2);
+      }
+      ref = m;
+    }
+  }
+  // Two logits. CLAMP: they may be minus infinity, or so low that c l is (t 2^t is no number then).
+  template <bool CLAMP>
+  __device__ __forceinline__ void add(uint64_t x2, uint64_t c2, uint64_t minus_ref2) {
+    uint64_t t2 = f2_mul(f2_add(x2, minus_ref2), c2);
+    float t0, t1;
+    f2_unpack(t2, t0, t1);
+    if (CLAMP) {
+      t0 = fmaxf(t0, -1.0e30f);
+      t1 = fmaxf(t1, -1.0e30f);
+      t2 = f2_pack(t0, t1);
+    }
+    const uint64_t e2 = f2_pack(ex2_approx(t0), ex2_approx(t1));
+    s = f2_add(s, e2);
+    q = f2_fma(e2, t2, q);
+  }
+  // The same where the reference is no ordinary number.
+  __device__ __forceinline__ void count(float x0, float x1) {
+    const float bad = m == m && m != -kMinusInf ? 0.0f : __uint_as_float(0x7FFFFFFFu);
+    s = f2_add(s, f2_pack(x0 == ref && bad == 0.0f ? 1.0f : bad, x1 == ref && bad == 0.0f ? 1.0f : bad));
+  }
+};
+
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLogprobThreads) token_logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_kernel(const LogprobParams p) {
   constexpr int N = Vec<T>::N;
   __shared__ LogprobShared sh;
+  extern __shared__ __align__(128) uint8_t ring[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const long long r = blockIdx.x / p.cluster;
+  const int clusters = gridDim.x / p.cluster;
+  const long long r0 = blockIdx.x / p.cluster;
+  const uint32_t full = smem_u32(sh.full), empty = smem_u32(sh.empty), ring_addr = smem_u32(ring);
+  constexpr uint32_t STAGE = kLogprobChunk * 16;
+  if (tid == 0) {
+    for (int s = 0; s < kLogprobStages; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, kLogprobWarps);
+    }
+    sh.abort = 0u;
+    fence_mbarrier_init_cluster();
+  }
+  __syncthreads();
+  const WaitCtx wctx{&sh.abort, p.status, p.wait_limit_ns};
   pdl_launch_dependents();
   pdl_wait();
-  const Row<T> row(static_cast<const T*>(p.logits) + r * p.ld, p.vocab);
-  const int v0 = static_cast<int>(static_cast<long long>(row.vectors) * rank / p.cluster);
-  const int v1 = static_cast<int>(static_cast<long long>(row.vectors) * (rank + 1) / p.cluster);
+  Feed<T> feed;
+  if (tid == 0) {
+    feed.logits = static_cast<const T*>(p.logits);
+    feed.ld = p.ld;
+    feed.step = clusters;
+    feed.rows = p.rows;
+    feed.vocab = p.vocab;
+    feed.rank = rank;
+    feed.cluster = p.cluster;
+    feed.start(r0);
+    for (int s = 0; s < kLogprobStages; ++s) feed.issue(ring_addr + s * STAGE, full + 8 * s);
+  }
   const float c = p.scale * kLog2e;
-
-  Triple t{kMinusInf, 0.0f, 0.0f};
-  float ref = 0.0f;  // t.m, or 0 while it is minus infinity
-  int best_vector = v0 + tid;
-  for (int v = v0 + tid; v < v1; v += kLogprobThreads) {
-    float x[N];
-    row.load(v, x);
-    float top = x[0];
+  const uint64_t c2 = f2_pack(c, c);
+  uint32_t stage = 0, parity = 0;  // of the next chunk
+  uint32_t chunks = 0;
+  bool ok = true;  // after a wait that gave up: no more waiting, the launch runs out (its results are void)
+  for (long long r = r0; r < p.rows; r += clusters) {
+    const Row<T> row(static_cast<const T*>(p.logits) + r * p.ld, p.vocab);
+    const Part<T> part(row, rank, p.cluster);
+    Running run{kMinusInf, 0.0f, 0ull, 0ull};
+    bool masked = false;
+    auto add_slow = [&](float x0, float x1) {
+      if (run.ordinary(c)) run.add<true>(f2_pack(x0, x1), c2, f2_pack(-run.ref, -run.ref));
+      else run.count(x0, x1);
+    };
+    // a vector at the row's ends that is partly outside it: its thread takes it element by element
+    auto partial = [&](int v) {
+      float x[N];
+      row.load(v, x);
+      float top = x[0];
 #pragma unroll
-    for (int j = 1; j < N; ++j) top = max_nan(top, x[j]);
-    if (!(top <= t.m)) {
-      const float m = max_nan(t.m, top);
-      if (t.m != kMinusInf) {
-        const float d = clamp_low(t.m - m), f = ex2_approx(d * c);
-        t.q = (t.q + t.s * d) * f;
-        t.s *= f;
-      }
-      if (t.m == t.m) best_vector = v;  // (the first NaN stays the largest)
-      t.m = ref = m;
-    }
+      for (int j = 1; j < N; ++j) top = max_nan(top, x[j]);
+      if (TOP) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const float d = clamp_low(x[j] - ref), e = ex2_approx(d * c);
-      t.s += e;
-      t.q = fmaf(e, d, t.q);
-    }
-  }
-  t = warp_join(t, c);
-  if (lane == 0) sh.parts[warp] = t;
-  __syncthreads();
-  if (warp == 0) {
-    t = lane < kLogprobWarps ? sh.parts[lane] : Triple{kMinusInf, 0.0f, 0.0f};
-    t = warp_join(t, c);
-    if (lane == 0) sh.total = t;
-  }
-  if constexpr (TOP) select_top(sh, row, v0, v1, best_vector, p.top);
-
-  if (p.cluster > 1) cluster_sync_all();
-  else __syncthreads();
-  if (rank == 0) {
-    const uint32_t total_addr = smem_u32(&sh.total);
-    Triple all = sh.total;
-    for (int k = 1; k < p.cluster; ++k) {
-      const uint32_t a = mapa_shared(total_addr, k);
-      all = join(all, Triple{__uint_as_float(ld_cluster_u32(a)), __uint_as_float(ld_cluster_u32(a + 4)),
-                             __uint_as_float(ld_cluster_u32(a + 8))},
-                 c);
-    }
-    const bool empty = all.m == kMinusInf;  // no logit has any mass
-    const float log_s = logf(all.s);
-    const float lse = empty ? kMinusInf : fmaf(p.scale, all.m, log_s);
-    if (tid == 0) {
-      p.lse[r] = lse;
-      p.entropy[r] = empty ? 0.0f : log_s - p.scale * (all.q / all.s);
-      if (p.logprob != nullptr) {
-        const long long token = p.tokens[r];
-        float lp = 0.0f;
-        if (token >= p.vocab) lp = __uint_as_float(0x7FFFFFFFu);
-        else if (token >= 0) lp = empty ? kMinusInf : p.scale * (Vec<T>::value(row.base[token]) - all.m) - log_s;
-        p.logprob[r] = lp;
+        for (int j = 0; j < N; ++j)
+          if (x[j] != kMinusInf) list_candidate(sh, key_of(x[j], row.first(v) + j));  // (what is no part of the row is)
       }
-    }
-    if constexpr (TOP) {
-      const int n = p.cluster * p.top;
-      unsigned long long key = 0;
-      if (tid < n) key = ld_cluster_u64(mapa_shared(smem_u32(&sh.top[tid % p.top]), tid / p.top));
-      if (tid < n) sh.joined[tid] = key;
-      __syncthreads();
-      if (key != 0) {
-        int place = 0;
-        for (int i = 0; i < n; ++i) place += sh.joined[i] > key ? 1 : 0;
-        if (place < p.top) {
-          const long long at = r * p.top + place;
-          p.top_ids[at] = key_index(key);
-          p.top_logprobs[at] = empty ? kMinusInf : p.scale * (key_value(key) - all.m) - log_s;
+      run.see(top, c);
+#pragma unroll
+      for (int j = 0; j < N; j += 2) add_slow(x[j], x[j + 1]);
+    };
+    Peaks peaks{kMinusInf, kMinusInf, 0};
+    if (TOP && tid == 0) sh.candidates = sh.left = sh.winners = sh.scanners = 0;
+    if (TOP && tid < kLogprobMaxTop) sh.top[tid] = 0;
+    if (TOP) __syncthreads();
+    if (part.v0 < part.n0 && tid == kLogprobThreads - 1) partial(part.v0);
+    for (int v = part.n0; v < part.n1; v += kLogprobChunk) {
+      if (tid == 0 && chunks > 0 && ok) {
+        // the chunk before this one: refill its place once every warp has read it
+        const uint32_t s = stage == 0 ? kLogprobStages - 1 : stage - 1;
+        const uint32_t ph = stage == 0 ? parity ^ 1u : parity;
+        ok = wait_phase(empty + 8 * s, ph, wctx, status_code(kRoleProducer, s));
+        if (ok) feed.issue(ring_addr + s * STAGE, full + 8 * s);
+      }
+      if (ok) ok = wait_phase(full + 8 * stage, parity, wctx, status_code(kRoleEpilogue, stage));
+      const uint32_t src = ring_addr + stage * STAGE + static_cast<uint32_t>(tid) * 16u;
+      const int left = part.n1 - v - tid;
+      uint4 raw[kLogprobBatch];
+      if (part.n1 - v >= kLogprobChunk) {
+#pragma unroll
+        for (int u = 0; u < kLogprobBatch; ++u)
+          ld_shared_v4(src + u * (kLogprobThreads * 16), raw[u].x, raw[u].y, raw[u].z, raw[u].w);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kLogprobBatch; ++u) {
+          constexpr uint32_t kNone = Vec<T>::kMinusInfWord;
+          raw[u] = make_uint4(kNone, kNone, kNone, kNone);
+          if (u * kLogprobThreads < left)
+            ld_shared_v4(src + u * (kLogprobThreads * 16), raw[u].x, raw[u].y, raw[u].z, raw[u].w);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(empty + 8 * stage);
+      ++chunks;
+      stage = stage + 1 == kLogprobStages ? 0u : stage + 1;
+      parity = stage == 0 ? parity ^ 1u : parity;
+      const float most = Vec<T>::largest(raw);
+      if (TOP) peaks.see(most, (v - part.n0) / kLogprobChunk);
+      run.see(most, c);
+      if (run.ordinary(c)) {
+        const uint64_t minus_ref2 = f2_pack(-run.ref, -run.ref);
+        const Running before = run;
+        const bool full_chunk = part.n1 - v >= kLogprobChunk;  // (else some of `raw` is minus infinity)
+        if (!masked && full_chunk) {
+#pragma unroll
+          for (int u = 0; u < kLogprobBatch; ++u)
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) run.add<false>(Vec<T>::pair(raw[u], j), c2, minus_ref2);
+          float q0, q1;
+          f2_unpack(run.q, q0, q1);
+          if (q0 != q0 || q1 != q1) {  // logits without mass among them: from here on with a clamp
+            masked = true;
+            run = before;
+          }
+        }
+        if (masked || !full_chunk) {
+#pragma unroll
+          for (int u = 0; u < kLogprobBatch; ++u)
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) run.add<true>(Vec<T>::pair(raw[u], j), c2, minus_ref2);
+        }
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < kLogprobBatch; ++u) {
+          float x[N];
+          uint4 w = raw[0];
+#pragma unroll
+          for (int i = 1; i < kLogprobBatch; ++i)
+            if (u == i) w = raw[i];
+          Vec<T>::unpack(w, x);
+#pragma unroll
+          for (int j = 0; j < N; j += 2) run.count(x[j], x[j + 1]);
         }
       }
     }
+    if (part.n1 < part.v1 && part.owner(part.n1) == tid) partial(part.n1);
+    Sums t;
+    {
+      float s0, s1, q0, q1;
+      f2_unpack(run.s, s0, s1);
+      f2_unpack(run.q, q0, q1);
+      t = Sums{run.m, run.ref, s0 + s1, q0 + q1};
+    }
+    t = warp_join(t, c);
+    if (lane == 0) sh.parts[warp] = t;
+    __syncthreads();
+    if (warp == 0) {
+      t = lane < kLogprobWarps ? sh.parts[lane] : Sums{kMinusInf, 0.0f, 0.0f, 0.0f};
+      t = warp_join(t, c);
+      if (lane == 0) sh.total = t;
+    }
+    if constexpr (TOP) select_top(sh, row, part, peaks, p.top);
+
+    if (p.cluster > 1) cluster_sync_all();
+    else __syncthreads();
+    if (rank == 0) {
+      const uint32_t total_addr = smem_u32(&sh.total);
+      Sums all = sh.total;
+      for (int k = 1; k < p.cluster; ++k) {
+        const uint32_t a = mapa_shared(total_addr, k);
+        all = join(all, Sums{__uint_as_float(ld_cluster_u32(a)), __uint_as_float(ld_cluster_u32(a + 4)),
+                             __uint_as_float(ld_cluster_u32(a + 8)), __uint_as_float(ld_cluster_u32(a + 12))},
+                   c);
+      }
+      const bool empty = all.m == kMinusInf;  // no logit has any mass
+      const float log_s = logf(all.s);
+      const float lse = empty ? kMinusInf : fmaf(p.scale, all.ref, log_s);
+      // log probability of a logit: no mass next to a reference that is no ordinary number, unless it is that number
+      const bool ordinary = fabsf(all.ref * c) < kOrdinary;
+      auto logp = [&](float l) {
+        if (empty) return kMinusInf;
+        if (ordinary || all.s != all.s) return p.scale * (l - all.ref) - log_s;
+        return l == all.ref ? -log_s : kMinusInf;
+      };
+      if (tid == 0) {
+        p.lse[r] = lse;
+        p.entropy[r] = empty ? 0.0f : log_s - kLn2 * (all.q / all.s);
+        if (p.logprob != nullptr) {
+          const long long token = p.tokens[r];
+          float lp = 0.0f;
+          if (token >= p.vocab) lp = __uint_as_float(0x7FFFFFFFu);
+          else if (token >= 0) lp = logp(Vec<T>::value(row.base[token]));
+          p.logprob[r] = lp;
+        }
+      }
+      if constexpr (TOP) {
+        const int n = p.cluster * p.top;
+        unsigned long long key = 0;
+        if (tid < n) key = ld_cluster_u64(mapa_shared(smem_u32(&sh.top[tid % p.top]), tid / p.top));
+        if (tid < n) sh.cand[tid] = key;
+        const int listed = __syncthreads_count(key != 0);  // (n <= 256)
+        auto write = [&](int place, int index, float l) {
+          if (place >= p.top) return;
+          p.top_ids[r * p.top + place] = index;
+          p.top_logprobs[r * p.top + place] = logp(l);
+        };
+        if (key != 0) {
+          int place = 0;
+#pragma unroll 8
+          for (int i = 0; i < n; ++i) place += sh.cand[i] > key ? 1 : 0;
+          write(place, key_index(key), key_value(key));
+        }
+        if (listed < p.top && tid < 32) {
+          // logits of minus infinity take the places left: the lowest indices, all among the first `top`
+          const bool none = lane < p.top && Vec<T>::value(row.base[lane]) == kMinusInf;
+          const uint32_t all_none = __ballot_sync(0xffffffffu, none);
+          if (none) write(listed + __popc(all_none & ((1u << lane) - 1u)), lane, kMinusInf);
+        }
+      }
+    }
+    // the CTAs' shared memory is read until here
+    if (p.cluster > 1) cluster_sync_all();
+    else __syncthreads();
   }
-  if (p.cluster > 1) cluster_sync_all();  // the others' shared memory is read until here
+  if (tid == 0 && !ok) settle_after_abort();
 }
 
 // ---------------------------------------------------------------- backward
@@ -449,7 +802,7 @@ __global__ void __launch_bounds__(kLogprobBackThreads) token_logprobs_backward_k
     const int c = row.first(v);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const float logp = clamp_low(fmaf(x[j], p.scale, -lse));
+      const float logp = max_nan(fmaf(x[j], p.scale, -lse), -1.0e30f);
       x[j] = ex2_approx(logp * kLog2e) * fmaf(B, logp, A);
       if (empty) x[j] = 0.0f;
     }
@@ -486,11 +839,22 @@ void launch_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], long
 }
 
 template <typename T>
-int run_token_logprobs(const LogprobParams& p, cudaStream_t stream) {
+int run_token_logprobs(const LogprobParams& p, int ctas, int device, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  launch_config(cfg, attr, static_cast<long long>(p.rows) * p.cluster, kLogprobThreads, p.cluster, stream);
   const auto kernel = p.top > 0 ? token_logprobs_kernel<T, true> : token_logprobs_kernel<T, false>;
+  static std::atomic<unsigned long long> sized[2] = {};  // devices whose limit of shared memory is raised, by kernel
+  const unsigned long long bit = 1ull << device;
+  if ((sized[p.top > 0].load(std::memory_order_acquire) & bit) == 0) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLogprobRingBytes) != cudaSuccess) {
+      cudaGetLastError();
+      return GEMM_ERR_LAUNCH;
+    }
+    sized[p.top > 0].fetch_or(bit, std::memory_order_release);
+  }
+  launch_config(cfg, attr, static_cast<long long>(std::min(p.rows, ctas / p.cluster)) * p.cluster, kLogprobThreads,
+                p.cluster, stream);
+  cfg.dynamicSmemBytes = kLogprobRingBytes;
   if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
@@ -525,8 +889,8 @@ using namespace dtcp;
 
 extern "C" {
 
-int gemm_token_logprobs(const void* logits, int type, const long long* tokens, float* logprob, float* entropy, float* lse,
-                        int top, float* top_logprobs, int* top_ids, int rows, int vocab, long long ld, float scale,
+int gemm_token_logprobs(const void* logits, int type, const long long* tokens, float* logprob, float* entropy,
+                        float* lse, int top, float* top_logprobs, int* top_ids, int rows, int vocab, long long ld, float scale,
                         void* stream) {
   if (rows < 0 || vocab < 0 || top < 0 || ld < 0 || (type != GEMM_LOGITS_BF16 && type != GEMM_LOGITS_F32))
     return GEMM_ERR_INVALID_ARG;
@@ -559,14 +923,26 @@ int gemm_token_logprobs(const void* logits, int type, const long long* tokens, f
   p.vocab = vocab;
   p.top = top;
   p.scale = scale;
-  // CTAs a row: while the rows alone leave SMs idle, and each CTA keeps at least a vector a thread
-  const long long vectors = vocab / (type == GEMM_LOGITS_BF16 ? 8 : 4);
+  p.status = device_status_word(device);
+  p.wait_limit_ns = RunOptions().wait_limit_ns;
+  if (p.status == nullptr) return GEMM_ERR_NO_DEVICE;
+  // kLogprobCtas CTAs an SM, each stepping over the rows (or its part of them). CTAs a row, by the time of the launch:
+  // its rounds, each as long as a part at the CTA's share of the memory's rate (15 KB a microsecond) and about 2.5 us
+  // of reductions, and as long as each thread has a vector at least.
+  const int ctas = kLogprobCtas * info->num_sms / 8 * 8;
+  const double row_us = static_cast<double>(vocab) * (type == GEMM_LOGITS_BF16 ? 2 : 4) / 15e3;
+  double best = 0.0;
   p.cluster = 1;
-  while (p.cluster < 8 && static_cast<long long>(rows) * p.cluster < 2LL * info->num_sms &&
-         vectors > static_cast<long long>(p.cluster) * kLogprobThreads)
-    p.cluster *= 2;
+  for (int c = 1; c <= 8; c *= 2) {
+    const double us = static_cast<double>((static_cast<long long>(rows) * c + ctas - 1) / ctas) * (row_us / c + 2.5);
+    if (c == 1 || (us < best && row_us * 15e3 >= c * 16.0 * kLogprobThreads)) {
+      best = us;
+      p.cluster = c;
+    }
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return type == GEMM_LOGITS_BF16 ? run_token_logprobs<uint16_t>(p, s) : run_token_logprobs<float>(p, s);
+  return type == GEMM_LOGITS_BF16 ? run_token_logprobs<uint16_t>(p, ctas, device, s)
+                                  : run_token_logprobs<float>(p, ctas, device, s);
 }
 
 int gemm_token_logprobs_backward(const void* logits, int type, const long long* tokens, const float* lse,
@@ -605,7 +981,8 @@ int gemm_token_logprobs_backward(const void* logits, int type, const long long* 
   p.parts = 1;
   p.scale = scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return type == GEMM_LOGITS_BF16 ? run_token_logprobs_backward<uint16_t>(p, s) : run_token_logprobs_backward<float>(p, s);
+  return type == GEMM_LOGITS_BF16 ? run_token_logprobs_backward<uint16_t>(p, s)
+                                  : run_token_logprobs_backward<float>(p, s);
 }
 
 }  // extern "C"
