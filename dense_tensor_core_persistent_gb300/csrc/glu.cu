@@ -11,7 +11,9 @@
 //            same features, and the epilogue has both in one TMEM lane: both projections, the
 //            activation and the product are one kernel, and X is read once for the two.
 //   dX:      A = [dg | du], B = [Wg ; Wu], the sum over both halves of the features in one accumulator.
-//   dWg/dWu: A = dg or du, B = X, summed over the rows of X; one launch covers both.
+//   dWg/dWu: A = dg or du, B = X, summed over the rows of X.
+// One launch computes all three: the tiles of dX, which are the longest, come first, and where their last wave leaves
+// clusters free, those go ahead with as many tiles of dW as take the same time.
 // The gradient's products need operands along their other dimension (W by columns, dg and X by
 // columns). The MMA takes them as they lie in memory: TMA boxes of 64 columns x 128 rows put the
 // non-summed dimension innermost and the descriptors say so ("MN-major"), so nothing is transposed.
@@ -37,16 +39,19 @@
 
 namespace dtcp {
 
-enum GluMode { kGluForward = 0, kGluForwardE4m3 = 1, kGluDx = 2, kGluDw = 3 };
+enum GluMode { kGluForward = 0, kGluForwardE4m3 = 1, kGluBackward = 2 };
+
+// The tiles of one product: rows x cols of output, the summed dimension `depth` (dX: of one half) in `k_iters` stages.
+struct GluProduct {
+  int rows, cols, depth, k_iters;
+  int num_m_blocks, num_n_blocks, num_tiles, group_m;
+  int split_tiles, num_items;  // trailing tiles cut into halves of their columns; work items = tiles + split_tiles
+};
 
 struct GluParams {
-  int rows, cols;        // of one output (dW: of dWg)
-  int num_m_blocks, num_n_blocks, num_tiles, k_iters;
-  int split_tiles, num_items;  // trailing tiles cut into halves of their columns; work items = tiles + split_tiles
-  int depth;             // the summed dimension (dX: of one half)
-  int half_blocks;       // dW: M-blocks of dWg; the ones after them are dWu's
-  int half_iters;        // dX: stages of the first half
-  int group_m;
+  GluProduct main;    // forward: H; backward: dX
+  GluProduct second;  // backward: dWg, then dWu (rows and blocks of both)
+  int ahead;          // backward: items of `second` that each cluster without a tile in dX's last wave takes meanwhile
   int act, save;
   const float* x_scale;  // E4M3: scales of X's rows, Wg's and Wu's
   const float* g_scale;
@@ -54,6 +59,35 @@ struct GluParams {
   unsigned* status;
   unsigned long long wait_limit_ns;
 };
+
+// One work item.
+struct GluItem {
+  int m_blk, n_blk, half;
+  bool second;
+};
+
+// Item `it` of a cluster; false past its last one.
+__device__ __forceinline__ bool glu_item(const GluParams& p, int cluster, int clusters, int it, GluItem& item) {
+  const GluProduct* q = &p.main;
+  int i = cluster + it * clusters;
+  item.second = i >= p.main.num_items;
+  if (item.second) {
+    q = &p.second;
+    const int in_last = p.main.num_items % clusters;  // clusters with a tile in the last wave of the first product
+    const int before = p.main.num_items / clusters + (cluster < in_last ? 1 : 0);
+    int s = it - before;
+    const int extra = in_last > 0 && cluster >= in_last ? p.ahead : 0;
+    const int taken = in_last > 0 ? p.ahead * (clusters - in_last) : 0;
+    i = s < extra ? s * (clusters - in_last) + cluster - in_last : taken + (s - extra) * clusters + cluster;
+    if (i >= p.second.num_items) return false;
+  }
+  const WorkItem w = work_item(i, q->num_tiles, q->split_tiles);
+  const TileCoord tc = tile_coord(w.tile, q->num_m_blocks, q->num_n_blocks, q->group_m);
+  item.m_blk = tc.m_blk;
+  item.n_blk = tc.n_blk;
+  item.half = w.half;
+  return true;
+}
 
 struct GluLayout {
   static constexpr int CG = 2;
@@ -114,55 +148,72 @@ __device__ __forceinline__ uint64_t umma_desc_mn(uint32_t smem_addr) {
 
 // ---------------------------------------------------------------- producers (warps 0, 2)
 
+struct GluMaps {
+  CUtensorMap a0, a1;      // forward: X (both); backward: dg, du
+  CUtensorMap b0, b1, b2;  // Wg, Wu; backward: X
+  CUtensorMap c0, c1, c2;  // forward: H, g, u; backward: dX, dWg, dWu
+};
+
 template <int MODE>
-__device__ __forceinline__ void glu_producer(const GluParams& p, const CUtensorMap* m0, const CUtensorMap* m1,
-                                             uint32_t base, uint32_t rank, bool load_a, int cluster_idx,
-                                             int num_clusters, const WaitCtx& wctx) {
+__device__ __forceinline__ void glu_producer(const GluParams& p, const GluMaps& maps, uint32_t base, uint32_t rank,
+                                             bool load_a, int cluster_idx, int num_clusters, const WaitCtx& wctx) {
   using L = GluLayout;
+  constexpr bool FORWARD = MODE != kGluBackward;
   constexpr int STAGE_K = MODE == kGluForwardE4m3 ? 256 : 128;
-  constexpr bool A_MN = MODE == kGluDw, B_MN = MODE == kGluDx || MODE == kGluDw;
   const uint32_t bar_full = base + L::OFF_BAR, bar_empty = bar_full + 8 * L::STAGES;
   const uint32_t dst0 = base + (load_a ? L::OFF_A : L::OFF_B);
   uint32_t stage = 0, phase = 0;
   bool ok = true;
-  int it = 0;
-  for (int i = cluster_idx; i < p.num_items && ok; i += num_clusters, ++it) {
-    const WorkItem w = work_item(i, p.num_tiles, p.split_tiles);
-    const TileCoord tc = tile_coord(w.tile, p.num_m_blocks, p.num_n_blocks, p.group_m);
-    const int half = w.half > 0 ? 1 : 0;
-    const int b_boxes = w.half >= 0 ? 1 : 2;  // of 64 rows (K-major: per atom) or 64 columns (MN-major)
+  GluItem item;
+  for (int it = 0; ok && glu_item(p, cluster_idx, num_clusters, it, item); ++it) {
+    const int half = item.half > 0 ? 1 : 0;
+    const int b_boxes = item.half >= 0 ? 1 : 2;  // of 64 rows (K-major: per atom) or 64 columns (MN-major)
     const uint32_t stage_bytes = L::OPERAND_BYTES + L::OPERAND_BYTES / 2 * b_boxes;
     const bool down = (it & 1) != 0;  // start on the blocks the last wave of tiles read last
-    const CUtensorMap* map = m0;
-    int first;  // the operand's first row (K-major) or column (MN-major)
+    const int k_iters = item.second ? p.second.k_iters : p.main.k_iters;
+    const CUtensorMap *m0, *m1;  // of the first and the second half of the stages
+    int first;                   // the operand's first row (K-major) or column (MN-major)
+    bool mn;
     if (load_a) {
-      int mb = tc.m_blk;
-      if (MODE == kGluDw && mb >= p.half_blocks) {
-        mb -= p.half_blocks;
-        map = m1;
+      int mb = item.m_blk;
+      m0 = &maps.a0;
+      m1 = &maps.a1;
+      if (item.second) {
+        const int half_blocks = p.second.num_m_blocks / 2;
+        if (mb >= half_blocks) {
+          mb -= half_blocks;
+          m0 = m1;
+        }
       }
       first = mb * L::TILE_M + static_cast<int>(rank) * L::CTA_M;
-    } else if (MODE == kGluForward || MODE == kGluForwardE4m3) {
-      if (rank == 1) map = m1;
-      first = tc.n_blk * L::FEATURES + half * (L::FEATURES / 2);
+      mn = !FORWARD && item.second;
+    } else if (FORWARD) {
+      m0 = m1 = rank == 1 ? &maps.b1 : &maps.b0;
+      first = item.n_blk * L::FEATURES + half * (L::FEATURES / 2);
+      mn = false;
     } else {
-      first = tc.n_blk * L::BLOCK_N + half * (L::BLOCK_N / 2) + static_cast<int>(rank) * 64 * b_boxes;
+      m0 = item.second ? &maps.b2 : &maps.b0;
+      m1 = &maps.b1;
+      first = item.n_blk * L::BLOCK_N + half * (L::BLOCK_N / 2) + static_cast<int>(rank) * 64 * b_boxes;
+      mn = true;
     }
-    for (int kb = 0; kb < p.k_iters; ++kb) {
+    const int half_iters = !FORWARD && !item.second ? k_iters / 2 : k_iters;
+    for (int kb = 0; kb < k_iters; ++kb) {
       if (!wait_phase_inline(bar_empty + 8 * stage, phase ^ 1u, wctx, status_code(kRoleProducer, stage))) {
         ok = false;
         break;
       }
-      int k = down ? p.k_iters - 1 - kb : kb;
-      if (MODE == kGluDx) {
-        map = k >= p.half_iters ? m1 : m0;
-        if (k >= p.half_iters) k -= p.half_iters;
+      int k = down ? k_iters - 1 - kb : kb;
+      const CUtensorMap* map = m0;
+      if (k >= half_iters) {
+        k -= half_iters;
+        map = m1;
       }
       const uint32_t full = bar_full + 8 * stage;
       if (load_a && rank == 0) mbar_arrive_expect_tx(full, 2u * stage_bytes);
       const uint32_t bar = mapa_shared(full, 0);
       const uint32_t dst = dst0 + stage * L::OPERAND_BYTES;
-      if (load_a ? A_MN : B_MN) {
+      if (mn) {
         const int boxes = load_a ? 2 : b_boxes;
         for (int c = 0; c < boxes; ++c)
           tma_load_2d_pair(dst + c * L::ATOM_BYTES, map, first + c * 64, k * STAGE_K, bar);
@@ -191,46 +242,48 @@ template <int MODE>
 __device__ __forceinline__ void glu_mma(const GluParams& p, uint32_t base, uint32_t tmem_base, int cluster_idx,
                                         int num_clusters, const WaitCtx& wctx) {
   using L = GluLayout;
-  constexpr bool A_MN = MODE == kGluDw, B_MN = MODE == kGluDx || MODE == kGluDw, E4M3 = MODE == kGluForwardE4m3;
+  constexpr bool FORWARD = MODE != kGluBackward, E4M3 = MODE == kGluForwardE4m3;
   constexpr int STAGE_K = E4M3 ? 256 : 128, MMA_K = E4M3 ? 32 : 16;
-  constexpr uint32_t IDESC_FULL = E4M3 ? idesc_e4m3(256, L::BLOCK_N) : idesc_glu(256, L::BLOCK_N, A_MN, B_MN);
-  constexpr uint32_t IDESC_HALF = E4M3 ? idesc_e4m3(256, L::BLOCK_N / 2) : idesc_glu(256, L::BLOCK_N / 2, A_MN, B_MN);
   const uint32_t bar_full = base + L::OFF_BAR, bar_empty = bar_full + 8 * L::STAGES;
   const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
-  const uint64_t a0 = A_MN ? umma_desc_mn(base + L::OFF_A) : umma_desc_sw128(base + L::OFF_A);
-  const uint64_t b0 = B_MN ? umma_desc_mn(base + L::OFF_B) : umma_desc_sw128(base + L::OFF_B);
-  // MMA kk of a stage: K-major operands advance 32 bytes inside the swizzle row, four per atom;
-  // MN-major ones by 16 rows of 128 bytes.
-  auto step = [&](bool mn, int kk) -> uint32_t {
-    return mn ? static_cast<uint32_t>(kk) * 2048u : static_cast<uint32_t>((kk / 4) * L::ATOM_BYTES + (kk % 4) * 32);
-  };
+  const uint64_t a_k = umma_desc_sw128(base + L::OFF_A), a_mn = umma_desc_mn(base + L::OFF_A);
+  const uint64_t b0 = FORWARD ? umma_desc_sw128(base + L::OFF_B) : umma_desc_mn(base + L::OFF_B);
   uint32_t stage = 0, phase = 0;
   bool ok = true;
-  int it = 0;
-  for (int i = cluster_idx; i < p.num_items && ok; i += num_clusters, ++it) {
-    const uint32_t idesc = work_item(i, p.num_tiles, p.split_tiles).half >= 0 ? IDESC_HALF : IDESC_FULL;
+  GluItem item;
+  for (int it = 0; ok && glu_item(p, cluster_idx, num_clusters, it, item); ++it) {
+    const bool dw = !FORWARD && item.second;
+    const uint32_t n = item.half >= 0 ? L::BLOCK_N / 2 : L::BLOCK_N;
+    const uint32_t idesc = E4M3 ? idesc_e4m3(256, n) : idesc_glu(256, n, dw, !FORWARD);
     const bool down = (it & 1) != 0;
     const uint32_t slot = static_cast<uint32_t>(it) & 1u;
+    const GluProduct& q = item.second ? p.second : p.main;
+    const int half_iters = !FORWARD && !item.second ? q.k_iters / 2 : q.k_iters;
     if (!wait_phase_inline(bar_tempty + 8 * slot, ((static_cast<uint32_t>(it) >> 1) & 1u) ^ 1u, wctx,
                            status_code(kRoleMma, 0x100 + slot))) {
       ok = false;
       break;
     }
     const uint32_t d = tmem_base + slot * L::ACC_COLS;
-    for (int kb = 0; kb < p.k_iters; ++kb) {
+    for (int kb = 0; kb < q.k_iters; ++kb) {
       if (!wait_phase_inline(bar_full + 8 * stage, phase, wctx, status_code(kRoleMma, stage))) {
         ok = false;
         break;
       }
       tc_fence_after_sync();
-      int k = down ? p.k_iters - 1 - kb : kb;
-      if (MODE == kGluDx && k >= p.half_iters) k -= p.half_iters;
-      const uint64_t a = umma_desc_advance(a0, stage * L::OPERAND_BYTES);
+      int k = down ? q.k_iters - 1 - kb : kb;
+      if (k >= half_iters) k -= half_iters;
+      const uint64_t a = umma_desc_advance(dw ? a_mn : a_k, stage * L::OPERAND_BYTES);
       const uint64_t b = umma_desc_advance(b0, stage * L::OPERAND_BYTES);
-      const int left = p.depth - k * STAGE_K;  // a ragged last stage: only the MMAs that hold any of it
+      const int left = q.depth - k * STAGE_K;  // a ragged last stage: only the MMAs that hold any of it
       const int steps = left >= STAGE_K ? L::KSTEPS : (left + MMA_K - 1) / MMA_K;
+      // MMA kk of a stage: K-major operands advance 32 bytes inside the swizzle row, four per atom;
+      // MN-major ones by 16 rows of 128 bytes.
       auto one = [&](int kk) {
-        const uint64_t ad = umma_desc_advance(a, step(A_MN, kk)), bd = umma_desc_advance(b, step(B_MN, kk));
+        const uint32_t step_k = static_cast<uint32_t>((kk / 4) * L::ATOM_BYTES + (kk % 4) * 32);
+        const uint32_t step_mn = static_cast<uint32_t>(kk) * 2048u;
+        const uint64_t ad = umma_desc_advance(a, dw ? step_mn : step_k);
+        const uint64_t bd = umma_desc_advance(b, FORWARD ? step_k : step_mn);
         if constexpr (E4M3) mma_e4m3_pair(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
         else mma_f16<2>(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
       };
@@ -279,8 +332,8 @@ struct GluStaging {
 };
 
 // 32 columns of this lane's row as BF16 (64-byte rows, 64-byte swizzle).
-__device__ __forceinline__ void glu_store_bf16(GluStaging& st, uint32_t lane, const CUtensorMap* map, const float (&v)[32],
-                                               int col, int row) {
+__device__ __forceinline__ void glu_store_bf16(GluStaging& st, uint32_t lane, const CUtensorMap* map,
+                                               const float (&v)[32], int col, int row) {
   const uint32_t buf = st.take(lane);
   const uint32_t addr = buf + lane * 64u, sw = (lane >> 1) & 3u;
 #pragma unroll
@@ -306,54 +359,54 @@ __device__ __forceinline__ void glu_store_f32(GluStaging& st, uint32_t lane, con
 }
 
 template <int MODE>
-__device__ __forceinline__ void glu_epilogue(const GluParams& p, const CUtensorMap* c0, const CUtensorMap* c1,
-                                             const CUtensorMap* pre_g, const CUtensorMap* pre_u, uint32_t base,
-                                             uint32_t tmem_base, uint32_t warp, uint32_t lane, uint32_t rank,
-                                             int cluster_idx, int num_clusters, const WaitCtx& wctx) {
+__device__ __forceinline__ void glu_epilogue(const GluParams& p, const GluMaps& maps, uint32_t base, uint32_t tmem_base,
+                                             uint32_t warp, uint32_t lane, uint32_t rank, int cluster_idx,
+                                             int num_clusters, const WaitCtx& wctx) {
   using L = GluLayout;
-  constexpr bool FORWARD = MODE == kGluForward || MODE == kGluForwardE4m3;
+  constexpr bool FORWARD = MODE != kGluBackward;
   const uint32_t bar_tfull = base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 16;
   const uint32_t q = warp & 3u;  // this warp may access TMEM lanes 32q .. 32q+31
   const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
   GluStaging st{base + L::OFF_EPI + q * L::EPI_BUFS * L::EPI_BUF_BYTES, 0u};
-  int it = 0;
-  for (int i = cluster_idx; i < p.num_items; i += num_clusters, ++it) {
-    const WorkItem w = work_item(i, p.num_tiles, p.split_tiles);
-    const TileCoord tc = tile_coord(w.tile, p.num_m_blocks, p.num_n_blocks, p.group_m);
-    const int columns = w.half >= 0 ? L::BLOCK_N / 2 : L::BLOCK_N;  // of the item's accumulator
-    const int col0 = tc.n_blk * (FORWARD ? L::FEATURES : L::BLOCK_N) + (w.half > 0 ? columns / (FORWARD ? 2 : 1) : 0);
+  GluItem item;
+  for (int it = 0; glu_item(p, cluster_idx, num_clusters, it, item); ++it) {
+    const int columns = item.half >= 0 ? L::BLOCK_N / 2 : L::BLOCK_N;  // of the item's accumulator
+    const int col0 = item.n_blk * (FORWARD ? L::FEATURES : L::BLOCK_N) +
+                     (item.half > 0 ? columns / (FORWARD ? 2 : 1) : 0);
     const uint32_t slot = static_cast<uint32_t>(it) & 1u;
+    int mb = item.m_blk, rows = p.main.rows, cols = p.main.cols;
+    const CUtensorMap* out = &maps.c0;
+    if (!FORWARD && item.second) {
+      const int half_blocks = p.second.num_m_blocks / 2;
+      out = mb >= half_blocks ? &maps.c2 : &maps.c1;
+      if (mb >= half_blocks) mb -= half_blocks;
+      rows = p.second.rows;
+      cols = p.second.cols;
+    }
+    const int row0 = mb * L::TILE_M + static_cast<int>(rank) * L::CTA_M + static_cast<int>(q) * 32;
     // E4M3: this lane's row scale and its features' scales, while the MMAs run
     float x_scale = 1.0f, w_scale[2][L::FEATURES / 32];
     if constexpr (MODE == kGluForwardE4m3) {
-      const int row = tc.m_blk * L::TILE_M + static_cast<int>(rank) * L::CTA_M + static_cast<int>(q * 32 + lane);
-      if (row < p.rows) x_scale = p.x_scale[row];
+      if (row0 + static_cast<int>(lane) < rows) x_scale = p.x_scale[row0 + lane];
 #pragma unroll
       for (int c = 0; c < L::FEATURES / 32; ++c) {
         const int f = col0 + c * 32 + static_cast<int>(lane);
-        w_scale[0][c] = f < p.cols ? p.g_scale[f] : 0.0f;
-        w_scale[1][c] = f < p.cols ? p.u_scale[f] : 0.0f;
+        w_scale[0][c] = f < cols ? p.g_scale[f] : 0.0f;
+        w_scale[1][c] = f < cols ? p.u_scale[f] : 0.0f;
       }
     }
     if (!wait_phase_warp(bar_tfull + 8 * slot, (static_cast<uint32_t>(it) >> 1) & 1u, wctx,
                          status_code(kRoleEpilogue, slot)))
       break;
     tc_fence_after_sync();
-    int mb = tc.m_blk;
-    const CUtensorMap* out = c0;
-    if (MODE == kGluDw && mb >= p.half_blocks) {
-      mb -= p.half_blocks;
-      out = c1;
-    }
-    const int row0 = mb * L::TILE_M + static_cast<int>(rank) * L::CTA_M + static_cast<int>(q) * 32;
     const uint32_t taddr = tmem_base + ((q * 32u) << 16) + slot * L::ACC_COLS;
-    if (row0 < p.rows) {
+    if (row0 < rows) {
       if constexpr (FORWARD) {
         const float xs = x_scale;
 #pragma unroll MODE == kGluForwardE4m3 ? 4 : 1
         for (int c = 0; c < L::FEATURES; c += 32) {
           const int col = col0 + c;
-          if (c >= columns / 2 || col >= p.cols) break;
+          if (c >= columns / 2 || col >= cols) break;
           float gs = 0.0f, us = 0.0f;  // E4M3: the scales of feature col + lane
           if constexpr (MODE == kGluForwardE4m3) {
             gs = w_scale[0][c / 32];
@@ -375,15 +428,15 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const CUtensorM
           }
           glu_store_bf16(st, lane, out, h, col, row0);
           if (p.save) {
-            glu_store_f32(st, lane, pre_g, g, col, row0);
-            glu_store_f32(st, lane, pre_u, u, col, row0);
+            glu_store_f32(st, lane, &maps.c1, g, col, row0);
+            glu_store_f32(st, lane, &maps.c2, u, col, row0);
           }
         }
       } else {
 #pragma unroll 1
         for (int c = 0; c < columns; c += 32) {
           const int col = col0 + c;
-          if (col >= p.cols) break;
+          if (col >= cols) break;
           uint32_t v[32];
           tmem_ld_32x32b_x32(taddr + c, v);
           tmem_ld_wait();
@@ -404,10 +457,7 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const CUtensorM
 
 template <int MODE>
 __global__ void __launch_bounds__(GluLayout::NUM_THREADS, 1)
-    glu_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
-               const __grid_constant__ CUtensorMap b0, const __grid_constant__ CUtensorMap b1,
-               const __grid_constant__ CUtensorMap c0, const __grid_constant__ CUtensorMap c1,
-               const __grid_constant__ CUtensorMap pre_g, const __grid_constant__ CUtensorMap pre_u, const GluParams p) {
+    glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluParams p) {
   using L = GluLayout;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -448,13 +498,14 @@ __global__ void __launch_bounds__(GluLayout::NUM_THREADS, 1)
 
   if (warp < L::EPI_WARP0) {
     if (lane == 0) {
-      if (warp == L::WARP_A) glu_producer<MODE>(p, &a0, &a1, base, rank, true, cluster_idx, num_clusters, wctx);
-      else if (warp == L::WARP_B) glu_producer<MODE>(p, &b0, &b1, base, rank, false, cluster_idx, num_clusters, wctx);
-      else if (warp == L::WARP_MMA && rank == 0) glu_mma<MODE>(p, base, tmem_base, cluster_idx, num_clusters, wctx);
+      if (warp == L::WARP_A || warp == L::WARP_B)
+        glu_producer<MODE>(p, maps, base, rank, warp == L::WARP_A, cluster_idx, num_clusters, wctx);
+      else if (warp == L::WARP_MMA && rank == 0)
+        glu_mma<MODE>(p, base, tmem_base, cluster_idx, num_clusters, wctx);
     }
     __syncwarp();
   } else {
-    glu_epilogue<MODE>(p, &c0, &c1, &pre_g, &pre_u, base, tmem_base, warp, lane, rank, cluster_idx, num_clusters, wctx);
+    glu_epilogue<MODE>(p, maps, base, tmem_base, warp, lane, rank, cluster_idx, num_clusters, wctx);
   }
   tc_fence_before_sync();
   cluster_sync_all();
@@ -504,17 +555,13 @@ __global__ void __launch_bounds__(256) glu_gate_grad_kernel(const uint16_t* dh, 
 
 // ---------------------------------------------------------------- host side
 
-struct GluMaps {
-  CUtensorMap a0, a1, b0, b1, c0, c1, pre_g, pre_u;
-};
-
 int glu_max_clusters(int device) {
   static std::mutex mu;
   static int cache[64] = {0};
   std::lock_guard<std::mutex> lock(mu);
   if (device < 0 || device >= 64) return 0;
   if (cache[device] > 0) return cache[device];
-  for (auto k : {glu_kernel<kGluForward>, glu_kernel<kGluForwardE4m3>, glu_kernel<kGluDx>, glu_kernel<kGluDw>})
+  for (auto k : {glu_kernel<kGluForward>, glu_kernel<kGluForwardE4m3>, glu_kernel<kGluBackward>})
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, GluLayout::SMEM_BYTES) != cudaSuccess) {
       cudaGetLastError();
       return 0;
@@ -558,24 +605,58 @@ int map_out(CUtensorMap* m, const void* p, int cols, int rows, long long ld) {
                         CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// The tiles of a rows x cols output (virtual sizes in units of the 256 x 256 tile's operands) on the co-resident pairs.
-template <int MODE>
-int glu_launch(GluMaps& m, GluParams& p, int virtual_rows, int virtual_cols, int virtual_depth, double bytes, int device,
-               const DeviceInfo* info, cudaStream_t stream) {
+// The tiles of a product; `rows` and `cols` are those of one output, of which `outputs` lie one after the other along
+// the rows; `cols_a_tile`: output columns of a 256-column accumulator.
+int plan_product(GluProduct* q, int rows, int cols, int depth, int stage, int halves, int outputs, int cols_a_tile) {
   using L = GluLayout;
-  const long long tiles = static_cast<long long>(p.num_m_blocks) * p.num_n_blocks;
-  if (tiles > 0x3FFFFFFFLL) return GEMM_ERR_UNSUPPORTED_SHAPE;
-  p.num_tiles = static_cast<int>(tiles);
+  q->rows = rows;
+  q->cols = cols;
+  q->depth = depth;
+  q->k_iters = halves * ceil_div(depth, stage);
+  const long long m = static_cast<long long>(outputs) * ceil_div(rows, L::TILE_M);
+  q->num_n_blocks = ceil_div(cols, cols_a_tile);
+  if (m * q->num_n_blocks > 0x1FFFFFFFLL) return GEMM_ERR_UNSUPPORTED_SHAPE;
+  q->num_m_blocks = static_cast<int>(m);
+  q->num_tiles = q->num_items = static_cast<int>(m * q->num_n_blocks);
+  q->split_tiles = 0;
+  return GEMM_OK;
+}
+
+// The order of a product's tiles on `clusters` pairs, for operands of `bytes` per element.
+void order_product(GluProduct* q, int clusters, double bytes, long long l2_bytes) {
+  using L = GluLayout;
+  q->group_m = choose_group_m(static_cast<int>(std::min<long long>(1LL * q->num_m_blocks * L::TILE_M, 0x7FFFFFFF)),
+                              static_cast<int>(std::min<long long>(1LL * q->num_n_blocks * L::BLOCK_N, 0x7FFFFFFF)),
+                              std::max(q->depth, 1), L::TILE_M, L::BLOCK_N, bytes, 0.0, clusters, l2_bytes);
+}
+
+// The co-resident pairs take the tiles of both products (the second may have none).
+template <int MODE>
+int glu_launch(const GluMaps& m, GluParams& p, double bytes, int device, const DeviceInfo* info, cudaStream_t stream) {
+  using L = GluLayout;
   p.status = device_status_word(device);
   p.wait_limit_ns = RunOptions().wait_limit_ns;
   if (p.status == nullptr) return GEMM_ERR_NO_DEVICE;
-  const int max_clusters = glu_max_clusters(device);
-  if (max_clusters <= 0) return GEMM_ERR_LAUNCH;
-  p.split_tiles = tail_split_tiles(p.num_tiles, max_clusters);
-  p.num_items = p.num_tiles + p.split_tiles;
-  const int clusters = std::min(p.num_items, max_clusters);
-  p.group_m = choose_group_m(virtual_rows, virtual_cols, virtual_depth, L::TILE_M, L::BLOCK_N, bytes, 0.0, clusters,
-                             info->l2_bytes);
+  const int wave = glu_max_clusters(device);
+  if (wave <= 0) return GEMM_ERR_LAUNCH;
+  GluProduct &a = p.main, &b = p.second;
+  p.ahead = 0;
+  if (b.num_tiles == 0) {
+    a.split_tiles = tail_split_tiles(a.num_tiles, wave);
+    a.num_items = a.num_tiles + a.split_tiles;
+  } else {
+    // clusters that a last partial wave of the first product leaves free go ahead with tiles of the second
+    const int clusters = std::min(a.num_tiles + b.num_tiles, wave);
+    const int in_last = a.num_tiles % clusters, idle = in_last > 0 ? clusters - in_last : 0;
+    if (idle > 0)
+      p.ahead = std::min((a.k_iters + b.k_iters / 2) / b.k_iters, ceil_div(b.num_tiles, idle));
+    const int rest = std::max(0, b.num_tiles - p.ahead * idle);
+    b.split_tiles = tail_split_tiles(rest, wave);
+    b.num_items = b.num_tiles + b.split_tiles;
+  }
+  const int clusters = std::min(a.num_items + b.num_items, wave);
+  order_product(&a, clusters, bytes, info->l2_bytes);
+  if (b.num_tiles > 0) order_product(&b, clusters, bytes, info->l2_bytes);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * L::CG), 1, 1);
@@ -590,8 +671,7 @@ int glu_launch(GluMaps& m, GluParams& p, int virtual_rows, int virtual_cols, int
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, glu_kernel<MODE>, m.a0, m.a1, m.b0, m.b1, m.c0, m.c1, m.pre_g, m.pre_u, p) !=
-      cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, glu_kernel<MODE>, m, p) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
   }
@@ -653,7 +733,8 @@ int gemm_glu_bf16(const void* X, const void* Wg, const void* Wu, void* H, float*
     return st;
   }
   if (M <= kGluFewRows) {
-    GluFewParams f = {X, Wg, Wu, static_cast<uint16_t*>(H), preact, nullptr, nullptr, nullptr, ld.x, ld.h, M, N, K, act};
+    const GluFewParams f = {X,       Wg,      Wu,   static_cast<uint16_t*>(H), preact, nullptr, nullptr,
+                            nullptr, ld.x,    ld.h, M,                         N,      K,       act};
     return run_glu_few(f, false, s);
   }
   GluMaps m;
@@ -663,26 +744,20 @@ int gemm_glu_bf16(const void* X, const void* Wg, const void* Wu, void* H, float*
   if (st == GEMM_OK) st = map_kb(&m.b1, Wu, K, N);
   if (st == GEMM_OK) st = map_out(&m.c0, H, N, M, ld.h);
   if (st != GEMM_OK) return st;
-  m.a1 = m.a0;
-  m.c1 = m.pre_g = m.pre_u = m.c0;
+  m.a1 = m.b2 = m.a0;
+  m.c1 = m.c2 = m.c0;
   if (preact != nullptr) {
-    st = encode_tmap_2d(&m.pre_g, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, preact, N, M, uint64_t(N) * 8, 32, 32,
+    st = encode_tmap_2d(&m.c1, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, preact, N, M, uint64_t(N) * 8, 32, 32,
                         CU_TENSOR_MAP_SWIZZLE_128B);
     if (st == GEMM_OK)
-      st = encode_tmap_2d(&m.pre_u, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, preact + N, N, M, uint64_t(N) * 8, 32, 32,
+      st = encode_tmap_2d(&m.c2, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, preact + N, N, M, uint64_t(N) * 8, 32, 32,
                           CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != GEMM_OK) return st;
   }
-  p.rows = M;
-  p.cols = N;
-  p.depth = K;
-  p.num_m_blocks = ceil_div(M, L::TILE_M);
-  p.num_n_blocks = ceil_div(N, L::FEATURES);
-  p.k_iters = ceil_div(K, 128);
   p.act = act;
   p.save = preact != nullptr ? 1 : 0;
-  const int virtual_cols = static_cast<int>(std::min<long long>(2LL * N, 0x7FFFFFFF));
-  return glu_launch<kGluForward>(m, p, M, virtual_cols, K, 2.0, device, info, s);
+  st = plan_product(&p.main, M, N, K, 128, 1, 1, L::FEATURES);
+  return st != GEMM_OK ? st : glu_launch<kGluForward>(m, p, 2.0, device, info, s);
 }
 
 int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const float* wg_scale, const void* Wu,
@@ -697,9 +772,9 @@ int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const flo
                                  wg_scale == nullptr || wu_scale == nullptr)))
     return GEMM_ERR_INVALID_ARG;
   if (K % 16 != 0 || N % 8 != 0 || ld.x % 16 != 0 || ld.h % 8 != 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
-  if (!aligned16(H) || (K > 0 && (!aligned16(X) || !aligned16(Wg) || !aligned16(Wu) ||
-                                  (reinterpret_cast<uintptr_t>(x_scale) & 3u) || (reinterpret_cast<uintptr_t>(wg_scale) & 3u) ||
-                                  (reinterpret_cast<uintptr_t>(wu_scale) & 3u))))
+  auto aligned4 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 3u) == 0; };
+  if (!aligned16(H) || (K > 0 && (!aligned16(X) || !aligned16(Wg) || !aligned16(Wu) || !aligned4(x_scale) ||
+                                  !aligned4(wg_scale) || !aligned4(wu_scale))))
     return GEMM_ERR_MISALIGNED;
   int device = 0, err = 0;
   const DeviceInfo* info = current_device_info(&device, &err);
@@ -707,33 +782,29 @@ int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const flo
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (K == 0) return zero_rows(H, size_t(N) * 2, ld.h * 2, M, s);
   if (M <= kGluFewRowsE4m3) {
-    GluFewParams f = {X, Wg, Wu, static_cast<uint16_t*>(H), nullptr, x_scale, wg_scale, wu_scale, ld.x, ld.h, M, N, K, act};
+    const GluFewParams f = {X,        Wg,   Wu,   static_cast<uint16_t*>(H), nullptr, x_scale, wg_scale,
+                            wu_scale, ld.x, ld.h, M,                         N,       K,       act};
     return run_glu_few(f, true, s);
   }
   GluMaps m;
   GluParams p = {};
   auto map8 = [&](CUtensorMap* t, const void* q, int rows, long long stride, int box_rows) {
-    return encode_tmap_2d(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, rows, stride, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    return encode_tmap_2d(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, rows, stride, 128, box_rows,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
   };
   int st = map8(&m.a0, X, M, ld.x, 128);
   if (st == GEMM_OK) st = map8(&m.b0, Wg, N, K, 64);
   if (st == GEMM_OK) st = map8(&m.b1, Wu, N, K, 64);
   if (st == GEMM_OK) st = map_out(&m.c0, H, N, M, ld.h);
   if (st != GEMM_OK) return st;
-  m.a1 = m.a0;
-  m.c1 = m.pre_g = m.pre_u = m.c0;
-  p.rows = M;
-  p.cols = N;
-  p.depth = K;
-  p.num_m_blocks = ceil_div(M, L::TILE_M);
-  p.num_n_blocks = ceil_div(N, L::FEATURES);
-  p.k_iters = ceil_div(K, 256);
+  m.a1 = m.b2 = m.a0;
+  m.c1 = m.c2 = m.c0;
   p.act = act;
   p.x_scale = x_scale;
   p.g_scale = wg_scale;
   p.u_scale = wu_scale;
-  const int virtual_cols = static_cast<int>(std::min<long long>(2LL * N, 0x7FFFFFFF));
-  return glu_launch<kGluForwardE4m3>(m, p, M, virtual_cols, K, 1.0, device, info, s);
+  st = plan_product(&p.main, M, N, K, 256, 1, 1, L::FEATURES);
+  return st != GEMM_OK ? st : glu_launch<kGluForwardE4m3>(m, p, 1.0, device, info, s);
 }
 
 int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const void* Wu, const float* preact, void* dX,
@@ -794,46 +865,25 @@ int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const 
       st = GEMM_OK;
     }
   }
-  if (st == GEMM_OK && dX != nullptr) {
+  if (st == GEMM_OK) {
     GluMaps m;
     GluParams p = {};
-    st = map_k(&m.a0, dgu, N, M, 2LL * N);
+    st = map_k(&m.a0, dgu, N, M, 2LL * N);  // (a box of 64 features x 128 rows is the same for either order)
     if (st == GEMM_OK) st = map_k(&m.a1, dgu + N, N, M, 2LL * N);
-    if (st == GEMM_OK) st = map_mn(&m.b0, Wg, K, N, K);
-    if (st == GEMM_OK) st = map_mn(&m.b1, Wu, K, N, K);
-    if (st == GEMM_OK) st = map_out(&m.c0, dX, K, M, ld.dx);
-    if (st == GEMM_OK) {
-      m.c1 = m.pre_g = m.pre_u = m.c0;
-      p.rows = M;
-      p.cols = K;
-      p.depth = N;
-      p.num_m_blocks = ceil_div(M, L::TILE_M);
-      p.num_n_blocks = ceil_div(K, L::BLOCK_N);
-      p.half_iters = ceil_div(N, 128);
-      p.k_iters = 2 * p.half_iters;
-      st = glu_launch<kGluDx>(m, p, M, K, 2 * N, 2.0, device, info, s);
+    m.b0 = m.b1 = m.b2 = m.c0 = m.c1 = m.c2 = m.a0;
+    if (dX != nullptr) {
+      if (st == GEMM_OK) st = map_mn(&m.b0, Wg, K, N, K);
+      if (st == GEMM_OK) st = map_mn(&m.b1, Wu, K, N, K);
+      if (st == GEMM_OK) st = map_out(&m.c0, dX, K, M, ld.dx);
+      if (st == GEMM_OK) st = plan_product(&p.main, M, K, N, 128, 2, 1, L::BLOCK_N);
     }
-  }
-  if (st == GEMM_OK && dWg != nullptr) {
-    GluMaps m;
-    GluParams p = {};
-    st = map_mn(&m.a0, dgu, N, M, 2LL * N);
-    if (st == GEMM_OK) st = map_mn(&m.a1, dgu + N, N, M, 2LL * N);
-    if (st == GEMM_OK) st = map_mn(&m.b0, X, K, M, ld.x);
-    if (st == GEMM_OK) st = map_out(&m.c0, dWg, K, N, K);
-    if (st == GEMM_OK) st = map_out(&m.c1, dWu, K, N, K);
-    if (st == GEMM_OK) {
-      m.b1 = m.b0;
-      m.pre_g = m.pre_u = m.c0;
-      p.rows = N;
-      p.cols = K;
-      p.depth = M;
-      p.half_blocks = ceil_div(N, L::TILE_M);
-      p.num_m_blocks = 2 * p.half_blocks;
-      p.num_n_blocks = ceil_div(K, L::BLOCK_N);
-      p.k_iters = ceil_div(M, 128);
-      st = glu_launch<kGluDw>(m, p, 2 * N, K, M, 2.0, device, info, s);
+    if (dWg != nullptr) {
+      if (st == GEMM_OK) st = map_mn(&m.b2, X, K, M, ld.x);
+      if (st == GEMM_OK) st = map_out(&m.c1, dWg, K, N, K);
+      if (st == GEMM_OK) st = map_out(&m.c2, dWu, K, N, K);
+      if (st == GEMM_OK) st = plan_product(&p.second, N, K, M, 128, 1, 2, L::BLOCK_N);
     }
+    if (st == GEMM_OK) st = glu_launch<kGluBackward>(m, p, 2.0, device, info, s);
   }
   if (cudaFreeAsync(ws, s) != cudaSuccess && st == GEMM_OK) st = GEMM_ERR_LAUNCH;
   return st;
