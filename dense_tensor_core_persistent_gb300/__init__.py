@@ -45,7 +45,7 @@ EXPORTS = (
     "gemm_nvfp4_noalloc", "gemm_measure_mma_rate", "gemm_bf16_fused", "gemm_nvfp4_fused", "gemm_nvfp4_blocked_fused",
     "gemm_bf16_plan", "gemm_clc_rule", "gemm_nvfp4_plan", "gemm_bf16_wide_rule",
     "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_token_logprobs", "gemm_token_logprobs_backward",
-    "gemm_glu_bf16", "gemm_glu_e4m3", "gemm_glu_bf16_backward",
+    "gemm_glu_bf16", "gemm_glu_e4m3", "gemm_glu_bf16_backward", "gemm_glu_plan",
 )
 
 # gemm_activation_t
@@ -228,6 +228,8 @@ def lib() -> ctypes.CDLL:
         l.gemm_glu_e4m3.restype = I
         l.gemm_glu_bf16_backward.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, P, GS]
         l.gemm_glu_bf16_backward.restype = I
+        l.gemm_glu_plan.argtypes = [I, I, I, I, ctypes.POINTER(I), ctypes.POINTER(I)]
+        l.gemm_glu_plan.restype = I
         _lib = l
     return _lib
 
@@ -484,6 +486,13 @@ def gemm_glu_bf16_backward(dH, X, Wg, Wu, preact, dX, dWg, dWu, M: int, N: int, 
     _check(lib().gemm_glu_bf16_backward(_ptr(dH), _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(preact), _ptr(dX), _ptr(dWg),
                                         _ptr(dWu), M, N, K, act, _stream(stream), _byref_or_null(strides)),
            "gemm_glu_bf16_backward")
+
+
+def glu_plan(M: int, N: int, K: int, wave: int = 76) -> tuple[int, int]:
+    """Rows of the pair tile that glu_bf16 (0: the few-row kernel) and its gradient use for this problem (host only)."""
+    fwd, bwd = ctypes.c_int(), ctypes.c_int()
+    _check(lib().gemm_glu_plan(M, N, K, wave, ctypes.byref(fwd), ctypes.byref(bwd)), "gemm_glu_plan")
+    return fwd.value, bwd.value
 
 
 # ---------------------------------------------------------------- torch-tensor conveniences

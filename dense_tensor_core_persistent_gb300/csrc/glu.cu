@@ -19,6 +19,7 @@
 // non-summed dimension innermost and the descriptors say so ("MN-major"), so nothing is transposed.
 //
 // A last wave of tiles at most half full runs as halves of its tiles (N = 128 MMAs).
+// BF16 products with enough tiles run on a 512 x 256 pair tile instead (glu_wide.cu; glu_wide_rule).
 // A stage holds 128 (BF16) or 256 (E4M3) of the summed dimension, 8 MMAs per barrier wait, 3 stages.
 // Warp roles: 0 loads A, 2 loads B, 1 allocates TMEM and issues the MMAs (leader CTA), 4..7 epilogue,
 // one TMEM lane quadrant each; stores go through swizzled staging tiles and TMA.
@@ -35,59 +36,10 @@
 
 #include "common.cuh"
 #include "glu_act.cuh"
+#include "glu_common.cuh"
 #include "host_common.h"
 
 namespace dtcp {
-
-enum GluMode { kGluForward = 0, kGluForwardE4m3 = 1, kGluBackward = 2 };
-
-// The tiles of one product: rows x cols of output, the summed dimension `depth` (dX: of one half) in `k_iters` stages.
-struct GluProduct {
-  int rows, cols, depth, k_iters;
-  int num_m_blocks, num_n_blocks, num_tiles, group_m;
-  int split_tiles, num_items;  // trailing tiles cut into halves of their columns; work items = tiles + split_tiles
-};
-
-struct GluParams {
-  GluProduct main;    // forward: H; backward: dX
-  GluProduct second;  // backward: dWg, then dWu (rows and blocks of both)
-  int ahead;          // backward: items of `second` that each cluster without a tile in dX's last wave takes meanwhile
-  int act, save;
-  const float* x_scale;  // E4M3: scales of X's rows, Wg's and Wu's
-  const float* g_scale;
-  const float* u_scale;
-  unsigned* status;
-  unsigned long long wait_limit_ns;
-};
-
-// One work item.
-struct GluItem {
-  int m_blk, n_blk, half;
-  bool second;
-};
-
-// Item `it` of a cluster; false past its last one.
-__device__ __forceinline__ bool glu_item(const GluParams& p, int cluster, int clusters, int it, GluItem& item) {
-  const GluProduct* q = &p.main;
-  int i = cluster + it * clusters;
-  item.second = i >= p.main.num_items;
-  if (item.second) {
-    q = &p.second;
-    const int in_last = p.main.num_items % clusters;  // clusters with a tile in the last wave of the first product
-    const int before = p.main.num_items / clusters + (cluster < in_last ? 1 : 0);
-    int s = it - before;
-    const int extra = in_last > 0 && cluster >= in_last ? p.ahead : 0;
-    const int taken = in_last > 0 ? p.ahead * (clusters - in_last) : 0;
-    i = s < extra ? s * (clusters - in_last) + cluster - in_last : taken + (s - extra) * clusters + cluster;
-    if (i >= p.second.num_items) return false;
-  }
-  const WorkItem w = work_item(i, q->num_tiles, q->split_tiles);
-  const TileCoord tc = tile_coord(w.tile, q->num_m_blocks, q->num_n_blocks, q->group_m);
-  item.m_blk = tc.m_blk;
-  item.n_blk = tc.n_blk;
-  item.half = w.half;
-  return true;
-}
 
 struct GluLayout {
   static constexpr int CG = 2;
@@ -119,10 +71,6 @@ struct GluLayout {
 
 namespace {
 
-// Instruction descriptor (see idesc_bf16): BF16 operands, bits 15 / 16: A / B has its M / N dimension innermost.
-__host__ __device__ constexpr uint32_t idesc_glu(int m, int n, bool a_mn, bool b_mn) {
-  return idesc_bf16(m, n) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
-}
 // kind::f8f6f4, E4M3 x E4M3 -> FP32 (operand formats 0), both operands K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
@@ -137,22 +85,7 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, 
       : "memory");
 }
 
-// Descriptor of an operand with its M (or N) dimension innermost, as a TMA box of 64 columns x 128
-// rows with 128-byte swizzle leaves it: 8 rows of the summed dimension are 1024 bytes (the stride
-// offset), the next 64 columns are the next box (the leading offset).
-__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t smem_addr) {
-  return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) |
-         (static_cast<uint64_t>(GluLayout::ATOM_BYTES >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
-         (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
-}
-
 // ---------------------------------------------------------------- producers (warps 0, 2)
-
-struct GluMaps {
-  CUtensorMap a0, a1;      // forward: X (both); backward: dg, du
-  CUtensorMap b0, b1, b2;  // Wg, Wu; backward: X
-  CUtensorMap c0, c1, c2;  // forward: H, g, u; backward: dX, dWg, dWu
-};
 
 template <int MODE>
 __device__ __forceinline__ void glu_producer(const GluParams& p, const GluMaps& maps, uint32_t base, uint32_t rank,
@@ -246,8 +179,8 @@ __device__ __forceinline__ void glu_mma(const GluParams& p, uint32_t base, uint3
   constexpr int STAGE_K = E4M3 ? 256 : 128, MMA_K = E4M3 ? 32 : 16;
   const uint32_t bar_full = base + L::OFF_BAR, bar_empty = bar_full + 8 * L::STAGES;
   const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
-  const uint64_t a_k = umma_desc_sw128(base + L::OFF_A), a_mn = umma_desc_mn(base + L::OFF_A);
-  const uint64_t b0 = FORWARD ? umma_desc_sw128(base + L::OFF_B) : umma_desc_mn(base + L::OFF_B);
+  const uint64_t a_k = umma_desc_sw128(base + L::OFF_A), a_mn = umma_desc_mn(base + L::OFF_A, L::ATOM_BYTES);
+  const uint64_t b0 = FORWARD ? umma_desc_sw128(base + L::OFF_B) : umma_desc_mn(base + L::OFF_B, L::ATOM_BYTES);
   uint32_t stage = 0, phase = 0;
   bool ok = true;
   GluItem item;
@@ -586,18 +519,9 @@ int glu_max_clusters(int device) {
   return n;
 }
 
-// B's boxes are half its rows, so that a half tile's load is one box.
-int map_kb(CUtensorMap* m, const void* p, int depth, int rows) {
-  return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, depth, rows, uint64_t(depth) * 2, 64, 64,
-                        CU_TENSOR_MAP_SWIZZLE_128B);
-}
-// A BF16 operand with the summed dimension along its rows (K-major) or along its columns (MN-major).
-int map_k(CUtensorMap* m, const void* p, int depth, int rows, long long ld) {
-  return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, depth, rows, uint64_t(ld) * 2, 64, 128,
-                        CU_TENSOR_MAP_SWIZZLE_128B);
-}
-int map_mn(CUtensorMap* m, const void* p, int cols, int depth, long long ld) {
-  return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, cols, depth, uint64_t(ld) * 2, 64, 128,
+// A BF16 operand in boxes of 64 elements of its rows (the summed dimension if it is K-major, else columns) x `rows`.
+int map_in(CUtensorMap* m, const void* p, int cols, int rows, long long ld, int box_rows) {
+  return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, cols, rows, uint64_t(ld) * 2, 64, box_rows,
                         CU_TENSOR_MAP_SWIZZLE_128B);
 }
 int map_out(CUtensorMap* m, const void* p, int cols, int rows, long long ld) {
@@ -606,14 +530,14 @@ int map_out(CUtensorMap* m, const void* p, int cols, int rows, long long ld) {
 }
 
 // The tiles of a product; `rows` and `cols` are those of one output, of which `outputs` lie one after the other along
-// the rows; `cols_a_tile`: output columns of a 256-column accumulator.
-int plan_product(GluProduct* q, int rows, int cols, int depth, int stage, int halves, int outputs, int cols_a_tile) {
-  using L = GluLayout;
+// the rows; tile_rows, cols_a_tile: rows of a pair's tile and output columns of its 256-column accumulator.
+int plan_product(GluProduct* q, int rows, int cols, int depth, int stage, int halves, int outputs, int tile_rows,
+                 int cols_a_tile) {
   q->rows = rows;
   q->cols = cols;
   q->depth = depth;
   q->k_iters = halves * ceil_div(depth, stage);
-  const long long m = static_cast<long long>(outputs) * ceil_div(rows, L::TILE_M);
+  const long long m = static_cast<long long>(outputs) * ceil_div(rows, tile_rows);
   q->num_n_blocks = ceil_div(cols, cols_a_tile);
   if (m * q->num_n_blocks > 0x1FFFFFFFLL) return GEMM_ERR_UNSUPPORTED_SHAPE;
   q->num_m_blocks = static_cast<int>(m);
@@ -623,21 +547,22 @@ int plan_product(GluProduct* q, int rows, int cols, int depth, int stage, int ha
 }
 
 // The order of a product's tiles on `clusters` pairs, for operands of `bytes` per element.
-void order_product(GluProduct* q, int clusters, double bytes, long long l2_bytes) {
-  using L = GluLayout;
-  q->group_m = choose_group_m(static_cast<int>(std::min<long long>(1LL * q->num_m_blocks * L::TILE_M, 0x7FFFFFFF)),
-                              static_cast<int>(std::min<long long>(1LL * q->num_n_blocks * L::BLOCK_N, 0x7FFFFFFF)),
-                              std::max(q->depth, 1), L::TILE_M, L::BLOCK_N, bytes, 0.0, clusters, l2_bytes);
+void order_product(GluProduct* q, int clusters, int tile_rows, double bytes, long long l2_bytes) {
+  constexpr int BLOCK_N = GluLayout::BLOCK_N;
+  q->group_m = choose_group_m(static_cast<int>(std::min<long long>(1LL * q->num_m_blocks * tile_rows, 0x7FFFFFFF)),
+                              static_cast<int>(std::min<long long>(1LL * q->num_n_blocks * BLOCK_N, 0x7FFFFFFF)),
+                              std::max(q->depth, 1), tile_rows, BLOCK_N, bytes, 0.0, clusters, l2_bytes);
 }
 
 // The co-resident pairs take the tiles of both products (the second may have none).
 template <int MODE>
-int glu_launch(const GluMaps& m, GluParams& p, double bytes, int device, const DeviceInfo* info, cudaStream_t stream) {
+int glu_launch(const GluMaps& m, GluParams& p, bool wide, double bytes, int device, const DeviceInfo* info,
+               cudaStream_t stream) {
   using L = GluLayout;
   p.status = device_status_word(device);
   p.wait_limit_ns = RunOptions().wait_limit_ns;
   if (p.status == nullptr) return GEMM_ERR_NO_DEVICE;
-  const int wave = glu_max_clusters(device);
+  const int wave = wide ? glu_wide_max_clusters(device) : glu_max_clusters(device);
   if (wave <= 0) return GEMM_ERR_LAUNCH;
   GluProduct &a = p.main, &b = p.second;
   p.ahead = 0;
@@ -655,8 +580,10 @@ int glu_launch(const GluMaps& m, GluParams& p, double bytes, int device, const D
     b.num_items = b.num_tiles + b.split_tiles;
   }
   const int clusters = std::min(a.num_items + b.num_items, wave);
-  order_product(&a, clusters, bytes, info->l2_bytes);
-  if (b.num_tiles > 0) order_product(&b, clusters, bytes, info->l2_bytes);
+  const int tile_rows = wide ? 2 * L::TILE_M : L::TILE_M;
+  order_product(&a, clusters, tile_rows, bytes, info->l2_bytes);
+  if (b.num_tiles > 0) order_product(&b, clusters, tile_rows, bytes, info->l2_bytes);
+  if (wide) return glu_wide_launch(m, p, MODE == kGluBackward, clusters, stream);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * L::CG), 1, 1);
@@ -680,6 +607,33 @@ int glu_launch(const GluMaps& m, GluParams& p, double bytes, int device, const D
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether BF16 products of the given tiles (512 rows each; std: 256 rows) and stages run on the 512 x 256 pair tile. It
+// moves a quarter fewer bytes from L2 per operation but has half the tiles and one accumulator, so it needs a deep sum
+// and is taken where the launch, in tile-times of the 256 x 256 tile, is shorter with wide tiles at 2 / 1.06 each (the
+// gain per unit of work that the two tiles of the plain product showed, schedule.h).
+bool glu_wide_rule(long long std_tiles, long long wide_tiles, int depth, int wave) {
+  return depth >= 2048 && 2.0 * launch_tile_times(wide_tiles, wave) / 1.06 < launch_tile_times(std_tiles, wave);
+}
+
+bool glu_forward_wide(int M, int N, int K, int wave) {
+  using L = GluLayout;
+  const long long n_tiles = ceil_div(N, L::FEATURES);
+  return glu_wide_rule(ceil_div(M, L::TILE_M) * n_tiles, ceil_div(M, 2 * L::TILE_M) * n_tiles, K, wave);
+}
+bool glu_backward_wide(int M, int N, int K, bool dx, bool dw, int wave) {
+  using L = GluLayout;
+  if (M == 0) return false;
+  // in tiles of dW (their depth is M), of which one of dX (depth 2 N) counts several
+  const double long_tile = dw ? 2.0 * N / M : 1.0;
+  const long long k_tiles = ceil_div(K, L::BLOCK_N);
+  auto tiles = [&](int tile_rows) {
+    return static_cast<long long>(dx ? long_tile * ceil_div(M, tile_rows) * k_tiles : 0.0) +
+           (dw ? 2LL * ceil_div(N, tile_rows) * k_tiles : 0LL);
+  };
+  const int depth = !dw ? static_cast<int>(std::min(2LL * N, 0x7FFFFFFFLL)) : !dx ? M : std::min(M, N);
+  return glu_wide_rule(tiles(L::TILE_M), tiles(2 * L::TILE_M), depth, wave);
+}
+
 bool known_act(int act) { return act == GEMM_GLU_SILU || act == GEMM_GLU_GELU_TANH || act == GEMM_GLU_RELU; }
 
 int zero_rows(void* p, size_t row_bytes, long long ld_bytes, int rows, cudaStream_t s) {
@@ -712,6 +666,13 @@ using namespace dtcp;
 
 extern "C" {
 
+int gemm_glu_plan(int M, int N, int K, int wave, int* forward, int* backward) {
+  if (M < 0 || N < 0 || K < 0 || wave <= 0 || forward == nullptr || backward == nullptr) return GEMM_ERR_INVALID_ARG;
+  *forward = M <= kGluFewRows ? 0 : glu_forward_wide(M, N, K, wave) ? 512 : 256;
+  *backward = glu_backward_wide(M, N, K, true, true, wave) ? 512 : 256;
+  return GEMM_OK;
+}
+
 int gemm_glu_bf16(const void* X, const void* Wg, const void* Wu, void* H, float* preact, int M, int N, int K, int act,
                   void* stream, const gemm_glu_strides_t* strides) {
   using L = GluLayout;
@@ -739,9 +700,10 @@ int gemm_glu_bf16(const void* X, const void* Wg, const void* Wu, void* H, float*
   }
   GluMaps m;
   GluParams p = {};
-  int st = map_k(&m.a0, X, K, M, ld.x);
-  if (st == GEMM_OK) st = map_kb(&m.b0, Wg, K, N);
-  if (st == GEMM_OK) st = map_kb(&m.b1, Wu, K, N);
+  const bool wide = glu_forward_wide(M, N, K, glu_max_clusters(device));
+  int st = map_in(&m.a0, X, K, M, ld.x, wide ? 64 : 128);
+  if (st == GEMM_OK) st = map_in(&m.b0, Wg, K, N, K, 64);  // (half its rows: a half tile's load is one box)
+  if (st == GEMM_OK) st = map_in(&m.b1, Wu, K, N, K, 64);
   if (st == GEMM_OK) st = map_out(&m.c0, H, N, M, ld.h);
   if (st != GEMM_OK) return st;
   m.a1 = m.b2 = m.a0;
@@ -756,8 +718,8 @@ int gemm_glu_bf16(const void* X, const void* Wg, const void* Wu, void* H, float*
   }
   p.act = act;
   p.save = preact != nullptr ? 1 : 0;
-  st = plan_product(&p.main, M, N, K, 128, 1, 1, L::FEATURES);
-  return st != GEMM_OK ? st : glu_launch<kGluForward>(m, p, 2.0, device, info, s);
+  st = plan_product(&p.main, M, N, K, wide ? 64 : 128, 1, 1, wide ? 2 * L::TILE_M : L::TILE_M, L::FEATURES);
+  return st != GEMM_OK ? st : glu_launch<kGluForward>(m, p, wide, 2.0, device, info, s);
 }
 
 int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const float* wg_scale, const void* Wu,
@@ -803,8 +765,8 @@ int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const flo
   p.x_scale = x_scale;
   p.g_scale = wg_scale;
   p.u_scale = wu_scale;
-  st = plan_product(&p.main, M, N, K, 256, 1, 1, L::FEATURES);
-  return st != GEMM_OK ? st : glu_launch<kGluForwardE4m3>(m, p, 1.0, device, info, s);
+  st = plan_product(&p.main, M, N, K, 256, 1, 1, L::TILE_M, L::FEATURES);
+  return st != GEMM_OK ? st : glu_launch<kGluForwardE4m3>(m, p, false, 1.0, device, info, s);
 }
 
 int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const void* Wu, const float* preact, void* dX,
@@ -868,22 +830,24 @@ int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const 
   if (st == GEMM_OK) {
     GluMaps m;
     GluParams p = {};
-    st = map_k(&m.a0, dgu, N, M, 2LL * N);  // (a box of 64 features x 128 rows is the same for either order)
-    if (st == GEMM_OK) st = map_k(&m.a1, dgu + N, N, M, 2LL * N);
+    const bool wide = glu_backward_wide(M, N, K, dX != nullptr, dWg != nullptr, glu_max_clusters(device));
+    const int stage = wide ? 64 : 128, tile_rows = wide ? 2 * L::TILE_M : L::TILE_M;
+    st = map_in(&m.a0, dgu, N, M, 2LL * N, stage);  // (a box of 64 features is the same for either order)
+    if (st == GEMM_OK) st = map_in(&m.a1, dgu + N, N, M, 2LL * N, stage);
     m.b0 = m.b1 = m.b2 = m.c0 = m.c1 = m.c2 = m.a0;
     if (dX != nullptr) {
-      if (st == GEMM_OK) st = map_mn(&m.b0, Wg, K, N, K);
-      if (st == GEMM_OK) st = map_mn(&m.b1, Wu, K, N, K);
+      if (st == GEMM_OK) st = map_in(&m.b0, Wg, K, N, K, stage);
+      if (st == GEMM_OK) st = map_in(&m.b1, Wu, K, N, K, stage);
       if (st == GEMM_OK) st = map_out(&m.c0, dX, K, M, ld.dx);
-      if (st == GEMM_OK) st = plan_product(&p.main, M, K, N, 128, 2, 1, L::BLOCK_N);
+      if (st == GEMM_OK) st = plan_product(&p.main, M, K, N, stage, 2, 1, tile_rows, L::BLOCK_N);
     }
     if (dWg != nullptr) {
-      if (st == GEMM_OK) st = map_mn(&m.b2, X, K, M, ld.x);
+      if (st == GEMM_OK) st = map_in(&m.b2, X, K, M, ld.x, stage);
       if (st == GEMM_OK) st = map_out(&m.c1, dWg, K, N, K);
       if (st == GEMM_OK) st = map_out(&m.c2, dWu, K, N, K);
-      if (st == GEMM_OK) st = plan_product(&p.second, N, K, M, 128, 1, 2, L::BLOCK_N);
+      if (st == GEMM_OK) st = plan_product(&p.second, N, K, M, stage, 1, 2, tile_rows, L::BLOCK_N);
     }
-    if (st == GEMM_OK) st = glu_launch<kGluBackward>(m, p, 2.0, device, info, s);
+    if (st == GEMM_OK) st = glu_launch<kGluBackward>(m, p, wide, 2.0, device, info, s);
   }
   if (cudaFreeAsync(ws, s) != cudaSuccess && st == GEMM_OK) st = GEMM_ERR_LAUNCH;
   return st;

@@ -1,0 +1,84 @@
+// glu_common.cuh -- what the gated feed-forward block's tensor-core kernels share: the products and their work items,
+// tensor maps, and descriptors for operands with their M or N dimension innermost.
+#pragma once
+
+#include <cuda.h>
+
+#include "common.cuh"
+#include "host_common.h"
+
+namespace dtcp {
+
+enum GluMode { kGluForward = 0, kGluForwardE4m3 = 1, kGluBackward = 2 };
+
+// The tiles of one product: rows x cols of output, the summed dimension `depth` (dX: of one half) in `k_iters` stages.
+struct GluProduct {
+  int rows, cols, depth, k_iters;
+  int num_m_blocks, num_n_blocks, num_tiles, group_m;
+  int split_tiles, num_items;  // trailing tiles cut into halves of their columns; work items = tiles + split_tiles
+};
+
+struct GluParams {
+  GluProduct main;    // forward: H; backward: dX
+  GluProduct second;  // backward: dWg, then dWu (rows and blocks of both)
+  int ahead;          // backward: items of `second` that each cluster without a tile in dX's last wave takes meanwhile
+  int act, save;
+  const float* x_scale;  // E4M3: scales of X's rows, Wg's and Wu's
+  const float* g_scale;
+  const float* u_scale;
+  unsigned* status;
+  unsigned long long wait_limit_ns;
+};
+
+// One work item.
+struct GluItem {
+  int m_blk, n_blk, half;
+  bool second;
+};
+
+// Item `it` of a cluster; false past its last one.
+__device__ __forceinline__ bool glu_item(const GluParams& p, int cluster, int clusters, int it, GluItem& item) {
+  const GluProduct* q = &p.main;
+  int i = cluster + it * clusters;
+  item.second = i >= p.main.num_items;
+  if (item.second) {
+    q = &p.second;
+    const int in_last = p.main.num_items % clusters;  // clusters with a tile in the last wave of the first product
+    const int before = p.main.num_items / clusters + (cluster < in_last ? 1 : 0);
+    int s = it - before;
+    const int extra = in_last > 0 && cluster >= in_last ? p.ahead : 0;
+    const int taken = in_last > 0 ? p.ahead * (clusters - in_last) : 0;
+    i = s < extra ? s * (clusters - in_last) + cluster - in_last : taken + (s - extra) * clusters + cluster;
+    if (i >= p.second.num_items) return false;
+  }
+  const WorkItem w = work_item(i, q->num_tiles, q->split_tiles);
+  const TileCoord tc = tile_coord(w.tile, q->num_m_blocks, q->num_n_blocks, q->group_m);
+  item.m_blk = tc.m_blk;
+  item.n_blk = tc.n_blk;
+  item.half = w.half;
+  return true;
+}
+
+struct GluMaps {
+  CUtensorMap a0, a1;      // forward: X (both); backward: dg, du
+  CUtensorMap b0, b1, b2;  // Wg, Wu; backward: X
+  CUtensorMap c0, c1, c2;  // forward: H, g, u; backward: dX, dWg, dWu
+};
+
+// Instruction descriptor (see idesc_bf16): BF16 operands, bits 15 / 16: A / B has its M / N dimension innermost.
+__host__ __device__ constexpr uint32_t idesc_glu(int m, int n, bool a_mn, bool b_mn) {
+  return idesc_bf16(m, n) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+// Descriptor of an operand with its M (or N) dimension innermost, as TMA boxes of 64 columns with 128-byte swizzle
+// leave it: 8 rows of the summed dimension are 1024 bytes (the stride offset), the next 64 columns are the next box,
+// `box_bytes` on (the leading offset).
+__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t smem_addr, uint32_t box_bytes) {
+  return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(box_bytes >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+// The 512 x 256 pair tile (glu_wide.cu): p's products are planned for it, `clusters` pairs take them.
+int glu_wide_max_clusters(int device);
+int glu_wide_launch(const GluMaps& m, const GluParams& p, bool backward, int clusters, cudaStream_t stream);
+
+}  // namespace dtcp

@@ -262,3 +262,28 @@ def test_many_tiles_per_cluster_repeat_bit_for_bit():
     want, root = gradient(dh, x, wg, wu, "silu")
     for a, b, r in zip(got, want, root):
         assert torch.all((a.double() - b).abs() <= 2.0 ** -8 * b.abs() + (8 / math.sqrt(3) * 2.0 ** -8 + 2.0 ** -10) * r)
+
+
+@pytest.mark.parametrize("M,N,K,act", [(2500, 7000, 2056, "silu"), (3000, 2600, 4104, "gelu_tanh"),
+                                       (3077, 5128, 2312, "silu")])
+def test_large_tiles(M, N, K, act):
+    """Ragged problems on the 512 x 256 pair tile, forward and backward, each against FP64 and twice bit for bit."""
+    assert g.glu_plan(M, N, K) == (512, 512)
+    x, wg, wu, dh = problem(M, N, K, M + K)
+    check_forward(g.glu_bf16(x, wg, wu, act=act), x.double(), wg.double(), wu.double(), act)
+    h, saved = g.glu_bf16(x, wg, wu, act=act, save=True)
+    gd, ud = check_forward(h, x.double(), wg.double(), wu.double(), act)
+    steps = (K / 16 + 16) * 2.0 ** -23
+    assert torch.all((saved[:, :N].double() - gd).abs() <= steps * (x.double().abs() @ wg.double().abs().T))
+    assert torch.all((saved[:, N:].double() - ud).abs() <= steps * (x.double().abs() @ wu.double().abs().T))
+    got = g.glu_bf16_backward(dh, x, wg, wu, saved, act=act)
+    want, root = gradient(dh, x, wg, wu, act)
+    for a, b, r in zip(got, want, root):
+        assert torch.all((a.double() - b).abs() <= 2.0 ** -8 * b.abs() + (8 / math.sqrt(3) * 2.0 ** -8 + 2.0 ** -10) * r)
+    again = g.glu_bf16_backward(dh, x, wg, wu, saved, act=act)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    only = g.glu_bf16_backward(dh, x, wg, wu, saved, act=act, weight_grads=False)[0]
+    assert torch.all((only.double() - want[0]).abs() <= 2.0 ** -8 * want[0].abs() + 0.02 * root[0])
+    only = g.glu_bf16_backward(dh, x, wg, wu, saved, act=act, input_grad=False)[1:]
+    for a, b, r in zip(only, want[1:], root[1:]):
+        assert torch.all((a.double() - b).abs() <= 2.0 ** -8 * b.abs() + 0.02 * r)

@@ -139,3 +139,14 @@ def test_glu_backward_refusals():
     assert glu_backward(strides=g.gemm_glu_strides_t(0, 0, 12, 0)) == SHAPE
     assert glu_backward(strides=g.gemm_glu_strides_t(0, 0, 0, 4)) == BAD
     assert glu_backward(dwg=8) == ALIGN and glu_backward(pre=8) == ALIGN
+
+
+def test_glu_plan():
+    assert g.glu_plan(1, 28672, 8192)[0] == 0 and g.glu_plan(16, 28672, 8192)[0] == 0
+    assert g.glu_plan(17, 28672, 8192)[0] == 256   # one row of tiles: no gain from taller ones
+    assert g.glu_plan(4096, 14336, 4096) == (512, 512)
+    assert g.glu_plan(4000, 14336, 1024)[0] == 256  # a shallow sum
+    assert g.glu_plan(300, 1368, 520) == (256, 256)
+    for bad in ((-1, 8, 8, 76), (8, -8, 8, 76), (8, 8, -8, 76), (8, 8, 8, 0)):
+        with pytest.raises(g.GemmError):
+            g.glu_plan(*bad)
