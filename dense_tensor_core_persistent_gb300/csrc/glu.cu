@@ -254,11 +254,13 @@ struct GluStaging {
     __syncwarp();
     return buf;
   }
-  __device__ __forceinline__ void store(uint32_t lane, const CUtensorMap* map, uint32_t buf, int col, int row) {
+  __device__ __forceinline__ void store(uint32_t lane, const CUtensorMap* map, uint32_t buf, int col, int row,
+                                        bool streaming) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(map, buf, col, row);
+      if (streaming) tma_store_2d_streaming(map, buf, col, row);
+      else tma_store_2d(map, buf, col, row);
       bulk_commit_group();
     }
   }
@@ -277,7 +279,7 @@ __device__ __forceinline__ void glu_store_bf16(GluStaging& st, uint32_t lane, co
       w[t] = pack_bf16x2_rn(__float_as_uint(v[8 * j + 2 * t]), __float_as_uint(v[8 * j + 2 * t + 1]));
     st_shared_v4(addr + ((static_cast<uint32_t>(j) ^ sw) << 4), w[0], w[1], w[2], w[3]);
   }
-  st.store(lane, map, buf, col, row);
+  st.store(lane, map, buf, col, row, false);
 }
 
 // 32 columns of this lane's row as FP32 (128-byte rows, 128-byte swizzle).
@@ -288,7 +290,7 @@ __device__ __forceinline__ void glu_store_f32(GluStaging& st, uint32_t lane, con
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     st_shared_v4(addr + ((static_cast<uint32_t>(j) ^ sw) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-  st.store(lane, map, buf, col, row);
+  st.store(lane, map, buf, col, row, true);
 }
 
 template <int MODE>
@@ -462,7 +464,8 @@ __global__ void __launch_bounds__(256) glu_gate_grad_kernel(const uint16_t* dh, 
     const uint4 d4 = *reinterpret_cast<const uint4*>(dh + row * lddh + col);
     const float4* gp = reinterpret_cast<const float4*>(pre + row * 2 * N + col);
     const float4* up = reinterpret_cast<const float4*>(pre + row * 2 * N + N + col);
-    const float4 ga = gp[0], gb = gp[1], ua = up[0], ub = up[1];
+    // (read once: streaming loads)
+    const float4 ga = __ldcs(gp), gb = __ldcs(gp + 1), ua = __ldcs(up), ub = __ldcs(up + 1);
     const float g[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
     const float u[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
     const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};

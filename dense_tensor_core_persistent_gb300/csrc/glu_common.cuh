@@ -77,6 +77,16 @@ __device__ __forceinline__ uint64_t umma_desc_mn(uint32_t smem_addr, uint32_t bo
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
 
+// 2-D tile store of data that is not read again soon: it leaves L2 first, before the operands that are read again.
+__device__ __forceinline__ void tma_store_2d_streaming(const CUtensorMap* m, uint32_t src, int32_t x, int32_t y) {
+  asm volatile(
+      "{\n\t.reg .b64 policy;\n\t"
+      "createpolicy.fractional.L2::evict_first.b64 policy, 1.0;\n\t"
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3}], [%1], policy;\n\t}" ::"l"(m),
+      "r"(src), "r"(x), "r"(y)
+      : "memory");
+}
+
 // The 512 x 256 pair tile (glu_wide.cu): p's products are planned for it, `clusters` pairs take them.
 int glu_wide_max_clusters(int device);
 int glu_wide_launch(const GluMaps& m, const GluParams& p, bool backward, int clusters, cudaStream_t stream);

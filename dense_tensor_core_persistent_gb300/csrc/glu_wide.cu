@@ -217,11 +217,13 @@ struct GluWideStaging {
     __syncwarp();
     return buf;
   }
-  __device__ __forceinline__ void store(uint32_t lane, const CUtensorMap* map, uint32_t buf, int col, int row) {
+  __device__ __forceinline__ void store(uint32_t lane, const CUtensorMap* map, uint32_t buf, int col, int row,
+                                        bool streaming) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(map, buf, col, row);
+      if (streaming) tma_store_2d_streaming(map, buf, col, row);
+      else tma_store_2d(map, buf, col, row);
       bulk_commit_group();
     }
   }
@@ -244,7 +246,7 @@ __device__ __forceinline__ void glu_wide_store(GluWideStaging& st, uint32_t lane
                    pack_bf16x2_rn(v[8 * j + 2], v[8 * j + 3]), pack_bf16x2_rn(v[8 * j + 4], v[8 * j + 5]),
                    pack_bf16x2_rn(v[8 * j + 6], v[8 * j + 7]));
   }
-  st.store(lane, map, buf, col, row);
+  st.store(lane, map, buf, col, row, f32);
 }
 
 template <bool BACKWARD>
