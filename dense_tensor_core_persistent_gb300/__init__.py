@@ -560,6 +560,11 @@ def _matrix(t, what, dtype, shape=None):
     return t.stride(0)
 
 
+def _address(t):
+    """A tensor's device address, or NULL for None (the conveniences call the library directly: 2 us less a call)."""
+    return None if t is None else t.data_ptr()
+
+
 def _vector(t, what, dtype, n):
     if t.dtype is not dtype or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous CUDA {dtype} vector of {n} is needed, got {t.dtype} {tuple(t.shape)}")
@@ -616,7 +621,11 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-5, out: str = "bf16"
         rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
     if ldx or ldr or lds:
         strides = gemm_norm_strides_t(ldx, ldr, lds, 0)
-    gemm_rms_norm(x, residual, weight, written, y, scales, rstd, rows, cols, eps, fmt, stream, strides)
+    status = lib().gemm_rms_norm(x.data_ptr(), _address(residual), _address(weight), _address(written), y.data_ptr(),
+                                 _address(scales), _address(rstd), rows, cols, eps, fmt, _stream(stream),
+                                 _byref_or_null(strides))
+    if status:
+        raise GemmError(status, "gemm_rms_norm")
     return NormOutput(y, scales, total, rstd)
 
 
@@ -632,10 +641,14 @@ def rms_norm_backward(dy, total, weight, rstd, dsum=None, weight_grad: bool = Tr
     _vector(rstd, "rstd", torch.float32, rows)
     if weight is not None:
         _vector(weight, "weight", bf16, cols)
-    dx = torch.empty((rows, cols), dtype=bf16, device=dy.device)
+    dx = torch.empty_like(dy, memory_format=torch.contiguous_format)
     dw = torch.empty(cols, dtype=torch.float32, device=dy.device) if weight_grad else None
     strides = gemm_norm_backward_strides_t(lddy, lds, ldds, 0) if lddy or lds or ldds else None
-    gemm_rms_norm_backward(dy, total, weight, rstd, dsum, dx, dw, rows, cols, stream, strides)
+    status = lib().gemm_rms_norm_backward(dy.data_ptr(), total.data_ptr(), _address(weight), rstd.data_ptr(),
+                                          _address(dsum), dx.data_ptr(), _address(dw), rows, cols, _stream(stream),
+                                          _byref_or_null(strides))
+    if status:
+        raise GemmError(status, "gemm_rms_norm_backward")
     return dx, dw
 
 
@@ -673,8 +686,11 @@ def token_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, stream
     if top > 0:
         top_logprobs = torch.empty((rows, top), dtype=torch.float32, device=logits.device)
         top_ids = torch.empty((rows, top), dtype=torch.int32, device=logits.device)
-    gemm_token_logprobs(logits, kind, tokens, logprob, entropy, lse, top, top_logprobs, top_ids, rows, vocab, ld, scale,
-                        stream)
+    status = lib().gemm_token_logprobs(logits.data_ptr(), kind, _address(tokens), _address(logprob), entropy.data_ptr(),
+                                       lse.data_ptr(), top, _address(top_logprobs), _address(top_ids), rows, vocab, ld,
+                                       scale, _stream(stream))
+    if status:
+        raise GemmError(status, "gemm_token_logprobs")
     return TokenLogprobs(logprob, entropy, lse, top_logprobs, top_ids)
 
 
@@ -692,8 +708,12 @@ def token_logprobs_backward(logits, tokens, lse, entropy, dlogprob, dentropy=Non
         if t is not None:
             _vector(t, what, dtype, rows)
     dlogits = logits if inplace else torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
-    gemm_token_logprobs_backward(logits, kind, tokens, lse, entropy, dlogprob, dentropy, dlogits, rows, vocab, ld,
-                                 ld if inplace else 0, scale, stream)
+    status = lib().gemm_token_logprobs_backward(logits.data_ptr(), kind, _address(tokens), lse.data_ptr(),
+                                                _address(entropy), _address(dlogprob), _address(dentropy),
+                                                dlogits.data_ptr(), rows, vocab, ld, ld if inplace else 0, scale,
+                                                _stream(stream))
+    if status:
+        raise GemmError(status, "gemm_token_logprobs_backward")
     return dlogits
 
 
@@ -724,7 +744,10 @@ def glu_bf16(x, wg, wu, act: str = "silu", save: bool = False, stream=None):
     _contiguous(wu, "wu", bf16, (N, K))
     h = torch.empty((M, N), dtype=bf16, device=x.device)
     saved = torch.empty((M, 2 * N), dtype=torch.float32, device=x.device) if save else None
-    gemm_glu_bf16(x, wg, wu, h, saved, M, N, K, kind, stream, gemm_glu_strides_t(ldx, 0, 0, 0) if ldx else None)
+    status = lib().gemm_glu_bf16(x.data_ptr(), wg.data_ptr(), wu.data_ptr(), h.data_ptr(), _address(saved), M, N, K, kind,
+                                 _stream(stream), gemm_glu_strides_t(ldx, 0, 0, 0) if ldx else None)
+    if status:
+        raise GemmError(status, "gemm_glu_bf16")
     return (h, saved) if save else h
 
 
@@ -740,8 +763,11 @@ def glu_e4m3(x, x_scale, wg, wg_scale, wu, wu_scale, act: str = "silu", stream=N
     for t, what, n in ((x_scale, "x_scale", M), (wg_scale, "wg_scale", N), (wu_scale, "wu_scale", N)):
         _vector(t, what, torch.float32, n)
     h = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    gemm_glu_e4m3(x, x_scale, wg, wg_scale, wu, wu_scale, h, M, N, K, kind, stream,
-                  gemm_glu_strides_t(ldx, 0, 0, 0) if ldx else None)
+    status = lib().gemm_glu_e4m3(x.data_ptr(), x_scale.data_ptr(), wg.data_ptr(), wg_scale.data_ptr(), wu.data_ptr(),
+                                 wu_scale.data_ptr(), h.data_ptr(), M, N, K, kind, _stream(stream),
+                                 gemm_glu_strides_t(ldx, 0, 0, 0) if ldx else None)
+    if status:
+        raise GemmError(status, "gemm_glu_e4m3")
     return h
 
 
@@ -758,8 +784,11 @@ def glu_bf16_backward(dh, x, wg, wu, saved, act: str = "silu", input_grad: bool 
     _contiguous(wu, "wu", bf16, (N, K))
     _contiguous(saved, "saved", torch.float32, (M, 2 * N))
     dx = torch.empty((M, K), dtype=bf16, device=x.device) if input_grad else None
-    dwg = torch.empty((N, K), dtype=bf16, device=x.device) if weight_grads else None
-    dwu = torch.empty((N, K), dtype=bf16, device=x.device) if weight_grads else None
-    gemm_glu_bf16_backward(dh, x, wg, wu, saved, dx, dwg, dwu, M, N, K, kind, stream,
-                           gemm_glu_strides_t(ldx, 0, lddh, 0) if ldx or lddh else None)
+    dwg = torch.empty_like(wg) if weight_grads else None
+    dwu = torch.empty_like(wg) if weight_grads else None
+    status = lib().gemm_glu_bf16_backward(dh.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), saved.data_ptr(),
+                                          _address(dx), _address(dwg), _address(dwu), M, N, K, kind, _stream(stream),
+                                          gemm_glu_strides_t(ldx, 0, lddh, 0) if ldx or lddh else None)
+    if status:
+        raise GemmError(status, "gemm_glu_bf16_backward")
     return dx, dwg, dwu
