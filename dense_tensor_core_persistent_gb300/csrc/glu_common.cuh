@@ -82,8 +82,8 @@ __device__ __forceinline__ void tma_store_2d_streaming(const CUtensorMap* m, uin
   asm volatile(
       "{\n\t.reg .b64 policy;\n\t"
       "createpolicy.fractional.L2::evict_first.b64 policy, 1.0;\n\t"
-      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3}], [%1], policy;\n\t}" ::"l"(m),
-      "r"(src), "r"(x), "r"(y)
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3}], [%1], policy;\n\t}"
+      ::"l"(m), "r"(src), "r"(x), "r"(y)
       : "memory");
 }
 

@@ -106,10 +106,11 @@ int run_pack_scales2_copy(const void* SF0, void* out0, int rows0, const void* SF
 int run_copy_rows(void* dst, const void* A, int M, int K, cudaStream_t stream, int pdl = 1);
 
 // The gated feed-forward block for few rows (glu_few.cu): X, Wg, Wu in BF16 or E4M3 (then with scales); preact:
-// [g | u] in FP32 or null. Up to these many rows it is the faster kernel, measured on GB300 against the 256 x 256
-// pair tile: BF16, 28672 x 8192 (N x K): 142 against 233 us for 1 row, 155 against 157 for 16; 14336 x 4096: 47 against
-// 50 for 16. E4M3, 28672 x 8192: 84 against 110 us for 8 rows, but 97 against 81 for 16.
-constexpr int kGluFewRows = 16, kGluFewRowsE4m3 = 8;
+// [g | u] in FP32 or null. Up to so many rows it is the faster kernel, measured on GB300 against the pair tile of glu.cu:
+// 8 rows x 28672 x 8192 142 against 146 us in BF16 and 75 against 76 in E4M3, x 14336 x 4096 39 against 48 and 23.6
+// against 24.5, x 8192 x 2048 13.9 against 15.7 and 7.8 against 12.5. With 16 rows (two passes of the matrix
+// instructions) it was the slower one, 155 against 151 us.
+constexpr int kGluFewRows = 8;
 struct GluFewParams {
   const void* x;
   const void* wg;

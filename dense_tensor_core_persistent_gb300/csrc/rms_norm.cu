@@ -467,7 +467,8 @@ __global__ void __maxnreg__(norm_regs<VPT>(80, 128)) rms_norm_backward_kernel(co
 
 // dw[c] = sum of the partial rows in a fixed order: 32 warps take every 32nd row of 32 columns, then add up.
 constexpr int kSumWarps = 32;
-__global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const float* partial, int rows, int cols, float* dw) {
+__global__ void __launch_bounds__(32 * kSumWarps)
+    column_sum_kernel(const float* partial, int rows, int cols, float* dw) {
   __shared__ float part[kSumWarps][33];
   pdl_launch_dependents();
   pdl_wait();
@@ -562,7 +563,8 @@ const void* backward_kernel(int vpt) {
 struct RowPlace {
   unsigned first, stride;
   RowPlace(const void* p, long long ld, int bytes)
-      : first(static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) / bytes % 8)), stride(static_cast<unsigned>(ld % 8)) {}
+      : first(static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) / bytes % 8)),
+        stride(static_cast<unsigned>(ld % 8)) {}
   bool operator==(const RowPlace& o) const { return first == o.first && stride == o.stride; }
   bool aligned() const { return first == 0 && stride == 0; }
 };
@@ -693,7 +695,8 @@ int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const f
       const float* partial = p.partial;
       int partial_rows = grid;
       void* sum_args[] = {&partial, &partial_rows, &cols, &dW};
-      rc = norm_launch(reinterpret_cast<const void*>(column_sum_kernel), ceil_div(cols, 32), 32 * kSumWarps, st, sum_args);
+      rc = norm_launch(reinterpret_cast<const void*>(column_sum_kernel), ceil_div(cols, 32), 32 * kSumWarps, st,
+                       sum_args);
     }
     if (cudaFreeAsync(ws, st) != cudaSuccess && rc == GEMM_OK) rc = GEMM_ERR_LAUNCH;
   }

@@ -890,8 +890,8 @@ using namespace dtcp;
 extern "C" {
 
 int gemm_token_logprobs(const void* logits, int type, const long long* tokens, float* logprob, float* entropy,
-                        float* lse, int top, float* top_logprobs, int* top_ids, int rows, int vocab, long long ld, float scale,
-                        void* stream) {
+                        float* lse, int top, float* top_logprobs, int* top_ids, int rows, int vocab, long long ld,
+                        float scale, void* stream) {
   if (rows < 0 || vocab < 0 || top < 0 || ld < 0 || (type != GEMM_LOGITS_BF16 && type != GEMM_LOGITS_F32))
     return GEMM_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || scale > 3.0e38f) return GEMM_ERR_INVALID_ARG;

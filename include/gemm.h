@@ -435,7 +435,8 @@ int gemm_measure_mma_rate(int kind, double* flop_per_clock_per_sm);
 enum {
   GEMM_NORM_BF16 = 0,  /* Y: rows x cols BF16 */
   GEMM_NORM_E4M3 = 1,  /* Y: rows x cols E4M3 codes; scales: one FP32 per row; y ~ code * scale */
-  GEMM_NORM_NVFP4 = 2  /* Y: rows x cols/2 bytes of E2M1 codes; scales: rows x cols/16 E4M3 bytes: A and SFA of gemm_nvfp4 */
+  GEMM_NORM_NVFP4 = 2  /* Y: rows x cols/2 bytes of E2M1 codes; scales: rows x cols/16 E4M3 bytes; A and SFA of
+                          gemm_nvfp4 */
 };
 
 /* Row strides in elements (E4M3: of Y in bytes); 0 = cols. A stride is at least cols. */
@@ -506,9 +507,9 @@ enum { GEMM_LOGITS_BF16 = 0, GEMM_LOGITS_F32 = 1 };
  * rows == 0: nothing to do. vocab == 0 with rows: GEMM_ERR_INVALID_ARG. One kernel launch, asynchronous on
  * `stream`, no workspace; the same inputs give the same bits.
  */
-int gemm_token_logprobs(const void* logits, int type, const long long* tokens, float* logprob, float* entropy, float* lse,
-                        int top, float* top_logprobs, int* top_ids, int rows, int vocab, long long ld, float scale,
-                        void* stream);
+int gemm_token_logprobs(const void* logits, int type, const long long* tokens, float* logprob, float* entropy,
+                        float* lse, int top, float* top_logprobs, int* top_ids, int rows, int vocab, long long ld,
+                        float scale, void* stream);
 
 /*
  * gemm_token_logprobs_backward -- gradient of logprob and entropy with respect to the logits:
