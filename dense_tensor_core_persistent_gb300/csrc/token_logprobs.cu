@@ -19,7 +19,8 @@
 // different. Logits of minus infinity take no part: where there are fewer others than are wanted, the lowest indices
 // follow.
 //
-// Bound by the bytes of the logits. A row is split over a cluster of 1 to 8 CTAs that join through
+// Bound by the bytes of the logits: measured on GB300, 4096 x 131072 BF16 159 us (6.7 TB/s), with 20 alternatives 211;
+// the gradient 328 us (6.5 TB/s). A row is split over a cluster of 1 to 8 CTAs that join through
 // shared memory, so few rows still use many SMs and no workspace or second launch is needed.
 #include <cuda_runtime.h>
 
@@ -39,9 +40,8 @@ constexpr int kLogprobMaxTop = 32;
 // holding registers, also through the reductions at a row's end, when they are the next row's.
 constexpr int kLogprobBatch = 8;  // vectors per thread and chunk
 constexpr int kLogprobChunk = kLogprobBatch * kLogprobThreads;  // vectors
-constexpr int kLogprobStages = 2;
-constexpr int kLogprobCtas = 3;  // per SM
-constexpr int kLogprobRingBytes = kLogprobStages * kLogprobChunk * 16;
+constexpr int kLogprobStages = 3;  // of the ring with two CTAs an SM; two with three CTAs
+constexpr int kLogprobCtas = 3;    // per SM at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct LogprobParams {
@@ -53,7 +53,7 @@ struct LogprobParams {
   float* top_logprobs;
   int* top_ids;
   long long ld;
-  int rows, vocab, top, cluster;
+  int rows, vocab, top, cluster, stages;
   float scale;
   unsigned* status;
   unsigned long long wait_limit_ns;
@@ -90,6 +90,7 @@ struct Vec<uint16_t> {  // BF16
   static constexpr int N = 8;
   static __device__ __forceinline__ float value(uint16_t e) { return __uint_as_float(static_cast<uint32_t>(e) << 16); }
   static constexpr uint32_t kMinusInfWord = 0xFF80FF80u;
+  static __device__ __forceinline__ uint16_t minus_inf() { return 0xFF80u; }
   static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -132,6 +133,7 @@ struct Vec<float> {
   static constexpr int N = 4;
   static __device__ __forceinline__ float value(float e) { return e; }
   static constexpr uint32_t kMinusInfWord = 0xFF800000u;
+  static __device__ __forceinline__ float minus_inf() { return kMinusInf; }
   template <int M>
   static __device__ __forceinline__ float largest(const uint4 (&p)[M]) {
     float a[M];
@@ -188,7 +190,7 @@ struct Row {
   }
 };
 
-// Part `k` of `parts` of a row: vectors [v0, v1), of which [n0, n1) are whole. Thread (v - n0) mod 512 owns vector v.
+// Part `k` of `parts` of a row: vectors [v0, v1), of which [n0, n1) are whole.
 template <typename T>
 struct Part {
   int v0, v1, n0, n1;
@@ -201,7 +203,6 @@ struct Part {
     if (v0 == 0 && !row.whole(0)) n0 = 1;
     if (n1 == row.vectors && n1 > n0 && !row.whole(n1 - 1)) --n1;
   }
-  __device__ __forceinline__ int owner(int v) const { return (v - n0) & (kLogprobThreads - 1); }
 };
 
 // Copies `bytes` (a multiple of 16) from global to this CTA's shared memory, both at 16-byte boundaries; completion is
@@ -260,6 +261,14 @@ __device__ __forceinline__ float key_value(unsigned long long key) {
   return __uint_as_float((hi & 0x80000000u) ? (hi == 0xFFFFFFFFu ? 0x7FFFFFFFu : hi & 0x7FFFFFFFu) : ~hi);
 }
 
+// The order of logits as unsigned numbers: 0 for minus infinity (and for none).
+__device__ __forceinline__ uint32_t order_of(float l) {
+  return l == kMinusInf ? 0u : static_cast<uint32_t>(key_of(l, 0) >> 32);
+}
+__device__ __forceinline__ float order_value(uint32_t o) {
+  return o == 0 ? kMinusInf : key_value(static_cast<unsigned long long>(o) << 32);
+}
+
 __device__ __forceinline__ unsigned long long warp_max_key(unsigned long long key) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32));
   const uint32_t lo =
@@ -278,37 +287,21 @@ struct Sums {
 // c (from - to), with no mass (and no NaN) left where that has no finite value.
 __device__ __forceinline__ float shift(float from, float to, float c) { return fmaxf((from - to) * c, -1.0e30f); }
 
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c) {
-  if (a.m == kMinusInf) return b;
-  if (b.m == kMinusInf) return a;
+// The sums of a warp's lanes as one, the same in every lane, relative to the largest of their references.
+__device__ __forceinline__ Sums warp_join(const Sums& a, float c) {
+  const bool mass = a.m != kMinusInf;
   Sums r;
-  r.m = max_nan(a.m, b.m);
-  if (a.ref == b.ref) {
-    r.ref = a.ref;
-    r.s = a.s + b.s;
-    r.q = a.q + b.q;
-    return r;
-  }
-  const bool a_low = a.m < b.m;  // (a NaN has made s one, whichever way this goes)
-  const Sums lo = a_low ? a : b, hi = a_low ? b : a;
-  const float d = shift(lo.ref, hi.ref, c), f = ex2_approx(d);
-  r.ref = hi.ref;
-  r.s = fmaf(lo.s, f, hi.s);
-  r.q = fmaf(fmaf(lo.s, d, lo.q), f, hi.q);
-  return r;
-}
-
-__device__ __forceinline__ Sums warp_join(Sums t, float c) {
+  r.m = order_value(__reduce_max_sync(0xffffffffu, order_of(a.m)));
+  r.ref = order_value(__reduce_max_sync(0xffffffffu, mass ? order_of(a.ref) : 0u));
+  const float d = a.ref == r.ref ? 0.0f : shift(a.ref, r.ref, c), f = ex2_approx(d);
+  r.s = mass ? a.s * f : 0.0f;
+  r.q = mass ? fmaf(a.s, d, a.q) * f : 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    Sums u;
-    u.m = __shfl_xor_sync(0xffffffffu, t.m, o);
-    u.ref = __shfl_xor_sync(0xffffffffu, t.ref, o);
-    u.s = __shfl_xor_sync(0xffffffffu, t.s, o);
-    u.q = __shfl_xor_sync(0xffffffffu, t.q, o);
-    t = join(t, u, c);
+    r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
+    r.q += __shfl_xor_sync(0xffffffffu, r.q, o);
   }
-  return t;
+  return r;
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -338,14 +331,6 @@ struct LogprobShared {
   int candidates, left, winners, scanners;
   uint32_t abort;
 };
-
-// The order of logits as unsigned numbers: 0 for minus infinity (and for none).
-__device__ __forceinline__ uint32_t order_of(float l) {
-  return l == kMinusInf ? 0u : static_cast<uint32_t>(key_of(l, 0) >> 32);
-}
-__device__ __forceinline__ float order_value(uint32_t o) {
-  return o == 0 ? kMinusInf : key_value(static_cast<unsigned long long>(o) << 32);
-}
 
 // An order that at least `top` of the threads' orders reach, or 0: if j of them in each of r warps reach one and
 // j r >= top, top do; the largest such one over j is the r-th largest of the warps' j-th largest. One barrier.
@@ -581,47 +566,43 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_
     feed.rank = rank;
     feed.cluster = p.cluster;
     feed.start(r0);
-    for (int s = 0; s < kLogprobStages; ++s) feed.issue(ring_addr + s * STAGE, full + 8 * s);
+    for (int s = 0; s < p.stages; ++s) feed.issue(ring_addr + s * STAGE, full + 8 * s);
   }
   const float c = p.scale * kLog2e;
   const uint64_t c2 = f2_pack(c, c);
   uint32_t stage = 0, parity = 0;  // of the next chunk
   uint32_t chunks = 0;
+  const bool asks = tid == 0 && rank == 0 && p.logprob != nullptr;
+  long long next_token = asks ? p.tokens[r0] : -1;
   bool ok = true;  // after a wait that gave up: no more waiting, the launch runs out (its results are void)
   for (long long r = r0; r < p.rows; r += clusters) {
     const Row<T> row(static_cast<const T*>(p.logits) + r * p.ld, p.vocab);
     const Part<T> part(row, rank, p.cluster);
     Running run{kMinusInf, 0.0f, 0ull, 0ull};
     bool masked = false;
-    auto add_slow = [&](float x0, float x1) {
-      if (run.ordinary(c)) run.add<true>(f2_pack(x0, x1), c2, f2_pack(-run.ref, -run.ref));
-      else run.count(x0, x1);
-    };
-    // a vector at the row's ends that is partly outside it: its thread takes it element by element
-    auto partial = [&](int v) {
-      float x[N];
-      row.load(v, x);
-      float top = x[0];
-#pragma unroll
-      for (int j = 1; j < N; ++j) top = max_nan(top, x[j]);
-      if (TOP) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (x[j] != kMinusInf) list_candidate(sh, key_of(x[j], row.first(v) + j));  // (what is no part of the row is)
-      }
-      run.see(top, c);
-#pragma unroll
-      for (int j = 0; j < N; j += 2) add_slow(x[j], x[j + 1]);
-    };
+    // the logits of vectors at the row's ends that are partly outside it, one per lane of the last warp: asked for here,
+    // taken after the chunks
+    T end_logit = Vec<T>::minus_inf();
+    int end_index = -1;
+    if (warp == kLogprobWarps - 1 && lane < 2 * N) {
+      const bool tail = lane >= N;
+      if (tail ? part.n1 < part.v1 : part.v0 < part.n0) end_index = row.first(tail ? part.n1 : part.v0) + lane % N;
+      if (end_index >= row.vocab) end_index = -1;
+      if (end_index >= 0) end_logit = row.base[end_index];
+    }
+    // the token's logit is asked for at the row's start, the next row's token before that
+    const long long token = next_token;
+    T given = T(0);
+    if (asks && token >= 0 && token < p.vocab) given = row.base[token];
+    if (asks && r + clusters < p.rows) next_token = p.tokens[r + clusters];
     Peaks peaks{kMinusInf, kMinusInf, 0};
     if (TOP && tid == 0) sh.candidates = sh.left = sh.winners = sh.scanners = 0;
     if (TOP && tid < kLogprobMaxTop) sh.top[tid] = 0;
     if (TOP) __syncthreads();
-    if (part.v0 < part.n0 && tid == kLogprobThreads - 1) partial(part.v0);
     for (int v = part.n0; v < part.n1; v += kLogprobChunk) {
       if (tid == 0 && chunks > 0 && ok) {
         // the chunk before this one: refill its place once every warp has read it
-        const uint32_t s = stage == 0 ? kLogprobStages - 1 : stage - 1;
+        const uint32_t s = stage == 0 ? p.stages - 1 : stage - 1;
         const uint32_t ph = stage == 0 ? parity ^ 1u : parity;
         ok = wait_phase(empty + 8 * s, ph, wctx, status_code(kRoleProducer, s));
         if (ok) feed.issue(ring_addr + s * STAGE, full + 8 * s);
@@ -646,8 +627,9 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_
       __syncwarp();
       if (lane == 0) mbar_arrive_local(empty + 8 * stage);
       ++chunks;
-      stage = stage + 1 == kLogprobStages ? 0u : stage + 1;
+      stage = stage + 1 == static_cast<uint32_t>(p.stages) ? 0u : stage + 1;
       parity = stage == 0 ? parity ^ 1u : parity;
+      if (left <= 0) continue;  // none of a row's last chunk (whole warps of a short one)
       const float most = Vec<T>::largest(raw);
       if (TOP) peaks.see(most, (v - part.n0) / kLogprobChunk);
       run.see(most, c);
@@ -669,9 +651,11 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_
         }
         if (masked || !full_chunk) {
 #pragma unroll
-          for (int u = 0; u < kLogprobBatch; ++u)
+          for (int u = 0; u < kLogprobBatch; ++u) {
+            if (u * kLogprobThreads >= left) continue;
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) run.add<true>(Vec<T>::pair(raw[u], j), c2, minus_ref2);
+          }
         }
       } else {
 #pragma unroll 1
@@ -687,7 +671,13 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_
         }
       }
     }
-    if (part.n1 < part.v1 && part.owner(part.n1) == tid) partial(part.n1);
+    if (end_index >= 0) {
+      const float x = Vec<T>::value(end_logit);
+      if (TOP && x != kMinusInf) list_candidate(sh, key_of(x, end_index));
+      run.see(x, c);
+      if (run.ordinary(c)) run.add<true>(f2_pack(x, kMinusInf), c2, f2_pack(-run.ref, -run.ref));
+      else run.count(x, kMinusInf);
+    }
     Sums t;
     {
       float s0, s1, q0, q1;
@@ -708,14 +698,13 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_
     if (p.cluster > 1) cluster_sync_all();
     else __syncthreads();
     if (rank == 0) {
-      const uint32_t total_addr = smem_u32(&sh.total);
-      Sums all = sh.total;
-      for (int k = 1; k < p.cluster; ++k) {
-        const uint32_t a = mapa_shared(total_addr, k);
-        all = join(all, Sums{__uint_as_float(ld_cluster_u32(a)), __uint_as_float(ld_cluster_u32(a + 4)),
-                             __uint_as_float(ld_cluster_u32(a + 8)), __uint_as_float(ld_cluster_u32(a + 12))},
-                   c);
+      Sums all{kMinusInf, 0.0f, 0.0f, 0.0f};
+      if (lane < p.cluster) {
+        const uint32_t at = mapa_shared(smem_u32(&sh.total), lane);
+        all = Sums{__uint_as_float(ld_cluster_u32(at)), __uint_as_float(ld_cluster_u32(at + 4)),
+                   __uint_as_float(ld_cluster_u32(at + 8)), __uint_as_float(ld_cluster_u32(at + 12))};
       }
+      all = warp_join(all, c);
       const bool empty = all.m == kMinusInf;  // no logit has any mass
       const float log_s = logf(all.s);
       const float lse = empty ? kMinusInf : fmaf(p.scale, all.ref, log_s);
@@ -846,7 +835,8 @@ int run_token_logprobs(const LogprobParams& p, int ctas, int device, cudaStream_
   static std::atomic<unsigned long long> sized[2] = {};  // devices whose limit of shared memory is raised, by kernel
   const unsigned long long bit = 1ull << device;
   if ((sized[p.top > 0].load(std::memory_order_acquire) & bit) == 0) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLogprobRingBytes) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kLogprobStages * kLogprobChunk * 16) != cudaSuccess) {
       cudaGetLastError();
       return GEMM_ERR_LAUNCH;
     }
@@ -854,7 +844,7 @@ int run_token_logprobs(const LogprobParams& p, int ctas, int device, cudaStream_
   }
   launch_config(cfg, attr, static_cast<long long>(std::min(p.rows, ctas / p.cluster)) * p.cluster, kLogprobThreads,
                 p.cluster, stream);
-  cfg.dynamicSmemBytes = kLogprobRingBytes;
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.stages) * kLogprobChunk * 16;
   if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
@@ -926,18 +916,23 @@ int gemm_token_logprobs(const void* logits, int type, const long long* tokens, f
   p.status = device_status_word(device);
   p.wait_limit_ns = RunOptions().wait_limit_ns;
   if (p.status == nullptr) return GEMM_ERR_NO_DEVICE;
-  // kLogprobCtas CTAs an SM, each stepping over the rows (or its part of them). CTAs a row, by the time of the launch:
-  // its rounds, each as long as a part at the CTA's share of the memory's rate (15 KB a microsecond) and about 2.5 us
-  // of reductions, and as long as each thread has a vector at least.
-  const int ctas = kLogprobCtas * info->num_sms / 8 * 8;
-  const double row_us = static_cast<double>(vocab) * (type == GEMM_LOGITS_BF16 ? 2 : 4) / 15e3;
+  // Two or three CTAs an SM, each stepping over the rows (or its part of them), and 1 to 8 CTAs a row, by the time of the
+  // launch: its rounds, each as long as a part at the CTA's share of the memory's rate (44 KB a microsecond and SM) and
+  // about 2.5 us of reductions; each thread has a vector at least. Measured on GB300: 1500 x 50001 FP32 51.1 us with
+  // two CTAs an SM and 53.9 with three, 4096 x 131072 BF16 166.8 and 159.2.
+  const double row_bytes = static_cast<double>(vocab) * (type == GEMM_LOGITS_BF16 ? 2 : 4);
   double best = 0.0;
-  p.cluster = 1;
-  for (int c = 1; c <= 8; c *= 2) {
-    const double us = static_cast<double>((static_cast<long long>(rows) * c + ctas - 1) / ctas) * (row_us / c + 2.5);
-    if (c == 1 || (us < best && row_us * 15e3 >= c * 16.0 * kLogprobThreads)) {
+  int ctas = 0;
+  for (int per_sm = kLogprobCtas; per_sm >= 2; --per_sm) {
+    const int n = per_sm * info->num_sms / 8 * 8;
+    for (int c = 1; c <= 8; c *= 2) {
+      const double us = static_cast<double>((static_cast<long long>(rows) * c + n - 1) / n) *
+                        (row_bytes * per_sm / (44e3 * c) + 2.5);
+      if (ctas != 0 && (us >= best || row_bytes < c * 16.0 * kLogprobThreads)) continue;
       best = us;
+      ctas = n;
       p.cluster = c;
+      p.stages = per_sm == 2 ? 3 : 2;
     }
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
