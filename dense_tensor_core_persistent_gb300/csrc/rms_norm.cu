@@ -298,7 +298,7 @@ template <int VPT>
 constexpr int norm_regs(int two, int four) { return VPT == 1 ? 64 : VPT == 2 ? two : VPT == 4 ? four : 128; }
 
 template <int VPT, int FORMAT, int ACCESS>
-__global__ void __maxnreg__(norm_regs<VPT>(64, 80)) rms_norm_kernel(const NormParams p) {
+__global__ void __maxnreg__(norm_regs<VPT>(56, 80)) rms_norm_kernel(const NormParams p) {
   __shared__ float slots[2][32];
   __shared__ uint32_t slots_max[2][32];
   const int warps = blockDim.x >> 5;
@@ -465,7 +465,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(80, 128)) rms_norm_backward_kernel(co
   }
 }
 
-// dw[c] = sum of the partial rows in a fixed order: 32 warps take every 32nd row of 32 columns, then add up.
+// dw[c] = sum of the partial rows in a fixed order: 32 warps take every 32nd row of 32 columns, then a column each.
 constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps)
     column_sum_kernel(const float* partial, int rows, int cols, float* dw) {
@@ -480,12 +480,8 @@ __global__ void __launch_bounds__(32 * kSumWarps)
     for (int r = warp; r < rows; r += kSumWarps) v += partial[static_cast<long long>(r) * cols + c];
   part[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && c < cols) {
-    v = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kSumWarps; ++k) v += part[k][lane];
-    dw[c] = v;
-  }
+  v = warp_sum(part[lane][warp]);  // one column a warp
+  if (lane == 0 && blockIdx.x * 32 + warp < cols) dw[blockIdx.x * 32 + warp] = v;
 }
 
 // ---------------------------------------------------------------- host side
