@@ -489,7 +489,7 @@ def gemm_glu_bf16_backward(dH, X, Wg, Wu, preact, dX, dWg, dWu, M: int, N: int, 
 
 
 def glu_plan(M: int, N: int, K: int, wave: int = 76) -> tuple[int, int]:
-    """Rows of the pair tile that glu_bf16 (0: the few-row kernel) and its gradient use for this problem (host only)."""
+    """Rows of the pair tile that glu_bf16 (0: the kernel for few rows) and its gradient use for this problem (host only)."""
     fwd, bwd = ctypes.c_int(), ctypes.c_int()
     _check(lib().gemm_glu_plan(M, N, K, wave, ctypes.byref(fwd), ctypes.byref(bwd)), "gemm_glu_plan")
     return fwd.value, bwd.value

@@ -21,7 +21,8 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libdtcp_gemm.so")
 SOURCES = ["api.cu", "gemm_bf16.cu", "gemm_bf16_wide.cu", "gemm_nvfp4.cu", "pack_scales.cu", "noalloc.cu",
-           "mma_rate.cu", "rms_norm.cu", "token_logprobs.cu", "glu.cu", "glu_few.cu", "glu_wide.cu"]
+           "mma_rate.cu", "rms_norm.cu", "token_logprobs.cu", "glu.cu", "glu_wide.cu",
+           "glu_rows.cu"]
 HEADERS = ["ptx.cuh", "common.cuh", "schedule.h", "host_common.h", "glu_act.cuh", "glu_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v", "-I", os.path.join(ROOT, "include")]

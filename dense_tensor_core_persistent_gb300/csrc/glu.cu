@@ -24,7 +24,7 @@
 // Warp roles: 0 loads A, 2 loads B, 1 allocates TMEM and issues the MMAs (leader CTA), 4..7 epilogue,
 // one TMEM lane quadrant each; stores go through swizzled staging tiles and TMA.
 //
-// Bound by the tensor cores for many rows and by the bytes of Wg and Wu for few.
+// Bound by the tensor cores; up to kGluRows rows, where the bytes of Wg and Wu are the bound, glu_rows.cu computes H^T.
 //
 // For the gradient g and u are kept in FP32 (8 bytes per element and a tenth of the block's time at
 // most): kept in BF16 they would add a rounding to dg and du next to the one their MMA operand needs.
@@ -41,25 +41,24 @@
 
 namespace dtcp {
 
-// ATOMS: 128-byte swizzle rows of the summed dimension per stage; A_ROWS: rows of A a CTA holds.
-template <int ATOMS_, int A_ROWS_, int STAGES_>
-struct GluLayoutOf {
+struct GluLayout {
   static constexpr int CG = 2;
   static constexpr int CTA_M = 128, TILE_M = 256;
   static constexpr int BLOCK_N = 256, B_ROWS = 128;  // B rows each CTA loads
   static constexpr int FEATURES = 128;               // forward: features of a tile
-  static constexpr int ATOMS = ATOMS_, A_ROWS = A_ROWS_, STAGES = STAGES_;
-  static constexpr int KSTEPS = 4 * ATOMS;           // MMAs per stage, 32 bytes of a K-major row each
+  static constexpr int ATOMS = 2;                    // 128-byte swizzle rows of the summed dimension per stage
+  static constexpr int KSTEPS = 8;                   // MMAs per stage, 32 bytes of a K-major row each
+  static constexpr int STAGES = 3;
   static constexpr int ATOM_BYTES = 128 * 128;       // 128 rows (or 128 K x 64 columns) of 128 bytes
-  static constexpr int A_ATOM_BYTES = A_ROWS * 128;
-  static constexpr int A_BYTES = ATOMS * A_ATOM_BYTES, B_BYTES = ATOMS * ATOM_BYTES;
+  static constexpr int OPERAND_BYTES = ATOMS * ATOM_BYTES;
+  static constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
   static constexpr int ACC_COLS = 256, TMEM_COLS = 512;
   static constexpr int WARP_A = 0, WARP_MMA = 1, WARP_B = 2, EPI_WARP0 = 4, EPI_WARPS = 4;
   static constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
   static constexpr int EPI_BUFS = 2, EPI_BUF_BYTES = 32 * 128;  // 32 rows of 128 bytes
   static constexpr int OFF_A = 0;
-  static constexpr int OFF_B = STAGES * A_BYTES;
-  static constexpr int OFF_EPI = OFF_B + STAGES * B_BYTES;
+  static constexpr int OFF_B = STAGES * OPERAND_BYTES;
+  static constexpr int OFF_EPI = OFF_B + STAGES * OPERAND_BYTES;
   static constexpr int OFF_BAR = OFF_EPI + EPI_WARPS * EPI_BUFS * EPI_BUF_BYTES;
   // full[S], empty[S], tmem_full[2], tmem_empty[2], drain
   static constexpr int NUM_BARS = 2 * STAGES + 5;
@@ -67,14 +66,8 @@ struct GluLayoutOf {
   static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
   static constexpr int SMEM_BYTES = OFF_ABORT + 4 + 1024;  // slack to align the base to 1024 bytes
   static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
-  static_assert(OFF_EPI % 1024 == 0 && A_ATOM_BYTES % 1024 == 0, "1024-byte alignment");
+  static_assert(OFF_EPI % 1024 == 0, "1024-byte alignment");
 };
-using GluLayout = GluLayoutOf<2, 128, 3>;
-// At most 64 rows of X: the weights' bytes are the bound, and with half of A a stage there is room for a fourth
-// stage of them. The MMA reads 128 rows of A all the same; what it takes for the other 64 (whatever the next bytes of
-// shared memory hold) makes accumulator rows that are never read. Measured on GB300, 64 rows x 28672 x 8192: 148 us
-// against 158 with three stages in BF16, 78 against 83 in E4M3; x 14336 x 4096: 43 against 47.5, and 25 against 28.
-using GluFewLayout = GluLayoutOf<2, 64, 4>;
 
 namespace {
 
@@ -94,11 +87,12 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, 
 
 // ---------------------------------------------------------------- producers (warps 0, 2)
 
-template <int MODE, class L>
+template <int MODE>
 __device__ __forceinline__ void glu_producer(const GluParams& p, const GluMaps& maps, uint32_t base, uint32_t rank,
                                              bool load_a, int cluster_idx, int num_clusters, const WaitCtx& wctx) {
+  using L = GluLayout;
   constexpr bool FORWARD = MODE != kGluBackward;
-  constexpr int STAGE_K = (MODE == kGluForwardE4m3 ? 128 : 64) * L::ATOMS;
+  constexpr int STAGE_K = MODE == kGluForwardE4m3 ? 256 : 128;
   const uint32_t bar_full = base + L::OFF_BAR, bar_empty = bar_full + 8 * L::STAGES;
   const uint32_t dst0 = base + (load_a ? L::OFF_A : L::OFF_B);
   uint32_t stage = 0, phase = 0;
@@ -107,7 +101,7 @@ __device__ __forceinline__ void glu_producer(const GluParams& p, const GluMaps& 
   for (int it = 0; ok && glu_item(p, cluster_idx, num_clusters, it, item); ++it) {
     const int half = item.half > 0 ? 1 : 0;
     const int b_boxes = item.half >= 0 ? 1 : 2;  // of 64 rows (K-major: per atom) or 64 columns (MN-major)
-    const uint32_t stage_bytes = L::A_BYTES + L::B_BYTES / 2 * b_boxes;
+    const uint32_t stage_bytes = L::OPERAND_BYTES + L::OPERAND_BYTES / 2 * b_boxes;
     const bool down = (it & 1) != 0;  // start on the blocks the last wave of tiles read last
     const int k_iters = item.second ? p.second.k_iters : p.main.k_iters;
     const CUtensorMap *m0, *m1;  // of the first and the second half of the stages
@@ -151,7 +145,7 @@ __device__ __forceinline__ void glu_producer(const GluParams& p, const GluMaps& 
       const uint32_t full = bar_full + 8 * stage;
       if (load_a && rank == 0) mbar_arrive_expect_tx(full, 2u * stage_bytes);
       const uint32_t bar = mapa_shared(full, 0);
-      const uint32_t dst = dst0 + stage * (load_a ? L::A_BYTES : L::B_BYTES);
+      const uint32_t dst = dst0 + stage * L::OPERAND_BYTES;
       if (mn) {
         const int boxes = load_a ? 2 : b_boxes;
         for (int c = 0; c < boxes; ++c)
@@ -161,7 +155,7 @@ __device__ __forceinline__ void glu_producer(const GluParams& p, const GluMaps& 
         for (int a = 0; a < L::ATOMS; ++a) {
           const int x = k * STAGE_K + a * (STAGE_K / L::ATOMS);
           if (load_a) {
-            tma_load_2d_pair(dst + a * L::A_ATOM_BYTES, map, x, first, bar);
+            tma_load_2d_pair(dst + a * L::ATOM_BYTES, map, x, first, bar);
           } else {
             for (int c = 0; c < b_boxes; ++c)
               tma_load_2d_pair(dst + a * L::ATOM_BYTES + c * (L::ATOM_BYTES / 2), map, x, first + c * 64, bar);
@@ -177,11 +171,12 @@ __device__ __forceinline__ void glu_producer(const GluParams& p, const GluMaps& 
 
 // ---------------------------------------------------------------- MMA issuer (leader, warp 1)
 
-template <int MODE, class L>
+template <int MODE>
 __device__ __forceinline__ void glu_mma(const GluParams& p, uint32_t base, uint32_t tmem_base, int cluster_idx,
                                         int num_clusters, const WaitCtx& wctx) {
+  using L = GluLayout;
   constexpr bool FORWARD = MODE != kGluBackward, E4M3 = MODE == kGluForwardE4m3;
-  constexpr int STAGE_K = (E4M3 ? 128 : 64) * L::ATOMS, MMA_K = E4M3 ? 32 : 16;
+  constexpr int STAGE_K = E4M3 ? 256 : 128, MMA_K = E4M3 ? 32 : 16;
   const uint32_t bar_full = base + L::OFF_BAR, bar_empty = bar_full + 8 * L::STAGES;
   const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
   const uint64_t a_k = umma_desc_sw128(base + L::OFF_A), a_mn = umma_desc_mn(base + L::OFF_A, L::ATOM_BYTES);
@@ -211,17 +206,17 @@ __device__ __forceinline__ void glu_mma(const GluParams& p, uint32_t base, uint3
       tc_fence_after_sync();
       int k = down ? q.k_iters - 1 - kb : kb;
       if (k >= half_iters) k -= half_iters;
-      const uint64_t a = umma_desc_advance(dw ? a_mn : a_k, stage * L::A_BYTES);
-      const uint64_t b = umma_desc_advance(b0, stage * L::B_BYTES);
+      const uint64_t a = umma_desc_advance(dw ? a_mn : a_k, stage * L::OPERAND_BYTES);
+      const uint64_t b = umma_desc_advance(b0, stage * L::OPERAND_BYTES);
       const int left = q.depth - k * STAGE_K;  // a ragged last stage: only the MMAs that hold any of it
       const int steps = left >= STAGE_K ? L::KSTEPS : (left + MMA_K - 1) / MMA_K;
       // MMA kk of a stage: K-major operands advance 32 bytes inside the swizzle row, four per atom;
       // MN-major ones by 16 rows of 128 bytes.
       auto one = [&](int kk) {
-        const uint32_t in_atom = static_cast<uint32_t>(kk % 4) * 32u, atom = static_cast<uint32_t>(kk / 4);
+        const uint32_t step_k = static_cast<uint32_t>((kk / 4) * L::ATOM_BYTES + (kk % 4) * 32);
         const uint32_t step_mn = static_cast<uint32_t>(kk) * 2048u;
-        const uint64_t ad = umma_desc_advance(a, dw ? step_mn : atom * L::A_ATOM_BYTES + in_atom);
-        const uint64_t bd = umma_desc_advance(b, FORWARD ? atom * L::ATOM_BYTES + in_atom : step_mn);
+        const uint64_t ad = umma_desc_advance(a, dw ? step_mn : step_k);
+        const uint64_t bd = umma_desc_advance(b, FORWARD ? step_k : step_mn);
         if constexpr (E4M3) mma_e4m3_pair(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
         else mma_f16<2>(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
       };
@@ -298,10 +293,11 @@ __device__ __forceinline__ void glu_store_f32(GluStaging& st, uint32_t lane, con
   st.store(lane, map, buf, col, row, true);
 }
 
-template <int MODE, class L>
+template <int MODE>
 __device__ __forceinline__ void glu_epilogue(const GluParams& p, const GluMaps& maps, uint32_t base, uint32_t tmem_base,
                                              uint32_t warp, uint32_t lane, uint32_t rank, int cluster_idx,
                                              int num_clusters, const WaitCtx& wctx) {
+  using L = GluLayout;
   constexpr bool FORWARD = MODE != kGluBackward;
   const uint32_t bar_tfull = base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 16;
   const uint32_t q = warp & 3u;  // this warp may access TMEM lanes 32q .. 32q+31
@@ -394,9 +390,10 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const GluMaps& 
   __syncwarp();
 }
 
-template <int MODE, class L>
-__global__ void __launch_bounds__(L::NUM_THREADS, 1)
+template <int MODE>
+__global__ void __launch_bounds__(GluLayout::NUM_THREADS, 1)
     glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluParams p) {
+  using L = GluLayout;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // same offset in both CTAs of a pair
@@ -437,13 +434,13 @@ __global__ void __launch_bounds__(L::NUM_THREADS, 1)
   if (warp < L::EPI_WARP0) {
     if (lane == 0) {
       if (warp == L::WARP_A || warp == L::WARP_B)
-        glu_producer<MODE, L>(p, maps, base, rank, warp == L::WARP_A, cluster_idx, num_clusters, wctx);
+        glu_producer<MODE>(p, maps, base, rank, warp == L::WARP_A, cluster_idx, num_clusters, wctx);
       else if (warp == L::WARP_MMA && rank == 0)
-        glu_mma<MODE, L>(p, base, tmem_base, cluster_idx, num_clusters, wctx);
+        glu_mma<MODE>(p, base, tmem_base, cluster_idx, num_clusters, wctx);
     }
     __syncwarp();
   } else {
-    glu_epilogue<MODE, L>(p, maps, base, tmem_base, warp, lane, rank, cluster_idx, num_clusters, wctx);
+    glu_epilogue<MODE>(p, maps, base, tmem_base, warp, lane, rank, cluster_idx, num_clusters, wctx);
   }
   tc_fence_before_sync();
   cluster_sync_all();
@@ -500,11 +497,8 @@ int glu_max_clusters(int device) {
   std::lock_guard<std::mutex> lock(mu);
   if (device < 0 || device >= 64) return 0;
   if (cache[device] > 0) return cache[device];
-  for (auto k : {glu_kernel<kGluForward, GluLayout>, glu_kernel<kGluForwardE4m3, GluLayout>,
-                 glu_kernel<kGluBackward, GluLayout>, glu_kernel<kGluForward, GluFewLayout>,
-                 glu_kernel<kGluForwardE4m3, GluFewLayout>})
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             std::max(GluLayout::SMEM_BYTES, GluFewLayout::SMEM_BYTES)) != cudaSuccess) {
+  for (auto k : {glu_kernel<kGluForward>, glu_kernel<kGluForwardE4m3>, glu_kernel<kGluBackward>})
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, GluLayout::SMEM_BYTES) != cudaSuccess) {
       cudaGetLastError();
       return 0;
     }
@@ -520,7 +514,7 @@ int glu_max_clusters(int device) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, glu_kernel<kGluForward, GluLayout>, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, glu_kernel<kGluForward>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     return 0;
   }
@@ -564,15 +558,14 @@ void order_product(GluProduct* q, int clusters, int tile_rows, double bytes, lon
 }
 
 // The co-resident pairs take the tiles of both products (the second may have none).
-enum GluTile { kGluStd, kGluFew, kGluWide };
 template <int MODE>
-int glu_launch(const GluMaps& m, GluParams& p, GluTile tile, double bytes, int device, const DeviceInfo* info,
+int glu_launch(const GluMaps& m, GluParams& p, bool wide, double bytes, int device, const DeviceInfo* info,
                cudaStream_t stream) {
   using L = GluLayout;
   p.status = device_status_word(device);
   p.wait_limit_ns = RunOptions().wait_limit_ns;
   if (p.status == nullptr) return GEMM_ERR_NO_DEVICE;
-  const int wave = tile == kGluWide ? glu_wide_max_clusters(device) : glu_max_clusters(device);
+  const int wave = wide ? glu_wide_max_clusters(device) : glu_max_clusters(device);
   if (wave <= 0) return GEMM_ERR_LAUNCH;
   GluProduct &a = p.main, &b = p.second;
   p.ahead = 0;
@@ -590,15 +583,15 @@ int glu_launch(const GluMaps& m, GluParams& p, GluTile tile, double bytes, int d
     b.num_items = b.num_tiles + b.split_tiles;
   }
   const int clusters = std::min(a.num_items + b.num_items, wave);
-  const int tile_rows = tile == kGluWide ? 2 * L::TILE_M : L::TILE_M;
+  const int tile_rows = wide ? 2 * L::TILE_M : L::TILE_M;
   order_product(&a, clusters, tile_rows, bytes, info->l2_bytes);
   if (b.num_tiles > 0) order_product(&b, clusters, tile_rows, bytes, info->l2_bytes);
-  if (tile == kGluWide) return glu_wide_launch(m, p, MODE == kGluBackward, clusters, stream);
+  if (wide) return glu_wide_launch(m, p, MODE == kGluBackward, clusters, stream);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * L::CG), 1, 1);
   cfg.blockDim = dim3(L::NUM_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = tile == kGluFew ? GluFewLayout::SMEM_BYTES : L::SMEM_BYTES;
+  cfg.dynamicSmemBytes = L::SMEM_BYTES;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = L::CG;
@@ -608,10 +601,7 @@ int glu_launch(const GluMaps& m, GluParams& p, GluTile tile, double bytes, int d
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  auto kernel = glu_kernel<MODE, GluLayout>;
-  if constexpr (MODE != kGluBackward)
-    if (tile == kGluFew) kernel = glu_kernel<MODE, GluFewLayout>;
-  if (cudaLaunchKernelEx(&cfg, kernel, m, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, glu_kernel<MODE>, m, p) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
   }
@@ -681,7 +671,7 @@ extern "C" {
 
 int gemm_glu_plan(int M, int N, int K, int wave, int* forward, int* backward) {
   if (M < 0 || N < 0 || K < 0 || wave <= 0 || forward == nullptr || backward == nullptr) return GEMM_ERR_INVALID_ARG;
-  *forward = M <= kGluFewRows ? 0 : glu_forward_wide(M, N, K, wave) ? 512 : 256;
+  *forward = M <= kGluRows ? 0 : glu_forward_wide(M, N, K, wave) ? 512 : 256;
   *backward = glu_backward_wide(M, N, K, true, true, wave) ? 512 : 256;
   return GEMM_OK;
 }
@@ -706,17 +696,15 @@ int gemm_glu_bf16(const void* X, const void* Wg, const void* Wu, void* H, float*
     if (st == GEMM_OK && preact != nullptr) st = zero_rows(preact, size_t(N) * 8, (long long)N * 8, M, s);
     return st;
   }
-  if (M <= kGluFewRows) {
-    const GluFewParams f = {X,       Wg,      Wu,   static_cast<uint16_t*>(H), preact, nullptr, nullptr,
-                            nullptr, ld.x,    ld.h, M,                         N,      K,       act};
-    return run_glu_few(f, false, s);
+  if (M <= kGluRows) {
+    const GluRowsOperands f = {X,       Wg,   Wu,   static_cast<uint16_t*>(H), preact, nullptr, nullptr,
+                               nullptr, ld.x, ld.h, M,                         N,      K,       act};
+    return run_glu_rows(f, false, device, info, s);
   }
   GluMaps m;
   GluParams p = {};
-  const GluTile tile = M <= GluFewLayout::A_ROWS                              ? kGluFew
-                       : glu_forward_wide(M, N, K, glu_max_clusters(device)) ? kGluWide
-                                                                             : kGluStd;
-  int st = map_in(&m.a0, X, K, M, ld.x, tile == kGluStd ? 128 : 64);
+  const bool wide = glu_forward_wide(M, N, K, glu_max_clusters(device));
+  int st = map_in(&m.a0, X, K, M, ld.x, wide ? 64 : 128);
   if (st == GEMM_OK) st = map_in(&m.b0, Wg, K, N, K, 64);  // (half its rows: a half tile's load is one box)
   if (st == GEMM_OK) st = map_in(&m.b1, Wu, K, N, K, 64);
   if (st == GEMM_OK) st = map_out(&m.c0, H, N, M, ld.h);
@@ -733,9 +721,8 @@ int gemm_glu_bf16(const void* X, const void* Wg, const void* Wu, void* H, float*
   }
   p.act = act;
   p.save = preact != nullptr ? 1 : 0;
-  st = plan_product(&p.main, M, N, K, tile == kGluWide ? 64 : 128, 1, 1, tile == kGluWide ? 2 * L::TILE_M : L::TILE_M,
-                    L::FEATURES);
-  return st != GEMM_OK ? st : glu_launch<kGluForward>(m, p, tile, 2.0, device, info, s);
+  st = plan_product(&p.main, M, N, K, wide ? 64 : 128, 1, 1, wide ? 2 * L::TILE_M : L::TILE_M, L::FEATURES);
+  return st != GEMM_OK ? st : glu_launch<kGluForward>(m, p, wide, 2.0, device, info, s);
 }
 
 int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const float* wg_scale, const void* Wu,
@@ -759,10 +746,10 @@ int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const flo
   if (info == nullptr) return err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (K == 0) return zero_rows(H, size_t(N) * 2, ld.h * 2, M, s);
-  if (M <= kGluFewRows) {
-    const GluFewParams f = {X,        Wg,   Wu,   static_cast<uint16_t*>(H), nullptr, x_scale, wg_scale,
-                            wu_scale, ld.x, ld.h, M,                         N,       K,       act};
-    return run_glu_few(f, true, s);
+  if (M <= kGluRows) {
+    const GluRowsOperands f = {X,        Wg,   Wu,   static_cast<uint16_t*>(H), nullptr, x_scale, wg_scale,
+                               wu_scale, ld.x, ld.h, M,                         N,       K,       act};
+    return run_glu_rows(f, true, device, info, s);
   }
   GluMaps m;
   GluParams p = {};
@@ -770,8 +757,7 @@ int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const flo
     return encode_tmap_2d(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, rows, stride, 128, box_rows,
                           CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  const bool few = M <= GluFewLayout::A_ROWS;
-  int st = map8(&m.a0, X, M, ld.x, few ? 64 : 128);
+  int st = map8(&m.a0, X, M, ld.x, 128);
   if (st == GEMM_OK) st = map8(&m.b0, Wg, N, K, 64);
   if (st == GEMM_OK) st = map8(&m.b1, Wu, N, K, 64);
   if (st == GEMM_OK) st = map_out(&m.c0, H, N, M, ld.h);
@@ -783,7 +769,7 @@ int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const flo
   p.g_scale = wg_scale;
   p.u_scale = wu_scale;
   st = plan_product(&p.main, M, N, K, 256, 1, 1, L::TILE_M, L::FEATURES);
-  return st != GEMM_OK ? st : glu_launch<kGluForwardE4m3>(m, p, few ? kGluFew : kGluStd, 1.0, device, info, s);
+  return st != GEMM_OK ? st : glu_launch<kGluForwardE4m3>(m, p, false, 1.0, device, info, s);
 }
 
 int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const void* Wu, const float* preact, void* dX,
@@ -864,7 +850,7 @@ int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const 
       if (st == GEMM_OK) st = map_out(&m.c2, dWu, K, N, K);
       if (st == GEMM_OK) st = plan_product(&p.second, N, K, M, stage, 1, 2, tile_rows, L::BLOCK_N);
     }
-    if (st == GEMM_OK) st = glu_launch<kGluBackward>(m, p, wide ? kGluWide : kGluStd, 2.0, device, info, s);
+    if (st == GEMM_OK) st = glu_launch<kGluBackward>(m, p, wide, 2.0, device, info, s);
   }
   if (cudaFreeAsync(ws, s) != cudaSuccess && st == GEMM_OK) st = GEMM_ERR_LAUNCH;
   return st;

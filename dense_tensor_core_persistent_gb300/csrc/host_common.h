@@ -105,13 +105,12 @@ int run_pack_scales2_copy(const void* SF0, void* out0, int rows0, const void* SF
 // with programmatic stream serialization (the GEMM after it starts its set-up early).
 int run_copy_rows(void* dst, const void* A, int M, int K, cudaStream_t stream, int pdl = 1);
 
-// The gated feed-forward block for few rows (glu_few.cu): X, Wg, Wu in BF16 or E4M3 (then with scales); preact:
-// [g | u] in FP32 or null. Up to so many rows it is the faster kernel, measured on GB300 against the pair tile of glu.cu:
-// 8 rows x 28672 x 8192 142 against 146 us in BF16 and 75 against 76 in E4M3, x 14336 x 4096 39 against 48 and 23.6
-// against 24.5, x 8192 x 2048 13.9 against 15.7 and 7.8 against 12.5. With 16 rows (two passes of the matrix
-// instructions) it was the slower one, 155 against 151 us.
-constexpr int kGluFewRows = 8;
-struct GluFewParams {
+// The gated feed-forward block for few rows (glu_rows.cu): X, Wg, Wu in BF16 or E4M3 (then with scales); preact:
+// [g | u] in FP32 or null. Up to so many rows it is the faster kernel, measured on GB300 against the pair tile of
+// glu.cu: 64 rows x 28672 x 8192 140 against 158 us in BF16 and 74 against 83 in E4M3, x 14336 x 4096 41 against 48 and
+// 24 against 28; 128 rows 154 against 159 and 82 against 85, 48 against 50 and 29.5 against 27.6.
+constexpr int kGluRows = 128;
+struct GluRowsOperands {
   const void* x;
   const void* wg;
   const void* wu;
@@ -123,7 +122,7 @@ struct GluFewParams {
   long long ldx, ldh;
   int rows, features, depth, act;
 };
-int run_glu_few(const GluFewParams& p, bool e4m3, cudaStream_t stream);
+int run_glu_rows(const GluRowsOperands& p, bool e4m3, int device, const DeviceInfo* info, cudaStream_t stream);
 
 // Group size along M for the persistent tile order (see gemm_choose_group_m).
 int choose_group_m(int M, int N, int K, int tile_m, int tile_n, double bytes_per_row_elem,

@@ -580,8 +580,8 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_
     const Part<T> part(row, rank, p.cluster);
     Running run{kMinusInf, 0.0f, 0ull, 0ull};
     bool masked = false;
-    // the logits of vectors at the row's ends that are partly outside it, one per lane of the last warp: asked for here,
-    // taken after the chunks
+    // the logits of vectors at the row's ends that are partly outside it, one per lane of the last warp: asked for
+    // here, taken after the chunks
     T end_logit = Vec<T>::minus_inf();
     int end_index = -1;
     if (warp == kLogprobWarps - 1 && lane < 2 * N) {
@@ -916,8 +916,8 @@ int gemm_token_logprobs(const void* logits, int type, const long long* tokens, f
   p.status = device_status_word(device);
   p.wait_limit_ns = RunOptions().wait_limit_ns;
   if (p.status == nullptr) return GEMM_ERR_NO_DEVICE;
-  // Two or three CTAs an SM, each stepping over the rows (or its part of them), and 1 to 8 CTAs a row, by the time of the
-  // launch: its rounds, each as long as a part at the CTA's share of the memory's rate (44 KB a microsecond and SM) and
+  // Two or three CTAs an SM, each stepping over the rows (or its part of them), and 1 to 8 CTAs a row, by the time of
+  // the launch: its rounds, each as long as a part at the CTA's share of the memory's rate (44 KB a microsecond and SM) and
   // about 2.5 us of reductions; each thread has a vector at least. Measured on GB300: 1500 x 50001 FP32 51.1 us with
   // two CTAs an SM and 53.9 with three, 4096 x 131072 BF16 166.8 and 159.2.
   const double row_bytes = static_cast<double>(vocab) * (type == GEMM_LOGITS_BF16 ? 2 : 4);

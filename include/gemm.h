@@ -574,7 +574,7 @@ int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const 
                            const gemm_glu_strides_t* strides);
 
 /*
- * gemm_glu_plan -- the rows of the pair tile that gemm_glu_bf16 (*forward; 0: the few-row kernel) and
+ * gemm_glu_plan -- the rows of the pair tile that gemm_glu_bf16 (*forward; 0: the kernel for up to 128 rows) and
  * gemm_glu_bf16_backward with all gradients (*backward) use for a problem, 256 or 512, with `wave` co-resident CTA
  * pairs (76 on a 152-SM GB300). Host evaluation, no GPU needed. GEMM_ERR_INVALID_ARG for negative sizes, wave <= 0 or
  * null outputs.

@@ -142,8 +142,8 @@ def test_glu_backward_refusals():
 
 
 def test_glu_plan():
-    assert g.glu_plan(1, 28672, 8192)[0] == 0 and g.glu_plan(8, 28672, 8192)[0] == 0
-    assert g.glu_plan(17, 28672, 8192)[0] == 256   # one row of tiles: no gain from taller ones
+    assert g.glu_plan(1, 28672, 8192)[0] == 0 and g.glu_plan(128, 28672, 8192)[0] == 0
+    assert g.glu_plan(129, 28672, 8192)[0] == 256  # one row of tiles: no gain from taller ones
     assert g.glu_plan(4096, 14336, 4096) == (512, 512)
     assert g.glu_plan(4000, 14336, 1024)[0] == 256  # a shallow sum
     assert g.glu_plan(300, 1368, 520) == (256, 256)
