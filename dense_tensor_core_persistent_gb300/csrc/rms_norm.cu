@@ -9,16 +9,22 @@
 // The norm reads the rounded stream s, the one that later layers and the gradient see.
 // All sums are FP32; every output is rounded once from FP32.
 //
-// Both directions are bound by the bytes they move (forward at most 8 per element, backward 8),
-// so a row is read once: a CTA keeps the whole row in registers between its reduction and its
-// output (groups of 8 columns per thread, up to 8 groups x 512 threads = 32768 columns).
-// CTAs are persistent and step over rows by the grid size, so a thread always owns the same
-// columns: the weight is read once per CTA and the weight's gradient is summed in registers,
-// one partial row per CTA, which a second kernel adds in a fixed order (no atomics).
+// Both directions are bound by the bytes they move (forward at most 8 per element, backward 8), so a row is read once:
+// a thread holds 2 groups of 8 columns (4 or 8 in rows longer than 8192 or 16384), up to 512 threads hold a row. CTAs
+// are persistent, as many as fit on the SMs, and step over rows by the grid size. Each thread copies its groups of the
+// CTA's next row to places of its own in shared memory (cp.async) before it takes the current one from there, so
+// loads stay in flight through the reductions and stores without holding registers or meeting at barriers.
+// A thread always owns the same columns: the weight is read once per CTA and the weight's gradient is summed in
+// registers, one partial row per CTA, which a second kernel adds in a fixed order (no atomics).
 //
 // Rows that no 16-byte vector divides: the groups of a row start at its 16-byte boundary, so
 // all but the first and last of its groups are whole vectors. The grid is a multiple of 8 (or
 // one CTA per row), so that boundary is at the same column for every row of a CTA.
+//
+// Measured on GB300 with inputs larger than L2, residual added: 4000 x 8192 43 us in BF16 (6.1 TB/s) and 38 to E4M3
+// (6.1), 4001 x 4099 22.9 us (5.7); gradient 4000 x 8192 44 us (5.9), with the weight's 48; 4001 x 4099 28.7 (4.6) and
+// 34.5. Off the boundary the rest goes to the row ends' parts and the warps that a row fills in part. With the rows
+// loaded to registers (and as many groups a thread as were best then) the same took 43, 37, 24, 55, 66, 33 and 39 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,6 +37,7 @@
 
 namespace dtcp {
 
+constexpr int kNormMaxSmem = 3 * 8 * 512 * 16;  // dynamic shared memory of a CTA: three inputs, eight groups
 constexpr int kNormMaxCols = 32768 - 8;  // 8 groups of 8 columns x 512 threads, less one group for the boundary
 
 struct NormParams {
@@ -94,54 +101,52 @@ __device__ __forceinline__ uint4 load_elements(const uint16_t* row, int c, int c
   return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
 
-// The groups of NT rows (a null row is not read) as BF16, zero outside [0, cols). Whole vectors are
-// read at a row's ends too, and what is not the row's is masked off (after everything is in flight;
-// `ends`: bit k if group k of any lane of the warp is at an end). `inner`: the vectors at the ends lie
-// between the tensor's first and last element; in its first and last row they are read element by element.
+// A thread's groups of NT rows (a null row is not read) on their way to its own places in shared memory: the copies run
+// through the reduction and the stores of the row before, hold no registers, and put zeros for what lies past the row's
+// end. Groups that start past it are not written. Whole vectors are read at a row's start too, and what lies before it
+// is masked off later (mask_start), but for the first row, where it may lie before the tensor.
 template <int NT, int VPT, int ACCESS>
-__device__ __forceinline__ void load_rows(uint4 (&v)[NT][VPT], const uint16_t* const (&row)[NT], const int (&col)[VPT],
-                                          int cols, bool inner, uint32_t ends) {
+__device__ __forceinline__ void fetch_rows(uint4* mine, const uint16_t* const (&row)[NT], const int (&col)[VPT],
+                                           int cols, long long index) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) v[t][k] = make_uint4(0u, 0u, 0u, 0u);
-  if (ACCESS == kElements || (ACCESS == kShared && !inner)) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int k = 0; k < VPT; ++k)
-        if (row[t] != nullptr) v[t][k] = load_elements(row[t], col[k], cols);
-    return;
-  }
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int k = 0; k < VPT; ++k)
-      if (row[t] != nullptr && col[k] < cols) v[t][k] = *reinterpret_cast<const uint4*>(row[t] + col[k]);
-  if (ACCESS == kShared) {
+  for (int t = 0; t < NT; ++t) {
+    if (row[t] == nullptr) continue;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (((ends >> k) & 1u) == 0) continue;
-      const int n = cols - col[k];  // elements up to the row's end
-      uint32_t m[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        m[j] = n >= 2 * j + 2 ? 0xFFFFFFFFu : n == 2 * j + 1 ? 0x0000FFFFu : 0u;
-        if (k == 0) {  // only a thread's first group can begin before the row
-          const int c = col[0] + 2 * j;
-          m[j] &= c >= 0 ? 0xFFFFFFFFu : c == -1 ? 0xFFFF0000u : 0u;
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        v[t][k].x &= m[0];
-        v[t][k].y &= m[1];
-        v[t][k].z &= m[2];
-        v[t][k].w &= m[3];
+      uint4* at = mine + (t * VPT + k) * static_cast<int>(blockDim.x);
+      if (ACCESS == kElements || (ACCESS == kShared && k == 0 && col[0] < 0 && index * cols < 7)) {
+        *at = load_elements(row[t], col[k], cols);
+      } else if (ACCESS == kAligned ? col[k] < cols : col[k] + 8 <= cols) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(at)), "l"(row[t] + col[k]) : "memory");
+      } else if (ACCESS == kShared && col[k] < cols) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at)), "l"(row[t] + col[k]),
+                     "r"(2 * (cols - col[k]))
+                     : "memory");
       }
     }
   }
+  asm volatile("cp.async.commit_group;" ::: "memory");
 }
+
+// What of a thread's first group (columns c ..) lies before the row becomes zero.
+__device__ __forceinline__ void mask_start(uint4& v, int c) {
+  v.x &= c >= 0 ? 0xFFFFFFFFu : c == -1 ? 0xFFFF0000u : 0u;
+  v.y &= c >= -2 ? 0xFFFFFFFFu : c == -3 ? 0xFFFF0000u : 0u;
+  v.z &= c >= -4 ? 0xFFFFFFFFu : c == -5 ? 0xFFFF0000u : 0u;
+  v.w &= c >= -6 ? 0xFFFFFFFFu : c == -7 ? 0xFFFF0000u : 0u;
+}
+
+// Waits for the row fetched before the last one (SLOTS == 2), or for the last one.
+template <int SLOTS>
+__device__ __forceinline__ void wait_fetched() {
+  if (SLOTS == 2)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Rows in shared memory at a time: eight groups leave room for one, and with one group a CTA has one row.
+__host__ __device__ constexpr int norm_slots(int vpt) { return vpt == 2 || vpt == 4 ? 2 : 1; }
 
 // The part of a vector of eight 2-byte elements that lies in the row, in at most three naturally aligned pieces a
 // side (the vector's own place is 16-byte aligned): elements a .. b-1.
@@ -166,15 +171,6 @@ __device__ __forceinline__ void store_part(uint16_t* at, uint4 v, int a, int b) 
     return;
   }
   for (int j = a; j < b; ++j) at[j] = half(j);  // a row inside one group
-}
-
-// Bit k if group k of any lane of the warp is neither whole nor empty.
-template <int VPT>
-__device__ __forceinline__ uint32_t row_ends(const int (&col)[VPT], int cols) {
-  uint32_t ends = 0;
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) ends |= __any_sync(0xffffffffu, edge(col[k], cols)) ? 1u << k : 0u;
-  return ends;
 }
 
 template <int ACCESS>
@@ -279,12 +275,6 @@ __device__ __forceinline__ uint32_t block_max_bits(uint32_t v, uint32_t* slots, 
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// Whether the 16-byte vectors at the ends of a row lie between the first element of the first row and the last
-// element of the last one (strides are at least cols).
-__device__ __forceinline__ bool row_inner(long long row, int rows, int cols) {
-  return row * cols >= 7 && (rows - 1 - row) * cols >= 7;
-}
-
 // The columns by which a row starts past a 16-byte boundary.
 __device__ __forceinline__ int row_phase(const uint16_t* row) {
   return static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 7u);
@@ -299,9 +289,13 @@ constexpr int norm_regs(int two, int four) { return VPT == 1 ? 64 : VPT == 2 ? t
 
 template <int VPT, int FORMAT, int ACCESS>
 __global__ void __maxnreg__(norm_regs<VPT>(56, 80)) rms_norm_kernel(const NormParams p) {
+  constexpr int SLOTS = norm_slots(VPT);
+  extern __shared__ uint4 fetched[];  // [SLOTS][2][VPT][threads]
   __shared__ float slots[2][32];
   __shared__ uint32_t slots_max[2][32];
   const int warps = blockDim.x >> 5;
+  uint4* const mine = fetched + threadIdx.x;
+  const int slot_size = 2 * VPT * static_cast<int>(blockDim.x);
   pdl_launch_dependents();
   pdl_wait();
   const int phase = ACCESS == kAligned ? 0 : row_phase(p.x + blockIdx.x * p.ldx);
@@ -309,25 +303,40 @@ __global__ void __maxnreg__(norm_regs<VPT>(56, 80)) rms_norm_kernel(const NormPa
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
     col[k] = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x)) - phase;
+  auto fetch = [&](long long row, int slot) {
+    const uint16_t* const rows[2] = {p.x + row * p.ldx, p.r != nullptr ? p.r + row * p.ldr : nullptr};
+    fetch_rows<2, VPT, ACCESS>(mine + slot * slot_size, rows, col, p.cols, row);
+  };
+  // (groups past the row's end stay zero)
+  for (int i = 0; i < SLOTS * 2 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
+  fetch(blockIdx.x, 0);
   uint4 w[VPT];
   load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
-  const uint32_t ends = ACCESS == kShared ? row_ends(col, p.cols) : 0u;
+  const bool starts = threadIdx.x < 32 && phase != 0;  // the warp with the row's start
   int parity = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
-    uint4 in[2][VPT];
-    const uint16_t* const rows[2] = {p.x + row * p.ldx, p.r != nullptr ? p.r + row * p.ldr : nullptr};
-    load_rows<2, VPT, ACCESS>(in, rows, col, p.cols, row_inner(row, p.rows, p.cols), ends);
-    uint4(&s)[VPT] = in[0];
-    if (p.r != nullptr) {
+    const bool more = row + gridDim.x < p.rows;
+    if (SLOTS == 2 && more) {
+      fetch(row + gridDim.x, parity ^ 1);
+      wait_fetched<2>();
+    } else {
+      wait_fetched<1>();
+    }
+    const uint4* const in = mine + (SLOTS == 2 ? parity * slot_size : 0);
+    uint4 s[VPT];
 #pragma unroll
-      for (int k = 0; k < VPT; ++k) {
+    for (int k = 0; k < VPT; ++k) {
+      s[k] = in[k * static_cast<int>(blockDim.x)];
+      if (p.r != nullptr) {
         F8 a = unpack8(s[k]);
-        const F8 b = unpack8(in[1][k]);
+        const F8 b = unpack8(in[(VPT + k) * static_cast<int>(blockDim.x)]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a.v[j] += b.v[j];
         s[k] = pack8(a);
       }
     }
+    if (ACCESS == kShared && starts) mask_start(s[0], col[0]);
+    if (SLOTS == 1 && more) fetch(row + gridDim.x, 0);
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
@@ -403,9 +412,13 @@ __global__ void __maxnreg__(norm_regs<VPT>(56, 80)) rms_norm_kernel(const NormPa
 // ---------------------------------------------------------------- backward
 
 template <int VPT, int ACCESS>
-__global__ void __maxnreg__(norm_regs<VPT>(80, 128)) rms_norm_backward_kernel(const NormBackwardParams p) {
+__global__ void __maxnreg__(norm_regs<VPT>(64, 96)) rms_norm_backward_kernel(const NormBackwardParams p) {
+  constexpr int SLOTS = norm_slots(VPT);
+  extern __shared__ uint4 fetched[];  // [SLOTS][3][VPT][threads]
   __shared__ float slots[2][32];
   const int warps = blockDim.x >> 5;
+  uint4* const mine = fetched + threadIdx.x;
+  const int slot_size = 3 * VPT * static_cast<int>(blockDim.x);
   pdl_launch_dependents();
   pdl_wait();
   const int phase = ACCESS == kAligned ? 0 : row_phase(p.s + blockIdx.x * p.lds);
@@ -413,6 +426,14 @@ __global__ void __maxnreg__(norm_regs<VPT>(80, 128)) rms_norm_backward_kernel(co
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
     col[k] = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x)) - phase;
+  auto fetch = [&](long long row, int slot) {
+    const uint16_t* const rows[3] = {p.s + row * p.lds, p.dy + row * p.lddy,
+                                     p.ds != nullptr ? p.ds + row * p.ldds : nullptr};
+    fetch_rows<3, VPT, ACCESS>(mine + slot * slot_size, rows, col, p.cols, row);
+  };
+  // (groups past the row's end stay zero)
+  for (int i = 0; i < SLOTS * 3 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
+  fetch(blockIdx.x, 0);
   uint4 w[VPT];
   F8 dw[VPT];
 #pragma unroll
@@ -420,19 +441,27 @@ __global__ void __maxnreg__(norm_regs<VPT>(80, 128)) rms_norm_backward_kernel(co
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[k].v[j] = 0.0f;
   load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
-  const uint32_t ends = ACCESS == kShared ? row_ends(col, p.cols) : 0u;
+  const bool starts = threadIdx.x < 32 && phase != 0;  // the warp with the row's start
   int parity = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
-    uint4 in[3][VPT];
-    const uint16_t* const rows[3] = {p.s + row * p.lds, p.dy + row * p.lddy,
-                                     p.ds != nullptr ? p.ds + row * p.ldds : nullptr};
-    load_rows<3, VPT, ACCESS>(in, rows, col, p.cols, row_inner(row, p.rows, p.cols), ends);
-    const uint4(&s)[VPT] = in[0], (&dy)[VPT] = in[1], (&ds)[VPT] = in[2];
+    const bool more = row + gridDim.x < p.rows;
+    if (SLOTS == 2 && more) {
+      fetch(row + gridDim.x, parity ^ 1);
+      wait_fetched<2>();
+    } else {
+      wait_fetched<1>();
+    }
+    const uint4* const in = mine + (SLOTS == 2 ? parity * slot_size : 0);
     const float rstd = p.rstd[row];
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const F8 a = unpack8(s[k]), d = unpack8(dy[k]), g = unpack8(w[k]);
+      uint4 v[2] = {in[k * static_cast<int>(blockDim.x)], in[(VPT + k) * static_cast<int>(blockDim.x)]};
+      if (ACCESS == kShared && k == 0 && starts) {
+        mask_start(v[0], col[0]);
+        mask_start(v[1], col[0]);
+      }
+      const F8 a = unpack8(v[0]), d = unpack8(v[1]), g = unpack8(w[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float xh = a.v[j] * rstd;
@@ -443,25 +472,32 @@ __global__ void __maxnreg__(norm_regs<VPT>(80, 128)) rms_norm_backward_kernel(co
     const float c = block_sum(sum, slots[parity], warps) / static_cast<float>(p.cols);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const F8 a = unpack8(s[k]), d = unpack8(dy[k]), g = unpack8(w[k]);
+      const F8 a = unpack8(in[k * static_cast<int>(blockDim.x)]);
+      const F8 d = unpack8(in[(VPT + k) * static_cast<int>(blockDim.x)]), g = unpack8(w[k]);
       F8 o;
 #pragma unroll
       for (int j = 0; j < 8; ++j) o.v[j] = rstd * (d.v[j] * g.v[j] - a.v[j] * rstd * c);
       if (p.ds != nullptr) {
-        const F8 e = unpack8(ds[k]);
+        const F8 e = unpack8(in[(2 * VPT + k) * static_cast<int>(blockDim.x)]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) o.v[j] += e.v[j];
       }
       store8<ACCESS>(p.dx + row * p.lddx, col[k], p.cols, pack8(o));
     }
+    if (SLOTS == 1 && more) fetch(row + gridDim.x, 0);
   }
-  if (p.partial != nullptr) {
+  if (p.partial != nullptr) {  // through shared memory, so that a warp writes 32 columns side by side
+    float* const sums = reinterpret_cast<float*>(fetched);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      float4* at = reinterpret_cast<float4*>(sums + col[k] + phase);
+      at[0] = make_float4(dw[k].v[0], dw[k].v[1], dw[k].v[2], dw[k].v[3]);
+      at[1] = make_float4(dw[k].v[4], dw[k].v[5], dw[k].v[6], dw[k].v[7]);
+    }
+    __syncthreads();
     float* out = p.partial + static_cast<long long>(blockIdx.x) * p.cols;
-#pragma unroll
-    for (int k = 0; k < VPT; ++k)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (col[k] + j >= 0 && col[k] + j < p.cols) out[col[k] + j] = dw[k].v[j];
+    for (int c = threadIdx.x; c < p.cols; c += blockDim.x) out[c] = sums[c + phase];
   }
 }
 
@@ -486,9 +522,9 @@ __global__ void __launch_bounds__(32 * kSumWarps)
 
 // ---------------------------------------------------------------- host side
 
-// Groups of 8 columns per thread for many rows; measured on GB300: forward 4000 x 4096 20.6 us with 4 and 21.3 with 2,
-// off the 16-byte boundary 4001 x 4099 28.4 and 26.5; backward 33.1 us with 2 and 39.4 with 4.
-constexpr int kForwardGroups = 4, kForwardGroupsOff = 2, kBackwardGroups = 2;
+// Groups of 8 columns per thread for many rows; measured on GB300: forward 4000 x 4096 17.9 us with 2 and 18.4 with 4,
+// off the 16-byte boundary 4001 x 4099 22.7 and 27.7; its gradient 29.5 and 38.9.
+constexpr int kNormGroups = 2;
 
 struct NormShape {
   int threads, vpt;
@@ -496,13 +532,11 @@ struct NormShape {
 
 // Threads and groups per thread that hold a row.
 //   Few rows (no more than SMs): one group per thread, the shortest time from load to output.
-//   Many rows: `many` groups per thread, so that an SM holds several CTAs whose reductions overlap
-//   the others' loads.
-NormShape norm_shape(int rows, int cols, int num_sms, bool aligned, int many) {
+//   Many rows: kNormGroups per thread, more where 512 threads do not hold a row.
+NormShape norm_shape(int rows, int cols, int num_sms, bool aligned) {
   const int groups = ceil_div(cols, 8) + (aligned ? 0 : 1);
   NormShape s;
-  s.vpt = rows <= num_sms ? 1 : many;
-  if (s.vpt > 1 && s.vpt < 4 && ceil_div(groups, s.vpt) > 288) s.vpt *= 2;
+  s.vpt = rows <= num_sms ? 1 : kNormGroups;
   for (;; s.vpt *= 2) {
     const int most = s.vpt == 1 ? 1024 : 512;
     s.threads = std::max(32, ceil_div(ceil_div(groups, s.vpt), 32) * 32);
@@ -510,16 +544,27 @@ NormShape norm_shape(int rows, int cols, int num_sms, bool aligned, int many) {
   }
 }
 
-// CTAs of a persistent launch: as many as fit on the SMs together, a multiple of 8, or one per row.
-int norm_grid(const void* kernel, int rows, int threads, int num_sms) {
-  return std::min(rows, std::max(8, num_sms * resident_ctas(kernel, threads, 0) / 8 * 8));
+// Bytes of a CTA's rows in shared memory, of `tensors` inputs.
+int norm_smem(const NormShape& shape, int tensors) {
+  return norm_slots(shape.vpt) * tensors * shape.vpt * shape.threads * 16;
 }
 
-int norm_launch(const void* kernel, int grid, int threads, cudaStream_t stream, void** args) {
+// CTAs of a persistent launch: as many as fit on the SMs together, a multiple of 8, or one per row; 0 on an error.
+int norm_grid(const void* kernel, int rows, int threads, int smem, int num_sms) {
+  if (smem > 46 * 1024 &&  // (a CTA has 48 KB without asking, a little of it for the reductions)
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return std::min(rows, std::max(8, num_sms * resident_ctas(kernel, threads, smem) / 8 * 8));
+}
+
+int norm_launch(const void* kernel, int grid, int threads, int smem, cudaStream_t stream, void** args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -615,13 +660,15 @@ int gemm_rms_norm(const void* X, const void* R, const void* W, void* S, void* Y,
   int device = 0, err = 0;
   const DeviceInfo* info = current_device_info(&device, &err);
   if (info == nullptr) return err;
-  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned, aligned ? kForwardGroups : kForwardGroupsOff);
+  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned);
   const void* kernel = format == GEMM_NORM_NVFP4  ? forward_kernel<GEMM_NORM_NVFP4, kAligned>(shape.vpt)
                        : format == GEMM_NORM_E4M3 ? forward_kernel<GEMM_NORM_E4M3>(shape.vpt, aligned, shared)
                                                   : forward_kernel<GEMM_NORM_BF16>(shape.vpt, aligned, shared);
   void* args[] = {&p};
-  return norm_launch(kernel, norm_grid(kernel, rows, shape.threads, info->num_sms), shape.threads,
-                     static_cast<cudaStream_t>(stream), args);
+  const int smem = norm_smem(shape, 2);
+  const int grid = norm_grid(kernel, rows, shape.threads, smem, info->num_sms);
+  if (grid == 0) return GEMM_ERR_LAUNCH;
+  return norm_launch(kernel, grid, shape.threads, smem, static_cast<cudaStream_t>(stream), args);
 }
 
 int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const float* rstd, const void* dS, void* dX,
@@ -667,11 +714,13 @@ int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const f
   const bool shared = RowPlace(dY, p.lddy, 2) == place && (dS == nullptr || RowPlace(dS, p.ldds, 2) == place) &&
                       RowPlace(dX, p.lddx, 2) == place;
   const bool aligned = shared && place.aligned() && cols % 8 == 0 && !misaligned(W, 16);
-  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned, kBackwardGroups);
+  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned);
   const void* kernel = aligned  ? backward_kernel<kAligned>(shape.vpt)
                        : shared ? backward_kernel<kShared>(shape.vpt)
                                 : backward_kernel<kElements>(shape.vpt);
-  const int grid = norm_grid(kernel, rows, shape.threads, info->num_sms);
+  const int smem = norm_smem(shape, 3);
+  const int grid = norm_grid(kernel, rows, shape.threads, smem, info->num_sms);
+  if (grid == 0) return GEMM_ERR_LAUNCH;
   void* ws = nullptr;
   if (dW != nullptr && grid > 1) {
     cudaMemPool_t pool = workspace_pool(device);
@@ -685,13 +734,13 @@ int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const f
     p.partial = dW;  // one CTA: its partial row is the sum
   }
   void* args[] = {&p};
-  int rc = norm_launch(kernel, grid, shape.threads, st, args);
+  int rc = norm_launch(kernel, grid, shape.threads, smem, st, args);
   if (ws != nullptr) {
     if (rc == GEMM_OK) {
       const float* partial = p.partial;
       int partial_rows = grid;
       void* sum_args[] = {&partial, &partial_rows, &cols, &dW};
-      rc = norm_launch(reinterpret_cast<const void*>(column_sum_kernel), ceil_div(cols, 32), 32 * kSumWarps, st,
+      rc = norm_launch(reinterpret_cast<const void*>(column_sum_kernel), ceil_div(cols, 32), 32 * kSumWarps, 0, st,
                        sum_args);
     }
     if (cudaFreeAsync(ws, st) != cudaSuccess && rc == GEMM_OK) rc = GEMM_ERR_LAUNCH;

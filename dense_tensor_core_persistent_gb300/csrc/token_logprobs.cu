@@ -917,9 +917,9 @@ int gemm_token_logprobs(const void* logits, int type, const long long* tokens, f
   p.wait_limit_ns = RunOptions().wait_limit_ns;
   if (p.status == nullptr) return GEMM_ERR_NO_DEVICE;
   // Two or three CTAs an SM, each stepping over the rows (or its part of them), and 1 to 8 CTAs a row, by the time of
-  // the launch: its rounds, each as long as a part at the CTA's share of the memory's rate (44 KB a microsecond and SM) and
-  // about 2.5 us of reductions; each thread has a vector at least. Measured on GB300: 1500 x 50001 FP32 51.1 us with
-  // two CTAs an SM and 53.9 with three, 4096 x 131072 BF16 166.8 and 159.2.
+  // the launch: its rounds, each as long as a part at the CTA's share of the memory's rate (44 KB a microsecond and
+  // SM) and about 2.5 us of reductions; each thread has a vector at least. Measured on GB300: 1500 x 50001 FP32
+  // 51.1 us with two CTAs an SM and 53.9 with three, 4096 x 131072 BF16 166.8 and 159.2.
   const double row_bytes = static_cast<double>(vocab) * (type == GEMM_LOGITS_BF16 ? 2 : 4);
   double best = 0.0;
   int ctas = 0;

@@ -460,7 +460,8 @@ typedef struct {
  *   factor, where one is wanted, goes into W and its inverse into gemm_epilogue_t.alpha.
  *   rstd: rows FP32 for the backward pass, or NULL.
  * An infinity or NaN in a row makes rstd 0 or NaN and shows in the row's outputs as the formula
- * gives it (NaN scales for E4M3 and NVFP4); other rows are not touched by it.
+ * gives it (NaN scales for E4M3 and NVFP4); other rows are not touched by it. The squares are summed in FP32, so a
+ * row whose sum of squares passes 3.4e38 counts as one with an infinity.
  * Constraints: rows, cols >= 0 (0: nothing to do); cols <= 32760; eps >= 0; pointers aligned to
  * their element; NVFP4: cols % 16 == 0, Y and scales without strides, X, R, W, S 16-byte aligned with
  * strides that are multiples of 8. Any other cols, stride or alignment is taken; rows that start
@@ -479,8 +480,9 @@ int gemm_rms_norm(const void* X, const void* R, const void* W, void* S, void* Y,
  *   dX: rows x cols BF16, the gradient of s and so of both X and R; it may be dY, dS or S itself.
  *   dW: cols FP32, or NULL (not computed). rows == 0 sets it to zero.
  * The same inputs give the same bits (dW: one partial sum a CTA, added in a fixed order).
- * Constraints as above. One kernel launch, and with dW and more than one row a second one and a
- * workspace of at most 8 * 152 * cols floats from the library's stream-ordered pool.
+ * Constraints as above. One kernel launch, and with dW and more than one row a second one and a workspace from the
+ * library's stream-ordered pool: a row of cols floats for each CTA of the first (at most the rows, and as many as
+ * the GPU's SMs hold together).
  */
 int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const float* rstd, const void* dS, void* dX,
                            float* dW, int rows, int cols, void* stream, const gemm_norm_backward_strides_t* strides);
