@@ -22,8 +22,8 @@
 // one CTA per row), so that boundary is at the same column for every row of a CTA.
 //
 // Measured on GB300 with inputs larger than L2, residual added: 4000 x 8192 43 us in BF16 (6.1 TB/s) and 38 to E4M3
-// (6.1), 4001 x 4099 22.9 us (5.7); gradient 4000 x 8192 44 us (5.9), with the weight's 48; 4001 x 4099 28.7 (4.6) and
-// 34.5. Off the boundary the rest goes to the row ends' parts and the warps that a row fills in part. With the rows
+// (6.1), 4001 x 4099 22.8 us (5.8); gradient 4000 x 8192 44 us (5.9), with the weight's 49; 4001 x 4099 27.3 (4.8) and
+// 31.0. Off the boundary the rest goes to the row ends' parts and the warps that a row fills in part. With the rows
 // loaded to registers (and as many groups a thread as were best then) the same took 43, 37, 24, 55, 66, 33 and 39 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "common.cuh"
 #include "host_common.h"
 #include "ptx.cuh"
 #include "schedule.h"
@@ -82,6 +83,15 @@ __device__ __forceinline__ F8 unpack8(uint4 p) {
 }
 __device__ __forceinline__ uint4 pack8(const F8& f) {
   return make_uint4(pack2(f.v[0], f.v[1]), pack2(f.v[2], f.v[3]), pack2(f.v[4], f.v[5]), pack2(f.v[6], f.v[7]));
+}
+
+// Eight values as four packed pairs.
+struct P8 {
+  uint64_t v[4];
+};
+__device__ __forceinline__ P8 unpack8_pairs(uint4 p) {
+  return P8{{f2_pack(bf_lo(p.x), bf_hi(p.x)), f2_pack(bf_lo(p.y), bf_hi(p.y)), f2_pack(bf_lo(p.z), bf_hi(p.z)),
+             f2_pack(bf_lo(p.w), bf_hi(p.w))}};
 }
 
 // How the rows of a call's tensors lie against the groups of 8 columns.
@@ -282,13 +292,14 @@ __device__ __forceinline__ int row_phase(const uint16_t* row) {
 
 // ---------------------------------------------------------------- forward
 
-// Registers per thread by groups per thread: 1024 threads with one group, 512 with more, and with two or
-// four as few as hold a row without spills, so that several CTAs fit on an SM.
+// Registers per thread by groups per thread: 1024 threads with one group, 512 with more, and with two or four as few as
+// hold a row without spills, so that several CTAs fit on an SM. Rows off the boundary need some more for their ends;
+// measured on GB300 at 16000 x 1023: forward 25.1 us with 64 and 26.7 with 56, gradient 36.3 with 80 and 42.8 with 64.
 template <int VPT>
 constexpr int norm_regs(int two, int four) { return VPT == 1 ? 64 : VPT == 2 ? two : VPT == 4 ? four : 128; }
 
 template <int VPT, int FORMAT, int ACCESS>
-__global__ void __maxnreg__(norm_regs<VPT>(56, 80)) rms_norm_kernel(const NormParams p) {
+__global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 56 : 64, 80)) rms_norm_kernel(const NormParams p) {
   constexpr int SLOTS = norm_slots(VPT);
   extern __shared__ uint4 fetched[];  // [SLOTS][2][VPT][threads]
   __shared__ float slots[2][32];
@@ -412,7 +423,8 @@ __global__ void __maxnreg__(norm_regs<VPT>(56, 80)) rms_norm_kernel(const NormPa
 // ---------------------------------------------------------------- backward
 
 template <int VPT, int ACCESS>
-__global__ void __maxnreg__(norm_regs<VPT>(64, 96)) rms_norm_backward_kernel(const NormBackwardParams p) {
+__global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 80, 96))
+    rms_norm_backward_kernel(const NormBackwardParams p) {
   constexpr int SLOTS = norm_slots(VPT);
   extern __shared__ uint4 fetched[];  // [SLOTS][3][VPT][threads]
   __shared__ float slots[2][32];
@@ -435,16 +447,19 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 96)) rms_norm_backward_kernel(con
   for (int i = 0; i < SLOTS * 3 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
   fetch(blockIdx.x, 0);
   uint4 w[VPT];
-  F8 dw[VPT];
+  P8 dw[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[k].v[j] = 0.0f;
+    for (int j = 0; j < 4; ++j) dw[k].v[j] = 0;
   load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
   const bool starts = threadIdx.x < 32 && phase != 0;  // the warp with the row's start
+  const float mean = 1.0f / static_cast<float>(p.cols);
+  float rstd = p.rstd[blockIdx.x], rstd_next = 0.0f;
   int parity = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
     const bool more = row + gridDim.x < p.rows;
+    if (more) rstd_next = p.rstd[row + gridDim.x];
     if (SLOTS == 2 && more) {
       fetch(row + gridDim.x, parity ^ 1);
       wait_fetched<2>();
@@ -452,8 +467,9 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 96)) rms_norm_backward_kernel(con
       wait_fetched<1>();
     }
     const uint4* const in = mine + (SLOTS == 2 ? parity * slot_size : 0);
-    const float rstd = p.rstd[row];
-    float sum = 0.0f;
+    const uint64_t r2 = f2_pack(rstd, rstd);
+    uint64_t sum2 = 0;
+    float lo, hi;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       uint4 v[2] = {in[k * static_cast<int>(blockDim.x)], in[(VPT + k) * static_cast<int>(blockDim.x)]};
@@ -461,15 +477,16 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 96)) rms_norm_backward_kernel(con
         mask_start(v[0], col[0]);
         mask_start(v[1], col[0]);
       }
-      const F8 a = unpack8(v[0]), d = unpack8(v[1]), g = unpack8(w[k]);
+      const P8 a = unpack8_pairs(v[0]), d = unpack8_pairs(v[1]), g = unpack8_pairs(w[k]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float xh = a.v[j] * rstd;
-        dw[k].v[j] = fmaf(d.v[j], xh, dw[k].v[j]);
-        sum = fmaf(d.v[j] * g.v[j], xh, sum);
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t xh = f2_mul(a.v[j], r2);
+        dw[k].v[j] = f2_fma(d.v[j], xh, dw[k].v[j]);
+        sum2 = f2_fma(f2_mul(d.v[j], g.v[j]), xh, sum2);
       }
     }
-    const float c = block_sum(sum, slots[parity], warps) / static_cast<float>(p.cols);
+    f2_unpack(sum2, lo, hi);
+    const float c = block_sum(lo + hi, slots[parity], warps) * mean;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const F8 a = unpack8(in[k * static_cast<int>(blockDim.x)]);
@@ -485,15 +502,16 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 96)) rms_norm_backward_kernel(con
       store8<ACCESS>(p.dx + row * p.lddx, col[k], p.cols, pack8(o));
     }
     if (SLOTS == 1 && more) fetch(row + gridDim.x, 0);
+    rstd = rstd_next;
   }
   if (p.partial != nullptr) {  // through shared memory, so that a warp writes 32 columns side by side
     float* const sums = reinterpret_cast<float*>(fetched);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      float4* at = reinterpret_cast<float4*>(sums + col[k] + phase);
-      at[0] = make_float4(dw[k].v[0], dw[k].v[1], dw[k].v[2], dw[k].v[3]);
-      at[1] = make_float4(dw[k].v[4], dw[k].v[5], dw[k].v[6], dw[k].v[7]);
+      ulonglong2* at = reinterpret_cast<ulonglong2*>(sums + col[k] + phase);
+      at[0] = make_ulonglong2(dw[k].v[0], dw[k].v[1]);
+      at[1] = make_ulonglong2(dw[k].v[2], dw[k].v[3]);
     }
     __syncthreads();
     float* out = p.partial + static_cast<long long>(blockIdx.x) * p.cols;
