@@ -25,6 +25,8 @@
 // one TMEM lane quadrant each; stores go through swizzled staging tiles and TMA.
 //
 // Bound by the tensor cores; up to kGluRows rows, where the bytes of Wg and Wu are the bound, glu_rows.cu computes H^T.
+// Measured on GB300 with this tile: 4000 x 14336 x 4096 553 us (535 on the 512 x 256 one), 128 x 28672 x 8192 in E4M3
+// 85 (82 as H^T); the gradient's first step, which only moves bytes, 120 us at 4096 x 14336 (6.8 TB/s).
 //
 // For the gradient g and u are kept in FP32 (8 bytes per element and a tenth of the block's time at
 // most): kept in BF16 they would add a rounding to dg and du next to the one their MMA operand needs.
