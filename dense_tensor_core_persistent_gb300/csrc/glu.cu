@@ -21,8 +21,8 @@
 // A last wave of tiles at most half full runs as halves of its tiles (N = 128 MMAs).
 // BF16 products with enough tiles run on a 512 x 256 pair tile instead (glu_wide.cu; glu_wide_rule).
 // A stage holds 128 (BF16) or 256 (E4M3) of the summed dimension, 8 MMAs per barrier wait, 3 stages.
-// Warp roles: 0 loads A, 2 loads B, 1 allocates TMEM and issues the MMAs (leader CTA), 4..7 epilogue,
-// one TMEM lane quadrant each; stores go through swizzled staging tiles and TMA.
+// Warp roles: 0 loads A, 2 loads B, 1 allocates TMEM and issues the MMAs (leader CTA), 4..11 epilogue, two to each
+// TMEM lane quadrant with half of the columns each; stores go through swizzled staging tiles and TMA.
 //
 // Bound by the tensor cores; up to kGluRows rows, where the bytes of Wg and Wu are the bound, glu_rows.cu computes H^T.
 // Measured on GB300 with this tile: 4000 x 14336 x 4096 553 us (535 on the 512 x 256 one), 128 x 28672 x 8192 in E4M3
@@ -55,13 +55,12 @@ struct GluLayout {
   static constexpr int OPERAND_BYTES = ATOMS * ATOM_BYTES;
   static constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
   static constexpr int ACC_COLS = 256, TMEM_COLS = 512;
-  static constexpr int WARP_A = 0, WARP_MMA = 1, WARP_B = 2, EPI_WARP0 = 4, EPI_WARPS = 4;
+  static constexpr int WARP_A = 0, WARP_MMA = 1, WARP_B = 2, EPI_WARP0 = 4, EPI_WARPS = 8;
   static constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-  static constexpr int EPI_BUFS = 2, EPI_BUF_BYTES = 32 * 128;  // 32 rows of 128 bytes
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = STAGES * OPERAND_BYTES;
   static constexpr int OFF_EPI = OFF_B + STAGES * OPERAND_BYTES;
-  static constexpr int OFF_BAR = OFF_EPI + EPI_WARPS * EPI_BUFS * EPI_BUF_BYTES;
+  static constexpr int OFF_BAR = OFF_EPI + EPI_WARPS * kGluStagingBytes;
   // full[S], empty[S], tmem_full[2], tmem_empty[2], drain
   static constexpr int NUM_BARS = 2 * STAGES + 5;
   static constexpr int OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
@@ -244,56 +243,7 @@ __device__ __forceinline__ void glu_mma(const GluParams& p, uint32_t base, uint3
   }
 }
 
-// ---------------------------------------------------------------- epilogue (warps 4..7)
-
-// The warp's two staging buffers in turn; each is free once the store before last has read it.
-struct GluStaging {
-  uint32_t base, next;
-  __device__ __forceinline__ uint32_t take(uint32_t lane) {
-    const uint32_t buf = base + next * GluLayout::EPI_BUF_BYTES;
-    next ^= 1u;
-    if (lane == 0) bulk_wait_group_read<1>();
-    __syncwarp();
-    return buf;
-  }
-  __device__ __forceinline__ void store(uint32_t lane, const CUtensorMap* map, uint32_t buf, int col, int row,
-                                        bool streaming) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      if (streaming) tma_store_2d_streaming(map, buf, col, row);
-      else tma_store_2d(map, buf, col, row);
-      bulk_commit_group();
-    }
-  }
-};
-
-// 32 columns of this lane's row as BF16 (64-byte rows, 64-byte swizzle).
-__device__ __forceinline__ void glu_store_bf16(GluStaging& st, uint32_t lane, const CUtensorMap* map,
-                                               const float (&v)[32], int col, int row) {
-  const uint32_t buf = st.take(lane);
-  const uint32_t addr = buf + lane * 64u, sw = (lane >> 1) & 3u;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t w[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      w[t] = pack_bf16x2_rn(__float_as_uint(v[8 * j + 2 * t]), __float_as_uint(v[8 * j + 2 * t + 1]));
-    st_shared_v4(addr + ((static_cast<uint32_t>(j) ^ sw) << 4), w[0], w[1], w[2], w[3]);
-  }
-  st.store(lane, map, buf, col, row, false);
-}
-
-// 32 columns of this lane's row as FP32 (128-byte rows, 128-byte swizzle).
-__device__ __forceinline__ void glu_store_f32(GluStaging& st, uint32_t lane, const CUtensorMap* map,
-                                              const uint32_t (&v)[32], int col, int row) {
-  const uint32_t buf = st.take(lane);
-  const uint32_t addr = buf + lane * 128u, sw = lane & 7u;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    st_shared_v4(addr + ((static_cast<uint32_t>(j) ^ sw) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-  st.store(lane, map, buf, col, row, true);
-}
+// ---------------------------------------------------------------- epilogue (warps 4..11)
 
 template <int MODE>
 __device__ __forceinline__ void glu_epilogue(const GluParams& p, const GluMaps& maps, uint32_t base, uint32_t tmem_base,
@@ -304,12 +254,14 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const GluMaps& 
   const uint32_t bar_tfull = base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 16;
   const uint32_t q = warp & 3u;  // this warp may access TMEM lanes 32q .. 32q+31
   const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
-  GluStaging st{base + L::OFF_EPI + q * L::EPI_BUFS * L::EPI_BUF_BYTES, 0u};
+  const uint32_t epi = warp - L::EPI_WARP0;
+  const int h = static_cast<int>(epi >> 2);  // its half of the columns
+  GluStaging st{base + L::OFF_EPI + epi * kGluStagingBytes, 0u, FORWARD && p.save != 0};
   GluItem item;
   for (int it = 0; glu_item(p, cluster_idx, num_clusters, it, item); ++it) {
     const int columns = item.half >= 0 ? L::BLOCK_N / 2 : L::BLOCK_N;  // of the item's accumulator
-    const int col0 = item.n_blk * (FORWARD ? L::FEATURES : L::BLOCK_N) +
-                     (item.half > 0 ? columns / (FORWARD ? 2 : 1) : 0);
+    const int width = columns / (FORWARD ? 4 : 2);  // output columns of this warp: forward 64 or 32, else 128 or 64
+    const int col0 = item.n_blk * (FORWARD ? L::FEATURES : L::BLOCK_N) + (item.half > 0 ? 2 * width : 0) + h * width;
     const uint32_t slot = static_cast<uint32_t>(it) & 1u;
     int mb = item.m_blk, rows = p.main.rows, cols = p.main.cols;
     const CUtensorMap* out = &maps.c0;
@@ -322,11 +274,11 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const GluMaps& 
     }
     const int row0 = mb * L::TILE_M + static_cast<int>(rank) * L::CTA_M + static_cast<int>(q) * 32;
     // E4M3: this lane's row scale and its features' scales, while the MMAs run
-    float x_scale = 1.0f, w_scale[2][L::FEATURES / 32];
+    float x_scale = 1.0f, w_scale[2][L::FEATURES / 64];
     if constexpr (MODE == kGluForwardE4m3) {
       if (row0 + static_cast<int>(lane) < rows) x_scale = p.x_scale[row0 + lane];
 #pragma unroll
-      for (int c = 0; c < L::FEATURES / 32; ++c) {
+      for (int c = 0; c < L::FEATURES / 64; ++c) {
         const int f = col0 + c * 32 + static_cast<int>(lane);
         w_scale[0][c] = f < cols ? p.g_scale[f] : 0.0f;
         w_scale[1][c] = f < cols ? p.u_scale[f] : 0.0f;
@@ -336,14 +288,14 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const GluMaps& 
                          status_code(kRoleEpilogue, slot)))
       break;
     tc_fence_after_sync();
-    const uint32_t taddr = tmem_base + ((q * 32u) << 16) + slot * L::ACC_COLS;
+    const uint32_t taddr = tmem_base + ((q * 32u) << 16) + slot * L::ACC_COLS + static_cast<uint32_t>(h * width);
     if (row0 < rows) {
       if constexpr (FORWARD) {
         const float xs = x_scale;
-#pragma unroll MODE == kGluForwardE4m3 ? 4 : 1
-        for (int c = 0; c < L::FEATURES; c += 32) {
+#pragma unroll MODE == kGluForwardE4m3 ? 2 : 1
+        for (int c = 0; c < L::FEATURES / 2; c += 32) {
           const int col = col0 + c;
-          if (c >= columns / 2 || col >= cols) break;
+          if (c >= width || col >= cols) break;
           float gs = 0.0f, us = 0.0f;  // E4M3: the scales of feature col + lane
           if constexpr (MODE == kGluForwardE4m3) {
             gs = w_scale[0][c / 32];
@@ -353,7 +305,10 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const GluMaps& 
           tmem_ld_32x32b_x32(taddr + c, g);
           tmem_ld_32x32b_x32(taddr + columns / 2 + c, u);
           tmem_ld_wait();
-          float h[32];
+          if (p.save) {
+            glu_store(st, lane, &maps.c1, g, col, row0, true);
+            glu_store(st, lane, &maps.c2, u, col, row0, true);
+          }
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             float gv = __uint_as_float(g[j]), uv = __uint_as_float(u[j]);
@@ -361,26 +316,19 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const GluMaps& 
               gv *= xs * __shfl_sync(0xffffffffu, gs, j);
               uv *= xs * __shfl_sync(0xffffffffu, us, j);
             }
-            h[j] = glu_act(gv, p.act) * uv;
+            g[j] = __float_as_uint(glu_act(gv, p.act) * uv);
           }
-          glu_store_bf16(st, lane, out, h, col, row0);
-          if (p.save) {
-            glu_store_f32(st, lane, &maps.c1, g, col, row0);
-            glu_store_f32(st, lane, &maps.c2, u, col, row0);
-          }
+          glu_store(st, lane, out, g, col, row0, false);
         }
       } else {
 #pragma unroll 1
-        for (int c = 0; c < columns; c += 32) {
+        for (int c = 0; c < width; c += 32) {
           const int col = col0 + c;
           if (col >= cols) break;
           uint32_t v[32];
           tmem_ld_32x32b_x32(taddr + c, v);
           tmem_ld_wait();
-          float f[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-          glu_store_bf16(st, lane, out, f, col, row0);
+          glu_store(st, lane, out, v, col, row0, false);
         }
       }
     }

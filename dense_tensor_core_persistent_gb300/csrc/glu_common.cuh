@@ -87,6 +87,55 @@ __device__ __forceinline__ void tma_store_2d_streaming(const CUtensorMap* m, uin
       : "memory");
 }
 
+// An epilogue warp's staging bytes: two BF16 tiles of 32 x 32 in turn, or (`whole`) one tile, FP32 or BF16, at a time.
+constexpr int kGluStagingBytes = 32 * 128;
+struct GluStaging {
+  uint32_t base, next;
+  bool whole;
+  __device__ __forceinline__ uint32_t take(uint32_t lane) {
+    uint32_t buf = base;
+    if (whole) {
+      if (lane == 0) bulk_wait_group_read<0>();
+    } else {
+      buf += next * (kGluStagingBytes / 2);
+      next ^= 1u;
+      if (lane == 0) bulk_wait_group_read<1>();
+    }
+    __syncwarp();
+    return buf;
+  }
+  __device__ __forceinline__ void store(uint32_t lane, const CUtensorMap* map, uint32_t buf, int col, int row,
+                                        bool streaming) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (streaming) tma_store_2d_streaming(map, buf, col, row);
+      else tma_store_2d(map, buf, col, row);
+      bulk_commit_group();
+    }
+  }
+};
+
+// 32 columns of this lane's row as BF16 (64-byte rows, 64-byte swizzle) or FP32 (128-byte rows, 128-byte swizzle).
+__device__ __forceinline__ void glu_store(GluStaging& st, uint32_t lane, const CUtensorMap* map, const uint32_t (&v)[32],
+                                          int col, int row, bool f32) {
+  const uint32_t buf = st.take(lane);
+  if (f32) {
+    const uint32_t addr = buf + lane * 128u, sw = lane & 7u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      st_shared_v4(addr + ((static_cast<uint32_t>(j) ^ sw) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  } else {
+    const uint32_t addr = buf + lane * 64u, sw = (lane >> 1) & 3u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      st_shared_v4(addr + ((static_cast<uint32_t>(j) ^ sw) << 4), pack_bf16x2_rn(v[8 * j], v[8 * j + 1]),
+                   pack_bf16x2_rn(v[8 * j + 2], v[8 * j + 3]), pack_bf16x2_rn(v[8 * j + 4], v[8 * j + 5]),
+                   pack_bf16x2_rn(v[8 * j + 6], v[8 * j + 7]));
+  }
+  st.store(lane, map, buf, col, row, f32);
+}
+
 // The 512 x 256 pair tile (glu_wide.cu): p's products are planned for it, `clusters` pairs take them.
 int glu_wide_max_clusters(int device);
 int glu_wide_launch(const GluMaps& m, const GluParams& p, bool backward, int clusters, cudaStream_t stream);

@@ -37,7 +37,7 @@ struct GluWideLayout {
   static constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
   // registers per thread after setmaxnreg (the launch gives 65536 / 384 -> 168)
   static constexpr int REGS_LAUNCH = 168, REGS_LOW = 56, REGS_EPI = 216;
-  static constexpr int EPI_BYTES = 32 * 128;          // per warp: one FP32 tile of 32 x 32 or two BF16 ones
+  static constexpr int EPI_BYTES = kGluStagingBytes;
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_EPI = OFF_B + STAGES * B_BYTES;
@@ -204,54 +204,6 @@ __device__ __forceinline__ void glu_wide_mma(const GluParams& p, uint32_t base, 
 
 // ---------------------------------------------------------------- epilogue (warps 4..11)
 
-// The warp's staging bytes: two BF16 tiles in turn, or (`whole`) one tile at a time.
-struct GluWideStaging {
-  uint32_t base, next;
-  bool whole;
-  __device__ __forceinline__ uint32_t take(uint32_t lane) {
-    uint32_t buf = base;
-    if (whole) {
-      if (lane == 0) bulk_wait_group_read<0>();
-    } else {
-      buf += next * (GluWideLayout::EPI_BYTES / 2);
-      next ^= 1u;
-      if (lane == 0) bulk_wait_group_read<1>();
-    }
-    __syncwarp();
-    return buf;
-  }
-  __device__ __forceinline__ void store(uint32_t lane, const CUtensorMap* map, uint32_t buf, int col, int row,
-                                        bool streaming) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      if (streaming) tma_store_2d_streaming(map, buf, col, row);
-      else tma_store_2d(map, buf, col, row);
-      bulk_commit_group();
-    }
-  }
-};
-
-// 32 columns of this lane's row as BF16 (64-byte rows, 64-byte swizzle) or FP32 (128-byte rows, 128-byte swizzle).
-__device__ __forceinline__ void glu_wide_store(GluWideStaging& st, uint32_t lane, const CUtensorMap* map,
-                                               const uint32_t (&v)[32], int col, int row, bool f32) {
-  const uint32_t buf = st.take(lane);
-  if (f32) {
-    const uint32_t addr = buf + lane * 128u, sw = lane & 7u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      st_shared_v4(addr + ((static_cast<uint32_t>(j) ^ sw) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-  } else {
-    const uint32_t addr = buf + lane * 64u, sw = (lane >> 1) & 3u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      st_shared_v4(addr + ((static_cast<uint32_t>(j) ^ sw) << 4), pack_bf16x2_rn(v[8 * j], v[8 * j + 1]),
-                   pack_bf16x2_rn(v[8 * j + 2], v[8 * j + 3]), pack_bf16x2_rn(v[8 * j + 4], v[8 * j + 5]),
-                   pack_bf16x2_rn(v[8 * j + 6], v[8 * j + 7]));
-  }
-  st.store(lane, map, buf, col, row, f32);
-}
-
 template <bool BACKWARD>
 __device__ __forceinline__ void glu_wide_epilogue(const GluParams& p, const GluMaps& maps, uint32_t base,
                                                   uint32_t tmem_base, uint32_t warp, uint32_t lane, uint32_t rank,
@@ -262,7 +214,7 @@ __device__ __forceinline__ void glu_wide_epilogue(const GluParams& p, const GluM
   const uint32_t epi = warp - L::EPI_WARP0;
   const int h = static_cast<int>(epi >> 2);  // its half of a wave's columns
   const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
-  GluWideStaging st{base + L::OFF_EPI + epi * L::EPI_BYTES, 0u, !BACKWARD && p.save != 0};
+  GluStaging st{base + L::OFF_EPI + epi * L::EPI_BYTES, 0u, !BACKWARD && p.save != 0};
   bool ok = true;
   GluItem item;
   for (int it = 0; ok && glu_item(p, cluster_idx, num_clusters, it, item); ++it) {
@@ -311,21 +263,21 @@ __device__ __forceinline__ void glu_wide_epilogue(const GluParams& p, const GluM
       if constexpr (BACKWARD) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (c * 32 < width && col0 + c * 32 < cols) glu_wide_store(st, lane, out, v[c], col0 + c * 32, row0, false);
+          if (c * 32 < width && col0 + c * 32 < cols) glu_store(st, lane, out, v[c], col0 + c * 32, row0, false);
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int col = col0 + c * 32;
           if (c * 32 < width && col < cols) {
             if (p.save) {
-              glu_wide_store(st, lane, &maps.c1, v[2 * c], col, row0, true);
-              glu_wide_store(st, lane, &maps.c2, v[2 * c + 1], col, row0, true);
+              glu_store(st, lane, &maps.c1, v[2 * c], col, row0, true);
+              glu_store(st, lane, &maps.c2, v[2 * c + 1], col, row0, true);
             }
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               v[2 * c][j] = __float_as_uint(glu_act(__uint_as_float(v[2 * c][j]), p.act) *
                                             __uint_as_float(v[2 * c + 1][j]));
-            glu_wide_store(st, lane, out, v[2 * c], col, row0, false);
+            glu_store(st, lane, out, v[2 * c], col, row0, false);
           }
         }
       }
