@@ -10,6 +10,9 @@
 // One persistent CTA per SM steps over tiles of 64 features; a last wave at most half full runs as halves of its
 // tiles (32 features; the other accumulator lanes hold what the stage held before and are not read). Warp roles: 0
 // loads W, 2 loads X, 1 allocates TMEM and issues the MMAs, 4..7 epilogue. Two accumulators in TMEM.
+// Where all tiles fit at once with 2, 4 or 8 CTAs each, the CTAs of a cluster share a tile's depth: one CTA alone draws
+// no more than some 50 GB/s. Each leaves its partial sums in its shared memory, and the CTAs take the rows of X in turn
+// and add the cluster's sums in a fixed order.
 // Measured on GB300 at 28672 x 8192 (N x K): 1 row 140 us in BF16 (6.7 TB/s of weights) and 72 in E4M3 (6.5), 64 rows
 // 140 and 74 us, 128 rows 154 and 82.
 // The box of X is as high as its rows need: zero rows that TMA fills in cost time too (17 rows in a box of 64 took
@@ -18,7 +21,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
+#include <mutex>
 
 #include "common.cuh"
 #include "glu_act.cuh"
@@ -27,9 +30,12 @@
 namespace dtcp {
 namespace {
 
+constexpr int kRowsMaxSplits = 8;
+
 struct GluRowsParams {
   GluRowsOperands x;  // operands and sizes
   int k_iters, num_tiles, split_tiles, num_items;
+  int splits;  // CTAs of a cluster that share a tile's depth; with more than one a cluster has one tile, and no halves
   int n;  // the MMA's N: the rows of X, rounded up to a multiple of 16
   unsigned* status;
   unsigned long long wait_limit_ns;
@@ -71,6 +77,22 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
 // The epilogue's four warps meet (barrier 1).
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
+__device__ __forceinline__ void store_h(const GluRowsOperands& x, int row, int f, float g, float u) {
+  const float h = glu_act(g, x.act) * u;
+  x.h[row * x.ldh + f] = static_cast<uint16_t>(pack_bf16x2_rn(__float_as_uint(h), 0u) & 0xFFFFu);
+  if (x.preact != nullptr) {
+    float* pre = x.preact + static_cast<long long>(row) * 2 * x.features + f;
+    pre[0] = g;
+    pre[x.features] = u;
+  }
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
 template <bool E4M3, int X_ROWS>
 __global__ void __launch_bounds__(GluRowsLayout<X_ROWS>::NUM_THREADS, 1)
     glu_rows_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_u,
@@ -111,16 +133,20 @@ __global__ void __launch_bounds__(GluRowsLayout<X_ROWS>::NUM_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   pdl_launch_dependents();
   pdl_wait();
+  const int splits = p.splits, rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = static_cast<int>(blockIdx.x) / splits, step = static_cast<int>(gridDim.x) / splits;  // items
+  const int k0 = rank * p.k_iters / splits, k1 = (rank + 1) * p.k_iters / splits;
+  float* const partial = reinterpret_cast<float*>(smem + L::OFF_W);  // [rows of X][128]: over the stages, once they are done
 
   if ((warp == L::WARP_W || warp == L::WARP_X) && lane == 0) {
     // ------------------------------------------------------------ producers
     uint32_t stage = 0, phase = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < p.num_items && ok; i += gridDim.x) {
+    for (int i = first; i < p.num_items && ok; i += step) {
       const WorkItem w = work_item(i, p.num_tiles, p.split_tiles);
       const int f0 = w.tile * L::FEATURES + (w.half > 0 ? L::FEATURES / 2 : 0);
       const int boxes = w.half >= 0 ? 1 : 2;  // of 32 features
-      for (int k = 0; k < p.k_iters; ++k) {
+      for (int k = k0; k < k1; ++k) {
         if (!wait_phase_inline(bar_empty + 8 * stage, phase ^ 1u, wctx, status_code(kRoleProducer, stage))) {
           ok = false;
           break;
@@ -157,7 +183,7 @@ __global__ void __launch_bounds__(GluRowsLayout<X_ROWS>::NUM_THREADS, 1)
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     int it = 0;
-    for (int i = blockIdx.x; i < p.num_items && ok; i += gridDim.x, ++it) {
+    for (int i = first; i < p.num_items && ok; i += step, ++it) {
       const uint32_t slot = static_cast<uint32_t>(it) & 1u;
       if (!wait_phase_inline(bar_tempty + 8 * slot, ((static_cast<uint32_t>(it) >> 1) & 1u) ^ 1u, wctx,
                              status_code(kRoleMma, 0x100 + slot))) {
@@ -165,7 +191,7 @@ __global__ void __launch_bounds__(GluRowsLayout<X_ROWS>::NUM_THREADS, 1)
         break;
       }
       const uint32_t d = tmem_base + slot * X_ROWS;
-      for (int k = 0; k < p.k_iters; ++k) {
+      for (int k = k0; k < k1; ++k) {
         if (!wait_phase_inline(bar_full + 8 * stage, phase, wctx, status_code(kRoleMma, stage))) {
           ok = false;
           break;
@@ -178,8 +204,8 @@ __global__ void __launch_bounds__(GluRowsLayout<X_ROWS>::NUM_THREADS, 1)
           const uint32_t in_atom = static_cast<uint32_t>(kk % 4) * 32u, atom = static_cast<uint32_t>(kk / 4);
           const uint64_t ad = umma_desc_advance(a, atom * L::W_ATOM_BYTES + in_atom);
           const uint64_t bd = umma_desc_advance(b, atom * L::X_ATOM_BYTES + in_atom);
-          if constexpr (E4M3) mma_e4m3(d, ad, bd, idesc, (k | kk) != 0 ? 1u : 0u);
-          else mma_f16<1>(d, ad, bd, idesc, (k | kk) != 0 ? 1u : 0u);
+          if constexpr (E4M3) mma_e4m3(d, ad, bd, idesc, k != k0 || kk != 0 ? 1u : 0u);
+          else mma_f16<1>(d, ad, bd, idesc, k != k0 || kk != 0 ? 1u : 0u);
         };
         if (steps == L::KSTEPS) {
 #pragma unroll
@@ -208,7 +234,7 @@ __global__ void __launch_bounds__(GluRowsLayout<X_ROWS>::NUM_THREADS, 1)
     float* tile = reinterpret_cast<float*>(smem + L::OFF_U) + (q & 1u) * 32u + lane;
     bool ok = true;
     int it = 0;
-    for (int i = blockIdx.x; i < p.num_items; i += gridDim.x, ++it) {
+    for (int i = first; i < p.num_items; i += step, ++it) {
       const WorkItem w = work_item(i, p.num_tiles, p.split_tiles);
       const int f = w.tile * L::FEATURES + (w.half > 0 ? L::FEATURES / 2 : 0) + static_cast<int>((q & 1u) * 32u + lane);
       const bool live = f < p.x.features && (w.half < 0 || (q & 1u) == 0);
@@ -225,6 +251,17 @@ __global__ void __launch_bounds__(GluRowsLayout<X_ROWS>::NUM_THREADS, 1)
       // Of each 32 rows of X the lower lanes' warps finish the first 16 and the upper ones' the others: a warp keeps
       // its own half of those values and leaves the other half where the other warp of its features finds it.
       const uint32_t taddr = tmem_base + ((q * 32u) << 16) + slot * X_ROWS;
+      if (splits > 1) {  // every MMA of the cluster's one tile in this CTA is done
+#pragma unroll 1
+        for (int c = 0; 32 * c < p.x.rows; ++c) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(taddr + 32 * c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) partial[(32 * c + j) * 128 + q * 32u + lane] = __uint_as_float(v[j]);
+        }
+        break;
+      }
       float own[X_ROWS / 32][16], xs[X_ROWS / 32];
 #pragma unroll
       for (int c = 0; c < X_ROWS / 32; ++c) {
@@ -256,15 +293,7 @@ __global__ void __launch_bounds__(GluRowsLayout<X_ROWS>::NUM_THREADS, 1)
             g *= x_scale * g_scale;
             u *= x_scale * u_scale;
           }
-          const float h = glu_act(g, p.x.act) * u;
-          if (live && ok && row < p.x.rows) {
-            p.x.h[row * p.x.ldh + f] = static_cast<uint16_t>(pack_bf16x2_rn(__float_as_uint(h), 0u) & 0xFFFFu);
-            if (p.x.preact != nullptr) {
-              float* pre = p.x.preact + static_cast<long long>(row) * 2 * p.x.features + f;
-              pre[0] = g;
-              pre[p.x.features] = u;
-            }
-          }
+          if (live && ok && row < p.x.rows) store_h(p.x, row, f, g, u);
         }
       }
       epilogue_sync();  // the tile has been read
@@ -272,6 +301,42 @@ __global__ void __launch_bounds__(GluRowsLayout<X_ROWS>::NUM_THREADS, 1)
   }
   __syncwarp();
   tc_fence_before_sync();
+  if (splits > 1) {
+    // The CTAs take the rows of X in turn and add the cluster's partial sums in the order of the depth.
+    cluster_sync_all();
+    const int f = first * L::FEATURES + static_cast<int>(threadIdx.x % L::FEATURES);
+    constexpr int AT_ONCE = L::NUM_THREADS / L::FEATURES;
+    if (f < p.x.features && *abort_flag == 0u) {
+      const float g_scale = E4M3 ? p.x.g_scale[f] : 1.0f, u_scale = E4M3 ? p.x.u_scale[f] : 1.0f;
+      for (int row = rank + splits * static_cast<int>(threadIdx.x / L::FEATURES); row < p.x.rows;
+           row += splits * AT_ONCE) {
+        const uint32_t at = smem_u32(partial) + (row * 128u + threadIdx.x % L::FEATURES) * 4u;
+        float part[2][kRowsMaxSplits];  // asked for together
+#pragma unroll
+        for (int s = 0; s < kRowsMaxSplits; ++s) {
+          part[0][s] = part[1][s] = 0.0f;
+          if (s < splits) {
+            const uint32_t from = mapa_shared(at, s);
+            part[0][s] = ld_cluster_f32(from);
+            part[1][s] = ld_cluster_f32(from + 4u * L::FEATURES);
+          }
+        }
+        float g = part[0][0], u = part[1][0];
+#pragma unroll
+        for (int s = 1; s < kRowsMaxSplits; ++s) {
+          g += part[0][s];
+          u += part[1][s];
+        }
+        if (E4M3) {
+          const float x_scale = p.x.x_scale[row];
+          g *= x_scale * g_scale;
+          u *= x_scale * u_scale;
+        }
+        store_h(p.x, row, f, g, u);
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its sums
+  }
   __syncthreads();
   if (warp == L::WARP_MMA) {
     tc_fence_after_sync();
@@ -280,6 +345,50 @@ __global__ void __launch_bounds__(GluRowsLayout<X_ROWS>::NUM_THREADS, 1)
 }
 
 // ---------------------------------------------------------------- host side
+
+void rows_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int grid, int threads, int smem, int splits,
+                 cudaStream_t stream) {
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = splits > 1 ? 2 : 1;
+}
+
+// Prepares a kernel on a device; clusters[s]: how many clusters of 2 << s CTAs the device holds at once.
+template <bool E4M3, int X_ROWS>
+bool prepare_rows(int device, int (&clusters)[3]) {
+  using L = GluRowsLayout<X_ROWS>;
+  static std::mutex mu;
+  static int cache[64][4] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  int(&c)[4] = cache[device & 63];
+  if (c[3] == 0) {
+    const auto kernel = glu_rows_kernel<E4M3, X_ROWS>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_BYTES) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    for (int s = 0; s < 3; ++s) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[2];
+      rows_config(cfg, attr, 16, L::NUM_THREADS, L::SMEM_BYTES, 2 << s, nullptr);
+      if (cudaOccupancyMaxActiveClusters(&c[s], kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        c[s] = 0;
+      }
+    }
+    c[3] = 1;
+  }
+  for (int s = 0; s < 3; ++s) clusters[s] = c[s];
+  return true;
+}
 
 template <bool E4M3, int X_ROWS>
 int launch_rows(const GluRowsOperands& x, int device, const DeviceInfo* info, cudaStream_t stream) {
@@ -299,35 +408,27 @@ int launch_rows(const GluRowsOperands& x, int device, const DeviceInfo* info, cu
     st = encode_tmap_2d(&rows, type, x.x, x.depth, x.rows, uint64_t(x.ldx) * SIZE, ATOM_K, p.n,
                         CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != GEMM_OK) return st;
-  const auto kernel = glu_rows_kernel<E4M3, X_ROWS>;
-  static std::atomic<unsigned long long> sized{0};  // devices whose limit of shared memory is raised
-  const unsigned long long bit = 1ull << device;
-  if ((sized.load(std::memory_order_acquire) & bit) == 0) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_BYTES) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_LAUNCH;
-    }
-    sized.fetch_or(bit, std::memory_order_release);
-  }
+  int clusters[3];
+  if (!prepare_rows<E4M3, X_ROWS>(device, clusters)) return GEMM_ERR_LAUNCH;
   p.x = x;
   p.k_iters = ceil_div(x.depth, ATOM_K * L::ATOMS);
   p.num_tiles = ceil_div(x.features, L::FEATURES);
-  p.split_tiles = tail_split_tiles(p.num_tiles, info->num_sms);
+  // As many CTAs to a tile as let every tile run at once: one CTA draws at most some 50 GB/s. Measured on GB300, 1 row
+  // x N x 8192 in BF16, without splits (but halves of tiles) and with the rule: N = 512 27.1 and 7.6 us (8 CTAs), 1792
+  // 27.1 and 12.7 (4), 4096 28.3 and 23.7 (2); N = 5120, where two CTAs no longer fit, 33.7 and 43.4 with 2.
+  p.splits = 1;
+  for (int s = 0; s < 3; ++s)
+    if (p.num_tiles <= clusters[s] && p.k_iters >= 2 << s) p.splits = 2 << s;
+  p.split_tiles = p.splits > 1 ? 0 : tail_split_tiles(p.num_tiles, info->num_sms);
   p.num_items = p.num_tiles + p.split_tiles;
   p.status = device_status_word(device);
   p.wait_limit_ns = RunOptions().wait_limit_ns;
   if (p.status == nullptr) return GEMM_ERR_NO_DEVICE;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min(p.num_items, info->num_sms)), 1, 1);
-  cfg.blockDim = dim3(L::NUM_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = L::SMEM_BYTES;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, g, u, rows, p) != cudaSuccess) {
+  cudaLaunchAttribute attr[2];
+  rows_config(cfg, attr, p.splits > 1 ? p.num_items * p.splits : std::min(p.num_items, info->num_sms), L::NUM_THREADS,
+              L::SMEM_BYTES, p.splits, stream);
+  if (cudaLaunchKernelEx(&cfg, glu_rows_kernel<E4M3, X_ROWS>, g, u, rows, p) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
   }

@@ -287,3 +287,37 @@ def test_large_tiles(M, N, K, act):
     only = g.glu_bf16_backward(dh, x, wg, wu, saved, act=act, input_grad=False)[1:]
     for a, b, r in zip(only, want[1:], root[1:]):
         assert torch.all((a.double() - b).abs() <= 2.0 ** -8 * b.abs() + 0.02 * r)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 512, 4096), (64, 64, 8192), (17, 1024, 1096), (100, 1792, 2056), (128, 4096, 520),
+                                   (2, 2304, 1288), (33, 2432, 640)])
+def test_few_rows_with_the_depth_shared(M, N, K):
+    """Weights with few features: up to 8 CTAs share a tile's depth (here also in uneven parts)."""
+    x, wg, wu, _ = problem(M, N, K, 7 * M + N + K)
+    xd, gd, ud = x.double(), wg.double(), wu.double()
+    h, saved = g.glu_bf16(x, wg, wu, save=True)
+    gate, up = check_forward(h, xd, gd, ud, "silu")
+    steps = (K / 16 + 16) * 2.0 ** -23
+    assert torch.all((saved[:, :N].double() - gate).abs() <= steps * (xd.abs() @ gd.abs().T))
+    assert torch.all((saved[:, N:].double() - up).abs() <= steps * (xd.abs() @ ud.abs().T))
+    assert torch.equal(h, g.glu_bf16(x, wg, wu))  # the same bits again
+
+    def rows(t):
+        s = t.float().abs().amax(1) / 448
+        return (t.float() / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn), s
+
+    if K % 16 == 0:
+        (xe, xs), (ge, gs), (ue, us) = rows(x), rows(wg), rows(wu)
+        h = g.glu_e4m3(xe, xs, ge, gs, ue, us)
+        check_forward(h, xe.double() * xs.double()[:, None], ge.double() * gs.double()[:, None],
+                      ue.double() * us.double()[:, None], "silu")
+
+
+def test_few_rows_with_the_depth_shared_exact():
+    """Small integers: every partial sum is exact, and so is the join."""
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x, wg, wu = (torch.randint(-2, 3, s, generator=gen, device=DEV).to(torch.bfloat16)
+                 for s in ((40, 1544), (1000, 1544), (1000, 1544)))
+    _, saved = g.glu_bf16(x, wg, wu, act="relu", save=True)
+    assert torch.equal(saved[:, :1000].double(), x.double() @ wg.double().T)
+    assert torch.equal(saved[:, 1000:].double(), x.double() @ wu.double().T)
