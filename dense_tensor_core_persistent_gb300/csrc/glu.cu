@@ -13,7 +13,8 @@
 //   dX:      A = [dg | du], B = [Wg ; Wu], the sum over both halves of the features in one accumulator.
 //   dWg/dWu: A = dg or du, B = X, summed over the rows of X.
 // One launch computes all three: the tiles of dX, which are the longest, come first, and where their last wave leaves
-// clusters free, those go ahead with as many tiles of dW as take the same time.
+// clusters free, those go ahead with as many tiles of dW as take the same time. Where dX has so few tiles that one
+// would be the whole launch, their sums are cut into slices with FP32 partial sums that a last kernel adds in order.
 // The gradient's products need operands along their other dimension (W by columns, dg and X by
 // columns). The MMA takes them as they lie in memory: TMA boxes of 64 columns x 128 rows put the
 // non-summed dimension innermost and the descriptors say so ("MN-major"), so nothing is transposed.
@@ -132,12 +133,12 @@ __device__ __forceinline__ void glu_producer(const GluParams& p, const GluMaps& 
       mn = true;
     }
     const int half_iters = !FORWARD && !item.second ? k_iters / 2 : k_iters;
-    for (int kb = 0; kb < k_iters; ++kb) {
+    for (int kb = 0; kb < item.k1 - item.k0; ++kb) {
       if (!wait_phase_inline(bar_empty + 8 * stage, phase ^ 1u, wctx, status_code(kRoleProducer, stage))) {
         ok = false;
         break;
       }
-      int k = down ? k_iters - 1 - kb : kb;
+      int k = down ? item.k1 - 1 - kb : item.k0 + kb;
       const CUtensorMap* map = m0;
       if (k >= half_iters) {
         k -= half_iters;
@@ -199,13 +200,13 @@ __device__ __forceinline__ void glu_mma(const GluParams& p, uint32_t base, uint3
       break;
     }
     const uint32_t d = tmem_base + slot * L::ACC_COLS;
-    for (int kb = 0; kb < q.k_iters; ++kb) {
+    for (int kb = 0; kb < item.k1 - item.k0; ++kb) {
       if (!wait_phase_inline(bar_full + 8 * stage, phase, wctx, status_code(kRoleMma, stage))) {
         ok = false;
         break;
       }
       tc_fence_after_sync();
-      int k = down ? q.k_iters - 1 - kb : kb;
+      int k = down ? item.k1 - 1 - kb : item.k0 + kb;
       if (k >= half_iters) k -= half_iters;
       const uint64_t a = umma_desc_advance(dw ? a_mn : a_k, stage * L::OPERAND_BYTES);
       const uint64_t b = umma_desc_advance(b0, stage * L::OPERAND_BYTES);
@@ -256,7 +257,7 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const GluMaps& 
   const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
   const uint32_t epi = warp - L::EPI_WARP0;
   const int h = static_cast<int>(epi >> 2);  // its half of the columns
-  GluStaging st{base + L::OFF_EPI + epi * kGluStagingBytes, 0u, FORWARD && p.save != 0};
+  GluStaging st{base + L::OFF_EPI + epi * kGluStagingBytes, 0u, FORWARD ? p.save != 0 : p.main.slices > 1};
   GluItem item;
   for (int it = 0; glu_item(p, cluster_idx, num_clusters, it, item); ++it) {
     const int columns = item.half >= 0 ? L::BLOCK_N / 2 : L::BLOCK_N;  // of the item's accumulator
@@ -328,7 +329,8 @@ __device__ __forceinline__ void glu_epilogue(const GluParams& p, const GluMaps& 
           uint32_t v[32];
           tmem_ld_32x32b_x32(taddr + c, v);
           tmem_ld_wait();
-          glu_store(st, lane, out, v, col, row0, false);
+          const bool partial = p.main.slices > 1 && !item.second;
+          glu_store(st, lane, out, v, col, row0 + item.slice * p.main.slice_rows, partial);
         }
       }
     }
@@ -439,6 +441,34 @@ __global__ void __launch_bounds__(256) glu_gate_grad_kernel(const uint16_t* dh, 
   }
 }
 
+// ---------------------------------------------------------------- dX from its slices
+
+// The sum of the slices' partial sums in their order, rounded once: 8 columns per thread.
+__global__ void __launch_bounds__(128) glu_join_kernel(const float* partial, int slices, long long slice_size,
+                                                       uint16_t* dx, long long lddx, int cols, long long vectors) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long v = blockIdx.x * 128LL + threadIdx.x;
+  if (v >= vectors) return;
+  const int per_row = cols / 8;
+  const long long row = v / per_row;
+  const int col = static_cast<int>(v - row * per_row) * 8;
+  const float* at = partial + row * cols + col;
+  float sum[8] = {};
+#pragma unroll 4
+  for (int s = 0; s < slices; ++s) {
+    const float4 a = *reinterpret_cast<const float4*>(at + s * slice_size);
+    const float4 b = *reinterpret_cast<const float4*>(at + s * slice_size + 4);
+    const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += f[j];
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2_rn(__float_as_uint(sum[2 * j]), __float_as_uint(sum[2 * j + 1]));
+  *reinterpret_cast<uint4*>(dx + row * lddx + col) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // ---------------------------------------------------------------- host side
 
 int glu_max_clusters(int device) {
@@ -496,7 +526,20 @@ int plan_product(GluProduct* q, int rows, int cols, int depth, int stage, int ha
   q->num_m_blocks = static_cast<int>(m);
   q->num_tiles = q->num_items = static_cast<int>(m * q->num_n_blocks);
   q->split_tiles = 0;
+  q->slices = 1;
   return GEMM_OK;
+}
+
+// Parts of dX's summed dimension, where its few tiles would be the launch's longest path: the stages of a tile against
+// the stages of all tiles of both products spread over the pairs (with two more for a short tile of dW's end). A part
+// has 6 stages at least, the parts run at once, and what is saved has to pay for the partial sums and the kernel that
+// adds them, some 4 us (8 stages). Measured on GB300, whole gradient: 512 x 4096 x 1024 44.2 us in one part and 24.3 in
+// four, 300 x 1368 x 520 22.3 and 17.3 in three; 10 x 2072 x 5576, which stays whole, 30.2 and 33.0 in three.
+int glu_slices(const GluProduct& dx, const GluProduct& dw, int wave) {
+  const long long work = 1LL * dx.num_tiles * dx.k_iters + 1LL * dw.num_tiles * (dw.k_iters + 2);
+  const int share = std::max<int>(6, static_cast<int>(std::min<long long>(work / wave, 0x7FFFFFFF)));
+  const int slices = std::min({8, dx.k_iters / share, wave / dx.num_tiles});
+  return slices > 1 && dx.k_iters - dx.k_iters / slices >= 12 ? slices : 1;
 }
 
 // The order of a product's tiles on `clusters` pairs, for operands of `bytes` per element.
@@ -519,15 +562,15 @@ int glu_launch(const GluMaps& m, GluParams& p, bool wide, double bytes, int devi
   if (wave <= 0) return GEMM_ERR_LAUNCH;
   GluProduct &a = p.main, &b = p.second;
   p.ahead = 0;
-  if (b.num_tiles == 0) {
+  if (b.num_tiles == 0 && a.slices == 1) {
     a.split_tiles = tail_split_tiles(a.num_tiles, wave);
     a.num_items = a.num_tiles + a.split_tiles;
-  } else {
+  } else if (b.num_tiles > 0) {
     // clusters that a last partial wave of the first product leaves free go ahead with tiles of the second
-    const int clusters = std::min(a.num_tiles + b.num_tiles, wave);
-    const int in_last = a.num_tiles % clusters, idle = in_last > 0 ? clusters - in_last : 0;
+    const int clusters = std::min(a.num_items + b.num_tiles, wave);
+    const int in_last = a.num_items % clusters, idle = in_last > 0 ? clusters - in_last : 0;
     if (idle > 0)
-      p.ahead = std::min((a.k_iters + b.k_iters / 2) / b.k_iters, ceil_div(b.num_tiles, idle));
+      p.ahead = std::min((a.k_iters / a.slices + b.k_iters / 2) / b.k_iters, ceil_div(b.num_tiles, idle));
     const int rest = std::max(0, b.num_tiles - p.ahead * idle);
     b.split_tiles = tail_split_tiles(rest, wave);
     b.num_items = b.num_tiles + b.split_tiles;
@@ -752,14 +795,32 @@ int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const 
     int st = zero_rows(dWg, size_t(K) * 2, (long long)K * 2, N, s);
     return st != GEMM_OK ? st : zero_rows(dWu, size_t(K) * 2, (long long)K * 2, N, s);
   }
+  GluParams p = {};
+  p.main.slices = p.second.slices = 1;
+  const int wave = glu_max_clusters(device);
+  if (wave <= 0) return GEMM_ERR_LAUNCH;
+  const bool wide = glu_backward_wide(M, N, K, dX != nullptr, dWg != nullptr, wave);
+  const int stage = wide ? 64 : 128, tile_rows = wide ? 2 * L::TILE_M : L::TILE_M;
+  int st = GEMM_OK;
+  if (dX != nullptr) st = plan_product(&p.main, M, K, N, stage, 2, 1, tile_rows, L::BLOCK_N);
+  if (st == GEMM_OK && dWg != nullptr) st = plan_product(&p.second, N, K, M, stage, 1, 2, tile_rows, L::BLOCK_N);
+  if (st != GEMM_OK) return st;
+  if (dX != nullptr && !wide) {
+    p.main.slices = glu_slices(p.main, p.second, wave);
+    p.main.num_items = p.main.num_tiles * p.main.slices;
+    p.main.slice_rows = ceil_div(M, 32) * 32;
+  }
+  const int slices = p.main.slices;
+  const size_t gate_bytes = size_t(M) * N * 4;  // N % 8 == 0: the partial sums start on a 16-byte boundary
+  const size_t slice_size = slices > 1 ? size_t(p.main.slice_rows) * K : 0;
   cudaMemPool_t pool = workspace_pool(device);
   void* ws = nullptr;
-  if (pool == nullptr || cudaMallocFromPoolAsync(&ws, size_t(M) * N * 4, pool, s) != cudaSuccess) {
+  if (pool == nullptr || cudaMallocFromPoolAsync(&ws, gate_bytes + slices * slice_size * 4, pool, s) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_OUT_OF_MEMORY;
   }
+  float* const partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + gate_bytes);
   uint16_t* dgu = static_cast<uint16_t*>(ws);
-  int st;
   {
     const long long vectors = static_cast<long long>(M) * (N / 8);
     cudaLaunchConfig_t cfg = {};
@@ -782,25 +843,43 @@ int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const 
   }
   if (st == GEMM_OK) {
     GluMaps m;
-    GluParams p = {};
-    const bool wide = glu_backward_wide(M, N, K, dX != nullptr, dWg != nullptr, glu_max_clusters(device));
-    const int stage = wide ? 64 : 128, tile_rows = wide ? 2 * L::TILE_M : L::TILE_M;
     st = map_in(&m.a0, dgu, N, M, 2LL * N, stage);  // (a box of 64 features is the same for either order)
     if (st == GEMM_OK) st = map_in(&m.a1, dgu + N, N, M, 2LL * N, stage);
     m.b0 = m.b1 = m.b2 = m.c0 = m.c1 = m.c2 = m.a0;
     if (dX != nullptr) {
       if (st == GEMM_OK) st = map_in(&m.b0, Wg, K, N, K, stage);
       if (st == GEMM_OK) st = map_in(&m.b1, Wu, K, N, K, stage);
-      if (st == GEMM_OK) st = map_out(&m.c0, dX, K, M, ld.dx);
-      if (st == GEMM_OK) st = plan_product(&p.main, M, K, N, stage, 2, 1, tile_rows, L::BLOCK_N);
+      if (st == GEMM_OK && slices == 1) st = map_out(&m.c0, dX, K, M, ld.dx);
+      if (st == GEMM_OK && slices > 1)
+        st = encode_tmap_2d(&m.c0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, partial, K, uint64_t(slices) * p.main.slice_rows,
+                            uint64_t(K) * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (dWg != nullptr) {
       if (st == GEMM_OK) st = map_in(&m.b2, X, K, M, ld.x, stage);
       if (st == GEMM_OK) st = map_out(&m.c1, dWg, K, N, K);
       if (st == GEMM_OK) st = map_out(&m.c2, dWu, K, N, K);
-      if (st == GEMM_OK) st = plan_product(&p.second, N, K, M, stage, 1, 2, tile_rows, L::BLOCK_N);
     }
     if (st == GEMM_OK) st = glu_launch<kGluBackward>(m, p, wide, 2.0, device, info, s);
+    if (st == GEMM_OK && slices > 1) {
+      const long long vectors = static_cast<long long>(M) * (K / 8);
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      cfg.gridDim = dim3(static_cast<unsigned>((vectors + 127) / 128), 1, 1);
+      cfg.blockDim = dim3(128, 1, 1);
+      cfg.stream = s;
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaLaunchKernelEx(&cfg, glu_join_kernel, static_cast<const float*>(partial), slices,
+                             static_cast<long long>(slice_size), static_cast<uint16_t*>(dX), ld.dx, K,
+                             vectors) != cudaSuccess) {
+        cudaGetLastError();
+        st = GEMM_ERR_LAUNCH;
+      } else {
+        count_launch();
+      }
+    }
   }
   if (cudaFreeAsync(ws, s) != cudaSuccess && st == GEMM_OK) st = GEMM_ERR_LAUNCH;
   return st;

@@ -16,6 +16,8 @@ struct GluProduct {
   int rows, cols, depth, k_iters;
   int num_m_blocks, num_n_blocks, num_tiles, group_m;
   int split_tiles, num_items;  // trailing tiles cut into halves of their columns; work items = tiles + split_tiles
+  int slices;                  // parts of the summed dimension, each an item of its own (then no halves)
+  int slice_rows;              // rows from one slice's partial sums to the next one's
 };
 
 struct GluParams {
@@ -34,6 +36,7 @@ struct GluParams {
 struct GluItem {
   int m_blk, n_blk, half;
   bool second;
+  int slice, k0, k1;  // its stages
 };
 
 // Item `it` of a cluster; false past its last one.
@@ -51,6 +54,13 @@ __device__ __forceinline__ bool glu_item(const GluParams& p, int cluster, int cl
     i = s < extra ? s * (clusters - in_last) + cluster - in_last : taken + (s - extra) * clusters + cluster;
     if (i >= p.second.num_items) return false;
   }
+  item.slice = 0;
+  if (q->slices > 1) {
+    item.slice = i / q->num_tiles;
+    i -= item.slice * q->num_tiles;
+  }
+  item.k0 = item.slice * q->k_iters / q->slices;
+  item.k1 = (item.slice + 1) * q->k_iters / q->slices;
   const WorkItem w = work_item(i, q->num_tiles, q->split_tiles);
   const TileCoord tc = tile_coord(w.tile, q->num_m_blocks, q->num_n_blocks, q->group_m);
   item.m_blk = tc.m_blk;
@@ -62,7 +72,7 @@ __device__ __forceinline__ bool glu_item(const GluParams& p, int cluster, int cl
 struct GluMaps {
   CUtensorMap a0, a1;      // forward: X (both); backward: dg, du
   CUtensorMap b0, b1, b2;  // Wg, Wu; backward: X
-  CUtensorMap c0, c1, c2;  // forward: H, g, u; backward: dX, dWg, dWu
+  CUtensorMap c0, c1, c2;  // forward: H, g, u; backward: dX (or its slices' partial sums), dWg, dWu
 };
 
 // Instruction descriptor (see idesc_bf16): BF16 operands, bits 15 / 16: A / B has its M / N dimension innermost.

@@ -569,7 +569,9 @@ int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const flo
  *   dH: M x N, dX: M x K, dWg, dWu: N x K, all BF16. dX may be NULL (not computed), dWg and dWu may both be.
  *   act'(0) of ReLU is 0.
  * Constraints as gemm_glu_bf16. Sums over nothing (M == 0 for dWg and dWu, N == 0 for dX) are set to zero.
- * Two kernel launches; [dg | du] lives in a workspace of 4 M N bytes from the library's stream-ordered pool.
+ * Two kernel launches; [dg | du] lives in a workspace of 4 M N bytes from the library's stream-ordered pool. Where dX
+ * has few tiles, its sum is cut into up to 8 slices: a third launch, and 4 K bytes a row and slice more of workspace.
+ * The same inputs give the same bits.
  */
 int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const void* Wu, const float* preact, void* dX,
                            void* dWg, void* dWu, int M, int N, int K, int act, void* stream,

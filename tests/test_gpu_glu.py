@@ -321,3 +321,20 @@ def test_few_rows_with_the_depth_shared_exact():
     _, saved = g.glu_bf16(x, wg, wu, act="relu", save=True)
     assert torch.equal(saved[:, :1000].double(), x.double() @ wg.double().T)
     assert torch.equal(saved[:, 1000:].double(), x.double() @ wu.double().T)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 264), (6, 2648, 824), (33, 4096, 136), (257, 2056, 520), (512, 4096, 1024)])
+def test_backward_with_dx_in_slices(M, N, K):
+    """Few tiles of dX and a long sum: partial sums of slices, with dX alone and beside dW, the same bits again."""
+    x, wg, wu, dh = problem(M, N, K, 5 * M + N + K)
+    _, saved = g.glu_bf16(x, wg, wu, save=True)
+    got = g.glu_bf16_backward(dh, x, wg, wu, saved)
+    want, root = gradient(dh, x, wg, wu, "silu")
+    for a, b, r in zip(got, want, root):
+        tol = 2.0 ** -8 * b.abs() + (8 / math.sqrt(3) * 2.0 ** -8 + 2.0 ** -10) * r + 1e-30
+        assert torch.all((a.double() - b).abs() <= tol)
+    again = g.glu_bf16_backward(dh, x, wg, wu, saved)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    alone, _, _ = g.glu_bf16_backward(dh, x, wg, wu, saved, weight_grads=False)
+    tol = 2.0 ** -8 * want[0].abs() + (8 / math.sqrt(3) * 2.0 ** -8 + 2.0 ** -10) * root[0] + 1e-30
+    assert torch.all((alone.double() - want[0]).abs() <= tol)
