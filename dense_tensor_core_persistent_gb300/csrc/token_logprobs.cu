@@ -4,13 +4,13 @@
 //   z = a l,  lse = log sum_j exp(z_j),  logprob = z_t - lse,  H = lse - sum_j p_j z_j,  p_j = exp(z_j - lse)
 //   dl_j = a (dlp (1[j = t] - p_j) - dH p_j (log p_j + H))
 //
-// One pass in powers of two: with c = a log2(e), a thread keeps the maximum m of its logits, a reference logit r with
-// m - 16 / c <= r <= m, s = sum 2^t and q = sum t 2^t over t = c (l - r), all FP32. The scale of s and q costs FP32 no
-// precision, so r follows m only when m has run 16 / c ahead: s f and (q + s d) f with d = c (r - r'), f = 2^d; a
-// warp's lanes hardly ever do that after their first logits, where following every new maximum would cost a warp a
-// rescaling in almost every step. Partial results join by the same rule, so threads, warps and the CTAs of a cluster
-// that share a row combine in a fixed order: lse = a r + ln s, H = ln s - ln 2 q / s. Where c r is beyond 2^60, logits
-// that differ at all have no mass next to m: s counts the logits equal to m.
+// One pass in powers of two: with c = a log2(e), a thread keeps the maximum m of its logits and, over t = c (l - m) of
+// all of them but one that is m itself, s = sum 2^t and q = sum t 2^t, all FP32. When m grows by d / c, the old one joins
+// the others: s becomes (s + 1) 2^-d and q (q - (s + 1) d) 2^-d. Partial results join by the same rule, so threads, warps
+// and the CTAs of a cluster that share a row combine in a fixed order: lse = a m + log1p(s), H = log1p(s) - ln 2 q /
+// (1 + s). The largest logit's own term is never rounded into s, and no two numbers of the results cancel, so a row that
+// one logit dominates keeps its digits, a log probability is never above 0 and an entropy never below it. Where c m is
+// beyond 2^60, logits that differ at all have no mass next to m: s counts the logits equal to m.
 //
 // Alternatives: a value that k threads' maxima reach is no larger than the k-th largest logit. At a row's end the CTA
 // takes such a bound, and the threads whose maxima reach it have the logits read again (from L2) that may: each thread
@@ -276,26 +276,30 @@ __device__ __forceinline__ unsigned long long warp_max_key(unsigned long long ke
   return static_cast<unsigned long long>(hi) << 32 | lo;
 }
 
-constexpr float kAhead = 16.0f;                        // (m - r) c at most
-constexpr float kOrdinary = 1.152921504606847e18f;     // |r c| below 2^60
+constexpr float kOrdinary = 1.152921504606847e18f;  // |m c| below 2^60
 
-// Sums of a part of a row, relative to its reference (see above); m minus infinity: no mass.
+// Sums of a part of a row relative to its maximum, without one logit that is the maximum (see above); m minus infinity:
+// no mass.
 struct Sums {
-  float m, ref, s, q;
+  float m, s, q;
 };
 
-// c (from - to), with no mass (and no NaN) left where that has no finite value.
-__device__ __forceinline__ float shift(float from, float to, float c) { return fmaxf((from - to) * c, -1.0e30f); }
+// c (from - to), with no mass (and no NaN) left where that has no finite value, nor where it multiplies a sum.
+__device__ __forceinline__ float shift(float from, float to, float c) { return fmaxf((from - to) * c, -1.0e20f); }
 
-// The sums of a warp's lanes as one, the same in every lane, relative to the largest of their references.
+// The sums of a warp's lanes as one, the same in every lane, relative to the largest of their maxima. The maximum left
+// out is that of the first lane that has it.
 __device__ __forceinline__ Sums warp_join(const Sums& a, float c) {
   const bool mass = a.m != kMinusInf;
   Sums r;
   r.m = order_value(__reduce_max_sync(0xffffffffu, order_of(a.m)));
-  r.ref = order_value(__reduce_max_sync(0xffffffffu, mass ? order_of(a.ref) : 0u));
-  const float d = a.ref == r.ref ? 0.0f : shift(a.ref, r.ref, c), f = ex2_approx(d);
-  r.s = mass ? a.s * f : 0.0f;
-  r.q = mass ? fmaf(a.s, d, a.q) * f : 0.0f;
+  const bool has = mass && a.m == r.m;
+  const uint32_t holders = __ballot_sync(0xffffffffu, has);  // (every lane takes part)
+  const bool first = static_cast<int>(threadIdx.x & 31) == __ffs(static_cast<int>(holders)) - 1;
+  const float d = has ? 0.0f : shift(a.m, r.m, c), f = ex2_approx(d);
+  const float all = first ? a.s : a.s + 1.0f;
+  r.s = mass ? all * f : 0.0f;
+  r.q = mass ? fmaf(all, d, a.q) * f : 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
@@ -490,48 +494,69 @@ __device__ void select_top(LogprobShared& sh, const Row<T>& row, const Part<T>& 
   });
 }
 
-// What a thread has seen of its row: its sums in two lanes of packed FP32.
+// What a thread has seen of its row.
 struct Running {
-  float m, ref;
-  uint64_t s, q;
+  float m, s, q;
 
   // (not NaN, not infinite)
-  __device__ __forceinline__ bool ordinary(float c) const { return fabsf(ref * c) < kOrdinary; }
-  // Logits follow of which `top` is the largest.
-  __device__ __forceinline__ void see(float top, float c) {
-    const bool none = m == kMinusInf;
-    m = max_nan(m, top);
-    if (none ? m != kMinusInf : !((m - ref) * c <= kAhead)) {
-      if (!none) {
-        const float d = shift(ref, m, c), f = ex2_approx(d);
-        const uint64_t f2 = f2_pack(f, f);
-        q = f2_mul(f2_fma(s, f2_pack(d, d), q), f2);
-        s = f2_mul(s, f2);
-      }
-      ref = m;
-    }
+  __device__ __forceinline__ bool ordinary(float c) const { return fabsf(m * c) < kOrdinary; }
+  // Logits follow of which `top` is the largest: whether it is the new maximum (then one of them is left out of s).
+  // Without a branch: some lane of a warp has a new maximum in almost every chunk.
+  __device__ __forceinline__ bool see(float top, float c) {
+    const float most = max_nan(m, top);
+    const bool fresh = most != m;
+    const float d = shift(m, most, c), f = ex2_approx(d);  // (0 and 1 where it stays)
+    const float all = fresh && m != kMinusInf ? s + 1.0f : s;
+    q = fmaf(all, d, q) * f;
+    s = all * f;
+    m = most;
+    return fresh;
   }
-  // Two logits. CLAMP: they may be minus infinity, or so low that c l is (t 2^t is no number then).
-  template <bool CLAMP>
-  __device__ __forceinline__ void add(uint64_t x2, uint64_t c2, uint64_t minus_ref2) {
-    uint64_t t2 = f2_mul(f2_add(x2, minus_ref2), c2);
-    float t0, t1;
-    f2_unpack(t2, t0, t1);
-    if (CLAMP) {
-      t0 = fmaxf(t0, -1.0e30f);
-      t1 = fmaxf(t1, -1.0e30f);
-      t2 = f2_pack(t0, t1);
-    }
-    const uint64_t e2 = f2_pack(ex2_approx(t0), ex2_approx(t1));
-    s = f2_add(s, e2);
-    q = f2_fma(e2, t2, q);
-  }
-  // The same where the reference is no ordinary number.
-  __device__ __forceinline__ void count(float x0, float x1) {
-    const float bad = m == m && m != -kMinusInf ? 0.0f : __uint_as_float(0x7FFFFFFFu);
-    s = f2_add(s, f2_pack(x0 == ref && bad == 0.0f ? 1.0f : bad, x1 == ref && bad == 0.0f ? 1.0f : bad));
+  // The sums of a chunk or of a row's end, in two lanes of packed FP32, added to this. A new maximum's own term comes out
+  // of the lane that has it (rounding could leave the sum of the others a little below 0 there).
+  __device__ __forceinline__ void take(uint64_t s2, uint64_t q2, bool fresh) {
+    float s0, s1, q0, q1;
+    f2_unpack(s2, s0, s1);
+    f2_unpack(q2, q0, q1);
+    s += max_nan(max_nan(s0, s1) - (fresh ? 1.0f : 0.0f) + fminf(s0, s1), 0.0f);
+    q += q0 + q1;
   }
 };
+
+// 2^t and t 2^t of two logits. CLAMP: they may be minus infinity, or so low that c l is (t 2^t is no number then).
+template <bool CLAMP>
+__device__ __forceinline__ uint64_t add_pair(uint64_t x2, uint64_t c2, uint64_t minus_m2, uint64_t& q2) {
+  uint64_t t2 = f2_mul(f2_add(x2, minus_m2), c2);
+  float t0, t1;
+  f2_unpack(t2, t0, t1);
+  if (CLAMP) {
+    t0 = fmaxf(t0, -1.0e30f);
+    t1 = fmaxf(t1, -1.0e30f);
+    t2 = f2_pack(t0, t1);
+  }
+  const uint64_t e2 = f2_pack(ex2_approx(t0), ex2_approx(t1));
+  q2 = f2_fma(e2, t2, q2);
+  return e2;
+}
+
+// The same of a vector, its powers added among themselves first: next to the maximum's 1 fewer of them are rounded off.
+template <typename T, bool CLAMP>
+__device__ __forceinline__ void add_vector(uint4 raw, uint64_t c2, uint64_t minus_m2, uint64_t& s2, uint64_t& q2) {
+  uint64_t e2 = f2_add(add_pair<CLAMP>(Vec<T>::pair(raw, 0), c2, minus_m2, q2),
+                       add_pair<CLAMP>(Vec<T>::pair(raw, 1), c2, minus_m2, q2));
+  if constexpr (Vec<T>::N == 8) {
+    const uint64_t f2 = f2_add(add_pair<CLAMP>(Vec<T>::pair(raw, 2), c2, minus_m2, q2),
+                               add_pair<CLAMP>(Vec<T>::pair(raw, 3), c2, minus_m2, q2));
+    e2 = f2_add(e2, f2);
+  }
+  s2 = f2_add(s2, e2);
+}
+
+// Where the maximum is no ordinary number: 1 for a logit equal to it, NaN if it is infinite or NaN.
+__device__ __forceinline__ float count_one(float x, float m) {
+  if (m != m || m == -kMinusInf) return __uint_as_float(0x7FFFFFFFu);
+  return x == m ? 1.0f : 0.0f;
+}
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_kernel(const LogprobParams p) {
@@ -578,7 +603,7 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_
   for (long long r = r0; r < p.rows; r += clusters) {
     const Row<T> row(static_cast<const T*>(p.logits) + r * p.ld, p.vocab);
     const Part<T> part(row, rank, p.cluster);
-    Running run{kMinusInf, 0.0f, 0ull, 0ull};
+    Running run{kMinusInf, 0.0f, 0.0f};
     bool masked = false;
     // the logits of vectors at the row's ends that are partly outside it, one per lane of the last warp: asked for
     // here, taken after the chunks
@@ -632,32 +657,30 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_
       if (left <= 0) continue;  // none of a row's last chunk (whole warps of a short one)
       const float most = Vec<T>::largest(raw);
       if (TOP) peaks.see(most, (v - part.n0) / kLogprobChunk);
-      run.see(most, c);
+      const bool fresh = run.see(most, c);
+      uint64_t s2 = 0, q2 = 0;
       if (run.ordinary(c)) {
-        const uint64_t minus_ref2 = f2_pack(-run.ref, -run.ref);
-        const Running before = run;
+        const uint64_t minus_m2 = f2_pack(-run.m, -run.m);
         const bool full_chunk = part.n1 - v >= kLogprobChunk;  // (else some of `raw` is minus infinity)
         if (!masked && full_chunk) {
 #pragma unroll
-          for (int u = 0; u < kLogprobBatch; ++u)
-#pragma unroll
-            for (int j = 0; j < N / 2; ++j) run.add<false>(Vec<T>::pair(raw[u], j), c2, minus_ref2);
+          for (int u = 0; u < kLogprobBatch; ++u) add_vector<T, false>(raw[u], c2, minus_m2, s2, q2);
           float q0, q1;
-          f2_unpack(run.q, q0, q1);
+          f2_unpack(q2, q0, q1);
           if (q0 != q0 || q1 != q1) {  // logits without mass among them: from here on with a clamp
             masked = true;
-            run = before;
+            s2 = q2 = 0;
           }
         }
         if (masked || !full_chunk) {
 #pragma unroll
           for (int u = 0; u < kLogprobBatch; ++u) {
             if (u * kLogprobThreads >= left) continue;
-#pragma unroll
-            for (int j = 0; j < N / 2; ++j) run.add<true>(Vec<T>::pair(raw[u], j), c2, minus_ref2);
+            add_vector<T, true>(raw[u], c2, minus_m2, s2, q2);
           }
         }
-      } else {
+      } else if (run.m != kMinusInf) {
+        float n = 0.0f;
 #pragma unroll 1
         for (int u = 0; u < kLogprobBatch; ++u) {
           float x[N];
@@ -667,29 +690,28 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_
             if (u == i) w = raw[i];
           Vec<T>::unpack(w, x);
 #pragma unroll
-          for (int j = 0; j < N; j += 2) run.count(x[j], x[j + 1]);
+          for (int j = 0; j < N; ++j) n += count_one(x[j], run.m);
         }
+        s2 = f2_pack(n, 0.0f);
       }
+      run.take(s2, q2, fresh);
     }
     if (end_index >= 0) {
       const float x = Vec<T>::value(end_logit);
       if (TOP && x != kMinusInf) list_candidate(sh, key_of(x, end_index));
-      run.see(x, c);
-      if (run.ordinary(c)) run.add<true>(f2_pack(x, kMinusInf), c2, f2_pack(-run.ref, -run.ref));
-      else run.count(x, kMinusInf);
+      const bool fresh = run.see(x, c);
+      if (run.m != kMinusInf) {
+        uint64_t e2, q2 = 0;
+        if (run.ordinary(c)) e2 = add_pair<true>(f2_pack(x, kMinusInf), c2, f2_pack(-run.m, -run.m), q2);
+        else e2 = f2_pack(count_one(x, run.m), 0.0f);
+        run.take(e2, q2, fresh);
+      }
     }
-    Sums t;
-    {
-      float s0, s1, q0, q1;
-      f2_unpack(run.s, s0, s1);
-      f2_unpack(run.q, q0, q1);
-      t = Sums{run.m, run.ref, s0 + s1, q0 + q1};
-    }
-    t = warp_join(t, c);
+    Sums t = warp_join(Sums{run.m, run.s, run.q}, c);
     if (lane == 0) sh.parts[warp] = t;
     __syncthreads();
     if (warp == 0) {
-      t = lane < kLogprobWarps ? sh.parts[lane] : Sums{kMinusInf, 0.0f, 0.0f, 0.0f};
+      t = lane < kLogprobWarps ? sh.parts[lane] : Sums{kMinusInf, 0.0f, 0.0f};
       t = warp_join(t, c);
       if (lane == 0) sh.total = t;
     }
@@ -698,26 +720,26 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_
     if (p.cluster > 1) cluster_sync_all();
     else __syncthreads();
     if (rank == 0) {
-      Sums all{kMinusInf, 0.0f, 0.0f, 0.0f};
+      Sums all{kMinusInf, 0.0f, 0.0f};
       if (lane < p.cluster) {
         const uint32_t at = mapa_shared(smem_u32(&sh.total), lane);
         all = Sums{__uint_as_float(ld_cluster_u32(at)), __uint_as_float(ld_cluster_u32(at + 4)),
-                   __uint_as_float(ld_cluster_u32(at + 8)), __uint_as_float(ld_cluster_u32(at + 12))};
+                   __uint_as_float(ld_cluster_u32(at + 8))};
       }
       all = warp_join(all, c);
       const bool empty = all.m == kMinusInf;  // no logit has any mass
-      const float log_s = logf(all.s);
-      const float lse = empty ? kMinusInf : fmaf(p.scale, all.ref, log_s);
-      // log probability of a logit: no mass next to a reference that is no ordinary number, unless it is that number
-      const bool ordinary = fabsf(all.ref * c) < kOrdinary;
+      const float log_s = log1pf(all.s);
+      const float lse = empty ? kMinusInf : fmaf(p.scale, all.m, log_s);
+      // log probability of a logit: no mass next to a maximum that is no ordinary number, unless it is that number
+      const bool ordinary = fabsf(all.m * c) < kOrdinary;
       auto logp = [&](float l) {
         if (empty) return kMinusInf;
-        if (ordinary || all.s != all.s) return p.scale * (l - all.ref) - log_s;
-        return l == all.ref ? -log_s : kMinusInf;
+        if (ordinary || all.s != all.s) return p.scale * (l - all.m) - log_s;
+        return l == all.m ? -log_s : kMinusInf;
       };
       if (tid == 0) {
         p.lse[r] = lse;
-        p.entropy[r] = empty ? 0.0f : log_s - kLn2 * (all.q / all.s);
+        p.entropy[r] = empty ? 0.0f : log_s - kLn2 * (all.q / (1.0f + all.s));
         if (p.logprob != nullptr) {
           const long long token = p.tokens[r];
           float lp = 0.0f;

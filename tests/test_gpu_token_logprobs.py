@@ -242,3 +242,36 @@ def test_repeats_stream_graph_and_empty():
     assert none.lse.numel() == 0 and none.top_ids.shape == (0, 8)
     free = g.token_logprobs(ld)
     assert free.logprob is None and torch.equal(free.lse, want.lse)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("others", [-44.0, -4.0])
+def test_rows_that_one_logit_dominates(dtype, others):
+    """A largest logit of 16, one of 16 - `lag` read by the same thread, in the same chunk of a row or in an earlier one,
+    and others far below: small log probabilities and entropies keep their digits and their signs.
+
+    Each power of two carries the rounding of an argument below 2^7 and its own, 1e-5 of itself with a margin; next to the
+    maximum, up to 64 of the other 70000 may be rounded off."""
+    rows, vocab = 320, 70000
+    n = 8 if dtype == torch.bfloat16 else 4
+    l = torch.full((rows, vocab), others)
+    t = torch.zeros(rows, dtype=torch.int64)
+    for i in range(rows):
+        lag, chunk, u, owner = (0.5, 3.0, 6.0, 8.0, 10.875)[i % 5], (0, 1, 3)[i // 5 % 3], i // 15 % 3, 37 * i % 256
+        first, later = n * owner, n * (owner + 256 * u + 2048 * chunk)
+        l[i, first + i % n] = 16.0 - lag
+        l[i, later + (i + 3) % n] = 16.0
+        t[i] = later + (i + 3) % n
+    l, t = l.to(dtype).to(DEV), t.to(DEV)
+    r = g.token_logprobs(l, t, top=2)
+    z = l.double()
+    rest = torch.exp(z - 16.0).sum(1) - 1.0
+    lp = -torch.log1p(rest)
+    p = torch.exp(z - 16.0 + lp[:, None])
+    ent = -(p * (z - 16.0 + lp[:, None])).sum(1)
+    rel = 1e-5 + 64 / 70000
+    assert torch.all(r.logprob <= 0) and torch.all(r.entropy >= 0)
+    assert torch.all((r.logprob.double() - lp).abs() <= rel * lp.abs())
+    assert torch.all((r.entropy.double() - ent).abs() <= rel * ent)
+    assert torch.equal(r.top_logprobs[:, 0], r.logprob) and torch.equal(r.top_ids[:, 0].long(), t)
+    assert torch.all((r.lse.double() - 16.0 + lp).abs() <= 32 * U)
