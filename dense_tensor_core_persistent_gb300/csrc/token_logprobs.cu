@@ -387,18 +387,19 @@ struct Peaks {
   }
 };
 
-// The `top` largest keys into sh.top by taking the largest one below the last, `top` times. below(last): the
-// thread's largest key below `last`.
+// The `top` largest keys into sh.top by taking the largest one below the last, `top` times. up_to(limit): the
+// thread's largest key that is no larger than `limit` (all of them at first: a NaN at index 0 has the largest there is).
 template <typename F>
-__device__ __forceinline__ void extract_top(LogprobShared& sh, int top, F below) {
+__device__ __forceinline__ void extract_top(LogprobShared& sh, int top, F up_to) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long last = ~0ull;
+  unsigned long long limit = ~0ull;
   for (int j = 0; j < top; ++j) {
-    const unsigned long long best = warp_max_key(below(last));
+    const unsigned long long best = warp_max_key(up_to(limit));
     if (lane == 0) sh.best[warp] = best;
     __syncthreads();
-    last = warp_max_key(lane < kLogprobWarps ? sh.best[lane] : 0ull);
-    if (threadIdx.x == 0) sh.top[j] = last;
+    const unsigned long long next = warp_max_key(lane < kLogprobWarps ? sh.best[lane] : 0ull);
+    if (threadIdx.x == 0) sh.top[j] = next;
+    limit = next == 0 ? 0 : next - 1;
     __syncthreads();
   }
 }
@@ -441,7 +442,7 @@ __device__ void select_top(LogprobShared& sh, const Row<T>& row, const Part<T>& 
   const int n = sh.candidates;
   if (n > kLogprobList) {
     // more candidates than the list holds (very many equal ones): from the row itself
-    extract_top(sh, top, [&](unsigned long long last) {
+    extract_top(sh, top, [&](unsigned long long limit) {
       unsigned long long best = 0;
       for (int v = part.v0 + tid; v < part.v1; v += kLogprobThreads) {
         float x[N];
@@ -451,7 +452,7 @@ __device__ void select_top(LogprobShared& sh, const Row<T>& row, const Part<T>& 
         for (int i = 0; i < N; ++i)
           if (x[i] != kMinusInf && c + i >= 0 && c + i < row.vocab) {
             const unsigned long long k = key_of(x[i], c + i);
-            if (k < last && k > best) best = k;
+            if (k <= limit && k > best) best = k;
           }
       }
       return best;
@@ -486,10 +487,10 @@ __device__ void select_top(LogprobShared& sh, const Row<T>& row, const Part<T>& 
     __syncthreads();
     return;
   }
-  extract_top(sh, top, [&](unsigned long long last) {
+  extract_top(sh, top, [&](unsigned long long limit) {
     unsigned long long best = 0;
     for (int i = tid; i < n; i += kLogprobThreads)
-      if (sh.cand[i] < last && sh.cand[i] > best) best = sh.cand[i];
+      if (sh.cand[i] <= limit && sh.cand[i] > best) best = sh.cand[i];
     return best;
   });
 }

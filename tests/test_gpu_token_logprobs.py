@@ -275,3 +275,15 @@ def test_rows_that_one_logit_dominates(dtype, others):
     assert torch.all((r.entropy.double() - ent).abs() <= rel * ent)
     assert torch.equal(r.top_logprobs[:, 0], r.logprob) and torch.equal(r.top_ids[:, 0].long(), t)
     assert torch.all((r.lse.double() - 16.0 + lp).abs() <= 32 * U)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_nan_at_the_first_index_among_many_candidates(dtype):
+    """More candidates than the list holds, the first logit NaN: it still comes first."""
+    l = torch.ones(3, 5001)
+    l[0] = math.nan
+    l[1, 0] = math.nan
+    l[1, 4000] = math.nan
+    r = g.token_logprobs(l.to(dtype).to(DEV), top=3)
+    assert r.top_ids.tolist() == [[0, 1, 2], [0, 4000, 1], [0, 1, 2]]
+    assert r.lse[:2].isnan().all() and r.lse[2].isfinite()
