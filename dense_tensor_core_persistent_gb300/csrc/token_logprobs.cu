@@ -814,7 +814,8 @@ __global__ void __launch_bounds__(kLogprobBackThreads) token_logprobs_backward_k
     const int c = row.first(v);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const float logp = max_nan(fmaf(x[j], p.scale, -lse), -1.0e30f);
+      // (no mass is left far above -1e4, and B times it stays finite for any B below 3e34)
+      const float logp = max_nan(fmaf(x[j], p.scale, -lse), -1.0e4f);
       x[j] = ex2_approx(logp * kLog2e) * fmaf(B, logp, A);
       if (empty) x[j] = 0.0f;
     }

@@ -287,3 +287,17 @@ def test_nan_at_the_first_index_among_many_candidates(dtype):
     r = g.token_logprobs(l.to(dtype).to(DEV), top=3)
     assert r.top_ids.tolist() == [[0, 1, 2], [0, 4000, 1], [0, 1, 2]]
     assert r.lse[:2].isnan().all() and r.lse[2].isfinite()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_gradients_leave_masked_logits_alone(dtype):
+    """Gradients of the entropy as large as a loss scale makes them: masked logits still get 0."""
+    l, t = problem(3, 1000, dtype, 4)
+    l[:, ::3] = -math.inf
+    l[:, 1::3] = torch.finfo(dtype).min
+    t = torch.tensor([2, 5, 8])
+    r = g.token_logprobs(l.to(DEV), t.to(DEV))
+    dl = g.token_logprobs_backward(l.to(DEV), t.to(DEV), r.lse, r.entropy, torch.ones(3, device=DEV),
+                                   torch.tensor([1e9, -1e12, 1e30], device=DEV)).cpu()
+    assert torch.all(dl[:, ::3] == 0) and torch.all(dl[:, 1::3] == 0)
+    assert dl.isfinite().all() and torch.all(dl[:, 2] != 0)
