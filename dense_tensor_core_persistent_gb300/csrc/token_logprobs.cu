@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(kLogprobBackThreads) token_logprobs_backward_k
   // dl_j = p_j (A + B log p_j), and a dlp more at the token
   const float bad = token >= p.vocab ? __uint_as_float(0x7FFFFFFFu) : 0.0f;
   const float A = -p.scale * (dlp + (dh != 0.0f ? dh * p.entropy[r] : 0.0f)) + bad, B = -p.scale * dh;
-  const bool empty = lse == kMinusInf;
+  const bool empty = lse == kMinusInf;  // no logit has any mass: zeros, unless the token is none of the vocabulary's
   const int v0 = part * (kLogprobBackThreads * kLogprobBackVectors) + static_cast<int>(threadIdx.x);
 #pragma unroll 2
   for (int k = 0; k < kLogprobBackVectors; ++k) {
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(kLogprobBackThreads) token_logprobs_backward_k
       // (no mass is left far above -1e4, and B times it stays finite for any B below 3e34)
       const float logp = max_nan(fmaf(x[j], p.scale, -lse), -1.0e4f);
       x[j] = ex2_approx(logp * kLog2e) * fmaf(B, logp, A);
-      if (empty) x[j] = 0.0f;
+      if (empty) x[j] = bad;
     }
     if (token >= c && token < c + N && !empty) {
 #pragma unroll

@@ -521,7 +521,8 @@ int gemm_token_logprobs(const void* logits, int type, const long long* tokens, f
  *   NULL, and dentropy (then entropy is not read). A negative token takes no part (its dlogprob is not read into
  *   the row); a token >= vocab makes the row NaN.
  *   dlogits: rows x vocab of the type of the logits, row stride ldd (0 = vocab); it may be the logits themselves
- *   (with ldd = ld). A row of nothing but minus infinity gets zeros; logits of minus infinity get 0.
+ *   (with ldd = ld). A row of nothing but minus infinity gets zeros (with a token >= vocab NaN, as any row); logits of
+ *   minus infinity get 0.
  * One kernel launch, asynchronous on `stream`, no workspace.
  */
 int gemm_token_logprobs_backward(const void* logits, int type, const long long* tokens, const float* lse,

@@ -301,3 +301,14 @@ def test_large_gradients_leave_masked_logits_alone(dtype):
                                    torch.tensor([1e9, -1e12, 1e30], device=DEV)).cpu()
     assert torch.all(dl[:, ::3] == 0) and torch.all(dl[:, 1::3] == 0)
     assert dl.isfinite().all() and torch.all(dl[:, 2] != 0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_token_outside_in_a_row_of_nothing(dtype):
+    """A token past the vocabulary makes its row NaN, also where the row has no mass."""
+    l = torch.full((3, 77), -math.inf, dtype=dtype, device=DEV)
+    t = torch.tensor([77, 3, -1], device=DEV)
+    r = g.token_logprobs(l, t)
+    assert r.logprob[0].isnan() and r.logprob[1] == -math.inf and r.logprob[2] == 0
+    dl = g.token_logprobs_backward(l, t, r.lse, r.entropy, torch.ones(3, device=DEV), torch.ones(3, device=DEV))
+    assert dl[0].isnan().all() and torch.all(dl[1:] == 0)
