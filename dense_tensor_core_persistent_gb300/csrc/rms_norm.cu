@@ -39,6 +39,7 @@
 namespace dtcp {
 
 constexpr int kNormMaxSmem = 3 * 8 * 512 * 16;  // dynamic shared memory of a CTA: three inputs, eight groups
+constexpr float kNormMostInverse = 1.7014118346046923e38f;  // 2^127, of an E4M3 row's scale
 constexpr int kNormMaxCols = 32768 - 8;  // 8 groups of 8 columns x 512 threads, less one group for the boundary
 
 struct NormParams {
@@ -378,10 +379,13 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 56 : 64, 80)) rm
           top = max(top, abs_bits(a.v[j] * rstd * g.v[j]));
       }
       top = block_max_bits(top, slots_max[parity], warps);
-      const float scale = __uint_as_float(top) / 448.0f;
-      // (finite for a row of denormals too; a NaN stays one)
+      float scale = __uint_as_float(top) / 448.0f;
+      // (a NaN stays one)
       float inverse = top == 0 ? 0.0f : 448.0f / __uint_as_float(top);
-      if (inverse > 3.0e38f) inverse = 3.0e38f;
+      if (inverse > kNormMostInverse) {  // a row near FP32's smallest numbers: the scale stops where its inverse does
+        inverse = kNormMostInverse;
+        scale = 1.0f / kNormMostInverse;
+      }
       if (threadIdx.x == 0) static_cast<float*>(p.scales)[row] = scale;
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {

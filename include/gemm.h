@@ -454,9 +454,10 @@ typedef struct {
  * in FP32 from the rounded s, y rounded once to the output format.
  *   X, R: rows x cols BF16; R may be NULL (s = X).   W: cols BF16, or NULL (all ones).
  *   S: rows x cols BF16, receives s; required with R, else may be NULL. S may be X or R itself.
- *   Y, scales: see the formats above. E4M3: scale = max|y| / 448 of the row, code = e4m3_rne(y / scale)
- *   (a row of zeros: scale 0, codes 0). NVFP4: scale = e4m3_rne(min(max|y| / 6, 448)) of the 16
- *   columns, code = e2m1_rne(y / scale), at most 6 in magnitude (scale 0: codes 0). A tensor-wide
+ *   Y, scales: see the formats above. E4M3: scale = max|y| / 448 of the row but at least 2^-127, code = e4m3_rne(y /
+ *   scale) (a row of zeros: scale 0, codes 0). NVFP4: scale = e4m3_rne(min(max|y| / 6, 448)) of the 16
+ *   columns, code = e2m1_rne(y / scale), at most 6 in magnitude (scale 0: codes 0). The quotients are products with a
+ *   rounded reciprocal: within 2^-21 of a tie, relative to y, a code may be the tie's other side. A tensor-wide
  *   factor, where one is wanted, goes into W and its inverse into gemm_epilogue_t.alpha.
  *   rstd: rows FP32 for the backward pass, or NULL.
  * An infinity or NaN in a row makes rstd 0 or NaN and shows in the row's outputs as the formula

@@ -263,3 +263,22 @@ def test_graph_capture():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("cols", [520, 1003, 16391])
+@pytest.mark.parametrize("weight", [2.0 ** -118, 2.0 ** -122, 2.0 ** -126, 2.0 ** -131])
+def test_e4m3_of_tiny_rows(cols, weight):
+    """Rows near FP32's smallest normal number: the scale stops at 2^-127, and codes and scale still belong together."""
+    rows = 5
+    x, _, w = problem(rows, cols, cols, residual=False)
+    w = (w.float() * weight).to(torch.bfloat16)
+    w[3] = 0.0
+    n = g.rms_norm(dev(x), dev(w), eps=EPS, out="e4m3")
+    _, _, y = definition(x, None, w)
+    got = n.scales.cpu().double()
+    tiny = 2.0 ** -149
+    assert torch.all((got - (y.abs().amax(1) / 448).clamp(min=2.0 ** -127)).abs() <= FP32_REL * got + tiny)
+    q = (y / got[:, None]).clamp(-448, 448)
+    half = torch.exp2(torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6))) - 4)
+    # y itself is a product of FP32 numbers, at its smallest in steps of 2^-149
+    assert torch.all((n.y.cpu().double() - q).abs() <= half + 2 * FP32_REL * q.abs() + 2 * tiny / got[:, None])
