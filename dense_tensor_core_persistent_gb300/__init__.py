@@ -496,6 +496,8 @@ def glu_plan(M: int, N: int, K: int, wave: int = 76) -> tuple[int, int]:
 
 
 # ---------------------------------------------------------------- torch-tensor conveniences
+# `stream`: a torch stream or a handle; torch's current stream if it is None. The matrix products allocate `out`, where it
+# is not given, on the current stream; the operators allocate on `stream` (see _on_stream).
 
 def matmul_bf16(A, B, out=None, stream=None, opts=None):
     """A (M x K) and B (N x K) BF16 CUDA tensors -> C = A @ B^T (M x N BF16)."""
@@ -571,6 +573,29 @@ def _vector(t, what, dtype, n):
     return t
 
 
+def _on_stream(stream, call, *args):
+    """call(*args) on `stream` (a torch stream, a handle or an object that has one), as under torch.cuda.stream: what it
+    allocates is that stream's memory. Its tensors are recorded on the streams that use them, so none is given away while
+    a kernel still reads or writes it; that its inputs are ready on `stream`, and its outputs where they are read, is the
+    caller's to order."""
+    import torch
+    here = torch.cuda.current_stream()
+    handle = _stream(stream)
+    if handle == here.cuda_stream:
+        return call(*args)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        got = call(*args)
+    for t in args:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+    for t in (got,) if isinstance(got, torch.Tensor) else got:
+        if t is not None:
+            t.record_stream(here)
+    return got
+
+
 class NormOutput(NamedTuple):
     """y: BF16, float8_e4m3fn, or packed E2M1 bytes; scales: None, FP32 a row, or E4M3 bytes per 16;
     sum: the residual stream after the addition; rstd: FP32 a row, or None."""
@@ -588,6 +613,8 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-5, out: str = "bf16"
     """RMS norm of the rows of x + residual (rows x cols BF16). `out`: "bf16", "e4m3" (scales: FP32 a row)
     or "nvfp4" (y and scales are A and SFA of matmul_nvfp4). `save`: keep rstd for rms_norm_backward.
     `inplace`: the sum overwrites `residual`."""
+    if stream is not None:
+        return _on_stream(stream, rms_norm, x, weight, residual, eps, out, save, inplace)
     import torch
     fmt = _NORM_FORMATS.get(out)
     if fmt is None:
@@ -622,7 +649,7 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-5, out: str = "bf16"
     if ldx or ldr or lds:
         strides = gemm_norm_strides_t(ldx, ldr, lds, 0)
     status = lib().gemm_rms_norm(x.data_ptr(), _address(residual), _address(weight), _address(written), y.data_ptr(),
-                                 _address(scales), _address(rstd), rows, cols, eps, fmt, _stream(stream),
+                                 _address(scales), _address(rstd), rows, cols, eps, fmt, _stream(None),
                                  _byref_or_null(strides))
     if status:
         raise GemmError(status, "gemm_rms_norm")
@@ -632,6 +659,8 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-5, out: str = "bf16"
 def rms_norm_backward(dy, total, weight, rstd, dsum=None, weight_grad: bool = True, stream=None):
     """(dx, dweight) of rms_norm with BF16 output: `total` and `rstd` are NormOutput.sum and .rstd, `dsum` the
     gradient that reaches the sum past the norm. dx is the gradient of x and of the residual; dweight is FP32."""
+    if stream is not None:
+        return _on_stream(stream, rms_norm_backward, dy, total, weight, rstd, dsum, weight_grad)
     import torch
     bf16 = torch.bfloat16
     lds = _matrix(total, "total", bf16)
@@ -645,7 +674,7 @@ def rms_norm_backward(dy, total, weight, rstd, dsum=None, weight_grad: bool = Tr
     dw = torch.empty(cols, dtype=torch.float32, device=dy.device) if weight_grad else None
     strides = gemm_norm_backward_strides_t(lddy, lds, ldds, 0) if lddy or lds or ldds else None
     status = lib().gemm_rms_norm_backward(dy.data_ptr(), total.data_ptr(), _address(weight), rstd.data_ptr(),
-                                          _address(dsum), dx.data_ptr(), _address(dw), rows, cols, _stream(stream),
+                                          _address(dsum), dx.data_ptr(), _address(dw), rows, cols, _stream(None),
                                           _byref_or_null(strides))
     if status:
         raise GemmError(status, "gemm_rms_norm_backward")
@@ -673,6 +702,8 @@ def _logits_kind(logits):
 def token_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, stream=None) -> TokenLogprobs:
     """Log probabilities of `tokens` (rows int64; negative: none) under softmax(scale * logits) of each row, the
     entropy, and the `top` most likely alternatives (equal logits: the lower index first)."""
+    if stream is not None:
+        return _on_stream(stream, token_logprobs, logits, tokens, top, scale)
     import torch
     kind = _logits_kind(logits)
     ld = _matrix(logits, "logits", logits.dtype)
@@ -688,7 +719,7 @@ def token_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, stream
         top_ids = torch.empty((rows, top), dtype=torch.int32, device=logits.device)
     status = lib().gemm_token_logprobs(logits.data_ptr(), kind, _address(tokens), _address(logprob), entropy.data_ptr(),
                                        lse.data_ptr(), top, _address(top_logprobs), _address(top_ids), rows, vocab, ld,
-                                       scale, _stream(stream))
+                                       scale, _stream(None))
     if status:
         raise GemmError(status, "gemm_token_logprobs")
     return TokenLogprobs(logprob, entropy, lse, top_logprobs, top_ids)
@@ -698,6 +729,8 @@ def token_logprobs_backward(logits, tokens, lse, entropy, dlogprob, dentropy=Non
                             inplace: bool = False, stream=None):
     """dlogits of token_logprobs, in the type of the logits; `inplace` overwrites them. tokens and dlogprob may
     both be None, and dentropy."""
+    if stream is not None:
+        return _on_stream(stream, token_logprobs_backward, logits, tokens, lse, entropy, dlogprob, dentropy, scale, inplace)
     import torch
     kind = _logits_kind(logits)
     ld = _matrix(logits, "logits", logits.dtype)
@@ -711,7 +744,7 @@ def token_logprobs_backward(logits, tokens, lse, entropy, dlogprob, dentropy=Non
     status = lib().gemm_token_logprobs_backward(logits.data_ptr(), kind, _address(tokens), lse.data_ptr(),
                                                 _address(entropy), _address(dlogprob), _address(dentropy),
                                                 dlogits.data_ptr(), rows, vocab, ld, ld if inplace else 0, scale,
-                                                _stream(stream))
+                                                _stream(None))
     if status:
         raise GemmError(status, "gemm_token_logprobs_backward")
     return dlogits
@@ -735,6 +768,8 @@ def _contiguous(t, what, dtype, shape):
 def glu_bf16(x, wg, wu, act: str = "silu", save: bool = False, stream=None):
     """act(x wg^T) * (x wu^T) for BF16 x (M x K), wg and wu (N x K) -> M x N BF16. `save`: also what
     glu_bf16_backward needs, as (h, saved)."""
+    if stream is not None:
+        return _on_stream(stream, glu_bf16, x, wg, wu, act, save)
     import torch
     kind, bf16 = _glu_act(act), torch.bfloat16
     ldx = _matrix(x, "x", bf16)
@@ -745,7 +780,7 @@ def glu_bf16(x, wg, wu, act: str = "silu", save: bool = False, stream=None):
     h = torch.empty((M, N), dtype=bf16, device=x.device)
     saved = torch.empty((M, 2 * N), dtype=torch.float32, device=x.device) if save else None
     status = lib().gemm_glu_bf16(x.data_ptr(), wg.data_ptr(), wu.data_ptr(), h.data_ptr(), _address(saved), M, N, K, kind,
-                                 _stream(stream), gemm_glu_strides_t(ldx, 0, 0, 0) if ldx else None)
+                                 _stream(None), gemm_glu_strides_t(ldx, 0, 0, 0) if ldx else None)
     if status:
         raise GemmError(status, "gemm_glu_bf16")
     return (h, saved) if save else h
@@ -753,6 +788,8 @@ def glu_bf16(x, wg, wu, act: str = "silu", save: bool = False, stream=None):
 
 def glu_e4m3(x, x_scale, wg, wg_scale, wu, wu_scale, act: str = "silu", stream=None):
     """glu_bf16 from float8_e4m3fn operands with an FP32 scale per row (x: rms_norm(..., out="e4m3"))."""
+    if stream is not None:
+        return _on_stream(stream, glu_e4m3, x, x_scale, wg, wg_scale, wu, wu_scale, act)
     import torch
     kind, e4m3 = _glu_act(act), torch.float8_e4m3fn
     ldx = _matrix(x, "x", e4m3)
@@ -764,7 +801,7 @@ def glu_e4m3(x, x_scale, wg, wg_scale, wu, wu_scale, act: str = "silu", stream=N
         _vector(t, what, torch.float32, n)
     h = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     status = lib().gemm_glu_e4m3(x.data_ptr(), x_scale.data_ptr(), wg.data_ptr(), wg_scale.data_ptr(), wu.data_ptr(),
-                                 wu_scale.data_ptr(), h.data_ptr(), M, N, K, kind, _stream(stream),
+                                 wu_scale.data_ptr(), h.data_ptr(), M, N, K, kind, _stream(None),
                                  gemm_glu_strides_t(ldx, 0, 0, 0) if ldx else None)
     if status:
         raise GemmError(status, "gemm_glu_e4m3")
@@ -774,6 +811,8 @@ def glu_e4m3(x, x_scale, wg, wg_scale, wu, wu_scale, act: str = "silu", stream=N
 def glu_bf16_backward(dh, x, wg, wu, saved, act: str = "silu", input_grad: bool = True, weight_grads: bool = True,
                       stream=None):
     """(dx, dwg, dwu) of glu_bf16(..., save=True); None in the place of a gradient that is not asked for."""
+    if stream is not None:
+        return _on_stream(stream, glu_bf16_backward, dh, x, wg, wu, saved, act, input_grad, weight_grads)
     import torch
     kind, bf16 = _glu_act(act), torch.bfloat16
     ldx = _matrix(x, "x", bf16)
@@ -787,7 +826,7 @@ def glu_bf16_backward(dh, x, wg, wu, saved, act: str = "silu", input_grad: bool 
     dwg = torch.empty_like(wg) if weight_grads else None
     dwu = torch.empty_like(wg) if weight_grads else None
     status = lib().gemm_glu_bf16_backward(dh.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), saved.data_ptr(),
-                                          _address(dx), _address(dwg), _address(dwu), M, N, K, kind, _stream(stream),
+                                          _address(dx), _address(dwg), _address(dwu), M, N, K, kind, _stream(None),
                                           gemm_glu_strides_t(ldx, 0, lddh, 0) if ldx or lddh else None)
     if status:
         raise GemmError(status, "gemm_glu_bf16_backward")
