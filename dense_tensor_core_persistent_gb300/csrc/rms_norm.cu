@@ -634,6 +634,15 @@ struct RowPlace {
 
 bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
+// Zeros, as the sum over nothing is (a null pointer: nothing to do).
+int zero_floats(void* p, int n, cudaStream_t stream) {
+  if (p != nullptr && cudaMemsetAsync(p, 0, static_cast<size_t>(n) * 4, stream) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_LAUNCH;
+  }
+  return GEMM_OK;
+}
+
 }  // namespace
 }  // namespace dtcp
 
@@ -645,7 +654,16 @@ int gemm_rms_norm(const void* X, const void* R, const void* W, void* S, void* Y,
                   int cols, float eps, int format, void* stream, const gemm_norm_strides_t* strides) {
   if (rows < 0 || cols < 0 || !(eps >= 0.0f)) return GEMM_ERR_INVALID_ARG;
   if (format != GEMM_NORM_BF16 && format != GEMM_NORM_E4M3 && format != GEMM_NORM_NVFP4) return GEMM_ERR_INVALID_ARG;
-  if (rows == 0 || cols == 0) return GEMM_OK;
+  if (rows == 0) return GEMM_OK;
+  if (cols == 0) {  // rows without columns: what is one number a row is 0
+    void* row_scales = format == GEMM_NORM_E4M3 ? scales : nullptr;
+    if (row_scales == nullptr && rstd == nullptr) return GEMM_OK;
+    if (misaligned(row_scales, 4) || misaligned(rstd, 4)) return GEMM_ERR_MISALIGNED;
+    int device = 0, err = 0;
+    if (current_device_info(&device, &err) == nullptr) return err;
+    const int st = zero_floats(row_scales, rows, static_cast<cudaStream_t>(stream));
+    return st != GEMM_OK ? st : zero_floats(rstd, rows, static_cast<cudaStream_t>(stream));
+  }
   if (X == nullptr || Y == nullptr || (format != GEMM_NORM_BF16 && scales == nullptr)) return GEMM_ERR_INVALID_ARG;
   if (R != nullptr && S == nullptr) return GEMM_ERR_INVALID_ARG;
   NormParams p;
@@ -716,13 +734,7 @@ int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const f
   const DeviceInfo* info = current_device_info(&device, &err);
   if (info == nullptr) return err;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (rows == 0) {  // the sum over no rows
-    if (cudaMemsetAsync(dW, 0, static_cast<size_t>(cols) * 4, st) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_LAUNCH;
-    }
-    return GEMM_OK;
-  }
+  if (rows == 0) return zero_floats(dW, cols, st);  // the sum over no rows
   p.dy = static_cast<const uint16_t*>(dY);
   p.s = static_cast<const uint16_t*>(S);
   p.w = static_cast<const uint16_t*>(W);

@@ -463,7 +463,8 @@ typedef struct {
  * An infinity or NaN in a row makes rstd 0 or NaN and shows in the row's outputs as the formula
  * gives it (NaN scales for E4M3 and NVFP4); other rows are not touched by it. The squares are summed in FP32, so a
  * row whose sum of squares passes 3.4e38 counts as one with an infinity.
- * Constraints: rows, cols >= 0 (0: nothing to do); cols <= 32760; eps >= 0; pointers aligned to
+ * Constraints: rows, cols >= 0 (no rows: nothing to do; no columns: rstd and the E4M3 scales are set to 0); cols <=
+ * 32760; eps >= 0; pointers aligned to
  * their element; NVFP4: cols % 16 == 0, Y and scales without strides, X, R, W, S 16-byte aligned with
  * strides that are multiples of 8. Any other cols, stride or alignment is taken; rows that start
  * on 16-byte boundaries are fastest, then rows whose tensors share their misalignment.

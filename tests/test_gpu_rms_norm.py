@@ -282,3 +282,18 @@ def test_e4m3_of_tiny_rows(cols, weight):
     half = torch.exp2(torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6))) - 4)
     # y itself is a product of FP32 numbers, at its smallest in steps of 2^-149
     assert torch.all((n.y.cpu().double() - q).abs() <= half + 2 * FP32_REL * q.abs() + 2 * tiny / got[:, None])
+
+
+def test_rows_without_columns():
+    """Rows of no columns: nothing to norm, a scale and an rstd of 0."""
+    x = torch.empty(300, 0, dtype=torch.bfloat16, device=DEV)
+    scales, rstd = torch.full((300,), 7.0, device=DEV), torch.full((300,), 7.0, device=DEV)
+    g.gemm_rms_norm(x, None, None, None, x, scales, rstd, 300, 0, EPS, g.GEMM_NORM_E4M3)
+    assert torch.all(scales == 0) and torch.all(rstd == 0)
+    rstd.fill_(7.0)
+    g.gemm_rms_norm(x, None, None, None, x, None, rstd, 300, 0, EPS)
+    assert torch.all(rstd == 0)
+    n = g.rms_norm(x, save=True)
+    assert n.y.shape == (300, 0)
+    dx, dw = g.rms_norm_backward(x, n.sum, None, n.rstd)
+    assert dx.shape == (300, 0) and dw.shape == (0,)
