@@ -546,6 +546,8 @@ def matmul_nvfp4(A, SFA, B, SFB, out=None, stream=None, opts=None):
 
 def _matrix(t, what, dtype, shape=None):
     """A CUDA matrix of `dtype` whose rows are contiguous -> its row stride (0: rows follow one another)."""
+    if t is None:
+        raise ValueError(f"{what}: a CUDA {dtype} matrix is needed, got None")
     size = t.shape
     if t.dtype is not dtype or len(size) != 2 or not t.is_cuda or (shape is not None and size != shape):
         want = "" if shape is None else f" of shape {tuple(shape)}"
@@ -568,6 +570,8 @@ def _address(t):
 
 
 def _vector(t, what, dtype, n):
+    if t is None:
+        raise ValueError(f"{what}: a CUDA {dtype} vector of {n} is needed, got None")
     if t.dtype is not dtype or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous CUDA {dtype} vector of {n} is needed, got {t.dtype} {tuple(t.shape)}")
     return t
@@ -735,9 +739,9 @@ def token_logprobs_backward(logits, tokens, lse, entropy, dlogprob, dentropy=Non
     kind = _logits_kind(logits)
     ld = _matrix(logits, "logits", logits.dtype)
     rows, vocab = logits.shape
-    for t, what, dtype in ((tokens, "tokens", torch.int64), (lse, "lse", torch.float32),
-                           (entropy, "entropy", torch.float32), (dlogprob, "dlogprob", torch.float32),
-                           (dentropy, "dentropy", torch.float32)):
+    _vector(lse, "lse", torch.float32, rows)
+    for t, what, dtype in ((tokens, "tokens", torch.int64), (entropy, "entropy", torch.float32),
+                           (dlogprob, "dlogprob", torch.float32), (dentropy, "dentropy", torch.float32)):
         if t is not None:
             _vector(t, what, dtype, rows)
     dlogits = logits if inplace else torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)

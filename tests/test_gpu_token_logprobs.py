@@ -312,3 +312,16 @@ def test_token_outside_in_a_row_of_nothing(dtype):
     assert r.logprob[0].isnan() and r.logprob[1] == -math.inf and r.logprob[2] == 0
     dl = g.token_logprobs_backward(l, t, r.lse, r.entropy, torch.ones(3, device=DEV), torch.ones(3, device=DEV))
     assert dl[0].isnan().all() and torch.all(dl[1:] == 0)
+
+
+def test_missing_tensors_are_refused():
+    l = torch.zeros(2, 32, dtype=torch.bfloat16, device=DEV)
+    one = torch.ones(2, device=DEV)
+    for call in (lambda: g.token_logprobs_backward(l, None, None, None, None),
+                 lambda: g.rms_norm(None),
+                 lambda: g.rms_norm_backward(l, l, None, None),
+                 lambda: g.rms_norm_backward(None, l, None, one),
+                 lambda: g.glu_bf16_backward(l, l, torch.zeros(32, 32, dtype=torch.bfloat16, device=DEV),
+                                             torch.zeros(32, 32, dtype=torch.bfloat16, device=DEV), None)):
+        with pytest.raises(ValueError):
+            call()
