@@ -45,9 +45,11 @@ def random_weights(width: int, hidden: int, vocab: int, device="cuda", seed: int
 
 
 def to_e4m3_rows(w: torch.Tensor):
-    """E4M3 codes and a scale per row of a weight matrix (done once, when the weights are loaded)."""
+    """E4M3 codes and a scale per row of a weight matrix (done once, when the weights are loaded). A row of zeros has
+    scale 0 and codes 0."""
     scale = w.float().abs().amax(1) / 448
-    return (w.float() / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn), scale
+    safe = torch.where(scale > 0, scale, 1.0)
+    return (w.float() / safe[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn), scale
 
 
 def add_product(h: torch.Tensor, w: torch.Tensor, residual: torch.Tensor) -> torch.Tensor:

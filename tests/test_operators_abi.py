@@ -1,4 +1,7 @@
 """Argument checks of the operators around the products (no GPU needed: refusals come before any device use)."""
+import importlib.util
+import os
+
 import pytest
 import torch
 
@@ -150,3 +153,16 @@ def test_glu_plan():
     for bad in ((-1, 8, 8, 76), (8, -8, 8, 76), (8, 8, -8, 76), (8, 8, 8, 0)):
         with pytest.raises(g.GemmError):
             g.glu_plan(*bad)
+
+
+def test_example_quantises_a_row_of_zeros():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "feed_forward.py")
+    spec = importlib.util.spec_from_file_location("feed_forward", path)
+    ff = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ff)
+    w = torch.randn(3, 32, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    w[1] = 0.0
+    codes, scale = ff.to_e4m3_rows(w)
+    assert scale[1] == 0 and torch.all(codes[1].float() == 0)
+    back = codes.float() * scale[:, None]
+    assert torch.all((back - w.float()).abs() <= 2.0 ** -4 * w.float().abs() + 2.0 ** -10 * scale[:, None])
