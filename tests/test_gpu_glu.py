@@ -338,3 +338,81 @@ def test_backward_with_dx_in_slices(M, N, K):
     alone, _, _ = g.glu_bf16_backward(dh, x, wg, wu, saved, weight_grads=False)
     tol = 2.0 ** -8 * want[0].abs() + (8 / math.sqrt(3) * 2.0 ** -8 + 2.0 ** -10) * root[0] + 1e-30
     assert torch.all((alone.double() - want[0]).abs() <= tol)
+
+
+def e4m3_rows(t):
+    s = t.float().abs().amax(1) / 448
+    return (t.float() / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn), s
+
+
+def check_e4m3(x, wg, wu, act="silu"):
+    """The E4M3 form on the quantised operands, against FP64."""
+    (xe, xs), (ge, gs), (ue, us) = e4m3_rows(x), e4m3_rows(wg), e4m3_rows(wu)
+    h = g.glu_e4m3(xe, xs, ge, gs, ue, us, act=act)
+    check_forward(h, xe.double() * xs.double()[:, None], ge.double() * gs.double()[:, None],
+                  ue.double() * us.double()[:, None], act)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 20016, 144), (20, 19464, 272), (64, 29192, 80), (100, 20008, 144), (128, 19520, 208),
+                                   (33, 16128, 1040)])
+def test_few_rows_with_several_tiles_a_cta(M, N, K):
+    """More tiles of 64 features than SMs: second and later items of a CTA, with halves in the last wave and (16128)
+    without."""
+    x, wg, wu, _ = problem(M, N, K, M + N + K)
+    xd, gd, ud = x.double(), wg.double(), wu.double()
+    h, saved = g.glu_bf16(x, wg, wu, act="gelu_tanh", save=True)
+    gate, up = check_forward(h, xd, gd, ud, "gelu_tanh")
+    steps = (K / 16 + 16) * 2.0 ** -23
+    assert torch.all((saved[:, :N].double() - gate).abs() <= steps * (xd.abs() @ gd.abs().T))
+    assert torch.all((saved[:, N:].double() - up).abs() <= steps * (xd.abs() @ ud.abs().T))
+    assert torch.equal(h, g.glu_bf16(x, wg, wu, act="gelu_tanh"))
+    check_e4m3(x, wg, wu, "gelu_tanh")
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 12800, 272), (300, 10880, 528), (1030, 5128, 272), (129, 19464, 144),
+                                   (2000, 2568, 2064)])
+@pytest.mark.parametrize("act", ["silu", "relu"])
+def test_e4m3_with_several_tiles_a_pair(M, N, K, act):
+    """Whole tiles of the pair tile in E4M3, and more of them than pairs (10880, 19464: a last wave of halves)."""
+    x, wg, wu, _ = problem(M, N, K, M + N + K)
+    check_e4m3(x, wg, wu, act)
+
+
+@pytest.mark.parametrize("M,N,K", [(128, 264, 136), (300, 264, 136), (2500, 7000, 2056)])
+def test_strides_on_each_tile(M, N, K):
+    """X, H, dH and dX with rows apart from one another, on the few-row kernel, the pair tile and the 512 x 256 one."""
+    assert g.glu_plan(M, N, K) == {128: (0, 256), 300: (256, 256), 2500: (512, 512)}[M]
+    x, wg, wu, dh = problem(M, N, K, 73)
+    h, saved = g.glu_bf16(x, wg, wu, save=True)
+    want = g.glu_bf16_backward(dh, x, wg, wu, saved)
+
+    def apart(t, before, after):
+        wide = torch.full((M, before + t.shape[1] + after), 7.0, dtype=t.dtype, device=DEV)
+        wide[:, before:before + t.shape[1]] = t
+        return wide[:, before:before + t.shape[1]]
+
+    xv, dhv = apart(x, 8, 16), apart(dh, 0, 40)
+    h2, saved2 = g.glu_bf16(xv, wg, wu, save=True)
+    assert torch.equal(h2, h) and torch.equal(saved2, saved)
+    assert all(torch.equal(a, b) for a, b in zip(g.glu_bf16_backward(dhv, xv, wg, wu, saved), want))
+    out, dx = (torch.full((M, n + 24), 3.0, dtype=torch.bfloat16, device=DEV) for n in (N, K))
+    g.gemm_glu_bf16(x, wg, wu, out, None, M, N, K, strides=g.gemm_glu_strides_t(0, N + 24, 0, 0))
+    g.gemm_glu_bf16_backward(dh, x, wg, wu, saved, dx, *(torch.empty_like(wg) for _ in range(2)), M, N, K,
+                             strides=g.gemm_glu_strides_t(0, 0, 0, K + 24))
+    assert torch.equal(out[:, :N], h) and torch.all(out[:, N:] == 3.0)
+    assert torch.equal(dx[:, :K], want[0]) and torch.all(dx[:, K:] == 3.0)
+
+
+@pytest.mark.parametrize("M", [37, 300])
+def test_e4m3_strides(M):
+    N, K = 264, 144
+    x, wg, wu, _ = problem(M, N, K, 79)
+    (xe, xs), (ge, gs), (ue, us) = e4m3_rows(x), e4m3_rows(wg), e4m3_rows(wu)
+    want = g.glu_e4m3(xe, xs, ge, gs, ue, us)
+    wide = torch.full((M, K + 48), 7.0, device=DEV).to(torch.float8_e4m3fn)
+    view = wide[:, 16:16 + K]
+    view.copy_(xe)
+    assert torch.equal(g.glu_e4m3(view, xs, ge, gs, ue, us), want)
+    out = torch.full((M, N + 16), 3.0, dtype=torch.bfloat16, device=DEV)
+    g.gemm_glu_e4m3(view, xs, ge, gs, ue, us, out, M, N, K, strides=g.gemm_glu_strides_t(K + 48, N + 16, 0, 0))
+    assert torch.equal(out[:, :N], want) and torch.all(out[:, N:] == 3.0)

@@ -297,3 +297,43 @@ def test_rows_without_columns():
     assert n.y.shape == (300, 0)
     dx, dw = g.rms_norm_backward(x, n.sum, None, n.rstd)
     assert dx.shape == (300, 0) and dw.shape == (0,)
+
+
+# Widths of two, four and eight groups a thread, on the 16-byte boundary and off it, with more rows than resident CTAs.
+SEVERAL_ROWS = [(1500, 4096), (2000, 2051), (400, 12000), (400, 12003), (330, 20000), (330, 20001)]
+
+
+@pytest.mark.parametrize("rows,cols", SEVERAL_ROWS)
+def test_several_rows_a_cta(rows, cols):
+    test_bf16(rows, cols, True)
+    test_e4m3(rows, cols)
+    test_backward(rows, cols, True)
+
+
+@pytest.mark.parametrize("rows,cols", [(6000, 256), (1500, 4096), (400, 12000), (330, 20000)])
+def test_nvfp4_with_several_rows_a_cta(rows, cols):
+    test_nvfp4(rows, cols)
+
+
+@pytest.mark.parametrize("cols", [1003, 9001])
+def test_several_rows_a_cta_that_share_no_alignment(cols):
+    """x, the residual and the gradients at offsets and strides of their own: element by element."""
+    rows = 1300
+    x, r, w = problem(rows, cols, cols)
+    dy, ds = rand(cols + 5, rows, cols), rand(cols + 6, rows, cols, std=0.5)
+
+    def apart(t, before, wide):
+        v = torch.full((rows, wide), 9.0, dtype=torch.bfloat16, device=DEV)[:, before:before + cols]
+        v.copy_(t)
+        return v
+
+    vx, vr = apart(x, 1, cols + 7), apart(r, 6, cols + 9)
+    n = g.rms_norm(vx, dev(w), residual=vr, eps=EPS, save=True)
+    s, rstd, y = definition(x, r, w)
+    assert torch.equal(n.sum.cpu(), s)
+    assert torch.all((n.rstd.cpu().double() - rstd[:, 0]).abs() <= FP32_REL * rstd[:, 0])
+    assert torch.all((n.y.cpu().double() - y).abs() <= (2.0 ** -8 + FP32_REL) * y.abs())
+    dx, dw = g.rms_norm_backward(apart(dy, 3, cols + 4), apart(s, 2, cols + 5), dev(w), n.rstd, dsum=apart(ds, 5, cols + 12))
+    want, terms, want_dw, terms_dw = backward_definition(dy, s, w, ds)
+    assert torch.all((dx.cpu().double() - want).abs() <= 2.0 ** -8 * want.abs() + FP32_REL * terms)
+    assert torch.all((dw.cpu().double() - want_dw).abs() <= 2.0 ** -14 * terms_dw + 1e-30)

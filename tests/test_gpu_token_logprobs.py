@@ -325,3 +325,25 @@ def test_missing_tensors_are_refused():
                                              torch.zeros(32, 32, dtype=torch.bfloat16, device=DEV), None)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(153, 262147, torch.float32), (153, 524293, torch.bfloat16)])
+def test_several_rows_a_cluster(rows, vocab, dtype):
+    """More rows than clusters of CTAs that share one, each with alternatives."""
+    gen = torch.Generator(device=DEV).manual_seed(vocab)
+    l = torch.randn(rows, vocab, generator=gen, device=DEV)
+    l = (l * (0.5 + 3 * torch.rand(rows, 1, generator=gen, device=DEV))).to(dtype)
+    t = torch.randint(0, vocab, (rows,), generator=gen, device=DEV)
+    r = g.token_logprobs(l, t, top=20)
+    lse, logp, _, ent, lp = definition(l, t)
+    d = delta(vocab)
+    tol = d + 8 * U * (lse.abs() + math.log(vocab) + l.double().amax(1).abs())
+    assert torch.all((r.lse.double() - lse).abs() <= tol)
+    assert torch.all((r.logprob.double() - lp).abs() <= tol + 8 * U * lp.abs())
+    assert torch.all((r.entropy.double() - ent).abs() <= 4 * d * (1 + math.log(vocab)))
+    order = torch.sort(l.float() + 0.0, dim=1, descending=True, stable=True).indices[:, :20]
+    assert torch.equal(r.top_ids.long(), order)
+    want = logp.gather(1, order)
+    assert torch.all((r.top_logprobs.double() - want).abs() <= tol[:, None] + 8 * U * want.abs())
+    again = g.token_logprobs(l, t, top=20)
+    assert all(torch.equal(a, b) for a, b in zip(r, again))
