@@ -792,13 +792,15 @@ __global__ void __launch_bounds__(kLogprobBackThreads) token_logprobs_backward_k
   T* out = static_cast<T*>(p.dlogits) + r * p.ldd;
   const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.base)) & 15u) == 0;
   const long long token = p.tokens != nullptr ? p.tokens[r] : -1;
-  const float lse = p.lse[r];
+  const float row_lse = p.lse[r];
   const float dlp = token >= 0 ? p.dlogprob[r] : 0.0f;
   const float dh = p.dentropy != nullptr ? p.dentropy[r] : 0.0f;
-  // dl_j = p_j (A + B log p_j), and a dlp more at the token
   const float bad = token >= p.vocab ? __uint_as_float(0x7FFFFFFFu) : 0.0f;
-  const float A = -p.scale * (dlp + (dh != 0.0f ? dh * p.entropy[r] : 0.0f)) + bad, B = -p.scale * dh;
-  const bool empty = lse == kMinusInf;  // no logit has any mass: zeros, unless the token is none of the vocabulary's
+  // dl_j = p_j (A + B log p_j), and a dlp more at the token. Where no logit has any mass every p_j is 0, against any lse.
+  const bool empty = row_lse == kMinusInf;
+  const float lse = empty ? 0.0f : row_lse;
+  const float A = empty ? bad : -p.scale * (dlp + (dh != 0.0f ? dh * p.entropy[r] : 0.0f)) + bad;
+  const float B = empty ? 0.0f : -p.scale * dh;
   const int v0 = part * (kLogprobBackThreads * kLogprobBackVectors) + static_cast<int>(threadIdx.x);
 #pragma unroll 2
   for (int k = 0; k < kLogprobBackVectors; ++k) {
@@ -812,7 +814,6 @@ __global__ void __launch_bounds__(kLogprobBackThreads) token_logprobs_backward_k
       // (no mass is left far above -1e4, and B times it stays finite for any B below 3e34)
       const float logp = max_nan(fmaf(x[j], p.scale, -lse), -1.0e4f);
       x[j] = ex2_approx(logp * kLog2e) * fmaf(B, logp, A);
-      if (empty) x[j] = bad;
     }
     if (token >= c && token < c + N && !empty) {
 #pragma unroll
