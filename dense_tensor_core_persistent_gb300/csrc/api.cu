@@ -191,8 +191,8 @@ int resident_ctas(const void* kernel, int threads, int smem) {
     const void* kernel;
     int threads, smem, ctas;
   };
-  // Every size of every kernel that asks: the norm's seven forward kernels with one group a thread take 32 thread counts,
-  // with two 16, with four and eight 8 each, and so do its three backward ones: 640 in all.
+  // Every size of every kernel that asks: the norm's seven forward kernels with one group a thread take 32 thread
+  // counts, with two 16, with four and eight 8 each, and so do its three backward ones: 640 in all.
   constexpr int kEntries = 640;
   static std::mutex mu;
   static Entry entries[kEntries];

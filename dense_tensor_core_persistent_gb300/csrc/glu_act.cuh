@@ -1,4 +1,7 @@
 // glu_act.cuh -- the activations of the gated feed-forward block and their derivatives.
+//
+// Exponential and reciprocal are the hardware's (ex2.approx, rcp.approx: 2^-22 and 2^-23 of their values). What they
+// give is rounded to BF16 (2^-9) right after, directly or as H, dg and du.
 #pragma once
 
 #include "common.cuh"

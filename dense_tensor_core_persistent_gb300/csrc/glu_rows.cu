@@ -415,7 +415,8 @@ int launch_rows(const GluRowsOperands& x, int device, const DeviceInfo* info, cu
   p.num_tiles = ceil_div(x.features, L::FEATURES);
   // As many CTAs to a tile as let every tile run at once: one CTA draws at most some 50 GB/s. Measured on GB300, 1 row
   // x N x 8192 in BF16, without splits (but halves of tiles) and with the rule: N = 512 27.1 and 7.6 us (8 CTAs), 1792
-  // 27.1 and 12.7 (4), 4096 28.3 and 23.7 (2); N = 5120, where two CTAs no longer fit, 33.7 and 43.4 with 2.
+  // 27.1 and 12.7 (4), 4096 28.3 and 23.7 (2); N = 5120, where two CTAs no longer fit, 33.7 and 43.4 with 2. Where the
+  // sum is short the join can cost more than it saves: 128 x 4096 x 1024 in E4M3 9.4 and 10.0.
   p.splits = 1;
   for (int s = 0; s < 3; ++s)
     if (p.num_tiles <= clusters[s] && p.k_iters >= 2 << s) p.splits = 2 << s;

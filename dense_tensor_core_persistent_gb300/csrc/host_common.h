@@ -105,10 +105,11 @@ int run_pack_scales2_copy(const void* SF0, void* out0, int rows0, const void* SF
 // with programmatic stream serialization (the GEMM after it starts its set-up early).
 int run_copy_rows(void* dst, const void* A, int M, int K, cudaStream_t stream, int pdl = 1);
 
-// The gated feed-forward block for few rows (glu_rows.cu): X, Wg, Wu in BF16 or E4M3 (then with scales); preact:
-// [g | u] in FP32 or null. Up to so many rows it is the faster kernel, measured on GB300 against the pair tile of
-// glu.cu: 64 rows x 28672 x 8192 140 against 158 us in BF16 and 74 against 83 in E4M3, x 14336 x 4096 41 against 48 and
-// 24 against 28; 128 rows 154 against 159 and 82 against 85, 48 against 50 and 29.5 against 27.6.
+// The gated feed-forward block for few rows (glu_rows.cu): X, Wg, Wu in BF16 or E4M3 (then with scales); preact: [g |
+// u] in FP32 or null. Up to so many rows it is taken, whatever the type and size. Measured on GB300 against the pair
+// tile of glu.cu: 64 rows x 28672 x 8192 140 against 158 us in BF16 and 74 against 83 in E4M3, x 14336 x 4096 41
+// against 48 and 24 against 28; 128 rows 154 against 159 and 82 against 85, 48 against 50 and, where it loses, in E4M3
+// with the smaller weights, 29.5 against 27.6.
 constexpr int kGluRows = 128;
 struct GluRowsOperands {
   const void* x;

@@ -13,18 +13,22 @@
 // a thread holds 2 groups of 8 columns (4 or 8 in rows longer than 8192 or 16384), up to 512 threads hold a row. CTAs
 // are persistent, as many as fit on the SMs, and step over rows by the grid size. Each thread copies its groups of the
 // CTA's next row to places of its own in shared memory (cp.async) before it takes the current one from there, so
-// loads stay in flight through the reductions and stores without holding registers or meeting at barriers.
-// A thread always owns the same columns: the weight is read once per CTA and the weight's gradient is summed in
-// registers, one partial row per CTA, which a second kernel adds in a fixed order (no atomics).
+// loads stay in flight through the reductions and stores without holding registers or meeting at barriers. (With eight
+// groups there is room for one row: the next one is asked for once the current one has been read, the gradient's once
+// it has been written, so little of it streams.) A thread always owns the same columns: the weight is read once per
+// CTA and the weight's gradient is summed in registers, one partial row per CTA, which a second kernel adds in a fixed
+// order (no atomics).
 //
 // Rows that no 16-byte vector divides: the groups of a row start at its 16-byte boundary, so
 // all but the first and last of its groups are whole vectors. The grid is a multiple of 8 (or
 // one CTA per row), so that boundary is at the same column for every row of a CTA.
 //
-// Measured on GB300 with inputs larger than L2, residual added: 4000 x 8192 43 us in BF16 (6.1 TB/s) and 38 to E4M3
-// (6.1), 4001 x 4099 22.8 us (5.8); gradient 4000 x 8192 44 us (5.9), with the weight's 49; 4001 x 4099 27.3 (4.8) and
-// 31.0. Off the boundary the rest goes to the row ends' parts and the warps that a row fills in part. With the rows
-// loaded to registers (and as many groups a thread as were best then) the same took 43, 37, 24, 55, 66, 33 and 39 us.
+// Measured on GB300 with inputs larger than L2, residual added: 4000 x 8192 44 us in BF16 (5.9 TB/s) and 37.6 to E4M3
+// (6.1), 4001 x 4099 24 us in both; gradient 4000 x 8192 45 us (5.8), with the weight's 51; 4001 x 4099 28 (4.7) and
+// 32. Off the boundary the rest goes to the row ends' parts and the warps that a row fills in part. Short rows are a
+// CTA of a few warps each, with a barrier a row: the gradient of 16000 x 1024 takes 24 us, with the weight's 34 (floor
+// 19.6), 131072 x 128 71 and 88 (floor 20.1). With the rows loaded to registers (and as many groups a thread as were
+// best then) the first ones took 43, 37, 24, 55, 66, 33 and 39 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -293,9 +297,11 @@ __device__ __forceinline__ int row_phase(const uint16_t* row) {
 
 // ---------------------------------------------------------------- forward
 
-// Registers per thread by groups per thread: 1024 threads with one group, 512 with more, and with two or four as few as
-// hold a row without spills, so that several CTAs fit on an SM. Rows off the boundary need some more for their ends;
-// measured on GB300 at 16000 x 1023: forward 25.1 us with 64 and 26.7 with 56, gradient 36.3 with 80 and 42.8 with 64.
+// Registers per thread by groups per thread: 1024 threads with one group, 512 with more. With two groups as few as
+// hold a row without spills, so that several CTAs fit on an SM; with four a little fewer (4 to 40 bytes a thread are
+// spilled in the gradient and in forward rows off the boundary); with eight the 128 that 512 threads leave, which do
+// not hold a row (44 to 184 bytes). Rows off the boundary need some more for their ends; measured on GB300 at 16000 x
+// 1023: forward 25.1 us with 64 and 26.7 with 56, gradient 36.3 with 80 and 42.8 with 64.
 template <int VPT>
 constexpr int norm_regs(int two, int four) { return VPT == 1 ? 64 : VPT == 2 ? two : VPT == 4 ? four : 128; }
 

@@ -5,23 +5,29 @@
 //   dl_j = a (dlp (1[j = t] - p_j) - dH p_j (log p_j + H))
 //
 // One pass in powers of two: with c = a log2(e), a thread keeps the maximum m of its logits and, over t = c (l - m) of
-// all of them but one that is m itself, s = sum 2^t and q = sum t 2^t, all FP32. When m grows by d / c, the old one joins
-// the others: s becomes (s + 1) 2^-d and q (q - (s + 1) d) 2^-d. Partial results join by the same rule, so threads, warps
-// and the CTAs of a cluster that share a row combine in a fixed order: lse = a m + log1p(s), H = log1p(s) - ln 2 q /
-// (1 + s). The largest logit's own term is never rounded into s, and no two numbers of the results cancel, so a row that
-// one logit dominates keeps its digits, a log probability is never above 0 and an entropy never below it. Where c m is
-// beyond 2^60, logits that differ at all have no mass next to m: s counts the logits equal to m.
+// all of them but one that is m itself, s = sum 2^t and q = sum t 2^t, all FP32. When m grows by d / c, the old one
+// joins the others: s becomes (s + 1) 2^-d and q (q - (s + 1) d) 2^-d. Partial results join by the same rule, so
+// threads, warps and the CTAs of a cluster that share a row combine in a fixed order: lse = a m + log1p(s), H =
+// log1p(s) - ln 2 q / (1 + s). The largest logit's own term is never rounded into s, and no two numbers of the results
+// cancel, so a row that one logit dominates keeps its digits, a log probability is never above 0 and an entropy never
+// below it. Where c m is beyond 2^60, logits that differ at all have no mass next to m: s counts the logits equal to
+// m.
 //
 // Alternatives: a value that k threads' maxima reach is no larger than the k-th largest logit. At a row's end the CTA
 // takes such a bound, and the threads whose maxima reach it have the logits read again (from L2) that may: each thread
 // remembers its two largest chunk maxima and the chunk of the first, so that is one chunk's part of 8 vectors for most
 // of them. The few logits that reach the bound are put in order by 64-bit keys (value, then the lower index), all
-// different. Logits of minus infinity take no part: where there are fewer others than are wanted, the lowest indices
-// follow.
+// different; the order in which they arrive (shared-memory atomics) does not matter. Logits of minus infinity take no
+// part: where there are fewer others than are wanted, the lowest indices follow.
 //
-// Bound by the bytes of the logits: measured on GB300, 4096 x 131072 BF16 159 us (6.7 TB/s), with 20 alternatives 211;
-// the gradient 328 us (6.5 TB/s). A row is split over a cluster of 1 to 8 CTAs that join through
-// shared memory, so few rows still use many SMs and no workspace or second launch is needed.
+// Powers of two are ex2.approx (2^-22): the sums average that out, and the results' errors are those of FP32 (log
+// probabilities 3e-8, entropy 5e-8 of their size). The gradient's p_j = exp(z_j - lse) takes lse as it was written,
+// rounded to FP32: an error of p_j of up to |lse| 2^-24, the same for all of a row (7e-7 at an lse of 12).
+//
+// Bound by the bytes of the logits: measured on GB300, 4096 x 131072 BF16 160.5 us (6.7 TB/s), with 20 alternatives
+// 214; 4096 x 65536 FP32 151 (7.1); their gradients 330 us (6.5 TB/s) and 319 (6.7). Following the maximum in every
+// chunk costs 1% against a reference that may trail it (158.6 us). A row is split over a cluster of 1 to 8 CTAs that
+// join through shared memory, so few rows still use many SMs and no workspace or second launch is needed.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -388,7 +394,8 @@ struct Peaks {
 };
 
 // The `top` largest keys into sh.top by taking the largest one below the last, `top` times. up_to(limit): the
-// thread's largest key that is no larger than `limit` (all of them at first: a NaN at index 0 has the largest there is).
+// thread's largest key that is no larger than `limit` (all of them at first: a NaN at index 0 has the largest there
+// is).
 template <typename F>
 __device__ __forceinline__ void extract_top(LogprobShared& sh, int top, F up_to) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -513,8 +520,8 @@ struct Running {
     m = most;
     return fresh;
   }
-  // The sums of a chunk or of a row's end, in two lanes of packed FP32, added to this. A new maximum's own term comes out
-  // of the lane that has it (rounding could leave the sum of the others a little below 0 there).
+  // The sums of a chunk or of a row's end, in two lanes of packed FP32, added to this. A new maximum's own term comes
+  // out of the lane that has it (rounding could leave the sum of the others a little below 0 there).
   __device__ __forceinline__ void take(uint64_t s2, uint64_t q2, bool fresh) {
     float s0, s1, q0, q1;
     f2_unpack(s2, s0, s1);
@@ -735,8 +742,9 @@ __global__ void __launch_bounds__(kLogprobThreads, kLogprobCtas) token_logprobs_
         p.lse[r] = lse;
         p.entropy[r] = empty ? 0.0f : log_s - kLn2 * (all.q / (1.0f + all.s));
         if (p.logprob != nullptr) {
-          // (Asked for at the row's start and carried to here, the token and its logit cost registers that the alternatives
-          // need: 4096 x 131072 BF16 with 20 of them 230 us instead of 214, without alternatives the same.)
+          // (Asked for at the row's start and carried to here, the token and its logit cost registers that the
+          // alternatives need: 4096 x 131072 BF16 with 20 of them 230 us instead of 214, though 1500 x 50001 FP32 without
+          // alternatives took 49.4 instead of 51.)
           const long long token = p.tokens[r];
           float lp = 0.0f;
           if (token >= p.vocab) lp = __uint_as_float(0x7FFFFFFFu);
@@ -796,7 +804,8 @@ __global__ void __launch_bounds__(kLogprobBackThreads) token_logprobs_backward_k
   const float dlp = token >= 0 ? p.dlogprob[r] : 0.0f;
   const float dh = p.dentropy != nullptr ? p.dentropy[r] : 0.0f;
   const float bad = token >= p.vocab ? __uint_as_float(0x7FFFFFFFu) : 0.0f;
-  // dl_j = p_j (A + B log p_j), and a dlp more at the token. Where no logit has any mass every p_j is 0, against any lse.
+  // dl_j = p_j (A + B log p_j), and a dlp more at the token. Where no logit has any mass every p_j is 0, against any
+  // lse.
   const bool empty = row_lse == kMinusInf;
   const float lse = empty ? 0.0f : row_lse;
   const float A = empty ? bad : -p.scale * (dlp + (dh != 0.0f ? dh * p.entropy[r] : 0.0f)) + bad;

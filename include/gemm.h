@@ -504,7 +504,8 @@ enum { GEMM_LOGITS_BF16 = 0, GEMM_LOGITS_F32 = 1 };
  *   top: 0..32 and at most vocab; top_logprobs: rows x top FP32, top_ids: rows x top int32. The order is
  *   that of the logits; equal logits (-0 and 0 among them) go by the lower index; NaN comes first.
  *   scale: an inverse temperature, finite and > 0.
- * Sums are FP32 with a running maximum. Logits of minus infinity (or of the type's lowest value next to
+ * Sums are FP32, relative to the maximum, whose own term is exact: no log probability is above 0 and no entropy
+ * below. Logits of minus infinity (or of the lowest value of their type next to
  * ordinary ones) have probability 0 and take no part in the entropy. A row of nothing but minus infinity has
  * lse and log probabilities of minus infinity (0 for a place without a token) and entropy 0. A NaN or plus
  * infinity in a row makes its outputs NaN.
@@ -519,9 +520,10 @@ int gemm_token_logprobs(const void* logits, int type, const long long* tokens, f
  * gemm_token_logprobs_backward -- gradient of logprob and entropy with respect to the logits:
  *   dlogits_j = scale * (dlogprob * (1[j = token] - p_j) - dentropy * p_j * (log p_j + entropy)),
  * rounded once to the type of the logits.
- *   lse, entropy: what gemm_token_logprobs wrote. dlogprob, dentropy: rows FP32; dlogprob and tokens may both be
- *   NULL, and dentropy (then entropy is not read). A negative token takes no part (its dlogprob is not read into
- *   the row); a token >= vocab makes the row NaN.
+ *   lse, entropy: what gemm_token_logprobs wrote; p_j = exp(z_j - lse) carries lse's rounding to FP32, a relative
+ *   error of up to |lse| 2^-24. dlogprob, dentropy: rows FP32; dlogprob and tokens may both be NULL, and dentropy
+ *   (then entropy is not read). A negative token takes no part (its dlogprob is not read into the row); a token >=
+ *   vocab makes the row NaN.
  *   dlogits: rows x vocab of the type of the logits, row stride ldd (0 = vocab); it may be the logits themselves
  *   (with ldd = ld). A row of nothing but minus infinity gets zeros (with a token >= vocab NaN, as any row); logits of
  *   minus infinity get 0.
@@ -573,7 +575,8 @@ int gemm_glu_e4m3(const void* X, const float* x_scale, const void* Wg, const flo
  *   act'(0) of ReLU is 0.
  * Constraints as gemm_glu_bf16. Sums over nothing (M == 0 for dWg and dWu, N == 0 for dX) are set to zero.
  * Two kernel launches; [dg | du] lives in a workspace of 4 M N bytes from the library's stream-ordered pool. Where dX
- * has few tiles, its sum is cut into up to 8 slices: a third launch, and 4 K bytes a row and slice more of workspace.
+ * has few tiles, its sum is cut into up to 8 slices: a third launch, and 4 K bytes more of workspace for each slice
+ * and row, M rounded up to a multiple of 32.
  * The same inputs give the same bits.
  */
 int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const void* Wu, const float* preact, void* dX,
