@@ -734,7 +734,8 @@ def token_logprobs_backward(logits, tokens, lse, entropy, dlogprob, dentropy=Non
     """dlogits of token_logprobs, in the type of the logits; `inplace` overwrites them. tokens and dlogprob may
     both be None, and dentropy."""
     if stream is not None:
-        return _on_stream(stream, token_logprobs_backward, logits, tokens, lse, entropy, dlogprob, dentropy, scale, inplace)
+        return _on_stream(stream, token_logprobs_backward, logits, tokens, lse, entropy, dlogprob, dentropy, scale,
+                          inplace)
     import torch
     kind = _logits_kind(logits)
     ld = _matrix(logits, "logits", logits.dtype)
