@@ -46,6 +46,7 @@ EXPORTS = (
     "gemm_bf16_plan", "gemm_clc_rule", "gemm_nvfp4_plan", "gemm_bf16_wide_rule",
     "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_token_logprobs", "gemm_token_logprobs_backward",
     "gemm_glu_bf16", "gemm_glu_e4m3", "gemm_glu_bf16_backward", "gemm_glu_plan",
+    "gemm_cross_entropy", "gemm_cross_entropy_backward", "gemm_cross_entropy_piece",
 )
 
 # gemm_activation_t
@@ -143,6 +144,10 @@ class gemm_glu_strides_t(ctypes.Structure):
                 ("dx", ctypes.c_longlong)]
 
 
+class gemm_cross_entropy_strides_t(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_longlong), ("dx", ctypes.c_longlong)]
+
+
 class gemm_norm_strides_t(ctypes.Structure):
     _fields_ = [("x", ctypes.c_longlong), ("residual", ctypes.c_longlong), ("sum", ctypes.c_longlong),
                 ("y", ctypes.c_longlong)]
@@ -230,6 +235,13 @@ def lib() -> ctypes.CDLL:
         l.gemm_glu_bf16_backward.restype = I
         l.gemm_glu_plan.argtypes = [I, I, I, I, ctypes.POINTER(I), ctypes.POINTER(I)]
         l.gemm_glu_plan.restype = I
+        CS = ctypes.POINTER(gemm_cross_entropy_strides_t)
+        l.gemm_cross_entropy.argtypes = [P, P, P, P, P, I, I, I, F, P, CS]
+        l.gemm_cross_entropy.restype = I
+        l.gemm_cross_entropy_backward.argtypes = [P, P, P, P, P, P, P, P, I, I, I, F, ctypes.c_size_t, P, CS]
+        l.gemm_cross_entropy_backward.restype = I
+        l.gemm_cross_entropy_piece.argtypes = [I, I, ctypes.c_size_t]
+        l.gemm_cross_entropy_piece.restype = I
         _lib = l
     return _lib
 
@@ -493,6 +505,30 @@ def glu_plan(M: int, N: int, K: int, wave: int = 76) -> tuple[int, int]:
     fwd, bwd = ctypes.c_int(), ctypes.c_int()
     _check(lib().gemm_glu_plan(M, N, K, wave, ctypes.byref(fwd), ctypes.byref(bwd)), "gemm_glu_plan")
     return fwd.value, bwd.value
+
+
+def gemm_cross_entropy(X, W, targets, loss, lse, M: int, vocab: int, K: int, scale: float = 1.0, stream=None,
+                       strides: gemm_cross_entropy_strides_t | None = None) -> None:
+    """Softmax cross entropy of X W^T against targets, without storing the logits; see include/gemm.h."""
+    _check(lib().gemm_cross_entropy(_ptr(X), _ptr(W), _ptr(targets), _ptr(loss), _ptr(lse), M, vocab, K, scale,
+                                    _stream(stream), _byref_or_null(strides)), "gemm_cross_entropy")
+
+
+def gemm_cross_entropy_backward(X, W, targets, lse, dloss, dlse, dX, dW, M: int, vocab: int, K: int, scale: float = 1.0,
+                                workspace: int = 0, stream=None,
+                                strides: gemm_cross_entropy_strides_t | None = None) -> None:
+    """Gradient of gemm_cross_entropy; see include/gemm.h."""
+    _check(lib().gemm_cross_entropy_backward(_ptr(X), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dlse),
+                                             _ptr(dX), _ptr(dW), M, vocab, K, scale, workspace, _stream(stream),
+                                             _byref_or_null(strides)), "gemm_cross_entropy_backward")
+
+
+def cross_entropy_piece(M: int, vocab: int, workspace: int = 0) -> int:
+    """Columns of the vocabulary that the gradient of cross_entropy takes at a time (host only)."""
+    n = lib().gemm_cross_entropy_piece(M, vocab, workspace)
+    if n < 0:
+        raise GemmError(-n, "gemm_cross_entropy_piece")
+    return n
 
 
 # ---------------------------------------------------------------- torch-tensor conveniences
@@ -836,3 +872,67 @@ def glu_bf16_backward(dh, x, wg, wu, saved, act: str = "silu", input_grad: bool 
     if status:
         raise GemmError(status, "gemm_glu_bf16_backward")
     return dx, dwg, dwu
+
+
+class CrossEntropy(NamedTuple):
+    """FP32 per row: loss (None without targets; 0 where there is none), lse."""
+    loss: object
+    lse: object
+
+
+def cross_entropy(x, head, targets=None, scale: float = 1.0, stream=None) -> CrossEntropy:
+    """Softmax cross entropy of scale * x head^T (x: rows x width, head: vocab x width, BF16) against `targets` (rows
+    int64; negative: none), without storing the logits."""
+    if stream is not None:
+        return _on_stream(stream, cross_entropy, x, head, targets, scale)
+    import torch
+    bf16 = torch.bfloat16
+    ldx = _matrix(x, "x", bf16)
+    rows, width = x.shape
+    _contiguous(head, "head", bf16, None)
+    vocab = head.shape[0]
+    if head.shape[1] != width:
+        raise ValueError(f"head: rows of {width} are needed, got {tuple(head.shape)}")
+    if targets is not None:
+        _vector(targets, "targets", torch.int64, rows)
+    lse = torch.empty(rows, dtype=torch.float32, device=x.device)
+    loss = torch.empty_like(lse) if targets is not None else None
+    status = lib().gemm_cross_entropy(x.data_ptr(), head.data_ptr(), _address(targets), _address(loss), lse.data_ptr(),
+                                      rows, vocab, width, scale, _stream(None),
+                                      gemm_cross_entropy_strides_t(ldx, 0) if ldx else None)
+    if status:
+        raise GemmError(status, "gemm_cross_entropy")
+    return CrossEntropy(loss, lse)
+
+
+def cross_entropy_backward(x, head, targets, lse, dloss, dlse=None, scale: float = 1.0, input_grad: bool = True,
+                           weight_grad: bool = True, workspace: int = 0, stream=None):
+    """(dx, dhead) of cross_entropy, BF16; None in the place of a gradient that is not asked for. targets and dloss may
+    both be None, and dlse. `workspace`: bytes that a piece of the logits' gradient may take (0: 512 MiB)."""
+    if stream is not None:
+        return _on_stream(stream, cross_entropy_backward, x, head, targets, lse, dloss, dlse, scale, input_grad,
+                          weight_grad, workspace)
+    import torch
+    bf16 = torch.bfloat16
+    ldx = _matrix(x, "x", bf16)
+    rows, width = x.shape
+    _contiguous(head, "head", bf16, None)
+    vocab = head.shape[0]
+    if head.shape[1] != width:
+        raise ValueError(f"head: rows of {width} are needed, got {tuple(head.shape)}")
+    if workspace < 0:
+        raise ValueError(f"workspace: bytes, or 0, are needed, got {workspace}")
+    _vector(lse, "lse", torch.float32, rows)
+    for t, what, dtype in ((targets, "targets", torch.int64), (dloss, "dloss", torch.float32),
+                           (dlse, "dlse", torch.float32)):
+        if t is not None:
+            _vector(t, what, dtype, rows)
+    dx = torch.empty((rows, width), dtype=bf16, device=x.device) if input_grad else None
+    dhead = torch.empty_like(head) if weight_grad else None
+    status = lib().gemm_cross_entropy_backward(x.data_ptr(), head.data_ptr(), _address(targets), lse.data_ptr(),
+                                               _address(dloss), _address(dlse), _address(dx), _address(dhead), rows,
+                                               vocab, width, scale, workspace, _stream(None),
+                                               gemm_cross_entropy_strides_t(ldx, 0) if ldx else None)
+    if status:
+        raise GemmError(status, "gemm_cross_entropy_backward")
+    return dx, dhead

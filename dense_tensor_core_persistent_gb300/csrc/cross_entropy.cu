@@ -1,0 +1,602 @@
+// cross_entropy.cu -- softmax cross entropy of the head's logits against given targets, and its gradient, without
+// storing the logits:
+//
+//   z = X W^T (M x V, FP32),  lse = log sum_j exp(scale z_j),  loss = lse - scale z_target
+//   G = scale ((dloss + dlse) p - dloss 1[target]),  p_j = exp(scale z_j - lse),  dX = G W,  dW = G^T X
+//
+// Forward: the products run on the pair tiles of pair_tile.cuh, and the epilogue reduces a row's 128 (or 64) columns of
+// a tile to their maximum m, the sum of exp(z - m) over the others, and the target's logit where it is among them. A
+// second kernel joins a row's parts in a fixed order. The maximum's own term is exactly 1 and is kept out of the sums,
+// so lse and loss end in log1p and a row that its target dominates keeps its digits.
+//
+// Gradient: for a piece of the vocabulary at a time the logits are computed again, their epilogue turns them into G
+// (BF16, the operand of two products) and pair_gradient.cu's launch takes G to the piece's rows of dW and to dX, whose
+// pieces are added in FP32. A piece is as large as G's workspace may be; fewer pieces are fewer joins and ramps. Not
+// keeping z costs its product a second time: 8 MVK operations where 6 would do with M x V logits in memory.
+//
+// Bound by the tensor cores, for few rows by W's bytes.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+#include <type_traits>
+
+#include "common.cuh"
+#include "host_common.h"
+#include "pair_tile.cuh"
+
+namespace dtcp {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr size_t kLossWorkspace = size_t(512) << 20;  // bytes of G at a time, where the caller gives no limit
+
+struct LossParams : PairParams {
+  float scale;
+  const long long* targets;  // or null
+  int first_col;             // the piece's first column
+  int vocab;
+  // forward
+  float2* parts;     // [blocks of 256 columns][2][rows]: (m, sum of the others)
+  float2* extra;     // [tiles cut in halves][2][rows of a tile]: the second 64 columns of a half
+  float* target_z;   // [rows]
+  int tile_rows;
+  // gradient
+  const float* lse;
+  const float* dloss;  // or null
+  const float* dlse;   // or null
+};
+
+// The place of a tile in its product's order.
+__device__ __forceinline__ int tile_index(const PairProduct& q, int m_blk, int n_blk) {
+  const int group_m = min(q.group_m, q.num_m_blocks);
+  const int g = m_blk / group_m, first = g * group_m, rows = min(q.num_m_blocks - first, group_m);
+  return g * group_m * q.num_n_blocks + n_blk * rows + m_blk - first;
+}
+
+// The maximum of a set of logits and the sum of exp(scale (z - m)) over all of them but one that is the maximum.
+struct SoftmaxPart {
+  float m, others;
+};
+__device__ __forceinline__ SoftmaxPart join(SoftmaxPart a, SoftmaxPart b, float c) {  // c = scale / ln 2
+  if (b.m > a.m) {
+    const SoftmaxPart t = a;
+    a = b;
+    b = t;
+  }
+  // (equal maxima, both minus infinity among them, count 1; a NaN among the others stays one)
+  const float w = a.m == b.m ? 1.0f : ex2_approx((b.m - a.m) * c);
+  return SoftmaxPart{a.m, fmaf(b.others + 1.0f, w, a.others)};
+}
+
+// 32 columns of a row, of which the first `valid` exist.
+__device__ __forceinline__ SoftmaxPart part_of(uint32_t (&v)[32], int valid, float c) {
+  if (valid < 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j >= valid) v[j] = 0xFF800000u;
+  }
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(v[j]));
+  const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  float sum[4] = {};
+  int equal = -1;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float z = __uint_as_float(v[j]);
+    const float e = ex2_approx((z - m) * c);
+    const bool is_top = z == m;
+    sum[j & 3] += is_top ? 0.0f : e;
+    equal += is_top;
+  }
+  return SoftmaxPart{m, static_cast<float>(equal) + ((sum[0] + sum[1]) + (sum[2] + sum[3]))};
+}
+
+__device__ __forceinline__ float pick(const uint32_t (&v)[32], int i) {
+  uint32_t r = v[0];
+#pragma unroll
+  for (int j = 1; j < 32; ++j) r = i == j ? v[j] : r;
+  return __uint_as_float(r);
+}
+
+// One row of the forward epilogue: chunks of 32 columns, then where the result goes.
+struct LossRow {
+  long long target;  // -1: none
+  SoftmaxPart part;
+  float c;
+  __device__ __forceinline__ void begin(const LossParams& p, int row) {
+    target = p.targets != nullptr && row < p.main.rows ? p.targets[row] : -1;
+    part = SoftmaxPart{-INFINITY, -1.0f};  // an empty set: joined to another it adds (-1 + 1) exp(-inf) = 0
+    c = p.scale * kLog2e;
+  }
+  __device__ __forceinline__ void chunk(const LossParams& p, uint32_t (&v)[32], int row, int col) {
+    const long long t = target - col;
+    if (t >= 0 && t < 32 && target < p.vocab) p.target_z[row] = pick(v, static_cast<int>(t));
+    part = join(part_of(v, p.main.cols - col, c), part, c);
+  }
+  __device__ __forceinline__ void end(const LossParams& p, const PairItem& item, int h, int row) {
+    if (row >= p.main.rows) return;
+    float2* to = p.parts + (static_cast<long long>(item.n_blk) * 2 + (item.half < 0 ? h : item.half)) * p.main.rows + row;
+    if (item.half >= 0 && h == 1) {
+      const int i = tile_index(p.main, item.m_blk, item.n_blk) - (p.main.num_tiles - p.main.split_tiles);
+      to = p.extra + (static_cast<long long>(i) * 2 + item.half) * p.tile_rows + (row - item.m_blk * p.tile_rows);
+    }
+    *to = make_float2(part.m, part.others);
+  }
+};
+
+// One row of the gradient's epilogue: logits become G.
+struct GradRow {
+  float lse, softmax, onehot, scale;
+  long long target;
+  bool dead;  // no gradient reaches the row: G is 0 whatever its logits are
+  __device__ __forceinline__ void begin(const LossParams& p, int row) {
+    target = -1;
+    lse = softmax = onehot = 0.0f;
+    scale = p.scale;
+    if (row < p.main.rows) {
+      const long long t = p.targets != nullptr ? p.targets[row] : -1;
+      lse = p.lse[row];
+      if (t >= 0 && p.dloss != nullptr) {
+        onehot = t < p.vocab ? p.dloss[row] : __int_as_float(0x7FC00000);
+        target = t - p.first_col;
+      }
+      softmax = onehot + (p.dlse != nullptr ? p.dlse[row] : 0.0f);
+    }
+    dead = onehot == 0.0f && softmax == 0.0f;
+    softmax *= scale;
+    onehot *= scale;
+  }
+  __device__ __forceinline__ void chunk(uint32_t (&v)[32], int col) const {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float e = ex2_approx(fmaf(__uint_as_float(v[j]), scale, -lse) * kLog2e) * softmax;
+      v[j] = __float_as_uint(dead ? 0.0f : e);
+    }
+    const long long t = target - col;
+    if (t >= 0 && t < 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (t == j) v[j] = __float_as_uint(__uint_as_float(v[j]) - onehot);
+    }
+  }
+};
+
+template <bool GRADIENT>
+__global__ void __launch_bounds__(PairLayout::NUM_THREADS, 1)
+    loss_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ LossParams p) {
+  using L = PairLayout;
+  pair_cta<kPairRows>(maps, p, [&](const PairCta& c) {
+    const uint32_t bar_tfull = c.base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 16;
+    const uint32_t q = c.warp & 3u;  // this warp may access TMEM lanes 32q .. 32q+31
+    const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
+    const uint32_t epi = c.warp - L::EPI_WARP0;
+    const int h = static_cast<int>(epi >> 2);  // its half of the columns
+    const int rows = p.main.rows, cols = p.main.cols;
+    PairStaging st{c.base + L::OFF_EPI + epi * kPairStagingBytes, 0u, false};
+    PairItem item;
+    for (int it = 0; pair_item(p, c.cluster_idx, c.num_clusters, it, item); ++it) {
+      const int width = item.half >= 0 ? L::BLOCK_N / 4 : L::BLOCK_N / 2;  // columns of this warp
+      const int col0 = item.n_blk * L::BLOCK_N + (item.half > 0 ? 2 * width : 0) + h * width;
+      const uint32_t slot = static_cast<uint32_t>(it) & 1u;
+      const int row0 = item.m_blk * L::TILE_M + static_cast<int>(c.rank) * L::CTA_M + static_cast<int>(q) * 32;
+      const int row = row0 + static_cast<int>(c.lane);
+      typename std::conditional<GRADIENT, GradRow, LossRow>::type r;
+      r.begin(p, row);  // (while the MMAs run)
+      if (!wait_phase_warp(bar_tfull + 8 * slot, (static_cast<uint32_t>(it) >> 1) & 1u, c.wctx,
+                           status_code(kRoleEpilogue, slot)))
+        break;
+      tc_fence_after_sync();
+      const uint32_t taddr = c.tmem_base + ((q * 32u) << 16) + slot * L::ACC_COLS + static_cast<uint32_t>(h * width);
+      if (row0 < rows) {
+#pragma unroll 1
+        for (int k = 0; k < width; k += 32) {
+          const int col = col0 + k;
+          if (col >= cols) break;
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(taddr + k, v);
+          tmem_ld_wait();
+          if constexpr (GRADIENT) {
+            r.chunk(v, col);
+            pair_store(st, c.lane, &maps.c0, v, col, row0, false);
+          } else {
+            r.chunk(p, v, row, col);
+          }
+        }
+        if constexpr (!GRADIENT) r.end(p, item, h, row);
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (c.lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * slot);  // orders tcgen05 work only
+    }
+    if (c.lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  });
+}
+
+template <bool GRADIENT>
+__global__ void __launch_bounds__(PairWideLayout::NUM_THREADS, 1)
+    loss_wide_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ LossParams p) {
+  using L = PairWideLayout;
+  pair_wide_cta<kPairRows>(maps, p, [&](const PairCta& c) {
+    const uint32_t bar_tfull = c.base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 8 * L::WAVES;
+    const uint32_t q = c.warp & 3u;  // this warp may access TMEM lanes 32q .. 32q+31
+    const uint32_t epi = c.warp - L::EPI_WARP0;
+    const int h = static_cast<int>(epi >> 2);  // its half of a wave's columns
+    const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
+    const int rows = p.main.rows, cols = p.main.cols;
+    PairStaging st{c.base + L::OFF_EPI + epi * L::EPI_BYTES, 0u, false};
+    bool ok = true;
+    PairItem item;
+    for (int it = 0; ok && pair_item(p, c.cluster_idx, c.num_clusters, it, item); ++it) {
+      const int width = item.half >= 0 ? L::BLOCK_N / 4 : L::BLOCK_N / 2;  // columns of this warp
+      const int col0 = item.n_blk * L::BLOCK_N + (item.half > 0 ? 2 * width : 0) + h * width;
+#pragma unroll 1
+      for (int w = 0; w < L::WAVES; ++w) {
+        const int row0 =
+            item.m_blk * L::TILE_M + static_cast<int>(c.rank) * L::CTA_M + w * 128 + static_cast<int>(q) * 32;
+        const int row = row0 + static_cast<int>(c.lane);
+        const bool live = row0 < rows && col0 < cols;
+        typename std::conditional<GRADIENT, GradRow, LossRow>::type r;
+        r.begin(p, row);  // (while the MMAs run)
+        if (!__all_sync(0xffffffffu, wait_phase_inline(bar_tfull + 8 * w, static_cast<uint32_t>(it) & 1u, c.wctx,
+                                                       status_code(kRoleEpilogue, w)))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t taddr = c.tmem_base + ((q * 32u) << 16) + static_cast<uint32_t>(w) * L::ACC_COLS +
+                               static_cast<uint32_t>(h * width);
+        uint32_t v[4][32];
+        if (live) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k * 32 < width) tmem_ld_32x32b_x32(taddr + k * 32, v[k]);
+          tmem_ld_wait();
+        }
+        // the wave's columns are read: hand them back to the MMA issuer (leader's barrier)
+        tc_fence_before_sync();
+        __syncwarp();
+        if (c.lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * w);  // orders tcgen05 work only
+        if (row0 >= rows) continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int col = col0 + k * 32;
+          if (k * 32 < width && col < cols) {
+            if constexpr (GRADIENT) {
+              r.chunk(v[k], col);
+              pair_store(st, c.lane, &maps.c0, v[k], col, row0, false);
+            } else {
+              r.chunk(p, v[k], row, col);
+            }
+          }
+        }
+        if constexpr (!GRADIENT) r.end(p, item, h, row);
+      }
+    }
+    if (c.lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  });
+}
+
+// ---------------------------------------------------------------- a row's parts
+
+struct LossJoin {
+  PairProduct q;
+  int tile_rows, vocab;
+  const float2* parts;
+  const float2* extra;
+  const float* target_z;
+  const long long* targets;
+  float* loss;
+  float* lse;
+  float scale;
+};
+
+// A CTA joins 32 rows: a warp takes every 32nd block of columns of all of them, then a row each.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(32 * kJoinWarps) loss_join_kernel(const LossJoin p) {
+  __shared__ float2 seen[kJoinWarps][33];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float c = p.scale * kLog2e;
+  SoftmaxPart part{-INFINITY, -1.0f};
+  {
+    const int row = blockIdx.x * 32 + lane;
+    if (row < p.q.rows) {
+      const int m_blk = row / p.tile_rows;
+#pragma unroll 4
+      for (int n = warp; n < p.q.num_n_blocks; n += kJoinWarps) {
+        const float2* at = p.parts + 2LL * n * p.q.rows + row;
+        const float2 a = at[0], b = at[p.q.rows];
+        part = join(part, SoftmaxPart{a.x, a.y}, c);
+        part = join(part, SoftmaxPart{b.x, b.y}, c);
+        const int i = tile_index(p.q, m_blk, n) - (p.q.num_tiles - p.q.split_tiles);
+        if (i >= 0) {
+          const float2* more = p.extra + 2LL * i * p.tile_rows + (row - m_blk * p.tile_rows);
+          const float2 d = more[0], e = more[p.tile_rows];
+          part = join(part, SoftmaxPart{d.x, d.y}, c);
+          part = join(part, SoftmaxPart{e.x, e.y}, c);
+        }
+      }
+    }
+  }
+  seen[warp][lane] = make_float2(part.m, part.others);
+  __syncthreads();
+  const float2 mine = seen[lane][warp];
+  part = SoftmaxPart{mine.x, mine.y};
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    part = join(part, SoftmaxPart{__shfl_down_sync(0xffffffffu, part.m, o), __shfl_down_sync(0xffffffffu, part.others, o)},
+                c);
+  const int row = blockIdx.x * 32 + warp;
+  if (lane != 0 || row >= p.q.rows) return;
+  if (p.q.num_n_blocks == 0) part = SoftmaxPart{0.0f, static_cast<float>(p.vocab - 1)};  // K == 0: every logit is 0
+  const float rest = log1pf(part.others) + (part.m - part.m);  // (an infinite maximum makes the row NaN)
+  p.lse[row] = fmaf(p.scale, part.m, rest);
+  if (p.loss == nullptr) return;
+  const long long t = p.targets[row];
+  float loss = 0.0f;
+  if (t >= p.vocab) loss = __int_as_float(0x7FC00000);
+  else if (t >= 0) loss = fmaf(p.scale, part.m - (p.q.num_n_blocks == 0 ? 0.0f : p.target_z[row]), rest);
+  p.loss[row] = loss;
+}
+
+// ---------------------------------------------------------------- host side
+
+template <bool GRADIENT>
+int loss_max_clusters(int device, bool wide) {
+  static std::mutex mu;
+  static int cache[64][2] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  if (device < 0 || device >= 64) return 0;
+  int& n = cache[device][wide ? 1 : 0];
+  if (n == 0) {
+    const void* kernel = wide ? reinterpret_cast<const void*>(loss_wide_kernel<GRADIENT>)
+                              : reinterpret_cast<const void*>(loss_kernel<GRADIENT>);
+    n = pair_max_clusters(&kernel, 1, wide);
+  }
+  return n;
+}
+
+bool loss_wide(int M, int N, int K, int wave) {
+  using L = PairLayout;
+  const long long n = ceil_div(N, L::BLOCK_N);
+  return pair_wide_rule(ceil_div(M, L::TILE_M) * n, ceil_div(M, 2 * L::TILE_M) * n, K, wave);
+}
+
+// X's rows against `cols` rows of W from its row p.first_col on, G (or nothing) to `out`.
+template <bool GRADIENT>
+int loss_launch(LossParams& p, bool wide, const void* X, long long ldx, const void* W, int K, int cols, void* out,
+                long long ldo, int device, const DeviceInfo* info, cudaStream_t stream) {
+  const int rows = p.main.rows;
+  PairMaps m;
+  int st = pair_map_in(&m.a0, X, K, rows, ldx, wide ? 64 : 128);
+  if (st == GEMM_OK)
+    st = pair_map_in(&m.b0, static_cast<const uint16_t*>(W) + static_cast<long long>(p.first_col) * K, K, cols, K, 64);
+  m.a1 = m.c0 = m.c1 = m.c2 = m.a0;
+  m.b1 = m.b2 = m.b0;
+  if (GRADIENT && st == GEMM_OK) st = pair_map_out(&m.c0, out, cols, rows, ldo);
+  if (st != GEMM_OK) return st;
+  const int wave = loss_max_clusters<GRADIENT>(device, wide);
+  if (wave <= 0) return GEMM_ERR_LAUNCH;
+  const int clusters = pair_schedule(&p, wide, 2.0, wave, device, info);
+  if (clusters < 0) return -clusters;
+  void* args[] = {&m, &p};
+  return pair_launch(wide ? reinterpret_cast<const void*>(loss_wide_kernel<GRADIENT>)
+                          : reinterpret_cast<const void*>(loss_kernel<GRADIENT>),
+                     args, wide, clusters, stream);
+}
+
+template <class... Params, class... Args>
+int simple_launch(void (*kernel)(Params...), int grid, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_LAUNCH;
+  }
+  count_launch();
+  return GEMM_OK;
+}
+
+bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+struct LossStrides {
+  long long x, dx;
+};
+int resolve(const gemm_cross_entropy_strides_t* s, int K, LossStrides* r) {
+  *r = LossStrides{K, K};
+  if (s == nullptr) return GEMM_OK;
+  if (s->x) r->x = s->x;
+  if (s->dx) r->dx = s->dx;
+  return r->x < K || r->dx < K ? GEMM_ERR_INVALID_ARG : GEMM_OK;
+}
+
+bool good_scale(float s) { return s > 0.0f && std::isfinite(s); }
+
+size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+
+}  // namespace
+}  // namespace dtcp
+
+using namespace dtcp;
+
+extern "C" {
+
+int gemm_cross_entropy_piece(int M, int vocab, size_t workspace) {
+  if (M < 0 || vocab < 0) return -GEMM_ERR_INVALID_ARG;
+  if (M == 0 || vocab == 0) return vocab;
+  if (workspace == 0) workspace = kLossWorkspace;
+  const long long most = std::max<long long>(256, static_cast<long long>(std::min<size_t>(workspace, size_t(1) << 50) /
+                                                                         (2 * static_cast<size_t>(M))) / 256 * 256);
+  if (most >= vocab) return vocab;
+  const long long pieces = (vocab + most - 1) / most;  // of about the same size
+  return static_cast<int>(round_up((vocab + pieces - 1) / pieces, 256));
+}
+
+int gemm_cross_entropy(const void* X, const void* W, const long long* targets, float* loss, float* lse, int M, int vocab,
+                       int K, float scale, void* stream, const gemm_cross_entropy_strides_t* strides) {
+  using L = PairLayout;
+  LossStrides ld;
+  if (M < 0 || vocab < 0 || K < 0 || !good_scale(scale) || resolve(strides, K, &ld) != GEMM_OK)
+    return GEMM_ERR_INVALID_ARG;
+  if (M == 0) return GEMM_OK;
+  if (vocab == 0 || lse == nullptr || (targets == nullptr) != (loss == nullptr) ||
+      (K > 0 && (X == nullptr || W == nullptr)))
+    return GEMM_ERR_INVALID_ARG;
+  if (K % 8 != 0 || ld.x % 8 != 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
+  if ((K > 0 && (!aligned(X, 16) || !aligned(W, 16))) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(lse, 4))
+    return GEMM_ERR_MISALIGNED;
+  int device = 0, err = 0;
+  const DeviceInfo* info = current_device_info(&device, &err);
+  if (info == nullptr) return err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  LossJoin j = {};
+  j.q.rows = M;
+  j.tile_rows = 1;
+  j.vocab = vocab;
+  j.targets = targets;
+  j.loss = loss;
+  j.lse = lse;
+  j.scale = scale;
+  const int join_ctas = ceil_div(M, 32);
+  if (K == 0) return simple_launch(loss_join_kernel, join_ctas, 32 * kJoinWarps, s, j);
+  const int wave = loss_max_clusters<false>(device, false);
+  if (wave <= 0) return GEMM_ERR_LAUNCH;
+  const bool wide = loss_wide(M, vocab, K, wave);
+  LossParams p = {};
+  p.tile_rows = wide ? 2 * L::TILE_M : L::TILE_M;
+  int st = pair_plan_product(&p.main, M, vocab, K, wide ? 64 : 128, 1, 1, p.tile_rows, L::BLOCK_N);
+  if (st != GEMM_OK) return st;
+  const size_t parts = size_t(p.main.num_n_blocks) * 2 * M;
+  // (at most half a wave's tiles are cut in halves)
+  const size_t extra = size_t(loss_max_clusters<false>(device, wide)) * p.tile_rows;
+  cudaMemPool_t pool = workspace_pool(device);
+  void* ws = nullptr;
+  if (pool == nullptr ||
+      cudaMallocFromPoolAsync(&ws, (parts + extra) * sizeof(float2) + size_t(M) * 4, pool, s) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_OUT_OF_MEMORY;
+  }
+  p.scale = scale;
+  p.targets = targets;
+  p.vocab = vocab;
+  p.parts = static_cast<float2*>(ws);
+  p.extra = p.parts + parts;
+  p.target_z = reinterpret_cast<float*>(p.extra + extra);
+  st = loss_launch<false>(p, wide, X, ld.x, W, K, vocab, nullptr, 0, device, info, s);
+  if (st == GEMM_OK) {
+    j.q = p.main;
+    j.tile_rows = p.tile_rows;
+    j.parts = p.parts;
+    j.extra = p.extra;
+    j.target_z = p.target_z;
+    st = simple_launch(loss_join_kernel, join_ctas, 32 * kJoinWarps, s, j);
+  }
+  if (cudaFreeAsync(ws, s) != cudaSuccess && st == GEMM_OK) st = GEMM_ERR_LAUNCH;
+  return st;
+}
+
+int gemm_cross_entropy_backward(const void* X, const void* W, const long long* targets, const float* lse,
+                                const float* dloss, const float* dlse, void* dX, void* dW, int M, int vocab, int K,
+                                float scale, size_t workspace, void* stream,
+                                const gemm_cross_entropy_strides_t* strides) {
+  using L = PairLayout;
+  LossStrides ld;
+  if (M < 0 || vocab < 0 || K < 0 || !good_scale(scale) || resolve(strides, K, &ld) != GEMM_OK)
+    return GEMM_ERR_INVALID_ARG;
+  if (vocab == 0 && M > 0) return GEMM_ERR_INVALID_ARG;
+  if ((targets == nullptr) != (dloss == nullptr)) return GEMM_ERR_INVALID_ARG;
+  if ((dX == nullptr && dW == nullptr) || K == 0 || vocab == 0) return GEMM_OK;
+  if (M > 0 && (X == nullptr || W == nullptr || lse == nullptr)) return GEMM_ERR_INVALID_ARG;
+  if (K % 8 != 0 || ld.x % 8 != 0 || ld.dx % 8 != 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(X, 16) || !aligned(W, 16) || !aligned(dX, 16) || !aligned(dW, 16) || !aligned(targets, 8) ||
+      !aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dlse, 4))
+    return GEMM_ERR_MISALIGNED;
+  if (M == 0 && dW == nullptr) return GEMM_OK;
+  int device = 0, err = 0;
+  const DeviceInfo* info = current_device_info(&device, &err);
+  if (info == nullptr) return err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {  // a sum over no rows
+    if (cudaMemsetAsync(dW, 0, size_t(vocab) * K * 2, s) == cudaSuccess) return GEMM_OK;
+    cudaGetLastError();
+    return GEMM_ERR_LAUNCH;
+  }
+  const int piece = gemm_cross_entropy_piece(M, vocab, workspace);
+  const bool pieces = piece < vocab;
+  const long long ldg = static_cast<long long>(round_up(piece, 8));
+  const int wave = loss_max_clusters<true>(device, false);
+  if (wave <= 0) return GEMM_ERR_LAUNCH;
+
+  PairGradient q = {};
+  q.x = X;
+  q.ldg = ldg;
+  q.ldx = ld.x;
+  q.lddx = ld.dx;
+  q.rows = M;
+  q.K = K;
+  q.parts = 1;
+  q.keep_sums = pieces && dX != nullptr;
+  auto at = [&](const void* p, int row) {
+    return static_cast<void*>(const_cast<uint16_t*>(static_cast<const uint16_t*>(p)) + static_cast<long long>(row) * K);
+  };
+  auto select = [&](int first) {  // the piece from column `first` on
+    q.features[0] = q.features[1] = std::min(piece, vocab - first);
+    q.w[0] = at(W, first);
+    q.dx = dX;
+    q.dw[0] = dW != nullptr ? at(dW, first) : nullptr;
+    q.add = first > 0;
+  };
+  select(0);
+  PairGradientPlan plan;
+  int st = pair_gradient_plan(q, device, &plan);
+  if (st != GEMM_OK) return st;
+  const size_t g_bytes = round_up(size_t(M) * ldg * 2, 256);
+  cudaMemPool_t pool = workspace_pool(device);
+  void* ws = nullptr;
+  if (pool == nullptr || cudaMallocFromPoolAsync(&ws, g_bytes + plan.sums * 4, pool, s) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_OUT_OF_MEMORY;
+  }
+  float* const sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + g_bytes);
+  q.g[0] = ws;
+  const int slices = q.most_slices = plan.p.main.slices;
+  const bool join = plan.sums > 0;
+  for (int first = 0; first < vocab && st == GEMM_OK; first += piece) {
+    select(first);
+    LossParams p = {};
+    p.scale = scale;
+    p.targets = targets;
+    p.first_col = first;
+    p.vocab = vocab;
+    p.lse = lse;
+    p.dloss = dloss;
+    p.dlse = dlse;
+    const bool wide = loss_wide(M, q.features[0], K, wave);
+    st = pair_plan_product(&p.main, M, q.features[0], K, wide ? 64 : 128, 1, 1, wide ? 2 * L::TILE_M : L::TILE_M,
+                           L::BLOCK_N);
+    if (st == GEMM_OK)
+      st = loss_launch<true>(p, wide, X, ld.x, W, K, q.features[0], ws, ldg, device, info, s);
+    // (a last piece of fewer slices adds to the first ones)
+    if (st == GEMM_OK && first > 0) st = pair_gradient_plan(q, device, &plan);
+    if (st == GEMM_OK) st = pair_gradient_launch(q, &plan, sums, device, info, s);
+  }
+  if (st == GEMM_OK && join) st = pair_gradient_join(sums, slices, dX, ld.dx, M, K, s);
+  if (cudaFreeAsync(ws, s) != cudaSuccess && st == GEMM_OK) st = GEMM_ERR_LAUNCH;
+  return st;
+}
+
+}  // extern "C"

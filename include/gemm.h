@@ -591,6 +591,54 @@ int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const 
  */
 int gemm_glu_plan(int M, int N, int K, int wave, int* forward, int* backward);
 
+/* Row strides in elements, 0 = contiguous; each is at least K and a multiple of 8. */
+typedef struct {
+  long long x, dx;
+} gemm_cross_entropy_strides_t;
+
+/*
+ * gemm_cross_entropy -- softmax cross entropy of the head's logits, which are never stored:
+ *   z = scale * X W^T (M x vocab, FP32 accumulation),  lse = log sum_j exp(z_j),  loss = lse - z_target.
+ *   X: M x K BF16; W: vocab x K BF16 (row-major, K contiguous).
+ *   targets: M int64. A negative target is a place without one: its loss is 0. A target >= vocab gives NaN. targets and
+ *   loss may both be NULL.
+ *   loss, lse: M FP32.
+ *   scale: an inverse temperature, finite and > 0.
+ * Sums are FP32, relative to the maximum, whose own term is exact: the loss of a row that its target dominates keeps
+ * its digits, and no loss is below 0. An infinity or NaN in a row of X makes that row's outputs NaN.
+ * Constraints: M, vocab, K >= 0; K % 8 == 0; X and W 16-byte aligned. Any M and vocab. M == 0: nothing to do. vocab == 0
+ * with rows: GEMM_ERR_INVALID_ARG. K == 0: every logit is 0.
+ * Two kernel launches, asynchronous on `stream`, and a workspace from the library's stream-ordered pool of 16 bytes for
+ * each row and 256 columns of the vocabulary (and up to 1 MB). The same inputs give the same bits.
+ */
+int gemm_cross_entropy(const void* X, const void* W, const long long* targets, float* loss, float* lse, int M, int vocab,
+                       int K, float scale, void* stream, const gemm_cross_entropy_strides_t* strides);
+
+/*
+ * gemm_cross_entropy_backward -- gradient of loss and lse, in pieces of the vocabulary whose logits are computed again:
+ *   G = bf16_rne(scale * ((dloss + dlse) * p - dloss * 1[target])),  p_j = exp(z_j - lse),
+ *   dX = bf16_rne(G W),  dW = bf16_rne(G^T X),  FP32 accumulation.
+ *   lse: what gemm_cross_entropy wrote; p carries its rounding to FP32, a relative error of up to |lse| 2^-24.
+ *   dloss, dlse: M FP32. targets and dloss may both be NULL, and dlse. A negative target takes no part (its dloss is not
+ *   read into the row); a target >= vocab makes the row of G NaN. A row that no gradient reaches (dloss and dlse 0 or
+ *   absent) has a G of 0 whatever its logits are; its X still takes part in dW as 0 * X and has to be finite.
+ *   dX: M x K, dW: vocab x K, BF16; either may be NULL (not computed).
+ *   workspace: bytes that the piece of G may take, 0 = 512 MiB; gemm_cross_entropy_piece gives the columns of a piece.
+ * Constraints as gemm_cross_entropy; dX and dW 16-byte aligned. M == 0 sets dW to zero.
+ * Two kernel launches a piece. Where dX needs FP32 sums (several pieces, or few tiles and so slices of its sum) one more
+ * launch, and 4 K bytes more of workspace for each row (M rounded up to a multiple of 32) and slice, of which there are up
+ * to 8. The workspace comes from the library's stream-ordered pool. The same inputs give the same bits.
+ */
+int gemm_cross_entropy_backward(const void* X, const void* W, const long long* targets, const float* lse,
+                                const float* dloss, const float* dlse, void* dX, void* dW, int M, int vocab, int K,
+                                float scale, size_t workspace, void* stream,
+                                const gemm_cross_entropy_strides_t* strides);
+
+/* Columns of the vocabulary that gemm_cross_entropy_backward takes at a time: all of them where their G fits into
+ * `workspace` bytes (0 = the default), else a multiple of 256, at least 256. -GEMM_ERR_INVALID_ARG for a negative size.
+ * Host evaluation, no GPU needed. */
+int gemm_cross_entropy_piece(int M, int vocab, size_t workspace);
+
 #ifdef __cplusplus
 }
 #endif

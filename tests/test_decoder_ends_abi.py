@@ -1,0 +1,77 @@
+"""Argument checks of the operators at a decoder's ends (no GPU needed: refusals come before any device use)."""
+import pytest
+import torch
+
+import dense_tensor_core_persistent_gb300 as g
+from dense_tensor_core_persistent_gb300 import build as gbuild
+
+BAD, SHAPE, ALIGN = g.GEMM_ERR_INVALID_ARG, g.GEMM_ERR_UNSUPPORTED_SHAPE, g.GEMM_ERR_MISALIGNED
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    gbuild.build()
+
+
+def loss(x=16, w=16, t=16, loss=16, lse=16, M=2, V=5, K=8, scale=1.0, strides=None):
+    return g.lib().gemm_cross_entropy(x, w, t, loss, lse, M, V, K, scale, 0, strides)
+
+
+def loss_backward(x=16, w=16, t=16, lse=16, dloss=16, dlse=16, dx=16, dw=16, M=2, V=5, K=8, scale=1.0, ws=0, strides=None):
+    return g.lib().gemm_cross_entropy_backward(x, w, t, lse, dloss, dlse, dx, dw, M, V, K, scale, ws, 0, strides)
+
+
+def test_cross_entropy_refusals():
+    assert loss(M=0, x=0, w=0, lse=0) == g.GEMM_OK
+    assert loss(M=-1) == BAD and loss(V=-1) == BAD and loss(K=-8) == BAD and loss(V=0) == BAD
+    assert loss(x=0) == BAD and loss(w=0) == BAD and loss(lse=0) == BAD
+    assert loss(t=0) == BAD and loss(loss=0) == BAD  # one without the other
+    assert loss(K=12) == SHAPE
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert loss(scale=scale) == BAD
+    assert loss(x=24) == ALIGN and loss(w=8) == ALIGN and loss(t=20) == ALIGN and loss(lse=18) == ALIGN
+    assert loss(strides=g.gemm_cross_entropy_strides_t(4, 0)) == BAD
+    assert loss(strides=g.gemm_cross_entropy_strides_t(12, 0)) == SHAPE
+
+
+def test_cross_entropy_backward_refusals():
+    assert loss_backward(dx=0, dw=0) == g.GEMM_OK  # nothing asked for
+    assert loss_backward(M=0, dw=0) == g.GEMM_OK and loss_backward(K=0) == g.GEMM_OK
+    assert loss_backward(M=-1) == BAD and loss_backward(V=-1) == BAD and loss_backward(V=0) == BAD
+    assert loss_backward(t=0) == BAD and loss_backward(dloss=0) == BAD  # one without the other
+    assert loss_backward(x=0) == BAD and loss_backward(w=0) == BAD and loss_backward(lse=0) == BAD
+    assert loss_backward(K=4) == SHAPE and loss_backward(scale=0.0) == BAD
+    assert loss_backward(strides=g.gemm_cross_entropy_strides_t(0, 12)) == SHAPE
+    assert loss_backward(strides=g.gemm_cross_entropy_strides_t(0, 4)) == BAD
+    assert loss_backward(dx=8) == ALIGN and loss_backward(dw=8) == ALIGN and loss_backward(dlse=18) == ALIGN
+    assert loss_backward(dloss=17) == ALIGN and loss_backward(t=20) == ALIGN
+
+
+def test_cross_entropy_piece():
+    assert g.cross_entropy_piece(4096, 50000) == 50000  # G fits
+    assert g.cross_entropy_piece(4096, 131072) == 65536
+    assert g.cross_entropy_piece(1, 131072) == 131072 and g.cross_entropy_piece(0, 7) == 7
+    assert g.cross_entropy_piece(1 << 20, 131072) == 256  # never less than a tile
+    for M, V, ws in ((300, 8005, 2 * 300 * 1000), (7, 3000, 1), (5000, 262144, 1 << 27)):
+        piece = g.cross_entropy_piece(M, V, ws)
+        assert piece % 256 == 0 and (piece == 256 or 2 * M * piece <= ws)
+    for bad in ((-1, 5), (5, -1)):
+        with pytest.raises(g.GemmError):
+            g.cross_entropy_piece(*bad)
+
+
+def test_binding_refuses_tensors_that_are_not_what_it_takes():
+    x = torch.zeros(2, 32, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="x:"):
+        g.cross_entropy(x, x)  # not on a GPU
+    with pytest.raises(ValueError, match="x:"):
+        g.cross_entropy(None, x)
+    with pytest.raises(ValueError, match="x:"):
+        g.cross_entropy_backward(None, x, None, None, None)
+
+
+def test_no_device_is_reported():
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert loss() == g.GEMM_ERR_NO_DEVICE
+    assert loss_backward() == g.GEMM_ERR_NO_DEVICE
