@@ -46,6 +46,7 @@ EXPORTS = (
     "gemm_bf16_plan", "gemm_clc_rule", "gemm_nvfp4_plan", "gemm_bf16_wide_rule",
     "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_token_logprobs", "gemm_token_logprobs_backward",
     "gemm_glu_bf16", "gemm_glu_e4m3", "gemm_glu_bf16_backward", "gemm_glu_plan",
+    "gemm_layer_norm", "gemm_layer_norm_backward",
     "gemm_cross_entropy", "gemm_cross_entropy_backward", "gemm_cross_entropy_piece",
 )
 
@@ -235,6 +236,11 @@ def lib() -> ctypes.CDLL:
         l.gemm_glu_bf16_backward.restype = I
         l.gemm_glu_plan.argtypes = [I, I, I, I, ctypes.POINTER(I), ctypes.POINTER(I)]
         l.gemm_glu_plan.restype = I
+        NS, NB = ctypes.POINTER(gemm_norm_strides_t), ctypes.POINTER(gemm_norm_backward_strides_t)
+        l.gemm_layer_norm.argtypes = [P, P, P, P, P, P, P, P, P, I, I, F, I, P, NS]
+        l.gemm_layer_norm.restype = I
+        l.gemm_layer_norm_backward.argtypes = [P, P, P, P, P, P, P, P, P, I, I, P, NB]
+        l.gemm_layer_norm_backward.restype = I
         CS = ctypes.POINTER(gemm_cross_entropy_strides_t)
         l.gemm_cross_entropy.argtypes = [P, P, P, P, P, I, I, I, F, P, CS]
         l.gemm_cross_entropy.restype = I
@@ -507,6 +513,22 @@ def glu_plan(M: int, N: int, K: int, wave: int = 76) -> tuple[int, int]:
     return fwd.value, bwd.value
 
 
+def gemm_layer_norm(X, R, W, B, S, Y, scales, mean, rstd, rows: int, cols: int, eps: float, fmt: int = GEMM_NORM_BF16,
+                    stream=None, strides: gemm_norm_strides_t | None = None) -> None:
+    """s = bf16(X + R), Y = (s - mean) / sqrt(var + eps) * W + B in one of three formats; see include/gemm.h."""
+    _check(lib().gemm_layer_norm(_ptr(X), _ptr(R), _ptr(W), _ptr(B), _ptr(S), _ptr(Y), _ptr(scales), _ptr(mean),
+                                 _ptr(rstd), rows, cols, eps, fmt, _stream(stream), _byref_or_null(strides)),
+           "gemm_layer_norm")
+
+
+def gemm_layer_norm_backward(dY, S, W, mean, rstd, dS, dX, dW, dB, rows: int, cols: int, stream=None,
+                             strides: gemm_norm_backward_strides_t | None = None) -> None:
+    """Gradient of gemm_layer_norm's BF16 form; see include/gemm.h."""
+    _check(lib().gemm_layer_norm_backward(_ptr(dY), _ptr(S), _ptr(W), _ptr(mean), _ptr(rstd), _ptr(dS), _ptr(dX),
+                                          _ptr(dW), _ptr(dB), rows, cols, _stream(stream), _byref_or_null(strides)),
+           "gemm_layer_norm_backward")
+
+
 def gemm_cross_entropy(X, W, targets, loss, lse, M: int, vocab: int, K: int, scale: float = 1.0, stream=None,
                        strides: gemm_cross_entropy_strides_t | None = None) -> None:
     """Softmax cross entropy of X W^T against targets, without storing the logits; see include/gemm.h."""
@@ -719,6 +741,94 @@ def rms_norm_backward(dy, total, weight, rstd, dsum=None, weight_grad: bool = Tr
     if status:
         raise GemmError(status, "gemm_rms_norm_backward")
     return dx, dw
+
+
+class LayerNormOutput(NamedTuple):
+    """As NormOutput, with the rows' means: mean and rstd are FP32 a row, or None."""
+    y: object
+    scales: object
+    sum: object
+    mean: object
+    rstd: object
+
+
+def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, out: str = "bf16", save: bool = False,
+               inplace: bool = False, stream=None) -> LayerNormOutput:
+    """Layer norm of the rows of x + residual (rows x cols BF16). `out`: "bf16", "e4m3" (scales: FP32 a row) or "nvfp4"
+    (y and scales are A and SFA of matmul_nvfp4). `save`: keep mean and rstd for layer_norm_backward. `inplace`: the sum
+    overwrites `residual`."""
+    if stream is not None:
+        return _on_stream(stream, layer_norm, x, weight, bias, residual, eps, out, save, inplace)
+    import torch
+    fmt = _NORM_FORMATS.get(out)
+    if fmt is None:
+        raise ValueError(f"out: one of {sorted(_NORM_FORMATS)} is needed, got {out!r}")
+    bf16 = torch.bfloat16
+    ldx, ldr, lds = _matrix(x, "x", bf16), 0, 0
+    size = x.shape
+    rows, cols = size
+    total, written = x, None
+    if residual is not None:
+        ldr = _matrix(residual, "residual", bf16, size)
+        if inplace:
+            total, lds = residual, ldr
+        else:
+            total = torch.empty_like(x, memory_format=torch.contiguous_format)
+        written = total
+    elif inplace:
+        raise ValueError("inplace: there is no residual to overwrite")
+    if weight is not None:
+        _vector(weight, "weight", bf16, cols)
+    if bias is not None:
+        _vector(bias, "bias", bf16, cols)
+    scales = mean = rstd = strides = None
+    if fmt == GEMM_NORM_BF16:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif fmt == GEMM_NORM_E4M3:
+        y = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+        scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+    else:
+        y = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=x.device)
+    if save:
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    if ldx or ldr or lds:
+        strides = gemm_norm_strides_t(ldx, ldr, lds, 0)
+    status = lib().gemm_layer_norm(x.data_ptr(), _address(residual), _address(weight), _address(bias), _address(written),
+                                   y.data_ptr(), _address(scales), _address(mean), _address(rstd), rows, cols, eps, fmt,
+                                   _stream(None), _byref_or_null(strides))
+    if status:
+        raise GemmError(status, "gemm_layer_norm")
+    return LayerNormOutput(y, scales, total, mean, rstd)
+
+
+def layer_norm_backward(dy, total, weight, mean, rstd, dsum=None, weight_grads: bool = True, stream=None):
+    """(dx, dweight, dbias) of layer_norm with BF16 output: `total`, `mean` and `rstd` are LayerNormOutput.sum, .mean and
+    .rstd, `dsum` the gradient that reaches the sum past the norm. dx is the gradient of x and of the residual; dweight
+    and dbias are FP32 (None without weight_grads)."""
+    if stream is not None:
+        return _on_stream(stream, layer_norm_backward, dy, total, weight, mean, rstd, dsum, weight_grads)
+    import torch
+    bf16 = torch.bfloat16
+    lds = _matrix(total, "total", bf16)
+    rows, cols = total.shape
+    lddy = _matrix(dy, "dy", bf16, total.shape)
+    ldds = _matrix(dsum, "dsum", bf16, total.shape) if dsum is not None else 0
+    _vector(mean, "mean", torch.float32, rows)
+    _vector(rstd, "rstd", torch.float32, rows)
+    if weight is not None:
+        _vector(weight, "weight", bf16, cols)
+    dx = torch.empty_like(dy, memory_format=torch.contiguous_format)
+    dw = torch.empty(cols, dtype=torch.float32, device=dy.device) if weight_grads else None
+    db = torch.empty_like(dw) if weight_grads else None
+    strides = gemm_norm_backward_strides_t(lddy, lds, ldds, 0) if lddy or lds or ldds else None
+    status = lib().gemm_layer_norm_backward(dy.data_ptr(), total.data_ptr(), _address(weight), mean.data_ptr(),
+                                            rstd.data_ptr(), _address(dsum), dx.data_ptr(), _address(dw), _address(db),
+                                            rows, cols, _stream(None), _byref_or_null(strides))
+    if status:
+        raise GemmError(status, "gemm_layer_norm_backward")
+    return dx, dw, db
 
 
 class TokenLogprobs(NamedTuple):

@@ -1,0 +1,500 @@
+// layer_norm.cu -- layer norm of the rows of a residual stream, with the residual's addition in front and the operand of
+// the next product behind: BF16, E4M3 with one scale a row, or NVFP4 as gemm_nvfp4 reads it; and its gradient.
+//
+//   s = bf16(x + r),  mu = mean(s),  rstd = 1 / sqrt(mean((s - mu)^2) + eps),  y = (s - mu) rstd w + b
+//   xh = (s - mu) rstd,  c1 = mean(dy w),  c2 = mean(dy w xh),  dx = rstd (dy w - c1 - xh c2) + ds,
+//   dw = sum over rows of dy xh,  db = sum over rows of dy
+//
+// The variance is of differences, never a difference of means of squares: a warp takes the mean of its own part of the
+// row and the squares about that; the CTA's warps then exchange (mean, squares) across one barrier and every thread adds
+//   M2 = sum_w M2_w + n_w (mu_w - mu)^2
+// (Chan, Golub and LeVeque's pairwise update), so a row whose mean is far larger than its spread keeps its digits and
+// the row costs one barrier, as in the RMS norm. All sums are FP32; every output is rounded once from FP32.
+//
+// Rows are held, fetched ahead and stored as rms_norm.cu's (norm_common.cuh): both directions are bound by the bytes they
+// move (forward at most 8 per element, gradient 8). The weight's and the bias's gradients are summed in registers by the
+// threads that own the columns, one partial row of each per CTA, which a second kernel adds in a fixed order.
+#include "norm_common.cuh"
+
+namespace dtcp {
+
+struct LayerNormParams {
+  const uint16_t* x;
+  const uint16_t* r;  // or null
+  const uint16_t* w;  // or null: all ones
+  const uint16_t* b;  // or null: zeros
+  uint16_t* s;        // or null
+  void* y;
+  void* scales;
+  float* mean;  // or null
+  float* rstd;  // or null
+  long long ldx, ldr, lds, ldy;
+  int rows, cols;
+  float eps;
+};
+
+struct LayerNormBackwardParams {
+  const uint16_t* dy;
+  const uint16_t* s;
+  const uint16_t* w;
+  const float* mean;
+  const float* rstd;
+  const uint16_t* ds;  // or null
+  uint16_t* dx;
+  float* partial;  // [grid][2][cols]: dw, db; or null
+  long long lddy, lds, ldds, lddx;
+  int rows, cols;
+};
+
+namespace {
+
+// The columns of a group that lie in the row.
+template <int ACCESS>
+__device__ __forceinline__ int group_size(int c, int cols) {
+  if (ACCESS == kAligned) return c < cols ? 8 : 0;
+  return max(0, min(c + 8, cols) - max(c, 0));
+}
+
+// f(j) for the columns of a group that lie in the row.
+template <int ACCESS, class F>
+__device__ __forceinline__ void in_row(int c, int cols, F f) {
+  if (ACCESS == kAligned ? c < cols : whole(c, cols)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f(j);
+  } else if (ACCESS != kAligned && edge(c, cols)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j >= 0 && c + j < cols) f(j);
+  }
+}
+
+template <int VPT, int ACCESS>
+__device__ __forceinline__ void load_bias(uint4 (&b)[VPT], const uint16_t* bias, const int (&col)[VPT], int cols) {
+  if (bias != nullptr) {
+    load_weight<VPT, ACCESS>(b, bias, col, cols);
+  } else {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) b[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// ---------------------------------------------------------------- forward
+
+template <int VPT, int FORMAT, int ACCESS>
+__global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 96)) layer_norm_kernel(const LayerNormParams p) {
+  constexpr int SLOTS = norm_slots(VPT);
+  extern __shared__ uint4 fetched[];  // [SLOTS][2][VPT][threads]
+  __shared__ float2 moments[2][32];   // a warp's mean and squares about it
+  __shared__ float counts[32];        // its columns
+  __shared__ uint32_t slots_max[2][32];
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint4* const mine = fetched + threadIdx.x;
+  const int slot_size = 2 * VPT * static_cast<int>(blockDim.x);
+  pdl_launch_dependents();
+  pdl_wait();
+  const int phase = ACCESS == kAligned ? 0 : row_phase(p.x + blockIdx.x * p.ldx);
+  int col[VPT], size = 0;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    col[k] = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x)) - phase;
+    size += group_size<ACCESS>(col[k], p.cols);
+  }
+  const float count = warp_sum(static_cast<float>(size)), inverse_count = count > 0.0f ? 1.0f / count : 0.0f;
+  if (lane == 0) counts[warp] = count;  // (read behind the first row's barrier)
+  const float inverse_cols = 1.0f / static_cast<float>(p.cols);
+  auto fetch = [&](long long row, int slot) {
+    const uint16_t* const rows[2] = {p.x + row * p.ldx, p.r != nullptr ? p.r + row * p.ldr : nullptr};
+    fetch_rows<2, VPT, ACCESS>(mine + slot * slot_size, rows, col, p.cols, row);
+  };
+  // (groups past the row's end stay zero)
+  for (int i = 0; i < SLOTS * 2 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
+  fetch(blockIdx.x, 0);
+  uint4 w[VPT], b[VPT];
+  load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
+  load_bias<VPT, ACCESS>(b, p.b, col, p.cols);
+  const bool starts = threadIdx.x < 32 && phase != 0;  // the warp with the row's start
+  int parity = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
+    const bool more = row + gridDim.x < p.rows;
+    if (SLOTS == 2 && more) {
+      fetch(row + gridDim.x, parity ^ 1);
+      wait_fetched<2>();
+    } else {
+      wait_fetched<1>();
+    }
+    const uint4* const in = mine + (SLOTS == 2 ? parity * slot_size : 0);
+    uint4 s[VPT];
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      s[k] = in[k * static_cast<int>(blockDim.x)];
+      if (p.r != nullptr) {
+        F8 a = unpack8(s[k]);
+        const F8 e = unpack8(in[(VPT + k) * static_cast<int>(blockDim.x)]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a.v[j] += e.v[j];
+        s[k] = pack8(a);
+      }
+      if (ACCESS == kShared && k == 0 && starts) mask_start(s[0], col[0]);
+      const F8 a = unpack8(s[k]);  // (zeros outside the row)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += a.v[j];
+    }
+    if (SLOTS == 1 && more) fetch(row + gridDim.x, 0);
+    const float warp_mean = warp_sum(sum) * inverse_count;
+    float squares = 0.0f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      if (p.s != nullptr) store8<ACCESS>(p.s + row * p.lds, col[k], p.cols, s[k]);
+      const F8 a = unpack8(s[k]);
+      in_row<ACCESS>(col[k], p.cols, [&](int j) {
+        const float d = a.v[j] - warp_mean;
+        squares = fmaf(d, d, squares);
+      });
+    }
+    squares = warp_sum(squares);
+    if (lane == 0) moments[parity][warp] = make_float2(warp_mean, squares);
+    __syncthreads();
+    const float2 part = lane < warps ? moments[parity][lane] : make_float2(0.0f, 0.0f);
+    const float n = lane < warps ? counts[lane] : 0.0f;
+    const float mean = warp_sum(n * part.x) * inverse_cols;
+    const float off = part.x - mean;
+    const float var = warp_sum(lane < warps ? fmaf(n * off, off, part.y) : 0.0f) * inverse_cols;
+    const float rstd = 1.0f / sqrtf(var + p.eps);
+    if (threadIdx.x == 0) {
+      if (p.mean != nullptr) p.mean[row] = mean;
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    }
+    auto value = [&](int k) {
+      const F8 a = unpack8(s[k]), g = unpack8(w[k]), h = unpack8(b[k]);
+      F8 y = {};
+      in_row<ACCESS>(col[k], p.cols, [&](int j) { y.v[j] = fmaf((a.v[j] - mean) * rstd, g.v[j], h.v[j]); });
+      return y;
+    };
+    norm_output<VPT, FORMAT, ACCESS>(value, p.y, p.ldy, p.scales, row, p.cols, col, slots_max[parity], warps);
+  }
+}
+
+// ---------------------------------------------------------------- backward
+
+// Two sums over the CTA, the same bits in every thread (see block_sum).
+__device__ __forceinline__ float2 block_sum2(float a, float b, float2* slots, int warps) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = make_float2(a, b);
+  __syncthreads();
+  const float2 v = (threadIdx.x & 31) < warps ? slots[threadIdx.x & 31] : make_float2(0.0f, 0.0f);
+  return make_float2(warp_sum(v.x), warp_sum(v.y));
+}
+
+template <int VPT, int ACCESS>
+__global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 96, 128))
+    layer_norm_backward_kernel(const LayerNormBackwardParams p) {
+  constexpr int SLOTS = norm_slots(VPT);
+  extern __shared__ uint4 fetched[];  // [SLOTS][3][VPT][threads]
+  __shared__ float2 slots[2][32];
+  const int warps = blockDim.x >> 5;
+  uint4* const mine = fetched + threadIdx.x;
+  const int slot_size = 3 * VPT * static_cast<int>(blockDim.x);
+  pdl_launch_dependents();
+  pdl_wait();
+  const int phase = ACCESS == kAligned ? 0 : row_phase(p.s + blockIdx.x * p.lds);
+  int col[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k)
+    col[k] = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x)) - phase;
+  auto fetch = [&](long long row, int slot) {
+    const uint16_t* const rows[3] = {p.s + row * p.lds, p.dy + row * p.lddy,
+                                     p.ds != nullptr ? p.ds + row * p.ldds : nullptr};
+    fetch_rows<3, VPT, ACCESS>(mine + slot * slot_size, rows, col, p.cols, row);
+  };
+  // (groups past the row's end stay zero)
+  for (int i = 0; i < SLOTS * 3 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
+  fetch(blockIdx.x, 0);
+  uint4 w[VPT];
+  P8 dw[VPT], db[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[k].v[j] = db[k].v[j] = 0;
+  load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
+  const bool starts = threadIdx.x < 32 && phase != 0;  // the warp with the row's start
+  const float inverse_cols = 1.0f / static_cast<float>(p.cols);
+  float rstd = p.rstd[blockIdx.x], mean = p.mean[blockIdx.x], rstd_next = 0.0f, mean_next = 0.0f;
+  int parity = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
+    const bool more = row + gridDim.x < p.rows;
+    if (more) {
+      rstd_next = p.rstd[row + gridDim.x];
+      mean_next = p.mean[row + gridDim.x];
+    }
+    if (SLOTS == 2 && more) {
+      fetch(row + gridDim.x, parity ^ 1);
+      wait_fetched<2>();
+    } else {
+      wait_fetched<1>();
+    }
+    const uint4* const in = mine + (SLOTS == 2 ? parity * slot_size : 0);
+    const uint64_t r2 = f2_pack(rstd, rstd), m2 = f2_pack(-mean, -mean);
+    uint64_t sum1 = 0, sum2 = 0;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      uint4 v[2] = {in[k * static_cast<int>(blockDim.x)], in[(VPT + k) * static_cast<int>(blockDim.x)]};
+      if (ACCESS == kShared && k == 0 && starts) {
+        mask_start(v[0], col[0]);
+        mask_start(v[1], col[0]);
+      }
+      // (outside the row dy is 0, and so is what it adds)
+      const P8 a = unpack8_pairs(v[0]), d = unpack8_pairs(v[1]), g = unpack8_pairs(w[k]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t xh = f2_mul(f2_add(a.v[j], m2), r2), dyw = f2_mul(d.v[j], g.v[j]);
+        dw[k].v[j] = f2_fma(d.v[j], xh, dw[k].v[j]);
+        db[k].v[j] = f2_add(d.v[j], db[k].v[j]);
+        sum1 = f2_add(dyw, sum1);
+        sum2 = f2_fma(dyw, xh, sum2);
+      }
+    }
+    float lo1, hi1, lo2, hi2;
+    f2_unpack(sum1, lo1, hi1);
+    f2_unpack(sum2, lo2, hi2);
+    const float2 c = block_sum2(lo1 + hi1, lo2 + hi2, slots[parity], warps);
+    const float c1 = c.x * inverse_cols, c2 = c.y * inverse_cols;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const F8 a = unpack8(in[k * static_cast<int>(blockDim.x)]);
+      const F8 d = unpack8(in[(VPT + k) * static_cast<int>(blockDim.x)]), g = unpack8(w[k]);
+      F8 o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xh = (a.v[j] - mean) * rstd;
+        o.v[j] = rstd * (fmaf(d.v[j], g.v[j], -c1) - xh * c2);
+      }
+      if (p.ds != nullptr) {
+        const F8 e = unpack8(in[(2 * VPT + k) * static_cast<int>(blockDim.x)]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.v[j] += e.v[j];
+      }
+      store8<ACCESS>(p.dx + row * p.lddx, col[k], p.cols, pack8(o));
+    }
+    if (SLOTS == 1 && more) fetch(row + gridDim.x, 0);
+    rstd = rstd_next;
+    mean = mean_next;
+  }
+  if (p.partial != nullptr) {  // through shared memory, so that a warp writes 32 columns side by side
+    float* const sums = reinterpret_cast<float*>(fetched);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const P8& v = t == 0 ? dw[k] : db[k];
+        ulonglong2* at = reinterpret_cast<ulonglong2*>(sums + col[k] + phase);
+        at[0] = make_ulonglong2(v.v[0], v.v[1]);
+        at[1] = make_ulonglong2(v.v[2], v.v[3]);
+      }
+      __syncthreads();
+      float* out = p.partial + (2LL * blockIdx.x + t) * p.cols;
+      for (int c = threadIdx.x; c < p.cols; c += blockDim.x) out[c] = sums[c + phase];
+    }
+  }
+}
+
+// dw and db (either may be null) from the partial rows in a fixed order: 32 warps take every 32nd row of 32 columns,
+// then a column each. blockIdx.y: 0 dw, 1 db.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps)
+    layer_norm_sum_kernel(const float* partial, int rows, int cols, float* dw, float* db) {
+  __shared__ float part[kSumWarps][33];
+  pdl_launch_dependents();
+  pdl_wait();
+  float* const out = blockIdx.y == 0 ? dw : db;
+  if (out == nullptr) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.0f;
+  if (c < cols)
+#pragma unroll 8
+    for (int r = warp; r < rows; r += kSumWarps) v += partial[(2LL * r + blockIdx.y) * cols + c];
+  part[warp][lane] = v;
+  __syncthreads();
+  v = warp_sum(part[lane][warp]);  // one column a warp
+  if (lane == 0 && blockIdx.x * 32 + warp < cols) out[blockIdx.x * 32 + warp] = v;
+}
+
+// ---------------------------------------------------------------- host side
+
+template <int FORMAT, int ACCESS>
+const void* forward_kernel(int vpt) {
+  return vpt == 1   ? reinterpret_cast<const void*>(layer_norm_kernel<1, FORMAT, ACCESS>)
+         : vpt == 2 ? reinterpret_cast<const void*>(layer_norm_kernel<2, FORMAT, ACCESS>)
+         : vpt == 4 ? reinterpret_cast<const void*>(layer_norm_kernel<4, FORMAT, ACCESS>)
+                    : reinterpret_cast<const void*>(layer_norm_kernel<8, FORMAT, ACCESS>);
+}
+template <int FORMAT>
+const void* forward_kernel(int vpt, bool aligned, bool shared) {
+  return aligned  ? forward_kernel<FORMAT, kAligned>(vpt)
+         : shared ? forward_kernel<FORMAT, kShared>(vpt)
+                  : forward_kernel<FORMAT, kElements>(vpt);
+}
+
+template <int ACCESS>
+const void* backward_kernel(int vpt) {
+  return vpt == 1   ? reinterpret_cast<const void*>(layer_norm_backward_kernel<1, ACCESS>)
+         : vpt == 2 ? reinterpret_cast<const void*>(layer_norm_backward_kernel<2, ACCESS>)
+         : vpt == 4 ? reinterpret_cast<const void*>(layer_norm_backward_kernel<4, ACCESS>)
+                    : reinterpret_cast<const void*>(layer_norm_backward_kernel<8, ACCESS>);
+}
+
+}  // namespace
+}  // namespace dtcp
+
+using namespace dtcp;
+
+extern "C" {
+
+int gemm_layer_norm(const void* X, const void* R, const void* W, const void* B, void* S, void* Y, void* scales,
+                    float* mean, float* rstd, int rows, int cols, float eps, int format, void* stream,
+                    const gemm_norm_strides_t* strides) {
+  if (rows < 0 || cols < 0 || !(eps >= 0.0f)) return GEMM_ERR_INVALID_ARG;
+  if (format != GEMM_NORM_BF16 && format != GEMM_NORM_E4M3 && format != GEMM_NORM_NVFP4) return GEMM_ERR_INVALID_ARG;
+  if (rows == 0) return GEMM_OK;
+  if (cols == 0) {  // rows without columns: what is one number a row is 0
+    void* const numbers[] = {format == GEMM_NORM_E4M3 ? scales : nullptr, mean, rstd};
+    if (numbers[0] == nullptr && mean == nullptr && rstd == nullptr) return GEMM_OK;
+    for (void* n : numbers)
+      if (misaligned(n, 4)) return GEMM_ERR_MISALIGNED;
+    int device = 0, err = 0;
+    if (current_device_info(&device, &err) == nullptr) return err;
+    int st = GEMM_OK;
+    for (void* n : numbers)
+      if (st == GEMM_OK) st = zero_floats(n, rows, static_cast<cudaStream_t>(stream));
+    return st;
+  }
+  if (X == nullptr || Y == nullptr || (format != GEMM_NORM_BF16 && scales == nullptr)) return GEMM_ERR_INVALID_ARG;
+  if (R != nullptr && S == nullptr) return GEMM_ERR_INVALID_ARG;
+  LayerNormParams p;
+  p.ldx = p.ldr = p.lds = p.ldy = cols;
+  if (strides != nullptr) {
+    if (strides->x) p.ldx = strides->x;
+    if (strides->residual) p.ldr = strides->residual;
+    if (strides->sum) p.lds = strides->sum;
+    if (strides->y) p.ldy = strides->y;
+    if (p.ldx < cols || p.ldr < cols || p.lds < cols || p.ldy < cols) return GEMM_ERR_INVALID_ARG;
+  }
+  if (cols > kNormMaxCols || (format == GEMM_NORM_NVFP4 && (cols % 16 != 0 || p.ldy != cols)))
+    return GEMM_ERR_UNSUPPORTED_SHAPE;
+  if (misaligned(X, 2) || misaligned(R, 2) || misaligned(W, 2) || misaligned(B, 2) || misaligned(S, 2) ||
+      misaligned(mean, 4) || misaligned(rstd, 4) ||
+      misaligned(Y, format == GEMM_NORM_BF16 ? 2 : format == GEMM_NORM_E4M3 ? 1 : 4) ||
+      misaligned(scales, format == GEMM_NORM_E4M3 ? 4 : 1))
+    return GEMM_ERR_MISALIGNED;
+  p.x = static_cast<const uint16_t*>(X);
+  p.r = static_cast<const uint16_t*>(R);
+  p.w = static_cast<const uint16_t*>(W);
+  p.b = static_cast<const uint16_t*>(B);
+  p.s = static_cast<uint16_t*>(S);
+  p.y = Y;
+  p.scales = scales;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.rows = rows;
+  p.cols = cols;
+  p.eps = eps;
+  const RowPlace place(X, p.ldx, 2);
+  bool shared = (R == nullptr || RowPlace(R, p.ldr, 2) == place) && (S == nullptr || RowPlace(S, p.lds, 2) == place);
+  if (format == GEMM_NORM_BF16) shared = shared && RowPlace(Y, p.ldy, 2) == place;
+  if (format == GEMM_NORM_E4M3) shared = shared && RowPlace(Y, p.ldy, 1) == place;  // (8-byte vectors of codes)
+  const bool aligned = shared && place.aligned() && cols % 8 == 0 && !misaligned(W, 16) && !misaligned(B, 16);
+  if (format == GEMM_NORM_NVFP4 && !aligned) return GEMM_ERR_MISALIGNED;
+  int device = 0, err = 0;
+  const DeviceInfo* info = current_device_info(&device, &err);
+  if (info == nullptr) return err;
+  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned);
+  const void* kernel = format == GEMM_NORM_NVFP4  ? forward_kernel<GEMM_NORM_NVFP4, kAligned>(shape.vpt)
+                       : format == GEMM_NORM_E4M3 ? forward_kernel<GEMM_NORM_E4M3>(shape.vpt, aligned, shared)
+                                                  : forward_kernel<GEMM_NORM_BF16>(shape.vpt, aligned, shared);
+  void* args[] = {&p};
+  const int smem = norm_smem(shape, 2);
+  const int grid = norm_grid(kernel, rows, shape.threads, smem, info->num_sms);
+  if (grid == 0) return GEMM_ERR_LAUNCH;
+  return norm_launch(kernel, dim3(grid), shape.threads, smem, static_cast<cudaStream_t>(stream), args);
+}
+
+int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const float* mean, const float* rstd,
+                             const void* dS, void* dX, float* dW, float* dB, int rows, int cols, void* stream,
+                             const gemm_norm_backward_strides_t* strides) {
+  if (rows < 0 || cols < 0) return GEMM_ERR_INVALID_ARG;
+  if (cols == 0) return GEMM_OK;
+  if (rows > 0 && (dY == nullptr || S == nullptr || mean == nullptr || rstd == nullptr || dX == nullptr))
+    return GEMM_ERR_INVALID_ARG;
+  LayerNormBackwardParams p;
+  p.lddy = p.lds = p.ldds = p.lddx = cols;
+  if (strides != nullptr) {
+    if (strides->dy) p.lddy = strides->dy;
+    if (strides->sum) p.lds = strides->sum;
+    if (strides->dsum) p.ldds = strides->dsum;
+    if (strides->dx) p.lddx = strides->dx;
+    if (p.lddy < cols || p.lds < cols || p.ldds < cols || p.lddx < cols) return GEMM_ERR_INVALID_ARG;
+  }
+  if (cols > kNormMaxCols) return GEMM_ERR_UNSUPPORTED_SHAPE;
+  if (misaligned(dY, 2) || misaligned(S, 2) || misaligned(W, 2) || misaligned(mean, 4) || misaligned(rstd, 4) ||
+      misaligned(dS, 2) || misaligned(dX, 2) || misaligned(dW, 4) || misaligned(dB, 4))
+    return GEMM_ERR_MISALIGNED;
+  const bool sums = dW != nullptr || dB != nullptr;
+  if (rows == 0 && !sums) return GEMM_OK;
+  int device = 0, err = 0;
+  const DeviceInfo* info = current_device_info(&device, &err);
+  if (info == nullptr) return err;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {  // the sums over no rows
+    const int rc = zero_floats(dW, cols, st);
+    return rc != GEMM_OK ? rc : zero_floats(dB, cols, st);
+  }
+  p.dy = static_cast<const uint16_t*>(dY);
+  p.s = static_cast<const uint16_t*>(S);
+  p.w = static_cast<const uint16_t*>(W);
+  p.mean = mean;
+  p.rstd = rstd;
+  p.ds = static_cast<const uint16_t*>(dS);
+  p.dx = static_cast<uint16_t*>(dX);
+  p.partial = nullptr;
+  p.rows = rows;
+  p.cols = cols;
+  const RowPlace place(S, p.lds, 2);
+  const bool shared = RowPlace(dY, p.lddy, 2) == place && (dS == nullptr || RowPlace(dS, p.ldds, 2) == place) &&
+                      RowPlace(dX, p.lddx, 2) == place;
+  const bool aligned = shared && place.aligned() && cols % 8 == 0 && !misaligned(W, 16);
+  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned);
+  const void* kernel = aligned  ? backward_kernel<kAligned>(shape.vpt)
+                       : shared ? backward_kernel<kShared>(shape.vpt)
+                                : backward_kernel<kElements>(shape.vpt);
+  const int smem = norm_smem(shape, 3);
+  const int grid = norm_grid(kernel, rows, shape.threads, smem, info->num_sms);
+  if (grid == 0) return GEMM_ERR_LAUNCH;
+  void* ws = nullptr;
+  if (sums) {
+    cudaMemPool_t pool = workspace_pool(device);
+    if (pool == nullptr ||
+        cudaMallocFromPoolAsync(&ws, static_cast<size_t>(grid) * 2 * cols * 4, pool, st) != cudaSuccess) {
+      cudaGetLastError();
+      return GEMM_ERR_OUT_OF_MEMORY;
+    }
+    p.partial = static_cast<float*>(ws);
+  }
+  void* args[] = {&p};
+  int rc = norm_launch(kernel, dim3(grid), shape.threads, smem, st, args);
+  if (ws != nullptr) {
+    if (rc == GEMM_OK) {
+      const float* partial = p.partial;
+      int partial_rows = grid;
+      void* sum_args[] = {&partial, &partial_rows, &cols, &dW, &dB};
+      rc = norm_launch(reinterpret_cast<const void*>(layer_norm_sum_kernel), dim3(ceil_div(cols, 32), 2), 32 * kSumWarps,
+                       0, st, sum_args);
+    }
+    if (cudaFreeAsync(ws, st) != cudaSuccess && rc == GEMM_OK) rc = GEMM_ERR_LAUNCH;
+  }
+  return rc;
+}
+
+}  // extern "C"

@@ -489,6 +489,36 @@ int gemm_rms_norm(const void* X, const void* R, const void* W, void* S, void* Y,
 int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const float* rstd, const void* dS, void* dX,
                            float* dW, int rows, int cols, void* stream, const gemm_norm_backward_strides_t* strides);
 
+/*
+ * gemm_layer_norm -- layer norm of each row of a residual stream:
+ *   s = bf16_rne(X + R),  mu = mean(s),  rstd = 1 / sqrt(mean((s - mu)^2) + eps),  y = (s - mu) * rstd * W + B,
+ * in FP32 from the rounded s, y rounded once to the output format. Arguments, formats, roundings, strides, alignments
+ * and limits are those of gemm_rms_norm, and
+ *   B: cols BF16, or NULL (zeros); NVFP4: 16-byte aligned.
+ *   mean, rstd: rows FP32 for the backward pass, or NULL.
+ * The variance is the mean of squared differences (never below 0): a row whose mean is far larger than its spread keeps
+ * its digits. An infinity or NaN in a row makes the row's outputs NaN, and only that row's. Rows without columns have
+ * mean, rstd and E4M3 scales of 0.
+ * One kernel launch, asynchronous on `stream`; no workspace.
+ */
+int gemm_layer_norm(const void* X, const void* R, const void* W, const void* B, void* S, void* Y, void* scales,
+                    float* mean, float* rstd, int rows, int cols, float eps, int format, void* stream,
+                    const gemm_norm_strides_t* strides);
+
+/*
+ * gemm_layer_norm_backward -- gradient of gemm_layer_norm with BF16 output:
+ *   xh = (S - mean) * rstd,  c1 = mean(dY * W),  c2 = mean(dY * W * xh),
+ *   dX = bf16_rne(rstd * (dY * W - c1 - xh * c2) + dS),
+ *   dW = sum over rows of dY * xh,  dB = sum over rows of dY   (FP32).
+ * Arguments as gemm_rms_norm_backward, with mean and rstd as the forward call wrote them. dW and dB: cols FP32, either
+ * may be NULL (not computed); rows == 0 sets them to zero. dX may be dY, dS or S itself. The same inputs give the same
+ * bits. One kernel launch, and with dW or dB a second one and a workspace from the library's stream-ordered pool: two
+ * rows of cols floats for each CTA of the first.
+ */
+int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const float* mean, const float* rstd,
+                             const void* dS, void* dX, float* dW, float* dB, int rows, int cols, void* stream,
+                             const gemm_norm_backward_strides_t* strides);
+
 /* Types of the logits of gemm_token_logprobs. */
 enum { GEMM_LOGITS_BF16 = 0, GEMM_LOGITS_F32 = 1 };
 

@@ -75,3 +75,56 @@ def test_no_device_is_reported():
         pytest.skip("a GPU is present")
     assert loss() == g.GEMM_ERR_NO_DEVICE
     assert loss_backward() == g.GEMM_ERR_NO_DEVICE
+
+
+def norm(x=16, r=0, w=16, b=16, s=0, y=16, scales=0, mean=0, rstd=0, rows=2, cols=32, eps=1e-5, fmt=0, strides=None):
+    return g.lib().gemm_layer_norm(x, r, w, b, s, y, scales, mean, rstd, rows, cols, eps, fmt, 0, strides)
+
+
+def norm_backward(dy=16, s=16, w=16, mean=16, rstd=16, ds=0, dx=16, dw=16, db=16, rows=2, cols=32, strides=None):
+    return g.lib().gemm_layer_norm_backward(dy, s, w, mean, rstd, ds, dx, dw, db, rows, cols, 0, strides)
+
+
+def test_layer_norm_refusals():
+    assert norm(rows=0, x=0, y=0) == g.GEMM_OK and norm(cols=0, x=0, y=0) == g.GEMM_OK
+    assert norm(rows=-1) == BAD and norm(cols=-1) == BAD
+    assert norm(eps=-1.0) == BAD and norm(eps=float("nan")) == BAD
+    assert norm(fmt=3) == BAD and norm(fmt=-1) == BAD
+    assert norm(x=0) == BAD and norm(y=0) == BAD
+    assert norm(fmt=g.GEMM_NORM_E4M3) == BAD  # no scales
+    assert norm(r=16, s=0) == BAD  # the sum has nowhere to go
+    assert norm(cols=32761) == SHAPE
+    assert norm(fmt=g.GEMM_NORM_NVFP4, scales=16, cols=24) == SHAPE
+    assert norm(fmt=g.GEMM_NORM_NVFP4, scales=16, x=18) == ALIGN and norm(fmt=g.GEMM_NORM_NVFP4, scales=16, b=18) == ALIGN
+    assert norm(x=17) == ALIGN and norm(b=17) == ALIGN and norm(mean=18) == ALIGN and norm(rstd=18) == ALIGN
+    assert norm(cols=0, mean=18) == ALIGN
+    assert norm(strides=g.gemm_norm_strides_t(31, 0, 0, 0)) == BAD
+    assert norm(fmt=g.GEMM_NORM_NVFP4, scales=16, strides=g.gemm_norm_strides_t(0, 0, 0, 48)) == SHAPE
+
+
+def test_layer_norm_backward_refusals():
+    assert norm_backward(cols=0, dy=0) == g.GEMM_OK
+    assert norm_backward(rows=0, dy=0, s=0, mean=0, rstd=0, dx=0, dw=0, db=0) == g.GEMM_OK
+    assert norm_backward(rows=-1) == BAD and norm_backward(cols=-3) == BAD
+    assert norm_backward(dy=0) == BAD and norm_backward(s=0) == BAD and norm_backward(dx=0) == BAD
+    assert norm_backward(mean=0) == BAD and norm_backward(rstd=0) == BAD
+    assert norm_backward(cols=32761) == SHAPE
+    assert norm_backward(dx=17) == ALIGN and norm_backward(dw=18) == ALIGN and norm_backward(db=18) == ALIGN
+    assert norm_backward(strides=g.gemm_norm_backward_strides_t(0, 0, 8, 0)) == BAD
+
+
+def test_layer_norm_binding_refuses():
+    x = torch.zeros(2, 32, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="x:"):
+        g.layer_norm(x)
+    with pytest.raises(ValueError, match="out:"):
+        g.layer_norm(x, out="int8")
+    with pytest.raises(ValueError, match="total:"):
+        g.layer_norm_backward(x, x, None, None, None)
+
+
+def test_layer_norm_without_a_device():
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert norm() == g.GEMM_ERR_NO_DEVICE
+    assert norm_backward() == g.GEMM_ERR_NO_DEVICE
