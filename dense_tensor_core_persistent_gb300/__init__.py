@@ -46,7 +46,7 @@ EXPORTS = (
     "gemm_bf16_plan", "gemm_clc_rule", "gemm_nvfp4_plan", "gemm_bf16_wide_rule",
     "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_token_logprobs", "gemm_token_logprobs_backward",
     "gemm_glu_bf16", "gemm_glu_e4m3", "gemm_glu_bf16_backward", "gemm_glu_plan",
-    "gemm_layer_norm", "gemm_layer_norm_backward",
+    "gemm_layer_norm", "gemm_layer_norm_backward", "gemm_embedding", "gemm_embedding_backward",
     "gemm_cross_entropy", "gemm_cross_entropy_backward", "gemm_cross_entropy_piece",
 )
 
@@ -138,6 +138,10 @@ GEMM_LOGITS_F32 = 1
 GEMM_GLU_SILU = 0
 GEMM_GLU_GELU_TANH = 1
 GEMM_GLU_RELU = 2
+
+
+GEMM_TABLE_BF16 = 0
+GEMM_TABLE_F32 = 1
 
 
 class gemm_glu_strides_t(ctypes.Structure):
@@ -241,6 +245,10 @@ def lib() -> ctypes.CDLL:
         l.gemm_layer_norm.restype = I
         l.gemm_layer_norm_backward.argtypes = [P, P, P, P, P, P, P, P, P, I, I, P, NB]
         l.gemm_layer_norm_backward.restype = I
+        l.gemm_embedding.argtypes = [P, I, P, P, I, I, I, LL, LL, F, P]
+        l.gemm_embedding.restype = I
+        l.gemm_embedding_backward.argtypes = [P, I, P, P, P, I, I, I, I, LL, F, P]
+        l.gemm_embedding_backward.restype = I
         CS = ctypes.POINTER(gemm_cross_entropy_strides_t)
         l.gemm_cross_entropy.argtypes = [P, P, P, P, P, I, I, I, F, P, CS]
         l.gemm_cross_entropy.restype = I
@@ -527,6 +535,20 @@ def gemm_layer_norm_backward(dY, S, W, mean, rstd, dS, dX, dW, dB, rows: int, co
     _check(lib().gemm_layer_norm_backward(_ptr(dY), _ptr(S), _ptr(W), _ptr(mean), _ptr(rstd), _ptr(dS), _ptr(dX),
                                           _ptr(dW), _ptr(dB), rows, cols, _stream(stream), _byref_or_null(strides)),
            "gemm_layer_norm_backward")
+
+
+def gemm_embedding(table, kind: int, tokens, Y, rows: int, vocab: int, cols: int, ldt: int = 0, ldy: int = 0,
+                   scale: float = 1.0, stream=None) -> None:
+    """Y[i] = scale * table[tokens[i]]; see include/gemm.h."""
+    _check(lib().gemm_embedding(_ptr(table), kind, _ptr(tokens), _ptr(Y), rows, vocab, cols, ldt, ldy, scale,
+                                _stream(stream)), "gemm_embedding")
+
+
+def gemm_embedding_backward(dY, dy_kind: int, tokens, base, dtable, table_kind: int, rows: int, vocab: int, cols: int,
+                            ldd: int = 0, scale: float = 1.0, stream=None) -> None:
+    """dtable[v] = base[v] + scale * sum of dY over the positions of token v; see include/gemm.h."""
+    _check(lib().gemm_embedding_backward(_ptr(dY), dy_kind, _ptr(tokens), _ptr(base), _ptr(dtable), table_kind, rows,
+                                         vocab, cols, ldd, scale, _stream(stream)), "gemm_embedding_backward")
 
 
 def gemm_cross_entropy(X, W, targets, loss, lse, M: int, vocab: int, K: int, scale: float = 1.0, stream=None,
@@ -1046,3 +1068,61 @@ def cross_entropy_backward(x, head, targets, lse, dloss, dlse=None, scale: float
     if status:
         raise GemmError(status, "gemm_cross_entropy_backward")
     return dx, dhead
+
+
+def _table_kind(t, what):
+    import torch
+    dtype = getattr(t, "dtype", t)
+    if dtype == torch.bfloat16:
+        return GEMM_TABLE_BF16
+    if dtype == torch.float32:
+        return GEMM_TABLE_F32
+    raise ValueError(f"{what}: BF16 or FP32 is needed, got {dtype}")
+
+
+def embedding(table, tokens, scale: float = 1.0, stream=None):
+    """scale * table[tokens] (table: vocab x width, BF16 or FP32; tokens: rows int64) in the type of the table. A negative
+    token gives zeros, one past the table NaN."""
+    if stream is not None:
+        return _on_stream(stream, embedding, table, tokens, scale)
+    import torch
+    kind = _table_kind(table, "table")
+    ldt = _matrix(table, "table", table.dtype)
+    vocab, width = table.shape
+    rows = 0 if tokens is None else tokens.numel()
+    _vector(tokens, "tokens", torch.int64, rows)
+    y = torch.empty((rows, width), dtype=table.dtype, device=table.device)
+    status = lib().gemm_embedding(table.data_ptr(), kind, tokens.data_ptr(), y.data_ptr(), rows, vocab, width, ldt, 0,
+                                  scale, _stream(None))
+    if status:
+        raise GemmError(status, "gemm_embedding")
+    return y
+
+
+def embedding_backward(dy, tokens, vocab: int, scale: float = 1.0, base=None, inplace: bool = False, dtype=None,
+                       stream=None):
+    """The dense gradient of embedding's table (vocab x width): base + scale * the sum of dy (rows x width, BF16 or FP32)
+    over each token's positions. `base`: what is there already (the head's gradient, with tied weights), zeros if None;
+    `inplace` adds to it. `dtype`: BF16 or FP32, base's or else dy's if None."""
+    if stream is not None:
+        return _on_stream(stream, embedding_backward, dy, tokens, vocab, scale, base, inplace, dtype)
+    import torch
+    dy_kind = _table_kind(dy, "dy")
+    ldd = _matrix(dy, "dy", dy.dtype)
+    rows, width = dy.shape
+    _vector(tokens, "tokens", torch.int64, rows)
+    if vocab < 0:
+        raise ValueError(f"vocab: a size is needed, got {vocab}")
+    if dtype is None:
+        dtype = dy.dtype if base is None else base.dtype
+    kind = _table_kind(dtype, "dtype")
+    if base is not None:
+        _contiguous(base, "base", dtype, (vocab, width))
+    elif inplace:
+        raise ValueError("inplace: there is no base to add to")
+    out = base if inplace else torch.empty((vocab, width), dtype=dtype, device=dy.device)
+    status = lib().gemm_embedding_backward(dy.data_ptr(), dy_kind, tokens.data_ptr(), _address(base), out.data_ptr(), kind,
+                                           rows, vocab, width, ldd, scale, _stream(None))
+    if status:
+        raise GemmError(status, "gemm_embedding_backward")
+    return out

@@ -23,7 +23,8 @@ LIB = os.path.join(LIBDIR, "libdtcp_gemm.so")
 SOURCES = ["api.cu", "gemm_bf16.cu", "gemm_bf16_wide.cu", "gemm_nvfp4.cu", "pack_scales.cu", "noalloc.cu",
            "mma_rate.cu", "rms_norm.cu", "token_logprobs.cu", "glu.cu", "glu_wide.cu",
            "glu_rows.cu", "pair_gradient.cu",
-           "cross_entropy.cu", "layer_norm.cu"]
+           "cross_entropy.cu", "layer_norm.cu",
+           "embedding.cu"]
 HEADERS = ["ptx.cuh", "common.cuh", "schedule.h", "host_common.h", "glu_act.cuh", "glu_common.cuh", "pair_tile.cuh",
            "norm_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

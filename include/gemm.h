@@ -621,6 +621,38 @@ int gemm_glu_bf16_backward(const void* dH, const void* X, const void* Wg, const 
  */
 int gemm_glu_plan(int M, int N, int K, int wave, int* forward, int* backward);
 
+/* Types of an embedding table and of what is read from it or added to it. */
+enum { GEMM_TABLE_BF16 = 0, GEMM_TABLE_F32 = 1 };
+
+/*
+ * gemm_embedding -- rows of an embedding table: Y[i] = round(scale * table[tokens[i]]), FP32 product, rounded once.
+ *   table: vocab x cols of `type`, row stride ldt elements (0 = cols); Y: rows x cols of the same type, row stride ldy
+ *   (0 = cols). Pointers aligned to their element; any cols and stride is taken, rows that start on 16-byte boundaries
+ *   and have a multiple of 8 columns are fastest.
+ *   tokens: rows int64. A negative token is a place without one: its row is 0. A token >= vocab gives a row of NaN.
+ *   scale: finite.
+ * cols <= 4194304. One kernel launch, asynchronous on `stream`; no workspace.
+ */
+int gemm_embedding(const void* table, int type, const long long* tokens, void* Y, int rows, int vocab, int cols,
+                   long long ldt, long long ldy, float scale, void* stream);
+
+/*
+ * gemm_embedding_backward -- gradient of the table, dense:
+ *   dtable[v] = round(base[v] + scale * sum over i with tokens[i] == v of dY[i]),
+ * summed in FP32 in the order of the positions (in runs that are joined in order) and rounded once.
+ *   dY: rows x cols of dy_type, row stride ldd elements (0 = cols), element-aligned.
+ *   base: vocab x cols of table_type, contiguous: what is there already (with tied weights the head's dW, from
+ *   gemm_cross_entropy_backward); NULL: zeros. base may be dtable: then only the rows of given tokens are written.
+ *   dtable: vocab x cols of table_type, contiguous. dtable and base are 16-byte aligned, in place element-aligned.
+ *   tokens: rows int64; a negative token or one >= vocab takes no part (its row of dY is not read).
+ * Constraints: vocab < 2^27, cols <= 4194304, scale finite. rows == 0: dtable is base or zeros.
+ * Up to three kernel launches, asynchronous on `stream`, and a workspace from the library's stream-ordered pool: 16 bytes
+ * a position and 8 cols bytes for each run of positions (of 16 to 256, so that there are about 512 or they are 256
+ * long). The same inputs give the same bits.
+ */
+int gemm_embedding_backward(const void* dY, int dy_type, const long long* tokens, const void* base, void* dtable,
+                            int table_type, int rows, int vocab, int cols, long long ldd, float scale, void* stream);
+
 /* Row strides in elements, 0 = contiguous; each is at least K and a multiple of 8. */
 typedef struct {
   long long x, dx;

@@ -128,3 +128,52 @@ def test_layer_norm_without_a_device():
         pytest.skip("a GPU is present")
     assert norm() == g.GEMM_ERR_NO_DEVICE
     assert norm_backward() == g.GEMM_ERR_NO_DEVICE
+
+
+def lookup(table=16, kind=0, tokens=16, y=16, rows=2, vocab=5, cols=8, ldt=0, ldy=0, scale=1.0):
+    return g.lib().gemm_embedding(table, kind, tokens, y, rows, vocab, cols, ldt, ldy, scale, 0)
+
+
+def table_grad(dy=16, dk=0, tokens=16, base=0, out=16, tk=0, rows=2, vocab=5, cols=8, ldd=0, scale=1.0):
+    return g.lib().gemm_embedding_backward(dy, dk, tokens, base, out, tk, rows, vocab, cols, ldd, scale, 0)
+
+
+def test_embedding_refusals():
+    assert lookup(rows=0, table=0) == g.GEMM_OK and lookup(cols=0) == g.GEMM_OK
+    assert lookup(rows=-1) == BAD and lookup(vocab=-1) == BAD and lookup(cols=-1) == BAD and lookup(kind=2) == BAD
+    assert lookup(table=0) == BAD and lookup(tokens=0) == BAD and lookup(y=0) == BAD
+    assert lookup(ldt=7) == BAD and lookup(ldy=-1) == BAD
+    assert lookup(scale=float("inf")) == BAD and lookup(scale=float("nan")) == BAD
+    assert lookup(cols=(1 << 22) + 1) == SHAPE
+    assert lookup(table=17) == ALIGN and lookup(kind=1, y=18) == ALIGN and lookup(tokens=20) == ALIGN
+
+
+def test_embedding_backward_refusals():
+    assert table_grad(vocab=0, out=0) == g.GEMM_OK and table_grad(cols=0) == g.GEMM_OK
+    assert table_grad(rows=0, base=16, out=16, dy=0) == g.GEMM_OK  # in place, and nothing to add
+    assert table_grad(rows=-1) == BAD and table_grad(vocab=-1) == BAD and table_grad(dk=2) == BAD and table_grad(tk=-1) == BAD
+    assert table_grad(dy=0) == BAD and table_grad(tokens=0) == BAD and table_grad(out=0) == BAD
+    assert table_grad(ldd=7) == BAD and table_grad(scale=float("nan")) == BAD
+    assert table_grad(vocab=1 << 27) == SHAPE and table_grad(cols=(1 << 22) + 1) == SHAPE
+    assert table_grad(dy=17) == ALIGN and table_grad(tokens=4) == ALIGN and table_grad(out=24) == ALIGN
+    assert table_grad(base=24, out=32) == ALIGN and table_grad(base=17, out=17) == ALIGN
+
+
+def test_embedding_binding_refuses():
+    x = torch.zeros(2, 32, dtype=torch.bfloat16)
+    ids = torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError, match="table:"):
+        g.embedding(x, ids)  # not on a GPU
+    with pytest.raises(ValueError, match="table:"):
+        g.embedding(x.half(), ids)
+    with pytest.raises(ValueError, match="dy:"):
+        g.embedding_backward(x, ids, 4)
+    with pytest.raises(ValueError, match="table:"):
+        g.embedding(None, ids)
+
+
+def test_embedding_without_a_device():
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert lookup() == g.GEMM_ERR_NO_DEVICE
+    assert table_grad() == g.GEMM_ERR_NO_DEVICE
