@@ -24,9 +24,9 @@ SOURCES = ["api.cu", "gemm_bf16.cu", "gemm_bf16_wide.cu", "gemm_nvfp4.cu", "pack
            "mma_rate.cu", "rms_norm.cu", "token_logprobs.cu", "glu.cu", "glu_wide.cu",
            "glu_rows.cu", "pair_gradient.cu",
            "cross_entropy.cu", "layer_norm.cu",
-           "embedding.cu"]
+           "embedding.cu", "cross_entropy_rows.cu"]
 HEADERS = ["ptx.cuh", "common.cuh", "schedule.h", "host_common.h", "glu_act.cuh", "glu_common.cuh", "pair_tile.cuh",
-           "norm_common.cuh"]
+           "norm_common.cuh", "loss_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v", "-I", os.path.join(ROOT, "include")]
 

@@ -21,16 +21,13 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
-#include <type_traits>
 
-#include "common.cuh"
-#include "host_common.h"
+#include "loss_common.cuh"
 #include "pair_tile.cuh"
 
 namespace dtcp {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr size_t kLossWorkspace = size_t(512) << 20;  // bytes of G at a time, where the caller gives no limit
 
 struct LossParams : PairParams {
@@ -42,7 +39,6 @@ struct LossParams : PairParams {
   float2* parts;     // [blocks of 256 columns][2][rows]: (m, sum of the others)
   float2* extra;     // [tiles cut in halves][2][rows of a tile]: the second 64 columns of a half
   float* target_z;   // [rows]
-  int tile_rows;
   // gradient
   const float* lse;
   const float* dloss;  // or null
@@ -56,50 +52,34 @@ __device__ __forceinline__ int tile_index(const PairProduct& q, int m_blk, int n
   return g * group_m * q.num_n_blocks + n_blk * rows + m_blk - first;
 }
 
-// The maximum of a set of logits and the sum of exp(scale (z - m)) over all of them but one that is the maximum.
-struct SoftmaxPart {
-  float m, others;
-};
-__device__ __forceinline__ SoftmaxPart join(SoftmaxPart a, SoftmaxPart b, float c) {  // c = scale / ln 2
-  if (b.m > a.m) {
-    const SoftmaxPart t = a;
-    a = b;
-    b = t;
-  }
-  // (equal maxima, both minus infinity among them, count 1; a NaN among the others stays one)
-  const float w = a.m == b.m ? 1.0f : ex2_approx((b.m - a.m) * c);
-  return SoftmaxPart{a.m, fmaf(b.others + 1.0f, w, a.others)};
-}
-
 // 32 columns of a row, of which the first `valid` exist.
-__device__ __forceinline__ SoftmaxPart part_of(uint32_t (&v)[32], int valid, float c) {
+__device__ __forceinline__ SoftmaxPart part_of(float (&v)[32], int valid, float c) {
   if (valid < 32) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (j >= valid) v[j] = 0xFF800000u;
+      if (j >= valid) v[j] = -INFINITY;
   }
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(v[j]));
+  for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
   const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
   float sum[4] = {};
   int equal = -1;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
-    const float z = __uint_as_float(v[j]);
-    const float e = ex2_approx((z - m) * c);
-    const bool is_top = z == m;
+    const float e = ex2_approx((v[j] - m) * c);
+    const bool is_top = v[j] == m;
     sum[j & 3] += is_top ? 0.0f : e;
     equal += is_top;
   }
   return SoftmaxPart{m, static_cast<float>(equal) + ((sum[0] + sum[1]) + (sum[2] + sum[3]))};
 }
 
-__device__ __forceinline__ float pick(const uint32_t (&v)[32], int i) {
-  uint32_t r = v[0];
+__device__ __forceinline__ float pick(const float (&v)[32], int i) {
+  float r = v[0];
 #pragma unroll
   for (int j = 1; j < 32; ++j) r = i == j ? v[j] : r;
-  return __uint_as_float(r);
+  return r;
 }
 
 // One row of the forward epilogue: chunks of 32 columns, then where the result goes.
@@ -112,7 +92,7 @@ struct LossRow {
     part = SoftmaxPart{-INFINITY, -1.0f};  // an empty set: joined to another it adds (-1 + 1) exp(-inf) = 0
     c = p.scale * kLog2e;
   }
-  __device__ __forceinline__ void chunk(const LossParams& p, uint32_t (&v)[32], int row, int col) {
+  __device__ __forceinline__ void chunk(const LossParams& p, float (&v)[32], int row, int col) {
     const long long t = target - col;
     if (t >= 0 && t < 32 && target < p.vocab) p.target_z[row] = pick(v, static_cast<int>(t));
     part = join(part_of(v, p.main.cols - col, c), part, c);
@@ -122,7 +102,8 @@ struct LossRow {
     float2* to = p.parts + (static_cast<long long>(item.n_blk) * 2 + (item.half < 0 ? h : item.half)) * p.main.rows + row;
     if (item.half >= 0 && h == 1) {
       const int i = tile_index(p.main, item.m_blk, item.n_blk) - (p.main.num_tiles - p.main.split_tiles);
-      to = p.extra + (static_cast<long long>(i) * 2 + item.half) * p.tile_rows + (row - item.m_blk * p.tile_rows);
+      constexpr int TILE_M = PairLayout::TILE_M;
+      to = p.extra + (static_cast<long long>(i) * 2 + item.half) * TILE_M + (row - item.m_blk * TILE_M);
     }
     *to = make_float2(part.m, part.others);
   }
@@ -165,9 +146,70 @@ struct GradRow {
   }
 };
 
-template <bool GRADIENT>
+// Forward: a row's 128 columns of a tile (64 of a half) are added over the parts of the depth, then reduced.
 __global__ void __launch_bounds__(PairLayout::NUM_THREADS, 1)
     loss_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ LossParams p) {
+  using L = PairLayout;
+  pair_cta<kPairRowsSums>(maps, p, [&](const PairCta& c) {
+    const uint32_t bar_tfull = c.base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 16;
+    const uint32_t q = c.warp & 3u;  // this warp may access TMEM lanes 32q .. 32q+31
+    const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
+    const int h = static_cast<int>((c.warp - L::EPI_WARP0) >> 2);  // its half of the columns
+    const int rows = p.main.rows, cols = p.main.cols;
+    const int parts = (p.main.k_iters + kPairSumStages - 1) / kPairSumStages;
+    uint32_t acc = 0;
+    bool ok = true;
+    PairItem item;
+    for (int it = 0; ok && pair_item(p, c.cluster_idx, c.num_clusters, it, item); ++it) {
+      const int width = item.half >= 0 ? L::BLOCK_N / 4 : L::BLOCK_N / 2;  // columns of this warp
+      const int col0 = item.n_blk * L::BLOCK_N + (item.half > 0 ? 2 * width : 0) + h * width;
+      const int row0 = item.m_blk * L::TILE_M + static_cast<int>(c.rank) * L::CTA_M + static_cast<int>(q) * 32;
+      const int row = row0 + static_cast<int>(c.lane);
+      const bool live = row0 < rows && col0 < cols;
+      LossRow r;
+      r.begin(p, row);  // (while the MMAs run)
+      float sum[4][32];
+#pragma unroll 1
+      for (int part = 0; part < parts; ++part, ++acc) {
+        const uint32_t slot = acc & 1u;
+        if (!__all_sync(0xffffffffu, wait_phase_inline(bar_tfull + 8 * slot, (acc >> 1) & 1u, c.wctx,
+                                                       status_code(kRoleEpilogue, slot)))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        if (live) {
+          const uint32_t taddr =
+              c.tmem_base + ((q * 32u) << 16) + slot * L::ACC_COLS + static_cast<uint32_t>(h * width);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k * 32 >= width) continue;
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(taddr + k * 32, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              sum[k][j] = part == 0 ? __uint_as_float(v[j]) : sum[k][j] + __uint_as_float(v[j]);
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (c.lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * slot);  // orders tcgen05 work only
+      }
+      if (!ok || row0 >= rows) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int col = col0 + k * 32;
+        if (k * 32 < width && col < cols) r.chunk(p, sum[k], row, col);
+      }
+      r.end(p, item, h, row);
+    }
+  });
+}
+
+// Gradient: a tile's logits become G.
+__global__ void __launch_bounds__(PairLayout::NUM_THREADS, 1)
+    grad_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ LossParams p) {
   using L = PairLayout;
   pair_cta<kPairRows>(maps, p, [&](const PairCta& c) {
     const uint32_t bar_tfull = c.base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 16;
@@ -184,7 +226,7 @@ __global__ void __launch_bounds__(PairLayout::NUM_THREADS, 1)
       const uint32_t slot = static_cast<uint32_t>(it) & 1u;
       const int row0 = item.m_blk * L::TILE_M + static_cast<int>(c.rank) * L::CTA_M + static_cast<int>(q) * 32;
       const int row = row0 + static_cast<int>(c.lane);
-      typename std::conditional<GRADIENT, GradRow, LossRow>::type r;
+      GradRow r;
       r.begin(p, row);  // (while the MMAs run)
       if (!wait_phase_warp(bar_tfull + 8 * slot, (static_cast<uint32_t>(it) >> 1) & 1u, c.wctx,
                            status_code(kRoleEpilogue, slot)))
@@ -199,14 +241,9 @@ __global__ void __launch_bounds__(PairLayout::NUM_THREADS, 1)
           uint32_t v[32];
           tmem_ld_32x32b_x32(taddr + k, v);
           tmem_ld_wait();
-          if constexpr (GRADIENT) {
-            r.chunk(v, col);
-            pair_store(st, c.lane, &maps.c0, v, col, row0, false);
-          } else {
-            r.chunk(p, v, row, col);
-          }
+          r.chunk(v, col);
+          pair_store(st, c.lane, &maps.c0, v, col, row0, false);
         }
-        if constexpr (!GRADIENT) r.end(p, item, h, row);
       }
       tc_fence_before_sync();
       __syncwarp();
@@ -217,9 +254,8 @@ __global__ void __launch_bounds__(PairLayout::NUM_THREADS, 1)
   });
 }
 
-template <bool GRADIENT>
 __global__ void __launch_bounds__(PairWideLayout::NUM_THREADS, 1)
-    loss_wide_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ LossParams p) {
+    grad_wide_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ LossParams p) {
   using L = PairWideLayout;
   pair_wide_cta<kPairRows>(maps, p, [&](const PairCta& c) {
     const uint32_t bar_tfull = c.base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 8 * L::WAVES;
@@ -240,7 +276,7 @@ __global__ void __launch_bounds__(PairWideLayout::NUM_THREADS, 1)
             item.m_blk * L::TILE_M + static_cast<int>(c.rank) * L::CTA_M + w * 128 + static_cast<int>(q) * 32;
         const int row = row0 + static_cast<int>(c.lane);
         const bool live = row0 < rows && col0 < cols;
-        typename std::conditional<GRADIENT, GradRow, LossRow>::type r;
+        GradRow r;
         r.begin(p, row);  // (while the MMAs run)
         if (!__all_sync(0xffffffffu, wait_phase_inline(bar_tfull + 8 * w, static_cast<uint32_t>(it) & 1u, c.wctx,
                                                        status_code(kRoleEpilogue, w)))) {
@@ -266,15 +302,10 @@ __global__ void __launch_bounds__(PairWideLayout::NUM_THREADS, 1)
         for (int k = 0; k < 4; ++k) {
           const int col = col0 + k * 32;
           if (k * 32 < width && col < cols) {
-            if constexpr (GRADIENT) {
-              r.chunk(v[k], col);
-              pair_store(st, c.lane, &maps.c0, v[k], col, row0, false);
-            } else {
-              r.chunk(p, v[k], row, col);
-            }
+            r.chunk(v[k], col);
+            pair_store(st, c.lane, &maps.c0, v[k], col, row0, false);
           }
         }
-        if constexpr (!GRADIENT) r.end(p, item, h, row);
       }
     }
     if (c.lane == 0) bulk_wait_group<0>();
@@ -285,9 +316,9 @@ __global__ void __launch_bounds__(PairWideLayout::NUM_THREADS, 1)
 // ---------------------------------------------------------------- a row's parts
 
 struct LossJoin {
-  PairProduct q;
-  int tile_rows, vocab;
-  const float2* parts;
+  const float2* parts;  // [count][rows]
+  int count, rows, vocab;
+  PairProduct q;  // its tiles cut in halves have more in `extra`
   const float2* extra;
   const float* target_z;
   const long long* targets;
@@ -296,7 +327,7 @@ struct LossJoin {
   float scale;
 };
 
-// A CTA joins 32 rows: a warp takes every 32nd block of columns of all of them, then a row each.
+// A CTA joins 32 rows: a warp takes every 32nd part of all of them, then a row each.
 constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps) loss_join_kernel(const LossJoin p) {
   __shared__ float2 seen[kJoinWarps][33];
@@ -307,18 +338,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) loss_join_kernel(const LossJo
   SoftmaxPart part{-INFINITY, -1.0f};
   {
     const int row = blockIdx.x * 32 + lane;
-    if (row < p.q.rows) {
-      const int m_blk = row / p.tile_rows;
-#pragma unroll 4
-      for (int n = warp; n < p.q.num_n_blocks; n += kJoinWarps) {
-        const float2* at = p.parts + 2LL * n * p.q.rows + row;
-        const float2 a = at[0], b = at[p.q.rows];
+    if (row < p.rows) {
+#pragma unroll 8
+      for (int i = warp; i < p.count; i += kJoinWarps) {
+        const float2 a = p.parts[static_cast<long long>(i) * p.rows + row];
         part = join(part, SoftmaxPart{a.x, a.y}, c);
-        part = join(part, SoftmaxPart{b.x, b.y}, c);
-        const int i = tile_index(p.q, m_blk, n) - (p.q.num_tiles - p.q.split_tiles);
-        if (i >= 0) {
-          const float2* more = p.extra + 2LL * i * p.tile_rows + (row - m_blk * p.tile_rows);
-          const float2 d = more[0], e = more[p.tile_rows];
+      }
+      if (p.q.split_tiles > 0) {
+        constexpr int TILE_M = PairLayout::TILE_M;
+        const int m_blk = row / TILE_M;
+        for (int n = warp; n < p.q.num_n_blocks; n += kJoinWarps) {
+          const int i = tile_index(p.q, m_blk, n) - (p.q.num_tiles - p.q.split_tiles);
+          if (i < 0) continue;
+          const float2* more = p.extra + 2LL * i * TILE_M + (row - m_blk * TILE_M);
+          const float2 d = more[0], e = more[TILE_M];
           part = join(part, SoftmaxPart{d.x, d.y}, c);
           part = join(part, SoftmaxPart{e.x, e.y}, c);
         }
@@ -334,62 +367,65 @@ __global__ void __launch_bounds__(32 * kJoinWarps) loss_join_kernel(const LossJo
     part = join(part, SoftmaxPart{__shfl_down_sync(0xffffffffu, part.m, o), __shfl_down_sync(0xffffffffu, part.others, o)},
                 c);
   const int row = blockIdx.x * 32 + warp;
-  if (lane != 0 || row >= p.q.rows) return;
-  if (p.q.num_n_blocks == 0) part = SoftmaxPart{0.0f, static_cast<float>(p.vocab - 1)};  // K == 0: every logit is 0
+  if (lane != 0 || row >= p.rows) return;
+  if (p.count == 0) part = SoftmaxPart{0.0f, static_cast<float>(p.vocab - 1)};  // K == 0: every logit is 0
   const float rest = log1pf(part.others) + (part.m - part.m);  // (an infinite maximum makes the row NaN)
   p.lse[row] = fmaf(p.scale, part.m, rest);
   if (p.loss == nullptr) return;
   const long long t = p.targets[row];
   float loss = 0.0f;
   if (t >= p.vocab) loss = __int_as_float(0x7FC00000);
-  else if (t >= 0) loss = fmaf(p.scale, part.m - (p.q.num_n_blocks == 0 ? 0.0f : p.target_z[row]), rest);
+  else if (t >= 0) loss = fmaf(p.scale, part.m - (p.count == 0 ? 0.0f : p.target_z[row]), rest);
   p.loss[row] = loss;
 }
 
 // ---------------------------------------------------------------- host side
 
-template <bool GRADIENT>
-int loss_max_clusters(int device, bool wide) {
+enum LossKernel { kLoss = 0, kGrad = 1, kGradWide = 2 };
+const void* loss_kernel_of(LossKernel k) {
+  return k == kLoss   ? reinterpret_cast<const void*>(loss_kernel)
+         : k == kGrad ? reinterpret_cast<const void*>(grad_kernel)
+                      : reinterpret_cast<const void*>(grad_wide_kernel);
+}
+
+int loss_max_clusters(int device, LossKernel k) {
   static std::mutex mu;
-  static int cache[64][2] = {};
+  static int cache[64][3] = {};
   std::lock_guard<std::mutex> lock(mu);
   if (device < 0 || device >= 64) return 0;
-  int& n = cache[device][wide ? 1 : 0];
+  int& n = cache[device][k];
   if (n == 0) {
-    const void* kernel = wide ? reinterpret_cast<const void*>(loss_wide_kernel<GRADIENT>)
-                              : reinterpret_cast<const void*>(loss_kernel<GRADIENT>);
-    n = pair_max_clusters(&kernel, 1, wide);
+    const void* kernel = loss_kernel_of(k);
+    n = pair_max_clusters(&kernel, 1, k == kGradWide);
   }
   return n;
 }
 
-bool loss_wide(int M, int N, int K, int wave) {
+bool grad_wide(int M, int N, int K, int wave) {
   using L = PairLayout;
   const long long n = ceil_div(N, L::BLOCK_N);
   return pair_wide_rule(ceil_div(M, L::TILE_M) * n, ceil_div(M, 2 * L::TILE_M) * n, K, wave);
 }
 
 // X's rows against `cols` rows of W from its row p.first_col on, G (or nothing) to `out`.
-template <bool GRADIENT>
-int loss_launch(LossParams& p, bool wide, const void* X, long long ldx, const void* W, int K, int cols, void* out,
+int loss_launch(LossParams& p, LossKernel k, const void* X, long long ldx, const void* W, int K, int cols, void* out,
                 long long ldo, int device, const DeviceInfo* info, cudaStream_t stream) {
   const int rows = p.main.rows;
+  const bool wide = k == kGradWide;
   PairMaps m;
   int st = pair_map_in(&m.a0, X, K, rows, ldx, wide ? 64 : 128);
   if (st == GEMM_OK)
     st = pair_map_in(&m.b0, static_cast<const uint16_t*>(W) + static_cast<long long>(p.first_col) * K, K, cols, K, 64);
   m.a1 = m.c0 = m.c1 = m.c2 = m.a0;
   m.b1 = m.b2 = m.b0;
-  if (GRADIENT && st == GEMM_OK) st = pair_map_out(&m.c0, out, cols, rows, ldo);
+  if (out != nullptr && st == GEMM_OK) st = pair_map_out(&m.c0, out, cols, rows, ldo);
   if (st != GEMM_OK) return st;
-  const int wave = loss_max_clusters<GRADIENT>(device, wide);
+  const int wave = loss_max_clusters(device, k);
   if (wave <= 0) return GEMM_ERR_LAUNCH;
   const int clusters = pair_schedule(&p, wide, 2.0, wave, device, info);
   if (clusters < 0) return -clusters;
   void* args[] = {&m, &p};
-  return pair_launch(wide ? reinterpret_cast<const void*>(loss_wide_kernel<GRADIENT>)
-                          : reinterpret_cast<const void*>(loss_kernel<GRADIENT>),
-                     args, wide, clusters, stream);
+  return pair_launch(loss_kernel_of(k), args, wide, clusters, stream);
 }
 
 template <class... Params, class... Args>
@@ -464,8 +500,7 @@ int gemm_cross_entropy(const void* X, const void* W, const long long* targets, f
   if (info == nullptr) return err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   LossJoin j = {};
-  j.q.rows = M;
-  j.tile_rows = 1;
+  j.rows = M;
   j.vocab = vocab;
   j.targets = targets;
   j.loss = loss;
@@ -473,16 +508,21 @@ int gemm_cross_entropy(const void* X, const void* W, const long long* targets, f
   j.scale = scale;
   const int join_ctas = ceil_div(M, 32);
   if (K == 0) return simple_launch(loss_join_kernel, join_ctas, 32 * kJoinWarps, s, j);
-  const int wave = loss_max_clusters<false>(device, false);
-  if (wave <= 0) return GEMM_ERR_LAUNCH;
-  const bool wide = loss_wide(M, vocab, K, wave);
+  const bool few = M <= kLossRows;
   LossParams p = {};
-  p.tile_rows = wide ? 2 * L::TILE_M : L::TILE_M;
-  int st = pair_plan_product(&p.main, M, vocab, K, wide ? 64 : 128, 1, 1, p.tile_rows, L::BLOCK_N);
-  if (st != GEMM_OK) return st;
-  const size_t parts = size_t(p.main.num_n_blocks) * 2 * M;
-  // (at most half a wave's tiles are cut in halves)
-  const size_t extra = size_t(loss_max_clusters<false>(device, wide)) * p.tile_rows;
+  int st = GEMM_OK;
+  size_t extra = 0;
+  if (few) {
+    j.count = loss_rows_ctas(vocab, info);
+  } else {
+    const int wave = loss_max_clusters(device, kLoss);
+    if (wave <= 0) return GEMM_ERR_LAUNCH;
+    st = pair_plan_product(&p.main, M, vocab, K, 128, 1, 1, L::TILE_M, L::BLOCK_N);
+    if (st != GEMM_OK) return st;
+    j.count = 2 * p.main.num_n_blocks;
+    extra = size_t(wave) * L::TILE_M;  // (at most half a wave's tiles are cut in halves)
+  }
+  const size_t parts = size_t(j.count) * M;
   cudaMemPool_t pool = workspace_pool(device);
   void* ws = nullptr;
   if (pool == nullptr ||
@@ -490,19 +530,24 @@ int gemm_cross_entropy(const void* X, const void* W, const long long* targets, f
     cudaGetLastError();
     return GEMM_ERR_OUT_OF_MEMORY;
   }
-  p.scale = scale;
-  p.targets = targets;
-  p.vocab = vocab;
-  p.parts = static_cast<float2*>(ws);
-  p.extra = p.parts + parts;
-  p.target_z = reinterpret_cast<float*>(p.extra + extra);
-  st = loss_launch<false>(p, wide, X, ld.x, W, K, vocab, nullptr, 0, device, info, s);
-  if (st == GEMM_OK) {
+  float2* const seen = static_cast<float2*>(ws);
+  float* const target_z = reinterpret_cast<float*>(seen + parts + extra);
+  if (few) {
+    st = run_loss_rows(LossRowsOperands{X, W, targets, seen, target_z, ld.x, M, vocab, K, scale}, device, info, s);
+  } else {
+    p.scale = scale;
+    p.targets = targets;
+    p.vocab = vocab;
+    p.parts = seen;
+    p.extra = seen + parts;
+    p.target_z = target_z;
+    st = loss_launch(p, kLoss, X, ld.x, W, K, vocab, nullptr, 0, device, info, s);
     j.q = p.main;
-    j.tile_rows = p.tile_rows;
-    j.parts = p.parts;
     j.extra = p.extra;
-    j.target_z = p.target_z;
+  }
+  if (st == GEMM_OK) {
+    j.parts = seen;
+    j.target_z = target_z;
     st = simple_launch(loss_join_kernel, join_ctas, 32 * kJoinWarps, s, j);
   }
   if (cudaFreeAsync(ws, s) != cudaSuccess && st == GEMM_OK) st = GEMM_ERR_LAUNCH;
@@ -538,7 +583,7 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
   const int piece = gemm_cross_entropy_piece(M, vocab, workspace);
   const bool pieces = piece < vocab;
   const long long ldg = static_cast<long long>(round_up(piece, 8));
-  const int wave = loss_max_clusters<true>(device, false);
+  const int wave = loss_max_clusters(device, kGrad);
   if (wave <= 0) return GEMM_ERR_LAUNCH;
 
   PairGradient q = {};
@@ -585,11 +630,11 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
     p.lse = lse;
     p.dloss = dloss;
     p.dlse = dlse;
-    const bool wide = loss_wide(M, q.features[0], K, wave);
+    const bool wide = grad_wide(M, q.features[0], K, wave);
     st = pair_plan_product(&p.main, M, q.features[0], K, wide ? 64 : 128, 1, 1, wide ? 2 * L::TILE_M : L::TILE_M,
                            L::BLOCK_N);
     if (st == GEMM_OK)
-      st = loss_launch<true>(p, wide, X, ld.x, W, K, q.features[0], ws, ldg, device, info, s);
+      st = loss_launch(p, wide ? kGradWide : kGrad, X, ld.x, W, K, q.features[0], ws, ldg, device, info, s);
     // (a last piece of fewer slices adds to the first ones)
     if (st == GEMM_OK && first > 0) st = pair_gradient_plan(q, device, &plan);
     if (st == GEMM_OK) st = pair_gradient_launch(q, &plan, sums, device, info, s);

@@ -1,0 +1,43 @@
+// loss_common.cuh -- what the cross entropy's kernels share: partial softmax statistics, and the few-row kernel's launch.
+#pragma once
+
+#include "common.cuh"
+#include "host_common.h"
+
+namespace dtcp {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The maximum of a set of logits and the sum of exp(scale (z - m)) over all of them but one that is the maximum.
+struct SoftmaxPart {
+  float m, others;
+};
+__device__ __forceinline__ SoftmaxPart join(SoftmaxPart a, SoftmaxPart b, float c) {  // c = scale / ln 2
+  if (b.m > a.m) {
+    const SoftmaxPart t = a;
+    a = b;
+    b = t;
+  }
+  // (equal maxima, both minus infinity among them, count 1; a NaN among the others stays one)
+  const float w = a.m == b.m ? 1.0f : ex2_approx((b.m - a.m) * c);
+  return SoftmaxPart{a.m, fmaf(b.others + 1.0f, w, a.others)};
+}
+
+// Up to 64 rows of X against all of W (cross_entropy_rows.cu): parts receives [CTAs][rows], target_z a logit for each row
+// with a target. Measured on GB300 against the pair tile: see there.
+constexpr int kLossRows = 64;
+struct LossRowsOperands {
+  const void* x;
+  const void* w;
+  const long long* targets;  // or null
+  float2* parts;
+  float* target_z;
+  long long ldx;
+  int rows, vocab, depth;
+  float scale;
+};
+// CTAs of the launch (and so parts of a row).
+int loss_rows_ctas(int vocab, const DeviceInfo* info);
+int run_loss_rows(const LossRowsOperands& p, int device, const DeviceInfo* info, cudaStream_t stream);
+
+}  // namespace dtcp

@@ -15,8 +15,14 @@ enum PairMode {
   kPairGated = 0,      // A: rows of X; B: 128 rows of Wg over the same 128 of Wu
   kPairGatedE4m3 = 1,  // the same in E4M3 (256 x 256 tile only)
   kPairGradient = 2,   // main: A = rows of G (K-major), B = W by columns; second: A = G, B = X, both by columns
-  kPairRows = 3        // A: rows of X; B: 256 rows of W
+  kPairRows = 3,       // A: rows of X; B: 256 rows of W
+  kPairRowsSums = 4    // the same, the depth in parts of kPairSumStages stages with an accumulator each, which the epilogue
+                       // adds in FP32 (256 x 256 tile only)
 };
+
+// A tensor-core step cuts what lies below its FP32 accumulator's last place, so a long sum in one accumulator shrinks
+// towards zero by some 2^-25 a step. Results that stay in FP32 are summed in parts of 256.
+constexpr int kPairSumStages = 2;
 
 // The tiles of one product: rows x cols of output, the summed dimension `depth` (dX: of one half) in `k_iters` stages.
 struct PairProduct {
@@ -163,6 +169,9 @@ __device__ __forceinline__ void pair_store(PairStaging& st, uint32_t lane, const
 
 // ---------------------------------------------------------------- the 256 x 256 tile
 
+// Registers per thread of a launch of 384 threads (65536 / 384 -> 168), and after setmaxnreg.
+constexpr int kPairRegsLaunch = 168, kPairRegsLow = 56, kPairRegsEpilogue = 216;
+
 struct PairLayout {
   static constexpr int CG = 2;
   static constexpr int CTA_M = 128, TILE_M = 256;
@@ -238,7 +247,7 @@ __device__ __forceinline__ void pair_producer(const PairParams& p, const PairMap
       }
       first = mb * L::TILE_M + static_cast<int>(rank) * L::CTA_M;
       mn = GRADIENT && item.second;
-    } else if (MODE == kPairRows) {
+    } else if (MODE == kPairRows || MODE == kPairRowsSums) {
       m0 = m1 = &maps.b0;
       first = item.n_blk * L::BLOCK_N + half * (L::BLOCK_N / 2) + static_cast<int>(rank) * 64 * b_boxes;
       mn = false;
@@ -302,7 +311,9 @@ __device__ __forceinline__ void pair_mma(const PairParams& p, uint32_t base, uin
   const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
   const uint64_t a_k = umma_desc_sw128(base + L::OFF_A), a_mn = umma_desc_mn(base + L::OFF_A, L::ATOM_BYTES);
   const uint64_t b0 = GRADIENT ? umma_desc_mn(base + L::OFF_B, L::ATOM_BYTES) : umma_desc_sw128(base + L::OFF_B);
+  constexpr bool SUMS = MODE == kPairRowsSums;
   uint32_t stage = 0, phase = 0;
+  int acc = 0;  // accumulators taken: one an item, or one for each part of its depth
   bool ok = true;
   PairItem item;
   for (int it = 0; ok && pair_item(p, cluster_idx, num_clusters, it, item); ++it) {
@@ -310,16 +321,21 @@ __device__ __forceinline__ void pair_mma(const PairParams& p, uint32_t base, uin
     const uint32_t n = item.half >= 0 ? L::BLOCK_N / 2 : L::BLOCK_N;
     const uint32_t idesc = E4M3 ? idesc_e4m3(256, n) : idesc_mn(256, n, dw, GRADIENT);
     const bool down = (it & 1) != 0;
-    const uint32_t slot = static_cast<uint32_t>(it) & 1u;
     const PairProduct& q = item.second ? p.second : p.main;
     const int part_iters = GRADIENT && !item.second ? q.k_iters / p.parts : q.k_iters;
-    if (!wait_phase_inline(bar_tempty + 8 * slot, ((static_cast<uint32_t>(it) >> 1) & 1u) ^ 1u, wctx,
-                           status_code(kRoleMma, 0x100 + slot))) {
-      ok = false;
-      break;
-    }
-    const uint32_t d = tmem_base + slot * L::ACC_COLS;
+    uint32_t slot = 0, d = 0;
     for (int kb = 0; kb < item.k1 - item.k0; ++kb) {
+      const int in_part = SUMS ? kb % kPairSumStages : kb;
+      if (in_part == 0) {
+        slot = static_cast<uint32_t>(acc) & 1u;
+        d = tmem_base + slot * L::ACC_COLS;
+        if (!wait_phase_inline(bar_tempty + 8 * slot, ((static_cast<uint32_t>(acc) >> 1) & 1u) ^ 1u, wctx,
+                               status_code(kRoleMma, 0x100 + slot))) {
+          ok = false;
+          break;
+        }
+        ++acc;
+      }
       if (!wait_phase_inline(bar_full + 8 * stage, phase, wctx, status_code(kRoleMma, stage))) {
         ok = false;
         break;
@@ -338,8 +354,8 @@ __device__ __forceinline__ void pair_mma(const PairParams& p, uint32_t base, uin
         const uint32_t step_mn = static_cast<uint32_t>(kk) * 2048u;
         const uint64_t ad = umma_desc_advance(a, dw ? step_mn : step_k);
         const uint64_t bd = umma_desc_advance(b, GRADIENT ? step_mn : step_k);
-        if constexpr (E4M3) mma_e4m3_pair(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
-        else mma_f16<2>(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+        if constexpr (E4M3) mma_e4m3_pair(d, ad, bd, idesc, (in_part | kk) != 0 ? 1u : 0u);
+        else mma_f16<2>(d, ad, bd, idesc, (in_part | kk) != 0 ? 1u : 0u);
       };
       if (steps == L::KSTEPS) {
 #pragma unroll
@@ -350,6 +366,8 @@ __device__ __forceinline__ void pair_mma(const PairParams& p, uint32_t base, uin
       mma_commit_pair_multicast(bar_empty + 8 * stage, 0x3);
       stage = stage + 1 == L::STAGES ? 0u : stage + 1;
       phase = stage == 0 ? phase ^ 1u : phase;
+      if (SUMS && in_part + 1 == kPairSumStages && kb + 1 < item.k1 - item.k0)
+        mma_commit_pair_multicast(bar_tfull + 8 * slot, 0x3);
     }
     if (ok) mma_commit_pair_multicast(bar_tfull + 8 * slot, 0x3);
   }
@@ -370,7 +388,18 @@ struct PairCta {
   WaitCtx wctx;
 };
 
-// A CTA of the launch: set-up, roles, teardown. Warps from EPI_WARP0 on run `epilogue`.
+// All roles meet here once their work is done; the MMA warp (which allocated TMEM) frees it.
+__device__ __forceinline__ void pair_teardown(uint32_t warp, uint32_t tmem_base) {
+  tc_fence_before_sync();
+  cluster_sync_all();
+  if (warp == PairLayout::WARP_MMA) {
+    tc_fence_after_sync();
+    tmem_dealloc<2>(tmem_base, PairLayout::TMEM_COLS);
+  }
+}
+
+// A CTA of the launch: set-up, roles, teardown. Warps from EPI_WARP0 on run `epilogue`; where it adds parts in registers,
+// the producer warpgroup gives up some of its own (as on the 512 x 256 tile).
 template <int MODE, class Epilogue>
 __device__ __forceinline__ void pair_cta(const PairMaps& maps, const PairParams& p, Epilogue epilogue) {
   using L = PairLayout;
@@ -411,7 +440,10 @@ __device__ __forceinline__ void pair_cta(const PairMaps& maps, const PairParams&
   pdl_launch_dependents();
   pdl_wait();
 
+  // One branch per role group, each running to the end of the kernel (the code after a change of register limit
+  // belongs to that limit).
   if (warp < L::EPI_WARP0) {
+    if constexpr (MODE == kPairRowsSums) regs_decrease<kPairRegsLow>();
     if (lane == 0) {
       if (warp == L::WARP_A || warp == L::WARP_B)
         pair_producer<MODE>(p, maps, base, rank, warp == L::WARP_A, cluster_idx, num_clusters, wctx);
@@ -419,14 +451,11 @@ __device__ __forceinline__ void pair_cta(const PairMaps& maps, const PairParams&
         pair_mma<MODE>(p, base, tmem_base, cluster_idx, num_clusters, wctx);
     }
     __syncwarp();
+    pair_teardown(warp, tmem_base);
   } else {
+    if constexpr (MODE == kPairRowsSums) regs_increase<kPairRegsEpilogue>();
     epilogue(PairCta{base, tmem_base, warp, lane, rank, cluster_idx, num_clusters, wctx});
-  }
-  tc_fence_before_sync();
-  cluster_sync_all();
-  if (warp == L::WARP_MMA) {
-    tc_fence_after_sync();
-    tmem_dealloc<2>(tmem_base, L::TMEM_COLS);
+    pair_teardown(warp, tmem_base);
   }
 }
 
@@ -444,8 +473,7 @@ struct PairWideLayout {
   static constexpr int ACC_COLS = 256, TMEM_COLS = 512;
   static constexpr int WARP_A = 0, WARP_MMA = 1, WARP_B = 2, EPI_WARP0 = 4, EPI_WARPS = 8;
   static constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-  // registers per thread after setmaxnreg (the launch gives 65536 / 384 -> 168)
-  static constexpr int REGS_LAUNCH = 168, REGS_LOW = 56, REGS_EPI = 216;
+  static constexpr int REGS_LAUNCH = kPairRegsLaunch, REGS_LOW = kPairRegsLow, REGS_EPI = kPairRegsEpilogue;
   static constexpr int EPI_BYTES = kPairStagingBytes;
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = STAGES * A_BYTES;
