@@ -52,27 +52,46 @@ __device__ __forceinline__ int tile_index(const PairProduct& q, int m_blk, int n
   return g * group_m * q.num_n_blocks + n_blk * rows + m_blk - first;
 }
 
-// 32 columns of a row, of which the first `valid` exist.
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if one is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 32 columns of a row, of which the first `valid` exist. A knockout leaves the maximum and its 31 losers, ties among them,
+// so that no element has to be told from the maximum. (v is used up.)
 __device__ __forceinline__ SoftmaxPart part_of(float (&v)[32], int valid, float c) {
   if (valid < 32) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
       if (j >= valid) v[j] = -INFINITY;
   }
-  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
-  const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-  float sum[4] = {};
-  int equal = -1;
+  for (int n = 16; n > 0; n >>= 1) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const float e = ex2_approx((v[j] - m) * c);
-    const bool is_top = v[j] == m;
-    sum[j & 3] += is_top ? 0.0f : e;
-    equal += is_top;
+    for (int j = 0; j < n; ++j) {
+      const float a = v[j], b = v[j + n];
+      v[j] = max_nan(a, b);
+      v[j + n] = min_nan(a, b);
+    }
   }
-  return SoftmaxPart{m, static_cast<float>(equal) + ((sum[0] + sum[1]) + (sum[2] + sum[3]))};
+  const float m = v[0];
+  const uint64_t off = f2_pack(-m, -m), c2 = f2_pack(c, c);
+  uint64_t sum[2] = {0, 0};
+  float e0, e1;
+#pragma unroll
+  for (int j = 2; j < 32; j += 2) {
+    f2_unpack(f2_mul(f2_add(f2_pack(v[j], v[j + 1]), off), c2), e0, e1);
+    sum[(j >> 1) & 1] = f2_add(sum[(j >> 1) & 1], f2_pack(ex2_approx(e0), ex2_approx(e1)));
+  }
+  f2_unpack(f2_add(sum[0], sum[1]), e0, e1);
+  const float others = ex2_approx((v[1] - m) * c) + (e0 + e1);
+  return SoftmaxPart{m, m == -INFINITY ? 0.0f : others};
 }
 
 __device__ __forceinline__ float pick(const float (&v)[32], int i) {
@@ -182,14 +201,17 @@ __global__ void __launch_bounds__(PairLayout::NUM_THREADS, 1)
           const uint32_t taddr =
               c.tmem_base + ((q * 32u) << 16) + slot * L::ACC_COLS + static_cast<uint32_t>(h * width);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 4; k += 2) {
             if (k * 32 >= width) continue;
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(taddr + k * 32, v);
+            uint32_t v[2][32];
+            tmem_ld_32x32b_x32(taddr + k * 32, v[0]);
+            tmem_ld_32x32b_x32(taddr + k * 32 + 32, v[1]);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              sum[k][j] = part == 0 ? __uint_as_float(v[j]) : sum[k][j] + __uint_as_float(v[j]);
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                sum[k + t][j] = part == 0 ? __uint_as_float(v[t][j]) : sum[k + t][j] + __uint_as_float(v[t][j]);
           }
         }
         tc_fence_before_sync();

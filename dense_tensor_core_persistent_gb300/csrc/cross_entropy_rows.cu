@@ -3,7 +3,7 @@
 // W's bytes are the bound, and on the 256-row pair tile most of each MMA would multiply rows that X does not have. Here 128
 // rows of W are the MMA's M and the rows of X its N: accumulator lane v holds the logits of token v, columns are the rows
 // of X. A CTA takes a run of the vocabulary in boxes of 32 tokens, so all CTAs stream the same bytes whatever the
-// vocabulary; its tiles are four boxes, the last one fewer. The depth is summed in parts of 256 (pair_tile.cuh says why),
+// vocabulary; its tiles are four boxes, the last one fewer. The depth is summed in parts of 512 (pair_tile.cuh says why),
 // which the epilogue adds in FP32.
 // The softmax is one pass: a thread keeps, for its lane's tokens and each of its rows of X, the maximum and the sum of the
 // others relative to it through all of the CTA's tiles; lanes, warps and (in the joining kernel) CTAs are joined at the
@@ -34,7 +34,7 @@ template <int X_ROWS>
 struct LossRowsLayout {
   static constexpr int BOX = 32, TILE_BOXES = 4;
   static constexpr int ATOMS = 2, KSTEPS = 8, STAGE_K = 128;  // 128-byte swizzle rows of K per stage; MMAs; elements
-  static constexpr int SUM_STAGES = 2;                        // stages of an accumulator
+  static constexpr int SUM_STAGES = 4;                        // stages of an accumulator
   static constexpr int BOX_BYTES = BOX * 128;
   static constexpr int W_ATOM_BYTES = TILE_BOXES * BOX_BYTES, X_ATOM_BYTES = X_ROWS * 128;
   static constexpr int W_BYTES = ATOMS * W_ATOM_BYTES, X_BYTES = ATOMS * X_ATOM_BYTES;

@@ -21,8 +21,10 @@ enum PairMode {
 };
 
 // A tensor-core step cuts what lies below its FP32 accumulator's last place, so a long sum in one accumulator shrinks
-// towards zero by some 2^-25 a step. Results that stay in FP32 are summed in parts of 256.
-constexpr int kPairSumStages = 2;
+// towards zero by some 2^-25 a step. Results that stay in FP32 are summed in parts of 512: measured on GB300, cross
+// entropy of 1500 x 50001 x 2056 and 4096 x 131072 x 4096 222 and 2256 us with one part (error against 64 bits 1.2e-6),
+// 224 and 2281 with parts of 512, 229 and 2346 with parts of 256 (1.2e-7).
+constexpr int kPairSumStages = 4;
 
 // The tiles of one product: rows x cols of output, the summed dimension `depth` (dX: of one half) in `k_iters` stages.
 struct PairProduct {
