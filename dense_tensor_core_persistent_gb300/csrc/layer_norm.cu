@@ -7,9 +7,8 @@
 //
 // The variance is of differences, never a difference of means of squares: a warp takes the mean of its own part of the
 // row and the squares about that; the CTA's warps then exchange (mean, squares) across one barrier and every thread adds
-//   M2 = sum_w M2_w + n_w (mu_w - mu)^2
-// (Chan, Golub and LeVeque's pairwise update), so a row whose mean is far larger than its spread keeps its digits and
-// the row costs one barrier, as in the RMS norm. All sums are FP32; every output is rounded once from FP32.
+// M2_w + n_w (mu_w - mu)^2 over them (Chan, Golub and LeVeque's update), so a row whose mean is far larger than its spread
+// keeps its digits and the row costs one barrier, as in the RMS norm. All sums are FP32; every output is rounded once from FP32.
 //
 // Rows are held, fetched ahead and stored as rms_norm.cu's (norm_common.cuh): both directions are bound by the bytes they
 // move (forward at most 8 per element, gradient 8). The weight's and the bias's gradients are summed in registers by the
@@ -55,17 +54,37 @@ __device__ __forceinline__ int group_size(int c, int cols) {
   return max(0, min(c + 8, cols) - max(c, 0));
 }
 
-// f(j) for the columns of a group that lie in the row.
-template <int ACCESS, class F>
-__device__ __forceinline__ void in_row(int c, int cols, F f) {
+// Whether a group lies in the row as a whole (then f2), else f1 for its columns that do.
+template <int ACCESS, class Whole, class Part>
+__device__ __forceinline__ void by_group(int c, int cols, Whole whole_group, Part part) {
   if (ACCESS == kAligned ? c < cols : whole(c, cols)) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f(j);
+    whole_group();
   } else if (ACCESS != kAligned && edge(c, cols)) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c + j >= 0 && c + j < cols) f(j);
+      if (c + j >= 0 && c + j < cols) part(j);
   }
+}
+
+__device__ __forceinline__ float pair_sum(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ float element(const P8& v, int j) {
+  float lo, hi;
+  f2_unpack(v.v[j >> 1], lo, hi);
+  return j & 1 ? hi : lo;
+}
+__device__ __forceinline__ uint4 pack8_pairs(const P8& p) {
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float lo, hi;
+    f2_unpack(p.v[j], lo, hi);
+    o[j] = pack2(lo, hi);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <int VPT, int ACCESS>
@@ -123,52 +142,93 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 96)) la
       wait_fetched<1>();
     }
     const uint4* const in = mine + (SLOTS == 2 ? parity * slot_size : 0);
-    uint4 s[VPT];
-    float sum = 0.0f;
+    P8 s[VPT];  // the stream (zeros outside the row), then the results
+    uint64_t sum = 0;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      s[k] = in[k * static_cast<int>(blockDim.x)];
+      uint4 v = in[k * static_cast<int>(blockDim.x)];
       if (p.r != nullptr) {
-        F8 a = unpack8(s[k]);
-        const F8 e = unpack8(in[(VPT + k) * static_cast<int>(blockDim.x)]);
+        P8 a = unpack8_pairs(v);
+        const P8 e = unpack8_pairs(in[(VPT + k) * static_cast<int>(blockDim.x)]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a.v[j] += e.v[j];
-        s[k] = pack8(a);
+        for (int j = 0; j < 4; ++j) a.v[j] = f2_add(a.v[j], e.v[j]);
+        v = pack8_pairs(a);
       }
-      if (ACCESS == kShared && k == 0 && starts) mask_start(s[0], col[0]);
-      const F8 a = unpack8(s[k]);  // (zeros outside the row)
+      if (ACCESS == kShared && k == 0 && starts) mask_start(v, col[0]);
+      if (p.s != nullptr) store8<ACCESS>(p.s + row * p.lds, col[k], p.cols, v);
+      s[k] = unpack8_pairs(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum += a.v[j];
+      for (int j = 0; j < 4; ++j) sum = f2_add(sum, s[k].v[j]);
     }
     if (SLOTS == 1 && more) fetch(row + gridDim.x, 0);
-    const float warp_mean = warp_sum(sum) * inverse_count;
+    const float warp_mean = warp_sum(pair_sum(sum)) * inverse_count;
+    const uint64_t minus = f2_pack(-warp_mean, -warp_mean);
+    uint64_t squares2 = 0;
     float squares = 0.0f;
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      if (p.s != nullptr) store8<ACCESS>(p.s + row * p.lds, col[k], p.cols, s[k]);
-      const F8 a = unpack8(s[k]);
-      in_row<ACCESS>(col[k], p.cols, [&](int j) {
-        const float d = a.v[j] - warp_mean;
-        squares = fmaf(d, d, squares);
-      });
-    }
-    squares = warp_sum(squares);
+    for (int k = 0; k < VPT; ++k)
+      by_group<ACCESS>(
+          col[k], p.cols,
+          [&] {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint64_t d = f2_add(s[k].v[j], minus);
+              squares2 = f2_fma(d, d, squares2);
+            }
+          },
+          [&](int j) {
+            const float d = element(s[k], j) - warp_mean;
+            squares = fmaf(d, d, squares);
+          });
+    squares = warp_sum(squares + pair_sum(squares2));
     if (lane == 0) moments[parity][warp] = make_float2(warp_mean, squares);
     __syncthreads();
-    const float2 part = lane < warps ? moments[parity][lane] : make_float2(0.0f, 0.0f);
-    const float n = lane < warps ? counts[lane] : 0.0f;
-    const float mean = warp_sum(n * part.x) * inverse_cols;
-    const float off = part.x - mean;
-    const float var = warp_sum(lane < warps ? fmaf(n * off, off, part.y) : 0.0f) * inverse_cols;
+    // The warps' moments about the first warp's mean: its distance from the row's mean is at most sqrt(warps) spreads, so
+    // taking it out again costs five bits of the variance's at the worst, and both sums run side by side.
+    const float about = moments[parity][0].x;
+    float first = 0.0f, second = 0.0f;
+    if (lane < warps) {
+      const float2 part = moments[parity][lane];
+      const float off = part.x - about, n_off = counts[lane] * off;
+      first = n_off;
+      second = fmaf(n_off, off, part.y);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      first += __shfl_xor_sync(0xffffffffu, first, o);
+      second += __shfl_xor_sync(0xffffffffu, second, o);
+    }
+    const float shift = first * inverse_cols, mean = about + shift;
+    const float var = fmaxf(fmaf(-first, shift, second), 0.0f) * inverse_cols + (second - second);  // (NaN stays NaN)
     const float rstd = 1.0f / sqrtf(var + p.eps);
     if (threadIdx.x == 0) {
       if (p.mean != nullptr) p.mean[row] = mean;
       if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
+    const uint64_t mean2 = f2_pack(-mean, -mean), rstd2 = f2_pack(rstd, rstd);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const P8 g = unpack8_pairs(w[k]), h = unpack8_pairs(b[k]);
+      P8 y = {};
+      by_group<ACCESS>(
+          col[k], p.cols,
+          [&] {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              y.v[j] = f2_fma(f2_mul(f2_add(s[k].v[j], mean2), rstd2), g.v[j], h.v[j]);
+          },
+          [&](int j) {
+            const float v = fmaf((element(s[k], j) - mean) * rstd, element(g, j), element(h, j));
+            float lo, hi;
+            f2_unpack(y.v[j >> 1], lo, hi);
+            y.v[j >> 1] = j & 1 ? f2_pack(lo, v) : f2_pack(v, hi);
+          });
+      s[k] = y;
+    }
     auto value = [&](int k) {
-      const F8 a = unpack8(s[k]), g = unpack8(w[k]), h = unpack8(b[k]);
-      F8 y = {};
-      in_row<ACCESS>(col[k], p.cols, [&](int j) { y.v[j] = fmaf((a.v[j] - mean) * rstd, g.v[j], h.v[j]); });
+      F8 y;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f2_unpack(s[k].v[j], y.v[2 * j], y.v[2 * j + 1]);
       return y;
     };
     norm_output<VPT, FORMAT, ACCESS>(value, p.y, p.ldy, p.scales, row, p.cols, col, slots_max[parity], warps);
@@ -255,27 +315,24 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 96, 128))
         sum2 = f2_fma(dyw, xh, sum2);
       }
     }
-    float lo1, hi1, lo2, hi2;
-    f2_unpack(sum1, lo1, hi1);
-    f2_unpack(sum2, lo2, hi2);
-    const float2 c = block_sum2(lo1 + hi1, lo2 + hi2, slots[parity], warps);
-    const float c1 = c.x * inverse_cols, c2 = c.y * inverse_cols;
+    const float2 c = block_sum2(pair_sum(sum1), pair_sum(sum2), slots[parity], warps);
+    // rstd (dy w - c1 - xh c2) = rstd dy w + (s - mean) (-rstd^2 c2) - rstd c1
+    const float c1 = c.x * inverse_cols * -rstd, c2 = c.y * inverse_cols * -(rstd * rstd);
+    const uint64_t c1_2 = f2_pack(c1, c1), c2_2 = f2_pack(c2, c2);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const F8 a = unpack8(in[k * static_cast<int>(blockDim.x)]);
-      const F8 d = unpack8(in[(VPT + k) * static_cast<int>(blockDim.x)]), g = unpack8(w[k]);
-      F8 o;
+      const P8 a = unpack8_pairs(in[k * static_cast<int>(blockDim.x)]);
+      const P8 d = unpack8_pairs(in[(VPT + k) * static_cast<int>(blockDim.x)]), g = unpack8_pairs(w[k]);
+      P8 o;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float xh = (a.v[j] - mean) * rstd;
-        o.v[j] = rstd * (fmaf(d.v[j], g.v[j], -c1) - xh * c2);
-      }
+      for (int j = 0; j < 4; ++j)
+        o.v[j] = f2_fma(f2_mul(d.v[j], g.v[j]), r2, f2_fma(f2_add(a.v[j], m2), c2_2, c1_2));
       if (p.ds != nullptr) {
-        const F8 e = unpack8(in[(2 * VPT + k) * static_cast<int>(blockDim.x)]);
+        const P8 e = unpack8_pairs(in[(2 * VPT + k) * static_cast<int>(blockDim.x)]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] += e.v[j];
+        for (int j = 0; j < 4; ++j) o.v[j] = f2_add(o.v[j], e.v[j]);
       }
-      store8<ACCESS>(p.dx + row * p.lddx, col[k], p.cols, pack8(o));
+      store8<ACCESS>(p.dx + row * p.lddx, col[k], p.cols, pack8_pairs(o));
     }
     if (SLOTS == 1 && more) fetch(row + gridDim.x, 0);
     rstd = rstd_next;
