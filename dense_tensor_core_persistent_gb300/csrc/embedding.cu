@@ -6,14 +6,13 @@
 //
 // Gradient: positions are sorted by token (stable, so a token's rows are added in the order of their positions and the
 // same inputs give the same bits), then a CTA takes a run of sorted positions and 8 columns a thread, adds dy's rows in
-// FP32 and writes a token's row once where the token begins and ends inside its run. What a run's first and last token
-// share with other runs is left as FP32 partial rows, which a last kernel adds in order: a token that is a tenth of all
-// positions costs no more than the others.
-// The sort is a least-significant-digit radix sort of 9 bits a pass (two passes up to 262143 tokens) by one cluster of 8
-// CTAs: a warp counts the digits of its part of the list, the CTAs exchange their totals through shared memory, and every
-// warp then knows where its part's digits go. Lists lie in global memory (L2), so their length is not limited. The other
-// CTAs of the same launch meanwhile write the rows that no token will touch, zeros or the base: that is most of the bytes
-// of a dense gradient, and it hides the sort.
+// FP32 and writes each token's row once. Tokens of more than 32 positions are summed by run, into FP32 partial rows that a
+// last kernel adds in order: a token that is a tenth of all positions costs no more than the others.
+// The sort is a least-significant-digit radix sort of up to 10 bits a pass (two passes up to 2^20 tokens) by one cluster of
+// 8 CTAs: a warp counts the digits of its part of the list, the CTAs exchange their totals through shared memory, and every
+// warp then knows where its part's digits go. The lists lie in global memory (L2), so their length is not limited. Beside
+// the sort another kernel writes the whole table, zeros or the base: that is most of the bytes of a dense gradient, and it
+// hides the sort.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -135,28 +134,30 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupPara
   }
 }
 
-// ---------------------------------------------------------------- positions by token, and the rows of no token
+// ---------------------------------------------------------------- positions by token
 
 constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
+constexpr int kMostDigitBits = 10, kMostDigits = 1 << kMostDigitBits;
+constexpr int kSortAhead = 4;  // steps of 32 positions that a warp asks for together
+
+// A position and its token, as they are sorted.
+struct __align__(8) Entry {
+  uint32_t token, pos;
+};
 
 struct SortParams {
   const long long* tokens;
   int count, vocab, passes, digit_bits;
-  int per_warp;      // positions of a warp, a multiple of 32
-  uint32_t* key[2];  // lists of `count` tokens and positions; the last pass writes list 0
-  uint32_t* pos[2];
-  // rows that no token touches
-  void* table;
-  const void* base;  // or null: zeros
-  long long bytes;   // 0: nothing to write
+  int per_warp;    // positions of a warp, a multiple of 32
+  Entry* list[2];  // of `count`; the last pass writes list 0
+  int* spans;      // a count that the sums start from zero
 };
 
 struct SortShared {
-  uint32_t counts[kSortWarps][kDigits];  // of a warp's digits; then where the warp's next one goes, within the CTA's
-  uint32_t totals[kDigits];              // of the CTA (read by the cluster)
-  uint32_t first[kDigits];               // where the CTA's digits go
+  uint32_t totals[kMostDigits];  // of the CTA (read by the cluster)
+  uint32_t first[kMostDigits];   // where the CTA's digits go
   uint32_t sums[kSortWarps];
+  uint32_t counts[1];  // [kSortWarps][digits]: of a warp's digits; then where its next one goes, within the CTA's
 };
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -165,44 +166,60 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
-__device__ void sort_positions(const SortParams& p, SortShared& s) {
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) {
+  extern __shared__ uint4 sort_shared[];
+  SortShared& s = *reinterpret_cast<SortShared*>(sort_shared);
+  pdl_wait();
+  pdl_launch_dependents();  // (only now: the rows' kernel starts beside this one, see there)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = static_cast<int>(cluster_ctarank());
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.spans = 0;
   const long long begin = static_cast<long long>(rank * kSortWarps + warp) * p.per_warp;
   const long long end = min(begin + p.per_warp, static_cast<long long>(p.count));
-  const uint32_t mask = (1u << p.digit_bits) - 1u;
+  const uint32_t digits = 1u << p.digit_bits, mask = digits - 1u;
+  uint32_t* const mine = s.counts + warp * digits;
   for (int pass = 0; pass < p.passes; ++pass) {
     const int from = (p.passes - pass) & 1, shift = pass * p.digit_bits;
-    auto key_at = [&](long long i) -> uint32_t {
-      if (pass > 0) return p.key[from][i];
+    auto entry_at = [&](long long i) -> Entry {
+      if (pass > 0) return p.list[from][i];
       const long long t = p.tokens[i];
       // (no token: behind all others)
-      return t >= 0 && t < p.vocab ? static_cast<uint32_t>(t) : static_cast<uint32_t>(p.vocab);
+      return Entry{t >= 0 && t < p.vocab ? static_cast<uint32_t>(t) : static_cast<uint32_t>(p.vocab),
+                   static_cast<uint32_t>(i)};
     };
-    for (int d = threadIdx.x; d < kSortWarps * kDigits; d += kSortThreads) (&s.counts[0][0])[d] = 0u;
+    auto load = [&](Entry(&e)[kSortAhead], long long i) {
+#pragma unroll
+      for (int a = 0; a < kSortAhead; ++a)
+        e[a] = i + 32 * a + lane < end ? entry_at(i + 32 * a + lane) : Entry{0u, 0u};
+    };
+    Entry e[kSortAhead];
+    for (uint32_t d = threadIdx.x; d < kSortWarps * digits; d += kSortThreads) s.counts[d] = 0u;
     __syncthreads();
-    uint32_t* const mine = s.counts[warp];
-#pragma unroll 4
-    for (long long i = begin; i < end; i += 32) {
-      const bool in = i + lane < end;
-      const uint32_t digit = in ? (key_at(i + lane) >> shift) & mask : kDigits;  // (lanes past the end among themselves)
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      if (in && (same & ((1u << lane) - 1u)) == 0u) mine[digit] += __popc(same);
-      __syncwarp();
+    for (long long i = begin; i < end; i += 32 * kSortAhead) {
+      load(e, i);
+#pragma unroll
+      for (int a = 0; a < kSortAhead; ++a) {
+        if (i + 32 * a >= end) break;
+        const bool in = i + 32 * a + lane < end;
+        const uint32_t digit = in ? (e[a].token >> shift) & mask : digits;  // (lanes past the end among themselves)
+        const uint32_t same = __match_any_sync(0xffffffffu, digit);
+        if (in && (same & ((1u << lane) - 1u)) == 0u) mine[digit] += __popc(same);
+        __syncwarp();
+      }
     }
     __syncthreads();
-    if (threadIdx.x < kDigits) {
+    if (threadIdx.x < digits) {
       uint32_t run = 0;
 #pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = s.counts[w][threadIdx.x];
-        s.counts[w][threadIdx.x] = run;
+        const uint32_t c = s.counts[w * digits + threadIdx.x];
+        s.counts[w * digits + threadIdx.x] = run;
         run += c;
       }
       s.totals[threadIdx.x] = run;
     }
     cluster_sync_all();
     uint32_t all = 0, before = 0;
-    if (threadIdx.x < kDigits) {
+    if (threadIdx.x < digits) {
       const uint32_t at = smem_u32(&s.totals[threadIdx.x]);
 #pragma unroll
       for (int r = 0; r < kSortCtas; ++r) {
@@ -219,73 +236,84 @@ __device__ void sort_positions(const SortParams& p, SortShared& s) {
     }
     if (lane == 31) s.sums[warp] = scan;
     __syncthreads();
-    if (threadIdx.x < kDigits) {
+    if (threadIdx.x < digits) {
       uint32_t lower = 0;
       for (int w = 0; w < warp; ++w) lower += s.sums[w];
       s.first[threadIdx.x] = lower + scan - all + before;
     }
     __syncthreads();
-#pragma unroll 4
-    for (long long i = begin; i < end; i += 32) {
-      const bool in = i + lane < end;
-      const uint32_t key = in ? key_at(i + lane) : 0u;
-      const uint32_t pos = !in ? 0u : pass > 0 ? p.pos[from][i + lane] : static_cast<uint32_t>(i + lane);
-      const uint32_t digit = in ? (key >> shift) & mask : kDigits;
-      const uint32_t same = __match_any_sync(0xffffffffu, digit), lower = same & ((1u << lane) - 1u);
-      uint32_t to = 0;
-      if (in) to = s.first[digit] + mine[digit] + __popc(lower);
-      __syncwarp();
-      if (in) {
-        if (lower == 0u) mine[digit] += __popc(same);
-        p.key[from ^ 1][to] = key;
-        p.pos[from ^ 1][to] = pos;
+    for (long long i = begin; i < end; i += 32 * kSortAhead) {
+      if (p.per_warp > 32 * kSortAhead) load(e, i);  // (else they still are here)
+#pragma unroll
+      for (int a = 0; a < kSortAhead; ++a) {
+        if (i + 32 * a >= end) break;
+        const bool in = i + 32 * a + lane < end;
+        const uint32_t digit = in ? (e[a].token >> shift) & mask : digits;
+        const uint32_t same = __match_any_sync(0xffffffffu, digit), lower = same & ((1u << lane) - 1u);
+        uint32_t to = 0;
+        if (in) to = s.first[digit] + mine[digit] + __popc(lower);
+        __syncwarp();
+        if (in) {
+          if (lower == 0u) mine[digit] += __popc(same);
+          p.list[from ^ 1][to] = e[a];
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
     cluster_sync_all();  // the list is written, and the totals are read
   }
 }
 
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) {
-  extern __shared__ uint4 sort_shared[];
+// ---------------------------------------------------------------- the rows of no token
+
+struct RowsParams {
+  void* table;
+  const void* base;  // or null: zeros
+  long long bytes;
+  int beside;  // it runs beside the sort, which has waited for all work before it
+};
+
+constexpr int kRowsThreads = 512, kRowsVectors = 4;  // of 16 bytes a thread
+
+// The whole table, zeros or the base (rows that tokens touch are written again by the sums). 32 KB a CTA, next to one
+// another: CTAs that come and go write 1 GB at 7.7 TB/s, resident ones that step over it by the grid's size at 6.4.
+// Beside the sort nothing here waits for it but the last CTA, so that the sums, which wait for this grid, find both done.
+__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsParams p) {
+  if (!p.beside) pdl_wait();
   pdl_launch_dependents();
-  pdl_wait();
-  if (blockIdx.x < kSortCtas) {
-    if (p.count > 0) sort_positions(p, *reinterpret_cast<SortShared*>(sort_shared));
-    return;
-  }
-  const long long ctas = gridDim.x - kSortCtas, step = ctas * kSortThreads;
-  const long long first = static_cast<long long>(blockIdx.x - kSortCtas) * kSortThreads + threadIdx.x;
   uint8_t* const to = static_cast<uint8_t*>(p.table);
   const uint8_t* const from = static_cast<const uint8_t*>(p.base);
   const long long vectors = p.bytes / 16;
-  if (from == nullptr) {
-    for (long long v = first; v < vectors; v += step) reinterpret_cast<uint4*>(to)[v] = make_uint4(0u, 0u, 0u, 0u);
-  } else {
-    long long v = first;
-    for (; v + 3 * step < vectors; v += 4 * step) {
-      uint4 r[4];
+  const long long first = static_cast<long long>(blockIdx.x) * kRowsVectors * kRowsThreads + threadIdx.x;
+  uint4 v[kRowsVectors];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) r[j] = __ldcs(reinterpret_cast<const uint4*>(from) + v + j * step);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) reinterpret_cast<uint4*>(to)[v + j * step] = r[j];
-    }
-    for (; v < vectors; v += step) reinterpret_cast<uint4*>(to)[v] = reinterpret_cast<const uint4*>(from)[v];
+  for (int j = 0; j < kRowsVectors; ++j) {
+    const long long i = first + j * kRowsThreads;
+    v[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (from != nullptr && i < vectors) v[j] = __ldcs(reinterpret_cast<const uint4*>(from) + i);
   }
-  const long long at = vectors * 16 + 2 * first;  // (fewer than 16 bytes are left, a multiple of two)
-  if (at < p.bytes)
-    *reinterpret_cast<uint16_t*>(to + at) = from != nullptr ? *reinterpret_cast<const uint16_t*>(from + at) : uint16_t(0);
+#pragma unroll
+  for (int j = 0; j < kRowsVectors; ++j) {
+    const long long i = first + j * kRowsThreads;
+    if (i < vectors) reinterpret_cast<uint4*>(to)[i] = v[j];
+  }
+  if (blockIdx.x + 1 == gridDim.x) {
+    const long long at = vectors * 16 + 2 * threadIdx.x;  // (fewer than 16 bytes are left, a multiple of two)
+    if (at < p.bytes)
+      *reinterpret_cast<uint16_t*>(to + at) = from != nullptr ? *reinterpret_cast<const uint16_t*>(from + at) : uint16_t(0);
+    if (p.beside) pdl_wait();
+  }
 }
 
 // ---------------------------------------------------------------- sums
 
 struct SumParams {
   const void* dy;
-  const uint32_t* key;  // sorted tokens and their positions
-  const uint32_t* pos;
-  const void* base;  // or null
+  const Entry* list;  // sorted
+  const void* base;   // or null
   void* table;
-  float* partial;  // [runs][2][cols]: what a run's first and last token share with others
+  float* partial;  // [runs][2][cols]: a run's parts of a long token that began before it, and of one that goes on behind it
+  int* spans;      // how many long tokens there are, and the runs in which they begin
   long long ldd;
   int count, vocab, cols, run;  // positions, tokens, columns, positions of a run
   float scale;
@@ -293,15 +321,22 @@ struct SumParams {
 
 constexpr int kMaxRun = 256;
 constexpr int kSumThreads = 128;
+constexpr int kLong = 32;  // a token of more positions is long
+template <bool VECTOR>
+constexpr int kSumAhead = VECTOR ? 8 : 4;  // rows of dy that a thread asks for together
 
+// table[token] = base + scale * sum, at this thread's columns.
 template <class TABLE, bool VECTOR>
-__device__ __forceinline__ void write_row(const SumParams& p, const Columns<VECTOR>& at, uint32_t token, const Eight& sum) {
-  const long long row = static_cast<long long>(token) * p.cols;
-  Eight o = {};
-  if (p.base != nullptr) o = at.load(static_cast<const TABLE*>(p.base) + row);
+__device__ __forceinline__ void write_row(const SumParams& p, const Columns<VECTOR>& at, uint32_t token, const Eight& sum,
+                                          Eight base) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o.v[j] = fmaf(p.scale, sum.v[j], o.v[j]);
-  at.store(static_cast<TABLE*>(p.table) + row, o);
+  for (int j = 0; j < 8; ++j) base.v[j] = fmaf(p.scale, sum.v[j], base.v[j]);
+  at.store(static_cast<TABLE*>(p.table) + static_cast<long long>(token) * p.cols, base);
+}
+template <class TABLE, bool BASE, bool VECTOR>
+__device__ __forceinline__ Eight base_row(const SumParams& p, const Columns<VECTOR>& at, uint32_t token) {
+  if constexpr (BASE) return at.load(static_cast<const TABLE*>(p.base) + static_cast<long long>(token) * p.cols);
+  return Eight{};
 }
 
 template <bool VECTOR>
@@ -311,97 +346,176 @@ __device__ __forceinline__ Columns<VECTOR> sum_columns(int cols) {
   return Columns<VECTOR>{VECTOR ? 8 * (block + t) : 8 * block + t, threads, cols};
 }
 
-// A run of sorted positions, 8 columns a thread.
-template <class DY, class TABLE, bool VECTOR>
+// How many lanes from the first one on say yes.
+__device__ __forceinline__ int leading(bool yes) {
+  const uint32_t no = ~__ballot_sync(0xffffffffu, yes);
+  return no == 0u ? 32 : __ffs(no) - 1;
+}
+
+// The tokens that begin in a run of sorted positions, 8 columns a thread. Tokens of up to kLong positions are summed by the
+// run in which they begin, even past its end; of longer ones every run sums its part, and join_rows_kernel adds those.
+template <class DY, class TABLE, bool BASE, bool VECTOR>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p) {
-  __shared__ uint32_t key[kMaxRun + 2], pos[kMaxRun];  // the tokens before and behind the run as well
+  constexpr int AHEAD = kSumAhead<VECTOR>;
+  __shared__ uint32_t keys[kLong + kMaxRun + kLong], places[kMaxRun + kLong];
   pdl_launch_dependents();
   pdl_wait();
   const long long begin = static_cast<long long>(blockIdx.x) * p.run;
-  const int length = static_cast<int>(min(static_cast<long long>(p.run), p.count - begin));
-  for (int i = threadIdx.x; i < length + 2; i += blockDim.x) {
-    const long long at = begin + i - 1;
-    key[i] = at >= 0 && at < p.count ? p.key[at] : 0xFFFFFFFFu;
-    if (i >= 1 && i <= length) pos[i - 1] = p.pos[at];
+  constexpr uint32_t NONE = 0xFFFFFFFFu;
+  for (int i = threadIdx.x; i < p.run + 2 * kLong; i += blockDim.x) {
+    const long long at = begin + i - kLong;
+    const Entry e = at >= 0 && at < p.count ? p.list[at] : Entry{NONE, 0u};
+    keys[i] = e.token < static_cast<uint32_t>(p.vocab) ? e.token : NONE;
+    if (i >= kLong) places[i - kLong] = e.pos;
   }
   __syncthreads();
+  const uint32_t* const key = keys + kLong;  // of the run's positions; from -kLong to run + kLong - 1
+  const int lane = threadIdx.x & 31;
+  if (key[0] == NONE) return;  // (positions without a token are behind all others)
+  // positions first .. end - 1 are this CTA's
+  int first = 0, end = p.run;
+  bool before = key[-1] == key[0], behind = false;  // its first token is a long one that began earlier; its last one goes on
+  if (before) {
+    const int back = leading(key[-1 - lane] == key[0]), on = leading(key[lane] == key[0]);
+    if (back + on <= kLong) {  // a short one: the run in which it began has it
+      first = on;
+      before = false;
+    }
+  }
+  if (key[p.run - 1] == NONE) {
+    end = 0;
+    for (int i = 0; i < p.run; i += 32) end += __popc(__ballot_sync(0xffffffffu, i + lane < p.run && key[i + lane] != NONE));
+  } else if (key[p.run] == key[p.run - 1] && !(before && key[p.run - 1] == key[0]) && first < p.run) {
+    const uint32_t last = key[p.run - 1];
+    const int back = leading(p.run - 1 - lane >= 0 && key[p.run - 1 - lane] == last), on = leading(key[p.run + lane] == last);
+    if (back + on <= kLong) end += on;
+    else behind = true;
+  }
+  if (first >= end) return;
+  if (behind && threadIdx.x == 0 && blockIdx.y == 0)
+    p.spans[1 + atomicAdd(p.spans, 1)] = static_cast<int>(blockIdx.x);  // (their order does not matter)
   const Columns<VECTOR> at = sum_columns<VECTOR>(p.cols);
   if (at.first >= p.cols) return;
-  const Columns<VECTOR> part = at;
   float* const partial = p.partial + 2LL * blockIdx.x * p.cols;
   const DY* const dy = static_cast<const DY*>(p.dy);
   Eight sum = {};
-  int start = 0;  // of the current token's part
-  constexpr int AHEAD = 4;
-  for (int i = 0; i < length; i += AHEAD) {
-    Eight e[AHEAD];
+  for (int i = first; i < end; i += AHEAD) {
+    Eight e[AHEAD], base[AHEAD];
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a)
-      if (i + a < length && key[i + a + 1] < static_cast<uint32_t>(p.vocab)) e[a] = at.load(dy + pos[i + a] * p.ldd);
+    for (int a = 0; a < AHEAD; ++a) e[a] = at.load(dy + places[min(i + a, end - 1)] * p.ldd);
+    if constexpr (BASE) {  // (asked for with dy's rows: the stores in between would keep them apart)
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a)
+        if (i + a < end && (i + a + 1 == end || key[i + a + 1] != key[i + a]))
+          base[a] = base_row<TABLE, true>(p, at, key[i + a]);
+    }
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) {
-      if (i + a >= length) break;
-      const uint32_t token = key[i + a + 1];
-      if (token >= static_cast<uint32_t>(p.vocab)) return;  // (no token: the list's end)
+      if (i + a >= end) break;
+      const uint32_t token = key[i + a];
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum.v[j] += e[a].v[j];
-      const bool last = i + a + 1 == length;
-      if (!last && key[i + a + 2] == token) continue;
-      // the token's part of this run is complete
-      const bool before = start == 0 && key[0] == token, behind = last && key[length + 1] == token;
-      if (before) part.store(partial, sum);
-      else if (behind) part.store(partial + p.cols, sum);
-      else write_row<TABLE>(p, at, token, sum);
+      const bool last = i + a + 1 == end;
+      if (!last && key[i + a + 1] == token) continue;
+      // the token is complete, or the run's part of a long one
+      if (before) at.store(partial, sum);
+      else if (last && behind) at.store(partial + p.cols, sum);
+      else write_row<TABLE>(p, at, token, sum, BASE ? base[a] : Eight{});
       sum = Eight{};
-      start = i + a + 1;
+      before = false;
     }
   }
 }
 
-// The tokens that begin in one run and end in a later one: the first run's last part and the later ones' first parts, in
-// order. The CTA's four groups of threads take every fourth run; their sums are added in order.
-constexpr int kJoinGroups = 4;
+// Long tokens: the part of the run in which one begins and those of the runs that it reaches. Each of the CTA's warps takes
+// every eighth run, of 256 columns; their sums are added in order.
+constexpr int kJoinGroups = 8;
 template <class TABLE, bool VECTOR>
-__global__ void __launch_bounds__(kJoinGroups* kSumThreads) join_rows_kernel(const SumParams p, int runs) {
-  __shared__ float parts[kJoinGroups - 1][8][kSumThreads];
+__global__ void __launch_bounds__(kJoinGroups * 32) join_rows_kernel(const SumParams p, int runs) {
+  __shared__ float parts[kJoinGroups][8][32];
   pdl_launch_dependents();
   pdl_wait();
-  const long long end = (static_cast<long long>(blockIdx.x) + 1) * p.run;
-  if (end >= p.count) return;
-  const uint32_t token = p.key[end - 1];
-  if (token >= static_cast<uint32_t>(p.vocab) || p.key[end] != token) return;
-  const long long begin = end - p.run;
-  if (begin > 0 && p.key[begin] == token && p.key[begin - 1] == token) return;  // it begins in an earlier run
-  // the runs that it reaches: a binary search for its end
-  long long low = end, high = p.count;  // key[low] == token; key[high] is another one (or the list's end)
-  while (high - low > 1) {
-    const long long mid = (low + high) / 2;
-    if (p.key[mid] == token) low = mid;
-    else high = mid;
-  }
-  const int last = static_cast<int>(low / p.run);
+  const int warp = static_cast<int>(threadIdx.y), lane = static_cast<int>(threadIdx.x);
   const Columns<VECTOR> at = sum_columns<VECTOR>(p.cols);
   const bool live = at.first < p.cols;
-  Eight sum = {};
-  if (live) {
-#pragma unroll 4
-    for (int r = static_cast<int>(blockIdx.x) + static_cast<int>(threadIdx.y); r <= last; r += kJoinGroups) {
-      const bool first = r == static_cast<int>(blockIdx.x);
-      const Eight e = at.load(p.partial + (2LL * r + (first ? 1 : 0)) * p.cols);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum.v[j] += e.v[j];
+  const int count = *p.spans;
+  for (int n = blockIdx.x; n < count; n += gridDim.x) {
+    const int from = p.spans[1 + n];
+    const uint32_t token = p.list[(from + 1LL) * p.run - 1].token;
+    // the runs that begin with the token
+    constexpr int THREADS = kJoinGroups * 32;
+    int last = from;
+    for (int more = THREADS; more == THREADS; last += more) {
+      const int r = last + 1 + warp * 32 + lane;
+      more = __syncthreads_count(r < runs && p.list[static_cast<long long>(r) * p.run].token == token);
     }
-    if (threadIdx.y > 0)
+    Eight sum = {};
+    if (live) {
+#pragma unroll 4
+      for (int r = from + warp; r <= last; r += kJoinGroups) {
+        const Eight e = at.load(p.partial + (2LL * r + (r == from ? 1 : 0)) * p.cols);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) parts[threadIdx.y - 1][j][threadIdx.x] = sum.v[j];
+        for (int j = 0; j < 8; ++j) sum.v[j] += e.v[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) parts[warp][j][lane] = sum.v[j];
+    __syncthreads();
+    if (warp == 0 && live) {
+      const int groups = min(kJoinGroups, last - from + 1);
+#pragma unroll 4
+      for (int g = 1; g < groups; ++g)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum.v[j] += parts[g][j][lane];
+      write_row<TABLE>(p, at, token, sum, p.base != nullptr ? base_row<TABLE, true>(p, at, token) : Eight{});
+    }
+    __syncthreads();  // the warps' sums are read
+  }
+}
+
+// Few positions, without a sort: a CTA for each position looks whether its token stands before it; if not, it collects the
+// token's positions in their order and adds their rows.
+constexpr int kDirect = 256;
+template <class DY, class TABLE, bool BASE, bool VECTOR>
+__global__ void __launch_bounds__(kSumThreads) direct_kernel(const SumParams p, const long long* tokens) {
+  constexpr int AHEAD = kSumAhead<VECTOR>;
+  __shared__ uint32_t mask[kDirect / 32];
+  __shared__ int places[kDirect];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int mine = blockIdx.x, lane = threadIdx.x & 31;
+  const long long token = tokens[mine];
+  if (token < 0 || token >= p.vocab) return;
+  for (int i = threadIdx.x; i < kDirect; i += blockDim.x) {  // (blockDim is a multiple of 32)
+    const uint32_t m = __ballot_sync(0xffffffffu, i < p.count && tokens[i] == token);
+    if (lane == 0) mask[i / 32] = m;
   }
   __syncthreads();
-  if (threadIdx.y > 0 || !live) return;
+  int count = 0;
+  for (int w = 0; w < kDirect / 32; ++w) {
+    const uint32_t m = mask[w];
+    if (w * 32 <= mine && (m & (mine - w * 32 >= 32 ? 0xffffffffu : (1u << (mine - w * 32)) - 1u)) != 0u) return;  // it stands before
+    if (threadIdx.x < 32 && (m >> lane & 1u) != 0u) places[count + __popc(m & ((1u << lane) - 1u))] = w * 32 + lane;
+    count += __popc(m);
+  }
+  __syncthreads();
+  const Columns<VECTOR> at = sum_columns<VECTOR>(p.cols);
+  if (at.first >= p.cols) return;
+  const DY* const dy = static_cast<const DY*>(p.dy);
+  const Eight base = base_row<TABLE, BASE>(p, at, static_cast<uint32_t>(token));
+  Eight sum = {};
+  for (int i = 0; i < count; i += AHEAD) {
+    Eight e[AHEAD];
 #pragma unroll
-  for (int g = 0; g < kJoinGroups - 1; ++g)
+    for (int a = 0; a < AHEAD; ++a)
+      if (i + a < count) e[a] = at.load(dy + places[i + a] * p.ldd);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum.v[j] += parts[g][j][threadIdx.x];
-  write_row<TABLE>(p, at, token, sum);
+    for (int a = 0; a < AHEAD; ++a)
+      if (i + a < count)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum.v[j] += e[a].v[j];
+  }
+  write_row<TABLE>(p, at, static_cast<uint32_t>(token), sum, base);
 }
 
 // ---------------------------------------------------------------- host side
@@ -425,7 +539,7 @@ int launch(const void* kernel, dim3 grid, dim3 threads, size_t smem, cudaStream_
   return GEMM_OK;
 }
 
-constexpr int kMaxVocab = (1 << 27) - 1;  // three digits
+constexpr int kMaxVocab = (1 << 27) - 1;
 constexpr int kMaxCols = 1 << 22;
 
 bool known_type(int t) { return t == GEMM_TABLE_BF16 || t == GEMM_TABLE_F32; }
@@ -440,10 +554,22 @@ const void* lookup(int units) {
                     : reinterpret_cast<const void*>(lookup_kernel<T, VECTOR, 4>);
 }
 
+template <class DY, class TABLE, bool BASE, bool VECTOR>
+const void* sum(bool direct) {
+  return direct ? reinterpret_cast<const void*>(direct_kernel<DY, TABLE, BASE, VECTOR>)
+                : reinterpret_cast<const void*>(sum_kernel<DY, TABLE, BASE, VECTOR>);
+}
 template <class DY, class TABLE>
-const void* sum(bool vector) {
-  return vector ? reinterpret_cast<const void*>(sum_kernel<DY, TABLE, true>)
-                : reinterpret_cast<const void*>(sum_kernel<DY, TABLE, false>);
+const void* sum(bool direct, bool base, bool vector) {
+  return base ? (vector ? sum<DY, TABLE, true, true>(direct) : sum<DY, TABLE, true, false>(direct))
+              : (vector ? sum<DY, TABLE, false, true>(direct) : sum<DY, TABLE, false, false>(direct));
+}
+const void* sum(int dy_type, int table_type, bool direct, bool base, bool vector) {
+  return dy_type == GEMM_TABLE_BF16
+             ? (table_type == GEMM_TABLE_BF16 ? sum<uint16_t, uint16_t>(direct, base, vector)
+                                              : sum<uint16_t, float>(direct, base, vector))
+             : (table_type == GEMM_TABLE_BF16 ? sum<float, uint16_t>(direct, base, vector)
+                                              : sum<float, float>(direct, base, vector));
 }
 template <class TABLE>
 const void* join_rows(bool vector) {
@@ -451,13 +577,15 @@ const void* join_rows(bool vector) {
                 : reinterpret_cast<const void*>(join_rows_kernel<TABLE, false>);
 }
 
+int sort_bytes(int digit_bits) { return static_cast<int>(sizeof(SortShared)) + (kSortWarps << digit_bits) * 4; }
+
 bool prepare_sort(int device) {
   static std::mutex mu;
   static bool done[64] = {};
   std::lock_guard<std::mutex> lock(mu);
   if (device < 0 || device >= 64) return false;
   if (!done[device]) {
-    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortShared)) !=
+    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_bytes(kMostDigitBits)) !=
         cudaSuccess) {
       cudaGetLastError();
       return false;
@@ -519,73 +647,84 @@ int gemm_embedding_backward(const void* dY, int dy_type, const long long* tokens
   int device = 0, err = 0;
   const DeviceInfo* info = current_device_info(&device, &err);
   if (info == nullptr) return err;
-  if (!prepare_sort(device)) return GEMM_ERR_LAUNCH;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
-  // runs of at least 16 positions, and about 512 of them at most
+  const bool vector = cols % 8 == 0 && rows_aligned(dY, dy_type, ldd) && rows_aligned(base, table_type, cols) &&
+                      rows_aligned(dtable, table_type, cols);
+  RowsParams rest = {dtable, base, in_place ? 0 : static_cast<long long>(vocab) * cols * type_bytes(table_type),
+                     rows > kDirect};
+  constexpr long long FILL = 16LL * kRowsVectors * kRowsThreads;  // bytes of a CTA
+  const long long fill_ctas = (rest.bytes + FILL - 1) / FILL;
+  if (fill_ctas > 0x7FFFFFFF) return GEMM_ERR_UNSUPPORTED_SHAPE;
+  void* rest_args[] = {&rest};
+  auto write_rest = [&] {
+    return rest.bytes == 0 ? GEMM_OK
+                           : launch(reinterpret_cast<const void*>(rows_kernel), dim3(static_cast<unsigned>(fill_ctas)),
+                                    dim3(kRowsThreads), 0, s, rest_args);
+  };
+  if (rows == 0) return write_rest();
+
   SumParams q = {};
-  q.run = std::min(kMaxRun, std::max(16, ceil_div(ceil_div(std::max(rows, 1), 512), 8) * 8));
-  const int runs = ceil_div(rows, q.run);
-  const size_t list = (size_t(rows) * 4 + 255) / 256 * 256;
-  uint8_t* ws = nullptr;
-  if (rows > 0) {
-    cudaMemPool_t pool = workspace_pool(device);
-    void* got = nullptr;
-    if (pool == nullptr || cudaMallocFromPoolAsync(&got, 4 * list + size_t(runs) * 2 * cols * 4, pool, s) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_OUT_OF_MEMORY;
-    }
-    ws = static_cast<uint8_t*>(got);
+  q.dy = dY;
+  q.base = base;
+  q.table = dtable;
+  q.ldd = ldd;
+  q.count = rows;
+  q.vocab = vocab;
+  q.cols = cols;
+  q.scale = scale;
+  const int units = ceil_div(cols, 8), threads = std::min(kSumThreads, ceil_div(units, 32) * 32);
+  const void* kernel = sum(dy_type, table_type, rows <= kDirect, base != nullptr, vector);
+  if (rows <= kDirect) {
+    const int st = write_rest();
+    if (st != GEMM_OK) return st;
+    void* args[] = {&q, &tokens};
+    return launch(kernel, dim3(rows, ceil_div(units, threads)), dim3(threads), 0, s, args);
   }
+
+  // runs of as many positions as a thread asks for at a time, longer ones where there would be more than 2048 of them
+  if (!prepare_sort(device)) return GEMM_ERR_LAUNCH;
+  const int ahead = vector ? kSumAhead<true> : kSumAhead<false>;
+  q.run = std::min(kMaxRun, ceil_div(ceil_div(rows, 2048), ahead) * ahead);
+  const int runs = ceil_div(rows, q.run);
+  const size_t list = (size_t(rows) * sizeof(Entry) + 255) / 256 * 256, spans = (size_t(runs) * 4 + 4 + 255) / 256 * 256;
+  cudaMemPool_t pool = workspace_pool(device);
+  void* got = nullptr;
+  if (pool == nullptr ||
+      cudaMallocFromPoolAsync(&got, 2 * list + spans + size_t(runs) * 2 * cols * 4, pool, s) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_OUT_OF_MEMORY;
+  }
+  uint8_t* const ws = static_cast<uint8_t*>(got);
   SortParams p = {};
   p.tokens = tokens;
   p.count = rows;
   p.vocab = vocab;
   int bits = 1;
   while ((vocab >> bits) != 0) ++bits;  // (the token after the last stands for none)
-  p.passes = ceil_div(bits, kDigitBits);
+  p.passes = ceil_div(bits, kMostDigitBits);
   p.digit_bits = ceil_div(bits, p.passes);
   p.per_warp = ceil_div(ceil_div(rows, kSortCtas * kSortWarps), 32) * 32;
-  for (int i = 0; i < 2; ++i) {
-    p.key[i] = reinterpret_cast<uint32_t*>(ws + i * list);
-    p.pos[i] = reinterpret_cast<uint32_t*>(ws + (2 + i) * list);
-  }
-  p.table = dtable;
-  p.base = base;
-  p.bytes = in_place ? 0 : static_cast<long long>(vocab) * cols * type_bytes(table_type);
-  const long long fill = (p.bytes + 16LL * kSortThreads - 1) / (16LL * kSortThreads);
-  const int fill_ctas = static_cast<int>(std::min<long long>((fill + kSortCtas - 1) / kSortCtas * kSortCtas,
-                                                             info->num_sms * 2 / kSortCtas * kSortCtas));
+  for (int i = 0; i < 2; ++i) p.list[i] = reinterpret_cast<Entry*>(ws + i * list);
+  p.spans = reinterpret_cast<int*>(ws + 2 * list);
   void* sort_args[] = {&p};
-  int st = launch(reinterpret_cast<const void*>(sort_kernel), dim3(kSortCtas + fill_ctas), dim3(kSortThreads),
-                  sizeof(SortShared), s, sort_args);
-  if (rows == 0) return st;
+  int st = launch(reinterpret_cast<const void*>(sort_kernel), dim3(kSortCtas), dim3(kSortThreads), sort_bytes(p.digit_bits),
+                  s, sort_args);
+  if (st == GEMM_OK) st = write_rest();
 
-  q.dy = dY;
-  q.key = p.key[0];
-  q.pos = p.pos[0];
-  q.base = base;
-  q.table = dtable;
-  q.partial = reinterpret_cast<float*>(ws + 4 * list);
-  q.ldd = ldd;
-  q.count = rows;
-  q.vocab = vocab;
-  q.cols = cols;
-  q.scale = scale;
-  const bool vector = cols % 8 == 0 && rows_aligned(dY, dy_type, ldd) && rows_aligned(base, table_type, cols) &&
-                      rows_aligned(dtable, table_type, cols);
-  const int units = ceil_div(cols, 8), threads = std::min(kSumThreads, ceil_div(units, 32) * 32);
+  q.list = p.list[0];
+  q.spans = p.spans;
+  q.partial = reinterpret_cast<float*>(ws + 2 * list + spans);
   const dim3 grid(runs, ceil_div(units, threads));
-  const void* kernel = dy_type == GEMM_TABLE_BF16
-                           ? (table_type == GEMM_TABLE_BF16 ? sum<uint16_t, uint16_t>(vector) : sum<uint16_t, float>(vector))
-                           : (table_type == GEMM_TABLE_BF16 ? sum<float, uint16_t>(vector) : sum<float, float>(vector));
   void* sum_args[] = {&q};
   if (st == GEMM_OK) st = launch(kernel, grid, dim3(threads), 0, s, sum_args);
   if (st == GEMM_OK && runs > 1) {
     int n = runs;
     void* join_args[] = {&q, &n};
-    st = launch(table_type == GEMM_TABLE_BF16 ? join_rows<uint16_t>(vector) : join_rows<float>(vector), grid,
-                dim3(threads, kJoinGroups), 0, s, join_args);
+    const int blocks = ceil_div(units, 32);
+    const dim3 join_grid(std::min(runs, std::max(1, 8 * info->num_sms / blocks)), blocks);
+    st = launch(table_type == GEMM_TABLE_BF16 ? join_rows<uint16_t>(vector) : join_rows<float>(vector), join_grid,
+                dim3(32, kJoinGroups), 0, s, join_args);
   }
   if (cudaFreeAsync(ws, s) != cudaSuccess && st == GEMM_OK) st = GEMM_ERR_LAUNCH;
   return st;

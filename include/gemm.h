@@ -639,16 +639,17 @@ int gemm_embedding(const void* table, int type, const long long* tokens, void* Y
 /*
  * gemm_embedding_backward -- gradient of the table, dense:
  *   dtable[v] = round(base[v] + scale * sum over i with tokens[i] == v of dY[i]),
- * summed in FP32 in the order of the positions (in runs that are joined in order) and rounded once.
+ * summed in FP32 in the order of the positions (more than 32 of a token in parts, which are added in a fixed order) and
+ * rounded once.
  *   dY: rows x cols of dy_type, row stride ldd elements (0 = cols), element-aligned.
  *   base: vocab x cols of table_type, contiguous: what is there already (with tied weights the head's dW, from
  *   gemm_cross_entropy_backward); NULL: zeros. base may be dtable: then only the rows of given tokens are written.
  *   dtable: vocab x cols of table_type, contiguous. dtable and base are 16-byte aligned, in place element-aligned.
  *   tokens: rows int64; a negative token or one >= vocab takes no part (its row of dY is not read).
  * Constraints: vocab < 2^27, cols <= 4194304, scale finite. rows == 0: dtable is base or zeros.
- * Up to three kernel launches, asynchronous on `stream`, and a workspace from the library's stream-ordered pool: 16 bytes
- * a position and 8 cols bytes for each run of positions (of 16 to 256, so that there are about 512 or they are 256
- * long). The same inputs give the same bits.
+ * Up to four kernel launches, asynchronous on `stream`, and a workspace from the library's stream-ordered pool: some 16
+ * bytes a position and 8 cols bytes for each run of positions (4 or 8 of them, more where there would be more than 2048
+ * runs, at most 256). The same inputs give the same bits.
  */
 int gemm_embedding_backward(const void* dY, int dy_type, const long long* tokens, const void* base, void* dtable,
                             int table_type, int rows, int vocab, int cols, long long ldd, float scale, void* stream);

@@ -200,3 +200,24 @@ def test_captured_and_replayed():
     torch.cuda.synchronize()
     for _, out in graphs:
         assert all(torch.equal(u, v) for u, v in zip(out, want))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("cols", [8, 5])
+def test_lengths_around_the_runs(dtype, cols):
+    """Tokens of 1 to 70 positions one behind the other, from every offset against the runs of positions: short ones that
+    cross a run's end, long ones that begin, cross and end anywhere, and places without a token behind them."""
+    for lead in range(0, 40, 3):
+        lengths = [lead] + [1, 31, 2, 32, 33, 1, 1, 34, 64, 7, 8, 9, 65, 3, 70, 40, 15, 16, 17, 36]
+        tokens = torch.cat([torch.full((n,), 2 * v) for v, n in enumerate(lengths)] + [torch.full((lead,), -1)])
+        order = torch.randperm(len(tokens), generator=torch.Generator().manual_seed(lead))
+        tokens = tokens[order].to(DEV)
+        dy = normal(lead, len(tokens), cols, dtype=dtype)
+        check_gradient(g.embedding_backward(dy, tokens, 43, scale=0.5), dy, tokens, 43, 0.5, None)
+
+
+def test_many_positions_of_few_tokens():
+    """Runs of more than the least length, and long tokens of thousands of runs."""
+    for rows, vocab in ((100000, 3), (70000, 1), (300001, 70000)):
+        tokens, dy = ids(rows, rows, vocab, "few" if vocab == 3 else "frequent"), normal(7, rows, 8)
+        check_gradient(g.embedding_backward(dy, tokens, vocab), dy, tokens, vocab, 1.0, None)
