@@ -64,17 +64,20 @@ __device__ __forceinline__ void store8(float* p, const Eight& e) {
 }
 
 // A thread's 8 columns: next to one another where rows start on 16-byte boundaries and have a multiple of 8 columns
-// (VECTOR), else `step` apart, so that a warp reads and writes side by side.
-template <bool VECTOR>
+// (VECTOR), else STEP apart (the threads that share a row; 0: known at run time), so that a warp reads and writes side by
+// side.
+template <bool VECTOR, int STEP>
 struct Columns {
-  int first, step, cols;
+  int first, cols, run_step;
+  __device__ __forceinline__ int step() const { return STEP > 0 ? STEP : run_step; }
   template <class T>
   __device__ __forceinline__ Eight load(const T* row) const {
     if constexpr (VECTOR) return load8(row + first);
     Eight r = {};
+    const T* const at = row + first;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (first + j * step < cols) r.v[j] = to_float(row[first + j * step]);
+      if (first + j * step() < cols) r.v[j] = to_float(at[j * step()]);
     return r;
   }
   template <class T>
@@ -82,9 +85,10 @@ struct Columns {
     if constexpr (VECTOR) {
       store8(row + first, e);
     } else {
+      T* const at = row + first;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (first + j * step < cols) from_float(row[first + j * step], e.v[j]);
+        if (first + j * step() < cols) from_float(at[j * step()], e.v[j]);
     }
   }
 };
@@ -116,12 +120,12 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupPara
   const T* from = static_cast<const T*>(p.table) + (given ? token : 0) * p.ldt;
   T* to = static_cast<T*>(p.y) + row * p.ldy;
   const float other = token < 0 ? 0.0f : __int_as_float(0x7FC00000);
-  Columns<VECTOR> at[UNITS];
+  Columns<VECTOR, 0> at[UNITS];
   Eight e[UNITS];
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {
     const int unit = (static_cast<int>(blockIdx.y) * UNITS + u) * p.row_threads;
-    at[u] = Columns<VECTOR>{VECTOR ? 8 * (unit + in_row) : 8 * unit + in_row, p.row_threads, p.cols};
+    at[u] = Columns<VECTOR, 0>{VECTOR ? 8 * (unit + in_row) : 8 * unit + in_row, p.cols, p.row_threads};
     e[u] = Eight{{other, other, other, other, other, other, other, other}};
     if (given && at[u].first < p.cols) e[u] = at[u].load(from);
   }
@@ -313,7 +317,7 @@ struct SumParams {
   const void* base;   // or null
   void* table;
   float* partial;  // [runs][2][cols]: a run's parts of a long token that began before it, and of one that goes on behind it
-  int* spans;      // how many long tokens there are, and the runs in which they begin
+  int* spans;      // how many long tokens there are, and (from place 2 on) the runs in which they begin, with the tokens
   long long ldd;
   int count, vocab, cols, run;  // positions, tokens, columns, positions of a run
   float scale;
@@ -322,28 +326,29 @@ struct SumParams {
 constexpr int kMaxRun = 256;
 constexpr int kSumThreads = 128;
 constexpr int kLong = 32;  // a token of more positions is long
-template <bool VECTOR>
-constexpr int kSumAhead = VECTOR ? 8 : 4;  // rows of dy that a thread asks for together
+template <bool VECTOR, bool BASE>
+constexpr int kSumAhead = VECTOR && !BASE ? 8 : 4;  // rows of dy (and of the base) that a thread asks for together
 
 // table[token] = base + scale * sum, at this thread's columns.
-template <class TABLE, bool VECTOR>
-__device__ __forceinline__ void write_row(const SumParams& p, const Columns<VECTOR>& at, uint32_t token, const Eight& sum,
+template <class TABLE, bool VECTOR, int STEP>
+__device__ __forceinline__ void write_row(const SumParams& p, const Columns<VECTOR, STEP>& at, uint32_t token, const Eight& sum,
                                           Eight base) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) base.v[j] = fmaf(p.scale, sum.v[j], base.v[j]);
   at.store(static_cast<TABLE*>(p.table) + static_cast<long long>(token) * p.cols, base);
 }
-template <class TABLE, bool BASE, bool VECTOR>
-__device__ __forceinline__ Eight base_row(const SumParams& p, const Columns<VECTOR>& at, uint32_t token) {
+template <class TABLE, bool BASE, bool VECTOR, int STEP>
+__device__ __forceinline__ Eight base_row(const SumParams& p, const Columns<VECTOR, STEP>& at, uint32_t token) {
   if constexpr (BASE) return at.load(static_cast<const TABLE*>(p.base) + static_cast<long long>(token) * p.cols);
   return Eight{};
 }
 
-template <bool VECTOR>
-__device__ __forceinline__ Columns<VECTOR> sum_columns(int cols) {
-  const int threads = static_cast<int>(blockDim.x), block = static_cast<int>(blockIdx.y) * threads;
+// The columns of a thread of blockDim.x that share a row (STEP of them where columns are STEP apart).
+template <bool VECTOR, int STEP>
+__device__ __forceinline__ Columns<VECTOR, STEP> sum_columns(int cols) {
+  const int threads = VECTOR ? static_cast<int>(blockDim.x) : STEP, block = static_cast<int>(blockIdx.y) * threads;
   const int t = static_cast<int>(threadIdx.x);
-  return Columns<VECTOR>{VECTOR ? 8 * (block + t) : 8 * block + t, threads, cols};
+  return Columns<VECTOR, STEP>{VECTOR ? 8 * (block + t) : 8 * block + t, cols, STEP};
 }
 
 // How many lanes from the first one on say yes.
@@ -356,7 +361,7 @@ __device__ __forceinline__ int leading(bool yes) {
 // run in which they begin, even past its end; of longer ones every run sums its part, and join_rows_kernel adds those.
 template <class DY, class TABLE, bool BASE, bool VECTOR>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p) {
-  constexpr int AHEAD = kSumAhead<VECTOR>;
+  constexpr int AHEAD = kSumAhead<VECTOR, BASE>;
   __shared__ uint32_t keys[kLong + kMaxRun + kLong], places[kMaxRun + kLong];
   pdl_launch_dependents();
   pdl_wait();
@@ -393,8 +398,9 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p) {
   }
   if (first >= end) return;
   if (behind && threadIdx.x == 0 && blockIdx.y == 0)
-    p.spans[1 + atomicAdd(p.spans, 1)] = static_cast<int>(blockIdx.x);  // (their order does not matter)
-  const Columns<VECTOR> at = sum_columns<VECTOR>(p.cols);
+    reinterpret_cast<int2*>(p.spans)[1 + atomicAdd(p.spans, 1)] =  // (their order does not matter)
+        make_int2(static_cast<int>(blockIdx.x), static_cast<int>(key[p.run - 1]));
+  const Columns<VECTOR, kSumThreads> at = sum_columns<VECTOR, kSumThreads>(p.cols);
   if (at.first >= p.cols) return;
   float* const partial = p.partial + 2LL * blockIdx.x * p.cols;
   const DY* const dy = static_cast<const DY*>(p.dy);
@@ -428,20 +434,25 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p) {
 }
 
 // Long tokens: the part of the run in which one begins and those of the runs that it reaches. Each of the CTA's warps takes
-// every eighth run, of 256 columns; their sums are added in order.
-constexpr int kJoinGroups = 8;
+// every 16th run, of 256 columns; their sums are added in order.
+constexpr int kJoinGroups = 16;
 template <class TABLE, bool VECTOR>
 __global__ void __launch_bounds__(kJoinGroups * 32) join_rows_kernel(const SumParams p, int runs) {
   __shared__ float parts[kJoinGroups][8][32];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = static_cast<int>(threadIdx.y), lane = static_cast<int>(threadIdx.x);
-  const Columns<VECTOR> at = sum_columns<VECTOR>(p.cols);
+  const Columns<VECTOR, 32> at = sum_columns<VECTOR, 32>(p.cols);
   const bool live = at.first < p.cols;
+  const int2* const spans = reinterpret_cast<const int2*>(p.spans);
   const int count = *p.spans;
+  int2 next = spans[1 + blockIdx.x];  // (asked for with the count; there is room for one a run)
   for (int n = blockIdx.x; n < count; n += gridDim.x) {
-    const int from = p.spans[1 + n];
-    const uint32_t token = p.list[(from + 1LL) * p.run - 1].token;
+    const int from = next.x;
+    const uint32_t token = static_cast<uint32_t>(next.y);
+    if (n + static_cast<int>(gridDim.x) < count) next = spans[1 + n + gridDim.x];
+    Eight base = {};
+    if (p.base != nullptr && live && warp == 0) base = base_row<TABLE, true>(p, at, token);
     // the runs that begin with the token
     constexpr int THREADS = kJoinGroups * 32;
     int last = from;
@@ -467,7 +478,7 @@ __global__ void __launch_bounds__(kJoinGroups * 32) join_rows_kernel(const SumPa
       for (int g = 1; g < groups; ++g)
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum.v[j] += parts[g][j][lane];
-      write_row<TABLE>(p, at, token, sum, p.base != nullptr ? base_row<TABLE, true>(p, at, token) : Eight{});
+      write_row<TABLE>(p, at, token, sum, base);
     }
     __syncthreads();  // the warps' sums are read
   }
@@ -478,7 +489,7 @@ __global__ void __launch_bounds__(kJoinGroups * 32) join_rows_kernel(const SumPa
 constexpr int kDirect = 256;
 template <class DY, class TABLE, bool BASE, bool VECTOR>
 __global__ void __launch_bounds__(kSumThreads) direct_kernel(const SumParams p, const long long* tokens) {
-  constexpr int AHEAD = kSumAhead<VECTOR>;
+  constexpr int AHEAD = kSumAhead<VECTOR, BASE>;
   __shared__ uint32_t mask[kDirect / 32];
   __shared__ int places[kDirect];
   pdl_launch_dependents();
@@ -499,7 +510,7 @@ __global__ void __launch_bounds__(kSumThreads) direct_kernel(const SumParams p, 
     count += __popc(m);
   }
   __syncthreads();
-  const Columns<VECTOR> at = sum_columns<VECTOR>(p.cols);
+  const Columns<VECTOR, kSumThreads> at = sum_columns<VECTOR, kSumThreads>(p.cols);
   if (at.first >= p.cols) return;
   const DY* const dy = static_cast<const DY*>(p.dy);
   const Eight base = base_row<TABLE, BASE>(p, at, static_cast<uint32_t>(token));
@@ -673,7 +684,7 @@ int gemm_embedding_backward(const void* dY, int dy_type, const long long* tokens
   q.vocab = vocab;
   q.cols = cols;
   q.scale = scale;
-  const int units = ceil_div(cols, 8), threads = std::min(kSumThreads, ceil_div(units, 32) * 32);
+  const int units = ceil_div(cols, 8), threads = vector ? std::min(kSumThreads, ceil_div(units, 32) * 32) : kSumThreads;
   const void* kernel = sum(dy_type, table_type, rows <= kDirect, base != nullptr, vector);
   if (rows <= kDirect) {
     const int st = write_rest();
@@ -684,10 +695,10 @@ int gemm_embedding_backward(const void* dY, int dy_type, const long long* tokens
 
   // runs of as many positions as a thread asks for at a time, longer ones where there would be more than 2048 of them
   if (!prepare_sort(device)) return GEMM_ERR_LAUNCH;
-  const int ahead = vector ? kSumAhead<true> : kSumAhead<false>;
+  const int ahead = vector && base == nullptr ? kSumAhead<true, false> : kSumAhead<false, false>;
   q.run = std::min(kMaxRun, ceil_div(ceil_div(rows, 2048), ahead) * ahead);
   const int runs = ceil_div(rows, q.run);
-  const size_t list = (size_t(rows) * sizeof(Entry) + 255) / 256 * 256, spans = (size_t(runs) * 4 + 4 + 255) / 256 * 256;
+  const size_t list = (size_t(rows) * sizeof(Entry) + 255) / 256 * 256, spans = (size_t(runs) * 8 + 8 + 255) / 256 * 256;
   cudaMemPool_t pool = workspace_pool(device);
   void* got = nullptr;
   if (pool == nullptr ||
@@ -722,7 +733,7 @@ int gemm_embedding_backward(const void* dY, int dy_type, const long long* tokens
     int n = runs;
     void* join_args[] = {&q, &n};
     const int blocks = ceil_div(units, 32);
-    const dim3 join_grid(std::min(runs, std::max(1, 8 * info->num_sms / blocks)), blocks);
+    const dim3 join_grid(std::min(runs, std::max(1, 4 * info->num_sms / blocks)), blocks);
     st = launch(table_type == GEMM_TABLE_BF16 ? join_rows<uint16_t>(vector) : join_rows<float>(vector), join_grid,
                 dim3(32, kJoinGroups), 0, s, join_args);
   }
