@@ -97,11 +97,38 @@ __device__ __forceinline__ void load_bias(uint4 (&b)[VPT], const uint16_t* bias,
   }
 }
 
+// The rows of a CTA on their way: SLOTS of them in shared memory, the current one and those fetched ahead (1: the next one is
+// fetched once the current one is read).
+template <int SLOTS>
+struct Ring {
+  int slot = 0;
+  // Before the first row: fetch(row, slot) for as many as go ahead.
+  template <class Fetch>
+  __device__ __forceinline__ void start(long long rows, const Fetch& fetch) {
+#pragma unroll
+    for (int i = 0; i < (SLOTS > 1 ? SLOTS - 1 : 1); ++i) one(blockIdx.x + static_cast<long long>(i) * gridDim.x, rows, i, fetch);
+  }
+  // Fetches the row that is SLOTS - 1 behind `row`, waits for `row` and gives its slot.
+  template <class Fetch>
+  __device__ __forceinline__ int next(long long row, long long rows, const Fetch& fetch) {
+    if (SLOTS > 1)
+      one(row + static_cast<long long>(SLOTS - 1) * gridDim.x, rows, SLOTS == 2 ? slot ^ 1 : (slot + SLOTS - 1) % SLOTS, fetch);
+    asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+    const int now = slot;
+    slot = SLOTS == 2 ? slot ^ 1 : (slot + 1) % SLOTS;
+    return now;
+  }
+  template <class Fetch>
+  __device__ __forceinline__ void one(long long row, long long rows, int to, const Fetch& fetch) {
+    if (row < rows) fetch(row, to);
+    else asm volatile("cp.async.commit_group;" ::: "memory");  // (groups are counted)
+  }
+};
+
 // ---------------------------------------------------------------- forward
 
-template <int VPT, int FORMAT, int ACCESS>
-__global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 96)) layer_norm_kernel(const LayerNormParams p) {
-  constexpr int SLOTS = norm_slots(VPT);
+template <int VPT, int SLOTS, int FORMAT, int ACCESS>
+__global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 128)) layer_norm_kernel(const LayerNormParams p) {
   extern __shared__ uint4 fetched[];  // [SLOTS][2][VPT][threads]
   __shared__ float2 moments[2][32];   // a warp's mean and squares about it
   __shared__ float counts[32];        // its columns
@@ -127,21 +154,15 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 96)) la
   };
   // (groups past the row's end stay zero)
   for (int i = 0; i < SLOTS * 2 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
-  fetch(blockIdx.x, 0);
+  Ring<SLOTS> ring;
+  ring.start(p.rows, fetch);
   uint4 w[VPT], b[VPT];
   load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
   load_bias<VPT, ACCESS>(b, p.b, col, p.cols);
   const bool starts = threadIdx.x < 32 && phase != 0;  // the warp with the row's start
   int parity = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
-    const bool more = row + gridDim.x < p.rows;
-    if (SLOTS == 2 && more) {
-      fetch(row + gridDim.x, parity ^ 1);
-      wait_fetched<2>();
-    } else {
-      wait_fetched<1>();
-    }
-    const uint4* const in = mine + (SLOTS == 2 ? parity * slot_size : 0);
+    const uint4* const in = mine + ring.next(row, p.rows, fetch) * slot_size;
     P8 s[VPT];  // the stream (zeros outside the row), then the results
     uint64_t sum = 0;
 #pragma unroll
@@ -160,7 +181,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 96)) la
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum = f2_add(sum, s[k].v[j]);
     }
-    if (SLOTS == 1 && more) fetch(row + gridDim.x, 0);
+    if (SLOTS == 1 && row + gridDim.x < p.rows) fetch(row + gridDim.x, 0);
     const float warp_mean = warp_sum(pair_sum(sum)) * inverse_count;
     const uint64_t minus = f2_pack(-warp_mean, -warp_mean);
     uint64_t squares2 = 0;
@@ -181,25 +202,29 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 96)) la
             squares = fmaf(d, d, squares);
           });
     squares = warp_sum(squares + pair_sum(squares2));
-    if (lane == 0) moments[parity][warp] = make_float2(warp_mean, squares);
-    __syncthreads();
-    // The warps' moments about the first warp's mean: its distance from the row's mean is at most sqrt(warps) spreads, so
-    // taking it out again costs five bits of the variance's at the worst, and both sums run side by side.
-    const float about = moments[parity][0].x;
-    float first = 0.0f, second = 0.0f;
-    if (lane < warps) {
-      const float2 part = moments[parity][lane];
-      const float off = part.x - about, n_off = counts[lane] * off;
-      first = n_off;
-      second = fmaf(n_off, off, part.y);
-    }
+    float mean = warp_mean, var = squares * inverse_cols;
+    if (warps > 1) {
+      if (lane == 0) moments[parity][warp] = make_float2(warp_mean, squares);
+      __syncthreads();
+      // The warps' moments about the first warp's mean: its distance from the row's mean is at most sqrt(warps) spreads,
+      // so taking it out again costs five bits of the variance's at the worst, and both sums run side by side.
+      const float about = moments[parity][0].x;
+      float first = 0.0f, second = 0.0f;
+      if (lane < warps) {
+        const float2 part = moments[parity][lane];
+        const float off = part.x - about, n_off = counts[lane] * off;
+        first = n_off;
+        second = fmaf(n_off, off, part.y);
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      first += __shfl_xor_sync(0xffffffffu, first, o);
-      second += __shfl_xor_sync(0xffffffffu, second, o);
+      for (int o = 16; o > 0; o >>= 1) {
+        first += __shfl_xor_sync(0xffffffffu, first, o);
+        second += __shfl_xor_sync(0xffffffffu, second, o);
+      }
+      const float shift = first * inverse_cols;
+      mean = about + shift;
+      var = fmaxf(fmaf(-first, shift, second), 0.0f) * inverse_cols + (second - second);  // (NaN stays NaN)
     }
-    const float shift = first * inverse_cols, mean = about + shift;
-    const float var = fmaxf(fmaf(-first, shift, second), 0.0f) * inverse_cols + (second - second);  // (NaN stays NaN)
     const float rstd = 1.0f / sqrtf(var + p.eps);
     if (threadIdx.x == 0) {
       if (p.mean != nullptr) p.mean[row] = mean;
@@ -241,16 +266,16 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 96)) la
 __device__ __forceinline__ float2 block_sum2(float a, float b, float2* slots, int warps) {
   a = warp_sum(a);
   b = warp_sum(b);
+  if (warps == 1) return make_float2(a, b);
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = make_float2(a, b);
   __syncthreads();
   const float2 v = (threadIdx.x & 31) < warps ? slots[threadIdx.x & 31] : make_float2(0.0f, 0.0f);
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-template <int VPT, int ACCESS>
+template <int VPT, int SLOTS, int ACCESS>
 __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 96, 128))
     layer_norm_backward_kernel(const LayerNormBackwardParams p) {
-  constexpr int SLOTS = norm_slots(VPT);
   extern __shared__ uint4 fetched[];  // [SLOTS][3][VPT][threads]
   __shared__ float2 slots[2][32];
   const int warps = blockDim.x >> 5;
@@ -270,7 +295,8 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 96, 128))
   };
   // (groups past the row's end stay zero)
   for (int i = 0; i < SLOTS * 3 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
-  fetch(blockIdx.x, 0);
+  Ring<SLOTS> ring;
+  ring.start(p.rows, fetch);
   uint4 w[VPT];
   P8 dw[VPT], db[VPT];
 #pragma unroll
@@ -288,13 +314,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 96, 128))
       rstd_next = p.rstd[row + gridDim.x];
       mean_next = p.mean[row + gridDim.x];
     }
-    if (SLOTS == 2 && more) {
-      fetch(row + gridDim.x, parity ^ 1);
-      wait_fetched<2>();
-    } else {
-      wait_fetched<1>();
-    }
-    const uint4* const in = mine + (SLOTS == 2 ? parity * slot_size : 0);
+    const uint4* const in = mine + ring.next(row, p.rows, fetch) * slot_size;
     const uint64_t r2 = f2_pack(rstd, rstd), m2 = f2_pack(-mean, -mean);
     uint64_t sum1 = 0, sum2 = 0;
 #pragma unroll
@@ -371,7 +391,7 @@ __global__ void __launch_bounds__(32 * kSumWarps)
   const int c = blockIdx.x * 32 + lane;
   float v = 0.0f;
   if (c < cols)
-#pragma unroll 8
+#pragma unroll 16
     for (int r = warp; r < rows; r += kSumWarps) v += partial[(2LL * r + blockIdx.y) * cols + c];
   part[warp][lane] = v;
   __syncthreads();
@@ -381,26 +401,48 @@ __global__ void __launch_bounds__(32 * kSumWarps)
 
 // ---------------------------------------------------------------- host side
 
+// Threads, groups a thread and rows in shared memory. Rows of up to 256 columns are a warp each, without a barrier, and of
+// those an SM holds 32 at most, so three rows go ahead; wider ones as norm_shape's.
+struct LayerNormShape {
+  NormShape at;
+  int slots;
+  int smem(int tensors) const { return slots * tensors * at.vpt * at.threads * 16; }
+};
+LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, bool is_aligned) {
+  const int groups = ceil_div(cols, 8) + (is_aligned ? 0 : 1);
+  if (groups <= 32 && rows > num_sms) return LayerNormShape{{32, 1}, 4};
+  const NormShape s = norm_shape(rows, cols, num_sms, is_aligned);
+  return LayerNormShape{s, norm_slots(s.vpt)};
+}
+
 template <int FORMAT, int ACCESS>
-const void* forward_kernel(int vpt) {
-  return vpt == 1   ? reinterpret_cast<const void*>(layer_norm_kernel<1, FORMAT, ACCESS>)
-         : vpt == 2 ? reinterpret_cast<const void*>(layer_norm_kernel<2, FORMAT, ACCESS>)
-         : vpt == 4 ? reinterpret_cast<const void*>(layer_norm_kernel<4, FORMAT, ACCESS>)
-                    : reinterpret_cast<const void*>(layer_norm_kernel<8, FORMAT, ACCESS>);
+const void* forward_kernel(const LayerNormShape& s) {
+  switch (s.at.vpt) {
+    case 1:
+      return s.slots == 1 ? reinterpret_cast<const void*>(layer_norm_kernel<1, 1, FORMAT, ACCESS>)
+                          : reinterpret_cast<const void*>(layer_norm_kernel<1, 4, FORMAT, ACCESS>);
+    case 2: return reinterpret_cast<const void*>(layer_norm_kernel<2, 2, FORMAT, ACCESS>);
+    case 4: return reinterpret_cast<const void*>(layer_norm_kernel<4, 2, FORMAT, ACCESS>);
+    default: return reinterpret_cast<const void*>(layer_norm_kernel<8, 1, FORMAT, ACCESS>);
+  }
 }
 template <int FORMAT>
-const void* forward_kernel(int vpt, bool aligned, bool shared) {
-  return aligned  ? forward_kernel<FORMAT, kAligned>(vpt)
-         : shared ? forward_kernel<FORMAT, kShared>(vpt)
-                  : forward_kernel<FORMAT, kElements>(vpt);
+const void* forward_kernel(const LayerNormShape& s, bool aligned, bool shared) {
+  return aligned  ? forward_kernel<FORMAT, kAligned>(s)
+         : shared ? forward_kernel<FORMAT, kShared>(s)
+                  : forward_kernel<FORMAT, kElements>(s);
 }
 
 template <int ACCESS>
-const void* backward_kernel(int vpt) {
-  return vpt == 1   ? reinterpret_cast<const void*>(layer_norm_backward_kernel<1, ACCESS>)
-         : vpt == 2 ? reinterpret_cast<const void*>(layer_norm_backward_kernel<2, ACCESS>)
-         : vpt == 4 ? reinterpret_cast<const void*>(layer_norm_backward_kernel<4, ACCESS>)
-                    : reinterpret_cast<const void*>(layer_norm_backward_kernel<8, ACCESS>);
+const void* backward_kernel(const LayerNormShape& s) {
+  switch (s.at.vpt) {
+    case 1:
+      return s.slots == 1 ? reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 1, ACCESS>)
+                          : reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 4, ACCESS>);
+    case 2: return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 2, ACCESS>);
+    case 4: return reinterpret_cast<const void*>(layer_norm_backward_kernel<4, 2, ACCESS>);
+    default: return reinterpret_cast<const void*>(layer_norm_backward_kernel<8, 1, ACCESS>);
+  }
 }
 
 }  // namespace
@@ -467,15 +509,15 @@ int gemm_layer_norm(const void* X, const void* R, const void* W, const void* B, 
   int device = 0, err = 0;
   const DeviceInfo* info = current_device_info(&device, &err);
   if (info == nullptr) return err;
-  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned);
-  const void* kernel = format == GEMM_NORM_NVFP4  ? forward_kernel<GEMM_NORM_NVFP4, kAligned>(shape.vpt)
-                       : format == GEMM_NORM_E4M3 ? forward_kernel<GEMM_NORM_E4M3>(shape.vpt, aligned, shared)
-                                                  : forward_kernel<GEMM_NORM_BF16>(shape.vpt, aligned, shared);
+  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, aligned);
+  const void* kernel = format == GEMM_NORM_NVFP4  ? forward_kernel<GEMM_NORM_NVFP4, kAligned>(shape)
+                       : format == GEMM_NORM_E4M3 ? forward_kernel<GEMM_NORM_E4M3>(shape, aligned, shared)
+                                                  : forward_kernel<GEMM_NORM_BF16>(shape, aligned, shared);
   void* args[] = {&p};
-  const int smem = norm_smem(shape, 2);
-  const int grid = norm_grid(kernel, rows, shape.threads, smem, info->num_sms);
+  const int smem = shape.smem(2);
+  const int grid = norm_grid(kernel, rows, shape.at.threads, smem, info->num_sms);
   if (grid == 0) return GEMM_ERR_LAUNCH;
-  return norm_launch(kernel, dim3(grid), shape.threads, smem, static_cast<cudaStream_t>(stream), args);
+  return norm_launch(kernel, dim3(grid), shape.at.threads, smem, static_cast<cudaStream_t>(stream), args);
 }
 
 int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const float* mean, const float* rstd,
@@ -522,12 +564,12 @@ int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const
   const bool shared = RowPlace(dY, p.lddy, 2) == place && (dS == nullptr || RowPlace(dS, p.ldds, 2) == place) &&
                       RowPlace(dX, p.lddx, 2) == place;
   const bool aligned = shared && place.aligned() && cols % 8 == 0 && !misaligned(W, 16);
-  const NormShape shape = norm_shape(rows, cols, info->num_sms, aligned);
-  const void* kernel = aligned  ? backward_kernel<kAligned>(shape.vpt)
-                       : shared ? backward_kernel<kShared>(shape.vpt)
-                                : backward_kernel<kElements>(shape.vpt);
-  const int smem = norm_smem(shape, 3);
-  const int grid = norm_grid(kernel, rows, shape.threads, smem, info->num_sms);
+  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, aligned);
+  const void* kernel = aligned  ? backward_kernel<kAligned>(shape)
+                       : shared ? backward_kernel<kShared>(shape)
+                                : backward_kernel<kElements>(shape);
+  const int smem = shape.smem(3);
+  const int grid = norm_grid(kernel, rows, shape.at.threads, smem, info->num_sms);
   if (grid == 0) return GEMM_ERR_LAUNCH;
   void* ws = nullptr;
   if (sums) {
@@ -540,7 +582,7 @@ int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const
     p.partial = static_cast<float*>(ws);
   }
   void* args[] = {&p};
-  int rc = norm_launch(kernel, dim3(grid), shape.threads, smem, st, args);
+  int rc = norm_launch(kernel, dim3(grid), shape.at.threads, smem, st, args);
   if (ws != nullptr) {
     if (rc == GEMM_OK) {
       const float* partial = p.partial;
