@@ -104,37 +104,45 @@ struct Ring {
   int slot = 0;
   // Before the first row: fetch(row, slot) for as many as go ahead.
   template <class Fetch>
-  __device__ __forceinline__ void start(long long rows, const Fetch& fetch) {
+  __device__ __forceinline__ void start(uint32_t rows, const Fetch& fetch) {
 #pragma unroll
-    for (int i = 0; i < (SLOTS > 1 ? SLOTS - 1 : 1); ++i) one(blockIdx.x + static_cast<long long>(i) * gridDim.x, rows, i, fetch);
+    for (int i = 0; i < (SLOTS > 1 ? SLOTS - 1 : 1); ++i) one(blockIdx.x + i * gridDim.x, rows, i, fetch);
   }
   // Fetches the row that is SLOTS - 1 behind `row`, waits for `row` and gives its slot.
   template <class Fetch>
-  __device__ __forceinline__ int next(long long row, long long rows, const Fetch& fetch) {
+  __device__ __forceinline__ int next(uint32_t row, uint32_t rows, const Fetch& fetch) {
     if (SLOTS > 1)
-      one(row + static_cast<long long>(SLOTS - 1) * gridDim.x, rows, SLOTS == 2 ? slot ^ 1 : (slot + SLOTS - 1) % SLOTS, fetch);
+      one(row + (SLOTS - 1) * gridDim.x, rows, SLOTS == 2 ? slot ^ 1 : (slot + SLOTS - 1) % SLOTS, fetch);
     asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
     const int now = slot;
     slot = SLOTS == 2 ? slot ^ 1 : (slot + 1) % SLOTS;
     return now;
   }
   template <class Fetch>
-  __device__ __forceinline__ void one(long long row, long long rows, int to, const Fetch& fetch) {
+  __device__ __forceinline__ void one(uint32_t row, uint32_t rows, int to, const Fetch& fetch) {
     if (row < rows) fetch(row, to);
     else asm volatile("cp.async.commit_group;" ::: "memory");  // (groups are counted)
   }
 };
 
+// 1 / sqrt(v) to FP32's last place: the approximation and one Newton step (0 and infinity are past it).
+__device__ __forceinline__ float inverse_sqrt(float v) {
+  const float r = rsqrtf(v);
+  const float better = fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+  return v > 0.0f && v < INFINITY ? better : r;
+}
+
 // ---------------------------------------------------------------- forward
 
 template <int VPT, int SLOTS, int FORMAT, int ACCESS>
-__global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 128)) layer_norm_kernel(const LayerNormParams p) {
-  extern __shared__ uint4 fetched[];  // [SLOTS][2][VPT][threads]
+__global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const LayerNormParams p) {
+  extern __shared__ uint4 fetched[];  // [SLOTS][2][VPT][threads], then (KEPT) weight and bias: [2][VPT][threads]
   __shared__ float2 moments[2][32];   // a warp's mean and squares about it
   __shared__ float counts[32];        // its columns
   __shared__ uint32_t slots_max[2][32];
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint4* const mine = fetched + threadIdx.x;
+  const uint32_t rows = static_cast<uint32_t>(p.rows);
   const int slot_size = 2 * VPT * static_cast<int>(blockDim.x);
   pdl_launch_dependents();
   pdl_wait();
@@ -148,21 +156,32 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 128)) l
   const float count = warp_sum(static_cast<float>(size)), inverse_count = count > 0.0f ? 1.0f / count : 0.0f;
   if (lane == 0) counts[warp] = count;  // (read behind the first row's barrier)
   const float inverse_cols = 1.0f / static_cast<float>(p.cols);
-  auto fetch = [&](long long row, int slot) {
+  auto fetch = [&](uint32_t row, int slot) {
     const uint16_t* const rows[2] = {p.x + row * p.ldx, p.r != nullptr ? p.r + row * p.ldr : nullptr};
     fetch_rows<2, VPT, ACCESS>(mine + slot * slot_size, rows, col, p.cols, row);
   };
   // (groups past the row's end stay zero)
   for (int i = 0; i < SLOTS * 2 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
   Ring<SLOTS> ring;
-  ring.start(p.rows, fetch);
+  ring.start(rows, fetch);
+  // Weight and bias: in shared memory too, each thread's its own, so that registers do not bound the CTAs (with eight groups
+  // there is no room).
+  constexpr bool KEPT = VPT < 8;
+  uint4* const affine = mine + SLOTS * slot_size;
   uint4 w[VPT], b[VPT];
   load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
   load_bias<VPT, ACCESS>(b, p.b, col, p.cols);
+  if constexpr (KEPT) {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      affine[k * static_cast<int>(blockDim.x)] = w[k];
+      affine[(VPT + k) * static_cast<int>(blockDim.x)] = b[k];
+    }
+  }
   const bool starts = threadIdx.x < 32 && phase != 0;  // the warp with the row's start
   int parity = 0;
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
-    const uint4* const in = mine + ring.next(row, p.rows, fetch) * slot_size;
+  for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {  // (no sum of them passes 32 bits)
+    const uint4* const in = mine + ring.next(row, rows, fetch) * slot_size;
     P8 s[VPT];  // the stream (zeros outside the row), then the results
     uint64_t sum = 0;
 #pragma unroll
@@ -181,7 +200,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 128)) l
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum = f2_add(sum, s[k].v[j]);
     }
-    if (SLOTS == 1 && row + gridDim.x < p.rows) fetch(row + gridDim.x, 0);
+    if (SLOTS == 1 && row + gridDim.x < rows) fetch(row + gridDim.x, 0);
     const float warp_mean = warp_sum(pair_sum(sum)) * inverse_count;
     const uint64_t minus = f2_pack(-warp_mean, -warp_mean);
     uint64_t squares2 = 0;
@@ -225,7 +244,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 128)) l
       mean = about + shift;
       var = fmaxf(fmaf(-first, shift, second), 0.0f) * inverse_cols + (second - second);  // (NaN stays NaN)
     }
-    const float rstd = 1.0f / sqrtf(var + p.eps);
+    const float rstd = inverse_sqrt(var + p.eps);
     if (threadIdx.x == 0) {
       if (p.mean != nullptr) p.mean[row] = mean;
       if (p.rstd != nullptr) p.rstd[row] = rstd;
@@ -233,7 +252,8 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 64 : 72, 128)) l
     const uint64_t mean2 = f2_pack(-mean, -mean), rstd2 = f2_pack(rstd, rstd);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const P8 g = unpack8_pairs(w[k]), h = unpack8_pairs(b[k]);
+      const P8 g = unpack8_pairs(KEPT ? affine[k * static_cast<int>(blockDim.x)] : w[k]);
+      const P8 h = unpack8_pairs(KEPT ? affine[(VPT + k) * static_cast<int>(blockDim.x)] : b[k]);
       P8 y = {};
       by_group<ACCESS>(
           col[k], p.cols,
@@ -274,12 +294,13 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float2* slots, in
 }
 
 template <int VPT, int SLOTS, int ACCESS>
-__global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 96, 128))
+__global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
     layer_norm_backward_kernel(const LayerNormBackwardParams p) {
   extern __shared__ uint4 fetched[];  // [SLOTS][3][VPT][threads]
   __shared__ float2 slots[2][32];
   const int warps = blockDim.x >> 5;
   uint4* const mine = fetched + threadIdx.x;
+  const uint32_t rows = static_cast<uint32_t>(p.rows);
   const int slot_size = 3 * VPT * static_cast<int>(blockDim.x);
   pdl_launch_dependents();
   pdl_wait();
@@ -288,7 +309,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 96, 128))
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
     col[k] = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x)) - phase;
-  auto fetch = [&](long long row, int slot) {
+  auto fetch = [&](uint32_t row, int slot) {
     const uint16_t* const rows[3] = {p.s + row * p.lds, p.dy + row * p.lddy,
                                      p.ds != nullptr ? p.ds + row * p.ldds : nullptr};
     fetch_rows<3, VPT, ACCESS>(mine + slot * slot_size, rows, col, p.cols, row);
@@ -296,7 +317,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 96, 128))
   // (groups past the row's end stay zero)
   for (int i = 0; i < SLOTS * 3 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
   Ring<SLOTS> ring;
-  ring.start(p.rows, fetch);
+  ring.start(rows, fetch);
   uint4 w[VPT];
   P8 dw[VPT], db[VPT];
 #pragma unroll
@@ -308,13 +329,13 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 96, 128))
   const float inverse_cols = 1.0f / static_cast<float>(p.cols);
   float rstd = p.rstd[blockIdx.x], mean = p.mean[blockIdx.x], rstd_next = 0.0f, mean_next = 0.0f;
   int parity = 0;
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
-    const bool more = row + gridDim.x < p.rows;
+  for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {  // (no sum of them passes 32 bits)
+    const bool more = row + gridDim.x < rows;
     if (more) {
       rstd_next = p.rstd[row + gridDim.x];
       mean_next = p.mean[row + gridDim.x];
     }
-    const uint4* const in = mine + ring.next(row, p.rows, fetch) * slot_size;
+    const uint4* const in = mine + ring.next(row, rows, fetch) * slot_size;
     const uint64_t r2 = f2_pack(rstd, rstd), m2 = f2_pack(-mean, -mean);
     uint64_t sum1 = 0, sum2 = 0;
 #pragma unroll
@@ -401,17 +422,24 @@ __global__ void __launch_bounds__(32 * kSumWarps)
 
 // ---------------------------------------------------------------- host side
 
-// Threads, groups a thread and rows in shared memory. Rows of up to 256 columns are a warp each, without a barrier, and of
-// those an SM holds 32 at most, so three rows go ahead; wider ones as norm_shape's.
+// Threads, groups a thread and rows in shared memory. Measured on GB300, us:
+//   up to 256 columns a warp a row, without a barrier; an SM holds 32 of those at most, so three rows go ahead:
+//     65536 x 256 forward 26 with two groups a thread and one row ahead, 17 so; gradient 43 and 26;
+//   forward on the 16-byte boundary four groups a thread, as what a row costs whatever its length (some 130 instructions a
+//     warp, in reductions and addresses) is most of it: 4000 x 8192 to E4M3 40.3 with two and 37.3, 16000 x 1024 14.8 and
+//     12.7; off the boundary two: 2001 x 5123 16.3 and 17.8 with four, 16000 x 1023 28.6 and 36.4;
+//   gradient two, where 80 registers let an SM hold two CTAs: 8192 x 4096 50.4 and 54.0 with four, 2000 x 5120 19.2 and
+//     20.2, but 4000 x 8192 66.5 and 53.0.
 struct LayerNormShape {
   NormShape at;
   int slots;
-  int smem(int tensors) const { return slots * tensors * at.vpt * at.threads * 16; }
+  int smem(int tensors, int kept) const { return (slots * tensors + kept) * at.vpt * at.threads * 16; }
 };
-LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, bool is_aligned) {
+LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, bool is_aligned, bool forward) {
   const int groups = ceil_div(cols, 8) + (is_aligned ? 0 : 1);
   if (groups <= 32 && rows > num_sms) return LayerNormShape{{32, 1}, 4};
-  const NormShape s = norm_shape(rows, cols, num_sms, is_aligned);
+  NormShape s = norm_shape(rows, cols, num_sms, is_aligned);
+  if (s.vpt == 2 && is_aligned && groups > (forward ? 96 : 800)) s = NormShape{ceil_div(ceil_div(groups, 4), 32) * 32, 4};
   return LayerNormShape{s, norm_slots(s.vpt)};
 }
 
@@ -509,12 +537,12 @@ int gemm_layer_norm(const void* X, const void* R, const void* W, const void* B, 
   int device = 0, err = 0;
   const DeviceInfo* info = current_device_info(&device, &err);
   if (info == nullptr) return err;
-  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, aligned);
+  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, aligned, true);
   const void* kernel = format == GEMM_NORM_NVFP4  ? forward_kernel<GEMM_NORM_NVFP4, kAligned>(shape)
                        : format == GEMM_NORM_E4M3 ? forward_kernel<GEMM_NORM_E4M3>(shape, aligned, shared)
                                                   : forward_kernel<GEMM_NORM_BF16>(shape, aligned, shared);
   void* args[] = {&p};
-  const int smem = shape.smem(2);
+  const int smem = shape.smem(2, shape.at.vpt < 8 ? 2 : 0);
   const int grid = norm_grid(kernel, rows, shape.at.threads, smem, info->num_sms);
   if (grid == 0) return GEMM_ERR_LAUNCH;
   return norm_launch(kernel, dim3(grid), shape.at.threads, smem, static_cast<cudaStream_t>(stream), args);
@@ -564,11 +592,11 @@ int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const
   const bool shared = RowPlace(dY, p.lddy, 2) == place && (dS == nullptr || RowPlace(dS, p.ldds, 2) == place) &&
                       RowPlace(dX, p.lddx, 2) == place;
   const bool aligned = shared && place.aligned() && cols % 8 == 0 && !misaligned(W, 16);
-  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, aligned);
+  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, aligned, false);
   const void* kernel = aligned  ? backward_kernel<kAligned>(shape)
                        : shared ? backward_kernel<kShared>(shape)
                                 : backward_kernel<kElements>(shape);
-  const int smem = shape.smem(3);
+  const int smem = shape.smem(3, 0);
   const int grid = norm_grid(kernel, rows, shape.at.threads, smem, info->num_sms);
   if (grid == 0) return GEMM_ERR_LAUNCH;
   void* ws = nullptr;
