@@ -450,6 +450,17 @@ int loss_launch(LossParams& p, LossKernel k, const void* X, long long ldx, const
   return pair_launch(loss_kernel_of(k), args, wide, clusters, stream);
 }
 
+// Rows of 8 columns at a time, `vectors` of them to a row, into rows `ldo` apart.
+__global__ void __launch_bounds__(256) copy_rows_kernel(const uint16_t* x, long long ldx, uint16_t* out, long long ldo,
+                                                        int vectors, long long total) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long i = blockIdx.x * 256LL + threadIdx.x;
+  if (i >= total) return;
+  const long long row = i / vectors, v = i - row * vectors;
+  *reinterpret_cast<uint4*>(out + row * ldo + 8 * v) = *reinterpret_cast<const uint4*>(x + row * ldx + 8 * v);
+}
+
 template <class... Params, class... Args>
 int simple_launch(void (*kernel)(Params...), int grid, int threads, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
@@ -467,6 +478,22 @@ int simple_launch(void (*kernel)(Params...), int grid, int threads, cudaStream_t
   }
   count_launch();
   return GEMM_OK;
+}
+
+// A 128-byte row of a TMA box that starts off a 128-byte boundary costs a fifth sector and a second line of L2, which large
+// launches feel: 1500 x 50001 x 2056 takes 221 us forward where 2048 deep takes 176. X, which every tile of columns reads
+// again, is worth a copy in rows that start on the boundary where its products are large (W, as large as what is read of
+// it, is not). With the copy it takes 204 forward, and 568
+// instead of 596 for the gradient; 8192 x 32001 x 1000 339 and 382 without, 970 and 1022.
+bool copy_pays(const void* X, long long ldx, int M, int vocab, int K) {
+  const bool on_boundary = (reinterpret_cast<uintptr_t>(X) & 127u) == 0 && ldx % 64 == 0;
+  return !on_boundary && 2.0 * M * vocab * K > 1e11 && vocab > 4096;
+}
+long long copy_stride(int K) { return (K + 63LL) / 64 * 64; }
+int copy_rows(const void* X, long long ldx, void* out, int M, int K, cudaStream_t stream) {
+  const long long total = static_cast<long long>(M) * (K / 8);
+  return simple_launch(copy_rows_kernel, static_cast<int>((total + 255) / 256), 256, stream,
+                       static_cast<const uint16_t*>(X), ldx, static_cast<uint16_t*>(out), copy_stride(K), K / 8, total);
 }
 
 bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
@@ -545,16 +572,24 @@ int gemm_cross_entropy(const void* X, const void* W, const long long* targets, f
     extra = size_t(wave) * L::TILE_M;  // (at most half a wave's tiles are cut in halves)
   }
   const size_t parts = size_t(j.count) * M;
+  const size_t copy = !few && copy_pays(X, ld.x, M, vocab, K) ? size_t(M) * copy_stride(K) * 2 : 0;  // a multiple of 128
   cudaMemPool_t pool = workspace_pool(device);
   void* ws = nullptr;
   if (pool == nullptr ||
-      cudaMallocFromPoolAsync(&ws, (parts + extra) * sizeof(float2) + size_t(M) * 4, pool, s) != cudaSuccess) {
+      cudaMallocFromPoolAsync(&ws, copy + (parts + extra) * sizeof(float2) + size_t(M) * 4, pool, s) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_OUT_OF_MEMORY;
   }
-  float2* const seen = static_cast<float2*>(ws);
+  if (copy > 0) {
+    st = copy_rows(X, ld.x, ws, M, K, s);
+    X = ws;
+    ld.x = copy_stride(K);
+  }
+  float2* const seen = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + copy);
   float* const target_z = reinterpret_cast<float*>(seen + parts + extra);
-  if (few) {
+  if (st != GEMM_OK) {
+    // (nothing to launch)
+  } else if (few) {
     st = run_loss_rows(LossRowsOperands{X, W, targets, seen, target_z, ld.x, M, vocab, K, scale}, device, info, s);
   } else {
     p.scale = scale;
@@ -604,7 +639,7 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
   }
   const int piece = gemm_cross_entropy_piece(M, vocab, workspace);
   const bool pieces = piece < vocab;
-  const long long ldg = static_cast<long long>(round_up(piece, 8));
+  const long long ldg = static_cast<long long>(round_up(piece, 64));  // (rows on 128-byte boundaries, see copy_rows)
   const int wave = loss_max_clusters(device, kGrad);
   if (wave <= 0) return GEMM_ERR_LAUNCH;
 
@@ -632,13 +667,20 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
   int st = pair_gradient_plan(q, device, &plan);
   if (st != GEMM_OK) return st;
   const size_t g_bytes = round_up(size_t(M) * ldg * 2, 256);
+  const size_t copy = copy_pays(X, ld.x, M, vocab, K) ? round_up(size_t(M) * copy_stride(K) * 2, 256) : 0;
   cudaMemPool_t pool = workspace_pool(device);
   void* ws = nullptr;
-  if (pool == nullptr || cudaMallocFromPoolAsync(&ws, g_bytes + plan.sums * 4, pool, s) != cudaSuccess) {
+  if (pool == nullptr || cudaMallocFromPoolAsync(&ws, g_bytes + copy + plan.sums * 4, pool, s) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_OUT_OF_MEMORY;
   }
-  float* const sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + g_bytes);
+  if (copy > 0) {
+    void* const to = static_cast<uint8_t*>(ws) + g_bytes;
+    st = copy_rows(X, ld.x, to, M, K, s);
+    q.x = X = to;
+    q.ldx = ld.x = copy_stride(K);
+  }
+  float* const sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + g_bytes + copy);
   q.g[0] = ws;
   const int slices = q.most_slices = plan.p.main.slices;
   const bool join = plan.sums > 0;

@@ -97,22 +97,22 @@ __device__ __forceinline__ void load_bias(uint4 (&b)[VPT], const uint16_t* bias,
   }
 }
 
-// The rows of a CTA on their way: SLOTS of them in shared memory, the current one and those fetched ahead (1: the next one is
+// The rows of a CTA (or a team) on their way, `step` apart: SLOTS of them in shared memory, the current one and those fetched ahead (1: the next one is
 // fetched once the current one is read).
 template <int SLOTS>
 struct Ring {
   int slot = 0;
   // Before the first row: fetch(row, slot) for as many as go ahead.
   template <class Fetch>
-  __device__ __forceinline__ void start(uint32_t rows, const Fetch& fetch) {
+  __device__ __forceinline__ void start(uint32_t row, uint32_t step, uint32_t rows, const Fetch& fetch) {
 #pragma unroll
-    for (int i = 0; i < (SLOTS > 1 ? SLOTS - 1 : 1); ++i) one(blockIdx.x + i * gridDim.x, rows, i, fetch);
+    for (int i = 0; i < (SLOTS > 1 ? SLOTS - 1 : 1); ++i) one(row + i * step, rows, i, fetch);
   }
   // Fetches the row that is SLOTS - 1 behind `row`, waits for `row` and gives its slot.
   template <class Fetch>
-  __device__ __forceinline__ int next(uint32_t row, uint32_t rows, const Fetch& fetch) {
+  __device__ __forceinline__ int next(uint32_t row, uint32_t step, uint32_t rows, const Fetch& fetch) {
     if (SLOTS > 1)
-      one(row + (SLOTS - 1) * gridDim.x, rows, SLOTS == 2 ? slot ^ 1 : (slot + SLOTS - 1) % SLOTS, fetch);
+      one(row + (SLOTS - 1) * step, rows, SLOTS == 2 ? slot ^ 1 : (slot + SLOTS - 1) % SLOTS, fetch);
     asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
     const int now = slot;
     slot = SLOTS == 2 ? slot ^ 1 : (slot + 1) % SLOTS;
@@ -163,7 +163,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const Lay
   // (groups past the row's end stay zero)
   for (int i = 0; i < SLOTS * 2 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
   Ring<SLOTS> ring;
-  ring.start(rows, fetch);
+  ring.start(blockIdx.x, gridDim.x, rows, fetch);
   // Weight and bias: in shared memory too, each thread's its own, so that registers do not bound the CTAs (with eight groups
   // there is no room).
   constexpr bool KEPT = VPT < 8;
@@ -181,7 +181,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const Lay
   const bool starts = threadIdx.x < 32 && phase != 0;  // the warp with the row's start
   int parity = 0;
   for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {  // (no sum of them passes 32 bits)
-    const uint4* const in = mine + ring.next(row, rows, fetch) * slot_size;
+    const uint4* const in = mine + ring.next(row, gridDim.x, rows, fetch) * slot_size;
     P8 s[VPT];  // the stream (zeros outside the row), then the results
     uint64_t sum = 0;
 #pragma unroll
@@ -293,15 +293,21 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float2* slots, in
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-template <int VPT, int SLOTS, int ACCESS>
+// TEAMS: rows of a warp, kTeams of them in a CTA at a time, so that the gradients of weight and bias leave a CTA as one
+// partial row instead of eight. Measured on GB300 with them: 65536 x 256 39 us in CTAs of a warp and 27, 8192 x 512 20 and
+// 15. (Wider rows lose by it what they gain: with as many teams as an SM holds 8192 x 4096 58 and 61.)
+constexpr int kTeams = 8;
+template <int VPT, int SLOTS, int ACCESS, bool TEAMS>
 __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
     layer_norm_backward_kernel(const LayerNormBackwardParams p) {
-  extern __shared__ uint4 fetched[];  // [SLOTS][3][VPT][threads]
+  extern __shared__ uint4 fetched[];  // [teams][SLOTS][3][VPT][threads]
   __shared__ float2 slots[2][32];
   const int warps = blockDim.x >> 5;
-  uint4* const mine = fetched + threadIdx.x;
+  const int team = TEAMS ? static_cast<int>(threadIdx.y) : 0;
+  const uint32_t first_row = blockIdx.x + (TEAMS ? gridDim.x * team : 0u), step = gridDim.x * (TEAMS ? kTeams : 1);
   const uint32_t rows = static_cast<uint32_t>(p.rows);
   const int slot_size = 3 * VPT * static_cast<int>(blockDim.x);
+  uint4* const mine = fetched + team * SLOTS * slot_size + threadIdx.x;
   pdl_launch_dependents();
   pdl_wait();
   const int phase = ACCESS == kAligned ? 0 : row_phase(p.s + blockIdx.x * p.lds);
@@ -317,7 +323,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
   // (groups past the row's end stay zero)
   for (int i = 0; i < SLOTS * 3 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
   Ring<SLOTS> ring;
-  ring.start(rows, fetch);
+  ring.start(first_row, step, rows, fetch);
   uint4 w[VPT];
   P8 dw[VPT], db[VPT];
 #pragma unroll
@@ -327,15 +333,19 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
   load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
   const bool starts = threadIdx.x < 32 && phase != 0;  // the warp with the row's start
   const float inverse_cols = 1.0f / static_cast<float>(p.cols);
-  float rstd = p.rstd[blockIdx.x], mean = p.mean[blockIdx.x], rstd_next = 0.0f, mean_next = 0.0f;
+  float rstd = 0.0f, mean = 0.0f, rstd_next = 0.0f, mean_next = 0.0f;
+  if (!TEAMS || first_row < rows) {
+    rstd = p.rstd[first_row];
+    mean = p.mean[first_row];
+  }
   int parity = 0;
-  for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {  // (no sum of them passes 32 bits)
-    const bool more = row + gridDim.x < rows;
+  for (uint32_t row = first_row; row < rows; row += step, parity ^= 1) {  // (no sum of them passes 32 bits)
+    const bool more = row + step < rows;
     if (more) {
-      rstd_next = p.rstd[row + gridDim.x];
-      mean_next = p.mean[row + gridDim.x];
+      rstd_next = p.rstd[row + step];
+      mean_next = p.mean[row + step];
     }
-    const uint4* const in = mine + ring.next(row, rows, fetch) * slot_size;
+    const uint4* const in = mine + ring.next(row, step, rows, fetch) * slot_size;
     const uint64_t r2 = f2_pack(rstd, rstd), m2 = f2_pack(-mean, -mean);
     uint64_t sum1 = 0, sum2 = 0;
 #pragma unroll
@@ -375,11 +385,12 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
       }
       store8<ACCESS>(p.dx + row * p.lddx, col[k], p.cols, pack8_pairs(o));
     }
-    if (SLOTS == 1 && more) fetch(row + gridDim.x, 0);
+    if (SLOTS == 1 && more) fetch(row + step, 0);
     rstd = rstd_next;
     mean = mean_next;
   }
-  if (p.partial != nullptr) {  // through shared memory, so that a warp writes 32 columns side by side
+  if (p.partial != nullptr) {  // through shared memory: teams are added there, and a warp writes 32 columns side by side
+    const int team_floats = SLOTS * slot_size * 4, threads = static_cast<int>(blockDim.x * blockDim.y);
     float* const sums = reinterpret_cast<float*>(fetched);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -387,13 +398,19 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const P8& v = t == 0 ? dw[k] : db[k];
-        ulonglong2* at = reinterpret_cast<ulonglong2*>(sums + col[k] + phase);
+        ulonglong2* at = reinterpret_cast<ulonglong2*>(sums + team * team_floats + col[k] + phase);
         at[0] = make_ulonglong2(v.v[0], v.v[1]);
         at[1] = make_ulonglong2(v.v[2], v.v[3]);
       }
       __syncthreads();
       float* out = p.partial + (2LL * blockIdx.x + t) * p.cols;
-      for (int c = threadIdx.x; c < p.cols; c += blockDim.x) out[c] = sums[c + phase];
+      for (int c = team * static_cast<int>(blockDim.x) + threadIdx.x; c < p.cols; c += threads) {
+        float v = sums[c + phase];
+        if (TEAMS)
+#pragma unroll
+          for (int i = 1; i < kTeams; ++i) v += sums[i * team_floats + c + phase];
+        out[c] = v;
+      }
     }
   }
 }
@@ -462,14 +479,17 @@ const void* forward_kernel(const LayerNormShape& s, bool aligned, bool shared) {
 }
 
 template <int ACCESS>
-const void* backward_kernel(const LayerNormShape& s) {
+const void* backward_kernel(const LayerNormShape& s, bool teams) {
   switch (s.at.vpt) {
     case 1:
-      return s.slots == 1 ? reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 1, ACCESS>)
-                          : reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 4, ACCESS>);
-    case 2: return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 2, ACCESS>);
-    case 4: return reinterpret_cast<const void*>(layer_norm_backward_kernel<4, 2, ACCESS>);
-    default: return reinterpret_cast<const void*>(layer_norm_backward_kernel<8, 1, ACCESS>);
+      return teams          ? reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 4, ACCESS, true>)
+             : s.slots == 1 ? reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 1, ACCESS, false>)
+                            : reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 4, ACCESS, false>);
+    case 2:
+      return teams ? reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 2, ACCESS, true>)
+                   : reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 2, ACCESS, false>);
+    case 4: return reinterpret_cast<const void*>(layer_norm_backward_kernel<4, 2, ACCESS, false>);
+    default: return reinterpret_cast<const void*>(layer_norm_backward_kernel<8, 1, ACCESS, false>);
   }
 }
 
@@ -545,7 +565,7 @@ int gemm_layer_norm(const void* X, const void* R, const void* W, const void* B, 
   const int smem = shape.smem(2, shape.at.vpt < 8 ? 2 : 0);
   const int grid = norm_grid(kernel, rows, shape.at.threads, smem, info->num_sms);
   if (grid == 0) return GEMM_ERR_LAUNCH;
-  return norm_launch(kernel, dim3(grid), shape.at.threads, smem, static_cast<cudaStream_t>(stream), args);
+  return norm_launch(kernel, dim3(grid), dim3(shape.at.threads), smem, static_cast<cudaStream_t>(stream), args);
 }
 
 int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const float* mean, const float* rstd,
@@ -593,11 +613,14 @@ int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const
                       RowPlace(dX, p.lddx, 2) == place;
   const bool aligned = shared && place.aligned() && cols % 8 == 0 && !misaligned(W, 16);
   const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, aligned, false);
-  const void* kernel = aligned  ? backward_kernel<kAligned>(shape)
-                       : shared ? backward_kernel<kShared>(shape)
-                                : backward_kernel<kElements>(shape);
-  const int smem = shape.smem(3, 0);
-  const int grid = norm_grid(kernel, rows, shape.at.threads, smem, info->num_sms);
+  // (a grid of a multiple of 8, or a row a team: rows of a CTA share the column at which their boundary lies)
+  const bool teams = sums && shape.at.threads == 32 && rows > info->num_sms && info->num_sms % 8 == 0;
+  const void* kernel = aligned  ? backward_kernel<kAligned>(shape, teams)
+                       : shared ? backward_kernel<kShared>(shape, teams)
+                                : backward_kernel<kElements>(shape, teams);
+  const dim3 threads(shape.at.threads, teams ? kTeams : 1);
+  const int smem = shape.smem(3, 0) * static_cast<int>(threads.y);
+  const int grid = norm_grid(kernel, rows, static_cast<int>(threads.x * threads.y), smem, info->num_sms);
   if (grid == 0) return GEMM_ERR_LAUNCH;
   void* ws = nullptr;
   if (sums) {
@@ -610,14 +633,14 @@ int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const
     p.partial = static_cast<float*>(ws);
   }
   void* args[] = {&p};
-  int rc = norm_launch(kernel, dim3(grid), shape.at.threads, smem, st, args);
+  int rc = norm_launch(kernel, dim3(grid), threads, smem, st, args);
   if (ws != nullptr) {
     if (rc == GEMM_OK) {
       const float* partial = p.partial;
       int partial_rows = grid;
       void* sum_args[] = {&partial, &partial_rows, &cols, &dW, &dB};
-      rc = norm_launch(reinterpret_cast<const void*>(layer_norm_sum_kernel), dim3(ceil_div(cols, 32), 2), 32 * kSumWarps,
-                       0, st, sum_args);
+      rc = norm_launch(reinterpret_cast<const void*>(layer_norm_sum_kernel), dim3(ceil_div(cols, 32), 2),
+                       dim3(32 * kSumWarps), 0, st, sum_args);
     }
     if (cudaFreeAsync(ws, st) != cudaSuccess && rc == GEMM_OK) rc = GEMM_ERR_LAUNCH;
   }

@@ -344,11 +344,11 @@ inline int norm_grid(const void* kernel, int rows, int threads, int smem, int nu
   return std::min(rows, std::max(8, num_sms * resident_ctas(kernel, threads, smem) / 8 * 8));
 }
 
-inline int norm_launch(const void* kernel, dim3 grid, int threads, int smem, cudaStream_t stream, void** args) {
+inline int norm_launch(const void* kernel, dim3 grid, dim3 threads, int smem, cudaStream_t stream, void** args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.blockDim = threads;
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
