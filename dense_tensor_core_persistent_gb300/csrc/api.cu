@@ -192,9 +192,9 @@ int resident_ctas(const void* kernel, int threads, int smem) {
     int threads, smem, ctas;
   };
   // Every size of every kernel that asks: a norm's seven forward kernels with one group a thread take 32 thread counts,
-  // with two 16, with four and eight 8 each, and so do its three backward ones: 640 for each of the two norms, and ten
-  // more for the layer norm's narrow rows.
-  constexpr int kEntries = 1290;
+  // with two 16, with four and eight 8 each, and so do its three backward ones: 640 for each of the two norms, and 32
+  // more for the layer norm's narrow rows and its gradient with three rows at a time.
+  constexpr int kEntries = 1312;
   static std::mutex mu;
   static Entry entries[kEntries];
   static int count = 0;

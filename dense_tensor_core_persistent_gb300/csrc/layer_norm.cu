@@ -446,7 +446,8 @@ __global__ void __launch_bounds__(32 * kSumWarps)
 //     warp, in reductions and addresses) is most of it: 4000 x 8192 to E4M3 40.3 with two and 37.3, 16000 x 1024 14.8 and
 //     12.7; off the boundary two: 2001 x 5123 16.3 and 17.8 with four, 16000 x 1023 28.6 and 36.4;
 //   gradient two, where 80 registers let an SM hold two CTAs: 8192 x 4096 50.4 and 54.0 with four, 2000 x 5120 19.2 and
-//     20.2, but 4000 x 8192 66.5 and 53.0.
+//     20.2, but 4000 x 8192 66.5 and 53.0; on the boundary with two rows ahead instead of one: 8192 x 4096 50.9 and 47.0,
+//     2000 x 5120 19.2 and 17.4 (off it 2001 x 5123 25.4 and 26.2).
 struct LayerNormShape {
   NormShape at;
   int slots;
@@ -457,7 +458,8 @@ LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, bool is_aligned
   if (groups <= 32 && rows > num_sms) return LayerNormShape{{32, 1}, 4};
   NormShape s = norm_shape(rows, cols, num_sms, is_aligned);
   if (s.vpt == 2 && is_aligned && groups > (forward ? 96 : 800)) s = NormShape{ceil_div(ceil_div(groups, 4), 32) * 32, 4};
-  return LayerNormShape{s, norm_slots(s.vpt)};
+  const bool three = s.vpt == 2 && is_aligned && !forward && s.threads > 32;
+  return LayerNormShape{s, three ? 3 : norm_slots(s.vpt)};
 }
 
 template <int FORMAT, int ACCESS>
@@ -486,6 +488,8 @@ const void* backward_kernel(const LayerNormShape& s, bool teams) {
              : s.slots == 1 ? reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 1, ACCESS, false>)
                             : reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 4, ACCESS, false>);
     case 2:
+      if constexpr (ACCESS == kAligned)
+        if (s.slots == 3) return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 3, ACCESS, false>);
       return teams ? reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 2, ACCESS, true>)
                    : reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 2, ACCESS, false>);
     case 4: return reinterpret_cast<const void*>(layer_norm_backward_kernel<4, 2, ACCESS, false>);
