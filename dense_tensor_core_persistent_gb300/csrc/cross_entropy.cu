@@ -651,6 +651,7 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
   q.rows = M;
   q.K = K;
   q.parts = 1;
+  q.even = true;
   q.keep_sums = pieces && dX != nullptr;
   auto at = [&](const void* p, int row) {
     return static_cast<void*>(const_cast<uint16_t*>(static_cast<const uint16_t*>(p)) + static_cast<long long>(row) * K);

@@ -191,6 +191,21 @@ int gradient_slices(const PairProduct& dx, const PairProduct& dw, int wave) {
   return slices > 1 && dx.k_iters - dx.k_iters / slices >= 12 ? slices : 1;
 }
 
+// What a tile of dW costs, in stages: a shallow one is bound by its store (64 rows x 32768 x 4096: 2.1 us a tile, where a
+// stage of dX takes 0.85).
+double shallow_cost(const PairProduct& dw) { return std::max<double>(dw.k_iters, 2.5); }
+
+// The same where the features are a piece of a large vocabulary: as many parts as bring a tile of dX within a twelfth of an
+// even share of the launch. Measured on GB300, whole gradient of the cross entropy, by parts (in parentheses a whole tile in
+// shares): 64 x 131072 x 4096 876 us in one, 638, 608, 582 in two to four (2.1); 700 x 50000 x 776 317 in one, 206, 166, 171
+// in two to four (3.2); 200 x 131072 x 1024 391, 254, 210, 190, 195 in two, four, six, eight, twelve (8.4); 128 x 8192 x
+// 8192, which stays whole, 99 and 105 in two (1.06).
+int gradient_slices_even(const PairProduct& dx, const PairProduct& dw, int wave) {
+  const double share = (1.0 * dx.num_tiles * dx.k_iters + dw.num_tiles * shallow_cost(dw)) / wave;
+  const int slices = static_cast<int>(dx.k_iters / std::max(share, 6.0) + 0.92);
+  return std::max(1, std::min(slices, 16));
+}
+
 // The order of a product's tiles on `clusters` pairs, for operands of `bytes` per element.
 void order_product(PairProduct* q, int clusters, int tile_rows, double bytes, long long l2_bytes) {
   constexpr int BLOCK_N = PairLayout::BLOCK_N;
@@ -285,7 +300,7 @@ bool pair_wide_rule(long long std_tiles, long long wide_tiles, int depth, int wa
   return depth >= 2048 && 2.0 * launch_tile_times(wide_tiles, wave) / 1.06 < launch_tile_times(std_tiles, wave);
 }
 
-int pair_schedule(PairParams* p, bool wide, double bytes, int wave, int device, const DeviceInfo* info) {
+int pair_schedule(PairParams* p, bool wide, double bytes, int wave, int device, const DeviceInfo* info, bool even) {
   using L = PairLayout;
   p->status = device_status_word(device);
   p->wait_limit_ns = RunOptions().wait_limit_ns;
@@ -300,7 +315,9 @@ int pair_schedule(PairParams* p, bool wide, double bytes, int wave, int device, 
     const int clusters = std::min(a.num_items + b.num_tiles, wave);
     const int in_last = a.num_items % clusters, idle = in_last > 0 ? clusters - in_last : 0;
     if (idle > 0)
-      p->ahead = std::min((a.k_iters / a.slices + b.k_iters / 2) / b.k_iters, ceil_div(b.num_tiles, idle));
+      p->ahead = std::min(even ? static_cast<int>(a.k_iters / a.slices / shallow_cost(b))
+                               : (a.k_iters / a.slices + b.k_iters / 2) / b.k_iters,
+                          ceil_div(b.num_tiles, idle));
     const int rest = std::max(0, b.num_tiles - p->ahead * idle);
     b.split_tiles = tail_split_tiles(rest, wave);
     b.num_items = b.num_tiles + b.split_tiles;
@@ -352,7 +369,8 @@ int pair_gradient_plan(const PairGradient& q, int device, PairGradientPlan* plan
     st = pair_plan_product(&p.second, q.features[0], q.K, q.rows, stage, 1, q.parts, tile_rows, L::BLOCK_N);
   if (st != GEMM_OK) return st;
   if (q.dx != nullptr) {
-    if (!plan->wide) p.main.slices = gradient_slices(p.main, p.second, wave);
+    if (!plan->wide)
+      p.main.slices = q.even ? gradient_slices_even(p.main, p.second, wave) : gradient_slices(p.main, p.second, wave);
     if (q.most_slices > 0) p.main.slices = std::min(p.main.slices, q.most_slices);
     p.main.num_items = p.main.num_tiles * p.main.slices;
     p.main.slice_rows = ceil_div(q.rows, 32) * 32;
@@ -388,7 +406,7 @@ int pair_gradient_launch(const PairGradient& q, PairGradientPlan* plan, float* s
   if (st != GEMM_OK) return st;
   const int wave = gradient_max_clusters(device, plan->wide);
   if (wave <= 0) return GEMM_ERR_LAUNCH;
-  const int clusters = pair_schedule(&p, plan->wide, 2.0, wave, device, info);
+  const int clusters = pair_schedule(&p, plan->wide, 2.0, wave, device, info, q.even);
   if (clusters < 0) return -clusters;
   void* args[] = {&m, &p};
   return pair_launch(plan->wide ? reinterpret_cast<const void*>(gradient_wide_kernel)

@@ -736,7 +736,8 @@ bool pair_wide_rule(long long std_tiles, long long wide_tiles, int depth, int wa
 
 // Fills in what a launch on `wave` co-resident pairs needs (halves of tiles, who goes ahead, orders; `bytes` per
 // element of the operands) and gives its pairs; a negative status on an error.
-int pair_schedule(PairParams* p, bool wide, double bytes, int wave, int device, const DeviceInfo* info);
+// even: see PairGradient.
+int pair_schedule(PairParams* p, bool wide, double bytes, int wave, int device, const DeviceInfo* info, bool even = false);
 
 // Launches `kernel` with the arguments of `args` on `clusters` pairs.
 int pair_launch(const void* kernel, void** args, bool wide, int clusters, cudaStream_t stream);
@@ -748,6 +749,7 @@ struct PairGradient {
   void *dx, *dw[2];  // either may be null
   int rows, features[2], K, parts;  // features[0] >= features[1]
   int most_slices;   // of dX's sum (0: no limit)
+  bool even;         // the parts of dX's sum by an even share of the launch, and shallow tiles of dW by their store
   bool keep_sums;    // dX stays in `sums` (FP32), to be joined later
   bool add;          // and is added to what is there
 };

@@ -671,8 +671,9 @@ typedef struct {
  * its digits, and no loss is below 0. An infinity or NaN in a row of X makes that row's outputs NaN.
  * Constraints: M, vocab, K >= 0; K % 8 == 0; X and W 16-byte aligned. Any M and vocab. M == 0: nothing to do. vocab == 0
  * with rows: GEMM_ERR_INVALID_ARG. K == 0: every logit is 0.
- * Two kernel launches, asynchronous on `stream`, and a workspace from the library's stream-ordered pool of 16 bytes for
- * each row and 256 columns of the vocabulary (and up to 1 MB). The same inputs give the same bits.
+ * Two kernel launches (and one that copies X, see below), asynchronous on `stream`, and a workspace from the library's
+ * stream-ordered pool: 16 bytes for each row and 256 columns of the vocabulary and up to 1 MB, up to 64 rows 8 bytes for
+ * each row and SM. The same inputs give the same bits.
  */
 int gemm_cross_entropy(const void* X, const void* W, const long long* targets, float* loss, float* lse, int M, int vocab,
                        int K, float scale, void* stream, const gemm_cross_entropy_strides_t* strides);
@@ -690,7 +691,9 @@ int gemm_cross_entropy(const void* X, const void* W, const long long* targets, f
  * Constraints as gemm_cross_entropy; dX and dW 16-byte aligned. M == 0 sets dW to zero.
  * Two kernel launches a piece. Where dX needs FP32 sums (several pieces, or few tiles and so slices of its sum) one more
  * launch, and 4 K bytes more of workspace for each row (M rounded up to a multiple of 32) and slice, of which there are up
- * to 8. The workspace comes from the library's stream-ordered pool. The same inputs give the same bits.
+ * to 16. Where rows of X do not start on 128-byte boundaries and the products are large, one more copies X to rows that do
+ * (2 K bytes a row of workspace; the forward call does so too). The workspace comes from the library's stream-ordered pool.
+ * The same inputs give the same bits.
  */
 int gemm_cross_entropy_backward(const void* X, const void* W, const long long* targets, const float* lse,
                                 const float* dloss, const float* dlse, void* dX, void* dW, int M, int vocab, int K,
