@@ -624,14 +624,29 @@ def matmul_nvfp4(A, SFA, B, SFB, out=None, stream=None, opts=None):
     return out
 
 
+_device = None
+
+
+def _elsewhere(t) -> bool:
+    """Whether a CUDA tensor lies on another device than the current one, on which the call would run."""
+    global _device
+    if _device is None:
+        import torch
+        _device = torch._C._cuda_getDevice
+    return t.get_device() != _device()
+
+
 def _matrix(t, what, dtype, shape=None):
-    """A CUDA matrix of `dtype` whose rows are contiguous -> its row stride (0: rows follow one another)."""
+    """A CUDA matrix of `dtype` on the current device whose rows are contiguous -> its row stride (0: rows follow one
+    another)."""
     if t is None:
         raise ValueError(f"{what}: a CUDA {dtype} matrix is needed, got None")
     size = t.shape
     if t.dtype is not dtype or len(size) != 2 or not t.is_cuda or (shape is not None and size != shape):
         want = "" if shape is None else f" of shape {tuple(shape)}"
         raise ValueError(f"{what}: a CUDA {dtype} matrix{want} is needed, got {t.dtype} {tuple(size)} on {t.device}")
+    if _elsewhere(t):
+        raise ValueError(f"{what}: lies on {t.device}, which is not the current device")
     if t.is_contiguous():
         return 0
     rows, cols = size
@@ -654,6 +669,8 @@ def _vector(t, what, dtype, n):
         raise ValueError(f"{what}: a CUDA {dtype} vector of {n} is needed, got None")
     if t.dtype is not dtype or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous CUDA {dtype} vector of {n} is needed, got {t.dtype} {tuple(t.shape)}")
+    if _elsewhere(t):
+        raise ValueError(f"{what}: lies on {t.device}, which is not the current device")
     return t
 
 

@@ -109,7 +109,7 @@ struct LossRow {
   __device__ __forceinline__ void begin(const LossParams& p, int row) {
     target = p.targets != nullptr && row < p.main.rows ? p.targets[row] : -1;
     part = SoftmaxPart{-INFINITY, -1.0f};  // an empty set: joined to another it adds (-1 + 1) exp(-inf) = 0
-    c = p.scale * kLog2e;
+    c = log2_scale(p.scale);
   }
   __device__ __forceinline__ void chunk(const LossParams& p, float (&v)[32], int row, int col) {
     const long long t = target - col;
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) loss_join_kernel(const LossJo
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float c = p.scale * kLog2e;
+  const float c = log2_scale(p.scale);
   SoftmaxPart part{-INFINITY, -1.0f};
   {
     const int row = blockIdx.x * 32 + lane;

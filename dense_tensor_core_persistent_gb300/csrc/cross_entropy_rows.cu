@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
     }
   }
   float2* const joined = reinterpret_cast<float2*>(smem + L::OFF_JOIN);
-  const float c = p.x.scale * kLog2e;
+  const float c = log2_scale(p.x.scale);
   if (warp >= L::EPI_WARP0) {
     // ------------------------------------------------------------ epilogue
     const uint32_t q = warp & 3u;                                    // TMEM lanes 32q .. 32q+31

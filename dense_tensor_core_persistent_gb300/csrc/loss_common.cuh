@@ -8,6 +8,9 @@ namespace dtcp {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// scale / ln 2; finite, so that equal logits stay apart by nothing.
+__device__ __forceinline__ float log2_scale(float scale) { return fminf(scale * kLog2e, 3.4028234663852886e38f); }
+
 // The maximum of a set of logits and the sum of exp(scale (z - m)) over all of them but one that is the maximum.
 struct SoftmaxPart {
   float m, others;

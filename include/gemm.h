@@ -643,7 +643,8 @@ int gemm_embedding(const void* table, int type, const long long* tokens, void* Y
  * rounded once.
  *   dY: rows x cols of dy_type, row stride ldd elements (0 = cols), element-aligned.
  *   base: vocab x cols of table_type, contiguous: what is there already (with tied weights the head's dW, from
- *   gemm_cross_entropy_backward); NULL: zeros. base may be dtable: then only the rows of given tokens are written.
+ *   gemm_cross_entropy_backward); NULL: zeros. base may be dtable: then only the rows of given tokens are written;
+ *   else they do not overlap.
  *   dtable: vocab x cols of table_type, contiguous. dtable and base are 16-byte aligned, in place element-aligned.
  *   tokens: rows int64; a negative token or one >= vocab takes no part (its row of dY is not read).
  * Constraints: vocab < 2^27, cols <= 4194304, scale finite. rows == 0: dtable is base or zeros.
@@ -686,7 +687,7 @@ int gemm_cross_entropy(const void* X, const void* W, const long long* targets, f
  *   dloss, dlse: M FP32. targets and dloss may both be NULL, and dlse. A negative target takes no part (its dloss is not
  *   read into the row); a target >= vocab makes the row of G NaN. A row that no gradient reaches (dloss and dlse 0 or
  *   absent) has a G of 0 whatever its logits are; its X still takes part in dW as 0 * X and has to be finite.
- *   dX: M x K, dW: vocab x K, BF16; either may be NULL (not computed).
+ *   dX: M x K, dW: vocab x K, BF16; either may be NULL (not computed). Neither may overlap another operand.
  *   workspace: bytes that the piece of G may take, 0 = 512 MiB; gemm_cross_entropy_piece gives the columns of a piece.
  * Constraints as gemm_cross_entropy; dX and dW 16-byte aligned. M == 0 sets dW to zero.
  * Two kernel launches a piece. Where dX needs FP32 sums (several pieces, or few tiles and so slices of its sum) one more

@@ -177,3 +177,64 @@ def test_embedding_without_a_device():
         pytest.skip("a GPU is present")
     assert lookup() == g.GEMM_ERR_NO_DEVICE
     assert table_grad() == g.GEMM_ERR_NO_DEVICE
+
+
+class OnDevice:
+    """As much of a CUDA tensor as the binding's checks look at."""
+
+    def __init__(self, index, dtype, shape):
+        self.index, self.dtype, self.shape, self.is_cuda, self.device = index, dtype, torch.Size(shape), True, f"cuda:{index}"
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return True
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    monkeypatch.setattr(g, "_device", lambda: 0)
+    bf16, i64 = torch.bfloat16, torch.int64
+    with pytest.raises(ValueError, match="x: lies on cuda:1"):
+        g.cross_entropy(OnDevice(1, bf16, (2, 8)), OnDevice(0, bf16, (5, 8)))
+    with pytest.raises(ValueError, match="head: lies on cuda:1"):
+        g.cross_entropy(OnDevice(0, bf16, (2, 8)), OnDevice(1, bf16, (5, 8)))
+    with pytest.raises(ValueError, match="tokens: lies on cuda:2"):
+        g.embedding(OnDevice(0, bf16, (5, 8)), OnDeviceVector(2, i64, 3))
+    with pytest.raises(ValueError, match="bias: lies on cuda:1"):
+        x = OnDevice(0, bf16, (2, 8))
+        g.layer_norm(x, None, OnDeviceVector(1, bf16, 8))
+
+
+class OnDeviceVector(OnDevice):
+    def __init__(self, index, dtype, n):
+        super().__init__(index, dtype, (n,))
+
+    def numel(self):
+        return self.shape[0]
+
+
+def test_sizes_that_do_not_belong_together_are_refused(monkeypatch):
+    monkeypatch.setattr(g, "_device", lambda: 0)
+    bf16, f32, i64 = torch.bfloat16, torch.float32, torch.int64
+    x, head = OnDevice(0, bf16, (2, 8)), OnDevice(0, bf16, (5, 8))
+    with pytest.raises(ValueError, match="head: rows of 8"):
+        g.cross_entropy(x, OnDevice(0, bf16, (5, 16)))
+    with pytest.raises(ValueError, match="targets:"):
+        g.cross_entropy(x, head, OnDeviceVector(0, i64, 3))
+    with pytest.raises(ValueError, match="targets:"):
+        g.cross_entropy(x, head, OnDeviceVector(0, torch.int32, 2))
+    with pytest.raises(ValueError, match="lse:"):
+        g.cross_entropy_backward(x, head, None, OnDeviceVector(0, f32, 3), None)
+    with pytest.raises(ValueError, match="workspace:"):
+        g.cross_entropy_backward(x, head, None, OnDeviceVector(0, f32, 2), None, workspace=-1)
+    with pytest.raises(ValueError, match="inplace:"):
+        g.embedding_backward(x, OnDeviceVector(0, i64, 2), 5, inplace=True)
+    with pytest.raises(ValueError, match="base:"):
+        g.embedding_backward(x, OnDeviceVector(0, i64, 2), 5, base=OnDevice(0, bf16, (4, 8)))
+    with pytest.raises(ValueError, match="dtype:"):
+        g.embedding_backward(x, OnDeviceVector(0, i64, 2), 5, dtype=torch.float16)
+    with pytest.raises(ValueError, match="inplace:"):
+        g.layer_norm(x, inplace=True)
+    with pytest.raises(ValueError, match="rstd:"):
+        g.layer_norm_backward(x, x, None, OnDeviceVector(0, f32, 2), OnDeviceVector(0, f32, 3))
