@@ -140,33 +140,138 @@ __device__ __forceinline__ void launch_dependents(int rows) {
   if (rows <= static_cast<int>(gridDim.x)) pdl_launch_dependents();
 }
 
+// Rows off the 16-byte boundary whose tensors share it (kShared): the whole vectors between a row's first and last boundary
+// are the groups of the CTA's threads, as on the boundary, and the up to 14 elements around them belong to the lanes of one
+// more warp, the last. With the ends as masked groups of the first and last warp instead, which the others then waited for,
+// 2001 x 5123 took 16.5 us forward (13.3 so) and its gradient 25.0 (22.3), 16000 x 1023 29.6 (25.4) and 39.7 (33.2).
+template <int ACCESS>
+struct RowPart {
+  static constexpr int AS = ACCESS == kShared ? kAligned : ACCESS;  // how groups are read and written
+  int threads, lead, end, phase;  // of the groups; columns before them; where they end; kElements: columns they start early
+  __device__ __forceinline__ RowPart(const uint16_t* row, int cols) {
+    const int off = ACCESS == kAligned ? 0 : row_phase(row);
+    threads = static_cast<int>(blockDim.x) - (ACCESS == kShared ? 32 : 0);
+    lead = ACCESS == kShared ? (8 - off) & 7 : 0;
+    end = ACCESS == kShared ? lead + (cols - lead) / 8 * 8 : cols;
+    phase = ACCESS == kElements ? off : 0;
+  }
+  __device__ __forceinline__ int column(int k) const {
+    return lead + 8 * (static_cast<int>(threadIdx.x) + k * threads) - phase;
+  }
+  __device__ __forceinline__ bool at_edge() const { return ACCESS == kShared && static_cast<int>(threadIdx.x) >= threads; }
+  // The column of a lane of the last warp, or -1.
+  __device__ __forceinline__ int edge_column(int cols) const {
+    const int lane = threadIdx.x & 31;
+    if (lane < 8) return lane < lead ? lane : -1;
+    return end + lane - 8 < cols ? end + lane - 8 : -1;
+  }
+};
+
+__device__ __forceinline__ void cta_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
+__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return static_cast<uint16_t>(pack2(v, 0.0f) & 0xFFFFu); }
+
 // ---------------------------------------------------------------- forward
+
+// Mean and variance of the row from its warps' moments, behind the barrier.
+// They are taken about the first warp's mean: its distance from the row's mean is at most sqrt(warps) spreads, so taking it
+// out again costs five bits of the variance's at the worst, and both sums run side by side.
+__device__ __forceinline__ void row_moments(const float2* moments, const float* counts, int warps, float inverse_cols,
+                                            float& mean, float& var) {
+  const int lane = threadIdx.x & 31;
+  const float about = moments[0].x;
+  float first = 0.0f, second = 0.0f;
+  if (lane < warps) {
+    const float2 part = moments[lane];
+    const float off = part.x - about, n_off = counts[lane] * off;
+    first = n_off;
+    second = fmaf(n_off, off, part.y);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    first += __shfl_xor_sync(0xffffffffu, first, o);
+    second += __shfl_xor_sync(0xffffffffu, second, o);
+  }
+  const float shift = first * inverse_cols;
+  mean = about + shift;
+  var = fmaxf(fmaf(-first, shift, second), 0.0f) * inverse_cols + (second - second);  // (NaN stays NaN)
+}
+
+struct NormShared {
+  float2 moments[2][32];  // a warp's mean and squares about it
+  float counts[32];       // its columns
+  uint32_t top[2][32];    // its largest result
+};
+
+// The elements around a row's vectors: a lane of the last warp each (column -1: none).
+template <int FORMAT>
+__device__ __forceinline__ void norm_edge(const LayerNormParams& p, NormShared& sh, int column, uint32_t rows, int warps,
+                                          float inverse_count, float inverse_cols) {
+  const bool on = column >= 0;
+  const int lane = threadIdx.x & 31;
+  const float w = on && p.w != nullptr ? bf16_value(p.w[column]) : 1.0f;
+  const float b = on && p.b != nullptr ? bf16_value(p.b[column]) : 0.0f;
+  auto load = [&](uint32_t row, uint16_t& x, uint16_t& r) {
+    x = on ? p.x[row * p.ldx + column] : uint16_t(0);
+    r = on && p.r != nullptr ? p.r[row * p.ldr + column] : uint16_t(0);
+  };
+  uint16_t x, r, x_next = 0, r_next = 0;
+  load(blockIdx.x, x, r);
+  int parity = 0;
+  for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
+    if (row + gridDim.x < rows) load(row + gridDim.x, x_next, r_next);
+    if (p.r != nullptr) x = bf16_bits(bf16_value(x) + bf16_value(r));
+    if (on && p.s != nullptr) p.s[row * p.lds + column] = x;
+    const float s = bf16_value(x);
+    const float warp_mean = warp_sum(s) * inverse_count, d = on ? s - warp_mean : 0.0f;
+    const float squares = warp_sum(d * d);
+    if (lane == 0) sh.moments[parity][threadIdx.x >> 5] = make_float2(warp_mean, squares);
+    cta_sync();
+    float mean, var;
+    row_moments(sh.moments[parity], sh.counts, warps, inverse_cols, mean, var);
+    const float y = on ? fmaf((s - mean) * inverse_sqrt(var + p.eps), w, b) : 0.0f;
+    if constexpr (FORMAT == GEMM_NORM_BF16) {
+      if (on) static_cast<uint16_t*>(p.y)[row * p.ldy + column] = bf16_bits(y);
+    } else {
+      const E4m3Scale scale(block_max_bits(abs_bits(y), sh.top[parity], warps));
+      if (on) static_cast<uint8_t*>(p.y)[row * p.ldy + column] = static_cast<uint8_t>(e4m3_code(y * scale.inverse));
+    }
+    x = x_next;
+    r = r_next;
+  }
+}
 
 template <int VPT, int SLOTS, int FORMAT, int ACCESS>
 __global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const LayerNormParams p) {
+  constexpr int AS = RowPart<ACCESS>::AS;
   extern __shared__ uint4 fetched[];  // [SLOTS][2][VPT][threads], then (KEPT) weight and bias: [2][VPT][threads]
-  __shared__ float2 moments[2][32];   // a warp's mean and squares about it
-  __shared__ float counts[32];        // its columns
-  __shared__ uint32_t slots_max[2][32];
+  __shared__ NormShared sh;
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint4* const mine = fetched + threadIdx.x;
   const uint32_t rows = static_cast<uint32_t>(p.rows);
   const int slot_size = 2 * VPT * static_cast<int>(blockDim.x);
   launch_dependents(p.rows);
   pdl_wait();
-  const int phase = ACCESS == kAligned ? 0 : row_phase(p.x + blockIdx.x * p.ldx);
+  const RowPart<ACCESS> part(p.x + blockIdx.x * p.ldx, p.cols);
   int col[VPT], size = 0;
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    col[k] = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x)) - phase;
-    size += group_size<ACCESS>(col[k], p.cols);
+    col[k] = part.column(k);
+    size += group_size<AS>(col[k], part.end);
   }
+  const int edge = part.at_edge() ? part.edge_column(p.cols) : -1;
+  if (part.at_edge()) size = edge >= 0 ? 1 : 0;
   const float count = warp_sum(static_cast<float>(size)), inverse_count = count > 0.0f ? 1.0f / count : 0.0f;
-  if (lane == 0) counts[warp] = count;  // (read behind the first row's barrier)
+  if (lane == 0) sh.counts[warp] = count;  // (read behind the first row's barrier)
   const float inverse_cols = 1.0f / static_cast<float>(p.cols);
+  if (part.at_edge()) {
+    if constexpr (ACCESS == kShared && FORMAT != GEMM_NORM_NVFP4)
+      norm_edge<FORMAT>(p, sh, edge, rows, warps, inverse_count, inverse_cols);
+    return;
+  }
   auto fetch = [&](uint32_t row, int slot) {
     const uint16_t* const rows[2] = {p.x + row * p.ldx, p.r != nullptr ? p.r + row * p.ldr : nullptr};
-    fetch_rows<2, VPT, ACCESS>(mine + slot * slot_size, rows, col, p.cols, row);
+    fetch_rows<2, VPT, AS>(mine + slot * slot_size, rows, col, part.end, row);
   };
   // (groups past the row's end stay zero)
   for (int i = 0; i < SLOTS * 2 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
@@ -177,8 +282,8 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const Lay
   constexpr bool KEPT = VPT < 8;
   uint4* const affine = mine + SLOTS * slot_size;
   uint4 w[VPT], b[VPT];
-  load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
-  load_bias<VPT, ACCESS>(b, p.b, col, p.cols);
+  load_weight<VPT, ACCESS>(w, p.w, col, part.end);
+  load_bias<VPT, ACCESS>(b, p.b, col, part.end);
   if constexpr (KEPT) {
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
@@ -186,7 +291,6 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const Lay
       affine[(VPT + k) * static_cast<int>(blockDim.x)] = b[k];
     }
   }
-  const bool starts = threadIdx.x < 32 && phase != 0;  // the warp with the row's start
   int parity = 0;
   for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {  // (no sum of them passes 32 bits)
     const uint4* const in = mine + ring.next(row, gridDim.x, rows, fetch) * slot_size;
@@ -202,8 +306,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const Lay
         for (int j = 0; j < 4; ++j) a.v[j] = f2_add(a.v[j], e.v[j]);
         v = pack8_pairs(a);
       }
-      if (ACCESS == kShared && k == 0 && starts) mask_start(v, col[0]);
-      if (p.s != nullptr) store8<ACCESS>(p.s + row * p.lds, col[k], p.cols, v);
+      if (p.s != nullptr) store8<AS>(p.s + row * p.lds, col[k], part.end, v);
       s[k] = unpack8_pairs(v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum = f2_add(sum, s[k].v[j]);
@@ -215,8 +318,8 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const Lay
     float squares = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
-      by_group<ACCESS>(
-          col[k], p.cols,
+      by_group<AS>(
+          col[k], part.end,
           [&] {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -231,26 +334,9 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const Lay
     squares = warp_sum(squares + pair_sum(squares2));
     float mean = warp_mean, var = squares * inverse_cols;
     if (warps > 1) {
-      if (lane == 0) moments[parity][warp] = make_float2(warp_mean, squares);
-      __syncthreads();
-      // The warps' moments about the first warp's mean: its distance from the row's mean is at most sqrt(warps) spreads,
-      // so taking it out again costs five bits of the variance's at the worst, and both sums run side by side.
-      const float about = moments[parity][0].x;
-      float first = 0.0f, second = 0.0f;
-      if (lane < warps) {
-        const float2 part = moments[parity][lane];
-        const float off = part.x - about, n_off = counts[lane] * off;
-        first = n_off;
-        second = fmaf(n_off, off, part.y);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        first += __shfl_xor_sync(0xffffffffu, first, o);
-        second += __shfl_xor_sync(0xffffffffu, second, o);
-      }
-      const float shift = first * inverse_cols;
-      mean = about + shift;
-      var = fmaxf(fmaf(-first, shift, second), 0.0f) * inverse_cols + (second - second);  // (NaN stays NaN)
+      if (lane == 0) sh.moments[parity][warp] = make_float2(warp_mean, squares);
+      cta_sync();
+      row_moments(sh.moments[parity], sh.counts, warps, inverse_cols, mean, var);
     }
     const float rstd = inverse_sqrt(var + p.eps);
     if (threadIdx.x == 0) {
@@ -263,8 +349,8 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const Lay
       const P8 g = unpack8_pairs(KEPT ? affine[k * static_cast<int>(blockDim.x)] : w[k]);
       const P8 h = unpack8_pairs(KEPT ? affine[(VPT + k) * static_cast<int>(blockDim.x)] : b[k]);
       P8 y = {};
-      by_group<ACCESS>(
-          col[k], p.cols,
+      by_group<AS>(
+          col[k], part.end,
           [&] {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -284,7 +370,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const Lay
       for (int j = 0; j < 4; ++j) f2_unpack(s[k].v[j], y.v[2 * j], y.v[2 * j + 1]);
       return y;
     };
-    norm_output<VPT, FORMAT, ACCESS>(value, p.y, p.ldy, p.scales, row, p.cols, col, slots_max[parity], warps);
+    norm_output<VPT, FORMAT, AS>(value, p.y, p.ldy, p.scales, row, part.end, col, sh.top[parity], warps);
   }
 }
 
@@ -296,9 +382,53 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float2* slots, in
   b = warp_sum(b);
   if (warps == 1) return make_float2(a, b);
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
+  cta_sync();
   const float2 v = (threadIdx.x & 31) < warps ? slots[threadIdx.x & 31] : make_float2(0.0f, 0.0f);
   return make_float2(warp_sum(v.x), warp_sum(v.y));
+}
+
+// The elements around a row's vectors, as norm_edge.
+__device__ __forceinline__ void norm_backward_edge(const LayerNormBackwardParams& p, float2 (&slots)[2][32], int column,
+                                                   uint32_t rows, int warps, float inverse_cols) {
+  const bool on = column >= 0;
+  const float w = on && p.w != nullptr ? bf16_value(p.w[column]) : 1.0f;
+  struct Element {
+    uint16_t s, dy, ds;
+    float mean, rstd;
+  };
+  auto load = [&](uint32_t row) {
+    Element e = {0, 0, 0, p.mean[row], p.rstd[row]};
+    if (on) {
+      e.s = p.s[row * p.lds + column];
+      e.dy = p.dy[row * p.lddy + column];
+      if (p.ds != nullptr) e.ds = p.ds[row * p.ldds + column];
+    }
+    return e;
+  };
+  Element e = load(blockIdx.x), next = e;
+  float dw = 0.0f, db = 0.0f;
+  int parity = 0;
+  for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
+    if (row + gridDim.x < rows) next = load(row + gridDim.x);
+    const float off = bf16_value(e.s) - e.mean, xh = off * e.rstd, dy = bf16_value(e.dy), dyw = dy * w;
+    if (on) {
+      dw = fmaf(dy, xh, dw);
+      db += dy;
+    }
+    const float2 c = block_sum2(on ? dyw : 0.0f, on ? dyw * xh : 0.0f, slots[parity], warps);
+    const float c1 = c.x * inverse_cols * -e.rstd, c2 = c.y * inverse_cols * -(e.rstd * e.rstd);
+    if (on)
+      p.dx[row * p.lddx + column] = bf16_bits(fmaf(dyw, e.rstd, fmaf(off, c2, c1)) + bf16_value(e.ds));
+    e = next;
+  }
+  if (p.partial != nullptr) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      cta_sync();
+      cta_sync();
+      if (on) p.partial[(2LL * blockIdx.x + t) * p.cols + column] = t == 0 ? dw : db;
+    }
+  }
 }
 
 // TEAMS: rows of a warp, kTeams of them in a CTA at a time, so that the gradients of weight and bias leave a CTA as one
@@ -308,6 +438,7 @@ constexpr int kTeams = 8;
 template <int VPT, int SLOTS, int ACCESS, bool TEAMS>
 __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
     layer_norm_backward_kernel(const LayerNormBackwardParams p) {
+  constexpr int AS = RowPart<ACCESS>::AS;
   extern __shared__ uint4 fetched[];  // [teams][SLOTS][3][VPT][threads]
   __shared__ float2 slots[2][32];
   const int warps = blockDim.x >> 5;
@@ -318,15 +449,19 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
   uint4* const mine = fetched + team * SLOTS * slot_size + threadIdx.x;
   launch_dependents(p.rows);
   pdl_wait();
-  const int phase = ACCESS == kAligned ? 0 : row_phase(p.s + blockIdx.x * p.lds);
+  const RowPart<ACCESS> part(p.s + blockIdx.x * p.lds, p.cols);
+  const float inverse_cols = 1.0f / static_cast<float>(p.cols);
+  if (part.at_edge()) {
+    if constexpr (ACCESS == kShared) norm_backward_edge(p, slots, part.edge_column(p.cols), rows, warps, inverse_cols);
+    return;
+  }
   int col[VPT];
 #pragma unroll
-  for (int k = 0; k < VPT; ++k)
-    col[k] = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x)) - phase;
+  for (int k = 0; k < VPT; ++k) col[k] = part.column(k);
   auto fetch = [&](uint32_t row, int slot) {
     const uint16_t* const rows[3] = {p.s + row * p.lds, p.dy + row * p.lddy,
                                      p.ds != nullptr ? p.ds + row * p.ldds : nullptr};
-    fetch_rows<3, VPT, ACCESS>(mine + slot * slot_size, rows, col, p.cols, row);
+    fetch_rows<3, VPT, AS>(mine + slot * slot_size, rows, col, part.end, row);
   };
   // (groups past the row's end stay zero)
   for (int i = 0; i < SLOTS * 3 * VPT; ++i) mine[i * static_cast<int>(blockDim.x)] = make_uint4(0u, 0u, 0u, 0u);
@@ -338,9 +473,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
   for (int k = 0; k < VPT; ++k)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[k].v[j] = db[k].v[j] = 0;
-  load_weight<VPT, ACCESS>(w, p.w, col, p.cols);
-  const bool starts = threadIdx.x < 32 && phase != 0;  // the warp with the row's start
-  const float inverse_cols = 1.0f / static_cast<float>(p.cols);
+  load_weight<VPT, ACCESS>(w, p.w, col, part.end);
   float rstd = 0.0f, mean = 0.0f, rstd_next = 0.0f, mean_next = 0.0f;
   if (!TEAMS || first_row < rows) {
     rstd = p.rstd[first_row];
@@ -358,11 +491,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
     uint64_t sum1 = 0, sum2 = 0;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      uint4 v[2] = {in[k * static_cast<int>(blockDim.x)], in[(VPT + k) * static_cast<int>(blockDim.x)]};
-      if (ACCESS == kShared && k == 0 && starts) {
-        mask_start(v[0], col[0]);
-        mask_start(v[1], col[0]);
-      }
+      const uint4 v[2] = {in[k * static_cast<int>(blockDim.x)], in[(VPT + k) * static_cast<int>(blockDim.x)]};
       // (outside the row dy is 0, and so is what it adds)
       const P8 a = unpack8_pairs(v[0]), d = unpack8_pairs(v[1]), g = unpack8_pairs(w[k]);
 #pragma unroll
@@ -391,32 +520,33 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
 #pragma unroll
         for (int j = 0; j < 4; ++j) o.v[j] = f2_add(o.v[j], e.v[j]);
       }
-      store8<ACCESS>(p.dx + row * p.lddx, col[k], p.cols, pack8_pairs(o));
+      store8<AS>(p.dx + row * p.lddx, col[k], part.end, pack8_pairs(o));
     }
     if (SLOTS == 1 && more) fetch(row + step, 0);
     rstd = rstd_next;
     mean = mean_next;
   }
   if (p.partial != nullptr) {  // through shared memory: teams are added there, and a warp writes 32 columns side by side
-    const int team_floats = SLOTS * slot_size * 4, threads = static_cast<int>(blockDim.x * blockDim.y);
+    const int team_floats = SLOTS * slot_size * 4, threads = part.threads * static_cast<int>(blockDim.y);
+    const int from = part.lead - part.phase;  // the column of the first place
     float* const sums = reinterpret_cast<float*>(fetched);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      __syncthreads();
+      cta_sync();
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const P8& v = t == 0 ? dw[k] : db[k];
-        ulonglong2* at = reinterpret_cast<ulonglong2*>(sums + team * team_floats + col[k] + phase);
+        ulonglong2* at = reinterpret_cast<ulonglong2*>(sums + team * team_floats + col[k] - from);
         at[0] = make_ulonglong2(v.v[0], v.v[1]);
         at[1] = make_ulonglong2(v.v[2], v.v[3]);
       }
-      __syncthreads();
+      cta_sync();
       float* out = p.partial + (2LL * blockIdx.x + t) * p.cols;
-      for (int c = team * static_cast<int>(blockDim.x) + threadIdx.x; c < p.cols; c += threads) {
-        float v = sums[c + phase];
+      for (int c = part.lead + team * part.threads + static_cast<int>(threadIdx.x); c < part.end; c += threads) {
+        float v = sums[c - from];
         if (TEAMS)
 #pragma unroll
-          for (int i = 1; i < kTeams; ++i) v += sums[i * team_floats + c + phase];
+          for (int i = 1; i < kTeams; ++i) v += sums[i * team_floats + c - from];
         out[c] = v;
       }
     }
@@ -461,7 +591,19 @@ struct LayerNormShape {
   int slots;
   int smem(int tensors, int kept) const { return (slots * tensors + kept) * at.vpt * at.threads * 16; }
 };
-LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, bool is_aligned, bool forward) {
+LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, NormAccess access, bool forward) {
+  if (access == kShared) {  // the whole groups, and a warp for the elements around them
+    const int groups = cols / 8;
+    if (groups <= 32 && rows > num_sms) return LayerNormShape{{64, 1}, 4};
+    NormShape s{0, rows <= num_sms ? 1 : groups > (forward ? 96 : 800) ? 4 : 2};
+    for (;; s.vpt *= 2) {
+      s.threads = std::max(32, ceil_div(ceil_div(groups, s.vpt), 32) * 32);
+      if (s.threads <= (s.vpt == 1 ? 992 : 480)) break;
+    }
+    s.threads += 32;
+    return LayerNormShape{s, s.vpt == 2 && !forward ? 3 : norm_slots(s.vpt)};
+  }
+  const bool is_aligned = access == kAligned;
   const int groups = ceil_div(cols, 8) + (is_aligned ? 0 : 1);
   if (groups <= 32 && rows > num_sms) return LayerNormShape{{32, 1}, 4};
   NormShape s = norm_shape(rows, cols, num_sms, is_aligned);
@@ -482,27 +624,39 @@ const void* forward_kernel(const LayerNormShape& s) {
   }
 }
 template <int FORMAT>
-const void* forward_kernel(const LayerNormShape& s, bool aligned, bool shared) {
-  return aligned  ? forward_kernel<FORMAT, kAligned>(s)
-         : shared ? forward_kernel<FORMAT, kShared>(s)
-                  : forward_kernel<FORMAT, kElements>(s);
+const void* forward_kernel(const LayerNormShape& s, NormAccess access) {
+  return access == kAligned  ? forward_kernel<FORMAT, kAligned>(s)
+         : access == kShared ? forward_kernel<FORMAT, kShared>(s)
+                             : forward_kernel<FORMAT, kElements>(s);
 }
 
 template <int ACCESS>
 const void* backward_kernel(const LayerNormShape& s, bool teams) {
+  if constexpr (ACCESS != kShared) {
+    if (teams && s.at.vpt == 1) return reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 4, ACCESS, true>);
+    if (teams) return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 2, ACCESS, true>);
+  }
   switch (s.at.vpt) {
     case 1:
-      return teams          ? reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 4, ACCESS, true>)
-             : s.slots == 1 ? reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 1, ACCESS, false>)
-                            : reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 4, ACCESS, false>);
+      return s.slots == 1 ? reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 1, ACCESS, false>)
+                          : reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 4, ACCESS, false>);
     case 2:
-      if constexpr (ACCESS == kAligned)
-        if (s.slots == 3) return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 3, ACCESS, false>);
-      return teams ? reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 2, ACCESS, true>)
-                   : reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 2, ACCESS, false>);
+      if constexpr (ACCESS == kShared) {
+        return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 3, ACCESS, false>);
+      } else {
+        if constexpr (ACCESS == kAligned)
+          if (s.slots == 3) return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 3, ACCESS, false>);
+        return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 2, ACCESS, false>);
+      }
     case 4: return reinterpret_cast<const void*>(layer_norm_backward_kernel<4, 2, ACCESS, false>);
     default: return reinterpret_cast<const void*>(layer_norm_backward_kernel<8, 1, ACCESS, false>);
   }
+}
+
+// How a call's rows lie: for kShared a row needs a whole vector between its boundaries, and no more of them than eight a
+// thread of 15 warps.
+NormAccess norm_access(bool aligned, bool shared, int cols) {
+  return aligned ? kAligned : shared && cols >= 16 && cols <= 30720 ? kShared : kElements;
 }
 
 }  // namespace
@@ -569,10 +723,11 @@ int gemm_layer_norm(const void* X, const void* R, const void* W, const void* B, 
   int device = 0, err = 0;
   const DeviceInfo* info = current_device_info(&device, &err);
   if (info == nullptr) return err;
-  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, aligned, true);
+  const NormAccess access = norm_access(aligned, shared, cols);
+  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, access, true);
   const void* kernel = format == GEMM_NORM_NVFP4  ? forward_kernel<GEMM_NORM_NVFP4, kAligned>(shape)
-                       : format == GEMM_NORM_E4M3 ? forward_kernel<GEMM_NORM_E4M3>(shape, aligned, shared)
-                                                  : forward_kernel<GEMM_NORM_BF16>(shape, aligned, shared);
+                       : format == GEMM_NORM_E4M3 ? forward_kernel<GEMM_NORM_E4M3>(shape, access)
+                                                  : forward_kernel<GEMM_NORM_BF16>(shape, access);
   void* args[] = {&p};
   const int smem = shape.smem(2, shape.at.vpt < 8 ? 2 : 0);
   const int grid = norm_grid(kernel, rows, shape.at.threads, smem, info->num_sms);
@@ -624,12 +779,13 @@ int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const
   const bool shared = RowPlace(dY, p.lddy, 2) == place && (dS == nullptr || RowPlace(dS, p.ldds, 2) == place) &&
                       RowPlace(dX, p.lddx, 2) == place;
   const bool aligned = shared && place.aligned() && cols % 8 == 0 && !misaligned(W, 16);
-  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, aligned, false);
+  const NormAccess access = norm_access(aligned, shared, cols);
+  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, access, false);
   // (a grid of a multiple of 8, or a row a team: rows of a CTA share the column at which their boundary lies)
   const bool teams = sums && shape.at.threads == 32 && rows > info->num_sms && info->num_sms % 8 == 0;
-  const void* kernel = aligned  ? backward_kernel<kAligned>(shape, teams)
-                       : shared ? backward_kernel<kShared>(shape, teams)
-                                : backward_kernel<kElements>(shape, teams);
+  const void* kernel = access == kAligned  ? backward_kernel<kAligned>(shape, teams)
+                       : access == kShared ? backward_kernel<kShared>(shape, teams)
+                                           : backward_kernel<kElements>(shape, teams);
   const dim3 threads(shape.at.threads, teams ? kTeams : 1);
   const int smem = shape.smem(3, 0) * static_cast<int>(threads.y);
   const int grid = norm_grid(kernel, rows, static_cast<int>(threads.x * threads.y), smem, info->num_sms);

@@ -242,6 +242,19 @@ __device__ __forceinline__ int row_phase(const uint16_t* row) {
   return static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 7u);
 }
 
+// An E4M3 row's scale and its inverse, from its largest magnitude's bits (a NaN stays one).
+struct E4m3Scale {
+  float scale, inverse;
+  __device__ __forceinline__ explicit E4m3Scale(uint32_t top) {
+    scale = __uint_as_float(top) / 448.0f;
+    inverse = top == 0 ? 0.0f : 448.0f / __uint_as_float(top);
+    if (inverse > kNormMostInverse) {  // a row near FP32's smallest numbers: the scale stops where its inverse does
+      inverse = kNormMostInverse;
+      scale = 1.0f / kNormMostInverse;
+    }
+  }
+};
+
 // A row's outputs in their format; value(k): the thread's eight results of group k, FP32.
 template <int VPT, int FORMAT, int ACCESS, class Value>
 __device__ __forceinline__ void norm_output(const Value& value, void* y, long long ldy, void* scales, long long row,
@@ -259,19 +272,13 @@ __device__ __forceinline__ void norm_output(const Value& value, void* y, long lo
       for (int j = 0; j < 8; ++j) top = max(top, abs_bits(a.v[j]));
     }
     top = block_max_bits(top, slots_max, warps);
-    float scale = __uint_as_float(top) / 448.0f;
-    // (a NaN stays one)
-    float inverse = top == 0 ? 0.0f : 448.0f / __uint_as_float(top);
-    if (inverse > kNormMostInverse) {  // a row near FP32's smallest numbers: the scale stops where its inverse does
-      inverse = kNormMostInverse;
-      scale = 1.0f / kNormMostInverse;
-    }
-    if (threadIdx.x == 0) static_cast<float*>(scales)[row] = scale;
+    const E4m3Scale s(top);
+    if (threadIdx.x == 0) static_cast<float*>(scales)[row] = s.scale;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       F8 a = value(k);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a.v[j] *= inverse;
+      for (int j = 0; j < 8; ++j) a.v[j] *= s.inverse;
       store8_bytes<ACCESS>(static_cast<uint8_t*>(y) + row * ldy, col[k], cols,
                            make_uint2(e4m3x4(a.v[0], a.v[1], a.v[2], a.v[3]), e4m3x4(a.v[4], a.v[5], a.v[6], a.v[7])));
     }

@@ -92,7 +92,8 @@ def dev(t):
 SHAPES = [(1, 1), (1, 8192), (3, 7), (2, 8), (5, 15), (17, 4099), (700, 520), (2, 16391), (3, 32760), (1300, 64),
           (4, 16384), (2500, 1032), (33, 4104), (1, 9), (64, 2049)]
 # two, four and eight groups a thread, on the 16-byte boundary and off it, with more rows than resident CTAs
-SEVERAL_ROWS = [(1500, 4096), (2000, 2051), (1500, 8192), (400, 12000), (400, 12003), (330, 20000), (330, 20001)]
+SEVERAL_ROWS = [(1500, 4096), (2000, 2051), (1500, 8192), (400, 12000), (400, 12003), (330, 20000), (330, 20001),
+                (200, 30719), (160, 30721), (3000, 16), (3000, 17), (5000, 257), (6000, 511), (5000, 23)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES + SEVERAL_ROWS)
