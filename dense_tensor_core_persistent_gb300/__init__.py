@@ -636,6 +636,9 @@ def _elsewhere(t) -> bool:
     return t.get_device() != _device()
 
 
+_MOST = 0x7FFFFFFF  # sizes of the library's calls have 32 bits (ctypes would cut a larger one without a word)
+
+
 def _matrix(t, what, dtype, shape=None):
     """A CUDA matrix of `dtype` on the current device whose rows are contiguous -> its row stride (0: rows follow one
     another)."""
@@ -645,6 +648,8 @@ def _matrix(t, what, dtype, shape=None):
     if t.dtype is not dtype or len(size) != 2 or not t.is_cuda or (shape is not None and size != shape):
         want = "" if shape is None else f" of shape {tuple(shape)}"
         raise ValueError(f"{what}: a CUDA {dtype} matrix{want} is needed, got {t.dtype} {tuple(size)} on {t.device}")
+    if size[0] > _MOST or size[1] > _MOST:
+        raise ValueError(f"{what}: sizes below 2^31 are needed, got {tuple(size)}")
     if _elsewhere(t):
         raise ValueError(f"{what}: lies on {t.device}, which is not the current device")
     if t.is_contiguous():
@@ -669,6 +674,8 @@ def _vector(t, what, dtype, n):
         raise ValueError(f"{what}: a CUDA {dtype} vector of {n} is needed, got None")
     if t.dtype is not dtype or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous CUDA {dtype} vector of {n} is needed, got {t.dtype} {tuple(t.shape)}")
+    if n > _MOST:
+        raise ValueError(f"{what}: sizes below 2^31 are needed, got {n}")
     if _elsewhere(t):
         raise ValueError(f"{what}: lies on {t.device}, which is not the current device")
     return t
@@ -1128,8 +1135,8 @@ def embedding_backward(dy, tokens, vocab: int, scale: float = 1.0, base=None, in
     ldd = _matrix(dy, "dy", dy.dtype)
     rows, width = dy.shape
     _vector(tokens, "tokens", torch.int64, rows)
-    if vocab < 0:
-        raise ValueError(f"vocab: a size is needed, got {vocab}")
+    if not 0 <= vocab <= _MOST:
+        raise ValueError(f"vocab: a size below 2^31 is needed, got {vocab}")
     if dtype is None:
         dtype = dy.dtype if base is None else base.dtype
     kind = _table_kind(dtype, "dtype")

@@ -238,3 +238,20 @@ def test_sizes_that_do_not_belong_together_are_refused(monkeypatch):
         g.layer_norm(x, inplace=True)
     with pytest.raises(ValueError, match="rstd:"):
         g.layer_norm_backward(x, x, None, OnDeviceVector(0, f32, 2), OnDeviceVector(0, f32, 3))
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """The library takes 32-bit sizes, to which ctypes would cut a larger one without a word."""
+    monkeypatch.setattr(g, "_device", lambda: 0)
+    bf16, i64, big = torch.bfloat16, torch.int64, (1 << 32) + 2
+    x = OnDevice(0, bf16, (2, 8))
+    with pytest.raises(ValueError, match="x: sizes below"):
+        g.layer_norm(OnDevice(0, bf16, (big, 8)))
+    with pytest.raises(ValueError, match="head: sizes below"):
+        g.cross_entropy(x, OnDevice(0, bf16, (big, 8)))
+    with pytest.raises(ValueError, match="table: sizes below"):
+        g.embedding(OnDevice(0, bf16, (2, 1 << 31)), OnDeviceVector(0, i64, 2))
+    with pytest.raises(ValueError, match="tokens: sizes below"):
+        g.embedding(x, OnDeviceVector(0, i64, big))
+    with pytest.raises(ValueError, match="vocab:"):
+        g.embedding_backward(x, OnDeviceVector(0, i64, 2), big)
