@@ -685,7 +685,7 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
   q.g[0] = ws;
   const int slices = q.most_slices = plan.p.main.slices;
   const bool join = plan.sums > 0;
-  for (int first = 0; first < vocab && st == GEMM_OK; first += piece) {
+  for (int first = 0; first < vocab && st == GEMM_OK; first += q.features[0]) {  // (no sum of them passes 31 bits)
     select(first);
     LossParams p = {};
     p.scale = scale;
