@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupPara
 
 constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kMostDigitBits = 10, kMostDigits = 1 << kMostDigitBits;
-constexpr int kSortAhead = 4;  // steps of 32 positions that a warp asks for together
+constexpr int kSortAhead = 8;  // steps of 32 positions that a warp asks for together
 
 // A position and its token, as they are sorted.
 struct __align__(8) Entry {
@@ -196,6 +196,7 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
         e[a] = i + 32 * a + lane < end ? entry_at(i + 32 * a + lane) : Entry{0u, 0u};
     };
     Entry e[kSortAhead];
+    uint32_t among[kSortAhead];  // earlier entries of the warp with its digit
     for (uint32_t d = threadIdx.x; d < kSortWarps * digits; d += kSortThreads) s.counts[d] = 0u;
     __syncthreads();
     for (long long i = begin; i < end; i += 32 * kSortAhead) {
@@ -205,8 +206,11 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
         if (i + 32 * a >= end) break;
         const bool in = i + 32 * a + lane < end;
         const uint32_t digit = in ? (e[a].token >> shift) & mask : digits;  // (lanes past the end among themselves)
-        const uint32_t same = __match_any_sync(0xffffffffu, digit);
-        if (in && (same & ((1u << lane) - 1u)) == 0u) mine[digit] += __popc(same);
+        const uint32_t same = __match_any_sync(0xffffffffu, digit), lower = same & ((1u << lane) - 1u);
+        const uint32_t seen = in ? mine[digit] : 0u;
+        among[a] = seen + __popc(lower);
+        __syncwarp();
+        if (in && lower == 0u) mine[digit] = seen + __popc(same);
         __syncwarp();
       }
     }
@@ -246,22 +250,31 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       s.first[threadIdx.x] = lower + scan - all + before;
     }
     __syncthreads();
-    for (long long i = begin; i < end; i += 32 * kSortAhead) {
-      if (p.per_warp > 32 * kSortAhead) load(e, i);  // (else they still are here)
+    if (p.per_warp <= 32 * kSortAhead) {  // (the entries and their ranks still are here)
 #pragma unroll
       for (int a = 0; a < kSortAhead; ++a) {
-        if (i + 32 * a >= end) break;
-        const bool in = i + 32 * a + lane < end;
-        const uint32_t digit = in ? (e[a].token >> shift) & mask : digits;
-        const uint32_t same = __match_any_sync(0xffffffffu, digit), lower = same & ((1u << lane) - 1u);
-        uint32_t to = 0;
-        if (in) to = s.first[digit] + mine[digit] + __popc(lower);
-        __syncwarp();
-        if (in) {
-          if (lower == 0u) mine[digit] += __popc(same);
-          p.list[from ^ 1][to] = e[a];
+        if (begin + 32 * a + lane >= end) break;
+        const uint32_t digit = (e[a].token >> shift) & mask;
+        p.list[from ^ 1][s.first[digit] + mine[digit] + among[a]] = e[a];
+      }
+    } else {
+      for (long long i = begin; i < end; i += 32 * kSortAhead) {
+        load(e, i);
+#pragma unroll
+        for (int a = 0; a < kSortAhead; ++a) {
+          if (i + 32 * a >= end) break;
+          const bool in = i + 32 * a + lane < end;
+          const uint32_t digit = in ? (e[a].token >> shift) & mask : digits;
+          const uint32_t same = __match_any_sync(0xffffffffu, digit), lower = same & ((1u << lane) - 1u);
+          uint32_t to = 0;
+          if (in) to = s.first[digit] + mine[digit] + __popc(lower);
+          __syncwarp();
+          if (in) {
+            if (lower == 0u) mine[digit] += __popc(same);
+            p.list[from ^ 1][to] = e[a];
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
     cluster_sync_all();  // the list is written, and the totals are read

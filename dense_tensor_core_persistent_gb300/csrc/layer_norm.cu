@@ -422,6 +422,7 @@ __device__ __forceinline__ void norm_backward_edge(const LayerNormBackwardParams
     e = next;
   }
   if (p.partial != nullptr) {
+    pdl_launch_dependents();
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       cta_sync();
@@ -527,6 +528,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
     mean = mean_next;
   }
   if (p.partial != nullptr) {  // through shared memory: teams are added there, and a warp writes 32 columns side by side
+    pdl_launch_dependents();  // (the next kernel is small and waits for this one's end: 0.3 us)
     const int team_floats = SLOTS * slot_size * 4, threads = part.threads * static_cast<int>(blockDim.y);
     const int from = part.lead - part.phase;  // the column of the first place
     float* const sums = reinterpret_cast<float*>(fetched);
