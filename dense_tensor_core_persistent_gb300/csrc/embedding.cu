@@ -9,7 +9,7 @@
 // FP32 and writes each token's row once. Tokens of more than 32 positions are summed by run, into FP32 partial rows that a
 // last kernel adds in order: a token that is a tenth of all positions costs no more than the others.
 // The sort is a least-significant-digit radix sort of up to 10 bits a pass (two passes up to 2^20 tokens) by one cluster of
-// 8 CTAs: a warp counts the digits of its part of the list, the CTAs exchange their totals through shared memory, and every
+// 8 or 16 CTAs: a warp counts the digits of its part of the list, the CTAs exchange their totals through shared memory, and every
 // warp then knows where its part's digits go. The lists lie in global memory (L2), so their length is not limited. Beside
 // the sort another kernel writes the whole table, zeros or the base: that is most of the bytes of a dense gradient, and it
 // hides the sort.
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupPara
 
 // ---------------------------------------------------------------- positions by token
 
-constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kMostDigitBits = 10, kMostDigits = 1 << kMostDigitBits;
 constexpr int kSortAhead = 8;  // steps of 32 positions that a warp asks for together
 
@@ -170,7 +170,8 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) {
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) {
   extern __shared__ uint4 sort_shared[];
   SortShared& s = *reinterpret_cast<SortShared*>(sort_shared);
   pdl_wait();
@@ -230,7 +231,7 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     if (threadIdx.x < digits) {
       const uint32_t at = smem_u32(&s.totals[threadIdx.x]);
 #pragma unroll
-      for (int r = 0; r < kSortCtas; ++r) {
+      for (int r = 0; r < CTAS; ++r) {
         const uint32_t c = ld_cluster_u32(mapa_shared(at, r));
         if (r < rank) before += c;
         all += c;
@@ -601,22 +602,51 @@ const void* join_rows(bool vector) {
                 : reinterpret_cast<const void*>(join_rows_kernel<TABLE, false>);
 }
 
+// The sort's cluster. Measured on GB300, whole gradient in place: 65536 positions into 131072 x 1024 90.4 us with 8 CTAs and
+// 82.2 with 16, into 262144 x 64 49.6 and 44.9; 16384 into 131072 x 4096 80 and 79, 5003 into 50001 x 1027 28.2 and 28.7.
+constexpr int kSortCtas = 8, kManySortCtas = 16, kManySorted = 16384;
+
 int sort_bytes(int digit_bits) { return static_cast<int>(sizeof(SortShared)) + (kSortWarps << digit_bits) * 4; }
 
-bool prepare_sort(int device) {
+const void* sort_kernel_of(int ctas) {
+  return ctas == kManySortCtas ? reinterpret_cast<const void*>(sort_kernel<kManySortCtas>)
+                               : reinterpret_cast<const void*>(sort_kernel<kSortCtas>);
+}
+
+// CTAs of the sort's cluster; 0 on an error. Eight fit everywhere; a device whose SMs are shared out may not have room for
+// more in one cluster.
+int sort_ctas(int device, int rows) {
   static std::mutex mu;
-  static bool done[64] = {};
+  static int most[64] = {};
   std::lock_guard<std::mutex> lock(mu);
-  if (device < 0 || device >= 64) return false;
-  if (!done[device]) {
-    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_bytes(kMostDigitBits)) !=
-        cudaSuccess) {
+  if (device < 0 || device >= 64) return 0;
+  if (most[device] == 0) {
+    for (int ctas : {kSortCtas, kManySortCtas})
+      if (cudaFuncSetAttribute(sort_kernel_of(ctas), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               sort_bytes(kMostDigitBits)) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+      }
+    most[device] = kSortCtas;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(kManySortCtas);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = sort_bytes(kMostDigitBits);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kManySortCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const void* many = sort_kernel_of(kManySortCtas);
+    if (cudaFuncSetAttribute(many, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, many, &cfg) == cudaSuccess && n > 0)
+      most[device] = kManySortCtas;
+    else
       cudaGetLastError();
-      return false;
-    }
-    done[device] = true;
   }
-  return true;
+  return rows > kManySorted ? most[device] : kSortCtas;
 }
 
 }  // namespace
@@ -707,7 +737,8 @@ int gemm_embedding_backward(const void* dY, int dy_type, const long long* tokens
   }
 
   // runs of as many positions as a thread asks for at a time, longer ones where there would be more than 2048 of them
-  if (!prepare_sort(device)) return GEMM_ERR_LAUNCH;
+  const int ctas = sort_ctas(device, rows);
+  if (ctas == 0) return GEMM_ERR_LAUNCH;
   const int ahead = vector && base == nullptr ? kSumAhead<true, false> : kSumAhead<false, false>;
   q.run = std::min(kMaxRun, ceil_div(ceil_div(rows, 2048), ahead) * ahead);
   const int runs = ceil_div(rows, q.run);
@@ -728,12 +759,11 @@ int gemm_embedding_backward(const void* dY, int dy_type, const long long* tokens
   while ((vocab >> bits) != 0) ++bits;  // (the token after the last stands for none)
   p.passes = ceil_div(bits, kMostDigitBits);
   p.digit_bits = ceil_div(bits, p.passes);
-  p.per_warp = ceil_div(ceil_div(rows, kSortCtas * kSortWarps), 32) * 32;
+  p.per_warp = ceil_div(ceil_div(rows, ctas * kSortWarps), 32) * 32;
   for (int i = 0; i < 2; ++i) p.list[i] = reinterpret_cast<Entry*>(ws + i * list);
   p.spans = reinterpret_cast<int*>(ws + 2 * list);
   void* sort_args[] = {&p};
-  int st = launch(reinterpret_cast<const void*>(sort_kernel), dim3(kSortCtas), dim3(kSortThreads), sort_bytes(p.digit_bits),
-                  s, sort_args);
+  int st = launch(sort_kernel_of(ctas), dim3(ctas), dim3(kSortThreads), sort_bytes(p.digit_bits), s, sort_args);
   if (st == GEMM_OK) st = write_rest();
 
   q.list = p.list[0];

@@ -221,3 +221,11 @@ def test_many_positions_of_few_tokens():
     for rows, vocab in ((100000, 3), (70000, 1), (300001, 70000)):
         tokens, dy = ids(rows, rows, vocab, "few" if vocab == 3 else "frequent"), normal(7, rows, 8)
         check_gradient(g.embedding_backward(dy, tokens, vocab), dy, tokens, vocab, 1.0, None)
+
+
+@pytest.mark.parametrize("rows,vocab", [(16384, 1025), (16385, 1 << 20), (131072, 1 << 10), (131073, 5000), (257, (1 << 21) + 3),
+                                        (40000, (1 << 21) + 3)])
+def test_sorts_of_every_kind(rows, vocab):
+    """Around the lengths from which the sort takes more CTAs and reads its entries again, in one to three passes."""
+    tokens, dy = ids(rows, rows, vocab, "frequent"), normal(rows, rows, 4)
+    check_gradient(g.embedding_backward(dy, tokens, vocab), dy, tokens, vocab, 1.0, None)
