@@ -14,7 +14,9 @@
 // pieces are added in FP32. A piece is as large as G's workspace may be; fewer pieces are fewer joins and ramps. Not
 // keeping z costs its product a second time: 8 MVK operations where 6 would do with M x V logits in memory.
 //
-// Bound by the tensor cores, for few rows by W's bytes.
+// Bound by the tensor cores, for few rows by W's bytes. Measured on GB300: 4096 x 131072 x 4096 forward 2.24 ms (1.96
+// PFLOP/s), gradient 7.3 ms on a cool device (1.81 PFLOP/s over its three products) and up to 8.0 ms under the power cap;
+// 4096 x 32768 x 1024 154 and 337 us; 64 x 131072 x 4096 gradient 608 us, where reading W twice and writing dW takes 475.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -9,6 +9,9 @@
 // others relative to it through all of the CTA's tiles; lanes, warps and (in the joining kernel) CTAs are joined at the
 // end, in a fixed order.
 //
+// Measured on GB300 with W of 131072 x 4096 (1.07 GB, 158 us at the rate of a copy): 1 row 159 to 169 us, where the pair
+// tile took 290; 16 rows 176; 64 rows 168, where the pair tile's 65 rows take 193 and its 128 191.
+//
 // One persistent CTA per SM. Warp roles: 0 loads W, 2 loads X, 1 allocates TMEM and issues the MMAs, 4..11 epilogue, two
 // to each TMEM lane quadrant with half of X's rows each. Two accumulators in TMEM.
 #include <cuda.h>

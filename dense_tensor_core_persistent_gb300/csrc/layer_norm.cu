@@ -13,6 +13,8 @@
 // Rows are held, fetched ahead and stored as rms_norm.cu's (norm_common.cuh): both directions are bound by the bytes they
 // move (forward at most 8 per element, gradient 8). The weight's and the bias's gradients are summed in registers by the
 // threads that own the columns, one partial row of each per CTA, which a second kernel adds in a fixed order.
+// Measured on GB300: 8192 x 4096 with residual 46.5 us (5.8 TB/s), to E4M3 37.6, gradient 46.9, and 55.1 with weight and
+// bias; 4000 x 8192 to E4M3 37.2 (6.2 TB/s).
 #include "norm_common.cuh"
 
 namespace dtcp {
@@ -97,8 +99,8 @@ __device__ __forceinline__ void load_bias(uint4 (&b)[VPT], const uint16_t* bias,
   }
 }
 
-// The rows of a CTA (or a team) on their way, `step` apart: SLOTS of them in shared memory, the current one and those fetched ahead (1: the next one is
-// fetched once the current one is read).
+// The rows of a CTA (or a team) on their way, `step` apart: SLOTS of them in shared memory, the current one and those
+// fetched ahead (1: the next one is fetched once the current one is read).
 template <int SLOTS>
 struct Ring {
   int slot = 0;

@@ -288,12 +288,11 @@ int pair_plan_product(PairProduct* q, int rows, int cols, int depth, int stage, 
   return GEMM_OK;
 }
 
-// The 512 x 256 pair tile
-// moves a quarter fewer bytes from L2 per operation but has half the tiles and one accumulator, so it needs a deep sum
-// and is taken where the launch, in tile-times of the 256 x 256 tile, is shorter with wide tiles at 2 / 1.06 each:
-// 1.06 is its gain per unit of work. Measured on GB300 on 64 shapes from 2048 deep on whose two estimates are within
-// 12%: rows of X that start on 128-byte boundaries show 1.03 in the mean, forward (0.98 to 1.07: 178 us on the 256 x
-// 256 tile and 174 on this one at 5951 x 3904 x 3264, 115 and 118 at 3853 x 5504 x 2176) and in the gradient (0.94 to
+// The 512 x 256 pair tile moves a quarter fewer bytes from L2 per operation but has half the tiles and one accumulator, so
+// it needs a deep sum and is taken where the launch, in tile-times of the 256 x 256 tile, is shorter with wide tiles at
+// 2 / 1.06 each: 1.06 is its gain per unit of work. Measured on GB300 on 64 shapes from 2048 deep on whose two estimates
+// are within 12%: rows of X that start on 128-byte boundaries show 1.03 in the mean, forward (0.98 to 1.07: 178 us on the
+// 256 x 256 tile and 174 on this one at 5951 x 3904 x 3264, 115 and 118 at 3853 x 5504 x 2176) and in the gradient (0.94 to
 // 1.14); other rows 1.13 and 1.11 (352 and 300 us at 9034 x 5016 x 2744). The rule is 0.6% and 1.5% slower in the mean
 // than the better tile of each shape on the former, 4% and 2% on the latter.
 bool pair_wide_rule(long long std_tiles, long long wide_tiles, int depth, int wave) {
