@@ -6,7 +6,7 @@
 //
 // Gradient: positions are sorted by token (stable, so a token's rows are added in the order of their positions and the
 // same inputs give the same bits), then a CTA takes a run of sorted positions and 8 columns a thread, adds dy's rows in
-// FP32 and writes each token's row once. Tokens of more than 32 positions are summed by run, into FP32 partial rows that a
+// FP32 and writes each token's row once. Tokens of more than 16 positions are summed by run, into FP32 partial rows that a
 // last kernel adds in order: a token that is a tenth of all positions costs no more than the others.
 // The sort is a least-significant-digit radix sort of up to 10 bits a pass (two passes up to 2^20 tokens) by one cluster of
 // 8 or 16 CTAs: a warp counts the digits of its part of the list, the CTAs exchange their totals through shared memory, and every
@@ -15,8 +15,8 @@
 // hides the sort.
 //
 // Both are bound by bytes. Measured on GB300: 16384 rows of 131072 x 4096 looked up in 30.5 us (8.8 TB/s, as frequent rows
-// come from L2); their gradient 181 us in a table of zeros (6.7 TB/s: 138 the table, 43 the sums), 79 in place (sort 15,
-// sums 50, parts of long tokens 8).
+// come from L2); their gradient 180 us in a table of zeros (6.7 TB/s: 138 the table, 42 the sums), 75 in place (sort 15,
+// sums 47, parts of long tokens 8).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -344,7 +344,10 @@ struct SumParams {
 
 constexpr int kMaxRun = 256;
 constexpr int kSumThreads = 128;
-constexpr int kLong = 32;  // a token of more positions is long
+// A token of more positions is long. Whole gradient in place, us, with 32, 16 and 8: 16384 positions into 131072 x 4096 78.5,
+// 75.5, 77.2; 5003 into 50001 x 1027 FP32 27.3, 25.8, 25.3 (the rows that one CTA adds are its longest path).
+constexpr int kLong = 16;
+constexpr int kBeside = 32;  // positions that a CTA sees before and behind its run
 constexpr int kJoinAlone = 8;  // parts of a long token that one warp adds
 template <bool VECTOR, bool BASE>
 constexpr int kSumAhead = VECTOR && !BASE ? 8 : 4;  // rows of dy (and of the base) that a thread asks for together
@@ -382,19 +385,19 @@ __device__ __forceinline__ int leading(bool yes) {
 template <class DY, class TABLE, bool BASE, bool VECTOR>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumParams p) {
   constexpr int AHEAD = kSumAhead<VECTOR, BASE>;
-  __shared__ uint32_t keys[kLong + kMaxRun + kLong], places[kMaxRun + kLong];
+  __shared__ uint32_t keys[kBeside + kMaxRun + kBeside], places[kMaxRun + kBeside];
   pdl_launch_dependents();
   pdl_wait();
   const long long begin = static_cast<long long>(blockIdx.x) * p.run;
   constexpr uint32_t NONE = 0xFFFFFFFFu;
-  for (int i = threadIdx.x; i < p.run + 2 * kLong; i += blockDim.x) {
-    const long long at = begin + i - kLong;
+  for (int i = threadIdx.x; i < p.run + 2 * kBeside; i += blockDim.x) {
+    const long long at = begin + i - kBeside;
     const Entry e = at >= 0 && at < p.count ? p.list[at] : Entry{NONE, 0u};
     keys[i] = e.token < static_cast<uint32_t>(p.vocab) ? e.token : NONE;
-    if (i >= kLong) places[i - kLong] = e.pos;
+    if (i >= kBeside) places[i - kBeside] = e.pos;
   }
   __syncthreads();
-  const uint32_t* const key = keys + kLong;  // of the run's positions; from -kLong to run + kLong - 1
+  const uint32_t* const key = keys + kBeside;  // of the run's positions; from -kBeside to run + kBeside - 1
   const int lane = threadIdx.x & 31;
   if (key[0] == NONE) return;  // (positions without a token are behind all others)
   // positions first .. end - 1 are this CTA's
