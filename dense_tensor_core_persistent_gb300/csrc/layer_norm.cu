@@ -244,7 +244,7 @@ __device__ __forceinline__ void norm_edge(const LayerNormParams& p, NormShared& 
 }
 
 template <int VPT, int SLOTS, int FORMAT, int ACCESS>
-__global__ void __maxnreg__(norm_regs<VPT>(64, 128)) layer_norm_kernel(const LayerNormParams p) {
+__global__ void __maxnreg__(norm_regs<VPT>(96, 128)) layer_norm_kernel(const LayerNormParams p) {
   constexpr int AS = RowPart<ACCESS>::AS;
   extern __shared__ uint4 fetched[];  // [SLOTS][2][VPT][threads], then (KEPT) weight and bias: [2][VPT][threads]
   __shared__ NormShared sh;
@@ -438,9 +438,14 @@ __device__ __forceinline__ void norm_backward_edge(const LayerNormBackwardParams
 // partial row instead of eight. Measured on GB300 with them: 65536 x 256 39 us in CTAs of a warp and 27, 8192 x 512 20 and
 // 15. (Wider rows lose by it what they gain: with as many teams as an SM holds 8192 x 4096 58 and 61.)
 constexpr int kTeams = 8;
-template <int VPT, int SLOTS, int ACCESS, bool TEAMS>
-__global__ void __maxnreg__(norm_regs<VPT>(ACCESS == kAligned ? 80 : 88, 128))
-    layer_norm_backward_kernel(const LayerNormBackwardParams p) {
+// REGS: what holds a row, its weight and the sums of dw and db without spills, 128 with two groups a thread, even if a CTA
+// is alone on its SM then: 8192 x 4096 46.9 us with 80 registers and two CTAs, 41.3 so; 4000 x 8192 42.4, with four groups
+// (which spill) 52.3; 16000 x 1023 33.1 with 88, 28.0 so. One group with a row a warp: 64 and 80 the same 65536 x 255 in 48.7
+// and 44.4. Nine warps, the last with a row's ends, fit twice with 96: 4000 x 4099 31.6 with 128, 27.4 so; ten do too, and
+// lose by it: 4000 x 5003 35.6 and 38.7. Seventeen fit once with 96.
+constexpr int backward_regs(int vpt, int slots, bool teams) { return vpt > 1 ? 128 : slots == 4 && !teams ? 80 : 64; }
+template <int VPT, int SLOTS, int ACCESS, bool TEAMS, int REGS = backward_regs(VPT, SLOTS, TEAMS)>
+__global__ void __maxnreg__(REGS) layer_norm_backward_kernel(const LayerNormBackwardParams p) {
   constexpr int AS = RowPart<ACCESS>::AS;
   extern __shared__ uint4 fetched[];  // [teams][SLOTS][3][VPT][threads]
   __shared__ float2 slots[2][32];
@@ -587,9 +592,8 @@ __global__ void __launch_bounds__(32 * kSumWarps)
 //   forward on the 16-byte boundary four groups a thread, as what a row costs whatever its length (some 130 instructions a
 //     warp, in reductions and addresses) is most of it: 4000 x 8192 to E4M3 40.3 with two and 37.3, 16000 x 1024 14.8 and
 //     12.7; off the boundary two: 2001 x 5123 16.3 and 17.8 with four, 16000 x 1023 28.6 and 36.4;
-//   gradient two, where 80 registers let an SM hold two CTAs: 8192 x 4096 50.4 and 54.0 with four, 2000 x 5120 19.2 and
-//     20.2, but 4000 x 8192 66.5 and 53.0; on the boundary with two rows ahead instead of one: 8192 x 4096 50.9 and 47.0,
-//     2000 x 5120 19.2 and 17.4 (off it 2001 x 5123 25.4 and 26.2).
+//   gradient two up to 512 threads (four do not fit into registers, see there), with two rows ahead: one or three ahead
+//     instead cost 8192 x 4096 50.9 instead of 47.0 (with 80 registers) and 42.4 instead of 41.3.
 struct LayerNormShape {
   NormShape at;
   int slots;
@@ -599,10 +603,10 @@ LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, NormAccess acce
   if (access == kShared) {  // the whole groups, and a warp for the elements around them
     const int groups = cols / 8;
     if (groups <= 32 && rows > num_sms) return LayerNormShape{{64, 1}, 4};
-    NormShape s{0, rows <= num_sms ? 1 : groups > (forward ? 96 : 800) ? 4 : 2};
+    NormShape s{0, rows <= num_sms ? 1 : forward && groups > 96 ? 4 : 2};
     for (;; s.vpt *= 2) {
       s.threads = std::max(32, ceil_div(ceil_div(groups, s.vpt), 32) * 32);
-      if (s.threads <= (s.vpt == 1 ? 992 : 480)) break;
+      if (s.threads <= (s.vpt == 1 ? 992 : s.vpt == 2 ? 512 : 480)) break;
     }
     s.threads += 32;
     return LayerNormShape{s, s.vpt == 2 && !forward ? 3 : norm_slots(s.vpt)};
@@ -611,7 +615,7 @@ LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, NormAccess acce
   const int groups = ceil_div(cols, 8) + (is_aligned ? 0 : 1);
   if (groups <= 32 && rows > num_sms) return LayerNormShape{{32, 1}, 4};
   NormShape s = norm_shape(rows, cols, num_sms, is_aligned);
-  if (s.vpt == 2 && is_aligned && groups > (forward ? 96 : 800)) s = NormShape{ceil_div(ceil_div(groups, 4), 32) * 32, 4};
+  if (s.vpt == 2 && is_aligned && forward && groups > 96) s = NormShape{ceil_div(ceil_div(groups, 4), 32) * 32, 4};
   const bool three = s.vpt == 2 && is_aligned && !forward && s.threads > 32;
   return LayerNormShape{s, three ? 3 : norm_slots(s.vpt)};
 }
@@ -646,6 +650,8 @@ const void* backward_kernel(const LayerNormShape& s, bool teams) {
                           : reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 4, ACCESS, false>);
     case 2:
       if constexpr (ACCESS == kShared) {
+        if (s.at.threads == 288 || s.at.threads == 544)
+          return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 3, ACCESS, false, 96>);
         return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 3, ACCESS, false>);
       } else {
         if constexpr (ACCESS == kAligned)
