@@ -443,11 +443,15 @@ constexpr int kTeams = 8;
 // (which spill) 52.3; 16000 x 1023 33.1 with 88, 28.0 so. One group with a row a warp: 64 and 80 the same 65536 x 255 in 48.7
 // and 44.4. Nine warps, the last with a row's ends, fit twice with 96: 4000 x 4099 31.6 with 128, 27.4 so; ten do too, and
 // lose by it: 4000 x 5003 35.6 and 38.7. Seventeen fit once with 96.
+// Three and four groups leave no registers for the weight: 4000 x 10000 82.9 us with four and the weight in registers, 78.2
+// with three, 73.3 with three and it in shared memory; 4000 x 16384 105.0 and 96.4 with four.
+__host__ __device__ constexpr bool weight_in_shared(int vpt) { return vpt == 3 || vpt == 4; }
 constexpr int backward_regs(int vpt, int slots, bool teams) { return vpt > 1 ? 128 : slots == 4 && !teams ? 80 : 64; }
 template <int VPT, int SLOTS, int ACCESS, bool TEAMS, int REGS = backward_regs(VPT, SLOTS, TEAMS)>
 __global__ void __maxnreg__(REGS) layer_norm_backward_kernel(const LayerNormBackwardParams p) {
   constexpr int AS = RowPart<ACCESS>::AS;
-  extern __shared__ uint4 fetched[];  // [teams][SLOTS][3][VPT][threads]
+  constexpr bool KEPT = weight_in_shared(VPT);
+  extern __shared__ uint4 fetched[];  // [teams][SLOTS][3][VPT][threads], then (KEPT) the weight: [VPT][threads]
   __shared__ float2 slots[2][32];
   const int warps = blockDim.x >> 5;
   const int team = TEAMS ? static_cast<int>(threadIdx.y) : 0;
@@ -482,6 +486,12 @@ __global__ void __maxnreg__(REGS) layer_norm_backward_kernel(const LayerNormBack
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[k].v[j] = db[k].v[j] = 0;
   load_weight<VPT, ACCESS>(w, p.w, col, part.end);
+  uint4* const kept = mine + SLOTS * slot_size;
+  if constexpr (KEPT) {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) kept[k * static_cast<int>(blockDim.x)] = w[k];
+  }
+  auto weight = [&](int k) { return unpack8_pairs(KEPT ? kept[k * static_cast<int>(blockDim.x)] : w[k]); };
   float rstd = 0.0f, mean = 0.0f, rstd_next = 0.0f, mean_next = 0.0f;
   if (!TEAMS || first_row < rows) {
     rstd = p.rstd[first_row];
@@ -501,7 +511,7 @@ __global__ void __maxnreg__(REGS) layer_norm_backward_kernel(const LayerNormBack
     for (int k = 0; k < VPT; ++k) {
       const uint4 v[2] = {in[k * static_cast<int>(blockDim.x)], in[(VPT + k) * static_cast<int>(blockDim.x)]};
       // (outside the row dy is 0, and so is what it adds)
-      const P8 a = unpack8_pairs(v[0]), d = unpack8_pairs(v[1]), g = unpack8_pairs(w[k]);
+      const P8 a = unpack8_pairs(v[0]), d = unpack8_pairs(v[1]), g = weight(k);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint64_t xh = f2_mul(f2_add(a.v[j], m2), r2), dyw = f2_mul(d.v[j], g.v[j]);
@@ -518,7 +528,7 @@ __global__ void __maxnreg__(REGS) layer_norm_backward_kernel(const LayerNormBack
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const P8 a = unpack8_pairs(in[k * static_cast<int>(blockDim.x)]);
-      const P8 d = unpack8_pairs(in[(VPT + k) * static_cast<int>(blockDim.x)]), g = unpack8_pairs(w[k]);
+      const P8 d = unpack8_pairs(in[(VPT + k) * static_cast<int>(blockDim.x)]), g = weight(k);
       P8 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -592,8 +602,8 @@ __global__ void __launch_bounds__(32 * kSumWarps)
 //   forward on the 16-byte boundary four groups a thread, as what a row costs whatever its length (some 130 instructions a
 //     warp, in reductions and addresses) is most of it: 4000 x 8192 to E4M3 40.3 with two and 37.3, 16000 x 1024 14.8 and
 //     12.7; off the boundary two: 2001 x 5123 16.3 and 17.8 with four, 16000 x 1023 28.6 and 36.4;
-//   gradient two up to 512 threads (four do not fit into registers, see there), with two rows ahead: one or three ahead
-//     instead cost 8192 x 4096 50.9 instead of 47.0 (with 80 registers) and 42.4 instead of 41.3.
+//   gradient two up to 512 threads, then three, then four (see backward_regs); with two of them two rows ahead: one ahead
+//     instead cost 8192 x 4096 50.9 instead of 47.0 (with 80 registers), three 42.4 instead of 41.3.
 struct LayerNormShape {
   NormShape at;
   int slots;
@@ -608,14 +618,16 @@ LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, NormAccess acce
       s.threads = std::max(32, ceil_div(ceil_div(groups, s.vpt), 32) * 32);
       if (s.threads <= (s.vpt == 1 ? 992 : s.vpt == 2 ? 512 : 480)) break;
     }
+    if (s.vpt == 4 && !forward && groups <= 3 * 480) s = NormShape{ceil_div(ceil_div(groups, 3), 32) * 32, 3};
     s.threads += 32;
-    return LayerNormShape{s, s.vpt == 2 && !forward ? 3 : norm_slots(s.vpt)};
+    return LayerNormShape{s, s.vpt == 2 && !forward ? 3 : s.vpt == 3 ? 2 : norm_slots(s.vpt)};
   }
   const bool is_aligned = access == kAligned;
   const int groups = ceil_div(cols, 8) + (is_aligned ? 0 : 1);
   if (groups <= 32 && rows > num_sms) return LayerNormShape{{32, 1}, 4};
   NormShape s = norm_shape(rows, cols, num_sms, is_aligned);
   if (s.vpt == 2 && is_aligned && forward && groups > 96) s = NormShape{ceil_div(ceil_div(groups, 4), 32) * 32, 4};
+  if (s.vpt == 4 && !forward && groups <= 3 * 512) return LayerNormShape{{ceil_div(ceil_div(groups, 3), 32) * 32, 3}, 2};
   const bool three = s.vpt == 2 && is_aligned && !forward && s.threads > 32;
   return LayerNormShape{s, three ? 3 : norm_slots(s.vpt)};
 }
@@ -658,6 +670,7 @@ const void* backward_kernel(const LayerNormShape& s, bool teams) {
           if (s.slots == 3) return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 3, ACCESS, false>);
         return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 2, ACCESS, false>);
       }
+    case 3: return reinterpret_cast<const void*>(layer_norm_backward_kernel<3, 2, ACCESS, false>);
     case 4: return reinterpret_cast<const void*>(layer_norm_backward_kernel<4, 2, ACCESS, false>);
     default: return reinterpret_cast<const void*>(layer_norm_backward_kernel<8, 1, ACCESS, false>);
   }
@@ -797,7 +810,7 @@ int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const
                        : access == kShared ? backward_kernel<kShared>(shape, teams)
                                            : backward_kernel<kElements>(shape, teams);
   const dim3 threads(shape.at.threads, teams ? kTeams : 1);
-  const int smem = shape.smem(3, 0) * static_cast<int>(threads.y);
+  const int smem = shape.smem(3, weight_in_shared(shape.at.vpt) ? 1 : 0) * static_cast<int>(threads.y);
   const int grid = norm_grid(kernel, rows, static_cast<int>(threads.x * threads.y), smem, info->num_sms);
   if (grid == 0) return GEMM_ERR_LAUNCH;
   void* ws = nullptr;

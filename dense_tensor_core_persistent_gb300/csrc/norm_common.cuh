@@ -16,7 +16,8 @@
 
 namespace dtcp {
 
-constexpr int kNormMaxSmem = 3 * 8 * 512 * 16;  // dynamic shared memory of a CTA: three inputs, eight groups
+// Dynamic shared memory of a CTA, at most: three inputs of two rows and a weight, four groups a thread.
+constexpr int kNormMaxSmem = (2 * 3 + 1) * 4 * 512 * 16;
 constexpr float kNormMostInverse = 1.7014118346046923e38f;  // 2^127, of an E4M3 row's scale
 constexpr int kNormMaxCols = 32768 - 8;  // 8 groups of 8 columns x 512 threads, less one group for the boundary
 

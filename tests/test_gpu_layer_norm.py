@@ -331,3 +331,21 @@ def test_graph_capture():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(got, want))
+
+
+# nine, sixteen and seventeen warps with the last at a row's ends; two, three and four groups a thread on either side of
+# where they begin
+@pytest.mark.parametrize("cols", [4095, 4097, 4604, 4617, 7675, 7693, 8190, 8192, 8193, 8200, 10001, 11527, 11530, 12288, 12290,
+                                  12296])
+@pytest.mark.parametrize("own", [False, True])
+def test_backward_around_the_shapes(cols, own):
+    """`own`: rows whose tensors lie differently against the 16-byte boundary."""
+    rows = 330
+    x, r, w, b = problem(rows, cols, cols)
+    dy, ds = rand(5, rows, cols), rand(6, rows, cols, std=0.5)
+    n = g.layer_norm(dev(x), dev(w), dev(b), residual=dev(r), eps=EPS, save=True)
+    put = dev(dy)
+    if own:
+        put = torch.empty(rows, cols + 5, dtype=BF16, device=DEV)[:, 3:cols + 3]
+        put.copy_(dy)
+    check_backward(*g.layer_norm_backward(put, n.sum, dev(w), n.mean, n.rstd, dsum=dev(ds)), dy, Definition(x, r, w, b), ds)
