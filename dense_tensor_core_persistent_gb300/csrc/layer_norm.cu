@@ -601,19 +601,28 @@ __global__ void __launch_bounds__(32 * kSumWarps)
 //     65536 x 256 forward 26 with two groups a thread and one row ahead, 17 so; gradient 43 and 26;
 //   forward on the 16-byte boundary four groups a thread, as what a row costs whatever its length (some 130 instructions a
 //     warp, in reductions and addresses) is most of it: 4000 x 8192 to E4M3 40.3 with two and 37.3, 16000 x 1024 14.8 and
-//     12.7; off the boundary two: 2001 x 5123 16.3 and 17.8 with four, 16000 x 1023 28.6 and 36.4;
+//     12.7; off the boundary two where two CTAs fit: 16000 x 1023 31.4 with four and 25.4, 4000 x 7001 38.5 and 45.2;
+//   four streams that pass L2 (two in, two out), on the boundary: with all rows that fit on their way, memory turns between
+//     reads and writes more than it need, so an SM has 8192 columns of rows at a time, two groups a thread and (from 4096
+//     columns on) two rows ahead: 8192 x 4096 46.5 with four groups and four CTAs an SM and 42.7, 32000 x 1024 45.3 and
+//     41.6, 4000 x 8192 44.5 and 41.5 (5000 x 4096, in L2 for the most part, 27.2 and 26.3);
 //   gradient two up to 512 threads, then three, then four (see backward_regs); with two of them two rows ahead: one ahead
 //     instead cost 8192 x 4096 50.9 instead of 47.0 (with 80 registers), three 42.4 instead of 41.3.
+constexpr int kSmemOfSm = 228 * 1024;
 struct LayerNormShape {
   NormShape at;
   int slots;
-  int smem(int tensors, int kept) const { return (slots * tensors + kept) * at.vpt * at.threads * 16; }
+  int most = 0;  // CTAs of an SM (0: as many as fit)
+  int smem(int tensors, int kept) const {
+    // (a limit by shared memory that one more CTA does not find, as a smaller grid would not spread evenly over the SMs)
+    return std::max((slots * tensors + kept) * at.vpt * at.threads * 16, most > 0 ? kSmemOfSm / (most + 1) : 0);
+  }
 };
-LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, NormAccess access, bool forward) {
+LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, NormAccess access, bool forward, bool four_streams) {
   if (access == kShared) {  // the whole groups, and a warp for the elements around them
     const int groups = cols / 8;
     if (groups <= 32 && rows > num_sms) return LayerNormShape{{64, 1}, 4};
-    NormShape s{0, rows <= num_sms ? 1 : forward && groups > 96 ? 4 : 2};
+    NormShape s{0, rows <= num_sms ? 1 : forward && groups > 704 ? 4 : 2};
     for (;; s.vpt *= 2) {
       s.threads = std::max(32, ceil_div(ceil_div(groups, s.vpt), 32) * 32);
       if (s.threads <= (s.vpt == 1 ? 992 : s.vpt == 2 ? 512 : 480)) break;
@@ -625,6 +634,9 @@ LayerNormShape layer_norm_shape(int rows, int cols, int num_sms, NormAccess acce
   const bool is_aligned = access == kAligned;
   const int groups = ceil_div(cols, 8) + (is_aligned ? 0 : 1);
   if (groups <= 32 && rows > num_sms) return LayerNormShape{{32, 1}, 4};
+  if (four_streams && rows > num_sms && groups > 96 && groups <= 1024) {
+    return LayerNormShape{{ceil_div(ceil_div(groups, 2), 32) * 32, 2}, groups < 512 ? 2 : 3, (1024 + groups / 2) / groups};
+  }
   NormShape s = norm_shape(rows, cols, num_sms, is_aligned);
   if (s.vpt == 2 && is_aligned && forward && groups > 96) s = NormShape{ceil_div(ceil_div(groups, 4), 32) * 32, 4};
   if (s.vpt == 4 && !forward && groups <= 3 * 512) return LayerNormShape{{ceil_div(ceil_div(groups, 3), 32) * 32, 3}, 2};
@@ -638,7 +650,10 @@ const void* forward_kernel(const LayerNormShape& s) {
     case 1:
       return s.slots == 1 ? reinterpret_cast<const void*>(layer_norm_kernel<1, 1, FORMAT, ACCESS>)
                           : reinterpret_cast<const void*>(layer_norm_kernel<1, 4, FORMAT, ACCESS>);
-    case 2: return reinterpret_cast<const void*>(layer_norm_kernel<2, 2, FORMAT, ACCESS>);
+    case 2:
+      if constexpr (FORMAT == GEMM_NORM_BF16 && ACCESS == kAligned)
+        if (s.slots == 3) return reinterpret_cast<const void*>(layer_norm_kernel<2, 3, FORMAT, ACCESS>);
+      return reinterpret_cast<const void*>(layer_norm_kernel<2, 2, FORMAT, ACCESS>);
     case 4: return reinterpret_cast<const void*>(layer_norm_kernel<4, 2, FORMAT, ACCESS>);
     default: return reinterpret_cast<const void*>(layer_norm_kernel<8, 1, FORMAT, ACCESS>);
   }
@@ -747,7 +762,9 @@ int gemm_layer_norm(const void* X, const void* R, const void* W, const void* B, 
   const DeviceInfo* info = current_device_info(&device, &err);
   if (info == nullptr) return err;
   const NormAccess access = norm_access(aligned, shared, cols);
-  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, access, true);
+  const bool four_streams =  // (some 1.5 times L2)
+      access == kAligned && R != nullptr && format == GEMM_NORM_BF16 && 16LL * rows * cols > 3 * info->l2_bytes;
+  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, access, true, four_streams);
   const void* kernel = format == GEMM_NORM_NVFP4  ? forward_kernel<GEMM_NORM_NVFP4, kAligned>(shape)
                        : format == GEMM_NORM_E4M3 ? forward_kernel<GEMM_NORM_E4M3>(shape, access)
                                                   : forward_kernel<GEMM_NORM_BF16>(shape, access);
@@ -803,7 +820,7 @@ int gemm_layer_norm_backward(const void* dY, const void* S, const void* W, const
                       RowPlace(dX, p.lddx, 2) == place;
   const bool aligned = shared && place.aligned() && cols % 8 == 0 && !misaligned(W, 16);
   const NormAccess access = norm_access(aligned, shared, cols);
-  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, access, false);
+  const LayerNormShape shape = layer_norm_shape(rows, cols, info->num_sms, access, false, false);
   // (a grid of a multiple of 8, or a row a team: rows of a CTA share the column at which their boundary lies)
   const bool teams = sums && shape.at.threads == 32 && rows > info->num_sms && info->num_sms % 8 == 0;
   const void* kernel = access == kAligned  ? backward_kernel<kAligned>(shape, teams)
