@@ -13,8 +13,8 @@
 // Rows are held, fetched ahead and stored as rms_norm.cu's (norm_common.cuh): both directions are bound by the bytes they
 // move (forward at most 8 per element, gradient 8). The weight's and the bias's gradients are summed in registers by the
 // threads that own the columns, one partial row of each per CTA, which a second kernel adds in a fixed order.
-// Measured on GB300: 8192 x 4096 with residual 46.5 us (5.8 TB/s), to E4M3 37.6, gradient 46.9, and 55.1 with weight and
-// bias; 4000 x 8192 to E4M3 37.2 (6.2 TB/s).
+// Measured on GB300: 8192 x 4096 with residual 42.8 us (6.3 TB/s), to E4M3 37.6, gradient 41.0 (6.5 TB/s), and 47.1 with
+// weight and bias; 4000 x 8192 to E4M3 37.2 (6.2 TB/s).
 #include "norm_common.cuh"
 
 namespace dtcp {
@@ -145,7 +145,8 @@ __device__ __forceinline__ void launch_dependents(int rows) {
 // Rows off the 16-byte boundary whose tensors share it (kShared): the whole vectors between a row's first and last boundary
 // are the groups of the CTA's threads, as on the boundary, and the up to 14 elements around them belong to the lanes of one
 // more warp, the last. With the ends as masked groups of the first and last warp instead, which the others then waited for,
-// 2001 x 5123 took 16.5 us forward (13.3 so) and its gradient 25.0 (22.3), 16000 x 1023 29.6 (25.4) and 39.7 (33.2).
+// 2001 x 5123 took 16.5 us forward (13.3 so) and its gradient 25.0 (22.3), 16000 x 1023 29.6 (25.4) and 39.7 (33.2), groups
+// and registers as they were then: 13.4 and 19.8, 19.7 and 27.9 with those below.
 template <int ACCESS>
 struct RowPart {
   static constexpr int AS = ACCESS == kShared ? kAligned : ACCESS;  // how groups are read and written
