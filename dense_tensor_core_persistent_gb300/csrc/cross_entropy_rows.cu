@@ -3,14 +3,15 @@
 // W's bytes are the bound, and on the 256-row pair tile most of each MMA would multiply rows that X does not have. Here 128
 // rows of W are the MMA's M and the rows of X its N: accumulator lane v holds the logits of token v, columns are the rows
 // of X. A CTA takes a run of the vocabulary in boxes of 32 tokens, so all CTAs stream the same bytes whatever the
-// vocabulary; its tiles are four boxes, the last one fewer. The depth is summed in parts of 512 (pair_tile.cuh says why),
+// vocabulary; its tiles are of up to four boxes and about the same size (a last one of what is left, which has less on its
+// way at a time, cost 30 x 100000 x 2048 72 us instead of 69). The depth is summed in parts of 512 (pair_tile.cuh says why),
 // which the epilogue adds in FP32.
 // The softmax is one pass: a thread keeps, for its lane's tokens and each of its rows of X, the maximum and the sum of the
 // others relative to it through all of the CTA's tiles; lanes, warps and (in the joining kernel) CTAs are joined at the
 // end, in a fixed order.
 //
-// Measured on GB300 with W of 131072 x 4096 (1.07 GB, 158 us at the rate of a copy): 1 row 159 to 169 us, where the pair
-// tile took 290; 16 rows 176; 64 rows 168, where the pair tile's 65 rows take 193 and its 128 191.
+// Measured on GB300 with W of 131072 x 4096 (1.07 GB, 158 us at the rate of a copy): 1 row 158 to 163 us, where the pair
+// tile took 290; 64 rows 160 to 166, where the pair tile's 65 rows take 193 and its 128 191.
 //
 // One persistent CTA per SM. Warp roles: 0 loads W, 2 loads X, 1 allocates TMEM and issues the MMAs, 4..11 epilogue, two
 // to each TMEM lane quadrant with half of X's rows each. Two accumulators in TMEM.
@@ -49,8 +50,8 @@ struct LossRowsLayout {
   static constexpr int OFF_W = 0;
   static constexpr int OFF_X = STAGES * W_BYTES;
   static constexpr int OFF_JOIN = OFF_X + STAGES * X_BYTES;       // [4][X_ROWS] (m, others)
-  static constexpr int OFF_TARGET = OFF_JOIN + 4 * X_ROWS * 8;    // [X_ROWS] int
-  static constexpr int OFF_BAR = OFF_TARGET + X_ROWS * 4;
+  static constexpr int OFF_TARGET = OFF_JOIN + 4 * X_ROWS * 8;    // [EPI_WARPS][COLS] int
+  static constexpr int OFF_BAR = OFF_TARGET + EPI_WARPS * COLS * 4;
   // full[S], empty[S], tmem_full[2], tmem_empty[2], drain
   static constexpr int NUM_BARS = 2 * STAGES + 5;
   static constexpr int OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
@@ -58,6 +59,24 @@ struct LossRowsLayout {
   static constexpr int SMEM_BYTES = OFF_ABORT + 4 + 1024;  // slack to align the base to 1024 bytes
   static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
 };
+
+// Joins the warp's lanes for each of COLS columns: lanes exchange halves of their columns until each has one, 31 joins a
+// lane for 32 columns where column by column would be 160 (64 x 131072 x 1024 54.4 us by columns, 47.7 so). Lane l has
+// column l * COLS / 32.
+template <int COLS>
+__device__ __forceinline__ SoftmaxPart join_lanes(SoftmaxPart (&s)[COLS], float c) {
+  const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16, n = COLS / 2; o > 0; o >>= 1, n >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int j = 0; j < (n > 0 ? n : 1); ++j) {
+      const SoftmaxPart keep = n > 0 && up ? s[j + n] : s[j], give = n > 0 && !up ? s[j + n] : s[j];
+      s[j] = join(keep, SoftmaxPart{__shfl_xor_sync(0xffffffffu, give.m, o), __shfl_xor_sync(0xffffffffu, give.others, o)}, c);
+    }
+  }
+  return s[0];
+}
 
 // COLS columns of this warp's TMEM lanes.
 template <int COLS>
@@ -81,7 +100,6 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
   const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_TMEM_SLOT);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_ABORT);
-  int* const target = reinterpret_cast<int*>(smem + L::OFF_TARGET);
   const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
 
   if (warp == 0 && lane == 0) {
@@ -102,26 +120,24 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
     tmem_relinquish<1>();
   }
   pdl_launch_dependents();
-  pdl_wait();
-  if (threadIdx.x < X_ROWS) {  // (no target, and one past the vocabulary: no token)
-    const int r = static_cast<int>(threadIdx.x);
-    const long long t = p.x.targets != nullptr && r < p.x.rows ? p.x.targets[r] : -1;
-    target[r] = t >= 0 && t < p.x.vocab ? static_cast<int>(t) : -1;
-  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
   // this CTA's boxes
   const int box0 = static_cast<int>(static_cast<long long>(blockIdx.x) * p.boxes / gridDim.x);
   const int box1 = static_cast<int>((static_cast<long long>(blockIdx.x) + 1) * p.boxes / gridDim.x);
+  const int tiles = (box1 - box0 + L::TILE_BOXES - 1) / L::TILE_BOXES;  // of about the same size
+  const int each = (box1 - box0) / tiles, one_more = (box1 - box0) % tiles;
+  auto tile_box = [&](int t) { return box0 + t * each + min(t, one_more); };
 
   if ((warp == L::WARP_W || warp == L::WARP_X) && lane == 0) {
     // ------------------------------------------------------------ producers
     uint32_t stage = 0, phase = 0;
     bool ok = true;
-    for (int b = box0; b < box1 && ok; b += L::TILE_BOXES) {
-      const int boxes = min(L::TILE_BOXES, box1 - b);
+    for (int t = 0; t < tiles && ok; ++t) {
+      const int b = tile_box(t), boxes = tile_box(t + 1) - b;
       for (int k = 0; k < p.k_iters; ++k) {
         if (!wait_phase_inline(bar_empty + 8 * stage, phase ^ 1u, wctx, status_code(kRoleProducer, stage))) {
           ok = false;
@@ -154,7 +170,7 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
     const uint64_t a0 = umma_desc_sw128(base + L::OFF_W), b0 = umma_desc_sw128(base + L::OFF_X);
     uint32_t stage = 0, phase = 0, acc = 0, slot = 0;
     bool ok = true;
-    for (int t = box0; t < box1 && ok; t += L::TILE_BOXES) {
+    for (int t = 0; t < tiles && ok; ++t) {
       for (int k = 0; k < p.k_iters; ++k) {
         const int in_part = k % L::SUM_STAGES;
         if (in_part == 0) {
@@ -208,15 +224,22 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
     const uint32_t q = warp & 3u;                                    // TMEM lanes 32q .. 32q+31
     const int col0 = static_cast<int>((warp - L::EPI_WARP0) >> 2) * L::COLS;  // its rows of X
     const bool live = col0 < p.x.rows;
+    int* const target = reinterpret_cast<int*>(smem + L::OFF_TARGET) + (warp - L::EPI_WARP0) * L::COLS;  // of its rows
+    if (lane < L::COLS) {  // (no target, and one past the vocabulary: no token)
+      const int r = col0 + static_cast<int>(lane);
+      const long long t = p.x.targets != nullptr && r < p.x.rows ? p.x.targets[r] : -1;
+      target[lane] = t >= 0 && t < p.x.vocab ? static_cast<int>(t) : -1;
+    }
+    __syncwarp();
     const int parts = (p.k_iters + L::SUM_STAGES - 1) / L::SUM_STAGES;
     SoftmaxPart s[L::COLS];
 #pragma unroll
     for (int j = 0; j < L::COLS; ++j) s[j] = SoftmaxPart{-INFINITY, -1.0f};
     uint32_t acc = 0;
     bool ok = true;
-    for (int b = box0; b < box1 && ok; b += L::TILE_BOXES) {
-      const int token = (b + static_cast<int>(q)) * L::BOX + static_cast<int>(lane);
-      const bool in = b + static_cast<int>(q) < box1 && token < p.x.vocab;
+    for (int t = 0; t < tiles && ok; ++t) {
+      const int b = tile_box(t), token = (b + static_cast<int>(q)) * L::BOX + static_cast<int>(lane);
+      const bool in = b + static_cast<int>(q) < tile_box(t + 1) && token < p.x.vocab;
       float z[L::COLS];
 #pragma unroll 1
       for (int part = 0; part < parts; ++part, ++acc) {
@@ -238,21 +261,15 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
       if (!ok || !live || !in) continue;
 #pragma unroll
       for (int j = 0; j < L::COLS; ++j) {
-        if (target[col0 + j] == token) p.x.target_z[col0 + j] = z[j];
+        if (target[j] == token) p.x.target_z[col0 + j] = z[j];
         // the new logit is the maximum, or one of the others; minus infinity adds nothing to either
         const float d = z[j] - s[j].m, e = ex2_approx(-fabsf(d) * c);
         if (z[j] != -INFINITY) s[j].others = d > 0.0f ? (s[j].others + 1.0f) * e : s[j].others + e;
         s[j].m = fmaxf(s[j].m, z[j]);
       }
     }
-#pragma unroll
-    for (int j = 0; j < L::COLS; ++j) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        s[j] = join(s[j], SoftmaxPart{__shfl_down_sync(0xffffffffu, s[j].m, o),
-                                      __shfl_down_sync(0xffffffffu, s[j].others, o)}, c);
-      if (lane == 0) joined[q * X_ROWS + col0 + j] = make_float2(s[j].m, s[j].others);
-    }
+    const SoftmaxPart all = join_lanes<L::COLS>(s, c);
+    if (lane % (32 / L::COLS) == 0) joined[q * X_ROWS + col0 + lane / (32 / L::COLS)] = make_float2(all.m, all.others);
   }
   __syncwarp();
   tc_fence_before_sync();
