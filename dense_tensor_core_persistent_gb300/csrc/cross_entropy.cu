@@ -11,7 +11,8 @@
 //
 // Gradient: for a piece of the vocabulary at a time the logits are computed again, their epilogue turns them into G
 // (BF16, the operand of two products) and pair_gradient.cu's launch takes G to the piece's rows of dW and to dX, whose
-// pieces are added in FP32. A piece is as large as G's workspace may be; fewer pieces are fewer joins and ramps. Not
+// pieces are added in FP32. (Up to 64 rows the logits come from cross_entropy_rows.cu here too: gradient of 64 x 131072 x
+// 4096 605 and 592 us, of 30 x 100000 x 2048 286 and 244.) A piece is as large as G's workspace may be; fewer pieces are fewer joins and ramps. Not
 // keeping z costs its product a second time: 8 MVK operations where 6 would do with M x V logits in memory.
 //
 // Bound by the tensor cores, for few rows by W's bytes. Measured on GB300: 4096 x 131072 x 4096 forward 2.24 ms (1.96
@@ -41,10 +42,7 @@ struct LossParams : PairParams {
   float2* parts;     // [blocks of 256 columns][2][rows]: (m, sum of the others)
   float2* extra;     // [tiles cut in halves][2][rows of a tile]: the second 64 columns of a half
   float* target_z;   // [rows]
-  // gradient
-  const float* lse;
-  const float* dloss;  // or null
-  const float* dlse;   // or null
+  LossGradient grad;
 };
 
 // The place of a tile in its product's order.
@@ -132,37 +130,21 @@ struct LossRow {
 
 // One row of the gradient's epilogue: logits become G.
 struct GradRow {
-  float lse, softmax, onehot, scale;
-  long long target;
-  bool dead;  // no gradient reaches the row: G is 0 whatever its logits are
+  GradientRow g;
+  float scale;
   __device__ __forceinline__ void begin(const LossParams& p, int row) {
-    target = -1;
-    lse = softmax = onehot = 0.0f;
+    g = GradientRow(p.grad, row);
     scale = p.scale;
-    if (row < p.main.rows) {
-      const long long t = p.targets != nullptr ? p.targets[row] : -1;
-      lse = p.lse[row];
-      if (t >= 0 && p.dloss != nullptr) {
-        onehot = t < p.vocab ? p.dloss[row] : __int_as_float(0x7FC00000);
-        target = t - p.first_col;
-      }
-      softmax = onehot + (p.dlse != nullptr ? p.dlse[row] : 0.0f);
-    }
-    dead = onehot == 0.0f && softmax == 0.0f;
-    softmax *= scale;
-    onehot *= scale;
   }
   __device__ __forceinline__ void chunk(uint32_t (&v)[32], int col) const {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float e = ex2_approx(fmaf(__uint_as_float(v[j]), scale, -lse) * kLog2e) * softmax;
-      v[j] = __float_as_uint(dead ? 0.0f : e);
-    }
-    const long long t = target - col;
+    for (int j = 0; j < 32; ++j)
+      v[j] = __float_as_uint(gradient_of(__uint_as_float(v[j]), scale, g.lse, g.softmax, g.dead));
+    const long long t = g.target - col;
     if (t >= 0 && t < 32) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (t == j) v[j] = __float_as_uint(__uint_as_float(v[j]) - onehot);
+        if (t == j) v[j] = __float_as_uint(__uint_as_float(v[j]) - g.onehot);
     }
   }
 };
@@ -691,17 +673,18 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
     select(first);
     LossParams p = {};
     p.scale = scale;
-    p.targets = targets;
     p.first_col = first;
-    p.vocab = vocab;
-    p.lse = lse;
-    p.dloss = dloss;
-    p.dlse = dlse;
+    p.grad = LossGradient{targets, lse, dloss, dlse, M, vocab, first, scale};
     const bool wide = grad_wide(M, q.features[0], K, wave);
-    st = pair_plan_product(&p.main, M, q.features[0], K, wide ? 64 : 128, 1, 1, wide ? 2 * L::TILE_M : L::TILE_M,
-                           L::BLOCK_N);
-    if (st == GEMM_OK)
-      st = loss_launch(p, wide ? kGradWide : kGrad, X, ld.x, W, K, q.features[0], ws, ldg, device, info, s);
+    if (M <= kLossRows) {
+      st = run_loss_rows_gradient(LossRowsOperands{X, q.w[0], nullptr, nullptr, nullptr, ld.x, M, q.features[0], K, scale},
+                                  p.grad, ws, ldg, device, info, s);
+    } else {
+      st = pair_plan_product(&p.main, M, q.features[0], K, wide ? 64 : 128, 1, 1, wide ? 2 * L::TILE_M : L::TILE_M,
+                             L::BLOCK_N);
+      if (st == GEMM_OK)
+        st = loss_launch(p, wide ? kGradWide : kGrad, X, ld.x, W, K, q.features[0], ws, ldg, device, info, s);
+    }
     // (a last piece of fewer slices adds to the first ones)
     if (st == GEMM_OK && first > 0) st = pair_gradient_plan(q, device, &plan);
     if (st == GEMM_OK) st = pair_gradient_launch(q, &plan, sums, device, info, s);

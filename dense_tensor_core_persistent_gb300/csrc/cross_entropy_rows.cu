@@ -1,4 +1,5 @@
-// cross_entropy_rows.cu -- the forward pass of the head's cross entropy for up to 64 rows, from a single position on.
+// cross_entropy_rows.cu -- the logits of the head's cross entropy for up to 64 rows, from a single position on: their
+// softmax statistics, or what they become in the gradient.
 //
 // W's bytes are the bound, and on the 256-row pair tile most of each MMA would multiply rows that X does not have. Here 128
 // rows of W are the MMA's M and the rows of X its N: accumulator lane v holds the logits of token v, columns are the rows
@@ -28,6 +29,9 @@ namespace {
 
 struct LossRowsParams {
   LossRowsOperands x;
+  LossGradient grad;
+  uint16_t* g;  // gradient
+  long long ldg;
   int k_iters, boxes;  // stages of a tile; boxes of 32 tokens in all
   int n;               // the MMA's N: the rows of X, rounded up to a multiple of 16
   unsigned* status;
@@ -50,8 +54,8 @@ struct LossRowsLayout {
   static constexpr int OFF_W = 0;
   static constexpr int OFF_X = STAGES * W_BYTES;
   static constexpr int OFF_JOIN = OFF_X + STAGES * X_BYTES;       // [4][X_ROWS] (m, others)
-  static constexpr int OFF_TARGET = OFF_JOIN + 4 * X_ROWS * 8;    // [EPI_WARPS][COLS] int
-  static constexpr int OFF_BAR = OFF_TARGET + EPI_WARPS * COLS * 4;
+  static constexpr int OFF_ROWS = OFF_JOIN + 4 * X_ROWS * 8;      // [EPI_WARPS][COLS]: forward targets, else float4
+  static constexpr int OFF_BAR = OFF_ROWS + EPI_WARPS * COLS * 16;
   // full[S], empty[S], tmem_full[2], tmem_empty[2], drain
   static constexpr int NUM_BARS = 2 * STAGES + 5;
   static constexpr int OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
@@ -86,7 +90,7 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[COLS]
   else tmem_ld_32x32b_x32(taddr, v);
 }
 
-template <int X_ROWS>
+template <int X_ROWS, bool GRAD>
 __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
     loss_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ LossRowsParams p) {
@@ -224,8 +228,19 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
     const uint32_t q = warp & 3u;                                    // TMEM lanes 32q .. 32q+31
     const int col0 = static_cast<int>((warp - L::EPI_WARP0) >> 2) * L::COLS;  // its rows of X
     const bool live = col0 < p.x.rows;
-    int* const target = reinterpret_cast<int*>(smem + L::OFF_TARGET) + (warp - L::EPI_WARP0) * L::COLS;  // of its rows
-    if (lane < L::COLS) {  // (no target, and one past the vocabulary: no token)
+    // of its rows: the target's token (no target, and one past the vocabulary: none); in the gradient its factors too
+    uint8_t* const of_rows = smem + L::OFF_ROWS + (warp - L::EPI_WARP0) * L::COLS * 16;
+    int* const target = reinterpret_cast<int*>(of_rows);
+    float4* const factors = reinterpret_cast<float4*>(of_rows);
+    uint32_t dead = 0;
+    if constexpr (GRAD) {
+      const GradientRow g(p.grad, col0 + static_cast<int>(lane));
+      if (lane < L::COLS) {
+        const int token = g.target >= 0 && g.target < p.x.vocab ? static_cast<int>(g.target) : -1;
+        factors[lane] = make_float4(g.lse, g.softmax, g.onehot, __int_as_float(token));
+      }
+      dead = __ballot_sync(0xffffffffu, g.dead);
+    } else if (lane < L::COLS) {
       const int r = col0 + static_cast<int>(lane);
       const long long t = p.x.targets != nullptr && r < p.x.rows ? p.x.targets[r] : -1;
       target[lane] = t >= 0 && t < p.x.vocab ? static_cast<int>(t) : -1;
@@ -259,6 +274,18 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
         for (int j = 0; j < L::COLS; ++j) z[j] = part == 0 ? __uint_as_float(v[j]) : z[j] + __uint_as_float(v[j]);
       }
       if (!ok || !live || !in) continue;
+      if constexpr (GRAD) {
+        uint16_t* const to = p.g + col0 * p.ldg + token;
+#pragma unroll
+        for (int j = 0; j < L::COLS; ++j) {
+          if (col0 + j >= p.x.rows) break;
+          const float4 f = factors[j];
+          float v = gradient_of(z[j], p.x.scale, f.x, f.y, (dead >> j & 1u) != 0u);
+          if (__float_as_int(f.w) == token) v -= f.z;
+          to[j * p.ldg] = static_cast<uint16_t>(pack_bf16x2_rn(__float_as_uint(v), 0u) & 0xFFFFu);
+        }
+        continue;
+      }
 #pragma unroll
       for (int j = 0; j < L::COLS; ++j) {
         if (target[j] == token) p.x.target_z[col0 + j] = z[j];
@@ -268,13 +295,15 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
         s[j].m = fmaxf(s[j].m, z[j]);
       }
     }
-    const SoftmaxPart all = join_lanes<L::COLS>(s, c);
-    if (lane % (32 / L::COLS) == 0) joined[q * X_ROWS + col0 + lane / (32 / L::COLS)] = make_float2(all.m, all.others);
+    if constexpr (!GRAD) {
+      const SoftmaxPart all = join_lanes<L::COLS>(s, c);
+      if (lane % (32 / L::COLS) == 0) joined[q * X_ROWS + col0 + lane / (32 / L::COLS)] = make_float2(all.m, all.others);
+    }
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if (threadIdx.x < static_cast<unsigned>(p.x.rows)) {
+  if (!GRAD && threadIdx.x < static_cast<unsigned>(p.x.rows)) {
     SoftmaxPart s{-INFINITY, -1.0f};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -289,10 +318,10 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
   }
 }
 
-template <int X_ROWS>
-int launch_rows(const LossRowsOperands& x, int device, const DeviceInfo* info, cudaStream_t stream) {
+template <int X_ROWS, bool GRAD>
+int launch_rows(const LossRowsOperands& x, const LossGradient& grad, void* g, long long ldg, int device, const DeviceInfo* info, cudaStream_t stream) {
   using L = LossRowsLayout<X_ROWS>;
-  const auto kernel = loss_rows_kernel<X_ROWS>;
+  const auto kernel = loss_rows_kernel<X_ROWS, GRAD>;
   {
     static std::mutex mu;
     static bool done[64] = {};
@@ -307,6 +336,9 @@ int launch_rows(const LossRowsOperands& x, int device, const DeviceInfo* info, c
   }
   LossRowsParams p;
   p.x = x;
+  p.grad = grad;
+  p.g = static_cast<uint16_t*>(g);
+  p.ldg = ldg;
   p.n = ceil_div(x.rows, 16) * 16;
   p.k_iters = ceil_div(x.depth, L::STAGE_K);
   p.boxes = ceil_div(x.vocab, L::BOX);
@@ -343,7 +375,14 @@ int launch_rows(const LossRowsOperands& x, int device, const DeviceInfo* info, c
 int loss_rows_ctas(int vocab, const DeviceInfo* info) { return std::min(ceil_div(vocab, 32), info->num_sms); }
 
 int run_loss_rows(const LossRowsOperands& p, int device, const DeviceInfo* info, cudaStream_t stream) {
-  return p.rows <= 16 ? launch_rows<16>(p, device, info, stream) : launch_rows<64>(p, device, info, stream);
+  return p.rows <= 16 ? launch_rows<16, false>(p, LossGradient{}, nullptr, 0, device, info, stream)
+                      : launch_rows<64, false>(p, LossGradient{}, nullptr, 0, device, info, stream);
+}
+
+int run_loss_rows_gradient(const LossRowsOperands& p, const LossGradient& grad, void* g, long long ldg, int device,
+                           const DeviceInfo* info, cudaStream_t stream) {
+  return p.rows <= 16 ? launch_rows<16, true>(p, grad, g, ldg, device, info, stream)
+                      : launch_rows<64, true>(p, grad, g, ldg, device, info, stream);
 }
 
 }  // namespace dtcp
