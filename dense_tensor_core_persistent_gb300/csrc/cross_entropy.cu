@@ -12,8 +12,9 @@
 // Gradient: for a piece of the vocabulary at a time the logits are computed again, their epilogue turns them into G
 // (BF16, the operand of two products) and pair_gradient.cu's launch takes G to the piece's rows of dW and to dX, whose
 // pieces are added in FP32. (Up to 64 rows the logits come from cross_entropy_rows.cu here too: gradient of 64 x 131072 x
-// 4096 605 and 592 us, of 30 x 100000 x 2048 286 and 244.) A piece is as large as G's workspace may be; fewer pieces are fewer joins and ramps. Not
-// keeping z costs its product a second time: 8 MVK operations where 6 would do with M x V logits in memory.
+// 4096 605 and 592 us, of 30 x 100000 x 2048 286 and 244.) A piece is as large as G's workspace may be; fewer pieces are
+// fewer joins and ramps. Not keeping z costs its product a second time: 8 MVK operations where 6 would do with M x V logits
+// in memory.
 //
 // Bound by the tensor cores, for few rows by W's bytes. Measured on GB300: 4096 x 131072 x 4096 forward 2.24 ms (1.96
 // PFLOP/s), gradient 7.3 ms on a cool device (1.81 PFLOP/s over its three products) and up to 8.0 ms under the power cap;
