@@ -18,7 +18,7 @@
 //
 // Bound by the tensor cores, for few rows by W's bytes. Measured on GB300: 4096 x 131072 x 4096 forward 2.24 ms (1.96
 // PFLOP/s), gradient 7.3 ms on a cool device (1.81 PFLOP/s over its three products) and up to 8.0 ms under the power cap;
-// 4096 x 32768 x 1024 154 and 491 us; 64 x 131072 x 4096 gradient 608 us, where reading W twice and writing dW takes 475.
+// 4096 x 32768 x 1024 154 and 491 us; 64 x 131072 x 4096 gradient 567 us, where reading W twice and writing dW takes 475.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -199,8 +199,17 @@ double shallow_cost(const PairProduct& dw) { return std::max<double>(dw.k_iters,
 // even share of the launch. Measured on GB300, whole gradient of the cross entropy, by parts (in parentheses a whole tile in
 // shares): 64 x 131072 x 4096 876 us in one, 638, 608, 582 in two to four (2.1); 700 x 50000 x 776 317 in one, 206, 166, 171
 // in two to four (3.2); 200 x 131072 x 1024 391, 254, 210, 190, 195 in two, four, six, eight, twelve (8.4); 128 x 8192 x
-// 8192, which stays whole, 99 and 105 in two (1.06).
+// 8192, which stays whole, 99 and 105 in two (1.06). Without dW nothing else fills a last round of parts, so their rounds
+// count: 64 x 131072 x 4096 439 us in five and 348 in nine, 700 x 50000 x 776 145 in seven and 116 in six.
 int gradient_slices_even(const PairProduct& dx, const PairProduct& dw, int wave) {
+  if (dw.num_tiles == 0) {
+    auto rounds = [&](int s) { return ceil_div(dx.num_tiles * s, wave) * (ceil_div(dx.k_iters, s) + 3); };
+    int best = 1;
+    if (dx.num_tiles < wave)
+      for (int s = 2; s <= 16 && dx.k_iters / s >= 6; ++s)
+        if (rounds(s) + 2 * s < rounds(best) + 2 * best) best = s;
+    return best;
+  }
   const double share = (1.0 * dx.num_tiles * dx.k_iters + dw.num_tiles * shallow_cost(dw)) / wave;
   const int slices = static_cast<int>(dx.k_iters / std::max(share, 6.0) + 0.92);
   return std::max(1, std::min(slices, 16));
@@ -325,6 +334,11 @@ int pair_schedule(PairParams* p, bool wide, double bytes, int wave, int device, 
   const int tile_rows = wide ? 2 * L::TILE_M : L::TILE_M;
   order_product(&a, clusters, tile_rows, bytes, info->l2_bytes);
   if (b.num_tiles > 0) order_product(&b, clusters, tile_rows, bytes, info->l2_bytes);
+  // dW of a large vocabulary: whole rows of it next to one another in time, which memory takes better, as soon as X's rows,
+  // that its tiles share, stay in L2 anyway. Measured on GB300, whole gradient of the cross entropy, with the order for
+  // operands from memory and with this: 64 x 131072 x 4096 590 and 567 us, 1000 x 64000 x 2048 505 and 447, 700 x 50000 x
+  // 776 169 and 157; from 2000 rows on the same.
+  if (even && b.num_tiles > 0) b.group_m = 4;
   return clusters;
 }
 
