@@ -5,8 +5,10 @@
 // rows of W are the MMA's M and the rows of X its N: accumulator lane v holds the logits of token v, columns are the rows
 // of X. A CTA takes a run of the vocabulary in boxes of 32 tokens, so all CTAs stream the same bytes whatever the
 // vocabulary; its tiles are of up to four boxes and about the same size (a last one of what is left, which has less on its
-// way at a time, cost 30 x 100000 x 2048 72 us instead of 69). The depth is summed in parts of 512 (pair_tile.cuh says why),
-// which the epilogue adds in FP32.
+// way at a time, cost 30 x 100000 x 2048 72 us instead of 69). The depth is summed in parts of 128 (pair_tile.cuh says why),
+// which the epilogue adds in FP32: a loss of a few rows has no others to average its error with, and here short parts cost
+// nothing. 4 x 9713 x 1008, mean over 24 inputs against 64 bits: lse 7.5e-8 and loss 1.3e-7 of their size, with parts of 512
+// 3.0e-7 and 5.5e-7 (FP32 products 3.4e-8 and 1.6e-7); parts of 64 would be 5.1e-8 and 1.1e-7 at 1.4 times the time.
 // The softmax is one pass: a thread keeps, for its lane's tokens and each of its rows of X, the maximum and the sum of the
 // others relative to it through all of the CTA's tiles; lanes, warps and (in the joining kernel) CTAs are joined at the
 // end, in a fixed order.
@@ -42,7 +44,7 @@ template <int X_ROWS>
 struct LossRowsLayout {
   static constexpr int BOX = 32, TILE_BOXES = 4;
   static constexpr int ATOMS = 2, KSTEPS = 8, STAGE_K = 128;  // 128-byte swizzle rows of K per stage; MMAs; elements
-  static constexpr int SUM_STAGES = 4;                        // stages of an accumulator
+  static constexpr int SUM_STAGES = 1;                        // stages of an accumulator
   static constexpr int BOX_BYTES = BOX * 128;
   static constexpr int W_ATOM_BYTES = TILE_BOXES * BOX_BYTES, X_ATOM_BYTES = X_ROWS * 128;
   static constexpr int W_BYTES = ATOMS * W_ATOM_BYTES, X_BYTES = ATOMS * X_ATOM_BYTES;
