@@ -11,14 +11,14 @@
 //
 // Gradient: for a piece of the vocabulary at a time the logits are computed again, their epilogue turns them into G
 // (BF16, the operand of two products) and pair_gradient.cu's launch takes G to the piece's rows of dW and to dX, whose
-// pieces are added in FP32. (Up to 64 rows the logits come from cross_entropy_rows.cu here too: gradient of 64 x 131072 x
-// 4096 605 and 592 us, of 30 x 100000 x 2048 286 and 244.) A piece is as large as G's workspace may be; fewer pieces are
+// pieces are added in FP32. (Up to 64 rows G comes from cross_entropy_rows.cu: gradient of 64 x 131072 x 4096 605 us with
+// the pair tile and 592 so, of 30 x 100000 x 2048 286 and 244.) A piece is as large as G's workspace may be; fewer pieces are
 // fewer joins and ramps. Not keeping z costs its product a second time: 8 MVK operations where 6 would do with M x V logits
 // in memory.
 //
 // Bound by the tensor cores, for few rows by W's bytes. Measured on GB300: 4096 x 131072 x 4096 forward 2.24 ms (1.96
 // PFLOP/s), gradient 7.3 ms on a cool device (1.81 PFLOP/s over its three products) and up to 8.0 ms under the power cap;
-// 4096 x 32768 x 1024 154 and 491 us; 64 x 131072 x 4096 gradient 567 us, where reading W twice and writing dW takes 475.
+// 4096 x 32768 x 1024 154 and 491 us; 64 x 131072 x 4096 gradient 579 us, where reading W twice and writing dW takes 475.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -509,8 +509,9 @@ int gemm_cross_entropy_piece(int M, int vocab, size_t workspace) {
   if (M < 0 || vocab < 0) return -GEMM_ERR_INVALID_ARG;
   if (M == 0 || vocab == 0) return vocab;
   if (workspace == 0) workspace = kLossWorkspace;
-  const long long most = std::max<long long>(256, static_cast<long long>(std::min<size_t>(workspace, size_t(1) << 50) /
-                                                                         (2 * static_cast<size_t>(M))) / 256 * 256);
+  const size_t column = (M <= kLossRows ? 4 : 2) * static_cast<size_t>(M);  // bytes (few rows: G as two numbers)
+  const long long most = std::max<long long>(
+      256, static_cast<long long>(std::min<size_t>(workspace, size_t(1) << 50) / column) / 256 * 256);
   if (most >= vocab) return vocab;
   const long long pieces = (vocab + most - 1) / most;  // of about the same size
   return static_cast<int>(round_up((vocab + pieces - 1) / pieces, 256));
@@ -628,16 +629,18 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
   const int wave = loss_max_clusters(device, kGrad);
   if (wave <= 0) return GEMM_ERR_LAUNCH;
 
+  const bool few = M <= kLossRows;
+  const int g_rows = few ? 2 * M : M;  // (see cross_entropy_rows.cu)
   PairGradient q = {};
   q.x = X;
   q.ldg = ldg;
   q.ldx = ld.x;
   q.lddx = ld.dx;
-  q.rows = M;
+  q.rows = g_rows;
   q.K = K;
   q.parts = 1;
   q.even = true;
-  q.keep_sums = pieces && dX != nullptr;
+  q.keep_sums = (pieces || few) && dX != nullptr;
   auto at = [&](const void* p, int row) {
     return static_cast<void*>(const_cast<uint16_t*>(static_cast<const uint16_t*>(p)) + static_cast<long long>(row) * K);
   };
@@ -652,8 +655,9 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
   PairGradientPlan plan;
   int st = pair_gradient_plan(q, device, &plan);
   if (st != GEMM_OK) return st;
-  const size_t g_bytes = round_up(size_t(M) * ldg * 2, 256);
-  const size_t copy = copy_pays(X, ld.x, M, vocab, K) ? round_up(size_t(M) * copy_stride(K) * 2, 256) : 0;
+  const size_t g_bytes = round_up(size_t(g_rows) * ldg * 2, 256);
+  const bool copied = few ? dW != nullptr : copy_pays(X, ld.x, M, vocab, K);
+  const size_t copy = copied ? round_up(size_t(g_rows) * copy_stride(K) * 2, 256) : 0;
   cudaMemPool_t pool = workspace_pool(device);
   void* ws = nullptr;
   if (pool == nullptr || cudaMallocFromPoolAsync(&ws, g_bytes + copy + plan.sums * 4, pool, s) != cudaSuccess) {
@@ -662,9 +666,13 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
   }
   if (copy > 0) {
     void* const to = static_cast<uint8_t*>(ws) + g_bytes;
-    st = copy_rows(X, ld.x, to, M, K, s);
-    q.x = X = to;
-    q.ldx = ld.x = copy_stride(K);
+    if (!few) {
+      st = copy_rows(X, ld.x, to, M, K, s);
+      X = to;
+      ld.x = copy_stride(K);
+    }
+    q.x = to;
+    q.ldx = copy_stride(K);
   }
   float* const sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + g_bytes + copy);
   q.g[0] = ws;
@@ -677,9 +685,10 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
     p.first_col = first;
     p.grad = LossGradient{targets, lse, dloss, dlse, M, vocab, first, scale};
     const bool wide = grad_wide(M, q.features[0], K, wave);
-    if (M <= kLossRows) {
+    if (few) {
+      uint16_t* const twice = copied ? static_cast<uint16_t*>(const_cast<void*>(q.x)) : nullptr;
       st = run_loss_rows_gradient(LossRowsOperands{X, q.w[0], nullptr, nullptr, nullptr, ld.x, M, q.features[0], K, scale},
-                                  p.grad, ws, ldg, device, info, s);
+                                  LossRowsGradient{p.grad, static_cast<uint16_t*>(ws), ldg, twice, q.ldx}, device, info, s);
     } else {
       st = pair_plan_product(&p.main, M, q.features[0], K, wide ? 64 : 128, 1, 1, wide ? 2 * L::TILE_M : L::TILE_M,
                              L::BLOCK_N);
@@ -690,7 +699,7 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
     if (st == GEMM_OK && first > 0) st = pair_gradient_plan(q, device, &plan);
     if (st == GEMM_OK) st = pair_gradient_launch(q, &plan, sums, device, info, s);
   }
-  if (st == GEMM_OK && join) st = pair_gradient_join(sums, slices, dX, ld.dx, M, K, s);
+  if (st == GEMM_OK && join) st = pair_gradient_join(sums, slices, dX, ld.dx, M, K, s, few);
   if (cudaFreeAsync(ws, s) != cudaSuccess && st == GEMM_OK) st = GEMM_ERR_LAUNCH;
   return st;
 }

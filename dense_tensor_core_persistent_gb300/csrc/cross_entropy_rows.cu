@@ -16,8 +16,13 @@
 // Measured on GB300 with W of 131072 x 4096 (1.07 GB, 158 us at the rate of a copy): 1 row 158 to 163 us, where the pair
 // tile took 290; 64 rows 160 to 166, where the pair tile's 65 rows take 193 and its 128 191.
 //
-// One persistent CTA per SM. Warp roles: 0 loads W, 2 loads X, 1 allocates TMEM and issues the MMAs, 4..11 epilogue, two
-// to each TMEM lane quadrant with half of X's rows each. Two accumulators in TMEM.
+// In the gradient G's two products have room for more rows than X has: their tiles are 256 rows, their stages 128. So G is
+// kept as two BF16 numbers, the second what the first one's rounding left, as rows of their own, and X's rows twice for the
+// product with both; the error of dX and dW against 64 bits is that of their own rounding (4 x 9713 x 1008 1.66e-3, with one
+// number 2.3e-3 in the mean and 3.0e-3 at the most). It costs 64 x 131072 x 4096 569 -> 579 us, 64 x 16000 x 1024 29 -> 32.
+//
+// One persistent CTA per SM. Warp roles: 0 loads W, 2 loads X, 1 allocates TMEM and issues the MMAs, 3 copies X for the
+// gradient, 4..11 epilogue, two to each TMEM lane quadrant with half of X's rows each. Two accumulators in TMEM.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -31,9 +36,7 @@ namespace {
 
 struct LossRowsParams {
   LossRowsOperands x;
-  LossGradient grad;
-  uint16_t* g;  // gradient
-  long long ldg;
+  LossRowsGradient grad;
   int k_iters, boxes;  // stages of a tile; boxes of 32 tokens in all
   int n;               // the MMA's N: the rows of X, rounded up to a multiple of 16
   unsigned* status;
@@ -50,7 +53,7 @@ struct LossRowsLayout {
   static constexpr int W_BYTES = ATOMS * W_ATOM_BYTES, X_BYTES = ATOMS * X_ATOM_BYTES;
   static constexpr int STAGES = X_ROWS == 16 ? 6 : 4;
   static constexpr int TMEM_COLS = 2 * X_ROWS;
-  static constexpr int WARP_W = 0, WARP_MMA = 1, WARP_X = 2, EPI_WARP0 = 4, EPI_WARPS = 8;
+  static constexpr int WARP_W = 0, WARP_MMA = 1, WARP_X = 2, WARP_COPY = 3, EPI_WARP0 = 4, EPI_WARPS = 8;
   static constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
   static constexpr int COLS = X_ROWS / 2;  // rows of X of an epilogue warp
   static constexpr int OFF_W = 0;
@@ -223,6 +226,18 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
       settle_after_abort();
     }
   }
+  if constexpr (GRAD) {
+    if (warp == L::WARP_COPY && p.grad.x_twice != nullptr) {  // X's rows twice, 8 columns at a time
+      const long long vectors = p.x.depth / 8, all = p.x.rows * vectors;
+      for (long long i = blockIdx.x * 32u + lane; i < all; i += gridDim.x * 32u) {
+        const long long row = i / vectors, col = (i - row * vectors) * 8;
+        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x.x) + row * p.x.ldx + col);
+        uint16_t* const to = p.grad.x_twice + row * p.grad.ldx_twice + col;
+        *reinterpret_cast<uint4*>(to) = v;
+        *reinterpret_cast<uint4*>(to + p.x.rows * p.grad.ldx_twice) = v;
+      }
+    }
+  }
   float2* const joined = reinterpret_cast<float2*>(smem + L::OFF_JOIN);
   const float c = log2_scale(p.x.scale);
   if (warp >= L::EPI_WARP0) {
@@ -236,7 +251,7 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
     float4* const factors = reinterpret_cast<float4*>(of_rows);
     uint32_t dead = 0;
     if constexpr (GRAD) {
-      const GradientRow g(p.grad, col0 + static_cast<int>(lane));
+      const GradientRow g(p.grad.row, col0 + static_cast<int>(lane));
       if (lane < L::COLS) {
         const int token = g.target >= 0 && g.target < p.x.vocab ? static_cast<int>(g.target) : -1;
         factors[lane] = make_float4(g.lse, g.softmax, g.onehot, __int_as_float(token));
@@ -277,14 +292,18 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
       }
       if (!ok || !live || !in) continue;
       if constexpr (GRAD) {
-        uint16_t* const to = p.g + col0 * p.ldg + token;
+        uint16_t* const to = p.grad.g + col0 * p.grad.ldg + token;
+        const long long half = p.x.rows * p.grad.ldg;
 #pragma unroll
         for (int j = 0; j < L::COLS; ++j) {
           if (col0 + j >= p.x.rows) break;
           const float4 f = factors[j];
           float v = gradient_of(z[j], p.x.scale, f.x, f.y, (dead >> j & 1u) != 0u);
           if (__float_as_int(f.w) == token) v -= f.z;
-          to[j * p.ldg] = static_cast<uint16_t>(pack_bf16x2_rn(__float_as_uint(v), 0u) & 0xFFFFu);
+          const uint32_t high = pack_bf16x2_rn(__float_as_uint(v), 0u) & 0xFFFFu;
+          const float left = v - __uint_as_float(high << 16);  // (of an infinity NaN, as of a NaN)
+          to[j * p.grad.ldg] = static_cast<uint16_t>(high);
+          to[j * p.grad.ldg + half] = static_cast<uint16_t>(pack_bf16x2_rn(__float_as_uint(left), 0u) & 0xFFFFu);
         }
         continue;
       }
@@ -321,7 +340,8 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
 }
 
 template <int X_ROWS, bool GRAD>
-int launch_rows(const LossRowsOperands& x, const LossGradient& grad, void* g, long long ldg, int device, const DeviceInfo* info, cudaStream_t stream) {
+int launch_rows(const LossRowsOperands& x, const LossRowsGradient& grad, int device, const DeviceInfo* info,
+                cudaStream_t stream) {
   using L = LossRowsLayout<X_ROWS>;
   const auto kernel = loss_rows_kernel<X_ROWS, GRAD>;
   {
@@ -339,8 +359,6 @@ int launch_rows(const LossRowsOperands& x, const LossGradient& grad, void* g, lo
   LossRowsParams p;
   p.x = x;
   p.grad = grad;
-  p.g = static_cast<uint16_t*>(g);
-  p.ldg = ldg;
   p.n = ceil_div(x.rows, 16) * 16;
   p.k_iters = ceil_div(x.depth, L::STAGE_K);
   p.boxes = ceil_div(x.vocab, L::BOX);
@@ -377,14 +395,14 @@ int launch_rows(const LossRowsOperands& x, const LossGradient& grad, void* g, lo
 int loss_rows_ctas(int vocab, const DeviceInfo* info) { return std::min(ceil_div(vocab, 32), info->num_sms); }
 
 int run_loss_rows(const LossRowsOperands& p, int device, const DeviceInfo* info, cudaStream_t stream) {
-  return p.rows <= 16 ? launch_rows<16, false>(p, LossGradient{}, nullptr, 0, device, info, stream)
-                      : launch_rows<64, false>(p, LossGradient{}, nullptr, 0, device, info, stream);
+  return p.rows <= 16 ? launch_rows<16, false>(p, LossRowsGradient{}, device, info, stream)
+                      : launch_rows<64, false>(p, LossRowsGradient{}, device, info, stream);
 }
 
-int run_loss_rows_gradient(const LossRowsOperands& p, const LossGradient& grad, void* g, long long ldg, int device,
-                           const DeviceInfo* info, cudaStream_t stream) {
-  return p.rows <= 16 ? launch_rows<16, true>(p, grad, g, ldg, device, info, stream)
-                      : launch_rows<64, true>(p, grad, g, ldg, device, info, stream);
+int run_loss_rows_gradient(const LossRowsOperands& p, const LossRowsGradient& grad, int device, const DeviceInfo* info,
+                           cudaStream_t stream) {
+  return p.rows <= 16 ? launch_rows<16, true>(p, grad, device, info, stream)
+                      : launch_rows<64, true>(p, grad, device, info, stream);
 }
 
 }  // namespace dtcp

@@ -79,8 +79,17 @@ struct LossRowsOperands {
 // CTAs of the launch (and so parts of a row).
 int loss_rows_ctas(int vocab, const DeviceInfo* info);
 int run_loss_rows(const LossRowsOperands& p, int device, const DeviceInfo* info, cudaStream_t stream);
-// The same for the gradient: G (rows ldg apart) of the piece of `vocab` columns whose rows of W start at w.
-int run_loss_rows_gradient(const LossRowsOperands& p, const LossGradient& grad, void* g, long long ldg, int device,
-                           const DeviceInfo* info, cudaStream_t stream);
+// The same for the gradient: G of the piece of `vocab` columns whose rows of W start at w, as the sum of two BF16 numbers:
+// 2 * rows rows, ldg apart, the second half what the first one's rounding left. x_twice (or null) receives X's rows twice,
+// ldx_twice apart, for the product with both halves.
+struct LossRowsGradient {
+  LossGradient row;
+  uint16_t* g;
+  long long ldg;
+  uint16_t* x_twice;
+  long long ldx_twice;
+};
+int run_loss_rows_gradient(const LossRowsOperands& p, const LossRowsGradient& grad, int device, const DeviceInfo* info,
+                           cudaStream_t stream);
 
 }  // namespace dtcp

@@ -139,8 +139,9 @@ __global__ void __launch_bounds__(PairWideLayout::NUM_THREADS, 1)
 
 // ---------------------------------------------------------------- dX from its slices
 
-// The sum of the slices' partial sums in their order, rounded once: 8 columns per thread.
-__global__ void __launch_bounds__(128) join_kernel(const float* partial, int slices, long long slice_size,
+// The sum of the slices' partial sums in their order, rounded once: 8 columns per thread. `half`: each slice has a second
+// part of the rows that far behind the first (0: none).
+__global__ void __launch_bounds__(128) join_kernel(const float* partial, int slices, long long slice_size, long long half,
                                                        uint16_t* dx, long long lddx, int cols, long long vectors) {
   pdl_launch_dependents();
   pdl_wait();
@@ -153,6 +154,13 @@ __global__ void __launch_bounds__(128) join_kernel(const float* partial, int sli
   float sum[8] = {};
 #pragma unroll 4
   for (int s = 0; s < slices; ++s) {
+    if (half > 0) {
+      const float4 a = *reinterpret_cast<const float4*>(at + s * slice_size + half);
+      const float4 b = *reinterpret_cast<const float4*>(at + s * slice_size + half + 4);
+      const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += f[j];
+    }
     const float4 a = *reinterpret_cast<const float4*>(at + s * slice_size);
     const float4 b = *reinterpret_cast<const float4*>(at + s * slice_size + 4);
     const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -427,7 +435,8 @@ int pair_gradient_launch(const PairGradient& q, PairGradientPlan* plan, float* s
                      args, plan->wide, clusters, stream);
 }
 
-int pair_gradient_join(const float* sums, int slices, void* dx, long long lddx, int rows, int K, cudaStream_t stream) {
+int pair_gradient_join(const float* sums, int slices, void* dx, long long lddx, int rows, int K, cudaStream_t stream,
+                       bool halves) {
   const long long vectors = static_cast<long long>(rows) * (K / 8);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -438,8 +447,9 @@ int pair_gradient_join(const float* sums, int slices, void* dx, long long lddx, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const long long slice_size = static_cast<long long>(ceil_div(rows, 32)) * 32 * K;
-  if (cudaLaunchKernelEx(&cfg, join_kernel, sums, slices, slice_size, static_cast<uint16_t*>(dx), lddx, K, vectors) !=
+  const long long slice_size = static_cast<long long>(ceil_div(halves ? 2 * rows : rows, 32)) * 32 * K;
+  const long long half = halves ? static_cast<long long>(rows) * K : 0;
+  if (cudaLaunchKernelEx(&cfg, join_kernel, sums, slices, slice_size, half, static_cast<uint16_t*>(dx), lddx, K, vectors) !=
       cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;

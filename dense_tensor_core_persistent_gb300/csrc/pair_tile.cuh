@@ -763,7 +763,9 @@ bool pair_gradient_is_wide(const PairGradient& q, int wave);
 int pair_gradient_plan(const PairGradient& q, int device, PairGradientPlan* plan);
 int pair_gradient_launch(const PairGradient& q, PairGradientPlan* plan, float* sums, int device, const DeviceInfo* info,
                          cudaStream_t stream);
-// dX = bf16_rne(the slices' partial sums, added in their order).
-int pair_gradient_join(const float* sums, int slices, void* dx, long long lddx, int rows, int K, cudaStream_t stream);
+// dX = bf16_rne(the slices' partial sums, added in their order). halves: the launch had 2 * rows rows, of which r and
+// r + rows belong together.
+int pair_gradient_join(const float* sums, int slices, void* dx, long long lddx, int rows, int K, cudaStream_t stream,
+                       bool halves = false);
 
 }  // namespace dtcp

@@ -688,12 +688,14 @@ int gemm_cross_entropy(const void* X, const void* W, const long long* targets, f
  *   read into the row); a target >= vocab makes the row of G NaN. A row that no gradient reaches (dloss and dlse 0 or
  *   absent) has a G of 0 whatever its logits are; its X still takes part in dW as 0 * X and has to be finite.
  *   dX: M x K, dW: vocab x K, BF16; either may be NULL (not computed). Neither may overlap another operand.
+ *   Up to 64 rows G is kept as the sum of two BF16 numbers, so its rounding is not seen in dX and dW.
  *   workspace: bytes that the piece of G may take, 0 = 512 MiB; gemm_cross_entropy_piece gives the columns of a piece.
  * Constraints as gemm_cross_entropy; dX and dW 16-byte aligned. M == 0 sets dW to zero.
- * Two kernel launches a piece. Where dX needs FP32 sums (several pieces, or few tiles and so slices of its sum) one more
- * launch, and 4 K bytes more of workspace for each row (M rounded up to a multiple of 32) and slice, of which there are up
- * to 16. Where rows of X do not start on 128-byte boundaries and the products are large, one more copies X to rows that do
- * (2 K bytes a row of workspace; the forward call does so too). The workspace comes from the library's stream-ordered pool.
+ * Two kernel launches a piece. Where dX needs FP32 sums (several pieces, few tiles and so slices of its sum, or up to 64
+ * rows) one more launch, and 4 K bytes more of workspace for each row (M rounded up to a multiple of 32; twice M up to 64
+ * rows) and slice, of which there are up to 16. Where rows of X do not start on 128-byte boundaries and the products are
+ * large, one more copies X to rows that do (2 K bytes a row of workspace; the forward call does so too); up to 64 rows X is
+ * copied twice by a launch that is there anyway. The workspace comes from the library's stream-ordered pool.
  * The same inputs give the same bits.
  */
 int gemm_cross_entropy_backward(const void* X, const void* W, const long long* targets, const float* lse,

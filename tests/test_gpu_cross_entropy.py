@@ -280,3 +280,26 @@ def test_captured_and_replayed_beside_another_stream():
     for _, out in graphs:
         assert all(torch.equal(u, v) for u, v in zip(out, want_a))
     assert all(torch.equal(u, v) for u, v in zip(got_b, want_b))
+
+
+@pytest.mark.parametrize("M,V,K", [(1, 300, 64), (3, 5000, 520), (16, 1000, 264), (17, 2049, 72), (64, 4100, 1032)])
+@pytest.mark.parametrize("workspace", [0, 1])
+def test_few_rows_do_not_see_the_rounding_of_g(M, V, K, workspace):
+    """Up to 64 rows G is the sum of two BF16 numbers: off by 2^-16 of itself instead of 2^-8."""
+    x, head, targets, dloss, dlse = problem(M, V, K, M + K)
+    wide = torch.zeros(M, K + 24, dtype=BF16, device=DEV)
+    wide[:, 8:K + 8] = x
+    x = wide[:, 8:K + 8]
+    r = g.cross_entropy(x, head, targets)
+    dx, dw = g.cross_entropy_backward(x, head, targets, r.lse, dloss, dlse=dlse, workspace=workspace)
+    d = Definition(x, head, targets, 1.0)
+    dl = dloss.double() * d.given
+    a = (dl + dlse.double())[:, None] * (d.z - d.lse[:, None]).exp()
+    G = a - dl[:, None] * d.onehot
+    e = (d.E + d.lse.abs() * 2.0 ** -23 + 2.0 ** -19)[:, None]
+    dG = e * a.abs() + 2.0 ** -16 * (G.abs() + e * a.abs())
+    pieces = -(-V // g.cross_entropy_piece(M, V, workspace))
+    for got, A, dA, B in ((dx, G, dG, d.w), (dw, G.T, dG.T, d.x)):
+        want, size = A @ B, A.abs() @ B.abs()
+        tol = dA @ B.abs() + (2 * A.shape[1] / 16 + 10 + 32 * pieces) * 2.0 ** -22 * size
+        assert torch.all((got.double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol) + 1e-37)
