@@ -9,16 +9,17 @@
 // second kernel joins a row's parts in a fixed order. The maximum's own term is exactly 1 and is kept out of the sums,
 // so lse and loss end in log1p and a row that its target dominates keeps its digits.
 //
-// Gradient: for a piece of the vocabulary at a time the logits are computed again, their epilogue turns them into G
-// (BF16, the operand of two products) and pair_gradient.cu's launch takes G to the piece's rows of dW and to dX, whose
-// pieces are added in FP32. (Up to 64 rows G comes from cross_entropy_rows.cu: gradient of 64 x 131072 x 4096 605 us with
-// the pair tile and 592 so, of 30 x 100000 x 2048 286 and 244.) A piece is as large as G's workspace may be; fewer pieces are
+// Gradient: for a piece of the vocabulary at a time the logits are computed again, in the same parts of their depth as the
+// forward pass, their epilogue turns them into G (BF16, the operand of two products) and pair_gradient.cu's launch takes G to the piece's rows of dW and to dX, whose
+// pieces are added in FP32. (Up to 64 rows G comes from cross_entropy_rows.cu: 30 x 100000 x 2048 286 us with the pair
+// tile, 242 so.) A piece is as large as G's workspace may be; fewer pieces are
 // fewer joins and ramps. Not keeping z costs its product a second time: 8 MVK operations where 6 would do with M x V logits
 // in memory.
 //
 // Bound by the tensor cores, for few rows by W's bytes. Measured on GB300: 4096 x 131072 x 4096 forward 2.24 ms (1.96
-// PFLOP/s), gradient 7.3 ms on a cool device (1.81 PFLOP/s over its three products) and up to 8.0 ms under the power cap;
-// 4096 x 32768 x 1024 154 and 491 us; 64 x 131072 x 4096 gradient 579 us, where reading W twice and writing dW takes 475.
+// PFLOP/s), gradient 7.5 ms on a cool device (1.76 PFLOP/s over its three products) and up to 8.0 ms under the power cap
+// (with one accumulator for the logits' depth 7.4);
+// 4096 x 32768 x 1024 154 and 500 us; 64 x 131072 x 4096 gradient 579 us, where reading W twice and writing dW takes 475.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -150,168 +151,116 @@ struct GradRow {
   }
 };
 
-// Forward: a row's 128 columns of a tile (64 of a half) are added over the parts of the depth, then reduced.
+// An epilogue warp's 128 columns of a tile (64 of a half), added over the parts of the depth; false if a wait ran out. An
+// accumulator goes back to the MMAs as soon as it is read.
+__device__ __forceinline__ bool add_parts(const PairCta& c, int parts, int width, bool live, uint32_t& acc,
+                                          float (&sum)[4][32]) {
+  using L = PairLayout;
+  const uint32_t bar_tfull = c.base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 16;
+  const uint32_t q = c.warp & 3u, h = (c.warp - L::EPI_WARP0) >> 2;
+  const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
+#pragma unroll 1
+  for (int part = 0; part < parts; ++part, ++acc) {
+    const uint32_t slot = acc & 1u;
+    if (!__all_sync(0xffffffffu, wait_phase_inline(bar_tfull + 8 * slot, (acc >> 1) & 1u, c.wctx,
+                                                   status_code(kRoleEpilogue, slot))))
+      return false;
+    tc_fence_after_sync();
+    if (live) {
+      const uint32_t taddr =
+          c.tmem_base + ((q * 32u) << 16) + slot * L::ACC_COLS + h * static_cast<uint32_t>(width);
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        if (k * 32 >= width) continue;
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(taddr + k * 32, v[0]);
+        tmem_ld_32x32b_x32(taddr + k * 32 + 32, v[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            sum[k + t][j] = part == 0 ? __uint_as_float(v[t][j]) : sum[k + t][j] + __uint_as_float(v[t][j]);
+      }
+    }
+    tc_fence_before_sync();
+    __syncwarp();
+    if (c.lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * slot);  // orders tcgen05 work only
+  }
+  return true;
+}
+
+// The rows and columns of an epilogue warp in a tile.
+struct LossPlace {
+  int width, col0, row0, row;
+  bool live;
+  __device__ __forceinline__ LossPlace(const LossParams& p, const PairCta& c, const PairItem& item) {
+    using L = PairLayout;
+    const int q = static_cast<int>(c.warp & 3u);  // this warp may access TMEM lanes 32q .. 32q+31
+    const int h = static_cast<int>((c.warp - L::EPI_WARP0) >> 2);  // its half of the columns
+    width = item.half >= 0 ? L::BLOCK_N / 4 : L::BLOCK_N / 2;
+    col0 = item.n_blk * L::BLOCK_N + (item.half > 0 ? 2 * width : 0) + h * width;
+    row0 = item.m_blk * L::TILE_M + static_cast<int>(c.rank) * L::CTA_M + q * 32;
+    row = row0 + static_cast<int>(c.lane);
+    live = row0 < p.main.rows && col0 < p.main.cols;
+  }
+};
+
+__device__ __forceinline__ int sum_parts(const LossParams& p) {
+  return (p.main.k_iters + kPairSumStages - 1) / kPairSumStages;
+}
+
+// Forward: a row's columns of a tile are reduced.
 __global__ void __launch_bounds__(PairLayout::NUM_THREADS, 1)
     loss_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ LossParams p) {
-  using L = PairLayout;
-  pair_cta<kPairRowsSums>(maps, p, [&](const PairCta& c) {
-    const uint32_t bar_tfull = c.base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 16;
-    const uint32_t q = c.warp & 3u;  // this warp may access TMEM lanes 32q .. 32q+31
-    const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
-    const int h = static_cast<int>((c.warp - L::EPI_WARP0) >> 2);  // its half of the columns
-    const int rows = p.main.rows, cols = p.main.cols;
-    const int parts = (p.main.k_iters + kPairSumStages - 1) / kPairSumStages;
+  pair_cta<kPairRows>(maps, p, [&](const PairCta& c) {
+    const int h = static_cast<int>((c.warp - PairLayout::EPI_WARP0) >> 2), parts = sum_parts(p);
     uint32_t acc = 0;
-    bool ok = true;
     PairItem item;
-    for (int it = 0; ok && pair_item(p, c.cluster_idx, c.num_clusters, it, item); ++it) {
-      const int width = item.half >= 0 ? L::BLOCK_N / 4 : L::BLOCK_N / 2;  // columns of this warp
-      const int col0 = item.n_blk * L::BLOCK_N + (item.half > 0 ? 2 * width : 0) + h * width;
-      const int row0 = item.m_blk * L::TILE_M + static_cast<int>(c.rank) * L::CTA_M + static_cast<int>(q) * 32;
-      const int row = row0 + static_cast<int>(c.lane);
-      const bool live = row0 < rows && col0 < cols;
+    for (int it = 0; pair_item(p, c.cluster_idx, c.num_clusters, it, item); ++it) {
+      const LossPlace at(p, c, item);
       LossRow r;
-      r.begin(p, row);  // (while the MMAs run)
+      r.begin(p, at.row);  // (while the MMAs run)
       float sum[4][32];
-#pragma unroll 1
-      for (int part = 0; part < parts; ++part, ++acc) {
-        const uint32_t slot = acc & 1u;
-        if (!__all_sync(0xffffffffu, wait_phase_inline(bar_tfull + 8 * slot, (acc >> 1) & 1u, c.wctx,
-                                                       status_code(kRoleEpilogue, slot)))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        if (live) {
-          const uint32_t taddr =
-              c.tmem_base + ((q * 32u) << 16) + slot * L::ACC_COLS + static_cast<uint32_t>(h * width);
-#pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            if (k * 32 >= width) continue;
-            uint32_t v[2][32];
-            tmem_ld_32x32b_x32(taddr + k * 32, v[0]);
-            tmem_ld_32x32b_x32(taddr + k * 32 + 32, v[1]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                sum[k + t][j] = part == 0 ? __uint_as_float(v[t][j]) : sum[k + t][j] + __uint_as_float(v[t][j]);
-          }
-        }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (c.lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * slot);  // orders tcgen05 work only
-      }
-      if (!ok || row0 >= rows) continue;
+      if (!add_parts(c, parts, at.width, at.live, acc, sum)) break;
+      if (at.row0 >= p.main.rows) continue;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int col = col0 + k * 32;
-        if (k * 32 < width && col < cols) r.chunk(p, sum[k], row, col);
+        const int col = at.col0 + k * 32;
+        if (k * 32 < at.width && col < p.main.cols) r.chunk(p, sum[k], at.row, col);
       }
-      r.end(p, item, h, row);
+      r.end(p, item, h, at.row);
     }
   });
 }
 
-// Gradient: a tile's logits become G.
+// Gradient: a tile's logits become G. They are added in the parts of the forward pass: p = exp(z - lse) takes the difference of
+// two numbers of the same size, and a row that its target dominates p - 1 behind it, so a z from one accumulator against an lse
+// from parts would be most of such a row's G (the size of its logit times 2^-25 a step of 16).
 __global__ void __launch_bounds__(PairLayout::NUM_THREADS, 1)
     grad_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ LossParams p) {
   using L = PairLayout;
   pair_cta<kPairRows>(maps, p, [&](const PairCta& c) {
-    const uint32_t bar_tfull = c.base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 16;
-    const uint32_t q = c.warp & 3u;  // this warp may access TMEM lanes 32q .. 32q+31
-    const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
-    const uint32_t epi = c.warp - L::EPI_WARP0;
-    const int h = static_cast<int>(epi >> 2);  // its half of the columns
-    const int rows = p.main.rows, cols = p.main.cols;
-    PairStaging st{c.base + L::OFF_EPI + epi * kPairStagingBytes, 0u, false};
+    const int parts = sum_parts(p);
+    PairStaging st{c.base + L::OFF_EPI + (c.warp - L::EPI_WARP0) * kPairStagingBytes, 0u, false};
+    uint32_t acc = 0;
     PairItem item;
     for (int it = 0; pair_item(p, c.cluster_idx, c.num_clusters, it, item); ++it) {
-      const int width = item.half >= 0 ? L::BLOCK_N / 4 : L::BLOCK_N / 2;  // columns of this warp
-      const int col0 = item.n_blk * L::BLOCK_N + (item.half > 0 ? 2 * width : 0) + h * width;
-      const uint32_t slot = static_cast<uint32_t>(it) & 1u;
-      const int row0 = item.m_blk * L::TILE_M + static_cast<int>(c.rank) * L::CTA_M + static_cast<int>(q) * 32;
-      const int row = row0 + static_cast<int>(c.lane);
+      const LossPlace at(p, c, item);
       GradRow r;
-      r.begin(p, row);  // (while the MMAs run)
-      if (!wait_phase_warp(bar_tfull + 8 * slot, (static_cast<uint32_t>(it) >> 1) & 1u, c.wctx,
-                           status_code(kRoleEpilogue, slot)))
-        break;
-      tc_fence_after_sync();
-      const uint32_t taddr = c.tmem_base + ((q * 32u) << 16) + slot * L::ACC_COLS + static_cast<uint32_t>(h * width);
-      if (row0 < rows) {
-#pragma unroll 1
-        for (int k = 0; k < width; k += 32) {
-          const int col = col0 + k;
-          if (col >= cols) break;
+      r.begin(p, at.row);  // (while the MMAs run)
+      float sum[4][32];
+      if (!add_parts(c, parts, at.width, at.live, acc, sum)) break;
+      if (at.row0 >= p.main.rows) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int col = at.col0 + k * 32;
+        if (k * 32 < at.width && col < p.main.cols) {
           uint32_t v[32];
-          tmem_ld_32x32b_x32(taddr + k, v);
-          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(sum[k][j]);
           r.chunk(v, col);
-          pair_store(st, c.lane, &maps.c0, v, col, row0, false);
-        }
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (c.lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * slot);  // orders tcgen05 work only
-    }
-    if (c.lane == 0) bulk_wait_group<0>();
-    __syncwarp();
-  });
-}
-
-__global__ void __launch_bounds__(PairWideLayout::NUM_THREADS, 1)
-    grad_wide_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ LossParams p) {
-  using L = PairWideLayout;
-  pair_wide_cta<kPairRows>(maps, p, [&](const PairCta& c) {
-    const uint32_t bar_tfull = c.base + L::OFF_BAR + 16 * L::STAGES, bar_tempty = bar_tfull + 8 * L::WAVES;
-    const uint32_t q = c.warp & 3u;  // this warp may access TMEM lanes 32q .. 32q+31
-    const uint32_t epi = c.warp - L::EPI_WARP0;
-    const int h = static_cast<int>(epi >> 2);  // its half of a wave's columns
-    const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
-    const int rows = p.main.rows, cols = p.main.cols;
-    PairStaging st{c.base + L::OFF_EPI + epi * L::EPI_BYTES, 0u, false};
-    bool ok = true;
-    PairItem item;
-    for (int it = 0; ok && pair_item(p, c.cluster_idx, c.num_clusters, it, item); ++it) {
-      const int width = item.half >= 0 ? L::BLOCK_N / 4 : L::BLOCK_N / 2;  // columns of this warp
-      const int col0 = item.n_blk * L::BLOCK_N + (item.half > 0 ? 2 * width : 0) + h * width;
-#pragma unroll 1
-      for (int w = 0; w < L::WAVES; ++w) {
-        const int row0 =
-            item.m_blk * L::TILE_M + static_cast<int>(c.rank) * L::CTA_M + w * 128 + static_cast<int>(q) * 32;
-        const int row = row0 + static_cast<int>(c.lane);
-        const bool live = row0 < rows && col0 < cols;
-        GradRow r;
-        r.begin(p, row);  // (while the MMAs run)
-        if (!__all_sync(0xffffffffu, wait_phase_inline(bar_tfull + 8 * w, static_cast<uint32_t>(it) & 1u, c.wctx,
-                                                       status_code(kRoleEpilogue, w)))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t taddr = c.tmem_base + ((q * 32u) << 16) + static_cast<uint32_t>(w) * L::ACC_COLS +
-                               static_cast<uint32_t>(h * width);
-        uint32_t v[4][32];
-        if (live) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k * 32 < width) tmem_ld_32x32b_x32(taddr + k * 32, v[k]);
-          tmem_ld_wait();
-        }
-        // the wave's columns are read: hand them back to the MMA issuer (leader's barrier)
-        tc_fence_before_sync();
-        __syncwarp();
-        if (c.lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * w);  // orders tcgen05 work only
-        if (row0 >= rows) continue;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int col = col0 + k * 32;
-          if (k * 32 < width && col < cols) {
-            r.chunk(v[k], col);
-            pair_store(st, c.lane, &maps.c0, v[k], col, row0, false);
-          }
+          pair_store(st, c.lane, &maps.c0, v, col, at.row0, false);
         }
       }
     }
@@ -388,39 +337,30 @@ __global__ void __launch_bounds__(32 * kJoinWarps) loss_join_kernel(const LossJo
 
 // ---------------------------------------------------------------- host side
 
-enum LossKernel { kLoss = 0, kGrad = 1, kGradWide = 2 };
+enum LossKernel { kLoss = 0, kGrad = 1 };
 const void* loss_kernel_of(LossKernel k) {
-  return k == kLoss   ? reinterpret_cast<const void*>(loss_kernel)
-         : k == kGrad ? reinterpret_cast<const void*>(grad_kernel)
-                      : reinterpret_cast<const void*>(grad_wide_kernel);
+  return k == kLoss ? reinterpret_cast<const void*>(loss_kernel) : reinterpret_cast<const void*>(grad_kernel);
 }
 
 int loss_max_clusters(int device, LossKernel k) {
   static std::mutex mu;
-  static int cache[64][3] = {};
+  static int cache[64][2] = {};
   std::lock_guard<std::mutex> lock(mu);
   if (device < 0 || device >= 64) return 0;
   int& n = cache[device][k];
   if (n == 0) {
     const void* kernel = loss_kernel_of(k);
-    n = pair_max_clusters(&kernel, 1, k == kGradWide);
+    n = pair_max_clusters(&kernel, 1, false);
   }
   return n;
-}
-
-bool grad_wide(int M, int N, int K, int wave) {
-  using L = PairLayout;
-  const long long n = ceil_div(N, L::BLOCK_N);
-  return pair_wide_rule(ceil_div(M, L::TILE_M) * n, ceil_div(M, 2 * L::TILE_M) * n, K, wave);
 }
 
 // X's rows against `cols` rows of W from its row p.first_col on, G (or nothing) to `out`.
 int loss_launch(LossParams& p, LossKernel k, const void* X, long long ldx, const void* W, int K, int cols, void* out,
                 long long ldo, int device, const DeviceInfo* info, cudaStream_t stream) {
   const int rows = p.main.rows;
-  const bool wide = k == kGradWide;
   PairMaps m;
-  int st = pair_map_in(&m.a0, X, K, rows, ldx, wide ? 64 : 128);
+  int st = pair_map_in(&m.a0, X, K, rows, ldx, 128);
   if (st == GEMM_OK)
     st = pair_map_in(&m.b0, static_cast<const uint16_t*>(W) + static_cast<long long>(p.first_col) * K, K, cols, K, 64);
   m.a1 = m.c0 = m.c1 = m.c2 = m.a0;
@@ -429,10 +369,10 @@ int loss_launch(LossParams& p, LossKernel k, const void* X, long long ldx, const
   if (st != GEMM_OK) return st;
   const int wave = loss_max_clusters(device, k);
   if (wave <= 0) return GEMM_ERR_LAUNCH;
-  const int clusters = pair_schedule(&p, wide, 2.0, wave, device, info);
+  const int clusters = pair_schedule(&p, false, 2.0, wave, device, info);
   if (clusters < 0) return -clusters;
   void* args[] = {&m, &p};
-  return pair_launch(loss_kernel_of(k), args, wide, clusters, stream);
+  return pair_launch(loss_kernel_of(k), args, false, clusters, stream);
 }
 
 // Rows of 8 columns at a time, `vectors` of them to a row, into rows `ldo` apart.
@@ -626,9 +566,6 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
   const int piece = gemm_cross_entropy_piece(M, vocab, workspace);
   const bool pieces = piece < vocab;
   const long long ldg = static_cast<long long>(round_up(piece, 64));  // (rows on 128-byte boundaries, see copy_rows)
-  const int wave = loss_max_clusters(device, kGrad);
-  if (wave <= 0) return GEMM_ERR_LAUNCH;
-
   const bool few = M <= kLossRows;
   const int g_rows = few ? 2 * M : M;  // (see cross_entropy_rows.cu)
   PairGradient q = {};
@@ -684,16 +621,13 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
     p.scale = scale;
     p.first_col = first;
     p.grad = LossGradient{targets, lse, dloss, dlse, M, vocab, first, scale};
-    const bool wide = grad_wide(M, q.features[0], K, wave);
     if (few) {
       uint16_t* const twice = copied ? static_cast<uint16_t*>(const_cast<void*>(q.x)) : nullptr;
       st = run_loss_rows_gradient(LossRowsOperands{X, q.w[0], nullptr, nullptr, nullptr, ld.x, M, q.features[0], K, scale},
                                   LossRowsGradient{p.grad, static_cast<uint16_t*>(ws), ldg, twice, q.ldx}, device, info, s);
     } else {
-      st = pair_plan_product(&p.main, M, q.features[0], K, wide ? 64 : 128, 1, 1, wide ? 2 * L::TILE_M : L::TILE_M,
-                             L::BLOCK_N);
-      if (st == GEMM_OK)
-        st = loss_launch(p, wide ? kGradWide : kGrad, X, ld.x, W, K, q.features[0], ws, ldg, device, info, s);
+      st = pair_plan_product(&p.main, M, q.features[0], K, 128, 1, 1, L::TILE_M, L::BLOCK_N);
+      if (st == GEMM_OK) st = loss_launch(p, kGrad, X, ld.x, W, K, q.features[0], ws, ldg, device, info, s);
     }
     // (a last piece of fewer slices adds to the first ones)
     if (st == GEMM_OK && first > 0) st = pair_gradient_plan(q, device, &plan);

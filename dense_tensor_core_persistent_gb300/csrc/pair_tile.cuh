@@ -15,15 +15,14 @@ enum PairMode {
   kPairGated = 0,      // A: rows of X; B: 128 rows of Wg over the same 128 of Wu
   kPairGatedE4m3 = 1,  // the same in E4M3 (256 x 256 tile only)
   kPairGradient = 2,   // main: A = rows of G (K-major), B = W by columns; second: A = G, B = X, both by columns
-  kPairRows = 3,       // A: rows of X; B: 256 rows of W
-  kPairRowsSums = 4    // the same, the depth in parts of kPairSumStages stages with an accumulator each, which the epilogue
-                       // adds in FP32 (256 x 256 tile only)
+  kPairRows = 3        // A: rows of X; B: 256 rows of W; the depth in parts of kPairSumStages stages with an accumulator each,
+                       // which the epilogue adds in FP32 (256 x 256 tile only)
 };
 
 // A tensor-core step cuts what lies below its FP32 accumulator's last place, so a long sum in one accumulator shrinks
-// towards zero by some 2^-25 a step. Results that stay in FP32 are summed in parts of 512: measured on GB300, cross
-// entropy of 1500 x 50001 x 2056 and 4096 x 131072 x 4096 222 and 2256 us with one part (error against 64 bits 1.2e-6),
-// 224 and 2281 with parts of 512, 229 and 2346 with parts of 256 (1.2e-7).
+// towards zero by some 2^-25 a step. Logits, which stay in FP32, are summed in parts of 512. Measured on GB300, cross entropy
+// of 1500 x 50001 x 2056 and 4096 x 131072 x 4096 (error of lse against 64 bits): one part 1% faster (1.2e-6), parts of 512
+// (1.7e-7), parts of 256 2 to 3% slower (1.2e-7).
 constexpr int kPairSumStages = 4;
 
 // The tiles of one product: rows x cols of output, the summed dimension `depth` (dX: of one half) in `k_iters` stages.
@@ -249,7 +248,7 @@ __device__ __forceinline__ void pair_producer(const PairParams& p, const PairMap
       }
       first = mb * L::TILE_M + static_cast<int>(rank) * L::CTA_M;
       mn = GRADIENT && item.second;
-    } else if (MODE == kPairRows || MODE == kPairRowsSums) {
+    } else if (MODE == kPairRows) {
       m0 = m1 = &maps.b0;
       first = item.n_blk * L::BLOCK_N + half * (L::BLOCK_N / 2) + static_cast<int>(rank) * 64 * b_boxes;
       mn = false;
@@ -313,7 +312,7 @@ __device__ __forceinline__ void pair_mma(const PairParams& p, uint32_t base, uin
   const uint32_t bar_tfull = bar_empty + 8 * L::STAGES, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
   const uint64_t a_k = umma_desc_sw128(base + L::OFF_A), a_mn = umma_desc_mn(base + L::OFF_A, L::ATOM_BYTES);
   const uint64_t b0 = GRADIENT ? umma_desc_mn(base + L::OFF_B, L::ATOM_BYTES) : umma_desc_sw128(base + L::OFF_B);
-  constexpr bool SUMS = MODE == kPairRowsSums;
+  constexpr bool SUMS = MODE == kPairRows;
   uint32_t stage = 0, phase = 0;
   int acc = 0;  // accumulators taken: one an item, or one for each part of its depth
   bool ok = true;
@@ -445,7 +444,7 @@ __device__ __forceinline__ void pair_cta(const PairMaps& maps, const PairParams&
   // One branch per role group, each running to the end of the kernel (the code after a change of register limit
   // belongs to that limit).
   if (warp < L::EPI_WARP0) {
-    if constexpr (MODE == kPairRowsSums) regs_decrease<kPairRegsLow>();
+    if constexpr (MODE == kPairRows) regs_decrease<kPairRegsLow>();
     if (lane == 0) {
       if (warp == L::WARP_A || warp == L::WARP_B)
         pair_producer<MODE>(p, maps, base, rank, warp == L::WARP_A, cluster_idx, num_clusters, wctx);
@@ -455,7 +454,7 @@ __device__ __forceinline__ void pair_cta(const PairMaps& maps, const PairParams&
     __syncwarp();
     pair_teardown(warp, tmem_base);
   } else {
-    if constexpr (MODE == kPairRowsSums) regs_increase<kPairRegsEpilogue>();
+    if constexpr (MODE == kPairRows) regs_increase<kPairRegsEpilogue>();
     epilogue(PairCta{base, tmem_base, warp, lane, rank, cluster_idx, num_clusters, wctx});
     pair_teardown(warp, tmem_base);
   }
@@ -522,10 +521,6 @@ __device__ __forceinline__ void pair_wide_producer(const PairParams& p, const Pa
       }
       first = mb * L::TILE_M + static_cast<int>(rank) * L::CTA_M;
       mn = GRADIENT && item.second;
-    } else if (MODE == kPairRows) {
-      m0 = m1 = &maps.b0;
-      first = item.n_blk * L::BLOCK_N + half * (L::BLOCK_N / 2) + static_cast<int>(rank) * 64 * b_boxes;
-      mn = false;
     } else if (!GRADIENT) {
       m0 = m1 = rank == 1 ? &maps.b1 : &maps.b0;
       first = item.n_blk * L::FEATURES + half * (L::FEATURES / 2);

@@ -303,3 +303,58 @@ def test_few_rows_do_not_see_the_rounding_of_g(M, V, K, workspace):
         want, size = A @ B, A.abs() @ B.abs()
         tol = dA @ B.abs() + (2 * A.shape[1] / 16 + 10 + 32 * pieces) * 2.0 ** -22 * size
         assert torch.all((got.double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol) + 1e-37)
+
+
+@pytest.mark.parametrize("M", [40, 130, 700])
+def test_gradient_takes_the_logits_that_the_forward_pass_took(M):
+    """A target whose logit is one product of 2^24 and 480 steps of 16 products that add 1/2 each, a quarter of that number's
+    last place: one accumulator never sees them, parts of the depth add them exactly. Every logit, its scale by 2^-20 and
+    their difference to lse are exact then, so p is off by lse's rounding (half of 2^-19), the exponential's 2^-22 and its
+    argument's product, less than 2^-20 + 2^-21 together; 1 - p is 3.4e-4."""
+    K, V, scale = 8192, 3001, 2.0 ** -20
+    x, head = torch.zeros(M, K), torch.zeros(V, K)
+    x[:, 0], x[:, 512:] = 2.0 ** 12, 2.0 ** -5
+    head[7, 0], head[7, 1:] = 2.0 ** 12, 1.0
+    x, head = x.to(BF16).to(DEV), head.to(BF16).to(DEV)
+    targets = torch.full((M,), 7, device=DEV)
+    r = g.cross_entropy(x, head, targets, scale=scale)
+    d = Definition(x, head, targets, scale)
+    assert d.z[0, 7].item() == 16 + 240 * scale
+    assert torch.all((r.lse.double() - d.lse).abs() <= 2.0 ** -20 + 2.0 ** -22)
+    dx, dw = g.cross_entropy_backward(x, head, targets, r.lse, torch.full((M,), 1 / scale, device=DEV), scale=scale)
+    p = (d.z - d.lse[:, None]).exp()
+    G, e = p - d.onehot, (2.0 ** -20 + 2.0 ** -21) * p
+    for got, A, dA, B in ((dx, G, e, d.w), (dw, G.T, e.T, d.x)):
+        want, tol = A @ B, (dA + 2.0 ** -8 * (A.abs() + dA)) @ B.abs()
+        assert torch.all((got.double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol) + 1e-37)
+
+
+@pytest.mark.parametrize("M", [40, 200])
+def test_long_sums_keep_their_digits(M):
+    """Rows that lean on one target: its logit grows evenly over 4096 products. A tensor-core step cuts what is below its
+    accumulator's last place, in the mean half of it, 2^-25 to 2^-24 of the accumulator; over n steps of an evenly growing sum
+    that is n / 2 of these on one side. One accumulator (256 steps) would shrink the logit, and lse with it, by at least 3.8e-6;
+    parts of 512 (32 steps) by 9.5e-7 at most, of 128 (8 steps, up to 64 rows) by 2.4e-7, and lse's rounding, 2^-24 on either
+    side, is left with at most 2^-24 / sqrt(40) x 4 = 4e-8 of it in the mean.
+    The target's share of G, p - 1 (read off a column of W that has a one in the target's row), is between 1/45 and 1/400 here,
+    and z / (1 - p) 1420 and 2930 in the mean: in parts the logit's error and lse's move it by at most 9.5e-7 x 1420 = 1.4e-3
+    of itself in the mean (up to 64 rows 2.4e-7 x 2930 = 7e-4), one accumulator by 5.4e-3 at least; G's and dX's roundings
+    (2^-8 at most each, 1.7e-3 in the square mean) leave 4 x 2.4e-3 / sqrt(M) in the mean on top: 7e-4, at 40 rows 1.6e-3."""
+    K, V, t = 4104, 2000, 7
+    gen = torch.Generator().manual_seed(M)
+    head = torch.randn(V, K, generator=gen) * 2 / K ** 0.5
+    head[:, 4096:] = 0.0
+    head[t, 4096] = 1.0
+    x = torch.randn(M, K, generator=gen) * 0.02
+    x += (2.9 + 0.4 * torch.rand(M, 1, generator=gen)) * head[t]
+    x[:, 4096:] = 0.0
+    x, head = x.to(BF16).to(DEV), head.to(BF16).to(DEV)
+    targets = torch.full((M,), t, device=DEV)
+    r = g.cross_entropy(x, head, targets)
+    d = Definition(x, head, targets, 1.0)
+    few = M <= 64
+    assert ((r.lse.double() - d.lse) / d.lse).mean().abs() <= (3e-7 if few else 1e-6)
+    dx, _ = g.cross_entropy_backward(x, head, targets, r.lse, torch.ones(M, device=DEV), weight_grad=False)
+    share = (d.z[:, t] - d.lse).exp() - 1
+    assert (d.z[:, t] / -share).mean() < (2930 if few else 1420)
+    assert (dx[:, 4096].double() / share - 1).mean().abs() <= (2.4e-3 if few else 3.4e-3)
