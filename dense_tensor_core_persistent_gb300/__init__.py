@@ -48,6 +48,7 @@ EXPORTS = (
     "gemm_glu_bf16", "gemm_glu_e4m3", "gemm_glu_bf16_backward", "gemm_glu_plan",
     "gemm_layer_norm", "gemm_layer_norm_backward", "gemm_embedding", "gemm_embedding_backward",
     "gemm_cross_entropy", "gemm_cross_entropy_backward", "gemm_cross_entropy_piece",
+    "gemm_cross_entropy_plan",
 )
 
 # gemm_activation_t
@@ -256,6 +257,8 @@ def lib() -> ctypes.CDLL:
         l.gemm_cross_entropy_backward.restype = I
         l.gemm_cross_entropy_piece.argtypes = [I, I, ctypes.c_size_t]
         l.gemm_cross_entropy_piece.restype = I
+        l.gemm_cross_entropy_plan.argtypes = [I, I, I, I, ctypes.c_size_t, I, I, ctypes.POINTER(I), ctypes.POINTER(I)]
+        l.gemm_cross_entropy_plan.restype = I
         _lib = l
     return _lib
 
@@ -573,6 +576,16 @@ def cross_entropy_piece(M: int, vocab: int, workspace: int = 0) -> int:
     if n < 0:
         raise GemmError(-n, "gemm_cross_entropy_piece")
     return n
+
+
+def cross_entropy_plan(M: int, vocab: int, K: int, workspace: int = 0, input_grad: bool = True, weight_grad: bool = True,
+                       wave: int = 76) -> tuple[int, bool]:
+    """(rows of the pair tile of the gradient's products, whether a contiguous X is copied) of cross_entropy_backward for
+    this problem (host only)."""
+    rows, copy = ctypes.c_int(), ctypes.c_int()
+    _check(lib().gemm_cross_entropy_plan(M, vocab, K, wave, workspace, input_grad, weight_grad, ctypes.byref(rows),
+                                         ctypes.byref(copy)), "gemm_cross_entropy_plan")
+    return rows.value, bool(copy.value)
 
 
 # ---------------------------------------------------------------- torch-tensor conveniences

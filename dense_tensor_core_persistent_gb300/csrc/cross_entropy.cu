@@ -410,9 +410,9 @@ int simple_launch(void (*kernel)(Params...), int grid, int threads, cudaStream_t
 // again, is worth a copy in rows that start on the boundary where its products are large (W, as large as what is read of
 // it, is not). With the copy it takes 204 forward, and 568
 // instead of 596 for the gradient; 8192 x 32001 x 1000 339 and 382 without, 970 and 1022.
-bool copy_pays(const void* X, long long ldx, int M, int vocab, int K) {
-  const bool on_boundary = (reinterpret_cast<uintptr_t>(X) & 127u) == 0 && ldx % 64 == 0;
-  return !on_boundary && 2.0 * M * vocab * K > 1e11 && vocab > 4096;
+bool on_boundary(const void* X, long long ldx) { return (reinterpret_cast<uintptr_t>(X) & 127u) == 0 && ldx % 64 == 0; }
+bool copy_pays(bool x_on_boundary, int M, int vocab, int K) {
+  return !x_on_boundary && 2.0 * M * vocab * K > 1e11 && vocab > 4096;
 }
 long long copy_stride(int K) { return (K + 63LL) / 64 * 64; }
 int copy_rows(const void* X, long long ldx, void* out, int M, int K, cudaStream_t stream) {
@@ -457,6 +457,22 @@ int gemm_cross_entropy_piece(int M, int vocab, size_t workspace) {
   return static_cast<int>(round_up((vocab + pieces - 1) / pieces, 256));
 }
 
+int gemm_cross_entropy_plan(int M, int vocab, int K, int wave, size_t workspace, int input_grad, int weight_grad,
+                            int* products, int* copy) {
+  if (M < 0 || vocab < 0 || K < 0 || wave <= 0 || products == nullptr || copy == nullptr) return GEMM_ERR_INVALID_ARG;
+  const bool few = M <= kLossRows;
+  PairGradient q = {};
+  q.dx = input_grad ? copy : nullptr;  // (nothing is read)
+  q.dw[0] = weight_grad ? copy : nullptr;
+  q.rows = few ? 2 * M : M;
+  q.features[0] = q.features[1] = gemm_cross_entropy_piece(M, vocab, workspace);
+  q.K = K;
+  q.parts = 1;
+  *products = pair_gradient_is_wide(q, wave) ? 512 : 256;
+  *copy = !few && copy_pays(K % 64 == 0, M, vocab, K) ? 1 : 0;
+  return GEMM_OK;
+}
+
 int gemm_cross_entropy(const void* X, const void* W, const long long* targets, float* loss, float* lse, int M, int vocab,
                        int K, float scale, void* stream, const gemm_cross_entropy_strides_t* strides) {
   using L = PairLayout;
@@ -498,7 +514,8 @@ int gemm_cross_entropy(const void* X, const void* W, const long long* targets, f
     extra = size_t(wave) * L::TILE_M;  // (at most half a wave's tiles are cut in halves)
   }
   const size_t parts = size_t(j.count) * M;
-  const size_t copy = !few && copy_pays(X, ld.x, M, vocab, K) ? size_t(M) * copy_stride(K) * 2 : 0;  // a multiple of 128
+  const bool copied = !few && copy_pays(on_boundary(X, ld.x), M, vocab, K);
+  const size_t copy = copied ? size_t(M) * copy_stride(K) * 2 : 0;  // a multiple of 128
   cudaMemPool_t pool = workspace_pool(device);
   void* ws = nullptr;
   if (pool == nullptr ||
@@ -593,7 +610,7 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
   int st = pair_gradient_plan(q, device, &plan);
   if (st != GEMM_OK) return st;
   const size_t g_bytes = round_up(size_t(g_rows) * ldg * 2, 256);
-  const bool copied = few ? dW != nullptr : copy_pays(X, ld.x, M, vocab, K);
+  const bool copied = few ? dW != nullptr : copy_pays(on_boundary(X, ld.x), M, vocab, K);
   const size_t copy = copied ? round_up(size_t(g_rows) * copy_stride(K) * 2, 256) : 0;
   cudaMemPool_t pool = workspace_pool(device);
   void* ws = nullptr;

@@ -711,6 +711,16 @@ int gemm_cross_entropy_backward(const void* X, const void* W, const long long* t
  * Host evaluation, no GPU needed. */
 int gemm_cross_entropy_piece(int M, int vocab, size_t workspace);
 
+/*
+ * gemm_cross_entropy_plan -- what gemm_cross_entropy_backward uses for the (first) piece of a problem with `wave`
+ * co-resident CTA pairs (76 on a 152-SM GB300), as gemm_glu_plan: *products, the rows of the pair tile of dX (input_grad
+ * not 0) and dW (weight_grad not 0), 256 or 512; *copy, whether it and the forward call copy an X whose first row starts
+ * on a 128-byte boundary and whose rows follow one another. Host evaluation, no GPU needed. GEMM_ERR_INVALID_ARG for
+ * negative sizes, wave <= 0 or null outputs.
+ */
+int gemm_cross_entropy_plan(int M, int vocab, int K, int wave, size_t workspace, int input_grad, int weight_grad,
+                            int* products, int* copy);
+
 #ifdef __cplusplus
 }
 #endif

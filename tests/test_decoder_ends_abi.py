@@ -255,3 +255,19 @@ def test_sizes_past_32_bits_are_refused(monkeypatch):
         g.embedding(x, OnDeviceVector(0, i64, big))
     with pytest.raises(ValueError, match="vocab:"):
         g.embedding_backward(x, OnDeviceVector(0, i64, 2), big)
+
+
+def test_cross_entropy_plan():
+    for wave in (68, 76):
+        assert g.cross_entropy_plan(4096, 131072, 4096, wave=wave) == (512, False)
+        assert g.cross_entropy_plan(300, 8005, 520, wave=wave) == (256, False)
+        assert g.cross_entropy_plan(1500, 50001, 2056, wave=wave)[1]  # rows off 128-byte boundaries, large products
+        assert not g.cross_entropy_plan(64, 131072, 4104, wave=wave)[1]
+        assert g.cross_entropy_plan(4096, 131072, 1024, input_grad=False, wave=wave)[0] == 512  # (its depth is the rows)
+        assert g.cross_entropy_plan(1024, 131072, 4096, input_grad=False, wave=wave)[0] == 256
+    for bad in ((-1, 8, 8), (8, -1, 8), (8, 8, -1)):
+        with pytest.raises(g.GemmError):
+            g.cross_entropy_plan(*bad)
+    with pytest.raises(g.GemmError):
+        g.cross_entropy_plan(8, 8, 8, wave=0)
+    assert g.lib().gemm_cross_entropy_plan(8, 8, 8, 76, 0, 1, 1, None, None) == BAD

@@ -358,3 +358,50 @@ def test_long_sums_keep_their_digits(M):
     share = (d.z[:, t] - d.lse).exp() - 1
     assert (d.z[:, t] / -share).mean() < (2930 if few else 1420)
     assert (dx[:, 4096].double() / share - 1).mean().abs() <= (2.4e-3 if few else 3.4e-3)
+
+
+# where the gradient's products run on the 512 x 256 pair tile: in one piece with X copied to rows on 128-byte boundaries, in
+# two pieces (the last one ragged) with such a copy, and in two without, of which the last one takes the 256 x 256 tile
+LARGE = [(3500, 7501, 2056, 0, True, 512), (3500, 7001, 2056, 3584, True, 512), (2304, 4090, 2048, 2048, False, 256)]
+
+
+@pytest.mark.parametrize("M,V,K,columns,copy,last", LARGE)
+def test_the_large_tile(M, V, K, columns, copy, last):
+    workspace = 2 * M * columns
+    piece = g.cross_entropy_piece(M, V, workspace)
+    for wave in range(68, 77):  # (whatever pairs the device holds)
+        assert g.cross_entropy_plan(M, V, K, workspace, wave=wave) == (512, copy)
+        assert g.cross_entropy_plan(M, (V - 1) % piece + 1, K, wave=wave)[0] == last
+        if K == 2056:
+            assert g.cross_entropy_plan(M, V, K, workspace, weight_grad=False, wave=wave)[0] == 512
+            assert g.cross_entropy_plan(M, V, K, workspace, input_grad=False, wave=wave)[0] == 512
+    x, head, targets, dloss, dlse = problem(M, V, K, M)
+    r = g.cross_entropy(x, head, targets)
+    d = Definition(x, head, targets, 1.0)
+    d.check_forward(r)
+    kw = dict(dlse=dlse, workspace=workspace)
+    pieces = -(-V // piece)
+    dx, dw = g.cross_entropy_backward(x, head, targets, r.lse, dloss, **kw)
+    d.check_backward(dloss, dlse, dx, dw, pieces=pieces)
+    again = g.cross_entropy_backward(x, head, targets, r.lse, dloss, **kw)
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+    d.check_backward(dloss, dlse, *g.cross_entropy_backward(x, head, targets, r.lse, dloss, weight_grad=False, **kw),
+                     pieces=pieces)
+    d.check_backward(dloss, dlse, *g.cross_entropy_backward(x, head, targets, r.lse, dloss, input_grad=False, **kw),
+                     pieces=pieces)
+    assert g.get_device_status()[0] == 0
+
+
+def test_a_copied_x_with_a_stride_and_what_lies_behind():
+    M, V, K = 2500, 10500, 2008
+    assert g.cross_entropy_plan(M, V, K)[1]
+    x, head, targets, dloss, dlse = problem(M, V, K, 3)
+    wide = torch.full((M + 1, K + 16), float("nan"), dtype=BF16, device=DEV)
+    wide[:M, 8:K + 8] = x
+    view = wide[:M, 8:K + 8]
+    r, s = g.cross_entropy(x, head, targets), g.cross_entropy(view, head, targets)
+    assert torch.equal(r.loss, s.loss) and torch.equal(r.lse, s.lse)
+    want = g.cross_entropy_backward(x, head, targets, r.lse, dloss, dlse=dlse)
+    got = g.cross_entropy_backward(view, head, targets, r.lse, dloss, dlse=dlse)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    Definition(x, head, targets, 1.0).check_backward(dloss, dlse, *got)

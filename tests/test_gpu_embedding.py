@@ -229,3 +229,24 @@ def test_sorts_of_every_kind(rows, vocab):
     """Around the lengths from which the sort takes more CTAs and reads its entries again, in one to three passes."""
     tokens, dy = ids(rows, rows, vocab, "frequent"), normal(rows, rows, 4)
     check_gradient(g.embedding_backward(dy, tokens, vocab), dy, tokens, vocab, 1.0, None)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,vocab,cols", [(16384, 3000, 4096), (1301, 70000, 4104), (1400, 900, 4099), (9000, 500, 1027),
+                                             (700001, 100, 8), (700001, 100, 7)])
+def test_lookup_of_many_rows(dtype, rows, vocab, cols):
+    """Rows and vectors enough for four loads a thread in flight."""
+    assert rows * -(-cols // 8) >= 4096 * torch.cuda.get_device_properties(DEV).multi_processor_count
+    gen = torch.Generator(device=DEV).manual_seed(cols)
+    table = torch.randn(vocab, cols + 8, generator=gen, device=DEV).to(dtype)[:, :cols]
+    tokens = torch.randint(0, vocab, (rows,), generator=gen, device=DEV)
+    tokens[torch.rand(rows, generator=gen, device=DEV) < 0.1] = -5
+    tokens[rows // 2] = vocab
+    want = torch.where((tokens >= 0)[:, None], table[tokens.clamp(0, vocab - 1)], 0.0)
+    want[rows // 2] = float("nan")
+    y = g.embedding(table, tokens)
+    assert torch.equal(y.nan_to_num(7.0), want.nan_to_num(7.0))
+    out = torch.full((rows + 1, cols + 8), 7.0, dtype=dtype, device=DEV)
+    g.gemm_embedding(table, g._table_kind(dtype, ""), tokens, out, rows, vocab, cols, cols + 8, cols + 8)
+    assert torch.equal(out[:rows, :cols].nan_to_num(7.0), want.nan_to_num(7.0))
+    assert torch.all(out[:, cols:] == 7) and torch.all(out[rows] == 7)

@@ -349,3 +349,33 @@ def test_backward_around_the_shapes(cols, own):
         put = torch.empty(rows, cols + 5, dtype=BF16, device=DEV)[:, 3:cols + 3]
         put.copy_(dy)
     check_backward(*g.layer_norm_backward(put, n.sum, dev(w), n.mean, n.rstd, dsum=dev(ds)), dy, Definition(x, r, w, b), ds)
+
+
+class OnTheDevice(Definition):
+    """The same, computed where the rows are (the CPU takes a minute for these)."""
+
+    def __init__(self, x, r, w, b):
+        with torch.device(DEV):
+            super().__init__(x, r, w, b)
+
+
+# with a residual to BF16 on the 16-byte boundary, 16 bytes for each of rows x cols elements of more than 1.5 times L2: fewer
+# rows on their way, two of them ahead from 4096 columns on, by a limit through shared memory; widths of whole and of ragged
+# warps, one to eight CTAs an SM
+@pytest.mark.parametrize("rows,cols", [(8192, 4096), (9000, 3080), (3301, 8192), (24001, 1160), (33000, 776), (6100, 4488)])
+def test_four_streams_past_l2(rows, cols):
+    assert 16 * rows * cols > 3 * torch.cuda.get_device_properties(DEV).L2_cache_size and 96 * 8 < cols <= 8192
+    gen = torch.Generator(device=DEV).manual_seed(cols)
+    x, r = (torch.randn(rows, cols, generator=gen, device=DEV).to(BF16) for _ in range(2))
+    _, _, w, b = problem(1, cols, 5)
+    w, b = dev(w), dev(b)
+    n = g.layer_norm(x, w, b, residual=r, eps=EPS, save=True)
+    d = OnTheDevice(x, r, w, b)
+    assert torch.equal(n.sum, d.s)
+    assert torch.all((n.mean.double()[:, None] - d.mean).abs() <= d.e)
+    assert torch.all((n.rstd.double()[:, None] - d.rstd).abs() <= d.R * d.rstd)
+    assert torch.all((n.y.double() - d.y).abs() <= 2.0 ** -8 * d.y.abs() + 2 * d.err)
+    stream = r.clone()
+    again = g.layer_norm(x, w, b, residual=stream, eps=EPS, save=True, inplace=True)
+    assert again.sum.data_ptr() == stream.data_ptr()
+    assert all(torch.equal(u, v) for u, v in zip((n.y, n.sum, n.mean, n.rstd), (again.y, stream, again.mean, again.rstd)))
