@@ -7,8 +7,9 @@
 // Gradient: positions are sorted by token (stable, so a token's rows are added in the order of their positions and the
 // same inputs give the same bits), then a CTA takes a run of sorted positions and 8 columns a thread, adds dy's rows in
 // FP32 and writes each token's row once. Tokens of more than 16 positions are summed by run, into FP32 partial rows that a
-// last kernel adds in order: a token that is a tenth of all positions costs no more than the others.
-// The sort is a least-significant-digit radix sort of up to 10 bits a pass (two passes up to 2^20 tokens) by one cluster of
+// last kernel adds in order: a token that is a tenth of all positions costs no more than the others. (Up to 256 positions
+// need no sort: direct_kernel.)
+// The sort is a least-significant-digit radix sort of up to 10 bits a pass (two passes below 2^20 tokens) by one cluster of
 // 8 or 16 CTAs: a warp counts the digits of its part of the list, the CTAs exchange their totals through shared memory, and every
 // warp then knows where its part's digits go. The lists lie in global memory (L2), so their length is not limited. Beside
 // the sort another kernel writes the whole table, zeros or the base: that is most of the bytes of a dense gradient, and it

@@ -639,10 +639,10 @@ int gemm_embedding(const void* table, int type, const long long* tokens, void* Y
 /*
  * gemm_embedding_backward -- gradient of the table, dense:
  *   dtable[v] = round(base[v] + scale * sum over i with tokens[i] == v of dY[i]),
- * summed in FP32 in the order of the positions (more than 16 of a token in parts, which are added in a fixed order) and
- * rounded once.
+ * summed in FP32 in the order of the positions (where there are more than 256 positions, more than 16 of a token in parts,
+ * which are added in a fixed order) and rounded once.
  *   dY: rows x cols of dy_type, row stride ldd elements (0 = cols), element-aligned.
- *   base: vocab x cols of table_type, contiguous: what is there already (with tied weights the head's dW, from
+ *   base: vocab x cols of table_type, contiguous: what is there already (with tied weights the head's dW, BF16 from
  *   gemm_cross_entropy_backward); NULL: zeros. base may be dtable: then only the rows of given tokens are written;
  *   else they do not overlap.
  *   dtable: vocab x cols of table_type, contiguous. dtable and base are 16-byte aligned, in place element-aligned.

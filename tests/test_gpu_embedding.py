@@ -250,3 +250,48 @@ def test_lookup_of_many_rows(dtype, rows, vocab, cols):
     g.gemm_embedding(table, g._table_kind(dtype, ""), tokens, out, rows, vocab, cols, cols + 8, cols + 8)
     assert torch.equal(out[:rows, :cols].nan_to_num(7.0), want.nan_to_num(7.0))
     assert torch.all(out[:, cols:] == 7) and torch.all(out[rows] == 7)
+
+
+@pytest.mark.parametrize("rows", [257, 4000, 16384, 20000, 131073, 200000])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_order_of_positions_through_the_sort(rows, dtype):
+    """As test_order_of_positions_and_repeats where positions are sorted: by 8 CTAs, by 16 (above 16384 positions), and with its
+    entries read again (above 131072). Three positions of a token a long way apart, in their order within one warp's part of
+    the list, in two warps' and in two CTAs', cancel before the small one comes, which any other order would lose; the short
+    tokens stand beside one another and beside a long one in the sorted list."""
+    vocab, cols = 5000, 8
+    gen = torch.Generator().manual_seed(rows)
+    tokens = torch.randint(0, 100, (rows,), generator=gen)  # (long ones, none above 99)
+    tokens[torch.rand(rows, generator=gen) < 0.1] = -1
+    dy = torch.zeros(rows, cols)
+    places = torch.randperm(rows, generator=gen)[:240].view(80, 3).sort(1).values
+    places[0] = torch.tensor([0, rows // 2, rows - 1])
+    places[1] = torch.tensor([1, 2, 3])
+    places[2] = torch.tensor([31, 32, 33])
+    places[3] = torch.tensor([63, 64, 255])
+    kept = torch.ones(80, dtype=torch.bool)
+    seen = set()
+    for i in range(80):  # (random ones that took another's place are left out)
+        if seen & set(places[i].tolist()):
+            kept[i] = False
+        else:
+            seen |= set(places[i].tolist())
+    places = places[kept]
+    ids = 1000 + 7 * torch.arange(len(places))
+    for i, (a, b, c) in enumerate(places.tolist()):
+        tokens[a] = tokens[b] = tokens[c] = ids[i]
+        dy[a], dy[b], dy[c] = 2.0 ** 27, -2.0 ** 27, 0.25
+    got = g.embedding_backward(dy.to(dtype).to(DEV), tokens.to(DEV), vocab)
+    assert torch.all(got[ids.to(DEV)] == 0.25)
+    # one token of 16 positions, the most that are added one after the other, within a run of sorted positions or across two
+    for lead in range(8):
+        tokens[:] = -1
+        tokens[:lead] = 1
+        at = torch.randperm(rows - lead, generator=gen)[:16].sort().values + lead
+        tokens[at] = 2
+        dy[:] = 0
+        for i in range(15):
+            dy[at[i]] = 2.0 ** 27 * (-1) ** i if i < 14 else 0.25
+        dy[at[15]] = 0.5
+        got = g.embedding_backward(dy.to(dtype).to(DEV), tokens.to(DEV), vocab)
+        assert torch.all(got[2] == 0.75)
