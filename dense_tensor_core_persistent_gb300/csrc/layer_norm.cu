@@ -442,12 +442,16 @@ constexpr int kTeams = 8;
 // REGS: what holds a row, its weight and the sums of dw and db without spills, 128 with two groups a thread, even if a CTA
 // is alone on its SM then: 8192 x 4096 46.9 us with 80 registers and two CTAs, 41.3 so; 4000 x 8192 42.4, with four groups
 // (which spill) 52.3; 16000 x 1023 33.1 with 88, 28.0 so. One group with a row a warp: 64 and 80 the same 65536 x 255 in 48.7
-// and 44.4. Nine warps, the last with a row's ends, fit twice with 96: 4000 x 4099 31.6 with 128, 27.4 so; ten do too, and
-// lose by it: 4000 x 5003 35.6 and 38.7. Seventeen fit once with 96.
+// and 44.4. Off the boundary 96 where a second CTA of the warps with a row's ends fits an SM so, nine and ten of them (4000 x
+// 4099 31.3 with 128, 27.1 so; 4000 x 4401 34.2 and 30.1), or the only one (seventeen).
 // Three and four groups leave no registers for the weight: 4000 x 10000 82.9 us with four and the weight in registers, 78.2
 // with three, 73.3 with three and it in shared memory; 4000 x 16384 105.0 and 96.4 with four.
 __host__ __device__ constexpr bool weight_in_shared(int vpt) { return vpt == 3 || vpt == 4; }
 constexpr int backward_regs(int vpt, int slots, bool teams) { return vpt > 1 ? 128 : slots == 4 && !teams ? 80 : 64; }
+inline bool fewer_regs_pay(int threads) {
+  const auto ctas = [&](int regs) { return 65536 / (regs * threads); };  // of an SM
+  return ctas(128) < 2 && ctas(96) > ctas(128);
+}
 template <int VPT, int SLOTS, int ACCESS, bool TEAMS, int REGS = backward_regs(VPT, SLOTS, TEAMS)>
 __global__ void __maxnreg__(REGS) layer_norm_backward_kernel(const LayerNormBackwardParams p) {
   constexpr int AS = RowPart<ACCESS>::AS;
@@ -678,7 +682,7 @@ const void* backward_kernel(const LayerNormShape& s, bool teams) {
                           : reinterpret_cast<const void*>(layer_norm_backward_kernel<1, 4, ACCESS, false>);
     case 2:
       if constexpr (ACCESS == kShared) {
-        if (s.at.threads == 288 || s.at.threads == 544)
+        if (fewer_regs_pay(s.at.threads))
           return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 3, ACCESS, false, 96>);
         return reinterpret_cast<const void*>(layer_norm_backward_kernel<2, 3, ACCESS, false>);
       } else {

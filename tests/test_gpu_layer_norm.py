@@ -379,3 +379,18 @@ def test_four_streams_past_l2(rows, cols):
     again = g.layer_norm(x, w, b, residual=stream, eps=EPS, save=True, inplace=True)
     assert again.sum.data_ptr() == stream.data_ptr()
     assert all(torch.equal(u, v) for u, v in zip((n.y, n.sum, n.mean, n.rstd), (again.y, stream, again.mean, again.rstd)))
+
+
+# rows enough for several a CTA, off the boundary with 8 to 11 and 17 warps (the last one with a row's ends) and three and four
+# groups a thread, on it with four
+@pytest.mark.parametrize("rows,cols", [(700, 4087), (700, 4099), (700, 4401), (700, 4701), (500, 8195), (400, 10003), (330, 14003),
+                                       (330, 16008), (330, 15366)])
+def test_rows_of_many_warps(rows, cols):
+    x, r, w, b = problem(rows, cols, cols)
+    d = Definition(x, r, w, b)
+    n = g.layer_norm(dev(x), dev(w), dev(b), residual=dev(r), eps=EPS, save=True)
+    d.check(n)
+    d.check_e4m3(g.layer_norm(dev(x), dev(w), dev(b), residual=dev(r), eps=EPS, out="e4m3"))
+    dy, ds = rand(rows, rows, cols), rand(cols + 1, rows, cols, std=0.5)
+    got = g.layer_norm_backward(dev(dy), n.sum, dev(w), n.mean, n.rstd, dsum=dev(ds))
+    check_backward(*got, dy, d, ds)
