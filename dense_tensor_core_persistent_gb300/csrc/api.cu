@@ -10,7 +10,10 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <map>
 #include <mutex>
+#include <new>
+#include <tuple>
 
 #include "common.cuh"
 #include "gemm.h"
@@ -187,26 +190,21 @@ int encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 int resident_ctas(const void* kernel, int threads, int smem) {
-  struct Entry {
-    const void* kernel;
-    int threads, smem, ctas;
-  };
-  // Every size of every kernel that asks: a norm's seven forward kernels with one group a thread take 32 thread counts,
-  // with two 16, with four and eight 8 each, and so do its three backward ones: 640 for each of the two norms, and 32
-  // more for the layer norm's narrow rows and its gradient with three rows at a time.
-  constexpr int kEntries = 1312;
   static std::mutex mu;
-  static Entry entries[kEntries];
-  static int count = 0;
+  static std::map<std::tuple<const void*, int, int>, int> seen;
   std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < count; ++i)
-    if (entries[i].kernel == kernel && entries[i].threads == threads && entries[i].smem == smem) return entries[i].ctas;
+  const auto key = std::make_tuple(kernel, threads, smem);
+  const auto at = seen.find(key);
+  if (at != seen.end()) return at->second;
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) {
     cudaGetLastError();
     return 1;
   }
-  if (count < kEntries) entries[count++] = Entry{kernel, threads, smem, n};
+  try {
+    seen.emplace(key, n);
+  } catch (const std::bad_alloc&) {  // (asked again next time)
+  }
   return n;
 }
 
