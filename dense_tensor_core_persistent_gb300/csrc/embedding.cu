@@ -300,7 +300,9 @@ constexpr int kRowsThreads = 512, kRowsVectors = 4;  // of 16 bytes a thread
 
 // The whole table, zeros or the base (rows that tokens touch are written again by the sums). 32 KB a CTA, next to one
 // another: CTAs that come and go write 1 GB at 7.7 TB/s, resident ones that step over it by the grid's size at 6.4.
-// Beside the sort nothing here waits for it but the last CTA, so that the sums, which wait for this grid, find both done.
+// Beside the sort nothing here waits for it but the last CTA, so that the sums, which wait for this grid, find both done. What
+// was done before the sort is done: the sort lets this grid start only behind its own wait for that. The base is read past L1
+// all the same, as only a grid that waits is promised an L1 without lines from before.
 __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsParams p) {
   if (!p.beside) pdl_wait();
   pdl_launch_dependents();
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsParams p) 
   for (int j = 0; j < kRowsVectors; ++j) {
     const long long i = first + j * kRowsThreads;
     v[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (from != nullptr && i < vectors) v[j] = __ldcs(reinterpret_cast<const uint4*>(from) + i);
+    if (from != nullptr && i < vectors) v[j] = __ldcg(reinterpret_cast<const uint4*>(from) + i);
   }
 #pragma unroll
   for (int j = 0; j < kRowsVectors; ++j) {
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsParams p) 
   if (blockIdx.x + 1 == gridDim.x) {
     const long long at = vectors * 16 + 2 * threadIdx.x;  // (fewer than 16 bytes are left, a multiple of two)
     if (at < p.bytes)
-      *reinterpret_cast<uint16_t*>(to + at) = from != nullptr ? *reinterpret_cast<const uint16_t*>(from + at) : uint16_t(0);
+      *reinterpret_cast<uint16_t*>(to + at) = from != nullptr ? __ldcg(reinterpret_cast<const uint16_t*>(from + at)) : uint16_t(0);
     if (p.beside) pdl_wait();
   }
 }

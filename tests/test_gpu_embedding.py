@@ -295,3 +295,18 @@ def test_order_of_positions_through_the_sort(rows, dtype):
         dy[at[15]] = 0.5
         got = g.embedding_backward(dy.to(dtype).to(DEV), tokens.to(DEV), vocab)
         assert torch.all(got[2] == 0.75)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_base_that_is_written_again_between_two_calls(dtype):
+    """By a copy from the host, which no SM sees, right after kernels have read it: what they left in an L1 must not be read
+    again by the kernel that copies the base beside the sort."""
+    for vocab in (1000, 20000):
+        cols, rows = 1024, 300
+        base = torch.zeros(vocab, cols, dtype=dtype, device=DEV)
+        tokens, dy = ids(1, rows, vocab), torch.zeros(rows, cols, dtype=dtype, device=DEV)
+        host = [torch.full((vocab, cols), float(v), dtype=dtype).pin_memory() for v in (1, 2)]
+        for i in range(10):
+            g.embedding_backward(dy, tokens, vocab, base=base)
+            base.copy_(host[i % 2], non_blocking=True)
+            assert torch.all(g.embedding_backward(dy, tokens, vocab, base=base) == 1 + i % 2)
