@@ -46,8 +46,8 @@ struct LossRowsParams {
 template <int X_ROWS>
 struct LossRowsLayout {
   static constexpr int BOX = 32, TILE_BOXES = 4;
-  static constexpr int ATOMS = 2, KSTEPS = 8, STAGE_K = 128;  // 128-byte swizzle rows of K per stage; MMAs; elements
-  static constexpr int SUM_STAGES = 1;                        // stages of an accumulator
+  // 128-byte swizzle rows of K per stage; MMAs; elements, which are a part of the depth with an accumulator of its own
+  static constexpr int ATOMS = 2, KSTEPS = 8, STAGE_K = 128;
   static constexpr int BOX_BYTES = BOX * 128;
   static constexpr int W_ATOM_BYTES = TILE_BOXES * BOX_BYTES, X_ATOM_BYTES = X_ROWS * 128;
   static constexpr int W_BYTES = ATOMS * W_ATOM_BYTES, X_BYTES = ATOMS * X_ATOM_BYTES;
@@ -177,19 +177,14 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
     // ------------------------------------------------------------ MMA issuer
     const uint32_t idesc = idesc_bf16(128, p.n);
     const uint64_t a0 = umma_desc_sw128(base + L::OFF_W), b0 = umma_desc_sw128(base + L::OFF_X);
-    uint32_t stage = 0, phase = 0, acc = 0, slot = 0;
+    uint32_t stage = 0, phase = 0, acc = 0;
     bool ok = true;
     for (int t = 0; t < tiles && ok; ++t) {
-      for (int k = 0; k < p.k_iters; ++k) {
-        const int in_part = k % L::SUM_STAGES;
-        if (in_part == 0) {
-          slot = acc & 1u;
-          if (!wait_phase_inline(bar_tempty + 8 * slot, ((acc >> 1) & 1u) ^ 1u, wctx,
-                                 status_code(kRoleMma, 0x100 + slot))) {
-            ok = false;
-            break;
-          }
-          ++acc;
+      for (int k = 0; k < p.k_iters; ++k, ++acc) {
+        const uint32_t slot = acc & 1u;
+        if (!wait_phase_inline(bar_tempty + 8 * slot, ((acc >> 1) & 1u) ^ 1u, wctx, status_code(kRoleMma, 0x100 + slot))) {
+          ok = false;
+          break;
         }
         if (!wait_phase_inline(bar_full + 8 * stage, phase, wctx, status_code(kRoleMma, stage))) {
           ok = false;
@@ -203,7 +198,7 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
         auto one = [&](int kk) {
           const uint32_t in_atom = static_cast<uint32_t>(kk % 4) * 32u, atom = static_cast<uint32_t>(kk / 4);
           mma_f16<1>(d, umma_desc_advance(a, atom * L::W_ATOM_BYTES + in_atom),
-                     umma_desc_advance(b, atom * L::X_ATOM_BYTES + in_atom), idesc, (in_part | kk) != 0 ? 1u : 0u);
+                     umma_desc_advance(b, atom * L::X_ATOM_BYTES + in_atom), idesc, kk != 0 ? 1u : 0u);
         };
         if (steps == L::KSTEPS) {
 #pragma unroll
@@ -214,7 +209,7 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
         mma_commit_local(bar_empty + 8 * stage);
         stage = stage + 1 == L::STAGES ? 0u : stage + 1;
         phase = stage == 0 ? phase ^ 1u : phase;
-        if (in_part + 1 == L::SUM_STAGES || k + 1 == p.k_iters) mma_commit_local(bar_tfull + 8 * slot);
+        mma_commit_local(bar_tfull + 8 * slot);
       }
     }
     if (!ok) {
@@ -263,7 +258,6 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
       target[lane] = t >= 0 && t < p.x.vocab ? static_cast<int>(t) : -1;
     }
     __syncwarp();
-    const int parts = (p.k_iters + L::SUM_STAGES - 1) / L::SUM_STAGES;
     SoftmaxPart s[L::COLS];
 #pragma unroll
     for (int j = 0; j < L::COLS; ++j) s[j] = SoftmaxPart{-INFINITY, -1.0f};
@@ -274,7 +268,7 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
       const bool in = b + static_cast<int>(q) < tile_box(t + 1) && token < p.x.vocab;
       float z[L::COLS];
 #pragma unroll 1
-      for (int part = 0; part < parts; ++part, ++acc) {
+      for (int part = 0; part < p.k_iters; ++part, ++acc) {
         const uint32_t slot = acc & 1u;
         if (!wait_phase_warp(bar_tfull + 8 * slot, (acc >> 1) & 1u, wctx, status_code(kRoleEpilogue, slot))) {
           ok = false;
@@ -305,15 +299,15 @@ __global__ void __launch_bounds__(LossRowsLayout<X_ROWS>::NUM_THREADS, 1)
           to[j * p.grad.ldg] = static_cast<uint16_t>(high);
           to[j * p.grad.ldg + half] = static_cast<uint16_t>(pack_bf16x2_rn(__float_as_uint(left), 0u) & 0xFFFFu);
         }
-        continue;
-      }
+      } else {
 #pragma unroll
-      for (int j = 0; j < L::COLS; ++j) {
-        if (target[j] == token) p.x.target_z[col0 + j] = z[j];
-        // the new logit is the maximum, or one of the others; minus infinity adds nothing to either
-        const float d = z[j] - s[j].m, e = ex2_approx(-fabsf(d) * c);
-        if (z[j] != -INFINITY) s[j].others = d > 0.0f ? (s[j].others + 1.0f) * e : s[j].others + e;
-        s[j].m = fmaxf(s[j].m, z[j]);
+        for (int j = 0; j < L::COLS; ++j) {
+          if (target[j] == token) p.x.target_z[col0 + j] = z[j];
+          // the new logit is the maximum, or one of the others; minus infinity adds nothing to either
+          const float d = z[j] - s[j].m, e = ex2_approx(-fabsf(d) * c);
+          if (z[j] != -INFINITY) s[j].others = d > 0.0f ? (s[j].others + 1.0f) * e : s[j].others + e;
+          s[j].m = fmaxf(s[j].m, z[j]);
+        }
       }
     }
     if constexpr (!GRAD) {
