@@ -197,7 +197,7 @@ __device__ __forceinline__ void row_moments(const float2* moments, const float* 
   }
   const float shift = first * inverse_cols;
   mean = about + shift;
-  var = fmaxf(fmaf(-first, shift, second), 0.0f) * inverse_cols + (second - second);  // (NaN stays NaN)
+  var = fmaxf(fmaf(-first, shift, second), 0.0f) * inverse_cols + (second - second);  // (NaN and infinity make it NaN)
 }
 
 struct NormShared {
@@ -335,7 +335,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(96, 128)) layer_norm_kernel(const Lay
             squares = fmaf(d, d, squares);
           });
     squares = warp_sum(squares + pair_sum(squares2));
-    float mean = warp_mean, var = squares * inverse_cols;
+    float mean = warp_mean, var = squares * inverse_cols + (squares - squares);  // (infinite squares make the row NaN)
     if (warps > 1) {
       if (lane == 0) sh.moments[parity][warp] = make_float2(warp_mean, squares);
       cta_sync();
@@ -343,7 +343,7 @@ __global__ void __maxnreg__(norm_regs<VPT>(96, 128)) layer_norm_kernel(const Lay
     }
     const float rstd = inverse_sqrt(var + p.eps);
     if (threadIdx.x == 0) {
-      if (p.mean != nullptr) p.mean[row] = mean;
+      if (p.mean != nullptr) p.mean[row] = mean + (var - var);  // (of a row with an infinity NaN, as its other outputs)
       if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
     const uint64_t mean2 = f2_pack(-mean, -mean), rstd2 = f2_pack(rstd, rstd);

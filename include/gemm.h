@@ -497,8 +497,9 @@ int gemm_rms_norm_backward(const void* dY, const void* S, const void* W, const f
  *   B: cols BF16, or NULL (zeros); NVFP4: 16-byte aligned.
  *   mean, rstd: rows FP32 for the backward pass, or NULL.
  * The variance is the mean of squared differences (never below 0): a row whose mean is far larger than its spread keeps
- * its digits. An infinity or NaN in a row makes the row's outputs NaN, and only that row's. Rows without columns have
- * mean, rstd and E4M3 scales of 0.
+ * its digits. An infinity or NaN in a row makes the row's outputs NaN (S apart, and NVFP4 codes, whose scales are NaN), and
+ * only that row's; so does a sum of values or of squared differences that passes 3.4e38. Rows without columns have mean,
+ * rstd and E4M3 scales of 0.
  * One kernel launch, asynchronous on `stream`; no workspace.
  */
 int gemm_layer_norm(const void* X, const void* R, const void* W, const void* B, void* S, void* Y, void* scales,

@@ -394,3 +394,29 @@ def test_rows_of_many_warps(rows, cols):
     dy, ds = rand(rows, rows, cols), rand(cols + 1, rows, cols, std=0.5)
     got = g.layer_norm_backward(dev(dy), n.sum, dev(w), n.mean, n.rstd, dsum=dev(ds))
     check_backward(*got, dy, d, ds)
+
+
+@pytest.mark.parametrize("cols", [16, 200, 255, 256, 257, 1024, 1025, 4099, 20000, 20001])
+@pytest.mark.parametrize("rows", [7, 700])
+def test_sums_past_fp32_make_the_row_nan_at_every_width(cols, rows):
+    """2^70 squared passes FP32's range: such a row counts as one with an infinity, whether a warp has it alone or not, and its
+    statistics are NaN as its other outputs."""
+    x = rand(cols, rows, cols).to(DEV)
+    at = torch.arange(cols, device=DEV)
+    x[1] = torch.where(at % 2 == 0, 2.0 ** 70, -(2.0 ** 70)).to(BF16)
+    x[2, cols // 2] = math.inf
+    x[3, 0] = -math.inf
+    x[4, cols - 1] = math.nan
+    x[5] = torch.where(at % 2 == 0, 2.0 ** 50, -(2.0 ** 50)).to(BF16)  # (squares that FP32 holds)
+    bad = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    bad[1:5] = True
+    w, b = (t.to(DEV) for t in problem(1, cols, 3)[2:])
+    n = g.layer_norm(x, w, b, save=True)
+    for t in (n.mean, n.rstd, n.y[:, 0], n.y[:, -1]):
+        assert torch.equal(t.isnan(), bad)
+    assert n.y[1:5].isnan().all() and not n.y[5:].isnan().any()
+    n = g.layer_norm(x, w, b, out="e4m3")
+    assert torch.equal(n.scales.isnan(), bad) and n.y[1:5].float().isnan().all() and not n.y[5:].float().isnan().any()
+    if cols % 16 == 0:
+        n = g.layer_norm(x, w, b, out="nvfp4")
+        assert torch.equal(n.scales.view(torch.float8_e4m3fn).float().isnan().all(1), bad)
