@@ -405,3 +405,22 @@ def test_a_copied_x_with_a_stride_and_what_lies_behind():
     got = g.cross_entropy_backward(view, head, targets, r.lse, dloss, dlse=dlse)
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
     Definition(x, head, targets, 1.0).check_backward(dloss, dlse, *got)
+
+
+@pytest.mark.parametrize("M,V", [(70, 300), (600, 5003)])
+def test_targets_outside_the_vocabulary_and_rows_of_nan_above_64_rows(M, V):
+    x, head, targets, dloss, _ = problem(M, V, 64, 3)
+    targets = targets.clamp(min=0)
+    targets[1], targets[2], targets[M - 1] = V, -1, 1 << 40
+    x[2], x[5, 3], x[M - 2, 63] = float("nan"), float("inf"), -float("inf")
+    head[:, 63] = head[:, 63].abs() + 1  # (every logit of a row minus infinity)
+    targets[5] = -1
+    r = g.cross_entropy(x, head, targets)
+    past = torch.zeros(M, dtype=torch.bool, device=DEV)
+    past[[1, M - 1]] = True
+    bad = torch.zeros_like(past)
+    bad[[2, 5, M - 2]] = True
+    assert torch.equal(r.lse.isnan(), bad)
+    assert torch.equal(r.loss.isnan(), past | (bad & (targets >= 0))) and r.loss[2] == 0 and r.loss[5] == 0
+    dx, _ = g.cross_entropy_backward(x, head, targets, r.lse, dloss, weight_grad=False)
+    assert torch.equal(dx.isnan().any(1), past | (bad & (targets >= 0))) and torch.all(dx[[2, 5]] == 0)
