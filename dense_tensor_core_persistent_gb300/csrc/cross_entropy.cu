@@ -10,16 +10,19 @@
 // so lse and loss end in log1p and a row that its target dominates keeps its digits.
 //
 // Gradient: for a piece of the vocabulary at a time the logits are computed again, in the same parts of their depth as the
-// forward pass, their epilogue turns them into G (BF16, the operand of two products) and pair_gradient.cu's launch takes G to the piece's rows of dW and to dX, whose
-// pieces are added in FP32. (Up to 64 rows G comes from cross_entropy_rows.cu: 30 x 100000 x 2048 286 us with the pair
-// tile, 242 so.) A piece is as large as G's workspace may be; fewer pieces are
-// fewer joins and ramps. Not keeping z costs its product a second time: 8 MVK operations where 6 would do with M x V logits
-// in memory.
+// forward pass, their epilogue turns them into G (BF16, the operand of two products) and pair_gradient.cu's launch takes G to
+// the piece's rows of dW and to dX, whose pieces are added in FP32. A piece is as large as G's workspace may be; fewer pieces
+// are fewer joins and ramps. Not keeping z costs its product a second time: 8 MVK operations where 6 would do with M x V
+// logits in memory. (Up to 64 rows G comes from cross_entropy_rows.cu: 30 x 100000 x 2048 286 us with the pair tile, 242 so.)
+//
+// G's rounding is seen: dX and dW are 2.4e-3 of their size from 64 bits, where their own rounding to BF16 alone leaves 1.7e-3.
+// A second BF16 number for what the first one's rounding left would take that away, at 4 MVK operations more on top of the 8
+// of both passes (TF32 operands, at half the rate, cost the same). So above 64 rows it is one number.
 //
 // Bound by the tensor cores, for few rows by W's bytes. Measured on GB300: 4096 x 131072 x 4096 forward 2.24 ms (1.96
-// PFLOP/s), gradient 7.5 ms on a cool device (1.76 PFLOP/s over its three products) and up to 8.0 ms under the power cap
-// (with one accumulator for the logits' depth 7.4);
-// 4096 x 32768 x 1024 154 and 500 us; 64 x 131072 x 4096 gradient 579 us, where reading W twice and writing dW takes 475.
+// PFLOP/s), gradient 7.5 ms on a cool device (1.76 PFLOP/s over its three products; with one accumulator for the logits' depth
+// 7.4) and up to 8.0 ms under the power cap; 4096 x 32768 x 1024 154 and 500 us; 64 x 131072 x 4096 gradient 579 us, where
+// reading W twice and writing dW takes 475.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

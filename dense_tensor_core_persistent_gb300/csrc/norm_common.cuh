@@ -306,9 +306,10 @@ __device__ __forceinline__ void norm_output(const Value& value, void* y, long lo
 }
 
 // Registers per thread by groups per thread: 1024 threads with one group, 512 with more. With two groups as few as
-// hold a row without spills, so that several CTAs fit on an SM; with four a little fewer (4 to 40 bytes a thread are
-// spilled in the gradient and in forward rows off the boundary); with eight the 128 that 512 threads leave, which do
-// not hold a row (44 to 184 bytes). Rows off the boundary need some more for their ends; measured on GB300 at 16000 x
+// hold a row without spills, so that several CTAs fit on an SM; with four a little fewer (4 to 36 bytes a thread are
+// spilled in the gradient and in the RMS norm's rows to E4M3 off the boundary); with eight the 128 that 512 threads leave, which
+// do not hold a row (RMS norm 44 to 76 bytes forward and 132 to 312 in the gradient, layer norm, whose values are FP32, 412 to
+// 824 and 904 to 1760). Rows off the boundary need some more for their ends; measured on GB300 at 16000 x
 // 1023: forward 25.1 us with 64 and 26.7 with 56, gradient 36.3 with 80 and 42.8 with 64.
 template <int VPT>
 constexpr int norm_regs(int two, int four) { return VPT == 1 ? 64 : VPT == 2 ? two : VPT == 4 ? four : 128; }

@@ -22,7 +22,7 @@ enum PairMode {
 // A tensor-core step cuts what lies below its FP32 accumulator's last place, so a long sum in one accumulator shrinks
 // towards zero by some 2^-25 a step. Logits, which stay in FP32, are summed in parts of 512. Measured on GB300, cross entropy
 // of 1500 x 50001 x 2056 and 4096 x 131072 x 4096 (error of lse against 64 bits): one part 1% faster (1.2e-6), parts of 512
-// (1.7e-7), parts of 256 2 to 3% slower (1.2e-7).
+// (2.5e-7), parts of 256 2 to 3% slower (1.2e-7).
 constexpr int kPairSumStages = 4;
 
 // The tiles of one product: rows x cols of output, the summed dimension `depth` (dX: of one half) in `k_iters` stages.
