@@ -687,7 +687,7 @@ int gemm_cross_entropy(const void* X, const void* W, const long long* targets, f
  *   lse: what gemm_cross_entropy wrote. p carries its rounding to FP32, a relative error of up to |lse| 2^-24, and the
  *   error of z, whose products are added as the forward call adds them: 16 at a time in an accumulator that cuts what lies
  *   below its last place, accumulators of 512 products (up to 64 rows: 128) in FP32. That is less than 2^-18 of the sum of
- *   the products' magnitudes, in the mean 2^-21 of z or less.
+ *   the products' magnitudes, in the mean 2^-20 of z or less.
  *   dloss, dlse: M FP32. targets and dloss may both be NULL, and dlse. A negative target takes no part (its dloss is not
  *   read into the row); a target >= vocab makes the row of G NaN. A row that no gradient reaches (dloss and dlse 0 or
  *   absent) has a G of 0 whatever its logits are; its X still takes part in dW as 0 * X and has to be finite.
